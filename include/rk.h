@@ -328,6 +328,171 @@ uint64_t rk_launch_count(const rk_handle* h);
  * into buf (at most len bytes).  Host only. */
 rk_status rk_describe_plan(rk_handle* h, const rk_problem* p, char* buf, int64_t len);
 
+/* ---- state space layers -------------------------------------------------
+ *
+ * The operators of a selective state space layer, a recurrent layer whose
+ * state decays by an amount each step chooses: the layer normalisation in
+ * front of it, its short causal convolution, its scan, and the gradients of
+ * the three.  The pages have no counterpart of these entry points; they keep
+ * the pages' frame (sequence_lens, layouts 0 and 1, initial and final
+ * states, buffers with element offsets and lengths, host checks before
+ * anything is launched, float32 arithmetic and float32 state) and the
+ * library's: handles, streams, errors, bit-identical runs.
+ *
+ * Row tensors hold one row of consecutive elements per step and batch row,
+ * [seq, batch] rows in layout 0 and [batch, seq] rows in layout 1.  Rows
+ * along the second of the two lie `pitch` elements apart (0: dense), along
+ * the first `outer_pitch` (0: as many pitches as the second has rows), so an
+ * operand may be a slice of the wider rows a projection wrote, some steps of
+ * a longer sequence, or a transposed view; rows must not overlap.  No
+ * alignment beyond the element's is required; rows that start on 16-byte
+ * boundaries are read and written in 16-byte pieces.
+ *
+ * sequence_lens (int32 [batch], optional, else seq) clamps to [0, seq].
+ * Steps past a row's length are not read; Y and the row gradients are
+ * exactly 0 there.  A row of length 0 leaves its state as it was: the final
+ * state is the initial state (zeros if absent).
+ *
+ * final_state may be the same buffer as initial_state (the same address: a
+ * state updated in place); no other output may overlap an operand.  Null
+ * outputs are not written, and not computed where that saves work.
+ *
+ * Scratch: floats the caller places, or null for the handle's own, grown on
+ * demand.  Growing allocates, so it fails (RK_ERR_UNSUPPORTED) while the
+ * stream is being captured into a graph: place the scratch there.  Calls
+ * that share scratch (the handle's own, or one placed buffer) and run on
+ * different streams have to be ordered by the caller.  The lengths are host
+ * arithmetic on the problem alone; -1 for an invalid problem, 0 where the
+ * call needs none. */
+
+typedef struct rk_rows {
+  void* ptr;
+  int64_t offset; /* elements from ptr to the first row */
+  int64_t length; /* elements available from ptr */
+  int64_t pitch;  /* elements between rows; 0: dense */
+  int64_t outer_pitch; /* between the first rows of two steps (layout 0) or batch rows (layout 1); 0: pitch times
+                          the rows between them.  Not used by the normalisation, whose rows lie `pitch` apart. */
+} rk_rows;
+
+typedef struct rk_workspace {
+  float* ptr;     /* ptr + offset must be 16-byte aligned */
+  int64_t offset; /* in floats */
+  int64_t length;
+} rk_workspace;
+
+/* Layer normalisation over the `cols` elements of each of `rows` rows:
+ *   mean = sum x / cols,  inv = 1 / sqrt(sum (x - mean)^2 / cols + epsilon),
+ *   y = (x - mean) inv scale + b.
+ * Scale and B are [cols] of the problem's dtype, optional (1 and 0).  Mean
+ * and InvStdDev are float32 [rows], optional outputs that the gradient
+ * needs. */
+typedef struct rk_norm_problem {
+  int32_t dtype;
+  float epsilon; /* >= 0 */
+  int64_t rows, cols;
+} rk_norm_problem;
+
+typedef struct rk_norm_operands {
+  rk_rows X, Y;
+  rk_tensor Scale, B, Mean, InvStdDev;
+} rk_norm_operands;
+
+/* Its gradient, with xhat = (x - mean) inv and g = dy scale:
+ *   dx = inv (g - sum g / cols - xhat sum (g xhat) / cols),
+ *   dScale = sum over rows of dy xhat,  dB = sum over rows of dy.
+ * dScale and dB are float32 [cols], whatever the problem's dtype: they are
+ * sums over all rows. */
+typedef struct rk_norm_grad_operands {
+  rk_rows X, dY, dX;
+  rk_tensor Scale, Mean, InvStdDev, dScale, dB;
+} rk_norm_grad_operands;
+
+/* Causal convolution of each channel with its own `width` taps (1 to 8):
+ *   p[s, c] = B[c] + sum_j W[c, j] x[s - (width - 1) + j, c],
+ *   y = p, or p sigmoid(p) with activation 1.
+ * Steps before 0 are the rows of initial_state [batch, width - 1, channels]
+ * (the last row is step -1), zeros if absent; final_state, same shape, holds
+ * the last width - 1 inputs of each row, so that a sequence may be run in
+ * pieces, down to single steps.  W [channels, width], B [channels]
+ * (optional, else 0), the states: the problem's dtype. */
+typedef struct rk_conv_problem {
+  int32_t dtype, layout;
+  int32_t activation; /* 0: none, 1: SiLU */
+  int32_t width;
+  int64_t seq, batch, channels;
+} rk_conv_problem;
+
+typedef struct rk_conv_operands {
+  rk_rows X, Y;
+  rk_tensor W, B, sequence_lens, initial_state, final_state;
+} rk_conv_operands;
+
+/* Its gradient: dX rows and d_initial_state in the problem's dtype, dW
+ * [channels, width] and dB [channels] float32.  d_final_state (optional) is
+ * the gradient that arrives at final_state. */
+typedef struct rk_conv_grad_operands {
+  rk_rows X, dY, dX;
+  rk_tensor W, B, sequence_lens, initial_state, d_final_state, dW, dB, d_initial_state;
+} rk_conv_grad_operands;
+
+/* Selective scan.  Per batch row n, channel c and state k, with
+ * group = c / (channels / groups):
+ *   dt = Delta[s, c] + delta_bias[c], or softplus of it with softplus 1,
+ *   h  = exp(dt A[c, k]) h + dt X[s, c] B[s, group, k],
+ *   y  = sum_k C[s, group, k] h + D[c] X[s, c],
+ *   Y  = y, or y Z sigmoid(Z) where Z is given.
+ * X, Delta, Z, Y are rows of `channels`, B and C rows of groups * state
+ * elements, in the problem's dtype.  A [channels, state], D and delta_bias
+ * [channels] (optional, else 0) are float32, and so are initial_state
+ * (optional, else 0) and final_state [batch, channels, state]: a state that
+ * is carried over many steps is not rounded between them.  state is 1 to
+ * 128; groups divides channels. */
+typedef struct rk_scan_problem {
+  int32_t dtype, layout;
+  int32_t softplus;
+  int32_t groups;
+  int64_t seq, batch, channels, state;
+} rk_scan_problem;
+
+typedef struct rk_scan_operands {
+  rk_rows X, Delta, B, C, Z, Y;
+  rk_tensor A, D, delta_bias, sequence_lens, initial_state, final_state;
+} rk_scan_operands;
+
+/* Its gradient.  The row gradients dX, dDelta, dB, dC, dZ (dZ only with Z)
+ * have the problem's dtype; dA, dD, d_delta_bias, d_initial_state and the
+ * optional input d_final_state are float32. */
+typedef struct rk_scan_grad_operands {
+  rk_rows X, Delta, B, C, Z, dY, dX, dDelta, dB, dC, dZ;
+  rk_tensor A, D, delta_bias, sequence_lens, initial_state, d_final_state;
+  rk_tensor dA, dD, d_delta_bias, d_initial_state;
+} rk_scan_grad_operands;
+
+int64_t rk_norm_grad_scratch_length(const rk_norm_problem* p);
+int64_t rk_conv_grad_scratch_length(const rk_conv_problem* p);
+int64_t rk_scan_scratch_length(const rk_scan_problem* p);
+int64_t rk_scan_grad_scratch_length(const rk_scan_problem* p);
+
+/* Each enqueues its operator on `stream` and returns; all pointers are
+ * device pointers.  Errors are those of rk_encode: RK_ERR_ARG for a null
+ * handle, problem or operand list, RK_ERR_SHAPE for a bad size, pitch,
+ * offset or missing operand (the message names the operator and the
+ * argument), RK_ERR_UNSUPPORTED past the limits above or 2^31 - 1 rows or
+ * elements of a row, RK_ERR_OOM, RK_ERR_CUDA.  rows, seq and batch may be 0:
+ * what is left of the outputs is written (weights' gradients over no rows
+ * are 0, the final state after no steps is the initial state).  cols,
+ * channels and state are at least 1. */
+rk_status rk_norm_encode(rk_handle* h, const rk_norm_problem* p, const rk_norm_operands* ops, void* stream);
+rk_status rk_norm_grad_encode(rk_handle* h, const rk_norm_problem* p, const rk_norm_grad_operands* ops,
+                              const rk_workspace* scratch, void* stream);
+rk_status rk_conv_encode(rk_handle* h, const rk_conv_problem* p, const rk_conv_operands* ops, void* stream);
+rk_status rk_conv_grad_encode(rk_handle* h, const rk_conv_problem* p, const rk_conv_grad_operands* ops,
+                              const rk_workspace* scratch, void* stream);
+rk_status rk_scan_encode(rk_handle* h, const rk_scan_problem* p, const rk_scan_operands* ops,
+                         const rk_workspace* scratch, void* stream);
+rk_status rk_scan_grad_encode(rk_handle* h, const rk_scan_problem* p, const rk_scan_grad_operands* ops,
+                              const rk_workspace* scratch, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -4,7 +4,9 @@ A thin Python binding over the C ABI in ``include/rk.h`` (``librk.so``, built
 in-tree by ``build()``).  The functions ``rk_create``, ``rk_encode``, ... carry
 the C names and only marshal arguments; every step of a layer runs in the
 library's CUDA kernels.  ``RecurrentLayer`` is a convenience wrapper that takes
-torch CUDA tensors (torch supplies device memory and streams only).
+torch CUDA tensors (torch supplies device memory and streams only);
+``StateSpaceLayer`` (module ``state_space``) is the same for the operators of a
+selective state space layer.
 
 There is no CPU path: if the library is missing the binding raises.
 """
@@ -26,6 +28,10 @@ __all__ = [
     "rk_encode_noalloc", "rk_validate_lengths", "RK_OK", "RK_ERR_SHAPE", "RK_ERR_UNSUPPORTED", "RK_ERR_CUDA", "RK_ERR_TIMEOUT", "RK_ERR_OOM", "RK_ERR_ARG",
     "RK_FORCE_SIMT_PROJECTION", "RK_FORCE_GRID_STEP", "RK_FORCE_GENERAL_STEP", "RK_FORCE_SIMT_STEP",
     "RK_SEPARATE_PROJECTION", "RK_PREFER_TENSOR_STEP", "EXPORTED_SYMBOLS",
+    "StateSpaceLayer", "NormProblem", "ConvProblem", "ScanProblem",
+    "rk_norm_encode", "rk_norm_grad_encode", "rk_conv_encode", "rk_conv_grad_encode", "rk_scan_encode",
+    "rk_scan_grad_encode", "rk_norm_grad_scratch_length", "rk_conv_grad_scratch_length", "rk_scan_scratch_length",
+    "rk_scan_grad_scratch_length",
 ]
 
 RK_OK, RK_ERR_SHAPE, RK_ERR_UNSUPPORTED, RK_ERR_CUDA, RK_ERR_TIMEOUT, RK_ERR_OOM, RK_ERR_ARG = range(7)
@@ -50,6 +56,9 @@ EXPORTED_SYMBOLS = [
     "rk_encode", "rk_encode_host", "rk_status_poll", "rk_set_wait_limit", "rk_last_error",
     "rk_launch_count", "rk_describe_plan", "rk_selftest_timeout", "rk_set_profiling", "rk_last_timings",
     "rk_encode_noalloc", "rk_validate_lengths",
+    "rk_norm_encode", "rk_norm_grad_encode", "rk_conv_encode", "rk_conv_grad_encode", "rk_scan_encode",
+    "rk_scan_grad_encode", "rk_norm_grad_scratch_length", "rk_conv_grad_scratch_length", "rk_scan_scratch_length",
+    "rk_scan_grad_scratch_length",
 ]
 
 
@@ -148,6 +157,7 @@ def load(path: Optional[str] = None):
         "rk_validate_lengths": (ctypes.c_int32, [H, P, ctypes.POINTER(ctypes.c_int32), ctypes.c_int64]),
         "rk_last_timings": (ctypes.c_int32, [H, ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_float)]),
     }
+    sig.update(state_space.SIGNATURES)
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
         fn.restype = res
@@ -418,3 +428,11 @@ class RecurrentLayer:
         self.encode(problem, stream=stream, X=X, W=W, R=R, B=B, sequence_lens=sequence_lens,
                     initial_h=initial_h, initial_c=initial_c, P=P, **outs)
         return outs
+
+
+from . import state_space  # noqa: E402  (uses the names above)
+from .state_space import (  # noqa: E402,F401
+    ConvProblem, NormProblem, ScanProblem, StateSpaceLayer, rk_conv_encode, rk_conv_grad_encode,
+    rk_conv_grad_scratch_length, rk_conv_problem, rk_norm_encode, rk_norm_grad_encode, rk_norm_grad_scratch_length,
+    rk_norm_problem, rk_rows, rk_scan_encode, rk_scan_grad_encode, rk_scan_grad_scratch_length, rk_scan_problem,
+    rk_scan_scratch_length, rk_workspace)

@@ -1,0 +1,310 @@
+// rk_conv.cu -- short causal convolution of each channel, its SiLU and its
+// gradient.
+//
+// Bound by HBM: each input element is used by `width` outputs, so a thread
+// runs along the steps of one 16-byte piece of channels with the last
+// width - 1 inputs in registers, and neighbouring threads hold neighbouring
+// pieces.  The sequence is cut into chunks that run side by side; a chunk
+// reads the width - 1 inputs before it once more (from L2).
+#include <algorithm>
+
+#include "rk.h"
+#include "rk_ssm_common.cuh"
+
+namespace rk {
+namespace {
+
+// Steps of a forward chunk.  At least width - 1, so that only the first
+// chunk's thread reads the initial state, which the same thread may then
+// overwrite with the final state.
+constexpr int kFwdChunk = 16;
+
+template <typename T, int V>
+__device__ __forceinline__ const T* row_at(const RowsArg& a, int s, int n) {
+  return static_cast<const T*>(a.p) + s * a.ss + n * a.ns;
+}
+
+// The input of step s of a sequence: a row of X, of the initial state before
+// step 0, or 0.
+template <typename T, int V, int W>
+__device__ __forceinline__ void load_input(const ConvParams& p, int s, int n, int c, float (&o)[V]) {
+  if (s >= 0) {
+    Piece<T, V>::load(row_at<T, V>(p.X, s, n) + c, o);
+  } else if (p.init != nullptr) {
+    Piece<T, V>::load(static_cast<const T*>(p.init) + ((long long)n * (W - 1) + s + W - 1) * p.C + c, o);
+  } else {
+    fill(o, 0.0f);
+  }
+}
+
+template <typename T, int V, int W>
+__device__ __forceinline__ void load_taps(const ConvParams& p, int c, float (&w)[W][V], float (&b)[V]) {
+  const T* W0 = static_cast<const T*>(p.W) + (long long)c * W;
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int j = 0; j < W; ++j) w[j][i] = Elem<T>::to_f(W0[i * W + j]);
+  if (p.B) Piece<T, V>::load(static_cast<const T*>(p.B) + c, b);
+  else fill(b, 0.0f);
+}
+
+template <typename T, int V, int W>
+__global__ void __launch_bounds__(128) conv_kernel(ConvParams p) {
+  const int pieces = p.C / V;
+  const int chunks = max((p.S + kFwdChunk - 1) / kFwdChunk, 1);
+  const long long item = (long long)blockIdx.x * 128 + threadIdx.x;
+  if (item >= (long long)pieces * chunks * p.N) return;
+  const int c = (int)(item % pieces) * V;
+  const int k = (int)(item / pieces % chunks), n = (int)(item / pieces / chunks);
+  const int len = row_length(p.lens, n, p.S);
+  const int s0 = k * kFwdChunk, s1 = min(s0 + kFwdChunk, p.S), live = min(s1, len);
+  if (p.Y.p) {
+    T* y = static_cast<T*>(p.Y.p) + n * p.Y.ns + c;
+    if (s0 < live) {
+      float w[W][V], b[V], x[W][V];  // x[j]: the input of step s - (W - 1) + j
+      load_taps<T, V, W>(p, c, w, b);
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j) load_input<T, V, W>(p, s0 - (W - 1) + j, n, c, x[j + 1]);
+#pragma unroll 8
+      for (int s = s0; s < live; ++s) {
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+          for (int i = 0; i < V; ++i) x[j][i] = x[j + 1][i];
+        Piece<T, V>::load(row_at<T, V>(p.X, s, n) + c, x[W - 1]);
+        float o[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          o[i] = b[i];
+#pragma unroll
+          for (int j = 0; j < W; ++j) o[i] = fmaf(w[j][i], x[j][i], o[i]);
+          if (p.silu) o[i] *= sigmoid_fast(o[i]);
+        }
+        Piece<T, V>::store(y + s * p.Y.ss, o);
+      }
+    }
+    float zero[V];
+    fill(zero, 0.0f);
+    for (int s = max(s0, live); s < s1; ++s) Piece<T, V>::store(y + s * p.Y.ss, zero);
+  }
+  if (k == 0 && p.final_state) {
+    // rows in increasing order: row j of the new state is row j + len of the
+    // old one, read before it is overwritten
+    T* f = static_cast<T*>(p.final_state) + (long long)n * (W - 1) * p.C + c;
+    float x[W][V];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) load_input<T, V, W>(p, len - (W - 1) + j, n, c, x[j]);
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) Piece<T, V>::store(f + (long long)j * p.C, x[j]);
+  }
+}
+
+// The gradient.  Per step s of the chunk the pre-activation is computed again
+// from the inputs, dp[s] = dy[s] act'(p[s]) joins the last width of them, and
+// dx[s - (W - 1)] = sum_j W[j] dp[s - j] is complete.  The W - 1 steps after
+// the chunk are run for their dp alone.  A block is 32 pieces of channels by
+// kGradRows chunks; its weights' gradients are added up in shared memory and
+// written as one slice.
+constexpr int kGradRows = 4;
+
+template <typename T, int V, int W>
+__global__ void __launch_bounds__(32 * kGradRows) conv_grad_kernel(ConvParams p) {
+  __shared__ float sums[kGradRows][32 * V];
+  const int lane = threadIdx.x % 32, part = threadIdx.x / 32;
+  const int tiles = (p.C / V + 31) / 32;
+  const int tile = blockIdx.x % tiles, slice = blockIdx.x / tiles;
+  const int c = (tile * 32 + lane) * V;
+  const int chunks = (p.S + p.chunk - 1) / p.chunk;
+  const long long q = (long long)slice * kGradRows + part;  // which chunk of which sequence
+  const long long n64 = q / chunks;
+  const int n = (int)min(n64, (long long)p.N), k = (int)(q % chunks);
+  float dw[W + 1][V];
+#pragma unroll
+  for (int j = 0; j <= W; ++j) fill(dw[j], 0.0f);
+  if (c < p.C && n < p.N) {
+    const int len = row_length(p.lens, n, p.S);
+    const int s0 = k * p.chunk, s1 = min(s0 + p.chunk, p.S);
+    float w[W][V], b[V], x[W][V], dp[W][V];  // dp[j]: of step s - j
+    load_taps<T, V, W>(p, c, w, b);
+#pragma unroll
+    for (int j = 0; j < W; ++j) fill(dp[j], 0.0f);
+    if (s0 < len) {
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j) load_input<T, V, W>(p, s0 - (W - 1) + j, n, c, x[j + 1]);
+    }
+    T* dx = p.dX.p ? static_cast<T*>(p.dX.p) + n * p.dX.ns + c : nullptr;
+    const T* df = p.dfinal ? static_cast<const T*>(p.dfinal) + (long long)n * (W - 1) * p.C + c : nullptr;
+    T* di = (p.dinit && k == 0) ? static_cast<T*>(p.dinit) + (long long)n * (W - 1) * p.C + c : nullptr;
+    for (int s = s0; s < s1 + W - 1; ++s) {
+#pragma unroll
+      for (int j = W - 1; j > 0; --j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) dp[j][i] = dp[j - 1][i];
+      if (s < len) {
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+          for (int i = 0; i < V; ++i) x[j][i] = x[j + 1][i];
+        Piece<T, V>::load(row_at<T, V>(p.X, s, n) + c, x[W - 1]);
+        Piece<T, V>::load(row_at<T, V>(p.dY, s, n) + c, dp[0]);
+        if (p.silu) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            float pre = b[i];
+#pragma unroll
+            for (int j = 0; j < W; ++j) pre = fmaf(w[j][i], x[j][i], pre);
+            const float sg = sigmoid_fast(pre);
+            dp[0][i] *= sg * (1.0f + pre * (1.0f - sg));
+          }
+        }
+        if (s < s1) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+#pragma unroll
+            for (int j = 0; j < W; ++j) dw[j][i] = fmaf(dp[0][i], x[j][i], dw[j][i]);
+            dw[W][i] += dp[0][i];
+          }
+        }
+      } else {
+        fill(dp[0], 0.0f);
+      }
+      const int t = s - (W - 1);  // the input whose gradient is complete
+      // before the chunk: another chunk's input, or a row of the initial state
+      if (t < s0 && (k > 0 || di == nullptr)) continue;
+      if (t >= 0 && dx == nullptr) continue;
+      float o[V];
+      fill(o, 0.0f);
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int j = 0; j < W; ++j) o[i] = fmaf(w[W - 1 - j][i], dp[W - 1 - j][i], o[i]);
+      const int f = t - len + (W - 1);  // the row of the final state that this input is
+      if (df && f >= 0 && f < W - 1) {
+        float g[V];
+        Piece<T, V>::load(df + (long long)f * p.C, g);
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] += g[i];
+      }
+      if (t >= 0) Piece<T, V>::store(dx + t * p.dX.ss, o);
+      else Piece<T, V>::store(di + (long long)(t + W - 1) * p.C, o);
+    }
+  }
+  if (p.partial == nullptr) return;
+#pragma unroll
+  for (int j = 0; j <= W; ++j) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < V; ++i) sums[part][lane * V + i] = dw[j][i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 32 * V; i += 32 * kGradRows) {
+      const int ch = tile * 32 * V + i;
+      float a = 0.0f;
+#pragma unroll
+      for (int r = 0; r < kGradRows; ++r) a += sums[r][i];
+      if (ch < p.C) p.partial[((long long)slice * (W + 1) + j) * p.C + ch] = a;
+    }
+  }
+}
+
+// dW and dB from the slices, added in a fixed order.
+__global__ void __launch_bounds__(256) conv_grad_reduce_kernel(ConvParams p) {
+  __shared__ float buf[8][33];
+  const int taps = p.width + 1;
+  const int col = blockIdx.x * 32 + threadIdx.x % 32, part = threadIdx.x / 32;  // tap-major
+  const int cols = taps * p.C;
+  float s = 0.0f;
+  if (col < cols) {
+#pragma unroll 4
+    for (int b = part; b < p.slices; b += 8) s += p.partial[(long long)b * cols + col];
+  }
+  buf[part][threadIdx.x % 32] = s;
+  __syncthreads();
+  if (part == 0 && col < cols) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) s += buf[i][threadIdx.x];
+    const int j = col / p.C, c = col % p.C;
+    if (j < p.width) {
+      if (p.dW) p.dW[(long long)c * p.width + j] = s;
+    } else if (p.dB) {
+      p.dB[c] = s;
+    }
+  }
+}
+
+template <typename T, int V, int W>
+cudaError_t run_conv(const ConvParams& p, cudaStream_t s) {
+  const long long items = (long long)(p.C / V) * std::max((p.S + kFwdChunk - 1) / kFwdChunk, 1) * p.N;
+  conv_kernel<T, V, W><<<(unsigned)((items + 127) / 128), 128, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+template <typename T, int V, int W>
+cudaError_t run_conv_grad(const ConvParams& p, cudaStream_t s) {
+  conv_grad_kernel<T, V, W><<<(unsigned)((p.C / V + 31) / 32 * p.slices), 32 * kGradRows, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+template <typename T, int V>
+cudaError_t by_width(const ConvParams& p, cudaStream_t s, bool grad) {
+#define RK_CONV_WIDTH(w) \
+  case w: return grad ? run_conv_grad<T, V, w>(p, s) : run_conv<T, V, w>(p, s);
+  switch (p.width) {
+    RK_CONV_WIDTH(1)
+    RK_CONV_WIDTH(2)
+    RK_CONV_WIDTH(3)
+    RK_CONV_WIDTH(4)
+    RK_CONV_WIDTH(5)
+    RK_CONV_WIDTH(6)
+    RK_CONV_WIDTH(7)
+    RK_CONV_WIDTH(8)
+  }
+#undef RK_CONV_WIDTH
+  return cudaErrorInvalidValue;
+}
+
+template <typename T>
+cudaError_t conv_typed(const ConvParams& p, cudaStream_t s, bool grad) {
+  // the gradient keeps twice the registers of the forward pass per channel:
+  // pieces of 8 bytes
+  constexpr int VG = sizeof(T) == 4 ? 2 : 4;
+  if (!p.vec) return by_width<T, 1>(p, s, grad);
+  return grad ? by_width<T, VG>(p, s, true) : by_width<T, kPiece<T>>(p, s, false);
+}
+
+cudaError_t conv_any(const ConvParams& p, cudaStream_t s, bool grad) {
+  switch (p.dtype) {
+    case RK_F32: return conv_typed<float>(p, s, grad);
+    case RK_F16: return conv_typed<__half>(p, s, grad);
+    default: return conv_typed<__nv_bfloat16>(p, s, grad);
+  }
+}
+
+}  // namespace
+
+int conv_grad_chunk(long long seq, long long batch, long long channels) {
+  (void)batch, (void)channels;
+  return (int)std::min<long long>(std::max<long long>(seq, 1), 32);
+}
+
+int conv_grad_slices(long long seq, long long batch, long long channels) {
+  const long long chunk = conv_grad_chunk(seq, batch, channels);
+  return (int)(((seq + chunk - 1) / chunk * batch + kGradRows - 1) / kGradRows);
+}
+
+cudaError_t launch_conv(const ConvParams& p, cudaStream_t s) { return conv_any(p, s, false); }
+
+cudaError_t launch_conv_grad(const ConvParams& p, cudaStream_t s, int* launches) {
+  *launches = 0;
+  cudaError_t e = cudaSuccess;
+  if (p.slices > 0) {
+    e = conv_any(p, s, true);
+    *launches += 1;
+  }
+  if (e != cudaSuccess || p.partial == nullptr) return e;
+  const long long cols = (long long)(p.width + 1) * p.C;
+  conv_grad_reduce_kernel<<<(unsigned)((cols + 31) / 32), 256, 0, s>>>(p);
+  *launches += 1;
+  return cudaGetLastError();
+}
+
+}  // namespace rk

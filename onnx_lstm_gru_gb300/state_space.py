@@ -1,0 +1,396 @@
+"""The operators of a selective state space layer, on the C ABI of ``include/rk.h``.
+
+``StateSpaceLayer`` takes torch CUDA tensors: layer normalisation, the short
+causal convolution and the selective scan, each with its gradient.  The
+formulas, shapes and rules are those the header states; here only arguments
+are checked and packed.  Row operands may be slices of wider rows, some steps
+of a longer sequence or transposed views: any strides with a dense last
+dimension.
+
+Prompts and single tokens are the same calls: a step is ``seq=1`` with
+``initial_state`` given and ``final_state`` asked for (or given: the same
+tensor as ``initial_state`` updates it in place).
+"""
+from __future__ import annotations
+
+import ctypes
+import struct
+from dataclasses import dataclass
+
+from . import DTYPES, RK_OK, RkError, load, rk_create, rk_destroy, rk_last_error, rk_launch_count, rk_tensor
+
+
+class rk_rows(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("offset", ctypes.c_int64), ("length", ctypes.c_int64),
+                ("pitch", ctypes.c_int64), ("outer_pitch", ctypes.c_int64)]
+
+
+class rk_workspace(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("offset", ctypes.c_int64), ("length", ctypes.c_int64)]
+
+
+class rk_norm_problem(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("epsilon", ctypes.c_float), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64)]
+
+
+class rk_conv_problem(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("layout", ctypes.c_int32), ("activation", ctypes.c_int32),
+                ("width", ctypes.c_int32), ("seq", ctypes.c_int64), ("batch", ctypes.c_int64),
+                ("channels", ctypes.c_int64)]
+
+
+class rk_scan_problem(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("layout", ctypes.c_int32), ("softplus", ctypes.c_int32),
+                ("groups", ctypes.c_int32), ("seq", ctypes.c_int64), ("batch", ctypes.c_int64),
+                ("channels", ctypes.c_int64), ("state", ctypes.c_int64)]
+
+
+# Operand lists in the C structs' order: row tensors, then the others.
+_OPERANDS = {
+    "norm": (("X", "Y"), ("Scale", "B", "Mean", "InvStdDev")),
+    "norm_grad": (("X", "dY", "dX"), ("Scale", "Mean", "InvStdDev", "dScale", "dB")),
+    "conv": (("X", "Y"), ("W", "B", "sequence_lens", "initial_state", "final_state")),
+    "conv_grad": (("X", "dY", "dX"), ("W", "B", "sequence_lens", "initial_state", "d_final_state", "dW", "dB",
+                                       "d_initial_state")),
+    "scan": (("X", "Delta", "B", "C", "Z", "Y"),
+             ("A", "D", "delta_bias", "sequence_lens", "initial_state", "final_state")),
+    "scan_grad": (("X", "Delta", "B", "C", "Z", "dY", "dX", "dDelta", "dB", "dC", "dZ"),
+                  ("A", "D", "delta_bias", "sequence_lens", "initial_state", "d_final_state", "dA", "dD",
+                   "d_delta_bias", "d_initial_state")),
+}
+
+
+def _operand_struct(op):
+    rows, tensors = _OPERANDS[op]
+    fields = [(n, rk_rows) for n in rows] + [(n, rk_tensor) for n in tensors]
+    return type(f"rk_{op}_operands", (ctypes.Structure,), {"_fields_": fields})
+
+
+rk_norm_operands = _operand_struct("norm")
+rk_norm_grad_operands = _operand_struct("norm_grad")
+rk_conv_operands = _operand_struct("conv")
+rk_conv_grad_operands = _operand_struct("conv_grad")
+rk_scan_operands = _operand_struct("scan")
+rk_scan_grad_operands = _operand_struct("scan_grad")
+
+_P = ctypes.c_void_p
+SIGNATURES = {
+    "rk_norm_grad_scratch_length": (ctypes.c_int64, [_P]),
+    "rk_conv_grad_scratch_length": (ctypes.c_int64, [_P]),
+    "rk_scan_scratch_length": (ctypes.c_int64, [_P]),
+    "rk_scan_grad_scratch_length": (ctypes.c_int64, [_P]),
+    "rk_norm_encode": (ctypes.c_int32, [_P, _P, _P, _P]),
+    "rk_norm_grad_encode": (ctypes.c_int32, [_P, _P, _P, _P, _P]),
+    "rk_conv_encode": (ctypes.c_int32, [_P, _P, _P, _P]),
+    "rk_conv_grad_encode": (ctypes.c_int32, [_P, _P, _P, _P, _P]),
+    "rk_scan_encode": (ctypes.c_int32, [_P, _P, _P, _P, _P]),
+    "rk_scan_grad_encode": (ctypes.c_int32, [_P, _P, _P, _P, _P]),
+}
+
+
+# ---- thin wrappers with the C names (argument marshalling only) ----------------------------
+
+def _ref(x):
+    return ctypes.byref(x) if x is not None else None
+
+
+def rk_norm_grad_scratch_length(problem: rk_norm_problem) -> int:
+    return load().rk_norm_grad_scratch_length(_ref(problem))
+
+
+def rk_conv_grad_scratch_length(problem: rk_conv_problem) -> int:
+    return load().rk_conv_grad_scratch_length(_ref(problem))
+
+
+def rk_scan_scratch_length(problem: rk_scan_problem) -> int:
+    return load().rk_scan_scratch_length(_ref(problem))
+
+
+def rk_scan_grad_scratch_length(problem: rk_scan_problem) -> int:
+    return load().rk_scan_grad_scratch_length(_ref(problem))
+
+
+def rk_norm_encode(handle, problem, ops, stream) -> int:
+    return load().rk_norm_encode(handle, _ref(problem), _ref(ops), stream)
+
+
+def rk_norm_grad_encode(handle, problem, ops, scratch, stream) -> int:
+    return load().rk_norm_grad_encode(handle, _ref(problem), _ref(ops), _ref(scratch), stream)
+
+
+def rk_conv_encode(handle, problem, ops, stream) -> int:
+    return load().rk_conv_encode(handle, _ref(problem), _ref(ops), stream)
+
+
+def rk_conv_grad_encode(handle, problem, ops, scratch, stream) -> int:
+    return load().rk_conv_grad_encode(handle, _ref(problem), _ref(ops), _ref(scratch), stream)
+
+
+def rk_scan_encode(handle, problem, ops, scratch, stream) -> int:
+    return load().rk_scan_encode(handle, _ref(problem), _ref(ops), _ref(scratch), stream)
+
+
+def rk_scan_grad_encode(handle, problem, ops, scratch, stream) -> int:
+    return load().rk_scan_grad_encode(handle, _ref(problem), _ref(ops), _ref(scratch), stream)
+
+
+# ---- problem descriptions ----------------------------------------------------------------------
+
+class _Problem:
+    """What the problems share: the C struct and the operands' shapes and types, made once (they are frozen)."""
+
+    def _keep(self, c, names):
+        object.__setattr__(self, "_c", c)
+        object.__setattr__(self, "_ref", ctypes.addressof(c))
+        object.__setattr__(self, "_names", names)
+        object.__setattr__(self, "_plans", {})
+
+    def to_c(self):
+        return type(self._c).from_buffer_copy(self._c)
+
+    def shapes(self) -> dict:
+        return {n: s for n, (s, _) in self._names.items()}
+
+    def _plan(self, op):
+        plan = self._plans.get(op)
+        if plan is None:
+            plan = self._plans[op] = _Plan(op, self)
+        return plan
+
+
+# element types of operands: the problem's ("t"), float32 ("f"), int32 ("i")
+@dataclass(frozen=True)
+class NormProblem(_Problem):
+    """Layer normalisation of ``rows`` rows of ``cols`` elements (mirrors rk_norm_problem)."""
+    rows: int
+    cols: int
+    dtype: str = "f32"
+    epsilon: float = 1e-5
+
+    def __post_init__(self):
+        row, col, one = (self.rows, self.cols), (self.cols,), (self.rows,)
+        self._keep(rk_norm_problem(DTYPES[self.dtype], self.epsilon, self.rows, self.cols), {
+            "X": (row, "t"), "Y": (row, "t"), "dY": (row, "t"), "dX": (row, "t"),
+            "Scale": (col, "t"), "B": (col, "t"), "dScale": (col, "f"), "dB": (col, "f"),
+            "Mean": (one, "f"), "InvStdDev": (one, "f")})
+
+
+def _row_shape(layout, seq, batch, inner):
+    return (seq, batch, inner) if layout == 0 else (batch, seq, inner)
+
+
+@dataclass(frozen=True)
+class ConvProblem(_Problem):
+    """Causal convolution (mirrors rk_conv_problem); ``activation`` is "silu" or "none"."""
+    seq: int
+    batch: int
+    channels: int
+    width: int = 4
+    dtype: str = "f32"
+    layout: int = 0
+    activation: str = "silu"
+
+    def __post_init__(self):
+        act = {"none": 0, "silu": 1}[self.activation]
+        row = _row_shape(self.layout, self.seq, self.batch, self.channels)
+        state, col = (self.batch, self.width - 1, self.channels), (self.channels,)
+        taps = (self.channels, self.width)
+        self._keep(rk_conv_problem(DTYPES[self.dtype], self.layout, act, self.width, self.seq, self.batch,
+                                   self.channels), {
+            "X": (row, "t"), "Y": (row, "t"), "dY": (row, "t"), "dX": (row, "t"),
+            "W": (taps, "t"), "B": (col, "t"), "dW": (taps, "f"), "dB": (col, "f"),
+            "sequence_lens": ((self.batch,), "i"), "initial_state": (state, "t"), "final_state": (state, "t"),
+            "d_initial_state": (state, "t"), "d_final_state": (state, "t")})
+
+
+@dataclass(frozen=True)
+class ScanProblem(_Problem):
+    """Selective scan (mirrors rk_scan_problem)."""
+    seq: int
+    batch: int
+    channels: int
+    state: int
+    groups: int = 1
+    dtype: str = "f32"
+    layout: int = 0
+    softplus: bool = True
+
+    def __post_init__(self):
+        row = _row_shape(self.layout, self.seq, self.batch, self.channels)
+        mix = _row_shape(self.layout, self.seq, self.batch, self.groups * self.state)
+        rates, col = (self.channels, self.state), (self.channels,)
+        state = (self.batch, self.channels, self.state)
+        names = {n: (row, "t") for n in ("X", "Delta", "Z", "Y", "dY", "dX", "dDelta", "dZ")}
+        names.update({n: (mix, "t") for n in ("B", "C", "dB", "dC")})
+        names.update({n: (state, "f") for n in ("initial_state", "final_state", "d_initial_state", "d_final_state")})
+        names.update({"A": (rates, "f"), "dA": (rates, "f"), "D": (col, "f"), "dD": (col, "f"),
+                      "delta_bias": (col, "f"), "d_delta_bias": (col, "f"), "sequence_lens": ((self.batch,), "i")})
+        self._keep(rk_scan_problem(DTYPES[self.dtype], self.layout, int(self.softplus), self.groups, self.seq,
+                                   self.batch, self.channels, self.state), names)
+
+
+_REQUIRED = {
+    "norm": ("X",), "norm_grad": ("X", "Mean", "InvStdDev", "dY"), "conv": ("X", "W"), "conv_grad": ("X", "W", "dY"),
+    "scan": ("X", "Delta", "A", "B", "C"), "scan_grad": ("X", "Delta", "A", "B", "C", "dY"),
+}
+
+
+class _Plan:
+    """How one operator's operands of one problem are packed."""
+
+    def __init__(self, op, problem):
+        import torch
+        types = {"t": (torch.float32, torch.float16, torch.bfloat16)[DTYPES[problem.dtype]], "f": torch.float32,
+                 "i": torch.int32}
+        rows, tensors = _OPERANDS[op]
+        self.op = op
+        self.pack = struct.Struct("=" + "Qqqqq" * len(rows) + "Qqq" * len(tensors)).pack
+        self.size = 5 * len(rows) + 3 * len(tensors)
+        # name -> first value of its entry, whether it is a row tensor, shape, type
+        self.entry = {}
+        at = 0
+        for names, is_rows, n in ((rows, True, 5), (tensors, False, 3)):
+            for name in names:
+                shape, kind = problem._names[name]
+                self.entry[name] = (at, is_rows, shape, types[kind])
+                at += n
+        lib = load()
+        self.call = getattr(lib, f"rk_{op}_encode")
+        length = getattr(lib, f"rk_{op}_scratch_length", None)
+        # None: the call takes no scratch
+        self.scratch = None if length is None else length(problem._ref)
+
+
+def _pitches(name, t, shape):
+    """Distances in elements between the rows of ``t`` along its last but one
+    dimension and its first (0 in a matrix), and the elements it spans."""
+    st = t.stride()
+    inner = shape[-1]
+    if inner > 1 and st[-1] != 1:
+        raise ValueError(f"{name}: the last dimension must be dense")
+    # where there is one row, its distance to the next is any
+    pitch = st[-2] if shape[-2] > 1 else inner
+    outer = st[0] if len(shape) == 3 and shape[0] > 1 else 0
+    if pitch < inner or (outer < inner and len(shape) == 3 and shape[0] > 1):
+        raise ValueError(f"{name}: rows overlap, strides {st}")
+    return pitch, outer, (shape[-2] - 1) * pitch + (shape[0] - 1) * outer + inner
+
+
+class StateSpaceLayer:
+    """Owns an rk handle.  Every method enqueues one operator on the current
+    torch stream (or ``stream``) and returns the outputs named in ``want``,
+    allocated unless they are passed by name.  Scratch comes from torch's
+    allocator, so calls may run on any stream and be captured into a graph.
+    No CPU path exists."""
+
+    def __init__(self, flags: int = 0):
+        load()
+        self.handle = rk_create(flags)
+
+    def close(self):
+        if getattr(self, "handle", None):
+            rk_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def launches(self) -> int:
+        return rk_launch_count(self.handle)
+
+    def norm(self, problem: NormProblem, X, want=("Y", "Mean", "InvStdDev"), stream=None, **tensors) -> dict:
+        """Y, Mean, InvStdDev from X, Scale, B."""
+        return self._run("norm", NormProblem, problem, X, want, stream, tensors)
+
+    def norm_grad(self, problem: NormProblem, X, want=("dX", "dScale", "dB"), stream=None, **tensors) -> dict:
+        """dX, dScale, dB from X, Scale, Mean, InvStdDev, dY."""
+        return self._run("norm_grad", NormProblem, problem, X, want, stream, tensors)
+
+    def conv(self, problem: ConvProblem, X, want=("Y", "final_state"), stream=None, **tensors) -> dict:
+        """Y, final_state from X, W, B, sequence_lens, initial_state."""
+        return self._run("conv", ConvProblem, problem, X, want, stream, tensors)
+
+    def conv_grad(self, problem: ConvProblem, X, want=("dX", "dW", "dB"), stream=None, **tensors) -> dict:
+        """dX, dW, dB, d_initial_state from conv's operands, dY and d_final_state."""
+        return self._run("conv_grad", ConvProblem, problem, X, want, stream, tensors)
+
+    def scan(self, problem: ScanProblem, X, want=("Y", "final_state"), stream=None, **tensors) -> dict:
+        """Y, final_state from X, Delta, A, B, C, D, Z, delta_bias, sequence_lens, initial_state."""
+        return self._run("scan", ScanProblem, problem, X, want, stream, tensors)
+
+    def scan_grad(self, problem: ScanProblem, X,
+                  want=("dX", "dDelta", "dA", "dB", "dC", "dD", "d_delta_bias"), stream=None, **tensors) -> dict:
+        """dX, dDelta, dA, dB, dC, dD, d_delta_bias, dZ, d_initial_state from scan's operands, dY and d_final_state."""
+        return self._run("scan_grad", ScanProblem, problem, X, want, stream, tensors)
+
+    def _run(self, op, kind, problem, X, want, stream, tensors):
+        import torch
+        if type(problem) is not kind:
+            raise TypeError(f"{op}: expected {kind.__name__}, got {type(problem).__name__}")
+        if not X.is_cuda:
+            raise ValueError("X: expected a CUDA tensor")
+        device = X.device
+        current = torch.cuda.current_stream(device)
+        if stream is not None and stream != current:
+            # memory made here belongs to that stream; what the caller passes is
+            # kept from reuse until the stream is past this call
+            with torch.cuda.stream(stream):
+                out = self._run(op, kind, problem, X, want, None, tensors)
+            for t in (X, *tensors.values()):
+                if t is not None:
+                    t.record_stream(stream)
+            return out
+        if device.index != torch.cuda.current_device():
+            with torch.cuda.device(device):
+                return self._run(op, kind, problem, X, want, None, tensors)
+        plan = problem._plan(op)
+        entry = plan.entry
+        vals = [0] * plan.size
+        tensors["X"] = X
+        out = {}
+        for name in want:
+            t = tensors.get(name)
+            if t is None:
+                if name not in entry:
+                    raise KeyError(name)
+                _, _, shape, dtype = entry[name]
+                tensors[name] = t = torch.empty(shape, dtype=dtype, device=device)
+            out[name] = t
+        for name, t in tensors.items():
+            if t is None:
+                continue
+            if name not in entry:
+                raise KeyError(name)
+            at, rows, shape, dtype = entry[name]
+            if t.dtype != dtype:
+                raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+            if t.shape != shape:
+                raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+            if t.device != device:
+                raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
+            n = t.numel()
+            if rows:
+                if n and not t.is_contiguous():
+                    vals[at + 3], vals[at + 4], n = _pitches(name, t, shape)
+            elif not t.is_contiguous():
+                raise ValueError(f"{name}: must be contiguous")
+            vals[at] = t.data_ptr()
+            vals[at + 2] = n
+        for name in _REQUIRED[op]:
+            if tensors.get(name) is None:
+                raise ValueError(f"{op}: {name} is required")
+        args = (self.handle, problem._ref, plan.pack(*vals))
+        if plan.scratch is not None:
+            if plan.scratch > 0:
+                work = torch.empty(plan.scratch, dtype=torch.float32, device=device)
+                args += (struct.pack("=Qqq", work.data_ptr(), 0, plan.scratch),)
+            else:
+                args += (None,)
+        st = plan.call(*args, current.cuda_stream)
+        if st != RK_OK:
+            raise RkError(st, rk_last_error(self.handle))
+        return out
