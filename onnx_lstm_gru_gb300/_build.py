@@ -10,6 +10,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,6 +21,11 @@ LIB = os.path.join(BUILD, "librk.so")
 # measurement aid of the benchmark (float32 FMA peak), its own shared object
 PROBE_SRC = os.path.join(PKG, "probe", "fma_peak.cu")
 PROBE_LIB = os.path.join(BUILD, "libfmapeak.so")
+
+# packs torch tensors for the state space entry points: a Python module that
+# includes torch's headers, its own shared object
+BINDING_SRC = os.path.join(PKG, "binding", "state_space_binding.cpp")
+BINDING_LIB = os.path.join(BUILD, "state_space_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -40,6 +46,24 @@ def sources():
 def _headers():
     return glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + \
         glob.glob(os.path.join(INCLUDE, "*.h"))
+
+
+def _build_binding():
+    """Compile the Python module against the installed torch."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    tmp = BINDING_LIB + f".{os.getpid()}.tmp"
+    include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], cuda]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(a for i in include for a in ("-I", i)),
+           BINDING_SRC, "-o", tmp, "-L", os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+           "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"build of state_space_binding.so failed:\n{r.stderr}")
+    os.replace(tmp, BINDING_LIB)
 
 
 def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -> str:
@@ -68,12 +92,17 @@ def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -
         os.replace(tmp, obj)
         return r.stderr
 
-    if todo:
-        n = jobs or min(len(todo), max(1, os.cpu_count() or 1))
+    binding = force or not os.path.exists(BINDING_LIB) or \
+        os.path.getmtime(BINDING_LIB) < os.path.getmtime(BINDING_SRC)
+    if todo or binding:
+        n = jobs or min(len(todo) + 1, max(1, os.cpu_count() or 1))
         with cf.ThreadPoolExecutor(max_workers=n) as ex:
+            extra = ex.submit(_build_binding) if binding else None
             for log in ex.map(compile_one, todo):
                 if verbose and log:
                     print(log)
+            if extra is not None:
+                extra.result()
     lib_time = os.path.getmtime(LIB) if os.path.exists(LIB) else -1.0
     if todo or lib_time < max(os.path.getmtime(o) for o in objs):
         tmp = LIB + f".{os.getpid()}.tmp"

@@ -3,7 +3,8 @@
 ``StateSpaceLayer`` takes torch CUDA tensors: layer normalisation, the short
 causal convolution and the selective scan, each with its gradient.  The
 formulas, shapes and rules are those the header states; here only arguments
-are checked and packed.  Row operands may be slices of wider rows, some steps
+are checked and packed (by the module that ``binding/state_space_binding.cpp``
+builds: a call's host time is what a single token waits for).  Row operands may be slices of wider rows, some steps
 of a longer sequence or transposed views: any strides with a dense last
 dimension.
 
@@ -14,10 +15,11 @@ tensor as ``initial_state`` updates it in place).
 from __future__ import annotations
 
 import ctypes
-import struct
+import functools
 from dataclasses import dataclass
 
-from . import DTYPES, RK_OK, RkError, load, rk_create, rk_destroy, rk_last_error, rk_launch_count, rk_tensor
+from . import DTYPES, RkError, load, rk_create, rk_destroy, rk_last_error, rk_launch_count, rk_tensor
+from ._build import BINDING_LIB
 
 
 class rk_rows(ctypes.Structure):
@@ -137,25 +139,32 @@ def rk_scan_grad_encode(handle, problem, ops, scratch, stream) -> int:
 
 # ---- problem descriptions ----------------------------------------------------------------------
 
+@functools.lru_cache(maxsize=None)
+def _binding():
+    """The built module that packs operands."""
+    import importlib.machinery
+    import importlib.util
+    import torch  # noqa: F401  (the module links against its libraries)
+    loader = importlib.machinery.ExtensionFileLoader("state_space_binding", BINDING_LIB)
+    spec = importlib.util.spec_from_file_location("state_space_binding", BINDING_LIB, loader=loader)
+    module = importlib.util.module_from_spec(spec)
+    loader.exec_module(module)
+    return module
+
+
 class _Problem:
-    """What the problems share: the C struct and the operands' shapes and types, made once (they are frozen)."""
-
-    def _keep(self, c, names):
-        object.__setattr__(self, "_c", c)
-        object.__setattr__(self, "_ref", ctypes.addressof(c))
-        object.__setattr__(self, "_names", names)
-        object.__setattr__(self, "_plans", {})
-
-    def to_c(self):
-        return type(self._c).from_buffer_copy(self._c)
+    """What the problems share."""
 
     def shapes(self) -> dict:
-        return {n: s for n, (s, _) in self._names.items()}
+        return {n: s for n, (s, _) in self._operands().items()}
 
     def _plan(self, op):
-        plan = self._plans.get(op)
+        plans = self.__dict__.get("_plans")
+        if plans is None:
+            plans = self.__dict__["_plans"] = {}
+        plan = plans.get(op)
         if plan is None:
-            plan = self._plans[op] = _Plan(op, self)
+            plan = plans[op] = _plan(op, self)
         return plan
 
 
@@ -168,12 +177,14 @@ class NormProblem(_Problem):
     dtype: str = "f32"
     epsilon: float = 1e-5
 
-    def __post_init__(self):
+    def to_c(self) -> rk_norm_problem:
+        return rk_norm_problem(DTYPES[self.dtype], self.epsilon, self.rows, self.cols)
+
+    def _operands(self):
         row, col, one = (self.rows, self.cols), (self.cols,), (self.rows,)
-        self._keep(rk_norm_problem(DTYPES[self.dtype], self.epsilon, self.rows, self.cols), {
-            "X": (row, "t"), "Y": (row, "t"), "dY": (row, "t"), "dX": (row, "t"),
-            "Scale": (col, "t"), "B": (col, "t"), "dScale": (col, "f"), "dB": (col, "f"),
-            "Mean": (one, "f"), "InvStdDev": (one, "f")})
+        return {"X": (row, "t"), "Y": (row, "t"), "dY": (row, "t"), "dX": (row, "t"),
+                "Scale": (col, "t"), "B": (col, "t"), "dScale": (col, "f"), "dB": (col, "f"),
+                "Mean": (one, "f"), "InvStdDev": (one, "f")}
 
 
 def _row_shape(layout, seq, batch, inner):
@@ -191,17 +202,18 @@ class ConvProblem(_Problem):
     layout: int = 0
     activation: str = "silu"
 
-    def __post_init__(self):
-        act = {"none": 0, "silu": 1}[self.activation]
+    def to_c(self) -> rk_conv_problem:
+        return rk_conv_problem(DTYPES[self.dtype], self.layout, {"none": 0, "silu": 1}[self.activation], self.width,
+                               self.seq, self.batch, self.channels)
+
+    def _operands(self):
         row = _row_shape(self.layout, self.seq, self.batch, self.channels)
         state, col = (self.batch, self.width - 1, self.channels), (self.channels,)
         taps = (self.channels, self.width)
-        self._keep(rk_conv_problem(DTYPES[self.dtype], self.layout, act, self.width, self.seq, self.batch,
-                                   self.channels), {
-            "X": (row, "t"), "Y": (row, "t"), "dY": (row, "t"), "dX": (row, "t"),
-            "W": (taps, "t"), "B": (col, "t"), "dW": (taps, "f"), "dB": (col, "f"),
-            "sequence_lens": ((self.batch,), "i"), "initial_state": (state, "t"), "final_state": (state, "t"),
-            "d_initial_state": (state, "t"), "d_final_state": (state, "t")})
+        return {"X": (row, "t"), "Y": (row, "t"), "dY": (row, "t"), "dX": (row, "t"),
+                "W": (taps, "t"), "B": (col, "t"), "dW": (taps, "f"), "dB": (col, "f"),
+                "sequence_lens": ((self.batch,), "i"), "initial_state": (state, "t"), "final_state": (state, "t"),
+                "d_initial_state": (state, "t"), "d_final_state": (state, "t")}
 
 
 @dataclass(frozen=True)
@@ -216,7 +228,11 @@ class ScanProblem(_Problem):
     layout: int = 0
     softplus: bool = True
 
-    def __post_init__(self):
+    def to_c(self) -> rk_scan_problem:
+        return rk_scan_problem(DTYPES[self.dtype], self.layout, int(self.softplus), self.groups, self.seq, self.batch,
+                               self.channels, self.state)
+
+    def _operands(self):
         row = _row_shape(self.layout, self.seq, self.batch, self.channels)
         mix = _row_shape(self.layout, self.seq, self.batch, self.groups * self.state)
         rates, col = (self.channels, self.state), (self.channels,)
@@ -226,8 +242,7 @@ class ScanProblem(_Problem):
         names.update({n: (state, "f") for n in ("initial_state", "final_state", "d_initial_state", "d_final_state")})
         names.update({"A": (rates, "f"), "dA": (rates, "f"), "D": (col, "f"), "dD": (col, "f"),
                       "delta_bias": (col, "f"), "d_delta_bias": (col, "f"), "sequence_lens": ((self.batch,), "i")})
-        self._keep(rk_scan_problem(DTYPES[self.dtype], self.layout, int(self.softplus), self.groups, self.seq,
-                                   self.batch, self.channels, self.state), names)
+        return names
 
 
 _REQUIRED = {
@@ -236,45 +251,25 @@ _REQUIRED = {
 }
 
 
-class _Plan:
-    """How one operator's operands of one problem are packed."""
-
-    def __init__(self, op, problem):
-        import torch
-        types = {"t": (torch.float32, torch.float16, torch.bfloat16)[DTYPES[problem.dtype]], "f": torch.float32,
-                 "i": torch.int32}
-        rows, tensors = _OPERANDS[op]
-        self.op = op
-        self.pack = struct.Struct("=" + "Qqqqq" * len(rows) + "Qqq" * len(tensors)).pack
-        self.size = 5 * len(rows) + 3 * len(tensors)
-        # name -> first value of its entry, whether it is a row tensor, shape, type
-        self.entry = {}
-        at = 0
-        for names, is_rows, n in ((rows, True, 5), (tensors, False, 3)):
-            for name in names:
-                shape, kind = problem._names[name]
-                self.entry[name] = (at, is_rows, shape, types[kind])
-                at += n
-        lib = load()
-        self.call = getattr(lib, f"rk_{op}_encode")
-        length = getattr(lib, f"rk_{op}_scratch_length", None)
-        # None: the call takes no scratch
-        self.scratch = None if length is None else length(problem._ref)
-
-
-def _pitches(name, t, shape):
-    """Distances in elements between the rows of ``t`` along its last but one
-    dimension and its first (0 in a matrix), and the elements it spans."""
-    st = t.stride()
-    inner = shape[-1]
-    if inner > 1 and st[-1] != 1:
-        raise ValueError(f"{name}: the last dimension must be dense")
-    # where there is one row, its distance to the next is any
-    pitch = st[-2] if shape[-2] > 1 else inner
-    outer = st[0] if len(shape) == 3 and shape[0] > 1 else 0
-    if pitch < inner or (outer < inner and len(shape) == 3 and shape[0] > 1):
-        raise ValueError(f"{name}: rows overlap, strides {st}")
-    return pitch, outer, (shape[-2] - 1) * pitch + (shape[0] - 1) * outer + inner
+@functools.lru_cache(maxsize=256)
+def _plan(op, problem):
+    """How one operator's operands of one problem are packed (equal problems share it)."""
+    codes = {"t": DTYPES[problem.dtype], "f": 0, "i": 3}
+    operands = problem._operands()
+    rows, tensors = _OPERANDS[op]
+    entries, at = [], 0
+    for names, is_rows, words in ((rows, True, 5), (tensors, False, 3)):
+        for name in names:
+            shape, kind = operands[name]
+            entries.append((name, at, is_rows, name in _REQUIRED[op], codes[kind], shape))
+            at += words
+    lib = load()
+    c = problem.to_c()
+    length = getattr(lib, f"rk_{op}_scratch_length", None)
+    encode = ctypes.cast(getattr(lib, f"rk_{op}_encode"), ctypes.c_void_p).value
+    # a problem that the entry will refuse has no scratch length: its message says why
+    scratch = -1 if length is None else max(length(ctypes.byref(c)), 0)
+    return _binding().Plan(encode, bytes(c), scratch, entries)
 
 
 class StateSpaceLayer:
@@ -328,69 +323,20 @@ class StateSpaceLayer:
         return self._run("scan_grad", ScanProblem, problem, X, want, stream, tensors)
 
     def _run(self, op, kind, problem, X, want, stream, tensors):
-        import torch
         if type(problem) is not kind:
             raise TypeError(f"{op}: expected {kind.__name__}, got {type(problem).__name__}")
-        if not X.is_cuda:
-            raise ValueError("X: expected a CUDA tensor")
-        device = X.device
-        current = torch.cuda.current_stream(device)
-        if stream is not None and stream != current:
-            # memory made here belongs to that stream; what the caller passes is
-            # kept from reuse until the stream is past this call
-            with torch.cuda.stream(stream):
-                out = self._run(op, kind, problem, X, want, None, tensors)
-            for t in (X, *tensors.values()):
-                if t is not None:
-                    t.record_stream(stream)
-            return out
-        if device.index != torch.cuda.current_device():
-            with torch.cuda.device(device):
-                return self._run(op, kind, problem, X, want, None, tensors)
-        plan = problem._plan(op)
-        entry = plan.entry
-        vals = [0] * plan.size
-        tensors["X"] = X
-        out = {}
-        for name in want:
-            t = tensors.get(name)
-            if t is None:
-                if name not in entry:
-                    raise KeyError(name)
-                _, _, shape, dtype = entry[name]
-                tensors[name] = t = torch.empty(shape, dtype=dtype, device=device)
-            out[name] = t
-        for name, t in tensors.items():
-            if t is None:
-                continue
-            if name not in entry:
-                raise KeyError(name)
-            at, rows, shape, dtype = entry[name]
-            if t.dtype != dtype:
-                raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-            if t.shape != shape:
-                raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
-            if t.device != device:
-                raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
-            n = t.numel()
-            if rows:
-                if n and not t.is_contiguous():
-                    vals[at + 3], vals[at + 4], n = _pitches(name, t, shape)
-            elif not t.is_contiguous():
-                raise ValueError(f"{name}: must be contiguous")
-            vals[at] = t.data_ptr()
-            vals[at + 2] = n
-        for name in _REQUIRED[op]:
-            if tensors.get(name) is None:
-                raise ValueError(f"{op}: {name} is required")
-        args = (self.handle, problem._ref, plan.pack(*vals))
-        if plan.scratch is not None:
-            if plan.scratch > 0:
-                work = torch.empty(plan.scratch, dtype=torch.float32, device=device)
-                args += (struct.pack("=Qqq", work.data_ptr(), 0, plan.scratch),)
-            else:
-                args += (None,)
-        st = plan.call(*args, current.cuda_stream)
-        if st != RK_OK:
-            raise RkError(st, rk_last_error(self.handle))
+        if stream is not None:
+            import torch
+            if stream != torch.cuda.current_stream(X.device):
+                # memory made here belongs to that stream; what the caller passes is
+                # kept from reuse until the stream is past this call
+                with torch.cuda.stream(stream):
+                    out = self._run(op, kind, problem, X, want, None, tensors)
+                for t in (X, *tensors.values()):
+                    if t is not None:
+                        t.record_stream(stream)
+                return out
+        out = problem._plan(op).run(self.handle, X, want, tensors)
+        if type(out) is int:
+            raise RkError(out, rk_last_error(self.handle))
         return out

@@ -173,19 +173,19 @@ def test_structs_are_packed_as_declared():
         assert ctypes.sizeof(struct) == 40 * len(rows) + 24 * len(tensors)
 
 
-def test_row_distance():
+def test_row_distance(handle):
     """Slices of wider rows, steps of longer sequences and transposed views are
-    taken as they are; rows that are not dense or that overlap are refused."""
+    taken as they are; rows that are not dense or that overlap are not."""
+    pitches = ss._binding().row_pitches
     wide = torch.zeros(5, 3, 16)
-    assert ss._pitches("X", wide[..., :4], (5, 3, 4)) == (16, 48, 4 * 48 + 2 * 16 + 4)
-    assert ss._pitches("X", wide[:, :2, 4:], (5, 2, 12)) == (16, 48, 4 * 48 + 16 + 12)
-    assert ss._pitches("X", wide[:, :1, 4:], (5, 1, 12)) == (12, 48, 4 * 48 + 12)
-    assert ss._pitches("X", wide[:1, :, 4:], (1, 3, 12)) == (16, 0, 2 * 16 + 12)
-    assert ss._pitches("X", wide.transpose(0, 1), (3, 5, 16)) == (48, 16, 4 * 48 + 2 * 16 + 16)
-    assert ss._pitches("X", torch.zeros(7, 9)[:, :2], (7, 2)) == (9, 0, 6 * 9 + 2)
+    assert pitches(wide[..., :4]) == (16, 48, 4 * 48 + 2 * 16 + 4)
+    assert pitches(wide[:, :2, 4:]) == (16, 48, 4 * 48 + 16 + 12)
+    assert pitches(wide[:, :1, 4:]) == (12, 48, 4 * 48 + 12)
+    assert pitches(wide[:1, :, 4:]) == (16, 0, 2 * 16 + 12)
+    assert pitches(wide.transpose(0, 1)) == (48, 16, 4 * 48 + 2 * 16 + 16)
+    assert pitches(torch.zeros(7, 9)[:, :2]) == (9, 0, 6 * 9 + 2)
     for bad in (wide[..., ::2], torch.zeros(1, 1, 4).expand(5, 3, 4), torch.zeros(5, 1, 4).expand(5, 3, 4)):
-        with pytest.raises(ValueError):
-            ss._pitches("X", bad, tuple(bad.shape))
+        assert pitches(bad) is None
 
 
 def test_overlapping_rows_are_refused(handle):
