@@ -3,9 +3,9 @@
 // Per step, channel and state: one exponential, a = exp(dt A), and the update
 // h = a h + (dt u) B, y += C h.  A thread keeps K states of one channel in
 // registers and runs along the steps; TPC neighbouring threads share a channel
-// of more states and add their parts of y by shuffles.  Every step's dt, u, B
-// and C are staged in shared memory by the whole block, in 16-byte loads, so
-// softplus is taken once per element and not once per thread.
+// of more states and add their parts of y by shuffles.  B and C are the same
+// for all channels of a group: the block stages them in shared memory as
+// float32.  A channel's own elements go from global memory to its thread.
 //
 // One sequence of a few thousand channels does not fill the card, so the
 // sequence is cut into chunks that run side by side.  The state that leaves a
@@ -14,6 +14,7 @@
 // runs through the chunks in order, and a third starts each chunk from its
 // state and computes the outputs.
 #include <algorithm>
+#include <type_traits>
 
 #include "rk.h"
 #include "rk_ssm_common.cuh"
@@ -21,195 +22,228 @@
 namespace rk {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kSub = 16;  // steps staged at once
+constexpr int kThreads = 128;  // most threads of a block
+constexpr int kBlocks = 5;     // of them per SM: what 96 registers per thread leave room for
+constexpr int kGroup = 4;      // steps whose elements are loaded ahead, while the group before is computed
 
-template <typename T, int V, int NSP>
-__device__ __forceinline__ void stage_group(const RowsArg& src, int n, int g, int states, int t, int live,
-                                            float (*dst)[NSP]) {
-  constexpr int kPieces = NSP / V;
-  for (int i = threadIdx.x; i < kSub * kPieces; i += kThreads) {
-    const int r = i / kPieces, k = i % kPieces * V;
-    float v[V];
-    if (t + r < live && k < states) {
-      Piece<T, V>::load(static_cast<const T*>(src.p) + n * src.ns + (t + r) * src.ss + (long long)g * states + k, v);
-    } else {
-      fill(v, 0.0f);
-    }
-#pragma unroll
-    for (int j = 0; j < V; ++j) dst[r][k + j] = v[j];
-  }
+// Steps of B and C staged at once.
+template <int PADDED>
+constexpr int kSubSteps = PADDED <= 32 ? 16 : 8;
+
+// Threads per channel, for 16 states per thread.
+constexpr int tpc_of(int states) { return states <= 16 ? 1 : states <= 32 ? 2 : states <= 64 ? 4 : 8; }
+
+// Threads of a block: the most whose channel tiles waste little of a group.
+int block_threads(int per, int states) {
+  const int tpc = tpc_of(states);
+  auto padded = [&](int nt) {
+    const long long ch = nt / tpc;
+    return (per + ch - 1) / ch * ch;
+  };
+  for (int nt = kThreads; nt > 32; nt /= 2)
+    if (padded(nt) * 15 <= padded(32) * 16) return nt;
+  return 32;
 }
 
-// K states per thread, TPC threads per channel.  OUT: the outputs, each chunk
-// from its own start; else every chunk's final state from zero and its sum of dt.
+// B and C of a subtile in shared memory, as float32: B's steps, then C's.
+template <typename T, int NSP, int TT, bool WITH_C>
+struct GroupTile {
+  static constexpr int kRow = NSP / 4;  // float4s of a step's row
+  static constexpr int kQuads = TT * kRow;
+  static constexpr int kAll = WITH_C ? 2 * kQuads : kQuads;
+  float4 v[kAll];
+
+  __device__ __forceinline__ void put(const ScanParams& p, int n, int g, int t, int live) {
+    for (int i = threadIdx.x; i < kAll; i += blockDim.x) {
+      const bool is_c = WITH_C && i >= kQuads;
+      const RowsArg& src = is_c ? p.Cm : p.Bm;
+      const int j = is_c ? i - kQuads : i;
+      const int s = t + j / kRow, k = j % kRow * 4;
+      float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (s < live && k < p.K) {
+        const T* from = static_cast<const T*>(src.p) + n * src.ns + s * src.ss + (long long)g * p.K + k;
+        if (p.bc_vec) {
+          Piece<T, 4>::load(from, x);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (k + e < p.K) x[e] = Elem<T>::to_f(from[e]);
+        }
+      }
+      v[i] = make_float4(x[0], x[1], x[2], x[3]);
+    }
+  }
+};
+
+// K states of one channel per thread, TPC threads per channel, two states to
+// a packed register.  OUT: the outputs, each chunk from its own start; else
+// every chunk's final state from zero and its sum of dt.  A group's elements
+// are loaded while the group before is computed; two buffers of B and C need
+// one barrier per subtile.
 template <typename T, int K, int TPC, bool OUT>
-__global__ void __launch_bounds__(kThreads) scan_kernel(ScanParams p) {
-  constexpr int CH = kThreads / TPC, NSP = K * TPC;
-  __shared__ float2 sd[kSub][CH];  // dt, u
-  __shared__ __align__(16) float sB[kSub][NSP];
-  __shared__ __align__(16) float sC[OUT ? kSub : 1][NSP];
-  __shared__ float sY[OUT ? kSub : 1][CH];
-  __shared__ float sbias[CH], sskip[CH];
+__global__ void __launch_bounds__(kThreads, kBlocks) scan_kernel(ScanParams p) {
+  constexpr int NSP = K * TPC, TT = kSubSteps<NSP>, P = K / 2;
+  using Tile = GroupTile<T, NSP, TT, OUT>;
+  __shared__ Tile bc[2];
+  const int CH = blockDim.x / TPC;
   const int per = p.C / p.G, tiles = (per + CH - 1) / CH;
   const int tile = blockIdx.x % tiles;
   int q = blockIdx.x / tiles;
   const int g = q % p.G;
   q /= p.G;
   const int chunk = q % p.chunks, n = q / p.chunks;
-  const int c0 = g * per + tile * CH, width = min(CH, per - tile * CH);
   const int t0 = chunk * p.chunk, t1 = min(t0 + p.chunk, p.S);
   const int live = min(t1, row_length(p.lens, n, p.S));
-  const int lc = threadIdx.x / TPC, part = threadIdx.x % TPC;
-  const bool mine = lc < width;
-  const int c = c0 + (mine ? lc : 0);
+  const int lc = tile * CH + threadIdx.x / TPC, part = threadIdx.x % TPC;
+  const bool mine = lc < per;
+  const int c = g * per + (mine ? lc : 0);
   const long long row = ((long long)n * p.chunks + chunk) * p.C + c;
 
-  for (int i = threadIdx.x; i < CH; i += kThreads) {
-    sbias[i] = (p.bias && i < width) ? p.bias[c0 + i] : 0.0f;
-    sskip[i] = (p.D && i < width) ? p.D[c0 + i] : 0.0f;
-  }
-  float A2[K], h[K];
-  load_states<K, TPC>(p.A + (long long)c * p.K, p.K, part, A2);
+  const T* delta = static_cast<const T*>(p.Delta.p) + n * p.Delta.ns + t0 * p.Delta.ss + c;
+  const T* x = static_cast<const T*>(p.X.p) + n * p.X.ns + t0 * p.X.ss + c;
+  const T* z = OUT && p.Z.p ? static_cast<const T*>(p.Z.p) + n * p.Z.ns + t0 * p.Z.ss + c : nullptr;
+  T* y = OUT && p.Y.p ? static_cast<T*>(p.Y.p) + n * p.Y.ns + t0 * p.Y.ss + c : nullptr;
+  const bool stores = y != nullptr && mine && part == 0;
+  // elements of the next group; the pointers stand at its first step
+  T nd[kGroup], nu[kGroup], nz[kGroup];
+  auto fetch = [&](int t) {
 #pragma unroll
-  for (int i = 0; i < K; ++i) A2[i] *= kLog2e;
-  fill(h, 0.0f);
-  if (OUT) {
-    if (p.chunks > 1) load_states<K, TPC>(p.carry + row * p.K, p.K, part, h);
-    else if (p.h0) load_states<K, TPC>(p.h0 + ((long long)n * p.C + c) * p.K, p.K, part, h);
+    for (int i = 0; i < kGroup; ++i) {
+      if (t + i < live) {
+        nd[i] = *delta, nu[i] = *x;
+        delta += p.Delta.ss, x += p.X.ss;
+        if (OUT && z) {
+          nz[i] = *z;
+          z += p.Z.ss;
+        }
+      }
+    }
+  };
+  if (t0 < live) {
+    fetch(t0);
+    bc[0].put(p, n, g, t0, live);
   }
+  const float bias = p.bias ? p.bias[c] : 0.0f;
+  const float skip = OUT && p.D ? p.D[c] : 0.0f;
+  F2 A2[P], h[P];
   float sum = 0.0f;
+  {
+    float a[K], v[K];
+    load_states<K, TPC>(p.A + (long long)c * p.K, p.K, part, a);
+    fill(v, 0.0f);
+    if (OUT) {
+      if (p.chunks > 1) load_states<K, TPC>(p.carry + row * p.K, p.K, part, v);
+      else if (p.h0) load_states<K, TPC>(p.h0 + ((long long)n * p.C + c) * p.K, p.K, part, v);
+    }
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      A2[i] = f2(rate2(a[2 * i]), rate2(a[2 * i + 1]));
+      h[i] = f2(v[2 * i], v[2 * i + 1]);
+    }
+  }
   __syncthreads();
 
-  auto stage = [&](auto piece, int t) {
-    constexpr int V = decltype(piece)::value;
-    constexpr int kPieces = CH / V > 0 ? CH / V : 1;
-    for (int i = threadIdx.x; i < kSub * kPieces; i += kThreads) {
-      const int r = i / kPieces, x = i % kPieces * V;
-      float d[V], u[V];
-      const bool on = t + r < live && x < width;
-      if (on) {
-        Piece<T, V>::load(static_cast<const T*>(p.Delta.p) + n * p.Delta.ns + (t + r) * p.Delta.ss + c0 + x, d);
-        Piece<T, V>::load(static_cast<const T*>(p.X.p) + n * p.X.ns + (t + r) * p.X.ss + c0 + x, u);
-      }
+  int b = 0;
+  for (int t = t0; t < live; t += TT, b ^= 1) {
+    if (t + TT < live) bc[b ^ 1].put(p, n, g, t + TT, live);
+#pragma unroll 1
+    for (int r = 0; r < TT && t + r < live; r += kGroup) {
+      T d[kGroup], u[kGroup], zz[kGroup];
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        float dt = 0.0f, uu = 0.0f;
-        if (on) {
-          dt = d[j] + sbias[x + j];
-          if (p.softplus) dt = softplus_f(dt);
-          uu = u[j];
+      for (int i = 0; i < kGroup; ++i) d[i] = nd[i], u[i] = nu[i], zz[i] = nz[i];
+      fetch(t + r + kGroup);
+      const ulonglong2* B = reinterpret_cast<const ulonglong2*>(&bc[b].v[r * Tile::kRow + part]);
+      const int steps = live - t - r;  // of the group; the rest stands still
+#pragma unroll
+      for (int i = 0; i < kGroup; ++i, B += Tile::kRow) {
+        const bool on = i < steps;
+        float dt = Elem<T>::to_f(d[i]) + bias, uu = Elem<T>::to_f(u[i]);
+        if (p.softplus) dt = softplus_f(dt);
+        if (!on) dt = 0.0f, uu = 0.0f;
+        const float du = dt * uu;
+        const F2 dt2 = f2(dt, dt), du2 = f2(du, du);
+        F2 y0 = f2(0.0f, 0.0f), y1 = y0;
+#pragma unroll
+        for (int k = 0; k < K / 4; ++k) {
+          const ulonglong2 v = B[k * TPC];
+          h[2 * k] = fma2(exp2_fast2(mul2(dt2, A2[2 * k])), h[2 * k], mul2(du2, F2{v.x}));
+          h[2 * k + 1] = fma2(exp2_fast2(mul2(dt2, A2[2 * k + 1])), h[2 * k + 1], mul2(du2, F2{v.y}));
+          if constexpr (OUT) {
+            const ulonglong2 e = B[Tile::kQuads + k * TPC];
+            y0 = k == 0 ? mul2(F2{e.x}, h[0]) : fma2(F2{e.x}, h[2 * k], y0);
+            y1 = k == 0 ? mul2(F2{e.y}, h[1]) : fma2(F2{e.y}, h[2 * k + 1], y1);
+          }
         }
-        sd[r][x + j] = make_float2(dt, uu);
-      }
-    }
-  };
-  auto emit = [&](auto piece, int t) {
-    constexpr int V = decltype(piece)::value;
-    constexpr int kPieces = CH / V > 0 ? CH / V : 1;
-    for (int i = threadIdx.x; i < kSub * kPieces; i += kThreads) {
-      const int r = i / kPieces, x = i % kPieces * V;
-      if (t + r >= live || x >= width) continue;
-      float y[V];
-#pragma unroll
-      for (int j = 0; j < V; ++j) y[j] = fmaf(sskip[x + j], sd[r][x + j].y, sY[r][x + j]);
-      if (p.Z.p) {
-        float z[V];
-        Piece<T, V>::load(static_cast<const T*>(p.Z.p) + n * p.Z.ns + (t + r) * p.Z.ss + c0 + x, z);
-#pragma unroll
-        for (int j = 0; j < V; ++j) y[j] *= z[j] * sigmoid_fast(z[j]);
-      }
-      Piece<T, V>::store(static_cast<T*>(p.Y.p) + n * p.Y.ns + (t + r) * p.Y.ss + c0 + x, y);
-    }
-  };
-  using Wide = std::integral_constant<int, (CH >= kPiece<T> ? kPiece<T> : 1)>;
-  using One = std::integral_constant<int, 1>;
-
-  for (int t = t0; t < live; t += kSub) {
-    if (p.vec) stage(Wide{}, t);
-    else stage(One{}, t);
-    if (p.bc_vec) {
-      stage_group<T, 4, NSP>(p.Bm, n, g, p.K, t, live, sB);
-      if constexpr (OUT) stage_group<T, 4, NSP>(p.Cm, n, g, p.K, t, live, sC);
-    } else {
-      stage_group<T, 1, NSP>(p.Bm, n, g, p.K, t, live, sB);
-      if constexpr (OUT) stage_group<T, 1, NSP>(p.Cm, n, g, p.K, t, live, sC);
-    }
-    __syncthreads();
-    const int steps = min(kSub, live - t);
-#pragma unroll 4
-    for (int r = 0; r < steps; ++r) {
-      const float2 v = sd[r][lc];
-      const float dtu = v.x * v.y;
-      float y = 0.0f;
-#pragma unroll
-      for (int i = 0; i < K; i += 4) {
-        const int k = state_of<TPC>(i, part);
-        const float4 b = *reinterpret_cast<const float4*>(&sB[r][k]);
-        h[i] = fmaf(exp2_fast(v.x * A2[i]), h[i], dtu * b.x);
-        h[i + 1] = fmaf(exp2_fast(v.x * A2[i + 1]), h[i + 1], dtu * b.y);
-        h[i + 2] = fmaf(exp2_fast(v.x * A2[i + 2]), h[i + 2], dtu * b.z);
-        h[i + 3] = fmaf(exp2_fast(v.x * A2[i + 3]), h[i + 3], dtu * b.w);
         if constexpr (OUT) {
-          const float4 e = *reinterpret_cast<const float4*>(&sC[r][k]);
-          y = fmaf(e.x, h[i], y);
-          y = fmaf(e.y, h[i + 1], y);
-          y = fmaf(e.z, h[i + 2], y);
-          y = fmaf(e.w, h[i + 3], y);
-        }
-      }
-      if constexpr (OUT) {
+          const float2 s2 = f2_get(add2(y0, y1));
+          float o = s2.x + s2.y;
 #pragma unroll
-        for (int o = TPC / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-        if (part == 0) sY[r][lc] = y;
-      } else {
-        sum += v.x;
+          for (int m = TPC / 2; m > 0; m >>= 1) o += __shfl_xor_sync(0xffffffffu, o, m);
+          o = fmaf(skip, uu, o);
+          if (z) {
+            const float zf = Elem<T>::to_f(zz[i]);
+            o *= zf * sigmoid_fast(zf);
+          }
+          if (on && stores) *y = Elem<T>::from_f(o);
+          y += p.Y.ss;
+        } else {
+          sum += dt;
+        }
       }
     }
     __syncthreads();
-    if constexpr (OUT) {
-      if (p.Y.p) {
-        if (p.vec) emit(Wide{}, t);
-        else emit(One{}, t);
-      }
-      __syncthreads();
+  }
+  if (!mine) return;
+  if constexpr (OUT) {
+    if (stores) {
+      const int from = max(t0, live);
+      y = static_cast<T*>(p.Y.p) + n * p.Y.ns + from * p.Y.ss + c;
+      for (int t = from; t < t1; ++t, y += p.Y.ss) *y = Elem<T>::from_f(0.0f);
     }
   }
+  float v[K];
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const float2 w = f2_get(h[i]);
+    v[2 * i] = w.x, v[2 * i + 1] = w.y;
+  }
   if constexpr (OUT) {
-    if (p.Y.p) {
-      const int from = max(t0, live);
-      for (int i = threadIdx.x; i < CH; i += kThreads) {
-        if (i >= width) continue;
-        T* y = static_cast<T*>(p.Y.p) + n * p.Y.ns + c0 + i;
-        for (int t = from; t < t1; ++t) y[t * p.Y.ss] = Elem<T>::from_f(0.0f);
-      }
-    }
-    if (p.chunks == 1 && p.hT && mine) store_states<K, TPC>(p.hT + ((long long)n * p.C + c) * p.K, p.K, part, h);
-  } else if (mine) {
-    store_states<K, TPC>(p.carry + row * p.K, p.K, part, h);
+    if (p.chunks == 1 && p.hT) store_states<K, TPC>(p.hT + ((long long)n * p.C + c) * p.K, p.K, part, v);
+  } else {
+    store_states<K, TPC>(p.carry + row * p.K, p.K, part, v);
     if (part == 0) p.sumdt[row] = sum;
   }
 }
 
 // Runs through the chunks of each (sequence, channel, state): the state each
 // starts from takes the place of its own final state.
-__global__ void __launch_bounds__(256) scan_carry_kernel(ScanParams p) {
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+__global__ void __launch_bounds__(64) scan_carry_kernel(ScanParams p) {
+  const long long i = (long long)blockIdx.x * 64 + threadIdx.x;
   const long long ck = (long long)p.C * p.K;
   if (i >= p.N * ck) return;
   const int n = (int)(i / ck);
   const long long at = i % ck;
   const int c = (int)(at / p.K);
-  const float A2 = p.A[at] * kLog2e;
+  const float A2 = rate2(p.A[at]);
   float run = p.h0 ? p.h0[i] : 0.0f;
   float* carry = p.carry + (long long)n * p.chunks * ck + at;
   const float* sumdt = p.sumdt + (long long)n * p.chunks * p.C + c;
-#pragma unroll 4
-  for (int q = 0; q < p.chunks; ++q) {
-    const float s = carry[q * ck], d = sumdt[(long long)q * p.C];
-    const float a = d == 0.0f ? 1.0f : exp2_fast(A2 * d);  // a chunk past the length keeps the state, whatever A
-    carry[q * ck] = run;
-    run = fmaf(a, run, s);
+  // a batch is read before any of it is overwritten: its loads are in flight together
+  constexpr int kBatch = 24;
+  for (int q0 = 0; q0 < p.chunks; q0 += kBatch) {
+    float s[kBatch], d[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int q = min(q0 + j, p.chunks - 1);
+      s[j] = carry[q * ck], d[j] = sumdt[(long long)q * p.C];
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      if (q0 + j < p.chunks) {
+        carry[(q0 + j) * ck] = run;
+        run = fmaf(exp2_fast(A2 * d[j]), run, s[j]);
+      }
+    }
   }
   if (p.hT) p.hT[i] = run;
 }
@@ -217,15 +251,18 @@ __global__ void __launch_bounds__(256) scan_carry_kernel(ScanParams p) {
 // A few steps: four states per thread, TPC threads per channel, the state
 // read and written once in 16-byte pieces and everything else straight from
 // global memory.  Bound by the state's bytes.
+constexpr int kStepThreads = 128;
 template <typename T, int TPC>
-__global__ void __launch_bounds__(kThreads) scan_step_kernel(ScanParams p) {
-  const long long item = ((long long)blockIdx.x * kThreads + threadIdx.x) / TPC;
+__global__ void __launch_bounds__(kStepThreads) scan_step_kernel(ScanParams p) {
+  const long long item = ((long long)blockIdx.x * kStepThreads + threadIdx.x) / TPC;
   const int part = threadIdx.x % TPC;
   const bool mine = item < (long long)p.N * p.C;
   const int n = mine ? (int)(item / p.C) : 0, c = mine ? (int)(item % p.C) : 0;
   const int g = c / (p.C / p.G);
   float A2[4], h[4];
   load_states<4, TPC>(p.A + (long long)c * p.K, p.K, part, A2);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) A2[i] = rate2(A2[i]);
   fill(h, 0.0f);
   if (p.h0) load_states<4, TPC>(p.h0 + ((long long)n * p.C + c) * p.K, p.K, part, h);
   const int len = row_length(p.lens, n, p.S);
@@ -255,7 +292,7 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(ScanParams p) {
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        h[j] = fmaf(exp2_fast(dt * A2[j] * kLog2e), h[j], dt * u * b[j]);
+        h[j] = fmaf(exp2_fast(dt * A2[j]), h[j], dt * u * b[j]);
         y = fmaf(e[j], h[j], y);
       }
       if (part == 0) y = fmaf(skip, u, y);
@@ -275,18 +312,18 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(ScanParams p) {
 
 template <typename T, int K, int TPC>
 cudaError_t run_scan(const ScanParams& p, cudaStream_t s, int* launches) {
-  constexpr int CH = kThreads / TPC;
+  const int nt = block_threads(p.C / p.G, p.K), CH = nt / TPC;
   const long long tiles = (p.C / p.G + CH - 1) / CH;
   const long long blocks = (long long)p.N * p.chunks * p.G * tiles;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   if (p.chunks > 1) {
-    scan_kernel<T, K, TPC, false><<<(unsigned)blocks, kThreads, 0, s>>>(p);
+    scan_kernel<T, K, TPC, false><<<(unsigned)blocks, nt, 0, s>>>(p);
     const long long states = (long long)p.N * p.C * p.K;
-    scan_carry_kernel<<<(unsigned)((states + 255) / 256), 256, 0, s>>>(p);
+    scan_carry_kernel<<<(unsigned)((states + 63) / 64), 64, 0, s>>>(p);
     *launches += 2;
   }
   if (p.Y.p || p.chunks == 1) {
-    scan_kernel<T, K, TPC, true><<<(unsigned)blocks, kThreads, 0, s>>>(p);
+    scan_kernel<T, K, TPC, true><<<(unsigned)blocks, nt, 0, s>>>(p);
     *launches += 1;
   }
   return cudaGetLastError();
@@ -295,7 +332,7 @@ cudaError_t run_scan(const ScanParams& p, cudaStream_t s, int* launches) {
 template <typename T, int TPC>
 cudaError_t run_step(const ScanParams& p, cudaStream_t s, int* launches) {
   const long long threads = (long long)p.N * p.C * TPC;
-  scan_step_kernel<T, TPC><<<(unsigned)((threads + kThreads - 1) / kThreads), kThreads, 0, s>>>(p);
+  scan_step_kernel<T, TPC><<<(unsigned)((threads + kStepThreads - 1) / kStepThreads), kStepThreads, 0, s>>>(p);
   *launches += 1;
   return cudaGetLastError();
 }
@@ -327,16 +364,15 @@ ScanPlan scan_plan(long long seq, long long batch, long long channels, int state
   pl.chunks = 1;
   pl.chunk = (int)std::max<long long>(seq, 1);
   if (seq <= kStepSeq || batch == 0) return pl;
-  const int tpc = state <= 16 ? 1 : state <= 32 ? 2 : state <= 64 ? 4 : 8;
-  const long long per = channels / groups, ch = kThreads / tpc;
-  const long long blocks = batch * groups * ((per + ch - 1) / ch);
-  // blocks that fill the card: five of 128 threads per SM
-  const long long want = kPlanSms * 5;
-  if (blocks < want / 2) {
-    const long long most = std::max<long long>(seq / 64, 1);
-    const long long chunks = std::min(most, std::max<long long>(want / blocks, 1));
+  const int nt = block_threads((int)(channels / groups), state);
+  const long long per = channels / groups, ch = nt / tpc_of(state);
+  const long long warps = batch * groups * ((per + ch - 1) / ch) * (nt / 32);
+  // warps that the card holds: registers for 20 per SM
+  const long long want = kPlanSms * kBlocks * (kThreads / 32);
+  if (warps * 3 < want) {
+    const long long chunks = std::min(want / warps, seq / 32);
     if (chunks > 1) {
-      pl.chunk = (int)((((seq + chunks - 1) / chunks) + kSub - 1) / kSub * kSub);
+      pl.chunk = (int)((((seq + chunks - 1) / chunks) + 7) / 8 * 8);
       pl.chunks = (int)((seq + pl.chunk - 1) / pl.chunk);
     }
   }

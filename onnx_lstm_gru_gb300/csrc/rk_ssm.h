@@ -80,7 +80,7 @@ struct ScanParams {
   RowsArg X, Delta, Bm, Cm, Z, Y;
   RowsArg dY, dX, dDelta, dB, dC, dZ;
   int vec;             // every operand with rows of C elements takes 16-byte pieces
-  int bc_vec;          // and those with rows of G * K, in pieces within a group
+  int bc_vec;          // operands with rows of G * K take pieces of four within a group
   const float* A;
   const float* D;
   const float* bias;

@@ -131,10 +131,10 @@ struct Call {
     if (p->layout == 1) std::swap(a.ss, a.ns);
     return a;
   }
-  // Likewise for pieces of four elements.
-  static bool fours(const RowsArg& a, int eb, int group) {
-    return a.p == nullptr || (reinterpret_cast<uintptr_t>(a.p) % (4 * eb) == 0 && a.ss % 4 == 0 && a.ns % 4 == 0 &&
-                              group % 4 == 0);
+  // Likewise for pieces of m elements.
+  static bool pieces(const RowsArg& a, int m, int eb, int group) {
+    return a.p == nullptr || (reinterpret_cast<uintptr_t>(a.p) % (m * eb) == 0 && a.ss % m == 0 && a.ns % m == 0 &&
+                              group % m == 0);
   }
   void cuda(const char* what, cudaError_t e) {
     if (!ok() || e == cudaSuccess) return;
@@ -274,7 +274,7 @@ rk::ScanParams scan_params(Call& c, const rk_scan_problem* p, const O* o) {
   sp.lens = c.tensor<int>("sequence_lens", o->sequence_lens, p->batch, 4);
   sp.h0 = c.tensor<float>("initial_state", o->initial_state, states * K, 4);
   sp.vec = sp.X.vec && sp.Delta.vec && sp.Z.vec;
-  sp.bc_vec = Call::fours(sp.Bm, c.eb, K) && Call::fours(sp.Cm, c.eb, K);
+  sp.bc_vec = Call::pieces(sp.Bm, 4, c.eb, K) && Call::pieces(sp.Cm, 4, c.eb, K);
   return sp;
 }
 
@@ -438,7 +438,6 @@ rk_status rk_scan_encode(rk_handle* h, const rk_scan_problem* p, const rk_scan_o
   rk::ScanParams sp = scan_params(c, p, o);
   sp.Y = c.steps("Y", o->Y, p, p->channels, (int)(p->channels / p->groups), false);
   sp.hT = c.tensor<float>("final_state", o->final_state, states, 4);
-  sp.vec = sp.vec && sp.Y.vec;
   if (!c.ok()) return c.st;
   if (rows == 0) {
     c.copy(sp.hT, sp.h0, states * 4, s);

@@ -78,16 +78,111 @@ __device__ __forceinline__ float exp2_fast(float x) {
 }
 constexpr float kLog2e = 1.4426950408889634f;
 
-__device__ __forceinline__ float sigmoid_fast(float x) { return __fdividef(1.0f, 1.0f + exp2_fast(-kLog2e * x)); }
+// 1 / x by the special function unit (relative error about 2^-23; 0 for an infinite x).
+__device__ __forceinline__ float rcp_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
-// log(1 + e^x); x itself where e^-x is lost beside it.
-__device__ __forceinline__ float softplus_f(float x) { return x > 20.0f ? x : log1pf(__expf(x)); }
+__device__ __forceinline__ float sigmoid_fast(float x) { return rcp_fast(1.0f + exp2_fast(-kLog2e * x)); }
+
+// log(1 + e^x) = max(x, 0) + log(1 + e) with e = e^-|x| <= 1, and
+// log(1 + e) = 2 artanh(s), s = e / (2 + e) <= 1/3; artanh(s) / s is a
+// polynomial in s^2, interpolated at the Chebyshev nodes of [0, 1/9] (relative
+// error 4e-9).  Nothing of a small result (steps of a thousandth are common)
+// is lost to 1 + e.
+__device__ __forceinline__ float softplus_f(float x) {
+  const float n = -(fabsf(x) < 100.0f ? fabsf(x) : 100.0f), t = n * kLog2e;
+  // what the product rounded away (its own factor's rounding too), put back
+  // behind the exponential
+  const float lo = fmaf(n, kLog2e, -t) + n * 1.9259629911e-8f;
+  const float e0 = exp2_fast(t), e = fmaf(e0, lo * 0.6931471806f, e0);
+  const float s = e * rcp_fast(2.0f + e), q = s * s;
+  float r = fmaf(q, 0.14078889f, 0.13982579f);
+  r = fmaf(r, q, 0.20012298f);
+  r = fmaf(r, q, 0.33333161f);
+  r = fmaf(r, q, 1.0f);
+  const float y = fmaf(2.0f * s, r, fmaxf(x, 0.0f));
+  return x == x ? y : x;  // the comparisons above drop a NaN
+}
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
+
+// Two float32 in one register pair: the packed forms take one issue slot for
+// two results.
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 f2_get(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 exp2_fast2(F2 x) {
+  const float2 t = f2_get(x);
+  return f2(exp2_fast(t.x), exp2_fast(t.y));
+}
+
+// softplus_f and x sigmoid(x) of two values.
+__device__ __forceinline__ F2 softplus2(F2 x) {
+  const float2 v = f2_get(x);
+  const float a = fabsf(v.x) < 100.0f ? fabsf(v.x) : 100.0f, b = fabsf(v.y) < 100.0f ? fabsf(v.y) : 100.0f;
+  const F2 n = f2(-a, -b), l = f2(kLog2e, kLog2e), t = mul2(n, l);
+  const float2 tv = f2_get(t);
+  const F2 lo = fma2(n, f2(1.9259629911e-8f, 1.9259629911e-8f), fma2(n, l, f2(-tv.x, -tv.y)));
+  const F2 e0 = exp2_fast2(t), e = fma2(e0, mul2(lo, f2(0.6931471806f, 0.6931471806f)), e0);
+  const float2 d = f2_get(add2(e, f2(2.0f, 2.0f)));
+  const F2 s = mul2(e, f2(rcp_fast(d.x), rcp_fast(d.y))), q = mul2(s, s);
+  F2 r = fma2(q, f2(0.14078889f, 0.14078889f), f2(0.13982579f, 0.13982579f));
+  r = fma2(r, q, f2(0.20012298f, 0.20012298f));
+  r = fma2(r, q, f2(0.33333161f, 0.33333161f));
+  r = fma2(r, q, f2(1.0f, 1.0f));
+  const float2 y = f2_get(fma2(add2(s, s), r, f2(fmaxf(v.x, 0.0f), fmaxf(v.y, 0.0f))));
+  return f2(v.x == v.x ? y.x : v.x, v.y == v.y ? y.y : v.y);
+}
+__device__ __forceinline__ F2 silu2(F2 x) {
+  const F2 e = exp2_fast2(mul2(x, f2(-kLog2e, -kLog2e)));
+  const float2 d = f2_get(add2(e, f2(1.0f, 1.0f)));
+  return mul2(x, f2(rcp_fast(d.x), rcp_fast(d.y)));
+}
+
+// A decay rate in base-2 exponents per unit of dt, finite, so that a step of
+// dt = 0 keeps the state whatever the rate.
+__device__ __forceinline__ float rate2(float a) { return fminf(fmaxf(a * kLog2e, -3.0e38f), 3.0e38f); }
+
+// Asynchronous copies of BYTES (4, 8 or 16) from global to shared memory, and
+// the wait for all that this thread has issued.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* to, const void* from) {
+  const uint32_t dst = (uint32_t)__cvta_generic_to_shared(to);
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(from), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // A row's length, clamped to the steps there are.
 __device__ __forceinline__ int row_length(const int* lens, int n, int S) {
