@@ -129,11 +129,11 @@ __global__ void __launch_bounds__(kThreads, kBlocks) scan_kernel(ScanParams p) {
   float sum = 0.0f;
   {
     float a[K], v[K];
-    load_states<K, TPC>(p.A + (long long)c * p.K, p.K, part, a);
+    load_states<K, TPC>(p.A + (long long)c * p.K, p.K, part, p.k_vec, a);
     fill(v, 0.0f);
     if (OUT) {
-      if (p.chunks > 1) load_states<K, TPC>(p.carry + row * p.K, p.K, part, v);
-      else if (p.h0) load_states<K, TPC>(p.h0 + ((long long)n * p.C + c) * p.K, p.K, part, v);
+      if (p.chunks > 1) load_states<K, TPC>(p.carry + row * p.K, p.K, part, p.k_vec, v);
+      else if (p.h0) load_states<K, TPC>(p.h0 + ((long long)n * p.C + c) * p.K, p.K, part, p.k_vec, v);
     }
 #pragma unroll
     for (int i = 0; i < P; ++i) {
@@ -208,9 +208,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks) scan_kernel(ScanParams p) {
     v[2 * i] = w.x, v[2 * i + 1] = w.y;
   }
   if constexpr (OUT) {
-    if (p.chunks == 1 && p.hT) store_states<K, TPC>(p.hT + ((long long)n * p.C + c) * p.K, p.K, part, v);
+    if (p.chunks == 1 && p.hT) store_states<K, TPC>(p.hT + ((long long)n * p.C + c) * p.K, p.K, part, p.k_vec, v);
   } else {
-    store_states<K, TPC>(p.carry + row * p.K, p.K, part, v);
+    store_states<K, TPC>(p.carry + row * p.K, p.K, part, p.k_vec, v);
     if (part == 0) p.sumdt[row] = sum;
   }
 }
@@ -260,11 +260,11 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(ScanParams p) {
   const int n = mine ? (int)(item / p.C) : 0, c = mine ? (int)(item % p.C) : 0;
   const int g = c / (p.C / p.G);
   float A2[4], h[4];
-  load_states<4, TPC>(p.A + (long long)c * p.K, p.K, part, A2);
+  load_states<4, TPC>(p.A + (long long)c * p.K, p.K, part, p.k_vec, A2);
 #pragma unroll
   for (int i = 0; i < 4; ++i) A2[i] = rate2(A2[i]);
   fill(h, 0.0f);
-  if (p.h0) load_states<4, TPC>(p.h0 + ((long long)n * p.C + c) * p.K, p.K, part, h);
+  if (p.h0) load_states<4, TPC>(p.h0 + ((long long)n * p.C + c) * p.K, p.K, part, p.k_vec, h);
   const int len = row_length(p.lens, n, p.S);
   const float bias = p.bias ? p.bias[c] : 0.0f, skip = p.D ? p.D[c] : 0.0f;
   for (int t = 0; t < p.S; ++t) {
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(ScanParams p) {
       static_cast<T*>(p.Y.p)[n * p.Y.ns + t * p.Y.ss + c] = Elem<T>::from_f(y);
     }
   }
-  if (mine && p.hT) store_states<4, TPC>(p.hT + ((long long)n * p.C + c) * p.K, p.K, part, h);
+  if (mine && p.hT) store_states<4, TPC>(p.hT + ((long long)n * p.C + c) * p.K, p.K, part, p.k_vec, h);
 }
 
 template <typename T, int K, int TPC>

@@ -7,19 +7,25 @@
 // It needs the states in reverse order.  They are computed again rather than
 // kept: a pass forward leaves the state at the start of every subtile in
 // global memory, and the way back runs one subtile at a time, forward with
-// its states in shared memory and then back.  Of the few bytes per element
+// its states in registers and then back.  Of the few bytes per element
 // that the gradient reads and writes none is per state.
 //
-// Four states per thread, TPC threads per channel.  dB and dC are sums over
-// the channels of a group: over a warp's channels by shuffles, over a block's
-// warps in shared memory, over the blocks in a second launch that adds their
-// slices in order.  dA, dD and d_delta_bias are sums over steps and
-// sequences, kept per block and added the same way.
+// A thread holds four states of two neighbouring channels, TPC threads a pair
+// of channels: what a step loads from shared memory serves two channels, and
+// dB and dC, sums over the channels of a group, are half added up before they
+// leave the registers.  The states of a subtile's eight steps stay in
+// registers.  The sums over states (for du and ddt) and over a warp's channels
+// (for dB and dC) halve the values with each exchange of halves between
+// lanes, so eight values over eight lanes take seven shuffles.  Over a block's
+// warps dB and dC are added in shared memory, over the blocks in a second
+// launch that adds their slices in order.  dA, dD and d_delta_bias are sums
+// over steps and sequences, kept per block and added the same way.
 //
 // Chunks of one sequence that run side by side are joined as in the forward
 // scan; e is linear in what arrives at a chunk's end with the same factor
 // exp(A sum dt), so one launch prepares both directions.
 #include <algorithm>
+#include <type_traits>
 
 #include "rk.h"
 #include "rk_ssm_common.cuh"
@@ -27,127 +33,327 @@
 namespace rk {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
+constexpr int kT = 8;  // steps of a subtile
+constexpr int kHalf = 4;   // of them whose states are in registers at once
+constexpr float kLn2 = 0.6931471805599453f;
 
-// Steps of a subtile, by threads per channel: what the shared memory of two
-// blocks per SM holds.
-constexpr int sub_steps(int tpc) { return (tpc == 2 || tpc == 4) ? 16 : 8; }
 constexpr int tpc_of(int states) {
-  return states <= 4 ? 1 : states <= 8 ? 2 : states <= 16 ? 4 : states <= 32 ? 8 : states <= 64 ? 16 : 32;
+  return states <= 8 ? 2 : states <= 16 ? 4 : states <= 32 ? 8 : states <= 64 ? 16 : 32;
 }
 
-template <int TPC>
-struct GradShape {
-  static constexpr int CH = kThreads / TPC, NSP = 4 * TPC, T = sub_steps(TPC);
-  // floats of shared memory: dt, u, dy, two sums and y per (step, channel);
-  // B, C; the states; the warps' sums of dB and dC; per-channel constants
-  static constexpr int kRows = T * CH;
-  static constexpr size_t smem =
-      sizeof(float) * (6 * kRows + 2 * T * NSP + T * kThreads * 4 + T * kWarps * 2 * NSP + 2 * CH);
+// A block's shared memory.  Rows are steps of the subtile; channel 2 j + e of
+// the tile has place e * P + j.
+template <typename T, int TPC>
+struct GradSmem {
+  static constexpr int P = kThreads / TPC, CH = 2 * P, NSP = 4 * TPC;
+  static constexpr int kPieces = kT * CH * (int)sizeof(T) / 16;  // 16-byte pieces of a row tensor's subtile
+  static constexpr int kQuads = kT * NSP / 4;                    // of B's or C's
+  using Quad = std::conditional_t<sizeof(T) == 4, float4, uint2>;
+  float4 dtu[kT][CH];   // dt, dt, dt u, dt u: packed operands
+  float2 dy[kT][CH];    // dy, dy: past the gate
+  float u[kT][CH];
+  float slope[kT][CH];  // of softplus
+  float gate[kT][CH];   // dY times the gate's slope
+  float y[kT][CH];      // sum of C h
+  float gb[kT][CH];     // sum of g B
+  float th[kT][CH];     // sum of x A, in base-2 rates
+  float B[kT][NSP], C[kT][NSP];
+  float part[kT][kWarps][2 * NSP];  // the warps' sums of dB and dC
+  float acc[kThreads][4];
+  uint4 raw[4][kPieces];  // the next subtile's Delta, X, dY and Z as stored, rows of CH elements
+  uint4 out[3][kPieces];  // this one's dX, dDelta and dZ
+  Quad quads[2][kQuads];  // the next one's B and C
+  float bias[CH], skip[CH];
 };
 
-// A row piece (step t + r, channels x..) of a block's tile, or zeros.
-template <typename T, int V>
-__device__ __forceinline__ void tile_load(const RowsArg& a, int n, int s, int c, float (&o)[V]) {
-  Piece<T, V>::load(static_cast<const T*>(a.p) + n * a.ns + s * a.ss + c, o);
-}
-template <typename T, int V>
-__device__ __forceinline__ void tile_store(const RowsArg& a, int n, int s, int c, const float (&o)[V]) {
-  Piece<T, V>::store(static_cast<T*>(a.p) + n * a.ns + s * a.ss + c, o);
-}
-
-template <typename T, int V, int NSP, int TT>
-__device__ __forceinline__ void stage_group(const RowsArg& src, int n, int g, int states, int t, int live,
-                                            float* dst) {
-  constexpr int kPieces = NSP / V;
-  for (int i = threadIdx.x; i < TT * kPieces; i += kThreads) {
-    const int r = i / kPieces, k = i % kPieces * V;
-    float v[V];
-    if (t + r < live && k < states) {
-      Piece<T, V>::load(static_cast<const T*>(src.p) + n * src.ns + (t + r) * src.ss + (long long)g * states + k, v);
-    } else {
-      fill(v, 0.0f);
-    }
-#pragma unroll
-    for (int j = 0; j < V; ++j) dst[r * NSP + k + j] = v[j];
+// Two neighbouring elements of a row.
+template <typename T>
+struct Duo {
+  T v[2];
+  __device__ __forceinline__ void load(const RowsArg& a, int n, int s, int c, bool second) {
+    const T* p = static_cast<const T*>(a.p) + n * a.ns + s * a.ss + c;
+    v[0] = p[0];
+    v[1] = second ? p[1] : v[0];
   }
-}
+  __device__ __forceinline__ float operator[](int i) const { return Elem<T>::to_f(v[i]); }
+  static __device__ __forceinline__ void store(const RowsArg& a, int n, int s, int c, bool second, float x, float y) {
+    T* p = static_cast<T*>(a.p) + n * a.ns + s * a.ss + c;
+    p[0] = Elem<T>::from_f(x);
+    if (second) p[1] = Elem<T>::from_f(y);
+  }
+};
 
-// What every kernel here works on: one channel tile of one group of one
-// chunk of one sequence.
+// One channel tile of one group of one chunk of one sequence.  fetch() starts
+// the copies of a subtile's elements to shared memory, as stored, while the
+// subtile before is computed; put() turns them into what the steps need:
+// kItems pairs of channels per thread, of one step each and always the same
+// pair.  Operands that do not take 16-byte pieces are read by put() itself.
+// STATES: dt and dt u.  DY: dy too.  ALL: everything the way back needs.
+enum Stage { STATES, DY, ALL };
+
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* to, const void* from) {
+  const uint32_t dst = (uint32_t)__cvta_generic_to_shared(to);
+  if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(from) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(from), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 template <typename T, int TPC>
 struct Tile {
-  using Sh = GradShape<TPC>;
-  static constexpr int CH = Sh::CH, NSP = Sh::NSP, TT = Sh::T;
+  using Sm = GradSmem<T, TPC>;
+  static constexpr int P = Sm::P, CH = Sm::CH, NSP = Sm::NSP, V = kPiece<T>;
+  static constexpr int kItems = kT * P > kThreads ? kT * P / kThreads : 1;
   const ScanParams& p;
-  int n, g, c0, width, t0, t1, live;
-  float *dt, *u, *dy, *sB, *sC, *bias, *skip;
+  Sm& sm;
+  int n, g, c0, width, live;
 
-  template <int V>
-  __device__ __forceinline__ void stage_v(int t, bool grads) {
-    constexpr int kPieces = CH / V > 0 ? CH / V : 1;
-    for (int i = threadIdx.x; i < TT * kPieces; i += kThreads) {
-      const int r = i / kPieces, x = i % kPieces * V;
-      float d[V], uu[V], gy[V];
-      if (t + r < live && x < width) {
-        tile_load<T, V>(p.Delta, n, t + r, c0 + x, d);
-        tile_load<T, V>(p.X, n, t + r, c0 + x, uu);
+  __device__ __forceinline__ int pair_of() const { return threadIdx.x % P; }
+  __device__ __forceinline__ int row_of(int i) const { return threadIdx.x / P + i * (kThreads / P); }
+  __device__ __forceinline__ bool has(int i, int t) const {
+    return row_of(i) < kT && t + row_of(i) < live && 2 * pair_of() < width;
+  }
+
+  __device__ __forceinline__ void fetch_rows(const RowsArg& src, int slot, int t) {
+    const T* base = static_cast<const T*>(src.p) + n * src.ns + t * src.ss + c0;
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          d[j] += bias[x + j];
-          if (p.softplus) d[j] = softplus_f(d[j]);
+    for (int i = threadIdx.x; i < Sm::kPieces; i += kThreads) {
+      const int r = i / (CH / V), x = i % (CH / V) * V;
+      if (t + r < live && x < width) copy_async<16>(&sm.raw[slot][i], base + r * src.ss + x);
+    }
+  }
+  __device__ __forceinline__ void fetch_quads(const RowsArg& src, int slot, int t) {
+    const T* base = static_cast<const T*>(src.p) + n * src.ns + t * src.ss + (long long)g * p.K;
+#pragma unroll
+    for (int i = threadIdx.x; i < Sm::kQuads; i += kThreads) {
+      const int r = i / (NSP / 4), k = i % (NSP / 4) * 4;
+      if (t + r < live && k < p.K) copy_async<sizeof(typename Sm::Quad)>(&sm.quads[slot][i], base + r * src.ss + k);
+    }
+  }
+  template <Stage S>
+  __device__ __forceinline__ void fetch(int t) {
+    if (p.vec) {
+      fetch_rows(p.Delta, 0, t);
+      fetch_rows(p.X, 1, t);
+      if constexpr (S != STATES) {
+        fetch_rows(p.dY, 2, t);
+        if (p.Z.p) fetch_rows(p.Z, 3, t);
+      }
+    }
+    if (p.bc_vec) {
+      fetch_quads(p.Bm, 0, t);
+      if constexpr (S != STATES) fetch_quads(p.Cm, 1, t);
+    }
+  }
+
+  __device__ __forceinline__ void put_quads(const RowsArg& src, int slot, float* to, int t) {
+#pragma unroll
+    for (int i = threadIdx.x; i < Sm::kQuads; i += kThreads) {
+      const int r = i / (NSP / 4), k = i % (NSP / 4) * 4;
+      float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (t + r < live && k < p.K) {
+        if (p.bc_vec) {
+          Piece<T, 4>::load(reinterpret_cast<const T*>(&sm.quads[slot][i]), v);
+        } else {
+          const T* from = static_cast<const T*>(src.p) + n * src.ns + (t + r) * src.ss + (long long)g * p.K + k;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (k + e < p.K) v[e] = Elem<T>::to_f(from[e]);
         }
-        if (grads) {
-          tile_load<T, V>(p.dY, n, t + r, c0 + x, gy);
-          if (p.Z.p) {
-            float z[V];
-            tile_load<T, V>(p.Z, n, t + r, c0 + x, z);
+      }
+      *reinterpret_cast<float4*>(to + 4 * i) = make_float4(v[0], v[1], v[2], v[3]);
+    }
+  }
+  // The pair of item i of one of the four row tensors.
+  __device__ __forceinline__ Duo<T> pair_at(const RowsArg& src, int slot, int i, int t, bool second) const {
+    Duo<T> d;
+    if (p.vec) {
+      using W = std::conditional_t<sizeof(T) == 4, uint2, uint32_t>;
+      const W w = reinterpret_cast<const W*>(sm.raw[slot])[row_of(i) * P + pair_of()];
+      __builtin_memcpy(d.v, &w, sizeof(w));
+    } else {
+      d.load(src, n, t + row_of(i), c0 + 2 * pair_of(), second);
+    }
+    return d;
+  }
+
+  template <Stage S>
+  __device__ __forceinline__ void put(int t) {
+    const bool second = 2 * pair_of() + 1 < width;
 #pragma unroll
-            for (int j = 0; j < V; ++j) gy[j] *= z[j] * sigmoid_fast(z[j]);
+    for (int i = 0; i < kItems; ++i) {
+      const int r = row_of(i);
+      if (r >= kT) continue;
+      Duo<T> d{}, x{}, gy2{}, z2{};
+      const bool on = has(i, t);
+      if (on) {
+        d = pair_at(p.Delta, 0, i, t, second);
+        x = pair_at(p.X, 1, i, t, second);
+        if constexpr (S != STATES) {
+          gy2 = pair_at(p.dY, 2, i, t, second);
+          if (p.Z.p) z2 = pair_at(p.Z, 3, i, t, second);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int at = e * P + pair_of();
+        float dt = 0.0f, u = 0.0f, gy = 0.0f, slope = 0.0f, gate = 0.0f;
+        if (on && (e == 0 || second)) {
+          u = x[e];
+          dt = d[e] + sm.bias[at];
+          slope = 1.0f;
+          if (p.softplus) {
+            if constexpr (S == ALL) dt = softplus_slope(dt, slope);
+            else dt = softplus_f(dt);
+          }
+          if constexpr (S != STATES) {
+            gy = gy2[e];
+            if (p.Z.p) {
+              const float zz = z2[e], sg = sigmoid_fast(zz);
+              if constexpr (S == ALL) gate = gy * sg * (1.0f + zz * (1.0f - sg));
+              gy *= zz * sg;
+            }
           }
         }
-      } else {
-        fill(d, 0.0f), fill(uu, 0.0f), fill(gy, 0.0f);
-      }
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        dt[r * CH + x + j] = d[j];
-        u[r * CH + x + j] = uu[j];
-        if (grads) dy[r * CH + x + j] = gy[j];
+        sm.dtu[r][at] = make_float4(dt, dt, dt * u, dt * u);
+        if constexpr (S != STATES) sm.dy[r][at] = make_float2(gy, gy);
+        if constexpr (S == ALL) {
+          sm.u[r][at] = u;
+          sm.slope[r][at] = slope;
+          sm.gate[r][at] = gate;
+        }
       }
     }
+    put_quads(p.Bm, 0, sm.B[0], t);
+    if constexpr (S != STATES) put_quads(p.Cm, 1, sm.C[0], t);
   }
-  __device__ __forceinline__ void stage(int t, bool grads) {
-    constexpr int V = kPiece<T>;
-    if (CH >= V && p.vec) stage_v<(CH >= V ? V : 1)>(t, grads);
-    else stage_v<1>(t, grads);
-    if (p.bc_vec) {
-      stage_group<T, 4, NSP, TT>(p.Bm, n, g, p.K, t, live, sB);
-      if (grads) stage_group<T, 4, NSP, TT>(p.Cm, n, g, p.K, t, live, sC);
+
+  // A pair of a row gradient: into shared memory where the rows take pieces
+  // (stored by flush), else to its place.
+  __device__ __forceinline__ void emit(const RowsArg& to, int slot, int i, int t, bool second, float a, float b) {
+    if (!to.p) return;
+    if (p.vec) {
+      if constexpr (sizeof(T) == 4) reinterpret_cast<float2*>(sm.out[slot])[row_of(i) * P + pair_of()] = make_float2(a, b);
+      else reinterpret_cast<uint32_t*>(sm.out[slot])[row_of(i) * P + pair_of()] = Elem<T>::pair_from_f(a, b);
     } else {
-      stage_group<T, 1, NSP, TT>(p.Bm, n, g, p.K, t, live, sB);
-      if (grads) stage_group<T, 1, NSP, TT>(p.Cm, n, g, p.K, t, live, sC);
+      Duo<T>::store(to, n, t + row_of(i), c0 + 2 * pair_of(), second, a, b);
     }
   }
+  __device__ __forceinline__ void flush(const RowsArg& to, int slot, int t) {
+    if (!to.p || !p.vec) return;
+    T* base = static_cast<T*>(to.p) + n * to.ns + t * to.ss + c0;
+#pragma unroll
+    for (int i = threadIdx.x; i < Sm::kPieces; i += kThreads) {
+      const int r = i / (CH / V), x = i % (CH / V) * V;
+      if (t + r < live && x < width) *reinterpret_cast<uint4*>(base + r * to.ss + x) = sm.out[slot][i];
+    }
+  }
+
   __device__ __forceinline__ void constants() {
     for (int i = threadIdx.x; i < CH; i += kThreads) {
-      bias[i] = (p.bias && i < width) ? p.bias[c0 + i] : 0.0f;
-      skip[i] = (p.D && i < width) ? p.D[c0 + i] : 0.0f;
+      const int ch = 2 * (i % P) + i / P;
+      sm.bias[i] = (p.bias && ch < width) ? p.bias[c0 + ch] : 0.0f;
+      sm.skip[i] = (p.D && ch < width) ? p.D[c0 + ch] : 0.0f;
     }
   }
 };
 
-// Every chunk's final state from zero, its sum of dt, and what leaves its
-// start of the state's gradient when nothing arrives at its end:
-// sum over its steps of (product of a from the chunk's start) C dy.
-template <typename T, int TPC>
-__global__ void __launch_bounds__(kThreads) scan_grad_chunks_kernel(ScanParams p) {
-  using Sh = GradShape<TPC>;
-  constexpr int CH = Sh::CH, NSP = Sh::NSP, TT = Sh::T;
-  __shared__ __align__(16) float sB[TT * NSP], sC[TT * NSP];
-  __shared__ float sdt[TT * CH], su[TT * CH], sdy[TT * CH], sbias[CH], sskip[CH];
-  const int per = p.C / p.G, tiles = (per + CH - 1) / CH;
+// Four states of two channels, as packed halves: [channel][half].
+struct States {
+  F2 v[2][2];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i / 2][i % 2] = f2(0.0f, 0.0f);
+  }
+  template <int TPC>
+  __device__ __forceinline__ void load(const float* rows, int c, int width_left, const ScanParams& p, int part) {
+    zero();
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      if (e >= width_left) continue;
+      float x[4];
+      load_states<4, TPC>(rows + (long long)(c + e) * p.K, p.K, part, p.k_vec, x);
+      v[e][0] = f2(x[0], x[1]), v[e][1] = f2(x[2], x[3]);
+    }
+  }
+  template <int TPC>
+  __device__ __forceinline__ void store(float* rows, int c, int width_left, const ScanParams& p, int part) const {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      if (e >= width_left) continue;
+      const float2 a = f2_get(v[e][0]), b = f2_get(v[e][1]);
+      const float x[4] = {a.x, a.y, b.x, b.y};
+      store_states<4, TPC>(rows + (long long)(c + e) * p.K, p.K, part, p.k_vec, x);
+    }
+  }
+  __device__ __forceinline__ void to_rates() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 a = f2_get(v[i / 2][i % 2]);
+      v[i / 2][i % 2] = f2(rate2(a.x), rate2(a.y));
+    }
+  }
+};
+
+// Adds `count` values over the lanes whose bits from FIRST down to LAST
+// differ.  Each exchange leaves a lane half of its values until one is left;
+// on return v[0 .. left) are the sums of values at + 0 .. left - 1.
+template <int COUNT, int FIRST, int LAST>
+__device__ __forceinline__ void lanes_sum(float* v, int lane, int& at) {
+  if constexpr (FIRST >= LAST && FIRST > 0) {
+    if constexpr (COUNT > 1) {
+      constexpr int H = COUNT / 2;
+      const bool hi = lane & FIRST;
+#pragma unroll
+      for (int i = 0; i < H; ++i) {
+        const float send = hi ? v[i] : v[i + H], keep = hi ? v[i + H] : v[i];
+        v[i] = keep + __shfl_xor_sync(0xffffffffu, send, FIRST);
+      }
+      if (hi) at += H;
+      lanes_sum<H, FIRST / 2, LAST>(v, lane, at);
+    } else {
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], FIRST);
+      lanes_sum<1, FIRST / 2, LAST>(v, lane, at);
+    }
+  }
+}
+// Values left of COUNT after log2(LANES) exchanges.
+template <int COUNT, int LANES>
+constexpr int kLeft = COUNT > LANES ? COUNT / LANES : 1;
+
+__device__ __forceinline__ float halves(F2 a) {
+  const float2 v = f2_get(a);
+  return v.x + v.y;
+}
+
+// h = a h + (dt u) B of one step.
+template <typename Sm>
+__device__ __forceinline__ void update(const Sm& sm, int r, int j, int part, const States& A2, States& h) {
+  const ulonglong2 B = *reinterpret_cast<const ulonglong2*>(&sm.B[r][part * 4]);
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(&sm.dtu[r][e * Sm::P + j]);
+    const F2 dt{w.x}, du{w.y};
+    h.v[e][0] = fma2(exp2_fast2(mul2(dt, A2.v[e][0])), h.v[e][0], mul2(du, F2{B.x}));
+    h.v[e][1] = fma2(exp2_fast2(mul2(dt, A2.v[e][1])), h.v[e][1], mul2(du, F2{B.y}));
+  }
+}
+
+// The way forward, every chunk from a zero state: the state and the sum of dt
+// at the start of each subtile (the true state is that plus the chunk's start
+// decayed by the sum) and at the chunk's end.  ADJOINT, for chunks that run
+// side by side: what leaves the chunk's start of the state's gradient when
+// nothing arrives at its end, the sum over its steps of (product of a from
+// the chunk's start) C dy.
+template <typename T, int TPC, bool ADJOINT>
+__global__ void __launch_bounds__(kThreads, 4) scan_grad_states_kernel(ScanParams p) {
+  using Sm = GradSmem<T, TPC>;
+  constexpr Stage S = ADJOINT ? DY : STATES;
+  extern __shared__ __align__(16) unsigned char smem[];
+  Sm& sm = *reinterpret_cast<Sm*>(smem);
+  const int per = p.C / p.G, tiles = (per + Sm::CH - 1) / Sm::CH;
   const int tile = blockIdx.x % tiles;
   int q = blockIdx.x / tiles;
   const int g = q % p.G;
@@ -155,338 +361,348 @@ __global__ void __launch_bounds__(kThreads) scan_grad_chunks_kernel(ScanParams p
   const int chunk = q % p.chunks, n = q / p.chunks;
   const int t0 = chunk * p.chunk, t1 = min(t0 + p.chunk, p.S);
   const int live = min(t1, row_length(p.lens, n, p.S));
-  Tile<T, TPC> b{p, n, g, g * per + tile * CH, min(CH, per - tile * CH), t0, t1, live,
-                 sdt, su, sdy, sB, sC, sbias, sskip};
-  const int lc = threadIdx.x / TPC, part = threadIdx.x % TPC;
-  const bool mine = lc < b.width;
-  const int c = b.c0 + (mine ? lc : 0);
+  Tile<T, TPC> b{p, sm, n, g, g * per + tile * Sm::CH, min(Sm::CH, per - tile * Sm::CH), live};
+  const int j = threadIdx.x / TPC, part = threadIdx.x % TPC;
+  const int left = b.width - 2 * j, c = b.c0 + (left > 0 ? 2 * j : 0);
+  const int subs = (p.S + kT - 1) / kT;
+  if (t0 < live) b.template fetch<S>(t0);
   b.constants();
-  float A2[4], h[4], pr[4], e[4];
-  load_states<4, TPC>(p.A + (long long)c * p.K, p.K, part, A2);
+  States A2, h, pr, e;
+  A2.template load<TPC>(p.A, c, left, p, part);
+  A2.to_rates();
+  h.zero(), e.zero();
+  float sum[2] = {0.0f, 0.0f};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) A2[i] *= kLog2e, h[i] = 0.0f, pr[i] = 1.0f, e[i] = 0.0f;
-  float sum = 0.0f;
-  __syncthreads();
-  for (int t = t0; t < live; t += TT) {
-    b.stage(t, true);
+  for (int i = 0; i < 4; ++i) pr.v[i / 2][i % 2] = f2(1.0f, 1.0f);
+  for (int t = t0; t < live; t += kT) {
+    copies_done();
     __syncthreads();
-    const int steps = min(TT, live - t);
-    for (int r = 0; r < steps; ++r) {
-      const float dt = sdt[r * CH + lc], dtu = dt * su[r * CH + lc], dy = sdy[r * CH + lc];
-      const float4 B = *reinterpret_cast<const float4*>(&sB[r * NSP + part * 4]);
-      const float4 C = *reinterpret_cast<const float4*>(&sC[r * NSP + part * 4]);
-      const float bb[4] = {B.x, B.y, B.z, B.w}, cc[4] = {C.x, C.y, C.z, C.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float a = exp2_fast(dt * A2[i]);
-        h[i] = fmaf(a, h[i], dtu * bb[i]);
-        pr[i] *= a;
-        e[i] = fmaf(pr[i], cc[i] * dy, e[i]);
-      }
-      sum += dt;
+    b.template put<S>(t);
+    __syncthreads();
+    if (t + kT < live) b.template fetch<S>(t + kT);
+    const long long at = (long long)n * subs + t / kT;
+    h.template store<TPC>(p.ckpt + at * p.C * p.K, c, left, p, part);
+    if (part == 0) {
+      if (left > 0) p.cum[at * p.C + c] = sum[0];
+      if (left > 1) p.cum[at * p.C + c + 1] = sum[1];
     }
-    __syncthreads();
+#pragma unroll 2
+    for (int r = 0; r < kT; ++r) {
+      const ulonglong2 B = *reinterpret_cast<const ulonglong2*>(&sm.B[r][part * 4]);
+      ulonglong2 C;
+      if constexpr (ADJOINT) C = *reinterpret_cast<const ulonglong2*>(&sm.C[r][part * 4]);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(&sm.dtu[r][k * Sm::P + j]);
+        const F2 dt{w.x}, du{w.y};
+        F2 dy;
+        if constexpr (ADJOINT) dy.v = *reinterpret_cast<const unsigned long long*>(&sm.dy[r][k * Sm::P + j]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const F2 a = exp2_fast2(mul2(dt, A2.v[k][i]));
+          h.v[k][i] = fma2(a, h.v[k][i], mul2(du, F2{i ? B.y : B.x}));
+          if constexpr (ADJOINT) {
+            pr.v[k][i] = mul2(pr.v[k][i], a);
+            e.v[k][i] = fma2(pr.v[k][i], mul2(F2{i ? C.y : C.x}, dy), e.v[k][i]);
+          }
+        }
+        sum[k] += f2_get(dt).x;
+      }
+    }
   }
-  if (mine) {
-    const long long row = ((long long)n * p.chunks + chunk) * p.C + c;
-    store_states<4, TPC>(p.carry + row * p.K, p.K, part, h);
-    store_states<4, TPC>(p.gcarry + row * p.K, p.K, part, e);
-    if (part == 0) p.sumdt[row] = sum;
+  if constexpr (ADJOINT) {
+    const long long row = ((long long)n * p.chunks + chunk) * p.C;
+    h.template store<TPC>(p.carry + row * p.K, c, left, p, part);
+    e.template store<TPC>(p.gcarry + row * p.K, c, left, p, part);
+    if (part == 0) {
+      if (left > 0) p.sumdt[row + c] = sum[0];
+      if (left > 1) p.sumdt[row + c + 1] = sum[1];
+    }
   }
 }
 
 // The chunks in order, forward for the states and backward for their gradient.
-__global__ void __launch_bounds__(256) scan_grad_carry_kernel(ScanParams p) {
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+__global__ void __launch_bounds__(64) scan_grad_carry_kernel(ScanParams p) {
+  const long long i = (long long)blockIdx.x * 64 + threadIdx.x;
   const long long ck = (long long)p.C * p.K;
   if (i >= p.N * ck) return;
+  const bool back = blockIdx.y != 0;
   const int n = (int)(i / ck);
   const long long at = i % ck;
-  const float A2 = p.A[at] * kLog2e;
-  const long long base = (long long)n * p.chunks * ck + at;
+  const float A2 = rate2(p.A[at]);
+  float* carry = (back ? p.gcarry : p.carry) + (long long)n * p.chunks * ck + at;
   const float* sumdt = p.sumdt + (long long)n * p.chunks * p.C + at / p.K;
-  if (blockIdx.y == 0) {
-    float run = p.h0 ? p.h0[i] : 0.0f;
-#pragma unroll 4
-    for (int q = 0; q < p.chunks; ++q) {
-      const float s = p.carry[base + q * ck], d = sumdt[(long long)q * p.C];
-      p.carry[base + q * ck] = run;
-      run = fmaf(d == 0.0f ? 1.0f : exp2_fast(A2 * d), run, s);
+  const float* from = back ? p.dhT : p.h0;
+  float run = from ? from[i] : 0.0f;
+  // a batch is read before any of it is overwritten: its loads are in flight together
+  constexpr int kBatch = 16;
+  for (int q0 = 0; q0 < p.chunks; q0 += kBatch) {
+    float s[kBatch], d[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      int q = min(q0 + j, p.chunks - 1);
+      if (back) q = p.chunks - 1 - q;
+      s[j] = carry[q * ck], d[j] = sumdt[(long long)q * p.C];
     }
-  } else {
-    float run = p.dhT ? p.dhT[i] : 0.0f;
-#pragma unroll 4
-    for (int q = p.chunks - 1; q >= 0; --q) {
-      const float s = p.gcarry[base + q * ck], d = sumdt[(long long)q * p.C];
-      p.gcarry[base + q * ck] = run;
-      run = fmaf(d == 0.0f ? 1.0f : exp2_fast(A2 * d), run, s);
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      if (q0 + j < p.chunks) {
+        carry[(back ? p.chunks - 1 - q0 - j : q0 + j) * ck] = run;
+        run = fmaf(exp2_fast(A2 * d[j]), run, s[j]);
+      }
     }
-    if (p.dh0) p.dh0[i] = run;
+  }
+  if (back && p.dh0) p.dh0[i] = run;
+}
+
+// A channel tile's chunk, from its end to its start.
+template <typename T, int TPC>
+__device__ __forceinline__ void grad_tile(const ScanParams& p, GradSmem<T, TPC>& sm, int n, int g, int chunk, int slice,
+                                          int tile, bool first) {
+  using Sm = GradSmem<T, TPC>;
+  constexpr int P = Sm::P, CH = Sm::CH, NSP = Sm::NSP;
+  const int per = p.C / p.G;
+  const int t0 = chunk * p.chunk, t1 = min(t0 + p.chunk, p.S);
+  const int live = min(t1, row_length(p.lens, n, p.S));
+  const int j = threadIdx.x / TPC, part = threadIdx.x % TPC;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int subs = (p.S + kT - 1) / kT;
+  const long long chunk_row = ((long long)n * p.chunks + chunk) * p.C;
+  Tile<T, TPC> b{p, sm, n, g, g * per + tile * CH, min(CH, per - tile * CH), live};
+  const int left = b.width - 2 * j, c = b.c0 + (left > 0 ? 2 * j : 0);
+  const int last = live > t0 ? t0 + (live - 1 - t0) / kT * kT : t0 - kT;
+  __syncthreads();
+  if (last >= t0) b.template fetch<ALL>(last);
+  b.constants();
+  States A2, e, dA;
+  A2.template load<TPC>(p.A, c, left, p, part);
+  A2.to_rates();
+  e.zero(), dA.zero();
+  if (p.chunks > 1) e.template load<TPC>(p.gcarry + chunk_row * p.K, c, left, p, part);
+  else if (p.dhT) e.template load<TPC>(p.dhT + (long long)n * p.C * p.K, c, left, p, part);
+  const float* start = p.chunks > 1 ? p.carry + chunk_row * p.K : p.h0 ? p.h0 + (long long)n * p.C * p.K : nullptr;
+  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // dD and d_delta_bias of this thread's pair
+  for (int t = last; t >= t0; t -= kT) {
+    // the state at the subtile's start: the chunk's own, and what is left of its start's
+    States h;
+    {
+      const long long at = (long long)n * subs + t / kT;
+      h.template load<TPC>(p.ckpt + at * p.C * p.K, c, left, p, part);
+      if (start) {
+        States h0;
+        h0.template load<TPC>(start, c, left, p, part);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float cum = k < left ? p.cum[at * p.C + c + k] : 0.0f;
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            h.v[k][i] = fma2(exp2_fast2(mul2(f2(cum, cum), A2.v[k][i])), h0.v[k][i], h.v[k][i]);
+        }
+      }
+    }
+    copies_done();
+    __syncthreads();
+    b.template put<ALL>(t);
+    __syncthreads();
+    if (t > t0) b.template fetch<ALL>(t - kT);
+    // Half of the subtile's steps at a time, the later ones first: as many
+    // states as leave the registers room to overlap steps.  Past the length
+    // dt, dt u and dy are 0: the state and its gradient stand still
+    States dAt;  // of this subtile: long sums of short ones keep more bits
+    dAt.zero();
+#pragma unroll 1
+    for (int base = kT - kHalf; base >= 0; base -= kHalf) {
+      States hs[kHalf + 1];  // hs[r]: the state before step base + r
+      hs[0] = h;
+#pragma unroll 1
+      for (int r = 0; r < base; ++r) update(sm, r, j, part, A2, hs[0]);
+#pragma unroll
+      for (int i = 0; i < kHalf; ++i) {
+        const int r = base + i;
+        hs[i + 1] = hs[i];
+        update(sm, r, j, part, A2, hs[i + 1]);
+        if (p.dZ.p) {
+          const ulonglong2 C = *reinterpret_cast<const ulonglong2*>(&sm.C[r][part * 4]);
+          float y[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            y[k] = halves(fma2(F2{C.y}, hs[i + 1].v[k][1], mul2(F2{C.x}, hs[i + 1].v[k][0])));
+          int at = 0;
+          lanes_sum<2, TPC / 2, 1>(y, lane, at);
+          constexpr int L = kLeft<2, TPC>;
+#pragma unroll
+          for (int m = 0; m < L; ++m) sm.y[r][(at + m) * P + j] = y[m];
+        }
+      }
+#pragma unroll
+      for (int q = kHalf - 1; q >= 0; --q) {
+        const int r = base + q;
+        const ulonglong2 B = *reinterpret_cast<const ulonglong2*>(&sm.B[r][part * 4]);
+        const ulonglong2 C = *reinterpret_cast<const ulonglong2*>(&sm.C[r][part * 4]);
+        F2 vb[2], vc[2];
+        float s[4];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(&sm.dtu[r][k * P + j]);
+          const F2 dt{w.x}, du{w.y}, dy{*reinterpret_cast<const unsigned long long*>(&sm.dy[r][k * P + j])};
+          F2 gb, th;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const F2 bi{i ? B.y : B.x}, ci{i ? C.y : C.x}, a2 = A2.v[k][i];
+            const F2 a = exp2_fast2(mul2(dt, a2)), gg = fma2(ci, dy, e.v[k][i]);
+            vc[i] = k ? fma2(hs[q + 1].v[k][i], dy, vc[i]) : mul2(hs[q + 1].v[k][i], dy);
+            vb[i] = k ? fma2(gg, du, vb[i]) : mul2(gg, du);
+            gb = i ? fma2(gg, bi, gb) : mul2(gg, bi);
+            e.v[k][i] = mul2(gg, a);
+            const F2 x = mul2(e.v[k][i], hs[q].v[k][i]);
+            th = i ? fma2(x, a2, th) : mul2(x, a2);
+            dAt.v[k][i] = fma2(x, dt, dAt.v[k][i]);
+          }
+          s[k] = halves(gb), s[2 + k] = halves(th);
+        }
+        int at = 0;
+        lanes_sum<4, TPC / 2, 1>(s, lane, at);
+        constexpr int L = kLeft<4, TPC>;
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+          const int v = at + i;
+          (v < 2 ? sm.gb : sm.th)[r][(v & 1) * P + j] = s[i];
+        }
+        const float2 b0 = f2_get(vb[0]), b1 = f2_get(vb[1]), c0 = f2_get(vc[0]), c1 = f2_get(vc[1]);
+        float v[8] = {b0.x, b0.y, b1.x, b1.y, c0.x, c0.y, c1.x, c1.y};
+        at = 0;
+        lanes_sum<8, 16, TPC>(v, lane, at);
+        constexpr int M = kLeft<8, 32 / TPC>;
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+          const int w = at + i;
+          sm.part[r][warp][w / 4 * NSP + part * 4 + w % 4] = v[i];
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dA.v[i / 2][i % 2] = add2(dA.v[i / 2][i % 2], dAt.v[i / 2][i % 2]);
+    __syncthreads();
+    // the subtile's row gradients
+    const int pj = b.pair_of();
+    const bool second = 2 * pj + 1 < b.width;
+#pragma unroll
+    for (int i = 0; i < Tile<T, TPC>::kItems; ++i) {
+      if (!b.has(i, t)) continue;
+      const int r = b.row_of(i);
+      float du[2], dd[2], dz[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int at = k * P + pj;
+        const float gb = sm.gb[r][at], u = sm.u[r][at], dy = sm.dy[r][at].x;
+        du[k] = fmaf(gb, sm.dtu[r][at].x, sm.skip[at] * dy);
+        dd[k] = fmaf(gb, u, sm.th[r][at] * kLn2) * sm.slope[r][at];
+        dz[k] = sm.gate[r][at] * fmaf(sm.skip[at], u, sm.y[r][at]);
+        acc[k] = fmaf(dy, u, acc[k]);
+        acc[2 + k] += dd[k];
+      }
+      b.emit(p.dX, 0, i, t, second, du[0], du[1]);
+      b.emit(p.dDelta, 1, i, t, second, dd[0], dd[1]);
+      b.emit(p.dZ, 2, i, t, second, dz[0], dz[1]);
+    }
+    if (p.bc_part) {
+      float* to = p.bc_part + ((((long long)slice * p.N + n) * p.S + t) * p.G + g) * 2 * p.K;
+#pragma unroll
+      for (int i = threadIdx.x; i < kT * 2 * NSP; i += kThreads) {
+        const int r = i / (2 * NSP), w = i % (2 * NSP), k = w % NSP;
+        if (k >= p.K || t + r >= live) continue;
+        float v = sm.part[r][0][w];
+#pragma unroll
+        for (int m = 1; m < kWarps; ++m) v += sm.part[r][m][w];
+        float* at = to + r * p.G * 2 * p.K + w / NSP * p.K + k;
+        *at = first ? v : *at + v;
+      }
+    }
+    if (p.vec) {
+      __syncthreads();
+      b.flush(p.dX, 0, t);
+      b.flush(p.dDelta, 1, t);
+      b.flush(p.dZ, 2, t);
+    }
+  }
+
+  // what is left: zeros past the length, the state's gradient, the sums over the chunk's steps
+  const int from = max(t0, live);
+  for (int i = threadIdx.x; i < (t1 - from) * P; i += kThreads) {
+    const int s = from + i / P, k = 2 * (i % P);
+    if (k >= b.width) continue;
+    for (const RowsArg* a : {&p.dX, &p.dDelta, &p.dZ})
+      if (a->p) Duo<T>::store(*a, n, s, b.c0 + k, k + 1 < b.width, 0.0f, 0.0f);
+  }
+  if (p.chunks == 1 && p.dh0) e.template store<TPC>(p.dh0 + (long long)n * p.C * p.K, c, left, p, part);
+  if (p.w_part) {
+    float* w = p.w_part + chunk_row * (p.K + 2);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (k >= left) continue;
+      const float2 lo = f2_get(dA.v[k][0]), hi = f2_get(dA.v[k][1]);
+      const float x[4] = {lo.x, lo.y, hi.x, hi.y};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (part * 4 + i < p.K) w[(long long)(c + k) * p.K + part * 4 + i] = x[i];
+    }
+    w += (long long)p.C * p.K;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sm.acc[threadIdx.x][i] = acc[i];
+    __syncthreads();
+    for (int ch = threadIdx.x; ch < b.width; ch += kThreads) {
+      float d = 0.0f, v = 0.0f;
+#pragma unroll 4
+      for (int q = ch / 2; q < kThreads; q += P) d += sm.acc[q][ch & 1], v += sm.acc[q][2 + (ch & 1)];
+      w[b.c0 + ch] = d;
+      w[p.C + b.c0 + ch] = v;
+    }
   }
 }
 
 template <typename T, int TPC>
-__global__ void __launch_bounds__(kThreads) scan_grad_kernel(ScanParams p) {
-  using Sh = GradShape<TPC>;
-  constexpr int CH = Sh::CH, NSP = Sh::NSP, TT = Sh::T, kRows = Sh::kRows;
-  extern __shared__ __align__(16) float smem[];
-  float4* sh = reinterpret_cast<float4*>(smem);            // [TT][kThreads]
-  float* sB = smem + TT * kThreads * 4;                    // [TT][NSP]
-  float* sC = sB + TT * NSP;
-  float* spart = sC + TT * NSP;                            // [TT][kWarps][2][NSP]
-  float* sdt = spart + TT * kWarps * 2 * NSP;              // [TT][CH], and the next five
-  float* su = sdt + kRows;
-  float* sdy = su + kRows;
-  float* sgb = sdy + kRows;  // sum of g B, then ddelta
-  float* sth = sgb + kRows;  // sum of A x, then dy u
-  float* sy = sth + kRows;   // sum of C h
-  float* sbias = sy + kRows;
-  float* sskip = sbias + CH;
-  const int per = p.C / p.G, tiles = (per + CH - 1) / CH;
+__global__ void __launch_bounds__(kThreads, 4) scan_grad_kernel(ScanParams p) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  using Sm = GradSmem<T, TPC>;
+  Sm& sm = *reinterpret_cast<Sm*>(smem);
+  const int tiles = (p.C / p.G + Sm::CH - 1) / Sm::CH;
   const int slice = blockIdx.x % p.slices;
   int q = blockIdx.x / p.slices;
   const int g = q % p.G;
   q /= p.G;
   const int chunk = q % p.chunks, n = q / p.chunks;
-  const int t0 = chunk * p.chunk, t1 = min(t0 + p.chunk, p.S);
-  const int live = min(t1, row_length(p.lens, n, p.S));
-  const int lc = threadIdx.x / TPC, part = threadIdx.x % TPC;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int subs = (p.S + TT - 1) / TT;
-  const long long chunk_row = (long long)n * p.chunks + chunk;
-
-  for (int tile = slice * p.slice_tiles; tile < min((slice + 1) * p.slice_tiles, tiles); ++tile) {
-    const bool first = tile == slice * p.slice_tiles;
-    Tile<T, TPC> b{p, n, g, g * per + tile * CH, min(CH, per - tile * CH), t0, t1, live,
-                   sdt, su, sdy, sB, sC, sbias, sskip};
-    const bool mine = lc < b.width;
-    const int c = b.c0 + (mine ? lc : 0);
-    __syncthreads();
-    b.constants();
-    float A2[4], h[4];
-    fill(A2, 0.0f), fill(h, 0.0f);  // what a thread without a channel keeps: it adds 0 to its warp's sums
-    if (mine) load_states<4, TPC>(p.A + (long long)c * p.K, p.K, part, A2);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) A2[i] *= kLog2e;
-    if (!mine) {
-    } else if (p.chunks > 1) load_states<4, TPC>(p.carry + (chunk_row * p.C + c) * p.K, p.K, part, h);
-    else if (p.h0) load_states<4, TPC>(p.h0 + ((long long)n * p.C + c) * p.K, p.K, part, h);
-    auto ckpt = [&](int t) { return p.ckpt + (((long long)n * subs + t / TT) * p.C + c) * p.K; };
-    __syncthreads();
-
-    // forward: the state at the start of each subtile
-    int last = t0;
-    for (int t = t0; t < live; t += TT) {
-      last = t;
-      if (mine) store_states<4, TPC>(ckpt(t), p.K, part, h);
-      if (t + TT >= live) break;
-      b.stage(t, false);
-      __syncthreads();
-#pragma unroll 4
-      for (int r = 0; r < TT; ++r) {
-        const float dt = sdt[r * CH + lc], dtu = dt * su[r * CH + lc];
-        const float4 B = *reinterpret_cast<const float4*>(&sB[r * NSP + part * 4]);
-        const float bb[4] = {B.x, B.y, B.z, B.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = fmaf(exp2_fast(dt * A2[i]), h[i], dtu * bb[i]);
-      }
-      __syncthreads();
-    }
-
-    // backward, one subtile at a time
-    float e[4], dA[4], dD = 0.0f, dbias = 0.0f;
-    fill(e, 0.0f), fill(dA, 0.0f);
-    if (!mine) {
-    } else if (p.chunks > 1) load_states<4, TPC>(p.gcarry + (chunk_row * p.C + c) * p.K, p.K, part, e);
-    else if (p.dhT) load_states<4, TPC>(p.dhT + ((long long)n * p.C + c) * p.K, p.K, part, e);
-    for (int t = last; t >= t0 && live > t0; t -= TT) {
-      const int steps = min(TT, live - t);
-      b.stage(t, true);
-      float start[4];
-      fill(start, 0.0f);
-      if (mine) load_states<4, TPC>(ckpt(t), p.K, part, start);
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < 4; ++i) h[i] = start[i];
-#pragma unroll 4
-      for (int r = 0; r < steps; ++r) {
-        const float dt = sdt[r * CH + lc], dtu = dt * su[r * CH + lc];
-        const float4 B = *reinterpret_cast<const float4*>(&sB[r * NSP + part * 4]);
-        const float bb[4] = {B.x, B.y, B.z, B.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = fmaf(exp2_fast(dt * A2[i]), h[i], dtu * bb[i]);
-        sh[r * kThreads + threadIdx.x] = make_float4(h[0], h[1], h[2], h[3]);
-        if (p.Z.p) {
-          const float4 C = *reinterpret_cast<const float4*>(&sC[r * NSP + part * 4]);
-          float y = h[0] * C.x + h[1] * C.y + h[2] * C.z + h[3] * C.w;
-#pragma unroll
-          for (int o = TPC / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-          if (part == 0) sy[r * CH + lc] = y;
-        }
-      }
-#pragma unroll 2
-      for (int r = steps - 1; r >= 0; --r) {
-        const float dt = sdt[r * CH + lc], dtu = dt * su[r * CH + lc], dy = sdy[r * CH + lc];
-        const float4 B = *reinterpret_cast<const float4*>(&sB[r * NSP + part * 4]);
-        const float4 C = *reinterpret_cast<const float4*>(&sC[r * NSP + part * 4]);
-        const float bb[4] = {B.x, B.y, B.z, B.w}, cc[4] = {C.x, C.y, C.z, C.w};
-        float before[4];
-        if (r > 0) {
-          const float4 v = sh[(r - 1) * kThreads + threadIdx.x];
-          before[0] = v.x, before[1] = v.y, before[2] = v.z, before[3] = v.w;
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) before[i] = start[i];
-        }
-        float gb = 0.0f, th = 0.0f, vb[4], vc[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float a = exp2_fast(dt * A2[i]);
-          const float gg = fmaf(cc[i], dy, e[i]);
-          vc[i] = h[i] * dy;
-          vb[i] = gg * dtu;
-          gb = fmaf(gg, bb[i], gb);
-          e[i] = gg * a;
-          const float x = e[i] * before[i];
-          th = fmaf(x, A2[i], th);
-          dA[i] = fmaf(x, dt, dA[i]);
-          h[i] = before[i];
-        }
-#pragma unroll
-        for (int o = TPC / 2; o > 0; o >>= 1) {
-          gb += __shfl_xor_sync(0xffffffffu, gb, o);
-          th += __shfl_xor_sync(0xffffffffu, th, o);
-        }
-        if (part == 0) sgb[r * CH + lc] = gb, sth[r * CH + lc] = th * (1.0f / kLog2e);
-#pragma unroll
-        for (int o = 16; o >= TPC; o >>= 1) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            vb[i] += __shfl_xor_sync(0xffffffffu, vb[i], o);
-            vc[i] += __shfl_xor_sync(0xffffffffu, vc[i], o);
-          }
-        }
-        if (lane < TPC) {
-          float* to = spart + (r * kWarps + warp) * 2 * NSP + part * 4;
-          *reinterpret_cast<float4*>(to) = make_float4(vb[0], vb[1], vb[2], vb[3]);
-          *reinterpret_cast<float4*>(to + NSP) = make_float4(vc[0], vc[1], vc[2], vc[3]);
-        }
-      }
-      __syncthreads();
-      // the subtile's row gradients
-      auto emit = [&](auto piece) {
-        constexpr int V = decltype(piece)::value;
-        constexpr int kPieces = CH / V > 0 ? CH / V : 1;
-        for (int i = threadIdx.x; i < steps * kPieces; i += kThreads) {
-          const int r = i / kPieces, x = i % kPieces * V;
-          if (x >= b.width) continue;
-          const int s = t + r;
-          float du[V], dd[V];
-#pragma unroll
-          for (int j = 0; j < V; ++j) {
-            const int at = r * CH + x + j;
-            const float gb = sgb[at], uu = su[at];
-            du[j] = fmaf(gb, sdt[at], sskip[x + j] * sdy[at]);
-            dd[j] = fmaf(gb, uu, sth[at]);
-            sth[at] = sdy[at] * uu;
-          }
-          if (p.softplus) {
-            float raw[V];
-            tile_load<T, V>(p.Delta, n, s, b.c0 + x, raw);
-#pragma unroll
-            for (int j = 0; j < V; ++j) dd[j] *= sigmoid_fast(raw[j] + sbias[x + j]);
-          }
-#pragma unroll
-          for (int j = 0; j < V; ++j) sgb[r * CH + x + j] = dd[j];
-          if (p.dX.p) tile_store<T, V>(p.dX, n, s, b.c0 + x, du);
-          if (p.dDelta.p) tile_store<T, V>(p.dDelta, n, s, b.c0 + x, dd);
-          if (p.dZ.p) {
-            float z[V], gy[V];
-            tile_load<T, V>(p.Z, n, s, b.c0 + x, z);
-            tile_load<T, V>(p.dY, n, s, b.c0 + x, gy);
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-              const int at = r * CH + x + j;
-              const float sg = sigmoid_fast(z[j]);
-              const float y = fmaf(sskip[x + j], su[at], sy[at]);
-              gy[j] *= y * sg * (1.0f + z[j] * (1.0f - sg));
-            }
-            tile_store<T, V>(p.dZ, n, s, b.c0 + x, gy);
-          }
-        }
-      };
-      constexpr int V = kPiece<T>;
-      if (CH >= V && p.vec) emit(std::integral_constant<int, (CH >= V ? V : 1)>{});
-      else emit(std::integral_constant<int, 1>{});
-      if (p.bc_part) {
-        for (int i = threadIdx.x; i < steps * 2 * NSP; i += kThreads) {
-          const int r = i / (2 * NSP), j = i % (2 * NSP);
-          const int k = j % NSP;
-          if (k >= p.K) continue;
-          float v = 0.0f;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) v += spart[(r * kWarps + w) * 2 * NSP + j];
-          float* to = p.bc_part + ((((long long)slice * p.N + n) * p.S + t + r) * p.G + g) * 2 * p.K + (j / NSP) * p.K + k;
-          *to = first ? v : *to + v;
-        }
-      }
-      __syncthreads();
-      if (threadIdx.x < CH && threadIdx.x < b.width) {
-        for (int r = 0; r < steps; ++r) {
-          dbias += sgb[r * CH + threadIdx.x];
-          dD += sth[r * CH + threadIdx.x];
-        }
-      }
-      __syncthreads();
-    }
-
-    // what is left: zeros past the length, the state's gradient, the sums over the chunk's steps
-    const int from = max(t0, live);
-    for (int i = threadIdx.x; i < CH; i += kThreads) {
-      if (i >= b.width) continue;
-      for (int t = from; t < t1; ++t) {
-        const float zero[1] = {0.0f};
-        if (p.dX.p) tile_store<T, 1>(p.dX, n, t, b.c0 + i, zero);
-        if (p.dDelta.p) tile_store<T, 1>(p.dDelta, n, t, b.c0 + i, zero);
-        if (p.dZ.p) tile_store<T, 1>(p.dZ, n, t, b.c0 + i, zero);
-      }
-    }
-    if (mine && p.chunks == 1 && p.dh0)
-      store_states<4, TPC>(p.dh0 + ((long long)n * p.C + c) * p.K, p.K, part, e);
-    if (p.w_part) {
-      float* w = p.w_part + chunk_row * p.C * (p.K + 2);
-      if (mine) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (part * 4 + i < p.K) w[(long long)c * p.K + part * 4 + i] = dA[i];
-      }
-      w += (long long)p.C * p.K;
-      if (threadIdx.x < CH && threadIdx.x < b.width) {
-        w[b.c0 + threadIdx.x] = dD;
-        w[p.C + b.c0 + threadIdx.x] = dbias;
-      }
-    }
-  }
+  const int from = slice * p.slice_tiles, to = min(from + p.slice_tiles, tiles);
+  for (int tile = from; tile < to; ++tile) grad_tile<T, TPC>(p, sm, n, g, chunk, slice, tile, tile == from);
 }
 
-// dB and dC from the slices, in order; zeros past the length.
-template <typename T>
-__global__ void __launch_bounds__(256) scan_grad_rows_kernel(ScanParams p) {
+// dB and dC from the slices, in order; zeros past the length.  V values per
+// thread, all of one row of dB or dC.
+template <typename T, int V>
+__global__ void __launch_bounds__(128) scan_grad_rows_kernel(ScanParams p) {
   const int row = p.G * 2 * p.K;
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  const long long i = ((long long)blockIdx.x * 128 + threadIdx.x) * V;
   const long long all = (long long)p.N * p.S * row;
   if (i >= all) return;
   const int j = (int)(i % row);
   const long long ns = i / row;
   const int s = (int)(ns % p.S), n = (int)(ns / p.S);
   const int g = j / (2 * p.K), which = j / p.K % 2, k = j % p.K;
-  float v = 0.0f;
+  float v[V];
+  fill(v, 0.0f);
   if (s < row_length(p.lens, n, p.S)) {
-#pragma unroll 8
-    for (int q = 0; q < p.slices; ++q) v += p.bc_part[q * all + i];
+#pragma unroll 16
+    for (int q = 0; q < p.slices; ++q) {
+      float w[V];
+      Piece<float, V>::load(p.bc_part + q * all + i, w);
+#pragma unroll
+      for (int e = 0; e < V; ++e) v[e] += w[e];
+    }
   }
   const RowsArg& to = which ? p.dC : p.dB;
-  if (to.p) static_cast<T*>(to.p)[n * to.ns + s * to.ss + (long long)g * p.K + k] = Elem<T>::from_f(v);
+  if (!to.p) return;
+  T* out = static_cast<T*>(to.p) + n * to.ns + s * to.ss + (long long)g * p.K + k;
+#pragma unroll
+  for (int e = 0; e < V; ++e) out[e] = Elem<T>::from_f(v[e]);
 }
 
 // dA, dD and d_delta_bias from the sequences' and chunks' sums, in a fixed order.
@@ -517,26 +733,37 @@ __global__ void __launch_bounds__(256) scan_grad_weights_kernel(ScanParams p) {
   }
 }
 
+template <typename T, int TPC, bool ADJOINT>
+cudaError_t run_states(const ScanParams& p, long long blocks, cudaStream_t s) {
+  constexpr int smem = (int)sizeof(GradSmem<T, TPC>);
+  const cudaError_t e = cudaFuncSetAttribute(scan_grad_states_kernel<T, TPC, ADJOINT>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) scan_grad_states_kernel<T, TPC, ADJOINT><<<(unsigned)blocks, kThreads, smem, s>>>(p);
+  return e;
+}
+
 template <typename T, int TPC>
 cudaError_t run_grad(const ScanParams& p, cudaStream_t s, int* launches) {
-  using Sh = GradShape<TPC>;
-  const long long tiles = (p.C / p.G + Sh::CH - 1) / Sh::CH;
+  using Sm = GradSmem<T, TPC>;
+  const long long tiles = (p.C / p.G + Sm::CH - 1) / Sm::CH;
   const long long rest = (long long)p.N * p.chunks * p.G;
   if (rest * tiles > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   cudaError_t e = cudaFuncSetAttribute(scan_grad_kernel<T, TPC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)Sh::smem);
+                                       (int)sizeof(Sm));
+  if (e != cudaSuccess) return e;
+  e = p.chunks > 1 ? run_states<T, TPC, true>(p, rest * tiles, s) : run_states<T, TPC, false>(p, rest * tiles, s);
   if (e != cudaSuccess) return e;
   if (p.chunks > 1) {
-    scan_grad_chunks_kernel<T, TPC><<<(unsigned)(rest * tiles), kThreads, 0, s>>>(p);
     const long long states = (long long)p.N * p.C * p.K;
-    scan_grad_carry_kernel<<<dim3((unsigned)((states + 255) / 256), 2), 256, 0, s>>>(p);
-    *launches += 2;
+    scan_grad_carry_kernel<<<dim3((unsigned)((states + 63) / 64), 2), 64, 0, s>>>(p);
+    *launches += 1;
   }
-  scan_grad_kernel<T, TPC><<<(unsigned)(rest * p.slices), kThreads, Sh::smem, s>>>(p);
-  *launches += 1;
+  scan_grad_kernel<T, TPC><<<(unsigned)(rest * p.slices), kThreads, sizeof(Sm), s>>>(p);
+  *launches += 2;
   if (p.bc_part) {
     const long long all = (long long)p.N * p.S * p.G * 2 * p.K;
-    scan_grad_rows_kernel<T><<<(unsigned)((all + 255) / 256), 256, 0, s>>>(p);
+    if (p.K % 4 == 0) scan_grad_rows_kernel<T, 4><<<(unsigned)((all / 4 + 127) / 128), 128, 0, s>>>(p);
+    else scan_grad_rows_kernel<T, 1><<<(unsigned)((all + 127) / 128), 128, 0, s>>>(p);
     *launches += 1;
   }
   if (p.w_part) {
@@ -549,7 +776,6 @@ cudaError_t run_grad(const ScanParams& p, cudaStream_t s, int* launches) {
 template <typename T>
 cudaError_t grad_typed(const ScanParams& p, cudaStream_t s, int* launches) {
   switch (tpc_of(p.K)) {
-    case 1: return run_grad<T, 1>(p, s, launches);
     case 2: return run_grad<T, 2>(p, s, launches);
     case 4: return run_grad<T, 4>(p, s, launches);
     case 8: return run_grad<T, 8>(p, s, launches);
@@ -572,16 +798,16 @@ ScanPlan scan_grad_plan(long long seq, long long batch, long long channels, int 
   pl.chunk = (int)std::max<long long>(seq, 1);
   pl.slices = pl.slice_tiles = 1;
   if (seq == 0 || batch == 0) return pl;
-  const int tpc = tpc_of(state), sub = sub_steps(tpc);
-  const long long per = channels / groups, ch = kThreads / tpc;
+  const long long per = channels / groups, ch = 2 * kThreads / tpc_of(state);
   const long long tiles = (per + ch - 1) / ch;
   const long long blocks = batch * groups * tiles;
-  const long long want = kPlanSms * 2;
-  if (blocks < want / 2) {
-    const long long most = std::max<long long>(seq / 64, 1);
+  // twice the blocks that the card holds: more, shorter ones fill it more evenly
+  const long long want = kPlanSms * 8;
+  if (blocks * 2 <= want) {
+    const long long most = std::max<long long>(seq / 32, 1);
     const long long chunks = std::min(most, std::max<long long>(want / blocks, 1));
     if (chunks > 1) {
-      pl.chunk = (int)((((seq + chunks - 1) / chunks) + 15) / 16 * 16);
+      pl.chunk = (int)((((seq + chunks - 1) / chunks) + kT - 1) / kT * kT);
       pl.chunks = (int)((seq + pl.chunk - 1) / pl.chunk);
     }
   }
@@ -592,7 +818,8 @@ ScanPlan scan_grad_plan(long long seq, long long batch, long long channels, int 
     pl.carry = pl.gcarry = up4(batch * pl.chunks * channels * state);
     pl.sumdt = up4(batch * pl.chunks * channels);
   }
-  pl.ckpt = up4(batch * ((seq + sub - 1) / sub) * channels * state);
+  pl.ckpt = up4(batch * ((seq + kT - 1) / kT) * channels * state);
+  pl.cum = up4(batch * ((seq + kT - 1) / kT) * channels);
   pl.bc_part = up4(pl.slices * row);
   pl.w_part = up4(batch * pl.chunks * channels * (state + 2));
   return pl;

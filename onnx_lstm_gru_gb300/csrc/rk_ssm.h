@@ -79,7 +79,8 @@ struct ScanParams {
   int S, N, C, K, G;   // K states, G groups
   RowsArg X, Delta, Bm, Cm, Z, Y;
   RowsArg dY, dX, dDelta, dB, dC, dZ;
-  int vec;             // every operand with rows of C elements takes 16-byte pieces
+  int vec;             // every operand with rows of C elements takes 16-byte pieces (the gradient's)
+  int k_vec;           // rows of K states take 16-byte pieces
   int bc_vec;          // operands with rows of G * K take pieces of four within a group
   const float* A;
   const float* D;
@@ -99,7 +100,8 @@ struct ScanParams {
   float* sumdt;        // [N][chunks][C]
   // gradient
   float* gcarry;       // [N][chunks][C][K]: the same for the state's gradient, from the chunk's end
-  float* ckpt;         // [N][subtiles][C][K]: states at the starts of the subtiles
+  float* ckpt;         // [N][subtiles][C][K]: states at the starts of the subtiles, from the chunk's zero start
+  float* cum;          // [N][subtiles][C]: the chunk's sum of dt up to there
   float* bc_part;      // [slices][N * S][G][2][K]: sums over a slice's channels
   float* w_part;       // [N * chunks][C][K + 2]: dA, dD, d_delta_bias
   int slices;          // per group
@@ -109,9 +111,9 @@ struct ScanParams {
 struct ScanPlan {
   int chunks, chunk;
   // floats of each scratch region (multiples of 4), in the order they are placed
-  long long carry, sumdt, gcarry, ckpt, bc_part, w_part;
+  long long carry, sumdt, gcarry, ckpt, cum, bc_part, w_part;
   int slices, slice_tiles;
-  long long total() const { return carry + sumdt + gcarry + ckpt + bc_part + w_part; }
+  long long total() const { return carry + sumdt + gcarry + ckpt + cum + bc_part + w_part; }
 };
 ScanPlan scan_plan(long long seq, long long batch, long long channels, int state, int groups);
 ScanPlan scan_grad_plan(long long seq, long long batch, long long channels, int state, int groups);

@@ -273,7 +273,7 @@ rk::ScanParams scan_params(Call& c, const rk_scan_problem* p, const O* o) {
   sp.bias = c.tensor<float>("delta_bias", o->delta_bias, p->channels, 4);
   sp.lens = c.tensor<int>("sequence_lens", o->sequence_lens, p->batch, 4);
   sp.h0 = c.tensor<float>("initial_state", o->initial_state, states * K, 4);
-  sp.vec = sp.X.vec && sp.Delta.vec && sp.Z.vec;
+  sp.k_vec = K % 4 == 0 && aligned16(sp.A) && aligned16(sp.h0);
   sp.bc_vec = Call::pieces(sp.Bm, 4, c.eb, K) && Call::pieces(sp.Cm, 4, c.eb, K);
   return sp;
 }
@@ -438,6 +438,7 @@ rk_status rk_scan_encode(rk_handle* h, const rk_scan_problem* p, const rk_scan_o
   rk::ScanParams sp = scan_params(c, p, o);
   sp.Y = c.steps("Y", o->Y, p, p->channels, (int)(p->channels / p->groups), false);
   sp.hT = c.tensor<float>("final_state", o->final_state, states, 4);
+  sp.k_vec = sp.k_vec && aligned16(sp.hT);
   if (!c.ok()) return c.st;
   if (rows == 0) {
     c.copy(sp.hT, sp.h0, states * 4, s);
@@ -477,7 +478,8 @@ rk_status rk_scan_grad_encode(rk_handle* h, const rk_scan_problem* p, const rk_s
   sp.dD = c.tensor<float>("dD", o->dD, p->channels, 4);
   sp.dbias = c.tensor<float>("d_delta_bias", o->d_delta_bias, p->channels, 4);
   sp.dh0 = c.tensor<float>("d_initial_state", o->d_initial_state, states, 4);
-  sp.vec = sp.vec && sp.dY.vec && sp.dX.vec && sp.dDelta.vec && sp.dZ.vec;
+  sp.k_vec = sp.k_vec && aligned16(sp.dhT) && aligned16(sp.dh0);
+  sp.vec = sp.X.vec && sp.Delta.vec && sp.Z.vec && sp.dY.vec && sp.dX.vec && sp.dDelta.vec && sp.dZ.vec;
   if (!c.ok()) return c.st;
   if (rows == 0) {
     c.zero(sp.dA, ck * 4, s);
@@ -494,6 +496,7 @@ rk_status rk_scan_grad_encode(rk_handle* h, const rk_scan_problem* p, const rk_s
   sp.sumdt = w, w += pl.sumdt;
   sp.gcarry = w, w += pl.gcarry;
   sp.ckpt = w, w += pl.ckpt;
+  sp.cum = w, w += pl.cum;
   sp.bc_part = (sp.dB.p || sp.dC.p) ? w : nullptr, w += pl.bc_part;
   sp.w_part = (sp.dA || sp.dD || sp.dbias) ? w : nullptr;
   int launches = 0;

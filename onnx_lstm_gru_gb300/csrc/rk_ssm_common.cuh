@@ -92,12 +92,13 @@ __device__ __forceinline__ float sigmoid_fast(float x) { return rcp_fast(1.0f + 
 // polynomial in s^2, interpolated at the Chebyshev nodes of [0, 1/9] (relative
 // error 4e-9).  Nothing of a small result (steps of a thousandth are common)
 // is lost to 1 + e.
-__device__ __forceinline__ float softplus_f(float x) {
+__device__ __forceinline__ float softplus_from(float x, float& e) {
   const float n = -(fabsf(x) < 100.0f ? fabsf(x) : 100.0f), t = n * kLog2e;
   // what the product rounded away (its own factor's rounding too), put back
   // behind the exponential
   const float lo = fmaf(n, kLog2e, -t) + n * 1.9259629911e-8f;
-  const float e0 = exp2_fast(t), e = fmaf(e0, lo * 0.6931471806f, e0);
+  const float e0 = exp2_fast(t);
+  e = fmaf(e0, lo * 0.6931471806f, e0);
   const float s = e * rcp_fast(2.0f + e), q = s * s;
   float r = fmaf(q, 0.14078889f, 0.13982579f);
   r = fmaf(r, q, 0.20012298f);
@@ -105,6 +106,18 @@ __device__ __forceinline__ float softplus_f(float x) {
   r = fmaf(r, q, 1.0f);
   const float y = fmaf(2.0f * s, r, fmaxf(x, 0.0f));
   return x == x ? y : x;  // the comparisons above drop a NaN
+}
+
+__device__ __forceinline__ float softplus_f(float x) {
+  float e;
+  return softplus_from(x, e);
+}
+// And its slope, sigmoid(x).
+__device__ __forceinline__ float softplus_slope(float x, float& slope) {
+  float e;
+  const float y = softplus_from(x, e), r = rcp_fast(1.0f + e);
+  slope = x >= 0.0f ? r : e * r;
+  return x == x ? y : (slope = x);
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -148,41 +161,9 @@ __device__ __forceinline__ F2 exp2_fast2(F2 x) {
   return f2(exp2_fast(t.x), exp2_fast(t.y));
 }
 
-// softplus_f and x sigmoid(x) of two values.
-__device__ __forceinline__ F2 softplus2(F2 x) {
-  const float2 v = f2_get(x);
-  const float a = fabsf(v.x) < 100.0f ? fabsf(v.x) : 100.0f, b = fabsf(v.y) < 100.0f ? fabsf(v.y) : 100.0f;
-  const F2 n = f2(-a, -b), l = f2(kLog2e, kLog2e), t = mul2(n, l);
-  const float2 tv = f2_get(t);
-  const F2 lo = fma2(n, f2(1.9259629911e-8f, 1.9259629911e-8f), fma2(n, l, f2(-tv.x, -tv.y)));
-  const F2 e0 = exp2_fast2(t), e = fma2(e0, mul2(lo, f2(0.6931471806f, 0.6931471806f)), e0);
-  const float2 d = f2_get(add2(e, f2(2.0f, 2.0f)));
-  const F2 s = mul2(e, f2(rcp_fast(d.x), rcp_fast(d.y))), q = mul2(s, s);
-  F2 r = fma2(q, f2(0.14078889f, 0.14078889f), f2(0.13982579f, 0.13982579f));
-  r = fma2(r, q, f2(0.20012298f, 0.20012298f));
-  r = fma2(r, q, f2(0.33333161f, 0.33333161f));
-  r = fma2(r, q, f2(1.0f, 1.0f));
-  const float2 y = f2_get(fma2(add2(s, s), r, f2(fmaxf(v.x, 0.0f), fmaxf(v.y, 0.0f))));
-  return f2(v.x == v.x ? y.x : v.x, v.y == v.y ? y.y : v.y);
-}
-__device__ __forceinline__ F2 silu2(F2 x) {
-  const F2 e = exp2_fast2(mul2(x, f2(-kLog2e, -kLog2e)));
-  const float2 d = f2_get(add2(e, f2(1.0f, 1.0f)));
-  return mul2(x, f2(rcp_fast(d.x), rcp_fast(d.y)));
-}
-
 // A decay rate in base-2 exponents per unit of dt, finite, so that a step of
 // dt = 0 keeps the state whatever the rate.
 __device__ __forceinline__ float rate2(float a) { return fminf(fmaxf(a * kLog2e, -3.0e38f), 3.0e38f); }
-
-// Asynchronous copies of BYTES (4, 8 or 16) from global to shared memory, and
-// the wait for all that this thread has issued.
-template <int BYTES>
-__device__ __forceinline__ void copy_async(void* to, const void* from) {
-  const uint32_t dst = (uint32_t)__cvta_generic_to_shared(to);
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(from), "n"(BYTES) : "memory");
-}
-__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // A row's length, clamped to the steps there are.
 __device__ __forceinline__ int row_length(const int* lens, int n, int S) {
@@ -197,13 +178,14 @@ __device__ __forceinline__ int state_of(int i, int part) {
   return (i / 4 * TPC + part) * 4 + i % 4;
 }
 
-// The K states of a thread from a [K]-row of global memory.
+// The K states of a thread from a row of global memory; vec: rows take
+// 16-byte pieces.
 template <int K, int TPC>
-__device__ __forceinline__ void load_states(const float* row, int states, int part, float (&h)[K]) {
+__device__ __forceinline__ void load_states(const float* row, int states, int part, bool vec, float (&h)[K]) {
 #pragma unroll
   for (int i = 0; i < K; i += 4) {
     const int k = state_of<TPC>(i, part);
-    if (states % 4 == 0 && (reinterpret_cast<uintptr_t>(row) & 15) == 0) {
+    if (vec) {
       if (k < states) {
         const float4 v = *reinterpret_cast<const float4*>(row + k);
         h[i] = v.x, h[i + 1] = v.y, h[i + 2] = v.z, h[i + 3] = v.w;
@@ -218,11 +200,11 @@ __device__ __forceinline__ void load_states(const float* row, int states, int pa
 }
 
 template <int K, int TPC>
-__device__ __forceinline__ void store_states(float* row, int states, int part, const float (&h)[K]) {
+__device__ __forceinline__ void store_states(float* row, int states, int part, bool vec, const float (&h)[K]) {
 #pragma unroll
   for (int i = 0; i < K; i += 4) {
     const int k = state_of<TPC>(i, part);
-    if (states % 4 == 0 && (reinterpret_cast<uintptr_t>(row) & 15) == 0) {
+    if (vec) {
       if (k < states) *reinterpret_cast<float4*>(row + k) = make_float4(h[i], h[i + 1], h[i + 2], h[i + 3]);
     } else {
 #pragma unroll
