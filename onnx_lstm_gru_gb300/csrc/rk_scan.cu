@@ -166,8 +166,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) scan_kernel(ScanParams p) {
 #pragma unroll
         for (int k = 0; k < K / 4; ++k) {
           const ulonglong2 v = B[k * TPC];
-          h[2 * k] = fma2(exp2_fast2(mul2(dt2, A2[2 * k])), h[2 * k], mul2(du2, F2{v.x}));
-          h[2 * k + 1] = fma2(exp2_fast2(mul2(dt2, A2[2 * k + 1])), h[2 * k + 1], mul2(du2, F2{v.y}));
+          h[2 * k] = fma2(decay2(dt2, A2[2 * k]), h[2 * k], mul2(du2, F2{v.x}));
+          h[2 * k + 1] = fma2(decay2(dt2, A2[2 * k + 1]), h[2 * k + 1], mul2(du2, F2{v.y}));
           if constexpr (OUT) {
             const ulonglong2 e = B[Tile::kQuads + k * TPC];
             y0 = k == 0 ? mul2(F2{e.x}, h[0]) : fma2(F2{e.x}, h[2 * k], y0);
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(ScanParams p) {
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        h[j] = fmaf(exp2_fast(dt * A2[j]), h[j], dt * u * b[j]);
+        h[j] = fmaf(decay(dt, A2[j]), h[j], dt * u * b[j]);
         y = fmaf(e[j], h[j], y);
       }
       if (part == 0) y = fmaf(skip, u, y);

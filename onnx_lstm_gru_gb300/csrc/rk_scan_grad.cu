@@ -336,8 +336,8 @@ __device__ __forceinline__ void update(const Sm& sm, int r, int j, int part, con
   for (int e = 0; e < 2; ++e) {
     const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(&sm.dtu[r][e * Sm::P + j]);
     const F2 dt{w.x}, du{w.y};
-    h.v[e][0] = fma2(exp2_fast2(mul2(dt, A2.v[e][0])), h.v[e][0], mul2(du, F2{B.x}));
-    h.v[e][1] = fma2(exp2_fast2(mul2(dt, A2.v[e][1])), h.v[e][1], mul2(du, F2{B.y}));
+    h.v[e][0] = fma2(decay2(dt, A2.v[e][0]), h.v[e][0], mul2(du, F2{B.x}));
+    h.v[e][1] = fma2(decay2(dt, A2.v[e][1]), h.v[e][1], mul2(du, F2{B.y}));
   }
 }
 
@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 4) scan_grad_states_kernel(ScanParam
         if constexpr (ADJOINT) dy.v = *reinterpret_cast<const unsigned long long*>(&sm.dy[r][k * Sm::P + j]);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const F2 a = exp2_fast2(mul2(dt, A2.v[k][i]));
+          const F2 a = decay2(dt, A2.v[k][i]);
           h.v[k][i] = fma2(a, h.v[k][i], mul2(du, F2{i ? B.y : B.x}));
           if constexpr (ADJOINT) {
             pr.v[k][i] = mul2(pr.v[k][i], a);
@@ -496,7 +496,7 @@ __device__ __forceinline__ void grad_tile(const ScanParams& p, GradSmem<T, TPC>&
           const float cum = k < left ? p.cum[at * p.C + c + k] : 0.0f;
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            h.v[k][i] = fma2(exp2_fast2(mul2(f2(cum, cum), A2.v[k][i])), h0.v[k][i], h.v[k][i]);
+            h.v[k][i] = fma2(decay2(f2(cum, cum), A2.v[k][i]), h0.v[k][i], h.v[k][i]);
         }
       }
     }
@@ -549,7 +549,7 @@ __device__ __forceinline__ void grad_tile(const ScanParams& p, GradSmem<T, TPC>&
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const F2 bi{i ? B.y : B.x}, ci{i ? C.y : C.x}, a2 = A2.v[k][i];
-            const F2 a = exp2_fast2(mul2(dt, a2)), gg = fma2(ci, dy, e.v[k][i]);
+            const F2 a = decay2(dt, a2), gg = fma2(ci, dy, e.v[k][i]);
             vc[i] = k ? fma2(hs[q + 1].v[k][i], dy, vc[i]) : mul2(hs[q + 1].v[k][i], dy);
             vb[i] = k ? fma2(gg, du, vb[i]) : mul2(gg, du);
             gb = i ? fma2(gg, bi, gb) : mul2(gg, bi);

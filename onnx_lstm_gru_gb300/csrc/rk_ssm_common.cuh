@@ -161,6 +161,13 @@ __device__ __forceinline__ F2 exp2_fast2(F2 x) {
   return f2(exp2_fast(t.x), exp2_fast(t.y));
 }
 
+// The decays 2^(dt A2).  The unit's results near 1 are 2.5e-8 too small on
+// average (measured), which a state that remembers a thousand steps adds up;
+// 3e-8 more in the exponent takes that out (left: under 6e-9) and still gives
+// exactly 1 for dt = 0.
+__device__ __forceinline__ F2 decay2(F2 dt, F2 A2) { return exp2_fast2(fma2(dt, A2, f2(3e-8f, 3e-8f))); }
+__device__ __forceinline__ float decay(float dt, float A2) { return exp2_fast(fmaf(dt, A2, 3e-8f)); }
+
 // A decay rate in base-2 exponents per unit of dt, finite, so that a step of
 // dt = 0 keeps the state whatever the rate.
 __device__ __forceinline__ float rate2(float a) { return fminf(fmaxf(a * kLog2e, -3.0e38f), 3.0e38f); }
