@@ -12,100 +12,152 @@
 namespace rk {
 namespace {
 
-// Sums of N values over the TPR threads of a row: shuffles inside a warp,
-// shared memory across the warps of a wider row (buf: [2][N][TPR / 32], its
-// halves used in turn so that one barrier per sum is enough).
+// Sums of N values (a power of two up to 8) over the TPR threads of a row
+// group, in a fixed order; every thread gets them.  Inside a warp the values
+// are halved with each exchange of lanes until a lane has one; across the
+// warps of a wider group they go through shared memory (two halves used in
+// turn, so that one barrier per call is enough).
 template <int TPR, int N>
-__device__ __forceinline__ void row_sum(float (&v)[N], float* buf, int& flip) {
+struct RowSum {
+  static constexpr int W = TPR / 32;
+  __align__(16) float buf[2][W][N];
+  template <int M>
+  __device__ __forceinline__ void operator()(float (&v)[M], int& flip) {
+    static_assert(M == N, "as many values as the buffer holds");
+    const int lane = threadIdx.x % 32;
+    int at = 0;
+    lanes_sum<N, 16, 1>(v, lane, at);
+    if constexpr (W == 1) {
+      const float mine = v[0];
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
-  if constexpr (TPR > 32) {
-    constexpr int W = TPR / 32;
-    float* b = buf + flip * N * W;
-    flip ^= 1;
-    const int warp = threadIdx.x / 32;
-    if (threadIdx.x % 32 == 0) {
+      for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, mine, i * (32 / N));
+    } else {
+      if (lane % (32 / N) == 0) buf[flip][threadIdx.x / 32][lane / (32 / N)] = v[0];
+      __syncthreads();
+      if constexpr (W <= 8) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) b[i * W + warp] = v[i];
-    }
-    __syncthreads();
+        for (int i = 0; i < N; ++i) {
+          v[i] = buf[flip][0][i];
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      float s = 0.0f;
+          for (int w = 1; w < W; ++w) v[i] += buf[flip][w][i];
+        }
+      } else {
 #pragma unroll
-      for (int w = 0; w < W; ++w) s += b[i * W + w];
-      v[i] = s;
+        for (int i = 0; i < N; ++i) v[i] = warp_sum(lane < W ? buf[flip][lane][i] : 0.0f);
+      }
+      flip ^= 1;
     }
   }
-}
+};
 
-// TPR threads per row, NV pieces of V elements per thread: cols <= TPR * V * NV.
-// Blocks of one-warp rows hold four of them; a wider row has its block alone.
-template <typename T, int V, int NV, int TPR>
-__global__ void __launch_bounds__(TPR > 32 ? TPR : 128) norm_kernel(NormParams p) {
-  constexpr int kRows = TPR > 32 ? 1 : 128 / TPR;
-  __shared__ float buf[2 * (TPR / 32)];
+// Threads of a block: a group of one warp shares it with three more.
+template <int TPR>
+constexpr int kBlock = TPR > 32 ? TPR : 128;
+
+// Threads per SM that the registers of a form leave room for, and the blocks
+// that makes: the grids are one wave of them, each block running many rows.
+constexpr int kNormThreads = 640, kGradThreads = 384;
+template <int TPR, int THREADS>
+constexpr int kResident = THREADS / kBlock<TPR> > 0 ? THREADS / kBlock<TPR> : 1;
+
+// TPR threads run R rows at a time, E elements of each per thread in pieces of
+// V (cols <= TPR * E).  The next rows are on their way while these are
+// computed.
+template <typename T, int V, int E, int TPR, int R>
+__global__ void __launch_bounds__(kBlock<TPR>, R > 1 ? kResident<TPR, kNormThreads> : 1) norm_kernel(NormParams p) {
+  constexpr int kGroups = kBlock<TPR> / TPR, NV = E / V;
+  __shared__ RowSum<TPR, R> sums;
   int flip = 0;
   const int lane = threadIdx.x % TPR;
   const float rn = 1.0f / (float)p.cols;
   const T* scale = static_cast<const T*>(p.scale);
   const T* bias = static_cast<const T*>(p.bias);
-  for (long long row = (long long)blockIdx.x * kRows + threadIdx.x / TPR; row < p.rows;
-       row += (long long)gridDim.x * kRows) {
-    const T* x = static_cast<const T*>(p.X.p) + row * p.X.ss;
-    float v[NV][V];
-    float sum[1] = {0.0f};
+  const long long stride = (long long)gridDim.x * kGroups * R;
+  long long row = ((long long)blockIdx.x * kGroups + threadIdx.x / TPR) * R;
+  const T* x = static_cast<const T*>(p.X.p) + row * p.X.ss + lane * V;
+  T* y = static_cast<T*>(p.Y.p) + row * p.Y.ss + lane * V;
+  Packed<T, V> next[R][NV];
+  auto fetch = [&](long long first) {
+    const T* at = x;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = (j * TPR + lane) * V;
-      if (c < p.cols) {
-        Piece<T, V>::load(x + c, v[j]);
-      } else {
-        fill(v[j], 0.0f);
-      }
+    for (int r = 0; r < R; ++r, at += p.X.ss) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (first + r < p.rows && (j * TPR + lane) * V < p.cols) next[r][j].load_streaming(at + j * TPR * V);
     }
+    x += stride * p.X.ss;
+  };
+  fetch(row);
+  for (; row < p.rows; row += stride) {
+    float v[R][NV][V], mean[R], inv[R];
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int i = 0; i < V; ++i) sum[0] += v[j][i];
-    row_sum<TPR>(sum, buf, flip);
-    const float mean = sum[0] * rn;
-    float sq[1] = {0.0f};
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = (j * TPR + lane) * V;
-      if (c < p.cols) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          v[j][i] -= mean;
-          sq[0] += v[j][i] * v[j][i];
-        }
-      }
-    }
-    row_sum<TPR>(sq, buf, flip);
-    const float inv = rsqrtf(sq[0] * rn + p.epsilon);
-    if (lane == 0) {
-      if (p.mean) p.mean[row] = mean;
-      if (p.inv) p.inv[row] = inv;
-    }
-    if (p.Y.p) {
-      T* y = static_cast<T*>(p.Y.p) + row * p.Y.ss;
+    for (int r = 0; r < R; ++r) {
+      mean[r] = 0.0f;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const int c = (j * TPR + lane) * V;
-        if (c < p.cols) {
-          float w[V], b[V];
-          if (scale) Piece<T, V>::load(scale + c, w);
-          else fill(w, 1.0f);
-          if (bias) Piece<T, V>::load(bias + c, b);
-          else fill(b, 0.0f);
+        if ((j * TPR + lane) * V < p.cols && row + r < p.rows) next[r][j].widen(v[r][j]);
+        else fill(v[r][j], 0.0f);
 #pragma unroll
-          for (int i = 0; i < V; ++i) w[i] = fmaf(v[j][i] * inv, w[i], b[i]);
-          Piece<T, V>::store(y + c, w);
+        for (int i = 0; i < V; ++i) mean[r] += v[r][j][i];
+      }
+    }
+    fetch(row + stride);
+    sums(mean, flip);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      mean[r] *= rn;
+      inv[r] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        if ((j * TPR + lane) * V < p.cols) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            v[r][j][i] -= mean[r];
+            inv[r] = fmaf(v[r][j][i], v[r][j][i], inv[r]);
+          }
         }
       }
     }
+    sums(inv, flip);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      inv[r] = rsqrtf(inv[r] * rn + p.epsilon);
+      if (lane == 0 && row + r < p.rows) {
+        if (p.mean) p.mean[row + r] = mean[r];
+        if (p.inv) p.inv[row + r] = inv[r];
+      }
+    }
+    if (!p.Y.p) continue;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * TPR + lane) * V;
+      if (c >= p.cols) continue;
+      float w[V], b[V];
+      if (scale) Piece<T, V>::load(scale + c, w);
+      else fill(w, 1.0f);
+      if (bias) Piece<T, V>::load(bias + c, b);
+      else fill(b, 0.0f);
+      T* at = y + j * TPR * V;
+#pragma unroll
+      for (int r = 0; r < R; ++r, at += p.Y.ss) {
+        if (row + r >= p.rows) continue;
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[r][j][i] = fmaf(v[r][j][i] * inv[r], w[i], b[i]);
+        Packed<T, V> out;
+        out.narrow(v[r][j]);
+        out.store_streaming(at);
+      }
+    }
+    y += stride * p.Y.ss;
   }
+}
+
+// The sum of one value over a block.
+template <int THREADS>
+__device__ __forceinline__ float block_sum(float v, RowSum<THREADS, 1>& sums, int& flip) {
+  float a[1] = {v};
+  sums(a, flip);
+  return a[0];
 }
 
 // Rows too wide for a block's registers: read three times (from L2 after the
@@ -113,24 +165,22 @@ __global__ void __launch_bounds__(TPR > 32 ? TPR : 128) norm_kernel(NormParams p
 constexpr int kWide = 1024;
 template <typename T>
 __global__ void __launch_bounds__(kWide) norm_wide_kernel(NormParams p) {
-  __shared__ float buf[2 * (kWide / 32)];
+  __shared__ RowSum<kWide, 1> sums;
   int flip = 0;
   const float rn = 1.0f / (float)p.cols;
   const T* scale = static_cast<const T*>(p.scale);
   const T* bias = static_cast<const T*>(p.bias);
   for (long long row = blockIdx.x; row < p.rows; row += gridDim.x) {
     const T* x = static_cast<const T*>(p.X.p) + row * p.X.ss;
-    float sum[1] = {0.0f};
-    for (int c = threadIdx.x; c < p.cols; c += kWide) sum[0] += Elem<T>::to_f(x[c]);
-    row_sum<kWide>(sum, buf, flip);
-    const float mean = sum[0] * rn;
-    float sq[1] = {0.0f};
+    float sum = 0.0f;
+    for (int c = threadIdx.x; c < p.cols; c += kWide) sum += Elem<T>::to_f(x[c]);
+    const float mean = block_sum(sum, sums, flip) * rn;
+    float sq = 0.0f;
     for (int c = threadIdx.x; c < p.cols; c += kWide) {
       const float d = Elem<T>::to_f(x[c]) - mean;
-      sq[0] += d * d;
+      sq += d * d;
     }
-    row_sum<kWide>(sq, buf, flip);
-    const float inv = rsqrtf(sq[0] * rn + p.epsilon);
+    const float inv = rsqrtf(block_sum(sq, sums, flip) * rn + p.epsilon);
     if (threadIdx.x == 0) {
       if (p.mean) p.mean[row] = mean;
       if (p.inv) p.inv[row] = inv;
@@ -145,37 +195,45 @@ __global__ void __launch_bounds__(kWide) norm_wide_kernel(NormParams p) {
   }
 }
 
-// The gradient: each thread keeps the sums of its own columns over the rows
-// its block runs; the block adds its rows' threads up at the end and writes
-// one partial row of dScale and dB.
-template <typename T, int V, int NV, int TPR>
-__global__ void __launch_bounds__(TPR > 32 ? TPR : 128) norm_grad_kernel(NormParams p) {
-  constexpr int kRows = TPR > 32 ? 1 : 128 / TPR;
-  constexpr int kBuf = 4 * (TPR / 32);
-  __shared__ float buf[kRows > 1 ? (kRows * TPR * V * 2 > kBuf ? kRows * TPR * V * 2 : kBuf) : kBuf];
+// The gradient: R rows at a time as above; each thread keeps the sums of its
+// own columns over the rows its block runs, and the block writes one partial
+// row of dScale and dB.
+template <typename T, int V, int E, int TPR, int R>
+__global__ void __launch_bounds__(kBlock<TPR>, kResident<TPR, kGradThreads>) norm_grad_kernel(NormParams p) {
+  constexpr int kGroups = kBlock<TPR> / TPR, NV = E / V;
+  __shared__ RowSum<TPR, 2 * R> sums;
+  __shared__ float cols[kGroups > 1 ? kBlock<TPR> * V * 2 : 1];
   int flip = 0;
+  next_may_start();
   const int lane = threadIdx.x % TPR, grp = threadIdx.x / TPR;
   const float rn = 1.0f / (float)p.cols;
   const T* scale = static_cast<const T*>(p.scale);
   float dw[NV][V], db[NV][V];
 #pragma unroll
   for (int j = 0; j < NV; ++j) fill(dw[j], 0.0f), fill(db[j], 0.0f);
-  for (long long row = (long long)blockIdx.x * kRows + grp; row < p.rows; row += (long long)gridDim.x * kRows) {
-    const T* x = static_cast<const T*>(p.X.p) + row * p.X.ss;
-    const T* dy = static_cast<const T*>(p.dY.p) + row * p.dY.ss;
-    const float mean = p.mean_in[row], inv = p.inv_in[row];
-    float xh[NV][V], g[NV][V];
+  const long long stride = (long long)gridDim.x * kGroups * R;
+  long long row = ((long long)blockIdx.x * kGroups + grp) * R;
+  Packed<T, V> nx[R][NV], ny[R][NV];
+  float nmean[R], ninv[R];
+  auto fetch = [&](long long first) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = (j * TPR + lane) * V;
-      if (c < p.cols) {
-        Piece<T, V>::load(x + c, xh[j]);
-        Piece<T, V>::load(dy + c, g[j]);
-      } else {
-        fill(xh[j], mean), fill(g[j], 0.0f);
+    for (int r = 0; r < R; ++r) {
+      if (first + r >= p.rows) continue;
+      const T* x = static_cast<const T*>(p.X.p) + (first + r) * p.X.ss;
+      const T* dy = static_cast<const T*>(p.dY.p) + (first + r) * p.dY.ss;
+      nmean[r] = p.mean_in[first + r], ninv[r] = p.inv_in[first + r];
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = (j * TPR + lane) * V;
+        if (c < p.cols) nx[r][j].load_streaming(x + c), ny[r][j].load_streaming(dy + c);
       }
     }
-    float sum[2] = {0.0f, 0.0f};
+  };
+  fetch(row);
+  for (; row < p.rows; row += stride) {
+    float xh[R][NV][V], g[R][NV][V], inv[R], sum[2 * R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) inv[r] = ninv[r], sum[r] = sum[R + r] = 0.0f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (j * TPR + lane) * V;
@@ -183,27 +241,39 @@ __global__ void __launch_bounds__(TPR > 32 ? TPR : 128) norm_grad_kernel(NormPar
       if (scale && c < p.cols) Piece<T, V>::load(scale + c, w);
       else fill(w, 1.0f);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        xh[j][i] = (xh[j][i] - mean) * inv;
-        dw[j][i] = fmaf(g[j][i], xh[j][i], dw[j][i]);
-        db[j][i] += g[j][i];
-        g[j][i] *= w[i];
-        sum[0] += g[j][i];
-        sum[1] = fmaf(g[j][i], xh[j][i], sum[1]);
+      for (int r = 0; r < R; ++r) {
+        if (c < p.cols && row + r < p.rows) {
+          nx[r][j].widen(xh[r][j]);
+          ny[r][j].widen(g[r][j]);
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            float& a = xh[r][j][i];
+            float& y = g[r][j][i];
+            a = (a - nmean[r]) * inv[r];
+            dw[j][i] = fmaf(y, a, dw[j][i]);
+            db[j][i] += y;
+            y *= w[i];
+            sum[r] += y;
+            sum[R + r] = fmaf(y, a, sum[R + r]);
+          }
+        }
       }
     }
-    if (p.dX.p) {
-      row_sum<TPR>(sum, buf, flip);
-      const float a = sum[0] * rn, b = sum[1] * rn;
-      T* dx = static_cast<T*>(p.dX.p) + row * p.dX.ss;
+    fetch(row + stride);
+    if (!p.dX.p) continue;
+    sums(sum, flip);
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int c = (j * TPR + lane) * V;
-        if (c < p.cols) {
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * TPR + lane) * V;
 #pragma unroll
-          for (int i = 0; i < V; ++i) g[j][i] = inv * (g[j][i] - a - xh[j][i] * b);
-          Piece<T, V>::store(dx + c, g[j]);
-        }
+      for (int r = 0; r < R; ++r) {
+        if (c >= p.cols || row + r >= p.rows) continue;
+        const float a = sum[r] * rn, b = sum[R + r] * rn;
+#pragma unroll
+        for (int i = 0; i < V; ++i) g[r][j][i] = inv[r] * (g[r][j][i] - a - xh[r][j][i] * b);
+        Packed<T, V> out;
+        out.narrow(g[r][j]);
+        out.store_streaming(static_cast<T*>(p.dX.p) + (row + r) * p.dX.ss + c);
       }
     }
   }
@@ -212,9 +282,9 @@ __global__ void __launch_bounds__(TPR > 32 ? TPR : 128) norm_grad_kernel(NormPar
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int c = (j * TPR + lane) * V;
-    if constexpr (kRows > 1) {
+    if constexpr (kGroups > 1) {
       __syncthreads();
-      float* mine = buf + (grp * TPR + lane) * V * 2;
+      float* mine = cols + (grp * TPR + lane) * V * 2;
 #pragma unroll
       for (int i = 0; i < V; ++i) mine[2 * i] = dw[j][i], mine[2 * i + 1] = db[j][i];
       __syncthreads();
@@ -223,15 +293,16 @@ __global__ void __launch_bounds__(TPR > 32 ? TPR : 128) norm_grad_kernel(NormPar
         for (int i = 0; i < V; ++i) {
           float a = 0.0f, b = 0.0f;
 #pragma unroll
-          for (int r = 0; r < kRows; ++r) {
-            a += buf[((r * TPR + lane) * V + i) * 2];
-            b += buf[((r * TPR + lane) * V + i) * 2 + 1];
+          for (int r = 0; r < kGroups; ++r) {
+            a += cols[((r * TPR + lane) * V + i) * 2];
+            b += cols[((r * TPR + lane) * V + i) * 2 + 1];
           }
           dw[j][i] = a, db[j][i] = b;
         }
       }
     }
     if (grp == 0 && c < p.cols) {
+      // rows of the partial sums start anywhere: single floats
 #pragma unroll
       for (int i = 0; i < V; ++i) out[c + i] = dw[j][i], out[p.cols + c + i] = db[j][i];
     }
@@ -242,7 +313,7 @@ __global__ void __launch_bounds__(TPR > 32 ? TPR : 128) norm_grad_kernel(NormPar
 // weights' gradients column by column.
 template <typename T>
 __global__ void __launch_bounds__(kWide) norm_grad_wide_kernel(NormParams p) {
-  __shared__ float buf[4 * (kWide / 32)];
+  __shared__ RowSum<kWide, 2> sums;
   int flip = 0;
   const float rn = 1.0f / (float)p.cols;
   const T* scale = static_cast<const T*>(p.scale);
@@ -257,7 +328,7 @@ __global__ void __launch_bounds__(kWide) norm_grad_wide_kernel(NormParams p) {
       sum[0] += g;
       sum[1] = fmaf(g, (Elem<T>::to_f(x[c]) - mean) * inv, sum[1]);
     }
-    row_sum<kWide>(sum, buf, flip);
+    sums(sum, flip);
     const float a = sum[0] * rn, b = sum[1] * rn;
     for (int c = threadIdx.x; c < p.cols; c += kWide) {
       const float g = Elem<T>::to_f(dy[c]) * (scale ? Elem<T>::to_f(scale[c]) : 1.0f);
@@ -268,6 +339,7 @@ __global__ void __launch_bounds__(kWide) norm_grad_wide_kernel(NormParams p) {
 template <typename T>
 __global__ void __launch_bounds__(256) norm_grad_wide_weights_kernel(NormParams p) {
   const int c = blockIdx.x * 256 + threadIdx.x;
+  next_may_start();
   if (c >= p.cols) return;
   float dw = 0.0f, db = 0.0f;
   for (long long row = blockIdx.y; row < p.rows; row += gridDim.y) {
@@ -280,37 +352,42 @@ __global__ void __launch_bounds__(256) norm_grad_wide_weights_kernel(NormParams 
   out[c] = dw, out[p.cols + c] = db;
 }
 
-// dScale and dB from the partial rows: 32 columns per block, eight threads
-// per column over the rows, added in a fixed order.
-__global__ void __launch_bounds__(256) norm_grad_reduce_kernel(NormParams p) {
-  __shared__ float buf[8][33];
+// dScale and dB from the partial rows: 32 columns per block, 32 threads per
+// column over the rows, added in a fixed order.
+constexpr int kParts = 32;
+__global__ void __launch_bounds__(32 * kParts) norm_grad_reduce_kernel(NormParams p) {
+  __shared__ float buf[kParts][33];
   const int col = blockIdx.x * 32 + threadIdx.x % 32, part = threadIdx.x / 32;
   // columns of dScale, then of dB: a partial row is both, one after the other
   float s = 0.0f;
+  previous_done();
   if (col < 2 * p.cols) {
-#pragma unroll 4
-    for (int b = part; b < p.blocks; b += 8) s += p.partial[(long long)b * 2 * p.cols + col];
+#pragma unroll 8
+    for (int b = part; b < p.blocks; b += kParts) s += p.partial[(long long)b * 2 * p.cols + col];
   }
   buf[part][threadIdx.x % 32] = s;
   __syncthreads();
-  if (part == 0 && col < 2 * p.cols) {
-#pragma unroll
-    for (int i = 1; i < 8; ++i) s += buf[i][threadIdx.x];
-    float* out = col < p.cols ? p.dscale : p.dbias;
-    if (out) out[col < p.cols ? col : col - p.cols] = s;
+  // a warp adds a column's parts up
+  const int out_col = blockIdx.x * 32 + part;
+  s = warp_sum(buf[threadIdx.x % 32][part]);
+  if (threadIdx.x % 32 == 0 && out_col < 2 * p.cols) {
+    float* out = out_col < p.cols ? p.dscale : p.dbias;
+    if (out) out[out_col < p.cols ? out_col : out_col - p.cols] = s;
   }
 }
 
-template <typename T, int V, int NV, int TPR>
+template <typename T, int V, int E, int TPR>
 cudaError_t run_norm(const NormParams& p, cudaStream_t s) {
-  constexpr int kRows = TPR > 32 ? 1 : 128 / TPR;
-  const long long blocks = (p.rows + kRows - 1) / kRows;
-  norm_kernel<T, V, NV, TPR><<<(unsigned)std::min<long long>(blocks, 1 << 20), TPR > 32 ? TPR : 128, 0, s>>>(p);
-  return cudaGetLastError();
-}
-template <typename T, int V, int NV, int TPR>
-cudaError_t run_norm_grad(const NormParams& p, cudaStream_t s) {
-  norm_grad_kernel<T, V, NV, TPR><<<p.blocks, TPR > 32 ? TPR : 128, 0, s>>>(p);
+  constexpr int kGroups = kBlock<TPR> / TPR, kRows = E > 8 || TPR > 512 ? 1 : TPR > 256 ? 2 : 4;
+  const long long full = kPlanSms * kResident<TPR, kNormThreads>;
+  // rows one by one where that is what it takes to give every SM some
+  if (kRows == 1 || p.rows < full * kGroups * kRows / 2) {
+    const long long blocks = (p.rows + kGroups - 1) / kGroups;
+    norm_kernel<T, V, E, TPR, 1><<<(unsigned)std::min(blocks, kPlanSms * 16LL), kBlock<TPR>, 0, s>>>(p);
+  } else {
+    const long long blocks = (p.rows + kGroups * kRows - 1) / (kGroups * kRows);
+    norm_kernel<T, V, E, TPR, kRows><<<(unsigned)std::min(blocks, full), kBlock<TPR>, 0, s>>>(p);
+  }
   return cudaGetLastError();
 }
 
@@ -319,31 +396,45 @@ cudaError_t norm_typed(const NormParams& p, cudaStream_t s) {
   constexpr int V = kPiece<T>;
   const int c = p.cols;
   if (p.vec) {
-    if (c <= 32 * V) return run_norm<T, V, 1, 32>(p, s);
-    if (c <= 64 * V) return run_norm<T, V, 2, 32>(p, s);
-    if (c <= 128 * V) return run_norm<T, V, 4, 32>(p, s);
-    if (c <= 256 * V) return run_norm<T, V, 2, 128>(p, s);
-    if (c <= 512 * V) return run_norm<T, V, 4, 128>(p, s);
-    if (c <= 1024 * V) return run_norm<T, V, 4, 256>(p, s);
-    if (c <= 4096 * V) return run_norm<T, V, 4, 1024>(p, s);
+    if (c <= 256) return run_norm<T, V, 8, 32>(p, s);
+    if (c <= 512) return run_norm<T, V, 8, 64>(p, s);
+    if (c <= 1024) return run_norm<T, V, 8, 128>(p, s);
+    if (c <= 2048) return run_norm<T, V, 8, 256>(p, s);
+    if (c <= 4096) return run_norm<T, V, 8, 512>(p, s);
+    if (c <= 8192) return run_norm<T, V, 8, 1024>(p, s);
+    if (c <= 16384) return run_norm<T, V, 16, 1024>(p, s);
   } else {
-    if (c <= 128) return run_norm<T, 1, 4, 32>(p, s);
-    if (c <= 512) return run_norm<T, 1, 16, 32>(p, s);
-    if (c <= 2048) return run_norm<T, 1, 16, 128>(p, s);
-    if (c <= 4096) return run_norm<T, 1, 16, 256>(p, s);
+    if (c <= 256) return run_norm<T, 1, 8, 32>(p, s);
+    if (c <= 1024) return run_norm<T, 1, 8, 128>(p, s);
+    if (c <= 4096) return run_norm<T, 1, 8, 512>(p, s);
     if (c <= 16384) return run_norm<T, 1, 16, 1024>(p, s);
   }
   norm_wide_kernel<T><<<(unsigned)std::min<long long>(p.rows, 1 << 20), kWide, 0, s>>>(p);
   return cudaGetLastError();
 }
 
-// Widest row the gradient's register form takes: 512 threads x 16 elements of
-// any type and alignment.
-constexpr int kGradCols = 512 * 16;
+// The gradient's form for a width: threads per row group and rows at a time.
+// Eight elements per thread and row up to 8192 columns, then the wide form.
+constexpr int kGradCols = 8192;
+int grad_threads(int cols, bool vec) {
+  if (vec)
+    for (int t = 32; t < 512; t *= 2)
+      if (cols <= 8 * t) return t;
+  return cols <= 256 ? 32 : cols <= 1024 ? 128 : cols <= 4096 ? 512 : 1024;
+}
+template <typename T, int TPR>
+cudaError_t run_norm_grad(const NormParams& p, cudaStream_t s) {
+  constexpr int V = kPiece<T>;
+  // rows at a time: what the registers hold twice, as read and as floats
+  constexpr int R = TPR == 1024 ? 1 : sizeof(T) == 2 && TPR < 512 ? 4 : 2;
+  if (p.vec) norm_grad_kernel<T, V, 8, TPR, R><<<p.blocks, kBlock<TPR>, 0, s>>>(p);
+  else if constexpr (TPR != 64 && TPR != 256)
+    norm_grad_kernel<T, 1, 8, TPR, (R < 2 ? R : 2)><<<p.blocks, kBlock<TPR>, 0, s>>>(p);
+  return cudaGetLastError();
+}
 
 template <typename T>
 cudaError_t norm_grad_typed(const NormParams& p, cudaStream_t s) {
-  constexpr int V = kPiece<T>;
   const int c = p.cols;
   if (c > kGradCols) {
     if (p.dX.p && p.rows > 0)
@@ -352,29 +443,24 @@ cudaError_t norm_grad_typed(const NormParams& p, cudaStream_t s) {
       norm_grad_wide_weights_kernel<T><<<dim3((c + 255) / 256, p.blocks), 256, 0, s>>>(p);
     return cudaGetLastError();
   }
-  if (p.vec) {
-    constexpr int E = 16 / V;  // pieces of 16 elements
-    if (c <= 32 * V) return run_norm_grad<T, V, 1, 32>(p, s);
-    if (c <= 512) return run_norm_grad<T, V, E, 32>(p, s);
-    if (c <= 1024) return run_norm_grad<T, V, 2 * E, 32>(p, s);
-    if (c <= 2048) return run_norm_grad<T, V, E, 128>(p, s);
-    if (c <= 4096) return run_norm_grad<T, V, E, 256>(p, s);
-    return run_norm_grad<T, V, E, 512>(p, s);
+  switch (grad_threads(c, p.vec)) {
+    case 32: return run_norm_grad<T, 32>(p, s);
+    case 64: return run_norm_grad<T, 64>(p, s);
+    case 128: return run_norm_grad<T, 128>(p, s);
+    case 256: return run_norm_grad<T, 256>(p, s);
+    case 512: return run_norm_grad<T, 512>(p, s);
+    default: return run_norm_grad<T, 1024>(p, s);
   }
-  if (c <= 128) return run_norm_grad<T, 1, 4, 32>(p, s);
-  if (c <= 512) return run_norm_grad<T, 1, 16, 32>(p, s);
-  if (c <= 1024) return run_norm_grad<T, 1, 8, 128>(p, s);
-  if (c <= 4096) return run_norm_grad<T, 1, 16, 256>(p, s);
-  return run_norm_grad<T, 1, 16, 512>(p, s);
 }
 
 }  // namespace
 
-int norm_grad_blocks(int dtype, long long rows, int cols) {
-  // enough blocks to fill the card, few enough that their partial rows stay small
+int norm_grad_blocks(long long rows, int cols) {
   if (cols > kGradCols) return (int)std::min<long long>(std::max<long long>(rows, 1), 32);
-  const long long groups = cols <= 1024 ? (rows + 3) / 4 : rows;
-  return (int)std::min<long long>(std::max<long long>(groups, 1), kPlanSms * (cols <= 4096 ? 4 : 2));
+  const int tpr = grad_threads(cols, false), block = std::max(tpr, 128);
+  const long long at_a_time = (long long)(block / tpr) * (tpr == 1024 ? 1 : 2);
+  const long long need = (std::max<long long>(rows, 1) + at_a_time - 1) / at_a_time;
+  return (int)std::min<long long>(need, kPlanSms * std::max(kGradThreads / block, 1));
 }
 
 cudaError_t launch_norm(const NormParams& p, cudaStream_t s) {
@@ -394,9 +480,8 @@ cudaError_t launch_norm_grad(const NormParams& p, cudaStream_t s, int* launches)
   }
   *launches = 1;
   if (e != cudaSuccess || p.partial == nullptr) return e;
-  norm_grad_reduce_kernel<<<(unsigned)((2LL * p.cols + 31) / 32), 256, 0, s>>>(p);
   *launches = 2;
-  return cudaGetLastError();
+  return launch_chained(norm_grad_reduce_kernel, (unsigned)((2LL * p.cols + 31) / 32), 32 * kParts, 0, s, p);
 }
 
 }  // namespace rk

@@ -85,6 +85,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) scan_kernel(ScanParams p) {
   constexpr int NSP = K * TPC, TT = kSubSteps<NSP>, P = K / 2;
   using Tile = GroupTile<T, NSP, TT, OUT>;
   __shared__ Tile bc[2];
+  if (!OUT) next_may_start();
   const int CH = blockDim.x / TPC;
   const int per = p.C / p.G, tiles = (per + CH - 1) / CH;
   const int tile = blockIdx.x % tiles;
@@ -132,6 +133,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) scan_kernel(ScanParams p) {
     load_states<K, TPC>(p.A + (long long)c * p.K, p.K, part, p.k_vec, a);
     fill(v, 0.0f);
     if (OUT) {
+      if (p.chunks > 1) previous_done();
       if (p.chunks > 1) load_states<K, TPC>(p.carry + row * p.K, p.K, part, p.k_vec, v);
       else if (p.h0) load_states<K, TPC>(p.h0 + ((long long)n * p.C + c) * p.K, p.K, part, p.k_vec, v);
     }
@@ -219,6 +221,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) scan_kernel(ScanParams p) {
 // starts from takes the place of its own final state.
 __global__ void __launch_bounds__(64) scan_carry_kernel(ScanParams p) {
   const long long i = (long long)blockIdx.x * 64 + threadIdx.x;
+  next_may_start();
   const long long ck = (long long)p.C * p.K;
   if (i >= p.N * ck) return;
   const int n = (int)(i / ck);
@@ -226,6 +229,7 @@ __global__ void __launch_bounds__(64) scan_carry_kernel(ScanParams p) {
   const int c = (int)(at / p.K);
   const float A2 = rate2(p.A[at]);
   float run = p.h0 ? p.h0[i] : 0.0f;
+  previous_done();
   float* carry = p.carry + (long long)n * p.chunks * ck + at;
   const float* sumdt = p.sumdt + (long long)n * p.chunks * p.C + c;
   // a batch is read before any of it is overwritten: its loads are in flight together
@@ -316,17 +320,21 @@ cudaError_t run_scan(const ScanParams& p, cudaStream_t s, int* launches) {
   const long long tiles = (p.C / p.G + CH - 1) / CH;
   const long long blocks = (long long)p.N * p.chunks * p.G * tiles;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  cudaError_t e = cudaSuccess;
   if (p.chunks > 1) {
     scan_kernel<T, K, TPC, false><<<(unsigned)blocks, nt, 0, s>>>(p);
     const long long states = (long long)p.N * p.C * p.K;
-    scan_carry_kernel<<<(unsigned)((states + 63) / 64), 64, 0, s>>>(p);
+    e = launch_chained(scan_carry_kernel, (unsigned)((states + 63) / 64), 64, 0, s, p);
     *launches += 2;
-  }
-  if (p.Y.p || p.chunks == 1) {
+    if (e == cudaSuccess && p.Y.p) {
+      e = launch_chained(scan_kernel<T, K, TPC, true>, (unsigned)blocks, nt, 0, s, p);
+      *launches += 1;
+    }
+  } else {
     scan_kernel<T, K, TPC, true><<<(unsigned)blocks, nt, 0, s>>>(p);
     *launches += 1;
   }
-  return cudaGetLastError();
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <typename T, int TPC>

@@ -297,28 +297,6 @@ struct States {
   }
 };
 
-// Adds `count` values over the lanes whose bits from FIRST down to LAST
-// differ.  Each exchange leaves a lane half of its values until one is left;
-// on return v[0 .. left) are the sums of values at + 0 .. left - 1.
-template <int COUNT, int FIRST, int LAST>
-__device__ __forceinline__ void lanes_sum(float* v, int lane, int& at) {
-  if constexpr (FIRST >= LAST && FIRST > 0) {
-    if constexpr (COUNT > 1) {
-      constexpr int H = COUNT / 2;
-      const bool hi = lane & FIRST;
-#pragma unroll
-      for (int i = 0; i < H; ++i) {
-        const float send = hi ? v[i] : v[i + H], keep = hi ? v[i + H] : v[i];
-        v[i] = keep + __shfl_xor_sync(0xffffffffu, send, FIRST);
-      }
-      if (hi) at += H;
-      lanes_sum<H, FIRST / 2, LAST>(v, lane, at);
-    } else {
-      v[0] += __shfl_xor_sync(0xffffffffu, v[0], FIRST);
-      lanes_sum<1, FIRST / 2, LAST>(v, lane, at);
-    }
-  }
-}
 // Values left of COUNT after log2(LANES) exchanges.
 template <int COUNT, int LANES>
 constexpr int kLeft = COUNT > LANES ? COUNT / LANES : 1;
@@ -353,6 +331,7 @@ __global__ void __launch_bounds__(kThreads, 4) scan_grad_states_kernel(ScanParam
   constexpr Stage S = ADJOINT ? DY : STATES;
   extern __shared__ __align__(16) unsigned char smem[];
   Sm& sm = *reinterpret_cast<Sm*>(smem);
+  next_may_start();
   const int per = p.C / p.G, tiles = (per + Sm::CH - 1) / Sm::CH;
   const int tile = blockIdx.x % tiles;
   int q = blockIdx.x / tiles;
@@ -425,6 +404,8 @@ __global__ void __launch_bounds__(kThreads, 4) scan_grad_states_kernel(ScanParam
 __global__ void __launch_bounds__(64) scan_grad_carry_kernel(ScanParams p) {
   const long long i = (long long)blockIdx.x * 64 + threadIdx.x;
   const long long ck = (long long)p.C * p.K;
+  next_may_start();
+  previous_done();
   if (i >= p.N * ck) return;
   const bool back = blockIdx.y != 0;
   const int n = (int)(i / ck);
@@ -478,6 +459,7 @@ __device__ __forceinline__ void grad_tile(const ScanParams& p, GradSmem<T, TPC>&
   A2.template load<TPC>(p.A, c, left, p, part);
   A2.to_rates();
   e.zero(), dA.zero();
+  previous_done();
   if (p.chunks > 1) e.template load<TPC>(p.gcarry + chunk_row * p.K, c, left, p, part);
   else if (p.dhT) e.template load<TPC>(p.dhT + (long long)n * p.C * p.K, c, left, p, part);
   const float* start = p.chunks > 1 ? p.carry + chunk_row * p.K : p.h0 ? p.h0 + (long long)n * p.C * p.K : nullptr;
@@ -665,6 +647,7 @@ __global__ void __launch_bounds__(kThreads, 4) scan_grad_kernel(ScanParams p) {
   extern __shared__ __align__(16) unsigned char smem[];
   using Sm = GradSmem<T, TPC>;
   Sm& sm = *reinterpret_cast<Sm*>(smem);
+  next_may_start();
   const int tiles = (p.C / p.G + Sm::CH - 1) / Sm::CH;
   const int slice = blockIdx.x % p.slices;
   int q = blockIdx.x / p.slices;
@@ -681,6 +664,8 @@ template <typename T, int V>
 __global__ void __launch_bounds__(128) scan_grad_rows_kernel(ScanParams p) {
   const int row = p.G * 2 * p.K;
   const long long i = ((long long)blockIdx.x * 128 + threadIdx.x) * V;
+  next_may_start();
+  previous_done();
   const long long all = (long long)p.N * p.S * row;
   if (i >= all) return;
   const int j = (int)(i % row);
@@ -713,6 +698,7 @@ __global__ void __launch_bounds__(256) scan_grad_weights_kernel(ScanParams p) {
   const int part = threadIdx.x / 32;
   const long long rows = (long long)p.N * p.chunks;
   float s = 0.0f;
+  previous_done();
   if (col < cols) {
 #pragma unroll 4
     for (long long b = part; b < rows; b += 8) s += p.w_part[b * cols + col];
@@ -755,22 +741,24 @@ cudaError_t run_grad(const ScanParams& p, cudaStream_t s, int* launches) {
   if (e != cudaSuccess) return e;
   if (p.chunks > 1) {
     const long long states = (long long)p.N * p.C * p.K;
-    scan_grad_carry_kernel<<<dim3((unsigned)((states + 63) / 64), 2), 64, 0, s>>>(p);
+    e = launch_chained(scan_grad_carry_kernel, dim3((unsigned)((states + 63) / 64), 2), 64, 0, s, p);
+    if (e != cudaSuccess) return e;
     *launches += 1;
   }
-  scan_grad_kernel<T, TPC><<<(unsigned)(rest * p.slices), kThreads, sizeof(Sm), s>>>(p);
+  e = launch_chained(scan_grad_kernel<T, TPC>, (unsigned)(rest * p.slices), kThreads, sizeof(Sm), s, p);
   *launches += 2;
-  if (p.bc_part) {
+  if (e == cudaSuccess && p.bc_part) {
     const long long all = (long long)p.N * p.S * p.G * 2 * p.K;
-    if (p.K % 4 == 0) scan_grad_rows_kernel<T, 4><<<(unsigned)((all / 4 + 127) / 128), 128, 0, s>>>(p);
-    else scan_grad_rows_kernel<T, 1><<<(unsigned)((all + 127) / 128), 128, 0, s>>>(p);
+    const int v = p.K % 4 == 0 ? 4 : 1;
+    e = launch_chained(v == 4 ? scan_grad_rows_kernel<T, 4> : scan_grad_rows_kernel<T, 1>,
+                       (unsigned)((all / v + 127) / 128), 128, 0, s, p);
     *launches += 1;
   }
-  if (p.w_part) {
-    scan_grad_weights_kernel<<<(unsigned)(((long long)p.C * (p.K + 2) + 31) / 32), 256, 0, s>>>(p);
+  if (e == cudaSuccess && p.w_part) {
+    e = launch_chained(scan_grad_weights_kernel, (unsigned)(((long long)p.C * (p.K + 2) + 31) / 32), 256, 0, s, p);
     *launches += 1;
   }
-  return cudaGetLastError();
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <typename T>

@@ -43,7 +43,7 @@ struct NormParams {
   int blocks;      // blocks of the gradient kernel
 };
 // Blocks the gradient kernel runs, one partial row of the weights' gradients each.
-int norm_grad_blocks(int dtype, long long rows, int cols);
+int norm_grad_blocks(long long rows, int cols);
 cudaError_t launch_norm(const NormParams& p, cudaStream_t s);
 cudaError_t launch_norm_grad(const NormParams& p, cudaStream_t s, int* launches);
 

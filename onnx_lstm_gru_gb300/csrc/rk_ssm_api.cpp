@@ -249,7 +249,7 @@ RowsArg norm_rows(Call& c, const char* name, const rk_rows& t, const rk_norm_pro
 }
 
 int64_t norm_scratch(const rk_norm_problem* p) {
-  return (int64_t)rk::norm_grad_blocks(p->dtype, p->rows, (int)p->cols) * 2 * p->cols;
+  return (int64_t)rk::norm_grad_blocks(p->rows, (int)p->cols) * 2 * p->cols;
 }
 int64_t conv_scratch(const rk_conv_problem* p) {
   return (int64_t)rk::conv_grad_slices(p->seq, p->batch, p->channels) * (p->width + 1) * p->channels;
@@ -353,7 +353,7 @@ rk_status rk_norm_grad_encode(rk_handle* h, const rk_norm_problem* p, const rk_n
   }
   if (np.dscale || np.dbias) np.partial = c.scratch(scratch, norm_scratch(p), s);
   if (!c.ok()) return c.st;
-  np.blocks = rk::norm_grad_blocks(p->dtype, p->rows, cols);
+  np.blocks = rk::norm_grad_blocks(p->rows, cols);
   np.vec = np.X.vec && np.dY.vec && np.dX.vec && aligned16(np.scale);
   int launches = 0;
   c.cuda("launch", rk::launch_norm_grad(np, s, &launches));

@@ -2,6 +2,8 @@
 // and stores of 16-byte pieces of any element type, and the scalar functions
 // in float32.
 #pragma once
+#include <type_traits>
+
 #include "rk_elem.cuh"
 #include "rk_ssm.h"
 
@@ -58,6 +60,48 @@ struct Piece {
       }
     }
   }
+};
+
+// V consecutive elements as stored, to be widened later.
+template <typename T, int V>
+struct Packed {
+  using Raw = std::conditional_t<V * sizeof(T) == 16, uint4,
+                                 std::conditional_t<V * sizeof(T) == 8, uint2,
+                                                    std::conditional_t<V * sizeof(T) == 4, uint32_t, uint16_t>>>;
+  Raw raw;
+  __device__ __forceinline__ void load(const T* p) { raw = *reinterpret_cast<const Raw*>(p); }
+  // read once: leaves the caches first
+  __device__ __forceinline__ void load_streaming(const T* p) { raw = __ldcs(reinterpret_cast<const Raw*>(p)); }
+  __device__ __forceinline__ void widen(float (&o)[V]) const {
+    T t[V];
+    __builtin_memcpy(t, &raw, sizeof(raw));
+    if constexpr (sizeof(T) == 2 && V > 1) {
+      uint32_t u[V / 2];
+      __builtin_memcpy(u, &raw, sizeof(raw));
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        const float2 f = Elem<T>::pair_to_f(u[i]);
+        o[2 * i] = f.x, o[2 * i + 1] = f.y;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) o[i] = Elem<T>::to_f(t[i]);
+    }
+  }
+  __device__ __forceinline__ void narrow(const float (&o)[V]) {
+    if constexpr (sizeof(T) == 2 && V > 1) {
+      uint32_t u[V / 2];
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) u[i] = Elem<T>::pair_from_f(o[2 * i], o[2 * i + 1]);
+      __builtin_memcpy(&raw, u, sizeof(raw));
+    } else {
+      T t[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) t[i] = Elem<T>::from_f(o[i]);
+      __builtin_memcpy(&raw, t, sizeof(raw));
+    }
+  }
+  __device__ __forceinline__ void store_streaming(T* p) const { __stcs(reinterpret_cast<Raw*>(p), raw); }
 };
 
 // Elements of a 16-byte piece.
@@ -171,6 +215,46 @@ __device__ __forceinline__ float decay(float dt, float A2) { return exp2_fast(fm
 // A decay rate in base-2 exponents per unit of dt, finite, so that a step of
 // dt = 0 keeps the state whatever the rate.
 __device__ __forceinline__ float rate2(float a) { return fminf(fmaxf(a * kLog2e, -3.0e38f), 3.0e38f); }
+
+// Adds COUNT values over the lanes whose bits from FIRST down to LAST
+// differ.  Each exchange leaves a lane half of its values until one is left;
+// on return v[0 .. left) are the sums of values at + 0 .. left - 1.
+template <int COUNT, int FIRST, int LAST>
+__device__ __forceinline__ void lanes_sum(float* v, int lane, int& at) {
+  if constexpr (FIRST >= LAST && FIRST > 0) {
+    if constexpr (COUNT > 1) {
+      constexpr int H = COUNT / 2;
+      const bool hi = lane & FIRST;
+#pragma unroll
+      for (int i = 0; i < H; ++i) {
+        const float send = hi ? v[i] : v[i + H], keep = hi ? v[i + H] : v[i];
+        v[i] = keep + __shfl_xor_sync(0xffffffffu, send, FIRST);
+      }
+      if (hi) at += H;
+      lanes_sum<H, FIRST / 2, LAST>(v, lane, at);
+    } else {
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], FIRST);
+      lanes_sum<1, FIRST / 2, LAST>(v, lane, at);
+    }
+  }
+}
+// The launches of one call are chained: the next kernel's blocks may take
+// their places as soon as every block of this one runs (next_may_start), and
+// wait there until this one has ended and its writes are visible
+// (previous_done; at once where nothing was chained).
+__device__ __forceinline__ void next_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void previous_done() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename P>
+cudaError_t launch_chained(void (*kernel)(P), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, const P& p) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t config{};
+  config.gridDim = grid, config.blockDim = block, config.dynamicSmemBytes = smem, config.stream = stream;
+  config.attrs = &attr, config.numAttrs = 1;
+  return cudaLaunchKernelEx(&config, kernel, p);
+}
 
 // A row's length, clamped to the steps there are.
 __device__ __forceinline__ int row_length(const int* lens, int n, int S) {
