@@ -14,10 +14,10 @@
 namespace rk {
 namespace {
 
-// Steps of a forward chunk.  At least width - 1, so that only the first
-// chunk's thread reads the initial state, which the same thread may then
-// overwrite with the final state.
-constexpr int kFwdChunk = 16;
+// Steps of a forward chunk: all of its inputs are on their way at once.  At
+// least width - 1, so that only the first chunk's thread reads the initial
+// state, which the same thread may then overwrite with the final state.
+constexpr int kFwdChunk = 8;
 
 template <typename T, int V>
 __device__ __forceinline__ const T* row_at(const RowsArg& a, int s, int n) {
@@ -37,13 +37,17 @@ __device__ __forceinline__ void load_input(const ConvParams& p, int s, int n, in
   }
 }
 
+// The taps of V channels, which lie together: w[j][i] is tap j of channel i.
 template <typename T, int V, int W>
 __device__ __forceinline__ void load_taps(const ConvParams& p, int c, float (&w)[W][V], float (&b)[V]) {
-  const T* W0 = static_cast<const T*>(p.W) + (long long)c * W;
+  const T* at = static_cast<const T*>(p.W) + (long long)c * W;
+  float t[W][V];
 #pragma unroll
-  for (int i = 0; i < V; ++i)
+  for (int j = 0; j < W; ++j) Piece<T, V>::load(at + j * V, t[j]);
 #pragma unroll
-    for (int j = 0; j < W; ++j) w[j][i] = Elem<T>::to_f(W0[i * W + j]);
+  for (int j = 0; j < W; ++j)
+#pragma unroll
+    for (int i = 0; i < V; ++i) w[j][i] = t[(i * W + j) / V][(i * W + j) % V];
   if (p.B) Piece<T, V>::load(static_cast<const T*>(p.B) + c, b);
   else fill(b, 0.0f);
 }
@@ -54,24 +58,39 @@ __global__ void __launch_bounds__(128) conv_kernel(ConvParams p) {
   const int chunks = max((p.S + kFwdChunk - 1) / kFwdChunk, 1);
   const long long item = (long long)blockIdx.x * 128 + threadIdx.x;
   if (item >= (long long)pieces * chunks * p.N) return;
-  const int c = (int)(item % pieces) * V;
-  const int k = (int)(item / pieces % chunks), n = (int)(item / pieces / chunks);
+  const unsigned q = (unsigned)(item / pieces);  // fits: chunks and N are at most 2^31 together
+  const int c = (int)(item - (long long)q * pieces) * V;
+  const int k = (int)(q % chunks), n = (int)(q / chunks);
   const int len = row_length(p.lens, n, p.S);
   const int s0 = k * kFwdChunk, s1 = min(s0 + kFwdChunk, p.S), live = min(s1, len);
   if (p.Y.p) {
-    T* y = static_cast<T*>(p.Y.p) + n * p.Y.ns + c;
+    T* y = static_cast<T*>(p.Y.p) + n * p.Y.ns + s0 * p.Y.ss + c;
     if (s0 < live) {
+      Packed<T, V> raw[kFwdChunk + W - 1];  // the inputs of steps s0 - (W - 1) ..
+      const T* in = static_cast<const T*>(p.X.p) + n * p.X.ns + (s0 - (W - 1)) * p.X.ss + c;
+      const T* init = static_cast<const T*>(p.init) + ((long long)n * (W - 1) + s0) * p.C + c;
+#pragma unroll
+      for (int j = 0; j < kFwdChunk + W - 1; ++j, in += p.X.ss, init += p.C) {
+        const int s = s0 - (W - 1) + j;
+        raw[j].raw = {};
+        if (s >= 0) {
+          if (s < live) raw[j].load(in);
+        } else if (j < W - 1 && p.init) {
+          raw[j].load(init);
+        }
+      }
       float w[W][V], b[V], x[W][V];  // x[j]: the input of step s - (W - 1) + j
       load_taps<T, V, W>(p, c, w, b);
 #pragma unroll
-      for (int j = 0; j < W - 1; ++j) load_input<T, V, W>(p, s0 - (W - 1) + j, n, c, x[j + 1]);
-#pragma unroll 8
-      for (int s = s0; s < live; ++s) {
+      for (int j = 0; j < W - 1; ++j) raw[j].widen(x[j + 1]);
+#pragma unroll
+      for (int r = 0; r < kFwdChunk; ++r, y += p.Y.ss) {
+        if (s0 + r >= live) break;
 #pragma unroll
         for (int j = 0; j < W - 1; ++j)
 #pragma unroll
           for (int i = 0; i < V; ++i) x[j][i] = x[j + 1][i];
-        Piece<T, V>::load(row_at<T, V>(p.X, s, n) + c, x[W - 1]);
+        raw[r + W - 1].widen(x[W - 1]);
         float o[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -80,12 +99,13 @@ __global__ void __launch_bounds__(128) conv_kernel(ConvParams p) {
           for (int j = 0; j < W; ++j) o[i] = fmaf(w[j][i], x[j][i], o[i]);
           if (p.silu) o[i] *= sigmoid_fast(o[i]);
         }
-        Piece<T, V>::store(y + s * p.Y.ss, o);
+        Piece<T, V>::store(y, o);
       }
     }
     float zero[V];
     fill(zero, 0.0f);
-    for (int s = max(s0, live); s < s1; ++s) Piece<T, V>::store(y + s * p.Y.ss, zero);
+    T* past = static_cast<T*>(p.Y.p) + n * p.Y.ns + c;
+    for (int s = max(s0, live); s < s1; ++s) Piece<T, V>::store(past + s * p.Y.ss, zero);
   }
   if (k == 0 && p.final_state) {
     // rows in increasing order: row j of the new state is row j + len of the
@@ -102,14 +122,17 @@ __global__ void __launch_bounds__(128) conv_kernel(ConvParams p) {
 // The gradient.  Per step s of the chunk the pre-activation is computed again
 // from the inputs, dp[s] = dy[s] act'(p[s]) joins the last width of them, and
 // dx[s - (W - 1)] = sum_j W[j] dp[s - j] is complete.  The W - 1 steps after
-// the chunk are run for their dp alone.  A block is 32 pieces of channels by
+// the chunk are run for their dp alone.  Steps go in groups of four, the next
+// group's elements on their way.  A block is 32 pieces of channels by
 // kGradRows chunks; its weights' gradients are added up in shared memory and
 // written as one slice.
 constexpr int kGradRows = 4;
+constexpr int kGroup = 4;  // steps loaded ahead
 
 template <typename T, int V, int W>
 __global__ void __launch_bounds__(32 * kGradRows) conv_grad_kernel(ConvParams p) {
   __shared__ float sums[kGradRows][32 * V];
+  next_may_start();
   const int lane = threadIdx.x % 32, part = threadIdx.x / 32;
   const int tiles = (p.C / V + 31) / 32;
   const int tile = blockIdx.x % tiles, slice = blockIdx.x / tiles;
@@ -124,69 +147,96 @@ __global__ void __launch_bounds__(32 * kGradRows) conv_grad_kernel(ConvParams p)
   if (c < p.C && n < p.N) {
     const int len = row_length(p.lens, n, p.S);
     const int s0 = k * p.chunk, s1 = min(s0 + p.chunk, p.S);
-    float w[W][V], b[V], x[W][V], dp[W][V];  // dp[j]: of step s - j
+    const int end = s1 + W - 1;
+    float w[W][V], b[V];
     load_taps<T, V, W>(p, c, w, b);
+    // the inputs and the pre-activations' gradients of a group's steps and the
+    // W - 1 before it
+    float x[W - 1 + kGroup][V], dp[W - 1 + kGroup][V];
 #pragma unroll
-    for (int j = 0; j < W; ++j) fill(dp[j], 0.0f);
-    if (s0 < len) {
-#pragma unroll
-      for (int j = 0; j < W - 1; ++j) load_input<T, V, W>(p, s0 - (W - 1) + j, n, c, x[j + 1]);
+    for (int j = 0; j < W - 1; ++j) {
+      fill(dp[kGroup + j], 0.0f);
+      if (s0 < len) load_input<T, V, W>(p, s0 - (W - 1) + j, n, c, x[kGroup + j]);
+      else fill(x[kGroup + j], 0.0f);
     }
-    T* dx = p.dX.p ? static_cast<T*>(p.dX.p) + n * p.dX.ns + c : nullptr;
+    T* dx = p.dX.p ? static_cast<T*>(p.dX.p) + n * p.dX.ns + (s0 - (W - 1)) * p.dX.ss + c : nullptr;
     const T* df = p.dfinal ? static_cast<const T*>(p.dfinal) + (long long)n * (W - 1) * p.C + c : nullptr;
     T* di = (p.dinit && k == 0) ? static_cast<T*>(p.dinit) + (long long)n * (W - 1) * p.C + c : nullptr;
-    for (int s = s0; s < s1 + W - 1; ++s) {
+    // the next group's inputs and gradients, on their way while one is computed
+    Packed<T, V> nx[kGroup], ny[kGroup];
+    const T* in = row_at<T, V>(p.X, s0, n) + c;
+    const T* gr = row_at<T, V>(p.dY, s0, n) + c;
+    auto fetch = [&](int s) {
 #pragma unroll
-      for (int j = W - 1; j > 0; --j)
+      for (int q = 0; q < kGroup; ++q, in += p.X.ss, gr += p.dY.ss)
+        if (s + q < min(end, len)) nx[q].load(in), ny[q].load(gr);
+    };
+    // one group; inside: all of its steps are the chunk's own and within the
+    // length, and the inputs it completes are the chunk's
+    auto group = [&](int first, auto inside) {
+      constexpr bool kInside = decltype(inside)::value;
 #pragma unroll
-        for (int i = 0; i < V; ++i) dp[j][i] = dp[j - 1][i];
-      if (s < len) {
+      for (int j = 0; j < W - 1; ++j)
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j)
+        for (int i = 0; i < V; ++i) x[j][i] = x[kGroup + j][i], dp[j][i] = dp[kGroup + j][i];
 #pragma unroll
-          for (int i = 0; i < V; ++i) x[j][i] = x[j + 1][i];
-        Piece<T, V>::load(row_at<T, V>(p.X, s, n) + c, x[W - 1]);
-        Piece<T, V>::load(row_at<T, V>(p.dY, s, n) + c, dp[0]);
+      for (int q = 0; q < kGroup; ++q) {
+        if (kInside || first + q < min(end, len)) nx[q].widen(x[W - 1 + q]), ny[q].widen(dp[W - 1 + q]);
+        else fill(x[W - 1 + q], 0.0f), fill(dp[W - 1 + q], 0.0f);
+      }
+      fetch(first + kGroup);
+#pragma unroll
+      for (int q = 0; q < kGroup; ++q) {
+        float(&d)[V] = dp[W - 1 + q];
         if (p.silu) {
 #pragma unroll
           for (int i = 0; i < V; ++i) {
             float pre = b[i];
 #pragma unroll
-            for (int j = 0; j < W; ++j) pre = fmaf(w[j][i], x[j][i], pre);
+            for (int j = 0; j < W; ++j) pre = fmaf(w[j][i], x[q + j][i], pre);
             const float sg = sigmoid_fast(pre);
-            dp[0][i] *= sg * (1.0f + pre * (1.0f - sg));
+            d[i] *= sg * fmaf(pre, 1.0f - sg, 1.0f);
           }
         }
-        if (s < s1) {
+        // the steps after the chunk are another's: their gradients count for
+        // this one's inputs alone
+        if (kInside || first + q < s1) {
 #pragma unroll
           for (int i = 0; i < V; ++i) {
 #pragma unroll
-            for (int j = 0; j < W; ++j) dw[j][i] = fmaf(dp[0][i], x[j][i], dw[j][i]);
-            dw[W][i] += dp[0][i];
+            for (int j = 0; j < W; ++j) dw[j][i] = fmaf(d[i], x[q + j][i], dw[j][i]);
+            dw[W][i] += d[i];
           }
         }
-      } else {
-        fill(dp[0], 0.0f);
+        const int t = first + q - (W - 1);  // the input whose gradient is complete
+        float o[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          o[i] = w[0][i] * dp[W - 1 + q][i];
+#pragma unroll
+          for (int j = 1; j < W; ++j) o[i] = fmaf(w[j][i], dp[W - 1 + q - j][i], o[i]);
+        }
+        if (kInside) {
+          if (dx) Piece<T, V>::store(dx, o);
+        } else if (t < s1) {
+          const int f = t - len + (W - 1);  // the row of the final state that this input is
+          if (df && f >= 0 && f < W - 1) {
+            float g[V];
+            Piece<T, V>::load(df + (long long)f * p.C, g);
+#pragma unroll
+            for (int i = 0; i < V; ++i) o[i] += g[i];
+          }
+          // before the chunk: another chunk's input, or a row of the initial state
+          if (t >= s0 && dx) Piece<T, V>::store(dx, o);
+          else if (t < 0 && di) Piece<T, V>::store(di + (long long)(t + W - 1) * p.C, o);
+        }
+        if (dx) dx += p.dX.ss;
       }
-      const int t = s - (W - 1);  // the input whose gradient is complete
-      // before the chunk: another chunk's input, or a row of the initial state
-      if (t < s0 && (k > 0 || di == nullptr)) continue;
-      if (t >= 0 && dx == nullptr) continue;
-      float o[V];
-      fill(o, 0.0f);
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-#pragma unroll
-        for (int j = 0; j < W; ++j) o[i] = fmaf(w[W - 1 - j][i], dp[W - 1 - j][i], o[i]);
-      const int f = t - len + (W - 1);  // the row of the final state that this input is
-      if (df && f >= 0 && f < W - 1) {
-        float g[V];
-        Piece<T, V>::load(df + (long long)f * p.C, g);
-#pragma unroll
-        for (int i = 0; i < V; ++i) o[i] += g[i];
-      }
-      if (t >= 0) Piece<T, V>::store(dx + t * p.dX.ss, o);
-      else Piece<T, V>::store(di + (long long)(t + W - 1) * p.C, o);
+    };
+    fetch(s0);
+    for (int first = s0; first < end; first += kGroup) {
+      if (first - (W - 1) >= s0 && first + kGroup <= min(s1, len)) group(first, std::true_type{});
+      else group(first, std::false_type{});
     }
   }
   if (p.partial == nullptr) return;
@@ -213,6 +263,7 @@ __global__ void __launch_bounds__(256) conv_grad_reduce_kernel(ConvParams p) {
   const int col = blockIdx.x * 32 + threadIdx.x % 32, part = threadIdx.x / 32;  // tap-major
   const int cols = taps * p.C;
   float s = 0.0f;
+  previous_done();
   if (col < cols) {
 #pragma unroll 4
     for (int b = part; b < p.slices; b += 8) s += p.partial[(long long)b * cols + col];
@@ -244,10 +295,12 @@ cudaError_t run_conv_grad(const ConvParams& p, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-template <typename T, int V>
-cudaError_t by_width(const ConvParams& p, cudaStream_t s, bool grad) {
-#define RK_CONV_WIDTH(w) \
-  case w: return grad ? run_conv_grad<T, V, w>(p, s) : run_conv<T, V, w>(p, s);
+template <typename T, int V, bool GRAD>
+cudaError_t by_width(const ConvParams& p, cudaStream_t s) {
+#define RK_CONV_WIDTH(w)                                       \
+  case w:                                                      \
+    if constexpr (GRAD) return run_conv_grad<T, V, w>(p, s);   \
+    else return run_conv<T, V, w>(p, s);
   switch (p.width) {
     RK_CONV_WIDTH(1)
     RK_CONV_WIDTH(2)
@@ -267,8 +320,8 @@ cudaError_t conv_typed(const ConvParams& p, cudaStream_t s, bool grad) {
   // the gradient keeps twice the registers of the forward pass per channel:
   // pieces of 8 bytes
   constexpr int VG = sizeof(T) == 4 ? 2 : 4;
-  if (!p.vec) return by_width<T, 1>(p, s, grad);
-  return grad ? by_width<T, VG>(p, s, true) : by_width<T, kPiece<T>>(p, s, false);
+  if (grad) return p.vec ? by_width<T, VG, true>(p, s) : by_width<T, 1, true>(p, s);
+  return p.vec ? by_width<T, kPiece<T>, false>(p, s) : by_width<T, 1, false>(p, s);
 }
 
 cudaError_t conv_any(const ConvParams& p, cudaStream_t s, bool grad) {
@@ -281,9 +334,14 @@ cudaError_t conv_any(const ConvParams& p, cudaStream_t s, bool grad) {
 
 }  // namespace
 
+// Steps of a gradient's chunk: up to 64, beyond which the steps after a chunk
+// that are run twice no longer show; fewer where that leaves SMs without their
+// six warps (512x8x2048 bf16: 30.7 us with chunks of 16, 27.9 with 32, 24.6
+// with 64).
 int conv_grad_chunk(long long seq, long long batch, long long channels) {
-  (void)batch, (void)channels;
-  return (int)std::min<long long>(std::max<long long>(seq, 1), 32);
+  const long long warps = kPlanSms * 6, tiles = (channels + 127) / 128;
+  const long long steps = seq * batch * tiles / warps / kGroup * kGroup;
+  return (int)std::min(std::max(steps, 8LL), 64LL);
 }
 
 int conv_grad_slices(long long seq, long long batch, long long channels) {
@@ -302,9 +360,8 @@ cudaError_t launch_conv_grad(const ConvParams& p, cudaStream_t s, int* launches)
   }
   if (e != cudaSuccess || p.partial == nullptr) return e;
   const long long cols = (long long)(p.width + 1) * p.C;
-  conv_grad_reduce_kernel<<<(unsigned)((cols + 31) / 32), 256, 0, s>>>(p);
   *launches += 1;
-  return cudaGetLastError();
+  return launch_chained(conv_grad_reduce_kernel, (unsigned)((cols + 31) / 32), 256, 0, s, p);
 }
 
 }  // namespace rk

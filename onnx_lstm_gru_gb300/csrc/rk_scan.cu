@@ -252,66 +252,116 @@ __global__ void __launch_bounds__(64) scan_carry_kernel(ScanParams p) {
   if (p.hT) p.hT[i] = run;
 }
 
-// A few steps: four states per thread, TPC threads per channel, the state
+// Single tokens: four states per thread, TPC threads per channel, the state
 // read and written once in 16-byte pieces and everything else straight from
-// global memory.  Bound by the state's bytes.
-constexpr int kStepThreads = 128;
-template <typename T, int TPC>
-__global__ void __launch_bounds__(kStepThreads) scan_step_kernel(ScanParams p) {
-  const long long item = ((long long)blockIdx.x * kStepThreads + threadIdx.x) / TPC;
+// global memory.  Bound by the state's bytes; next to that by instructions, so
+// the threads of a channel share out what belongs to the channel: each
+// prepares its part of kTokens sequences, and stores its outputs.  VEC: states,
+// B and C take pieces of four; then all loads are issued before the first is
+// used.
+constexpr int kTokenThreads = 128, kTokens = 4;
+template <typename T, int TPC, bool VEC>
+__global__ void __launch_bounds__(kTokenThreads) scan_token_kernel(ScanParams p) {
+  constexpr int kOwn = (kTokens + TPC - 1) / TPC;  // sequences per thread
   const int part = threadIdx.x % TPC;
-  const bool mine = item < (long long)p.N * p.C;
-  const int n = mine ? (int)(item / p.C) : 0, c = mine ? (int)(item % p.C) : 0;
-  const int g = c / (p.C / p.G);
-  float A2[4], h[4];
-  load_states<4, TPC>(p.A + (long long)c * p.K, p.K, part, p.k_vec, A2);
+  const int c0 = blockIdx.x * (kTokenThreads / TPC) + threadIdx.x / TPC;
+  const bool mine = c0 < p.C;
+  const int c = mine ? c0 : 0, g = c / (p.C / p.G);
+  const bool holds = part * 4 < p.K;  // this thread has states
+  const int k = holds ? part * 4 : 0;
+  const long long row = (long long)p.C * p.K;  // a sequence's states
+  for (long long n0 = (long long)blockIdx.y * kTokens; n0 < p.N; n0 += (long long)gridDim.y * kTokens) {
+    const int left = (int)min((long long)kTokens, p.N - n0);
+    T u[kOwn], d[kOwn], z[kOwn];
+    int len[kOwn];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) A2[i] = rate2(A2[i]);
-  fill(h, 0.0f);
-  if (p.h0) load_states<4, TPC>(p.h0 + ((long long)n * p.C + c) * p.K, p.K, part, p.k_vec, h);
-  const int len = row_length(p.lens, n, p.S);
-  const float bias = p.bias ? p.bias[c] : 0.0f, skip = p.D ? p.D[c] : 0.0f;
-  for (int t = 0; t < p.S; ++t) {
-    float y = 0.0f;
-    if (t < len) {  // the threads of a channel share its sequence
-      const float u = Elem<T>::to_f(static_cast<const T*>(p.X.p)[n * p.X.ns + t * p.X.ss + c]);
-      float dt = Elem<T>::to_f(static_cast<const T*>(p.Delta.p)[n * p.Delta.ns + t * p.Delta.ss + c]) + bias;
-      if (p.softplus) dt = softplus_f(dt);
-      const T* B = static_cast<const T*>(p.Bm.p) + n * p.Bm.ns + t * p.Bm.ss + (long long)g * p.K;
-      const T* C = static_cast<const T*>(p.Cm.p) + n * p.Cm.ns + t * p.Cm.ss + (long long)g * p.K;
-      float b[4], e[4];
-      if (p.bc_vec) {
-        fill(b, 0.0f), fill(e, 0.0f);
-        if (part * 4 < p.K) {
-          Piece<T, 4>::load(B + part * 4, b);
-          Piece<T, 4>::load(C + part * 4, e);
-        }
-      } else {
+    for (int j = 0; j < kOwn; ++j) {
+      // past the last sequence: the last one again, not stored
+      const long long n = n0 + min(j * TPC + part, left - 1);
+      len[j] = p.lens ? p.lens[n] : 1;
+      u[j] = static_cast<const T*>(p.X.p)[n * p.X.ns + c];
+      d[j] = static_cast<const T*>(p.Delta.p)[n * p.Delta.ns + c];
+      z[j] = p.Z.p ? static_cast<const T*>(p.Z.p)[n * p.Z.ns + c] : u[j];
+    }
+    const float* rates = p.A + (long long)c * p.K + k;
+    const float* from = p.h0 ? p.h0 + n0 * row + (long long)c * p.K + k : nullptr;
+    const T* B = static_cast<const T*>(p.Bm.p) + n0 * p.Bm.ns + (long long)g * p.K + k;
+    const T* C = static_cast<const T*>(p.Cm.p) + n0 * p.Cm.ns + (long long)g * p.K + k;
+    float A2[4], h[kTokens][4], b[kTokens][4], e[kTokens][4];
+    if constexpr (VEC) {
+      Packed<T, 4> rb[kTokens], rc[kTokens];
+      Packed<float, 4> rh[kTokens], ra;
+      ra.load(rates);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const bool on = part * 4 + j < p.K;
-          b[j] = on ? Elem<T>::to_f(B[part * 4 + j]) : 0.0f;
-          e[j] = on ? Elem<T>::to_f(C[part * 4 + j]) : 0.0f;
-        }
+      for (int i = 0; i < kTokens; ++i) {
+        const int at = min(i, left - 1);
+        rb[i].load(B + at * p.Bm.ns);
+        rc[i].load(C + at * p.Cm.ns);
+        rh[i].raw = {};
+        if (from) rh[i].load(from + at * row);
       }
+      ra.widen(A2);
+#pragma unroll
+      for (int i = 0; i < kTokens; ++i) rb[i].widen(b[i]), rc[i].widen(e[i]), rh[i].widen(h[i]);
+    } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        h[j] = fmaf(decay(dt, A2[j]), h[j], dt * u * b[j]);
-        y = fmaf(e[j], h[j], y);
+        const bool on = k + j < p.K;
+        A2[j] = on ? rates[j] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < kTokens; ++i) {
+          const int at = min(i, left - 1);
+          b[i][j] = on ? Elem<T>::to_f(B[at * p.Bm.ns + j]) : 0.0f;
+          e[i][j] = on ? Elem<T>::to_f(C[at * p.Cm.ns + j]) : 0.0f;
+          h[i][j] = on && from ? from[at * row + j] : 0.0f;
+        }
       }
-      if (part == 0) y = fmaf(skip, u, y);
     }
 #pragma unroll
-    for (int o = TPC / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-    if (mine && part == 0 && p.Y.p) {
-      if (t < len && p.Z.p) {
-        const float z = Elem<T>::to_f(static_cast<const T*>(p.Z.p)[n * p.Z.ns + t * p.Z.ss + c]);
-        y *= z * sigmoid_fast(z);
+    for (int j = 0; j < 4; ++j) A2[j] = rate2(A2[j]);
+    // this thread's sequences: dt, dt u, D u, and the gate
+    const float bias = p.bias ? p.bias[c] : 0.0f, skip = p.D ? p.D[c] : 0.0f;
+    float dt[kOwn], du[kOwn], sk[kOwn], gate[kOwn];
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) {
+      const float uu = Elem<T>::to_f(u[j]), zz = Elem<T>::to_f(z[j]);
+      dt[j] = Elem<T>::to_f(d[j]) + bias;
+      if (p.softplus) dt[j] = softplus_f(dt[j]);
+      gate[j] = p.Z.p ? zz * sigmoid_fast(zz) : 1.0f;
+      du[j] = dt[j] * uu;
+      sk[j] = skip * uu;
+    }
+    float* to = p.hT ? p.hT + n0 * row + (long long)c * p.K + k : nullptr;
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+      const float dti = __shfl_sync(0xffffffffu, dt[i / TPC], i % TPC, TPC);
+      const float dui = __shfl_sync(0xffffffffu, du[i / TPC], i % TPC, TPC);
+      // a sequence without this step keeps its state, whatever its row holds
+      const bool live = __shfl_sync(0xffffffffu, len[i / TPC], i % TPC, TPC) > 0;
+      float y = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float next = fmaf(decay(dti, A2[j]), h[i][j], dui * b[i][j]);
+        if (live) h[i][j] = next;
+        y = fmaf(e[i][j], h[i][j], y);
       }
-      static_cast<T*>(p.Y.p)[n * p.Y.ns + t * p.Y.ss + c] = Elem<T>::from_f(y);
+      if (!holds) y = 0.0f;
+#pragma unroll
+      for (int o = TPC / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+      if (!mine || i >= left) continue;
+      if (part == i % TPC && p.Y.p)
+        static_cast<T*>(p.Y.p)[(n0 + i) * p.Y.ns + c] =
+            Elem<T>::from_f(live ? (y + sk[i / TPC]) * gate[i / TPC] : 0.0f);
+      if (!to || !holds) continue;
+      if constexpr (VEC) {
+        *reinterpret_cast<float4*>(to + i * row) = make_float4(h[i][0], h[i][1], h[i][2], h[i][3]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (k + j < p.K) to[i * row + j] = h[i][j];
+      }
     }
   }
-  if (mine && p.hT) store_states<4, TPC>(p.hT + ((long long)n * p.C + c) * p.K, p.K, part, p.k_vec, h);
 }
 
 template <typename T, int K, int TPC>
@@ -338,24 +388,25 @@ cudaError_t run_scan(const ScanParams& p, cudaStream_t s, int* launches) {
 }
 
 template <typename T, int TPC>
-cudaError_t run_step(const ScanParams& p, cudaStream_t s, int* launches) {
-  const long long threads = (long long)p.N * p.C * TPC;
-  scan_step_kernel<T, TPC><<<(unsigned)((threads + kStepThreads - 1) / kStepThreads), kStepThreads, 0, s>>>(p);
+cudaError_t run_token(const ScanParams& p, cudaStream_t s, int* launches) {
+  const int per = kTokenThreads / TPC, tiles = (p.C + per - 1) / per;
+  const int rows = std::min((p.N + kTokens - 1) / kTokens, 65535);
+  const dim3 grid(tiles, rows);
+  if (p.k_vec && p.bc_vec) scan_token_kernel<T, TPC, true><<<grid, kTokenThreads, 0, s>>>(p);
+  else scan_token_kernel<T, TPC, false><<<grid, kTokenThreads, 0, s>>>(p);
   *launches += 1;
   return cudaGetLastError();
 }
 
-constexpr int kStepSeq = 4;  // sequences of at most this many steps take the step kernel
-
 template <typename T>
 cudaError_t scan_typed(const ScanParams& p, cudaStream_t s, int* launches) {
-  if (p.S <= kStepSeq) {
-    if (p.K <= 4) return run_step<T, 1>(p, s, launches);
-    if (p.K <= 8) return run_step<T, 2>(p, s, launches);
-    if (p.K <= 16) return run_step<T, 4>(p, s, launches);
-    if (p.K <= 32) return run_step<T, 8>(p, s, launches);
-    if (p.K <= 64) return run_step<T, 16>(p, s, launches);
-    return run_step<T, 32>(p, s, launches);
+  if (p.S == 1) {
+    if (p.K <= 4) return run_token<T, 1>(p, s, launches);
+    if (p.K <= 8) return run_token<T, 2>(p, s, launches);
+    if (p.K <= 16) return run_token<T, 4>(p, s, launches);
+    if (p.K <= 32) return run_token<T, 8>(p, s, launches);
+    if (p.K <= 64) return run_token<T, 16>(p, s, launches);
+    return run_token<T, 32>(p, s, launches);
   }
   if (p.K <= 4) return run_scan<T, 4, 1>(p, s, launches);
   if (p.K <= 8) return run_scan<T, 8, 1>(p, s, launches);
@@ -371,7 +422,7 @@ ScanPlan scan_plan(long long seq, long long batch, long long channels, int state
   ScanPlan pl{};
   pl.chunks = 1;
   pl.chunk = (int)std::max<long long>(seq, 1);
-  if (seq <= kStepSeq || batch == 0) return pl;
+  if (seq <= 1 || batch == 0) return pl;
   const int nt = block_threads((int)(channels / groups), state);
   const long long per = channels / groups, ch = nt / tpc_of(state);
   const long long warps = batch * groups * ((per + ch - 1) / ch) * (nt / 32);

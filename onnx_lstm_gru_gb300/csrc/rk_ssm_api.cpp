@@ -379,7 +379,7 @@ rk_status rk_conv_encode(rk_handle* h, const rk_conv_problem* p, const rk_conv_o
   cp.init = c.tensor<void>("initial_state", o->initial_state, state, c.eb);
   cp.final_state = c.tensor<void>("final_state", o->final_state, state, c.eb);
   if (!c.ok() || p->batch == 0) return c.st;
-  cp.vec = cp.X.vec && cp.Y.vec && aligned16(cp.B) && aligned16(cp.init) && aligned16(cp.final_state);
+  cp.vec = cp.X.vec && cp.Y.vec && aligned16(cp.W) && aligned16(cp.B) && aligned16(cp.init) && aligned16(cp.final_state);
   c.cuda("launch", rk::launch_conv(cp, static_cast<cudaStream_t>(stream)));
   if (c.ok()) h->launches += 1;
   return c.st;
@@ -419,7 +419,7 @@ rk_status rk_conv_grad_encode(rk_handle* h, const rk_conv_problem* p, const rk_c
   if (!c.ok()) return c.st;
   cp.chunk = rk::conv_grad_chunk(p->seq, p->batch, p->channels);
   cp.slices = rk::conv_grad_slices(p->seq, p->batch, p->channels);
-  cp.vec = cp.X.vec && cp.dY.vec && cp.dX.vec && aligned16(cp.B) && aligned16(cp.init) && aligned16(cp.dfinal) &&
+  cp.vec = cp.X.vec && cp.dY.vec && cp.dX.vec && aligned16(cp.W) && aligned16(cp.B) && aligned16(cp.init) && aligned16(cp.dfinal) &&
            aligned16(cp.dinit);
   int launches = 0;
   c.cuda("launch", rk::launch_conv_grad(cp, s, &launches));
