@@ -217,19 +217,12 @@ __global__ void __launch_bounds__(kThreads, kBlocks) scan_kernel(ScanParams p) {
   }
 }
 
-// Runs through the chunks of each (sequence, channel, state): the state each
-// starts from takes the place of its own final state.
-__global__ void __launch_bounds__(64) scan_carry_kernel(ScanParams p) {
-  const long long i = (long long)blockIdx.x * 64 + threadIdx.x;
-  next_may_start();
-  const long long ck = (long long)p.C * p.K;
-  if (i >= p.N * ck) return;
-  const int n = (int)(i / ck);
-  const long long at = i % ck;
-  const int c = (int)(at / p.K);
-  const float A2 = rate2(p.A[at]);
+// The chunks of one sequence in order, for one state of one channel: the state
+// each starts from takes the place of its own final state.
+__device__ __forceinline__ void carry_chunks(const ScanParams& p, int n, unsigned at, unsigned c, long long ck,
+                                             float A2) {
+  const long long i = n * ck + at;
   float run = p.h0 ? p.h0[i] : 0.0f;
-  previous_done();
   float* carry = p.carry + (long long)n * p.chunks * ck + at;
   const float* sumdt = p.sumdt + (long long)n * p.chunks * p.C + c;
   // a batch is read before any of it is overwritten: its loads are in flight together
@@ -238,8 +231,7 @@ __global__ void __launch_bounds__(64) scan_carry_kernel(ScanParams p) {
     float s[kBatch], d[kBatch];
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
-      const int q = min(q0 + j, p.chunks - 1);
-      s[j] = carry[q * ck], d[j] = sumdt[(long long)q * p.C];
+      if (q0 + j < p.chunks) s[j] = carry[(q0 + j) * ck], d[j] = sumdt[(long long)(q0 + j) * p.C];
     }
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
@@ -250,6 +242,18 @@ __global__ void __launch_bounds__(64) scan_carry_kernel(ScanParams p) {
     }
   }
   if (p.hT) p.hT[i] = run;
+}
+
+__global__ void __launch_bounds__(64) scan_carry_kernel(ScanParams p) {
+  const unsigned ck = (unsigned)p.C * (unsigned)p.K;  // at most 2^31
+  const unsigned at = blockIdx.x * 64u + threadIdx.x;
+  next_may_start();
+  const bool on = at < ck;
+  const float A2 = on ? rate2(p.A[at]) : 0.0f;
+  previous_done();
+  if (!on) return;
+  const unsigned c = at / (unsigned)p.K;
+  for (int n = blockIdx.y; n < p.N; n += gridDim.y) carry_chunks(p, n, at, c, ck, A2);
 }
 
 // Single tokens: four states per thread, TPC threads per channel, the state
@@ -373,8 +377,8 @@ cudaError_t run_scan(const ScanParams& p, cudaStream_t s, int* launches) {
   cudaError_t e = cudaSuccess;
   if (p.chunks > 1) {
     scan_kernel<T, K, TPC, false><<<(unsigned)blocks, nt, 0, s>>>(p);
-    const long long states = (long long)p.N * p.C * p.K;
-    e = launch_chained(scan_carry_kernel, (unsigned)((states + 63) / 64), 64, 0, s, p);
+    const long long states = (long long)p.C * p.K;
+    e = launch_chained(scan_carry_kernel, dim3((unsigned)((states + 63) / 64), std::min(p.N, 65535)), 64, 0, s, p);
     *launches += 2;
     if (e == cudaSuccess && p.Y.p) {
       e = launch_chained(scan_kernel<T, K, TPC, true>, (unsigned)blocks, nt, 0, s, p);

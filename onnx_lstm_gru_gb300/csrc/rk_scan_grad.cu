@@ -402,38 +402,40 @@ __global__ void __launch_bounds__(kThreads, 4) scan_grad_states_kernel(ScanParam
 
 // The chunks in order, forward for the states and backward for their gradient.
 __global__ void __launch_bounds__(64) scan_grad_carry_kernel(ScanParams p) {
-  const long long i = (long long)blockIdx.x * 64 + threadIdx.x;
-  const long long ck = (long long)p.C * p.K;
+  const unsigned all = (unsigned)p.C * (unsigned)p.K;  // at most 2^31
+  const unsigned at = blockIdx.x * 64u + threadIdx.x;
+  const bool back = blockIdx.z != 0, on = at < all;
   next_may_start();
+  const float A2 = on ? rate2(p.A[at]) : 0.0f;
   previous_done();
-  if (i >= p.N * ck) return;
-  const bool back = blockIdx.y != 0;
-  const int n = (int)(i / ck);
-  const long long at = i % ck;
-  const float A2 = rate2(p.A[at]);
-  float* carry = (back ? p.gcarry : p.carry) + (long long)n * p.chunks * ck + at;
-  const float* sumdt = p.sumdt + (long long)n * p.chunks * p.C + at / p.K;
-  const float* from = back ? p.dhT : p.h0;
-  float run = from ? from[i] : 0.0f;
-  // a batch is read before any of it is overwritten: its loads are in flight together
-  constexpr int kBatch = 16;
-  for (int q0 = 0; q0 < p.chunks; q0 += kBatch) {
-    float s[kBatch], d[kBatch];
+  if (!on) return;
+  const long long ck = all;
+  const unsigned c = at / (unsigned)p.K;
+  for (int n = blockIdx.y; n < p.N; n += gridDim.y) {
+    const long long i = n * ck + at;
+    float* carry = (back ? p.gcarry : p.carry) + (long long)n * p.chunks * ck + at;
+    const float* sumdt = p.sumdt + (long long)n * p.chunks * p.C + c;
+    const float* from = back ? p.dhT : p.h0;
+    float run = from ? from[i] : 0.0f;
+    // a batch is read before any of it is overwritten: its loads are in flight together
+    constexpr int kBatch = 16;
+    for (int q0 = 0; q0 < p.chunks; q0 += kBatch) {
+      float s[kBatch], d[kBatch];
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      int q = min(q0 + j, p.chunks - 1);
-      if (back) q = p.chunks - 1 - q;
-      s[j] = carry[q * ck], d[j] = sumdt[(long long)q * p.C];
-    }
+      for (int j = 0; j < kBatch; ++j) {
+        const int q = back ? p.chunks - 1 - q0 - j : q0 + j;
+        if (q0 + j < p.chunks) s[j] = carry[q * ck], d[j] = sumdt[(long long)q * p.C];
+      }
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      if (q0 + j < p.chunks) {
-        carry[(back ? p.chunks - 1 - q0 - j : q0 + j) * ck] = run;
-        run = fmaf(exp2_fast(A2 * d[j]), run, s[j]);
+      for (int j = 0; j < kBatch; ++j) {
+        if (q0 + j < p.chunks) {
+          carry[(back ? p.chunks - 1 - q0 - j : q0 + j) * ck] = run;
+          run = fmaf(exp2_fast(A2 * d[j]), run, s[j]);
+        }
       }
     }
+    if (back && p.dh0) p.dh0[i] = run;
   }
-  if (back && p.dh0) p.dh0[i] = run;
 }
 
 // A channel tile's chunk, from its end to its start.
@@ -740,8 +742,9 @@ cudaError_t run_grad(const ScanParams& p, cudaStream_t s, int* launches) {
   e = p.chunks > 1 ? run_states<T, TPC, true>(p, rest * tiles, s) : run_states<T, TPC, false>(p, rest * tiles, s);
   if (e != cudaSuccess) return e;
   if (p.chunks > 1) {
-    const long long states = (long long)p.N * p.C * p.K;
-    e = launch_chained(scan_grad_carry_kernel, dim3((unsigned)((states + 63) / 64), 2), 64, 0, s, p);
+    const long long states = (long long)p.C * p.K;
+    e = launch_chained(scan_grad_carry_kernel, dim3((unsigned)((states + 63) / 64), std::min(p.N, 65535), 2), 64, 0,
+                       s, p);
     if (e != cudaSuccess) return e;
     *launches += 1;
   }

@@ -533,3 +533,23 @@ def test_binding_refusals(layer):
                    B=torch.zeros(4, 1, 200, device="cuda"), C=torch.zeros(4, 1, 200, device="cuda"))
     assert e.value.code == rk.RK_ERR_UNSUPPORTED and "SelectiveScan: state" in e.value.message
     assert layer.launches() == before
+
+
+# ---- all of them together ----------------------------------------------------------------------------------
+
+def test_example_layer(layer):
+    """The example: a layer that is trained through every gradient learns its
+    task (to remember inputs; its target has variance 1, which is the loss of
+    not learning), and gives token by token what it gives for the whole
+    sequence.  The two runs differ in the order of float32 sums of a few
+    hundred terms of size 1: 2^-24 * 300 * 10."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "state_space_layer.py")
+    spec = importlib.util.spec_from_file_location("state_space_layer_example", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    first, last, off = example.main(steps=250)
+    assert last < 0.5 * first and last < 0.5
+    assert off < 2e-4
