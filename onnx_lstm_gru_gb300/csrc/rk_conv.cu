@@ -6,6 +6,11 @@
 // width - 1 inputs in registers, and neighbouring threads hold neighbouring
 // pieces.  The sequence is cut into chunks that run side by side; a chunk
 // reads the width - 1 inputs before it once more (from L2).
+//   p[s] = b + sum_j w[j] x[s - (width - 1) + j], y = p sigmoid(p) or p
+// 512 steps x 8 x 2048 bf16, width 4, half of the steps past their length: 8.3
+// us, the floor of its bytes being 3.7; 4096 x 4 x 2048 without lengths: 31.3 us
+// (4.3 TB/s).  At these sizes a wave of blocks is short: what is left is
+// starting and draining it.
 #include <algorithm>
 
 #include "rk.h"
@@ -14,7 +19,8 @@
 namespace rk {
 namespace {
 
-// Steps of a forward chunk: all of its inputs are on their way at once.  At
+// Steps of a forward chunk: all of its inputs are on their way at once (512 x 8 x
+// 2048 bf16: 10.4 us, with 16 steps 12.4; 4096 x 4 x 2048 31.3 and 37.3).  At
 // least width - 1, so that only the first chunk's thread reads the initial
 // state, which the same thread may then overwrite with the final state.
 constexpr int kFwdChunk = 8;
@@ -125,7 +131,10 @@ __global__ void __launch_bounds__(128) conv_kernel(ConvParams p) {
 // the chunk are run for their dp alone.  Steps go in groups of four, the next
 // group's elements on their way.  A block is 32 pieces of channels by
 // kGradRows chunks; its weights' gradients are added up in shared memory and
-// written as one slice.
+// written as one slice.  512 x 8 x 2048 bf16, width 4: 24.4 us with the second
+// launch's 3.8 (50 MB: 2.1 TB/s); bound by its instructions, about 30 per
+// element for the pre-activation, SiLU's slope, dx and dw, and by the registers
+// (two groups' elements, inputs, gradients, taps), which leave few warps.
 constexpr int kGradRows = 4;
 constexpr int kGroup = 4;  // steps loaded ahead
 
@@ -318,7 +327,7 @@ cudaError_t by_width(const ConvParams& p, cudaStream_t s) {
 template <typename T>
 cudaError_t conv_typed(const ConvParams& p, cudaStream_t s, bool grad) {
   // the gradient keeps twice the registers of the forward pass per channel:
-  // pieces of 8 bytes
+  // pieces of 8 bytes (512 x 8 x 2048 bf16: 23.0 us, with 16 bytes 33.2)
   constexpr int VG = sizeof(T) == 4 ? 2 : 4;
   if (grad) return p.vec ? by_width<T, VG, true>(p, s) : by_width<T, 1, true>(p, s);
   return p.vec ? by_width<T, kPiece<T>, false>(p, s) : by_width<T, 1, false>(p, s);

@@ -5,25 +5,40 @@
 //   g = e + C dy;  dC += dy h;  dB += (dt u) g;  du += dt B g;
 //   x = g a h_before;  ddt += A x + u B g;  dA += dt x;  e = a g.
 // It needs the states in reverse order.  They are computed again rather than
-// kept: a pass forward leaves the state at the start of every subtile in
-// global memory, and the way back runs one subtile at a time, forward with
-// its states in registers and then back.  Of the few bytes per element
-// that the gradient reads and writes none is per state.
+// kept: a launch forward (scan_grad_states_kernel) leaves the state, and the
+// sum of dt since the chunk's start, at every eighth step in global memory, and
+// the way back (scan_grad_kernel) runs one such subtile at a time, forward and
+// then back.  Of the bytes per element that the gradient reads and writes there
+// are 4 / 8 per state for that, twice.
 //
 // A thread holds four states of two neighbouring channels, TPC threads a pair
 // of channels: what a step loads from shared memory serves two channels, and
 // dB and dC, sums over the channels of a group, are half added up before they
-// leave the registers.  The states of a subtile's eight steps stay in
-// registers.  The sums over states (for du and ddt) and over a warp's channels
-// (for dB and dC) halve the values with each exchange of halves between
-// lanes, so eight values over eight lanes take seven shuffles.  Over a block's
-// warps dB and dC are added in shared memory, over the blocks in a second
-// launch that adds their slices in order.  dA, dD and d_delta_bias are sums
-// over steps and sequences, kept per block and added the same way.
+// leave the registers.  Four steps' states are in registers at once: the
+// subtile's later half is run first, from the checkpoint through the earlier
+// half, which is then computed again.  All eight in registers leave no room to
+// overlap steps (the compiler spills); eight in shared memory measured
+// slower, and so did 16 states of one channel per thread, two blocks per SM
+// (546 us against 357 for the case below: 31 exchanges instead of 7 for dB and
+// dC of a step, 8 warps per SM instead of 16).
+// The sums over states (for du and ddt) and over a warp's channels (for dB and
+// dC) halve the values with each exchange of halves between lanes, so eight
+// values over eight lanes take seven shuffles.  Over a block's warps dB and dC
+// are added in shared memory, over the blocks in a second launch that adds
+// their slices in order.  dA, dD and d_delta_bias are sums over steps and
+// sequences, kept per block and added the same way.
 //
 // Chunks of one sequence that run side by side are joined as in the forward
 // scan; e is linear in what arrives at a chunk's end with the same factor
 // exp(A sum dt), so one launch prepares both directions.
+//
+// Bound by instructions: 38 per step, channel and state on the way back, half
+// of them the formulas above (2.5 decays, each an exponential, among them) and
+// half exchanges, shared memory and what belongs to a channel's step.
+// 512 steps x 8 sequences x 2048 channels x 16 states, bf16 with a gate: 357 us
+// in all, of which forward 87 us, chunks' carry 12, back 249 (2.1 instructions
+// per clock and SM, 16 warps), rows 10, weights 4; the bytes alone would take
+// 17 us, the exponentials of two passes 29.
 #include <algorithm>
 #include <type_traits>
 
@@ -792,11 +807,15 @@ ScanPlan scan_grad_plan(long long seq, long long batch, long long channels, int 
   const long long per = channels / groups, ch = 2 * kThreads / tpc_of(state);
   const long long tiles = (per + ch - 1) / ch;
   const long long blocks = batch * groups * tiles;
-  // twice the blocks that the card holds: more, shorter ones fill it more evenly
-  const long long want = kPlanSms * 8;
-  if (blocks * 2 <= want) {
-    const long long most = std::max<long long>(seq / 32, 1);
-    const long long chunks = std::min(most, std::max<long long>(want / blocks, 1));
+  // Chunks where the sequences alone fill up to two thirds of the card's places
+  // (four blocks per SM): 1024 steps x 2048 channels x 16 states bf16, 8
+  // sequences 831 us without and 625 with, 12 sequences 1084 and 899, 14
+  // sequences 1081 and 1134.  Twice as many blocks as places fill the card more
+  // evenly (8 sequences 625 against 677 us) while a chunk keeps 64 steps; a
+  // single sequence's chunks of 32 would cost 101 us against 94.
+  const long long places = kPlanSms * 4;
+  if (blocks * 3 <= places * 2) {
+    const long long chunks = std::max(std::min(seq / 64, places * 2 / blocks), std::min(seq / 32, places / blocks));
     if (chunks > 1) {
       pl.chunk = (int)((((seq + chunks - 1) / chunks) + kT - 1) / kT * kT);
       pl.chunks = (int)((seq + pl.chunk - 1) / pl.chunk);
