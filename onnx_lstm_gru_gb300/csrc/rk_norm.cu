@@ -82,65 +82,83 @@ __global__ void __launch_bounds__(kBlock<TPR>, R > 1 ? kResident<TPR, kNormThrea
   const T* scale = static_cast<const T*>(p.scale);
   const T* bias = static_cast<const T*>(p.bias);
   const long long stride = (long long)gridDim.x * kGroups * R;
-  long long row = ((long long)blockIdx.x * kGroups + threadIdx.x / TPR) * R;
+  const long long row = ((long long)blockIdx.x * kGroups + threadIdx.x / TPR) * R;
   const T* x = static_cast<const T*>(p.X.p) + row * p.X.ss + lane * V;
   T* y = static_cast<T*>(p.Y.p) + row * p.Y.ss + lane * V;
+  float* mean_to = p.mean ? p.mean + row : nullptr;
+  float* inv_to = p.inv ? p.inv + row : nullptr;
+  bool on[NV];  // pieces of this thread that are columns
   Packed<T, V> next[R][NV];
-  auto fetch = [&](long long first) {
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    on[j] = (j * TPR + lane) * V < p.cols;
+#pragma unroll
+    for (int r = 0; r < R; ++r) next[r][j].raw = {};  // and stay 0 where they are not
+  }
+  auto fetch = [&](long long rows) {
     const T* at = x;
 #pragma unroll
     for (int r = 0; r < R; ++r, at += p.X.ss) {
+      if (r >= rows) break;
 #pragma unroll
       for (int j = 0; j < NV; ++j)
-        if (first + r < p.rows && (j * TPR + lane) * V < p.cols) next[r][j].load_streaming(at + j * TPR * V);
+        if (on[j]) next[r][j].load_streaming(at + j * TPR * V);
     }
     x += stride * p.X.ss;
   };
-  fetch(row);
-  for (; row < p.rows; row += stride) {
+  long long left = p.rows - row;  // from this thread's next row on
+  fetch(left);
+  for (; left > 0; left -= stride) {
+    // past the last row: an earlier one again, not stored
+    const int rows = (int)min(left, (long long)R);
     float v[R][NV][V], mean[R], inv[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       mean[r] = 0.0f;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        if ((j * TPR + lane) * V < p.cols && row + r < p.rows) next[r][j].widen(v[r][j]);
-        else fill(v[r][j], 0.0f);
+        next[r][j].widen(v[r][j]);
 #pragma unroll
         for (int i = 0; i < V; ++i) mean[r] += v[r][j][i];
       }
     }
-    fetch(row + stride);
+    fetch(left - stride);
     sums(mean, flip);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       mean[r] *= rn;
       inv[r] = 0.0f;
+    }
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        if ((j * TPR + lane) * V < p.cols) {
+    for (int j = 0; j < NV; ++j) {
+      if (!on[j]) continue;
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            v[r][j][i] -= mean[r];
-            inv[r] = fmaf(v[r][j][i], v[r][j][i], inv[r]);
-          }
+      for (int r = 0; r < R; ++r) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          v[r][j][i] -= mean[r];
+          inv[r] = fmaf(v[r][j][i], v[r][j][i], inv[r]);
         }
       }
     }
     sums(inv, flip);
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      inv[r] = rsqrtf(inv[r] * rn + p.epsilon);
-      if (lane == 0 && row + r < p.rows) {
-        if (p.mean) p.mean[row + r] = mean[r];
-        if (p.inv) p.inv[row + r] = inv[r];
+    for (int r = 0; r < R; ++r) inv[r] = rsqrtf(inv[r] * rn + p.epsilon);
+    if (lane == 0) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (r >= rows) break;
+        if (mean_to) mean_to[r] = mean[r];
+        if (inv_to) inv_to[r] = inv[r];
       }
     }
+    if (mean_to) mean_to += stride;
+    if (inv_to) inv_to += stride;
     if (!p.Y.p) continue;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
+      if (!on[j]) continue;
       const int c = (j * TPR + lane) * V;
-      if (c >= p.cols) continue;
       float w[V], b[V];
       if (scale) Piece<T, V>::load(scale + c, w);
       else fill(w, 1.0f);
@@ -149,7 +167,7 @@ __global__ void __launch_bounds__(kBlock<TPR>, R > 1 ? kResident<TPR, kNormThrea
       T* at = y + j * TPR * V;
 #pragma unroll
       for (int r = 0; r < R; ++r, at += p.Y.ss) {
-        if (row + r >= p.rows) continue;
+        if (r >= rows) break;
 #pragma unroll
         for (int i = 0; i < V; ++i) v[r][j][i] = fmaf(v[r][j][i] * inv[r], w[i], b[i]);
         Packed<T, V> out;
@@ -222,70 +240,78 @@ __global__ void __launch_bounds__(kBlock<TPR>, kResident<TPR, kGradThreads>) nor
 #pragma unroll
   for (int j = 0; j < NV; ++j) fill(dw[j], 0.0f), fill(db[j], 0.0f);
   const long long stride = (long long)gridDim.x * kGroups * R;
-  long long row = ((long long)blockIdx.x * kGroups + grp) * R;
+  const long long row = ((long long)blockIdx.x * kGroups + grp) * R;
+  const T* x = static_cast<const T*>(p.X.p) + row * p.X.ss + lane * V;
+  const T* dy = static_cast<const T*>(p.dY.p) + row * p.dY.ss + lane * V;
+  T* dx = static_cast<T*>(p.dX.p) + row * p.dX.ss + lane * V;
+  const float *mean = p.mean_in + row, *scale_of = p.inv_in + row;
+  bool on[NV];  // pieces of this thread that are columns
+#pragma unroll
+  for (int j = 0; j < NV; ++j) on[j] = (j * TPR + lane) * V < p.cols;
   Packed<T, V> nx[R][NV], ny[R][NV];
   float nmean[R], ninv[R];
-  auto fetch = [&](long long first) {
+  auto fetch = [&](long long rows) {
+    const T *ax = x, *ay = dy;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      if (first + r >= p.rows) continue;
-      const T* x = static_cast<const T*>(p.X.p) + (first + r) * p.X.ss;
-      const T* dy = static_cast<const T*>(p.dY.p) + (first + r) * p.dY.ss;
-      nmean[r] = p.mean_in[first + r], ninv[r] = p.inv_in[first + r];
+    for (int r = 0; r < R; ++r, ax += p.X.ss, ay += p.dY.ss) {
+      if (r >= rows) break;
+      nmean[r] = mean[r], ninv[r] = scale_of[r];
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int c = (j * TPR + lane) * V;
-        if (c < p.cols) nx[r][j].load_streaming(x + c), ny[r][j].load_streaming(dy + c);
-      }
+      for (int j = 0; j < NV; ++j)
+        if (on[j]) nx[r][j].load_streaming(ax + j * TPR * V), ny[r][j].load_streaming(ay + j * TPR * V);
     }
+    x += stride * p.X.ss, dy += stride * p.dY.ss, mean += stride, scale_of += stride;
   };
-  fetch(row);
-  for (; row < p.rows; row += stride) {
+  long long left = p.rows - row;  // from this thread's next row on
+  fetch(left);
+  for (; left > 0; left -= stride) {
+    const int rows = (int)min(left, (long long)R);
     float xh[R][NV][V], g[R][NV][V], inv[R], sum[2 * R];
 #pragma unroll
     for (int r = 0; r < R; ++r) inv[r] = ninv[r], sum[r] = sum[R + r] = 0.0f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (j * TPR + lane) * V;
+      if (!on[j]) continue;
       float w[V];
-      if (scale && c < p.cols) Piece<T, V>::load(scale + c, w);
+      if (scale) Piece<T, V>::load(scale + (j * TPR + lane) * V, w);
       else fill(w, 1.0f);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        if (c < p.cols && row + r < p.rows) {
-          nx[r][j].widen(xh[r][j]);
-          ny[r][j].widen(g[r][j]);
+        if (r >= rows) break;
+        nx[r][j].widen(xh[r][j]);
+        ny[r][j].widen(g[r][j]);
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            float& a = xh[r][j][i];
-            float& y = g[r][j][i];
-            a = (a - nmean[r]) * inv[r];
-            dw[j][i] = fmaf(y, a, dw[j][i]);
-            db[j][i] += y;
-            y *= w[i];
-            sum[r] += y;
-            sum[R + r] = fmaf(y, a, sum[R + r]);
-          }
+        for (int i = 0; i < V; ++i) {
+          float& a = xh[r][j][i];
+          float& y = g[r][j][i];
+          a = (a - nmean[r]) * inv[r];
+          dw[j][i] = fmaf(y, a, dw[j][i]);
+          db[j][i] += y;
+          y *= w[i];
+          sum[r] += y;
+          sum[R + r] = fmaf(y, a, sum[R + r]);
         }
       }
     }
-    fetch(row + stride);
+    fetch(left - stride);
     if (!p.dX.p) continue;
     sums(sum, flip);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (j * TPR + lane) * V;
+      if (!on[j]) continue;
+      T* at = dx + j * TPR * V;
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        if (c >= p.cols || row + r >= p.rows) continue;
+      for (int r = 0; r < R; ++r, at += p.dX.ss) {
+        if (r >= rows) break;
         const float a = sum[r] * rn, b = sum[R + r] * rn;
 #pragma unroll
         for (int i = 0; i < V; ++i) g[r][j][i] = inv[r] * (g[r][j][i] - a - xh[r][j][i] * b);
         Packed<T, V> out;
         out.narrow(g[r][j]);
-        out.store_streaming(static_cast<T*>(p.dX.p) + (row + r) * p.dX.ss + c);
+        out.store_streaming(at);
       }
     }
+    dx += stride * p.dX.ss;
   }
   if (p.partial == nullptr) return;
   float* out = p.partial + (long long)blockIdx.x * 2 * p.cols;
@@ -362,25 +388,34 @@ __global__ void __launch_bounds__(256) norm_grad_wide_weights_kernel(NormParams 
   out[c] = dw, out[p.cols + c] = db;
 }
 
-// dScale and dB from the partial rows: 32 columns per block, 32 threads per
-// column over the rows, added in a fixed order.
-constexpr int kParts = 32;
-__global__ void __launch_bounds__(32 * kParts) norm_grad_reduce_kernel(NormParams p) {
-  __shared__ float buf[kParts][33];
-  const int col = blockIdx.x * 32 + threadIdx.x % 32, part = threadIdx.x / 32;
+// dScale and dB from the partial rows: 8 columns per block, 32 threads per
+// column over the rows, added in a fixed order.  All loads of a thread are in
+// flight at once: bound by one round trip to L2.
+constexpr int kParts = 32, kReduceCols = 8;
+__global__ void __launch_bounds__(kReduceCols * kParts) norm_grad_reduce_kernel(NormParams p) {
+  __shared__ float buf[kParts][kReduceCols + 1];
+  const int lane = threadIdx.x % kReduceCols, part = threadIdx.x / kReduceCols;
   // columns of dScale, then of dB: a partial row is both, one after the other
+  const int all = 2 * p.cols, col = blockIdx.x * kReduceCols + lane;
+  constexpr int kBatch = 16;
   float s = 0.0f;
   previous_done();
-  if (col < 2 * p.cols) {
-#pragma unroll 8
-    for (int b = part; b < p.blocks; b += kParts) s += p.partial[(long long)b * 2 * p.cols + col];
+  if (col < all) {
+    const float* at = p.partial + (long long)part * all + col;
+    for (int b = part; b < p.blocks; b += kParts * kBatch) {
+      float v[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i, at += (long long)kParts * all) v[i] = b + i * kParts < p.blocks ? *at : 0.0f;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) s += v[i];
+    }
   }
-  buf[part][threadIdx.x % 32] = s;
+  buf[part][lane] = s;
   __syncthreads();
   // a warp adds a column's parts up
-  const int out_col = blockIdx.x * 32 + part;
-  s = warp_sum(buf[threadIdx.x % 32][part]);
-  if (threadIdx.x % 32 == 0 && out_col < 2 * p.cols) {
+  const int warp = threadIdx.x / 32, out_col = blockIdx.x * kReduceCols + warp;
+  s = warp_sum(buf[threadIdx.x % 32][warp]);
+  if (threadIdx.x % 32 == 0 && out_col < all) {
     float* out = out_col < p.cols ? p.dscale : p.dbias;
     if (out) out[out_col < p.cols ? out_col : out_col - p.cols] = s;
   }
@@ -495,7 +530,8 @@ cudaError_t launch_norm_grad(const NormParams& p, cudaStream_t s, int* launches)
   *launches = 1;
   if (e != cudaSuccess || p.partial == nullptr) return e;
   *launches = 2;
-  return launch_chained(norm_grad_reduce_kernel, (unsigned)((2LL * p.cols + 31) / 32), 32 * kParts, 0, s, p);
+  return launch_chained(norm_grad_reduce_kernel, (unsigned)((2LL * p.cols + kReduceCols - 1) / kReduceCols),
+                        kReduceCols * kParts, 0, s, p);
 }
 
 }  // namespace rk
