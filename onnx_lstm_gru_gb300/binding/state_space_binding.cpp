@@ -11,6 +11,8 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -162,7 +164,7 @@ PyObject* plan_run(PyObject* self, PyObject* const* args, Py_ssize_t n) {
       if (PyDict_SetItem(out, name, given) != 0) return nullptr;
       continue;
     }
-    const at::Tensor t = at::empty(e->shape, at::TensorOptions().dtype(e->type).device(device));
+    const at::Tensor t(at::detail::empty_cuda(e->shape, e->type, device, std::nullopt));
     words[e->at] = reinterpret_cast<int64_t>(t.data_ptr());
     words[e->at + 2] = t.numel();
     THPObjectPtr obj(THPVariable_Wrap(t));
@@ -174,11 +176,11 @@ PyObject* plan_run(PyObject* self, PyObject* const* args, Py_ssize_t n) {
     st = reinterpret_cast<Call>(p->encode)(handle, p->problem->data(), words, stream);
   } else {
     // from torch's allocator: the stream's own memory, and a graph's where one is captured
-    at::Tensor t;
+    c10::DataPtr memory;
     int64_t work[3] = {};
     if (p->scratch > 0) {
-      t = at::empty({p->scratch}, at::TensorOptions().dtype(at::kFloat).device(device));
-      work[0] = reinterpret_cast<int64_t>(t.data_ptr());
+      memory = c10::cuda::CUDACachingAllocator::get()->allocate((size_t)p->scratch * sizeof(float));
+      work[0] = reinterpret_cast<int64_t>(memory.get());
       work[2] = p->scratch;
     }
     st = reinterpret_cast<ScratchCall>(p->encode)(handle, p->problem->data(), words, work, stream);
