@@ -7,7 +7,7 @@
 // pieces.  The sequence is cut into chunks that run side by side; a chunk
 // reads the width - 1 inputs before it once more (from L2).
 //   p[s] = b + sum_j w[j] x[s - (width - 1) + j], y = p sigmoid(p) or p
-// 512 steps x 8 x 2048 bf16, width 4, half of the steps past their length: 8.3
+// 512 steps x 8 x 2048 Half, width 4, half of the steps past their length: 8.3
 // us, the floor of its bytes being 3.7; 4096 x 4 x 2048 without lengths: 31.3 us
 // (4.3 TB/s).  At these sizes a wave of blocks is short: what is left is
 // starting and draining it.

@@ -436,7 +436,7 @@ cudaError_t scan_typed(const ScanParams& p, cudaStream_t s, int* launches) {
 
 }  // namespace
 
-ScanPlan scan_plan(long long seq, long long batch, long long channels, int state, int groups) {
+ScanPlan scan_plan(long long seq, long long batch, long long channels, int state, int groups, bool ragged) {
   ScanPlan pl{};
   pl.chunks = 1;
   pl.chunk = (int)std::max<long long>(seq, 1);
@@ -448,9 +448,14 @@ ScanPlan scan_plan(long long seq, long long batch, long long channels, int state
   // chunks pay for their second pass over the exponentials: 1024 steps x 2048
   // channels x 16 states bf16, 1 sequence (64 warps) 247 us without and 37
   // with, 8 sequences 270 and 201, 12 sequences 305 and 306, 16 sequences 308
-  // and 447.
-  const long long want = kPlanSms * kBlocks * (kThreads / 32);
-  if (warps * 3 < want) {
+  // and 447.  Where rows have lengths, chunks past them end at once: twice as
+  // many keep the card full where half of the steps are (lengths uniform in
+  // 1..1024: 2 sequences 47 us with as many, 37 with twice, 8 sequences 162 and
+  // 105), and they pay up to 0.4 of the warps (16 sequences 285 us without and
+  // 210 with, 24 sequences 317 and 407).
+  const long long places = kPlanSms * kBlocks * (kThreads / 32);
+  const long long want = ragged ? places * 2 : places;
+  if (ragged ? warps * 5 < places * 2 : warps * 3 < places) {
     const long long chunks = std::min(want / warps, seq / 32);
     if (chunks > 1) {
       pl.chunk = (int)((((seq + chunks - 1) / chunks) + 7) / 8 * 8);

@@ -798,7 +798,7 @@ constexpr long long kSliceFloats = 64LL << 20;
 
 }  // namespace
 
-ScanPlan scan_grad_plan(long long seq, long long batch, long long channels, int state, int groups) {
+ScanPlan scan_grad_plan(long long seq, long long batch, long long channels, int state, int groups, bool ragged) {
   ScanPlan pl{};
   pl.chunks = 1;
   pl.chunk = (int)std::max<long long>(seq, 1);
@@ -812,8 +812,11 @@ ScanPlan scan_grad_plan(long long seq, long long batch, long long channels, int 
   // sequences 831 us without and 625 with, 12 sequences 1084 and 899, 14
   // sequences 1081 and 1134.  Twice as many blocks as places fill the card more
   // evenly (8 sequences 625 against 677 us) while a chunk keeps 64 steps; a
-  // single sequence's chunks of 32 would cost 101 us against 94.
-  const long long places = kPlanSms * 4;
+  // single sequence's chunks of 32 would cost 101 us against 94.  Where rows
+  // have lengths, half of the steps are taken to be past them, and twice the
+  // blocks wanted (lengths uniform in 1..1024: 8 sequences 373 us without that
+  // and 319 with, 16 sequences 863 and 665, 24 sequences 1209 and 1217).
+  const long long places = kPlanSms * 4 * (ragged ? 2 : 1);
   if (blocks * 3 <= places * 2) {
     const long long chunks = std::max(std::min(seq / 64, places * 2 / blocks), std::min(seq / 32, places / blocks));
     if (chunks > 1) {

@@ -115,8 +115,9 @@ struct ScanPlan {
   int slices, slice_tiles;
   long long total() const { return carry + sumdt + gcarry + ckpt + cum + bc_part + w_part; }
 };
-ScanPlan scan_plan(long long seq, long long batch, long long channels, int state, int groups);
-ScanPlan scan_grad_plan(long long seq, long long batch, long long channels, int state, int groups);
+// ragged: rows have lengths of their own.
+ScanPlan scan_plan(long long seq, long long batch, long long channels, int state, int groups, bool ragged);
+ScanPlan scan_grad_plan(long long seq, long long batch, long long channels, int state, int groups, bool ragged);
 cudaError_t launch_scan(const ScanParams& p, cudaStream_t s, int* launches);
 cudaError_t launch_scan_grad(const ScanParams& p, cudaStream_t s, int* launches);
 

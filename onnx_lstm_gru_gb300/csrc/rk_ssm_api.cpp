@@ -254,6 +254,14 @@ int64_t norm_scratch(const rk_norm_problem* p) {
 int64_t conv_scratch(const rk_conv_problem* p) {
   return (int64_t)rk::conv_grad_slices(p->seq, p->batch, p->channels) * (p->width + 1) * p->channels;
 }
+// What a call takes with row lengths or without them.
+template <typename PLAN>
+int64_t scan_scratch(PLAN plan, const rk_scan_problem* p) {
+  auto total = [&](bool ragged) {
+    return (int64_t)plan(p->seq, p->batch, p->channels, (int)p->state, (int)p->groups, ragged).total();
+  };
+  return std::max(total(false), total(true));
+}
 
 // The operands that the scan and its gradient share.
 template <typename O>
@@ -297,13 +305,13 @@ int64_t rk_conv_grad_scratch_length(const rk_conv_problem* p) {
 int64_t rk_scan_scratch_length(const rk_scan_problem* p) {
   Call c = begin(nullptr, "SelectiveScan", p, nullptr, false);
   if (c.ok()) check(c, p);
-  return c.ok() ? rk::scan_plan(p->seq, p->batch, p->channels, (int)p->state, (int)p->groups).total() : -1;
+  return c.ok() ? scan_scratch(rk::scan_plan, p) : -1;
 }
 
 int64_t rk_scan_grad_scratch_length(const rk_scan_problem* p) {
   Call c = begin(nullptr, "SelectiveScanGrad", p, nullptr, false);
   if (c.ok()) check(c, p);
-  return c.ok() ? rk::scan_grad_plan(p->seq, p->batch, p->channels, (int)p->state, (int)p->groups).total() : -1;
+  return c.ok() ? scan_scratch(rk::scan_grad_plan, p) : -1;
 }
 
 rk_status rk_norm_encode(rk_handle* h, const rk_norm_problem* p, const rk_norm_operands* o, void* stream) {
@@ -444,8 +452,8 @@ rk_status rk_scan_encode(rk_handle* h, const rk_scan_problem* p, const rk_scan_o
     c.copy(sp.hT, sp.h0, states * 4, s);
     return c.st;
   }
-  const rk::ScanPlan pl = rk::scan_plan(p->seq, p->batch, p->channels, sp.K, sp.G);
-  float* w = c.scratch(scratch, pl.total(), s);
+  const rk::ScanPlan pl = rk::scan_plan(p->seq, p->batch, p->channels, sp.K, sp.G, sp.lens != nullptr);
+  float* w = c.scratch(scratch, scan_scratch(rk::scan_plan, p), s);
   if (!c.ok()) return c.st;
   sp.chunks = pl.chunks, sp.chunk = pl.chunk;
   sp.carry = w;
@@ -488,8 +496,8 @@ rk_status rk_scan_grad_encode(rk_handle* h, const rk_scan_problem* p, const rk_s
     c.copy(sp.dh0, sp.dhT, states * 4, s);
     return c.st;
   }
-  const rk::ScanPlan pl = rk::scan_grad_plan(p->seq, p->batch, p->channels, sp.K, sp.G);
-  float* w = c.scratch(scratch, pl.total(), s);
+  const rk::ScanPlan pl = rk::scan_grad_plan(p->seq, p->batch, p->channels, sp.K, sp.G, sp.lens != nullptr);
+  float* w = c.scratch(scratch, scan_scratch(rk::scan_grad_plan, p), s);
   if (!c.ok()) return c.st;
   sp.chunks = pl.chunks, sp.chunk = pl.chunk, sp.slices = pl.slices, sp.slice_tiles = pl.slice_tiles;
   sp.carry = w, w += pl.carry;
