@@ -452,13 +452,16 @@ ScanPlan scan_plan(long long seq, long long batch, long long channels, int state
   // many keep the card full where half of the steps are (lengths uniform in
   // 1..1024: 2 sequences 47 us with as many, 37 with twice, 8 sequences 162 and
   // 105), and they pay up to 0.4 of the warps (16 sequences 285 us without and
-  // 210 with, 24 sequences 317 and 407).
+  // 210 with, 24 sequences 317 and 407).  A chunk of 8 steps is as short as pays
+  // (128 steps of one sequence: 12.7 us, with 16 at least 14.6, with 32 22.7),
+  // and the two launches more from 40 steps on (40 steps 12.3 us against 14.4,
+  // 24 steps 12.1 against 10.4).
   const long long places = kPlanSms * kBlocks * (kThreads / 32);
   const long long want = ragged ? places * 2 : places;
-  if (ragged ? warps * 5 < places * 2 : warps * 3 < places) {
-    const long long chunks = std::min(want / warps, seq / 32);
+  if (seq >= 40 && (ragged ? warps * 5 < places * 2 : warps * 3 < places)) {
+    const long long chunks = std::min(want / warps, seq / 8);
     if (chunks > 1) {
-      pl.chunk = (int)((((seq + chunks - 1) / chunks) + 7) / 8 * 8);
+      pl.chunk = (int)((((seq + chunks - 1) / chunks) + kGroup - 1) / kGroup * kGroup);
       pl.chunks = (int)((seq + pl.chunk - 1) / pl.chunk);
     }
   }

@@ -811,14 +811,17 @@ ScanPlan scan_grad_plan(long long seq, long long batch, long long channels, int 
   // (four blocks per SM): 1024 steps x 2048 channels x 16 states bf16, 8
   // sequences 831 us without and 625 with, 12 sequences 1084 and 899, 14
   // sequences 1081 and 1134.  Twice as many blocks as places fill the card more
-  // evenly (8 sequences 625 against 677 us) while a chunk keeps 64 steps; a
-  // single sequence's chunks of 32 would cost 101 us against 94.  Where rows
-  // have lengths, half of the steps are taken to be past them, and twice the
-  // blocks wanted (lengths uniform in 1..1024: 8 sequences 373 us without that
-  // and 319 with, 16 sequences 863 and 665, 24 sequences 1209 and 1217).
+  // evenly (8 sequences 625 against 677 us) while a chunk keeps 64 steps (a
+  // single sequence's chunks of 32 would cost 101 us against 94); up to the
+  // places chunks go down to a subtile (201 steps x 3 x 519 x 24: 38 us, with 16
+  // steps at least 44, with 32 53).  From 24 steps on (2048 channels: 24 steps
+  // 24.6 us against 28.9 without chunks, 16 steps the same).  Where rows have
+  // lengths, half of the steps are taken to be past them, and twice the blocks
+  // wanted (lengths uniform in 1..1024: 8 sequences 373 us without that and 319
+  // with, 16 sequences 863 and 665, 24 sequences 1209 and 1217).
   const long long places = kPlanSms * 4 * (ragged ? 2 : 1);
-  if (blocks * 3 <= places * 2) {
-    const long long chunks = std::max(std::min(seq / 64, places * 2 / blocks), std::min(seq / 32, places / blocks));
+  if (seq >= 24 && blocks * 3 <= places * 2) {
+    const long long chunks = std::max(std::min(seq / 64, places * 2 / blocks), std::min(seq / kT, places / blocks));
     if (chunks > 1) {
       pl.chunk = (int)((((seq + chunks - 1) / chunks) + kT - 1) / kT * kT);
       pl.chunks = (int)((seq + pl.chunk - 1) / pl.chunk);
