@@ -40,9 +40,9 @@ struct NormParams {
   float* dscale;
   float* dbias;
   float* partial;  // [blocks][2][cols]
-  int blocks;      // blocks of the gradient kernel
+  int blocks;      // most blocks of the gradient kernel
 };
-// Blocks the gradient kernel runs, one partial row of the weights' gradients each.
+// Most blocks that the gradient kernel runs, one partial row of the weights' gradients each.
 int norm_grad_blocks(long long rows, int cols);
 cudaError_t launch_norm(const NormParams& p, cudaStream_t s);
 cudaError_t launch_norm_grad(const NormParams& p, cudaStream_t s, int* launches);
