@@ -8,11 +8,12 @@
 //   g = dy w, xh = (x - mean) inv; dx = inv (g - avg(g) - xh avg(g xh))
 //   dw = sum over rows of dy xh; db = sum over rows of dy
 // A block runs rows one after the other with the next ones' loads in flight.
-// 32768 x 1024 bf16: forward 24.8 us (5.4 TB/s over its 134 MB), gradient 46.8
-// us (4.3 TB/s over 202 MB, with its second launch of 6 us).  The gradient is
-// held back by its instructions (12 warps per SM are what its registers leave:
-// two rows' elements as read and as floats, and the column sums); one or two
-// rows at a time, packed arithmetic and loads that stay in L2 measured slower.
+// 32768 x 1024 bf16: forward 24.6 us (5.5 TB/s over its 134 MB), gradient 43.6
+// us (4.6 TB/s over 202 MB, about 4 us of it the second launch).  The gradient
+// is held back by the loads that 12 warps per SM keep in flight, which is what
+// its registers leave (four rows' elements as read, and the column sums), and by
+// 23 instructions per element; one or two rows at a time, packed arithmetic and
+// loads that stay in L2 measured slower.
 #include <algorithm>
 
 #include "rk.h"
