@@ -126,6 +126,22 @@ def test_norm_grad(layer, rows, cols, dtype):
         same_bits(got, layer.norm_grad(p, X, **args))
 
 
+# many rows, read in pieces and element by element: whole turns of all blocks, one row less and more
+@pytest.mark.parametrize("rows,cols", [(455, 130), (457, 130), (913, 264), (3649, 264), (2433, 1031), (7296, 777),
+                                       (7297, 777), (29185, 33)])
+def test_norm_grad_many_rows(layer, rows, cols):
+    for dtype in ("f32", "bf16"):
+        i = Inputs(rows + cols, dtype)
+        X, dY, S = i.rows(rows, cols), i.rows(rows, cols), i.normal(cols, mean=1.0, scale=0.2)
+        f = ref.norm(X.double().cpu(), epsilon=1e-3)
+        args = dict(Scale=S, Mean=f["Mean"].float().cuda(), InvStdDev=f["InvStdDev"].float().cuda(), dY=dY)
+        got = layer.norm_grad(rk.NormProblem(rows, cols, dtype, epsilon=1e-3), X, **args)
+        h = host(dict(X=X, **args))
+        want = ref.norm_grad(h["X"], h["dY"], h["Mean"], h["InvStdDev"], h["Scale"])
+        for k in want:
+            check(got[k], want[k], k)
+
+
 def test_norm_without_weights(layer):
     i = Inputs(1, "f32")
     X, dY = i.normal(6, 50), i.normal(6, 50)
@@ -365,6 +381,28 @@ def test_scan(layer, seq, batch, channels, state, groups, layout, lens, dtype):
             past_zero(p, {**got, **back}, ("Y", "dX", "dDelta", "dZ", "dB", "dC"), lens)
         same_bits(got, layer.scan(p, **t))
         same_bits(back, layer.scan_grad(p, **t, **g, want=grads))
+
+
+# lengths on both sides of where sequences are cut into chunks, chunks of every remainder, lengths that end inside,
+# at the end and before a chunk
+@pytest.mark.parametrize("ragged", [False, True])
+@pytest.mark.parametrize("seq,batch,channels,state", [(23, 2, 40, 16), (24, 2, 40, 16), (39, 3, 33, 16),
+                                                      (40, 3, 33, 16), (41, 1, 130, 4), (43, 2, 24, 64),
+                                                      (50, 2, 17, 100), (203, 2, 70, 16), (209, 3, 20, 24)])
+def test_scan_around_chunks(layer, seq, batch, channels, state, ragged):
+    lens = [[seq - 1, 8, 0][n % 3] for n in range(batch)] if ragged else None
+    for dtype, layout in (("f32", 0), ("bf16", 1)):
+        p = rk.ScanProblem(seq, batch, channels, state, 1, dtype, layout)
+        t, g = scan_inputs(p, seq * state, True, lens)
+        if lens:
+            poison(p, t, ("X", "Delta", "B", "C", "Z"), lens)
+            poison(p, g, ("dY",), lens)
+        got = layer.scan(p, **t)
+        back = layer.scan_grad(p, **t, **g, want=("dX", "dDelta", "dA", "dB", "dC", "dD", "d_delta_bias",
+                                                  "d_initial_state", "dZ"))
+        want = scan_want(p, t, g)
+        for k, v in {**got, **back}.items():
+            check(v, want[k], k)
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
