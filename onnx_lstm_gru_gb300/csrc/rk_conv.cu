@@ -61,7 +61,7 @@ __device__ __forceinline__ void load_taps(const ConvParams& p, int c, float (&w)
 template <typename T, int V, int W>
 __global__ void __launch_bounds__(128) conv_kernel(ConvParams p) {
   const int pieces = p.C / V;
-  const int chunks = max((p.S + kFwdChunk - 1) / kFwdChunk, 1);
+  const int chunks = (p.S + kFwdChunk - 1) / kFwdChunk;
   const long long item = (long long)blockIdx.x * 128 + threadIdx.x;
   if (item >= (long long)pieces * chunks * p.N) return;
   const unsigned q = (unsigned)(item / pieces);  // fits: chunks and N are at most 2^31 together
@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(256) conv_grad_reduce_kernel(ConvParams p) {
 
 template <typename T, int V, int W>
 cudaError_t run_conv(const ConvParams& p, cudaStream_t s) {
-  const long long items = (long long)(p.C / V) * std::max((p.S + kFwdChunk - 1) / kFwdChunk, 1) * p.N;
+  const long long items = (long long)(p.C / V) * ((p.S + kFwdChunk - 1) / kFwdChunk) * p.N;
   conv_kernel<T, V, W><<<(unsigned)((items + 127) / 128), 128, 0, s>>>(p);
   return cudaGetLastError();
 }

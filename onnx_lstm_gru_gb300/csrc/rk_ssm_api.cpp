@@ -81,10 +81,11 @@ struct Call {
                bool required) {
     RowsArg a{};
     if (!ok()) return a;
+    const int piece = 16 / eb;
     if (t.ptr == nullptr || outer == 0 || inner == 0) {
       a.p = range<void>(name, t.ptr, t.offset, t.length, 0, eb, required && outer > 0 && inner > 0);
       if (t.ptr == nullptr && required && outer > 0 && inner > 0) bad(RK_ERR_SHAPE, "%s: %s: required tensor is null", name);
-      a.vec = 1;
+      a.vec = group % piece == 0;  // no rows stand in the way of pieces, but their elements still have to divide
       return a;
     }
     const int64_t pitch = t.pitch == 0 ? elems : t.pitch;
@@ -119,7 +120,6 @@ struct Call {
     a.ns = inner == 1 ? 0 : pitch;
     // 16-byte pieces: `group` consecutive elements, the ones that tiles are
     // cut from, hold whole pieces
-    const int piece = 16 / eb;
     a.vec = reinterpret_cast<uintptr_t>(a.p) % 16 == 0 && a.ss % piece == 0 && a.ns % piece == 0 && group % piece == 0;
     return a;
   }
@@ -387,6 +387,10 @@ rk_status rk_conv_encode(rk_handle* h, const rk_conv_problem* p, const rk_conv_o
   cp.init = c.tensor<void>("initial_state", o->initial_state, state, c.eb);
   cp.final_state = c.tensor<void>("final_state", o->final_state, state, c.eb);
   if (!c.ok() || p->batch == 0) return c.st;
+  if (p->seq == 0) {
+    c.copy(cp.final_state, cp.init, state * c.eb, static_cast<cudaStream_t>(stream));
+    return c.st;
+  }
   cp.vec = cp.X.vec && cp.Y.vec && aligned16(cp.W) && aligned16(cp.B) && aligned16(cp.init) && aligned16(cp.final_state);
   c.cuda("launch", rk::launch_conv(cp, static_cast<cudaStream_t>(stream)));
   if (c.ok()) h->launches += 1;
