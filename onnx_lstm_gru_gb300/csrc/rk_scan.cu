@@ -248,7 +248,7 @@ __device__ __forceinline__ void carry_chunks(const ScanParams& p, int n, unsigne
     for (int j = 0; j < kBatch; ++j) {
       if (q0 + j < p.chunks) {
         carry[(q0 + j) * ck] = run;
-        run = fmaf(exp2_fast(A2 * d[j]), run, s[j]);
+        run = fmaf(chunk_decay(A2, d[j]), run, s[j]);
       }
     }
   }

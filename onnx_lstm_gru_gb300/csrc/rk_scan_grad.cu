@@ -6,7 +6,8 @@
 //   x = g a h_before;  ddt += A x + u B g;  dA += dt x;  e = a g.
 // It needs the states in reverse order.  They are computed again rather than
 // kept: a launch forward (scan_grad_states_kernel) leaves the state, and the
-// sum of dt since the chunk's start, at every eighth step in global memory, and
+// sum of dt since the chunk's start, at every eighth step (counted from the
+// last one back, first_subtile) in global memory, and
 // the way back (scan_grad_kernel) runs one such subtile at a time, forward and
 // then back.  Of the bytes per element that the gradient reads and writes there
 // are 4 / 8 per state for that, twice.
@@ -108,6 +109,14 @@ struct Duo {
 // STATES: dt and dt u.  DY: dy too.  ALL: everything the way back needs.
 enum Stage { STATES, DY, ALL };
 
+// The subtiles of a chunk whose steps are t0 .. live - 1 end where they end;
+// the first one starts up to seven steps before t0.  Its steps before t0 have
+// dt = 0, and the way back comes to them when it has done with all others:
+// what a rate that is no number makes of them reaches no step.
+__device__ __forceinline__ int first_subtile(int t0, int live) { return live - (live - t0 + kT - 1) / kT * kT; }
+// Which one of its sequence the subtile that starts at t is (t0 is a multiple of kT).
+__device__ __forceinline__ int subtile_index(int t, int t0) { return t0 / kT + (t - t0 + kT - 1) / kT; }
+
 template <int BYTES>
 __device__ __forceinline__ void copy_async(void* to, const void* from) {
   const uint32_t dst = (uint32_t)__cvta_generic_to_shared(to);
@@ -123,12 +132,12 @@ struct Tile {
   static constexpr int kItems = kT * P > kThreads ? kT * P / kThreads : 1;
   const ScanParams& p;
   Sm& sm;
-  int n, g, c0, width, live;
+  int n, g, c0, width, begin;
 
   __device__ __forceinline__ int pair_of() const { return threadIdx.x % P; }
   __device__ __forceinline__ int row_of(int i) const { return threadIdx.x / P + i * (kThreads / P); }
   __device__ __forceinline__ bool has(int i, int t) const {
-    return row_of(i) < kT && t + row_of(i) < live && 2 * pair_of() < width;
+    return row_of(i) < kT && t + row_of(i) >= begin && 2 * pair_of() < width;
   }
 
   __device__ __forceinline__ void fetch_rows(const RowsArg& src, int slot, int t) {
@@ -136,7 +145,7 @@ struct Tile {
 #pragma unroll
     for (int i = threadIdx.x; i < Sm::kPieces; i += kThreads) {
       const int r = i / (CH / V), x = i % (CH / V) * V;
-      if (t + r < live && x < width) copy_async<16>(&sm.raw[slot][i], base + r * src.ss + x);
+      if (t + r >= begin && x < width) copy_async<16>(&sm.raw[slot][i], base + r * src.ss + x);
     }
   }
   __device__ __forceinline__ void fetch_quads(const RowsArg& src, int slot, int t) {
@@ -144,7 +153,7 @@ struct Tile {
 #pragma unroll
     for (int i = threadIdx.x; i < Sm::kQuads; i += kThreads) {
       const int r = i / (NSP / 4), k = i % (NSP / 4) * 4;
-      if (t + r < live && k < p.K) copy_async<sizeof(typename Sm::Quad)>(&sm.quads[slot][i], base + r * src.ss + k);
+      if (t + r >= begin && k < p.K) copy_async<sizeof(typename Sm::Quad)>(&sm.quads[slot][i], base + r * src.ss + k);
     }
   }
   template <Stage S>
@@ -168,7 +177,7 @@ struct Tile {
     for (int i = threadIdx.x; i < Sm::kQuads; i += kThreads) {
       const int r = i / (NSP / 4), k = i % (NSP / 4) * 4;
       float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      if (t + r < live && k < p.K) {
+      if (t + r >= begin && k < p.K) {
         if (p.bc_vec) {
           Piece<T, 4>::load(reinterpret_cast<const T*>(&sm.quads[slot][i]), v);
         } else {
@@ -262,7 +271,7 @@ struct Tile {
 #pragma unroll
     for (int i = threadIdx.x; i < Sm::kPieces; i += kThreads) {
       const int r = i / (CH / V), x = i % (CH / V) * V;
-      if (t + r < live && x < width) *reinterpret_cast<uint4*>(base + r * to.ss + x) = sm.out[slot][i];
+      if (t + r >= begin && x < width) *reinterpret_cast<uint4*>(base + r * to.ss + x) = sm.out[slot][i];
     }
   }
 
@@ -355,11 +364,12 @@ __global__ void __launch_bounds__(kThreads, 4) scan_grad_states_kernel(ScanParam
   const int chunk = q % p.chunks, n = q / p.chunks;
   const int t0 = chunk * p.chunk, t1 = min(t0 + p.chunk, p.S);
   const int live = min(t1, row_length(p.lens, n, p.S));
-  Tile<T, TPC> b{p, sm, n, g, g * per + tile * Sm::CH, min(Sm::CH, per - tile * Sm::CH), live};
+  Tile<T, TPC> b{p, sm, n, g, g * per + tile * Sm::CH, min(Sm::CH, per - tile * Sm::CH), t0};
   const int j = threadIdx.x / TPC, part = threadIdx.x % TPC;
   const int left = b.width - 2 * j, c = b.c0 + (left > 0 ? 2 * j : 0);
   const int subs = (p.S + kT - 1) / kT;
-  if (t0 < live) b.template fetch<S>(t0);
+  const int first = first_subtile(t0, live);
+  if (t0 < live) b.template fetch<S>(first);
   b.constants();
   States A2, h, pr, e;
   A2.template load<TPC>(p.A, c, left, p, part);
@@ -368,13 +378,13 @@ __global__ void __launch_bounds__(kThreads, 4) scan_grad_states_kernel(ScanParam
   float sum[2] = {0.0f, 0.0f};
 #pragma unroll
   for (int i = 0; i < 4; ++i) pr.v[i / 2][i % 2] = f2(1.0f, 1.0f);
-  for (int t = t0; t < live; t += kT) {
+  for (int t = first; t < live; t += kT) {
     copies_done();
     __syncthreads();
     b.template put<S>(t);
     __syncthreads();
     if (t + kT < live) b.template fetch<S>(t + kT);
-    const long long at = (long long)n * subs + t / kT;
+    const long long at = (long long)n * subs + subtile_index(t, t0);
     h.template store<TPC>(p.ckpt + at * p.C * p.K, c, left, p, part);
     if (part == 0) {
       if (left > 0) p.cum[at * p.C + c] = sum[0];
@@ -445,7 +455,7 @@ __global__ void __launch_bounds__(64) scan_grad_carry_kernel(ScanParams p) {
       for (int j = 0; j < kBatch; ++j) {
         if (q0 + j < p.chunks) {
           carry[(back ? p.chunks - 1 - q0 - j : q0 + j) * ck] = run;
-          run = fmaf(exp2_fast(A2 * d[j]), run, s[j]);
+          run = fmaf(chunk_decay(A2, d[j]), run, s[j]);
         }
       }
     }
@@ -466,11 +476,10 @@ __device__ __forceinline__ void grad_tile(const ScanParams& p, GradSmem<T, TPC>&
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int subs = (p.S + kT - 1) / kT;
   const long long chunk_row = ((long long)n * p.chunks + chunk) * p.C;
-  Tile<T, TPC> b{p, sm, n, g, g * per + tile * CH, min(CH, per - tile * CH), live};
+  Tile<T, TPC> b{p, sm, n, g, g * per + tile * CH, min(CH, per - tile * CH), t0};
   const int left = b.width - 2 * j, c = b.c0 + (left > 0 ? 2 * j : 0);
-  const int last = live > t0 ? t0 + (live - 1 - t0) / kT * kT : t0 - kT;
   __syncthreads();
-  if (last >= t0) b.template fetch<ALL>(last);
+  if (live > t0) b.template fetch<ALL>(live - kT);
   b.constants();
   States A2, e, dA;
   A2.template load<TPC>(p.A, c, left, p, part);
@@ -481,11 +490,11 @@ __device__ __forceinline__ void grad_tile(const ScanParams& p, GradSmem<T, TPC>&
   else if (p.dhT) e.template load<TPC>(p.dhT + (long long)n * p.C * p.K, c, left, p, part);
   const float* start = p.chunks > 1 ? p.carry + chunk_row * p.K : p.h0 ? p.h0 + (long long)n * p.C * p.K : nullptr;
   float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // dD and d_delta_bias of this thread's pair
-  for (int t = last; t >= t0; t -= kT) {
+  for (int t = live - kT; t > t0 - kT; t -= kT) {
     // the state at the subtile's start: the chunk's own, and what is left of its start's
     States h;
     {
-      const long long at = (long long)n * subs + t / kT;
+      const long long at = (long long)n * subs + subtile_index(t, t0);
       h.template load<TPC>(p.ckpt + at * p.C * p.K, c, left, p, part);
       if (start) {
         States h0;
@@ -505,7 +514,7 @@ __device__ __forceinline__ void grad_tile(const ScanParams& p, GradSmem<T, TPC>&
     __syncthreads();
     if (t > t0) b.template fetch<ALL>(t - kT);
     // Half of the subtile's steps at a time, the later ones first: as many
-    // states as leave the registers room to overlap steps.  Past the length
+    // states as leave the registers room to overlap steps.  Before the chunk
     // dt, dt u and dy are 0: the state and its gradient stand still
     States dAt;  // of this subtile: long sums of short ones keep more bits
     dAt.zero();
@@ -609,7 +618,7 @@ __device__ __forceinline__ void grad_tile(const ScanParams& p, GradSmem<T, TPC>&
 #pragma unroll
       for (int i = threadIdx.x; i < kT * 2 * NSP; i += kThreads) {
         const int r = i / (2 * NSP), w = i % (2 * NSP), k = w % NSP;
-        if (k >= p.K || t + r >= live) continue;
+        if (k >= p.K || t + r < t0) continue;
         float v = sm.part[r][0][w];
 #pragma unroll
         for (int m = 1; m < kWarps; ++m) v += sm.part[r][m][w];

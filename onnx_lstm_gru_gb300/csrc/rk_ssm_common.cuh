@@ -212,9 +212,19 @@ __device__ __forceinline__ F2 exp2_fast2(F2 x) {
 __device__ __forceinline__ F2 decay2(F2 dt, F2 A2) { return exp2_fast2(fma2(dt, A2, f2(3e-8f, 3e-8f))); }
 __device__ __forceinline__ float decay(float dt, float A2) { return exp2_fast(fmaf(dt, A2, 3e-8f)); }
 
-// A decay rate in base-2 exponents per unit of dt, finite, so that a step of
-// dt = 0 keeps the state whatever the rate.
-__device__ __forceinline__ float rate2(float a) { return fminf(fmaxf(a * kLog2e, -3.0e38f), 3.0e38f); }
+// A decay rate in base-2 exponents per unit of dt, not infinite, so that a
+// step of dt = 0 keeps the state.  A rate that is no number stays none, and
+// with it the state: these forms of min and max hand a NaN on.
+__device__ __forceinline__ float rate2(float a) {
+  float r = a * kLog2e;
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(r) : "f"(-3.0e38f));
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(r) : "f"(3.0e38f));
+  return r;
+}
+
+// What a chunk whose steps sum to d leaves of the state that enters it.  All
+// of it where no step is within the row's length, whatever the rate.
+__device__ __forceinline__ float chunk_decay(float A2, float d) { return d == 0.0f ? 1.0f : exp2_fast(A2 * d); }
 
 // Adds COUNT values over the lanes whose bits from FIRST down to LAST
 // differ.  Each exchange leaves a lane half of its values until one is left;

@@ -6,9 +6,22 @@ import pytest
 import torch
 
 import onnx_lstm_gru_gb300 as rk
-from test_state_space_gpu import DTYPES, conv_inputs, layer  # noqa: F401  (layer: the fixture)
+from test_state_space_gpu import (  # noqa: F401  (layer: the fixture)
+    DTYPES, F64, check, conv_inputs, layer, poison, scan_inputs, scan_want)
 
 pytestmark = pytest.mark.gpu
+
+SCAN_GRADS = ("dX", "dDelta", "dA", "dB", "dC", "dD", "d_delta_bias", "d_initial_state", "dZ")
+
+
+def check_all(got, want, name=""):
+    """``check`` where the definition is finite; NaN and infinities exactly where it has them."""
+    g, w = got.double().cpu(), want.to(F64)
+    assert g.shape == w.shape, name
+    assert torch.equal(g.isnan(), w.isnan()), f"{name}: {int(g.isnan().sum())} NaN, {int(w.isnan().sum())} by definition"
+    assert torch.equal(g[w.isinf()], w[w.isinf()]), f"{name}: infinities"
+    on = w.isfinite()
+    check(torch.where(on.to(got.device), got, torch.zeros_like(got)), torch.where(on, w, torch.zeros_like(w)), name)
 
 
 # ---- nothing to do -----------------------------------------------------------------------------------
@@ -30,3 +43,26 @@ def test_conv_no_steps_any_channels(layer, channels, width, dtype):
     assert not layer.conv(p, **t, final_state=final)["final_state"].any()
     state = final.fill_(3.0)
     assert bool((layer.conv(p, **t, initial_state=state, final_state=state)["final_state"] == 3).all())
+
+
+# ---- values that are not numbers --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("seq,batch,channels,state,groups,lens", [
+    (1, 3, 40, 16, 2, [1, 0, 1]), (1, 2, 40, 5, 1, None), (21, 3, 40, 16, 2, [21, 5, 0]), (13, 2, 24, 5, 1, None),
+    (16, 2, 24, 64, 1, [16, 9]), (203, 3, 40, 16, 2, [203, 13, 0]), (203, 2, 24, 7, 1, [100, 61]),
+    (67, 1, 24, 100, 1, None)])
+def test_scan_nan_rate(layer, seq, batch, channels, state, groups, lens, dtype):
+    """A rate that is no number makes none of its channel's state, and of
+    nothing else: not of a sequence without steps, and not of the gradient that
+    reaches the last step, which no decay has touched."""
+    p = rk.ScanProblem(seq, batch, channels, state, groups, dtype)
+    t, g = scan_inputs(p, seq + state, True, lens)
+    t["A"][3, 2] = float("nan")
+    if lens:
+        poison(p, t, ("X", "Delta", "B", "C", "Z"), lens)
+        poison(p, g, ("dY",), lens)
+    want = scan_want(p, t, g)
+    assert bool(want["Y"].isnan().any()) and not bool(want["Y"].isnan().all())
+    for k, v in {**layer.scan(p, **t), **layer.scan_grad(p, **t, **g, want=SCAN_GRADS)}.items():
+        check_all(v, want[k], k)
