@@ -167,6 +167,10 @@ class _Problem:
             plan = plans[op] = _plan(op, self)
         return plan
 
+    def __getstate__(self):
+        # the plans belong to this process: a copy finds its own
+        return {k: v for k, v in self.__dict__.items() if k != "_plans"}
+
 
 # element types of operands: the problem's ("t"), float32 ("f"), int32 ("i")
 @dataclass(frozen=True)

@@ -1,7 +1,10 @@
 """Host side of the state space operators: refusals, scratch lengths, packing
 and the 64-bit definitions the GPU tests compare with.  No GPU call is made:
 every refused call is refused before anything is launched."""
+import copy
 import ctypes
+import dataclasses
+import pickle
 
 import pytest
 import torch
@@ -186,6 +189,17 @@ def test_row_distance(handle):
     assert pitches(torch.zeros(7, 9)[:, :2]) == (9, 0, 6 * 9 + 2)
     for bad in (wide[..., ::2], torch.zeros(1, 1, 4).expand(5, 3, 4), torch.zeros(5, 1, 4).expand(5, 3, 4)):
         assert pitches(bad) is None
+
+
+@pytest.mark.parametrize("op", list(PROBLEMS))
+def test_used_problems_are_copied_and_pickled(handle, op):
+    """A problem that a call has packed its operands by is still plain data."""
+    p = PROBLEMS[op]
+    plan = p._plan(op)
+    for q in (copy.copy(p), copy.deepcopy(p), pickle.loads(pickle.dumps(p)), dataclasses.replace(p)):
+        assert q == p and hash(q) == hash(p) and type(q) is type(p)
+        assert q._plan(op) is plan  # and finds what equal problems share
+        assert bytes(q.to_c()) == bytes(p.to_c())
 
 
 def test_overlapping_rows_are_refused(handle):
