@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -23,7 +24,8 @@ PROBE_SRC = os.path.join(PKG, "probe", "fma_peak.cu")
 PROBE_LIB = os.path.join(BUILD, "libfmapeak.so")
 
 # packs torch tensors for the state space entry points: a Python module that
-# includes torch's headers, its own shared object
+# includes torch's headers, its own shared object.  Left out where there is no
+# torch, which the C library does not need.
 BINDING_SRC = os.path.join(PKG, "binding", "state_space_binding.cpp")
 BINDING_LIB = os.path.join(BUILD, "state_space_binding.so")
 
@@ -49,8 +51,10 @@ def _headers():
 
 
 def _build_binding():
-    """Compile the Python module against the installed torch."""
+    """Compile the Python module against the installed torch, if that is one for CUDA."""
     import torch
+    if torch.version.cuda is None:
+        return
     root = os.path.dirname(torch.__file__)
     cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
     tmp = BINDING_LIB + f".{os.getpid()}.tmp"
@@ -67,7 +71,8 @@ def _build_binding():
 
 
 def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -> str:
-    """Compile every translation unit under csrc/ and link _build/librk.so."""
+    """Compile every translation unit under csrc/ and link _build/librk.so;
+    beside it, where torch is installed, the module that packs its tensors."""
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
     hdr_time = max([os.path.getmtime(h) for h in _headers()] + [0.0])
@@ -92,8 +97,9 @@ def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -
         os.replace(tmp, obj)
         return r.stderr
 
-    binding = force or not os.path.exists(BINDING_LIB) or \
-        os.path.getmtime(BINDING_LIB) < os.path.getmtime(BINDING_SRC)
+    binding = importlib.util.find_spec("torch") is not None and (
+        force or not os.path.exists(BINDING_LIB) or os.path.getmtime(BINDING_LIB) < os.path.getmtime(BINDING_SRC))
+    extra = None
     if todo or binding:
         n = jobs or min(len(todo) + 1, max(1, os.cpu_count() or 1))
         with cf.ThreadPoolExecutor(max_workers=n) as ex:
@@ -101,8 +107,6 @@ def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -
             for log in ex.map(compile_one, todo):
                 if verbose and log:
                     print(log)
-            if extra is not None:
-                extra.result()
     lib_time = os.path.getmtime(LIB) if os.path.exists(LIB) else -1.0
     if todo or lib_time < max(os.path.getmtime(o) for o in objs):
         tmp = LIB + f".{os.getpid()}.tmp"
@@ -118,6 +122,8 @@ def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -
         if r.returncode != 0:
             raise RuntimeError(f"build of libfmapeak.so failed:\n{r.stderr}")
         os.replace(tmp, PROBE_LIB)
+    if extra is not None:
+        extra.result()  # raises what went wrong there, with the library in place
     return LIB
 
 

@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import os
 from dataclasses import dataclass
 
 from . import DTYPES, RkError, load, rk_create, rk_destroy, rk_last_error, rk_launch_count, rk_tensor
@@ -145,6 +146,8 @@ def _binding():
     import importlib.machinery
     import importlib.util
     import torch  # noqa: F401  (the module links against its libraries)
+    if not os.path.exists(BINDING_LIB):
+        raise RuntimeError(f"{BINDING_LIB} missing: run onnx_lstm_gru_gb300.build() where torch is installed")
     loader = importlib.machinery.ExtensionFileLoader("state_space_binding", BINDING_LIB)
     spec = importlib.util.spec_from_file_location("state_space_binding", BINDING_LIB, loader=loader)
     module = importlib.util.module_from_spec(spec)
