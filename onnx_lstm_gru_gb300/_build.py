@@ -50,6 +50,28 @@ def _headers():
         glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
+def _binding_for():
+    """What the Python module is built against: the interpreter's binary
+    interface and the installed torch; None without torch (not imported here)."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or spec.origin is None:
+        return None
+    try:
+        with open(os.path.join(os.path.dirname(spec.origin), "version.py")) as f:
+            version = f.read()
+    except OSError:
+        version = ""
+    return f"{sysconfig.get_config_var('SOABI')}\n{spec.origin}\n{version}"
+
+
+def _built_for():
+    try:
+        with open(BINDING_LIB + ".for") as f:
+            return f.read()
+    except OSError:
+        return None
+
+
 def _build_binding():
     """Compile the Python module against the installed torch, if that is one for CUDA."""
     import torch
@@ -97,8 +119,10 @@ def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -
         os.replace(tmp, obj)
         return r.stderr
 
-    binding = importlib.util.find_spec("torch") is not None and (
-        force or not os.path.exists(BINDING_LIB) or os.path.getmtime(BINDING_LIB) < os.path.getmtime(BINDING_SRC))
+    binding_for = _binding_for()
+    binding = binding_for is not None and (
+        force or not os.path.exists(BINDING_LIB) or _built_for() != binding_for or
+        os.path.getmtime(BINDING_LIB) < os.path.getmtime(BINDING_SRC))
     extra = None
     if todo or binding:
         n = jobs or min(len(todo) + 1, max(1, os.cpu_count() or 1))
@@ -124,6 +148,9 @@ def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -
         os.replace(tmp, PROBE_LIB)
     if extra is not None:
         extra.result()  # raises what went wrong there, with the library in place
+        if os.path.exists(BINDING_LIB):
+            with open(BINDING_LIB + ".for", "w") as f:
+                f.write(binding_for)
     return LIB
 
 

@@ -35,3 +35,28 @@ def test_library_is_built_before_a_binding_that_fails(small, monkeypatch):
     with pytest.raises(RuntimeError, match="not today"):
         _build.build()
     assert ctypes.CDLL(_build.LIB).one() == 1
+
+
+def test_binding_follows_the_installed_torch(small, monkeypatch):
+    """Another torch has other headers and another binary interface."""
+    torch = small / "site" / "torch"
+    torch.mkdir(parents=True)
+    (torch / "__init__.py").write_text("")
+    (torch / "version.py").write_text("__version__ = '1'\n")
+    monkeypatch.delitem(sys.modules, "torch", raising=False)
+    monkeypatch.syspath_prepend(str(small / "site"))
+    (small / "binding.cpp").write_text("")
+    monkeypatch.setattr(_build, "BINDING_SRC", str(small / "binding.cpp"))
+    built = []
+
+    def binding():
+        built.append(1)
+        open(_build.BINDING_LIB, "w").close()
+    monkeypatch.setattr(_build, "_build_binding", binding)
+    for _ in range(2):
+        _build.build()
+        assert len(built) == 1
+    (torch / "version.py").write_text("__version__ = '2'\n")
+    for _ in range(2):
+        _build.build()
+        assert len(built) == 2
