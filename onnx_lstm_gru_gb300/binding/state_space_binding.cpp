@@ -30,7 +30,7 @@ namespace {
 struct Entry {
   PyObject* name;
   int at;
-  bool rows, required;
+  bool rows, required, output;
   at::ScalarType type;
   std::vector<int64_t> shape;
 };
@@ -164,6 +164,10 @@ PyObject* plan_run(PyObject* self, PyObject* const* args, Py_ssize_t n) {
       if (PyDict_SetItem(out, name, given) != 0) return nullptr;
       continue;
     }
+    if (!e->output) {
+      PyErr_Format(PyExc_ValueError, "%U: wanted, but an input of this operator that was not passed", e->name);
+      return nullptr;
+    }
     const at::Tensor t(at::detail::empty_cuda(e->shape, e->type, device, std::nullopt));
     words[e->at] = reinterpret_cast<int64_t>(t.data_ptr());
     words[e->at + 2] = t.numel();
@@ -190,7 +194,7 @@ PyObject* plan_run(PyObject* self, PyObject* const* args, Py_ssize_t n) {
 }
 
 // Plan(encode address, problem bytes, scratch floats or -1,
-//      [(name, word, rows, required, type code, shape)]); type codes: 0
+//      [(name, word, rows, required, output, type code, shape)]); type codes: 0
 //      float32, 1 Half, 2 bfloat16, 3 int32.
 PyObject* plan_new(PyTypeObject* type, PyObject* args, PyObject*) {
   HANDLE_TH_ERRORS
@@ -203,16 +207,16 @@ PyObject* plan_new(PyTypeObject* type, PyObject* args, PyObject*) {
   std::vector<Entry> entries;
   for (Py_ssize_t i = 0; i < PyList_GET_SIZE(list); ++i) {
     PyObject *name, *shape;
-    int at, rows, required, code;
-    if (!PyArg_ParseTuple(PyList_GET_ITEM(list, i), "UippiO!", &name, &at, &rows, &required, &code, &PyTuple_Type,
-                          &shape))
+    int at, rows, required, output, code;
+    if (!PyArg_ParseTuple(PyList_GET_ITEM(list, i), "UipppiO!", &name, &at, &rows, &required, &output, &code,
+                          &PyTuple_Type, &shape))
       return nullptr;
     constexpr at::ScalarType kTypes[] = {at::kFloat, at::kHalf, at::kBFloat16, at::kInt};
     if (i >= kMaxOperands || at < 0 || at + (rows ? 5 : 3) > kWords || code < 0 || code > 3) {
       PyErr_SetString(PyExc_ValueError, "Plan: entry out of range");
       return nullptr;
     }
-    Entry e{name, at, rows != 0, required != 0, kTypes[code], {}};
+    Entry e{name, at, rows != 0, required != 0, output != 0, kTypes[code], {}};
     for (Py_ssize_t d = 0; d < PyTuple_GET_SIZE(shape); ++d) {
       e.shape.push_back(PyLong_AsLongLong(PyTuple_GET_ITEM(shape, d)));
       if (PyErr_Occurred()) return nullptr;

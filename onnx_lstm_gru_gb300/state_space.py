@@ -256,6 +256,11 @@ _REQUIRED = {
     "norm": ("X",), "norm_grad": ("X", "Mean", "InvStdDev", "dY"), "conv": ("X", "W"), "conv_grad": ("X", "W", "dY"),
     "scan": ("X", "Delta", "A", "B", "C"), "scan_grad": ("X", "Delta", "A", "B", "C", "dY"),
 }
+_OUTPUTS = {
+    "norm": ("Y", "Mean", "InvStdDev"), "norm_grad": ("dX", "dScale", "dB"), "conv": ("Y", "final_state"),
+    "conv_grad": ("dX", "dW", "dB", "d_initial_state"), "scan": ("Y", "final_state"),
+    "scan_grad": ("dX", "dDelta", "dB", "dC", "dZ", "dA", "dD", "d_delta_bias", "d_initial_state"),
+}
 
 
 @functools.lru_cache(maxsize=256)
@@ -268,7 +273,7 @@ def _plan(op, problem):
     for names, is_rows, words in ((rows, True, 5), (tensors, False, 3)):
         for name in names:
             shape, kind = operands[name]
-            entries.append((name, at, is_rows, name in _REQUIRED[op], codes[kind], shape))
+            entries.append((name, at, is_rows, name in _REQUIRED[op], name in _OUTPUTS[op], codes[kind], shape))
             at += words
     lib = load()
     c = problem.to_c()
@@ -282,7 +287,8 @@ def _plan(op, problem):
 class StateSpaceLayer:
     """Owns an rk handle.  Every method enqueues one operator on the current
     torch stream (or ``stream``) and returns the outputs named in ``want``,
-    allocated unless they are passed by name.  Scratch comes from torch's
+    allocated unless they are passed by name (an input cannot be wanted that
+    was not passed).  Scratch comes from torch's
     allocator, so calls may run on any stream and be captured into a graph.
     No CPU path exists."""
 

@@ -66,3 +66,27 @@ def test_scan_nan_rate(layer, seq, batch, channels, state, groups, lens, dtype):
     assert bool(want["Y"].isnan().any()) and not bool(want["Y"].isnan().all())
     for k, v in {**layer.scan(p, **t), **layer.scan_grad(p, **t, **g, want=SCAN_GRADS)}.items():
         check_all(v, want[k], k)
+
+
+# ---- calls ----------------------------------------------------------------------------------------------
+
+def test_inputs_are_not_made_up(layer):
+    """A wanted name is an output or a tensor that was passed; memory made for
+    anything else would be read as an operand."""
+    p = rk.ScanProblem(4, 2, 16, 16)
+    t, g = scan_inputs(p, 1, state=False, extras=False)
+    before = layer.launches()
+    for name in ("Z", "D", "delta_bias", "sequence_lens", "initial_state"):
+        with pytest.raises(ValueError, match=name):
+            layer.scan(p, **t, want=("Y", name))
+    for name in ("Z", "d_final_state"):
+        with pytest.raises(ValueError, match=name):
+            layer.scan_grad(p, **t, **g, want=("dX", name))
+    with pytest.raises(ValueError, match="initial_state"):
+        layer.conv(rk.ConvProblem(4, 2, 16), t["X"], W=torch.zeros(16, 4, device="cuda"), want=("initial_state",))
+    with pytest.raises(ValueError, match="Scale"):
+        layer.norm(rk.NormProblem(4, 16), torch.zeros(4, 16, device="cuda"), want=("Y", "Scale"))
+    assert layer.launches() == before
+    got = layer.scan(p, **t, want=("Y", "X", "A"))
+    assert got["X"] is t["X"] and got["A"] is t["A"]
+    assert layer.scan_grad(p, **t, **g, want=SCAN_GRADS[:-1]).keys() == set(SCAN_GRADS[:-1])

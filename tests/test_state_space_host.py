@@ -4,6 +4,7 @@ every refused call is refused before anything is launched."""
 import copy
 import ctypes
 import dataclasses
+import inspect
 import pickle
 
 import pytest
@@ -189,6 +190,16 @@ def test_row_distance(handle):
     assert pitches(torch.zeros(7, 9)[:, :2]) == (9, 0, 6 * 9 + 2)
     for bad in (wide[..., ::2], torch.zeros(1, 1, 4).expand(5, 3, 4), torch.zeros(5, 1, 4).expand(5, 3, 4)):
         assert pitches(bad) is None
+
+
+def test_every_operand_is_an_input_or_an_output():
+    """The outputs are what the header's operand lists write; each operator's
+    default choice is among them."""
+    for op, outputs in ss._OUTPUTS.items():
+        names = sum(ss._OPERANDS[op], ())
+        assert set(outputs) <= set(names) and not set(outputs) & set(ss._REQUIRED[op])
+        want = inspect.signature(getattr(rk.StateSpaceLayer, op)).parameters["want"].default
+        assert set(want) <= set(outputs)
 
 
 @pytest.mark.parametrize("op", list(PROBLEMS))
