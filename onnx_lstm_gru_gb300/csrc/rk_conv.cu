@@ -156,9 +156,15 @@ __global__ void __launch_bounds__(32 * kGradRows) conv_grad_kernel(ConvParams p)
   if (c < p.C && n < p.N) {
     const int len = row_length(p.lens, n, p.S);
     const int s0 = k * p.chunk, s1 = min(s0 + p.chunk, p.S);
-    const int end = s1 + W - 1;
+    const int end = min(s1 + W - 1, len), own = min(s1, len);  // steps from here on are none, or another chunk's
     float w[W][V], b[V];
     load_taps<T, V, W>(p, c, w, b);
+    float probe = 0.0f;  // NaN where a weight is infinite or none
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) probe = fmaf(w[j][i], 0.0f, probe);
+    const bool special = probe != 0.0f;
     // the inputs and the pre-activations' gradients of a group's steps and the
     // W - 1 before it
     float x[W - 1 + kGroup][V], dp[W - 1 + kGroup][V];
@@ -178,7 +184,7 @@ __global__ void __launch_bounds__(32 * kGradRows) conv_grad_kernel(ConvParams p)
     auto fetch = [&](int s) {
 #pragma unroll
       for (int q = 0; q < kGroup; ++q, in += p.X.ss, gr += p.dY.ss)
-        if (s + q < min(end, len)) nx[q].load(in), ny[q].load(gr);
+        if (s + q < end) nx[q].load(in), ny[q].load(gr);
     };
     // one group; inside: all of its steps are the chunk's own and within the
     // length, and the inputs it completes are the chunk's
@@ -190,14 +196,17 @@ __global__ void __launch_bounds__(32 * kGradRows) conv_grad_kernel(ConvParams p)
         for (int i = 0; i < V; ++i) x[j][i] = x[kGroup + j][i], dp[j][i] = dp[kGroup + j][i];
 #pragma unroll
       for (int q = 0; q < kGroup; ++q) {
-        if (kInside || first + q < min(end, len)) nx[q].widen(x[W - 1 + q]), ny[q].widen(dp[W - 1 + q]);
+        if (kInside || first + q < end) nx[q].widen(x[W - 1 + q]), ny[q].widen(dp[W - 1 + q]);
         else fill(x[W - 1 + q], 0.0f), fill(dp[W - 1 + q], 0.0f);
       }
       fetch(first + kGroup);
 #pragma unroll
       for (int q = 0; q < kGroup; ++q) {
         float(&d)[V] = dp[W - 1 + q];
-        if (p.silu) {
+        // past the length d stays 0, whatever the last inputs and the weights
+        // would make of a step there
+        const bool on = kInside || first + q < end;
+        if (p.silu && on) {
 #pragma unroll
           for (int i = 0; i < V; ++i) {
             float pre = b[i];
@@ -209,7 +218,7 @@ __global__ void __launch_bounds__(32 * kGradRows) conv_grad_kernel(ConvParams p)
         }
         // the steps after the chunk are another's: their gradients count for
         // this one's inputs alone
-        if (kInside || first + q < s1) {
+        if (kInside || first + q < own) {
 #pragma unroll
           for (int i = 0; i < V; ++i) {
 #pragma unroll
@@ -224,6 +233,15 @@ __global__ void __launch_bounds__(32 * kGradRows) conv_grad_kernel(ConvParams p)
           o[i] = w[0][i] * dp[W - 1 + q][i];
 #pragma unroll
           for (int j = 1; j < W; ++j) o[i] = fmaf(w[j][i], dp[W - 1 + q - j][i], o[i]);
+        }
+        if (!kInside && special) {  // their products with steps that there are not are not 0: left out
+          fill(o, 0.0f);
+#pragma unroll
+          for (int j = 0; j < W; ++j) {
+            if (first + q - j < s0 || first + q - j >= end) continue;
+#pragma unroll
+            for (int i = 0; i < V; ++i) o[i] = fmaf(w[j][i], dp[W - 1 + q - j][i], o[i]);
+          }
         }
         if (kInside) {
           if (dx) Piece<T, V>::store(dx, o);
@@ -243,8 +261,8 @@ __global__ void __launch_bounds__(32 * kGradRows) conv_grad_kernel(ConvParams p)
       }
     };
     fetch(s0);
-    for (int first = s0; first < end; first += kGroup) {
-      if (first - (W - 1) >= s0 && first + kGroup <= min(s1, len)) group(first, std::true_type{});
+    for (int first = s0; first < s1 + W - 1; first += kGroup) {
+      if (first - (W - 1) >= s0 && first + kGroup <= own) group(first, std::true_type{});
       else group(first, std::false_type{});
     }
   }

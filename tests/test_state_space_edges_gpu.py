@@ -7,7 +7,7 @@ import torch
 
 import onnx_lstm_gru_gb300 as rk
 from test_state_space_gpu import (  # noqa: F401  (layer: the fixture)
-    DTYPES, F64, check, conv_inputs, layer, poison, scan_inputs, scan_want)
+    DTYPES, F64, check, conv_inputs, conv_want, layer, past_zero, poison, scan_inputs, scan_want)
 
 pytestmark = pytest.mark.gpu
 
@@ -66,6 +66,30 @@ def test_scan_nan_rate(layer, seq, batch, channels, state, groups, lens, dtype):
     assert bool(want["Y"].isnan().any()) and not bool(want["Y"].isnan().all())
     for k, v in {**layer.scan(p, **t), **layer.scan_grad(p, **t, **g, want=SCAN_GRADS)}.items():
         check_all(v, want[k], k)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("act", ["none", "silu"])
+@pytest.mark.parametrize("seq,batch,channels,lens", [(21, 3, 24, [21, 5, 0]), (7, 2, 10, [0, 2]), (40, 1, 16, None),
+                                                     (90, 2, 16, [90, 64])])
+def test_conv_special_weights(layer, seq, batch, channels, lens, act, dtype):
+    """Weights that are infinite or no numbers meet the steps that there are,
+    not the zeros past a row's length or on both sides of a chunk."""
+    for width in (1, 3, 4, 8):
+        p = rk.ConvProblem(seq, batch, channels, width, dtype, 1, act)
+        t, g = conv_inputs(p, seq, True, lens)
+        t["W"][5, 0], t["W"][7, width // 2] = float("inf"), float("nan")
+        t["W"][9, width - 1] = -float("inf")
+        t["B"][2] = float("nan")
+        if lens:
+            poison(p, t, ("X",), lens)
+            poison(p, g, ("dY",), lens)
+        want = conv_want(p, t, g)
+        got = {**layer.conv(p, **t), **layer.conv_grad(p, **t, **g, want=("dX", "dW", "dB", "d_initial_state"))}
+        for k, v in got.items():
+            check_all(v, want[k], f"{k} width={width}")
+        if lens:
+            past_zero(p, got, ("Y", "dX"), lens)
 
 
 # ---- calls ----------------------------------------------------------------------------------------------
