@@ -505,7 +505,7 @@ template <typename T>
 cudaError_t norm_grad_typed(NormParams& p, cudaStream_t s) {
   const int c = p.cols;
   if (c > kGradCols) {
-    if (p.dX.p && p.rows > 0)
+    if (p.dX.p)
       norm_grad_wide_kernel<T><<<(unsigned)std::min<long long>(p.rows, 1 << 20), kWide, 0, s>>>(p);
     if (p.partial)
       norm_grad_wide_weights_kernel<T><<<dim3((c + 255) / 256, p.blocks), 256, 0, s>>>(p);
@@ -549,9 +549,10 @@ cudaError_t launch_norm_grad(const NormParams& all, cudaStream_t s, int* launche
     case RK_F16: e = norm_grad_typed<__half>(p, s); break;
     default: e = norm_grad_typed<__nv_bfloat16>(p, s);
   }
-  *launches = 1;
+  // wide rows: a launch for dX, one for the weights' partial sums
+  *launches = p.cols > kGradCols ? (p.dX.p != nullptr) + (p.partial != nullptr) : 1;
   if (e != cudaSuccess || p.partial == nullptr) return e;
-  *launches = 2;
+  *launches += 1;
   return launch_chained(norm_grad_reduce_kernel, (unsigned)((2LL * p.cols + kReduceCols - 1) / kReduceCols),
                         kReduceCols * kParts, 0, s, p);
 }

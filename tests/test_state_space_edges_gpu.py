@@ -114,3 +114,16 @@ def test_inputs_are_not_made_up(layer):
     got = layer.scan(p, **t, want=("Y", "X", "A"))
     assert got["X"] is t["X"] and got["A"] is t["A"]
     assert layer.scan_grad(p, **t, **g, want=SCAN_GRADS[:-1]).keys() == set(SCAN_GRADS[:-1])
+
+
+@pytest.mark.parametrize("cols,counts", [(64, (2, 1, 2)), (8192, (2, 1, 2)), (8200, (3, 1, 2))])
+def test_launches_are_counted(layer, cols, counts):
+    """All gradients, the rows' alone, the weights' alone: dX of rows too wide
+    for registers is a launch of its own."""
+    p = rk.NormProblem(40, cols)
+    X, dY = torch.randn(40, cols, device="cuda"), torch.randn(40, cols, device="cuda")
+    f = layer.norm(p, X)
+    for want, n in zip((("dX", "dScale", "dB"), ("dX",), ("dB",)), counts):
+        before = layer.launches()
+        layer.norm_grad(p, X, dY=dY, Mean=f["Mean"], InvStdDev=f["InvStdDev"], want=want)
+        assert layer.launches() - before == n, want
