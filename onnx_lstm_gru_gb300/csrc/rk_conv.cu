@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(128) conv_kernel(ConvParams p) {
           o[i] = b[i];
 #pragma unroll
           for (int j = 0; j < W; ++j) o[i] = fmaf(w[j][i], x[j][i], o[i]);
-          if (p.silu) o[i] *= sigmoid_fast(o[i]);
+          if (p.silu) o[i] *= sigmoid_of<T>(o[i]);
         }
         Piece<T, V>::store(y, o);
       }
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(32 * kGradRows) conv_grad_kernel(ConvParams p)
             float pre = b[i];
 #pragma unroll
             for (int j = 0; j < W; ++j) pre = fmaf(w[j][i], x[q + j][i], pre);
-            const float sg = sigmoid_fast(pre);
+            const float sg = sigmoid_of<T>(pre);
             d[i] *= sg * fmaf(pre, 1.0f - sg, 1.0f);
           }
         }

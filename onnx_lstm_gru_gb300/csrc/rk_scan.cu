@@ -173,6 +173,11 @@ __global__ void __launch_bounds__(kThreads, kBlocks) scan_kernel(ScanParams p) {
         float dt = Elem<T>::to_f(d[i]) + bias, uu = Elem<T>::to_f(u[i]);
         if (p.softplus) dt = softplus_f(dt);
         if (!on) dt = 0.0f, uu = 0.0f;
+        float gate = 1.0f;
+        if (OUT && z) {
+          const float zf = Elem<T>::to_f(zz[i]);
+          gate = zf * sigmoid_of<T>(zf);
+        }
         const float du = dt * uu;
         const F2 dt2 = f2(dt, dt), du2 = f2(du, du);
         F2 y0 = f2(0.0f, 0.0f), y1 = y0;
@@ -192,11 +197,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) scan_kernel(ScanParams p) {
           float o = s2.x + s2.y;
 #pragma unroll
           for (int m = TPC / 2; m > 0; m >>= 1) o += __shfl_xor_sync(0xffffffffu, o, m);
-          o = fmaf(skip, uu, o);
-          if (z) {
-            const float zf = Elem<T>::to_f(zz[i]);
-            o *= zf * sigmoid_fast(zf);
-          }
+          o = fmaf(skip, uu, o) * gate;
           if (on && stores) *y = Elem<T>::from_f(o);
           y += p.Y.ss;
         } else {
@@ -345,7 +346,7 @@ __global__ void __launch_bounds__(kTokenThreads) scan_token_kernel(ScanParams p)
       const float uu = Elem<T>::to_f(u[j]), zz = Elem<T>::to_f(z[j]);
       dt[j] = Elem<T>::to_f(d[j]) + bias;
       if (p.softplus) dt[j] = softplus_f(dt[j]);
-      gate[j] = p.Z.p ? zz * sigmoid_fast(zz) : 1.0f;
+      gate[j] = p.Z.p ? zz * sigmoid_of<T>(zz) : 1.0f;
       du[j] = dt[j] * uu;
       sk[j] = skip * uu;
     }

@@ -53,7 +53,6 @@ constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kT = 8;  // steps of a subtile
 constexpr int kHalf = 4;   // of them whose states are in registers at once
-constexpr float kLn2 = 0.6931471805599453f;
 
 constexpr int tpc_of(int states) {
   return states <= 8 ? 2 : states <= 16 ? 4 : states <= 32 ? 8 : states <= 64 ? 16 : 32;
@@ -235,7 +234,7 @@ struct Tile {
           if constexpr (S != STATES) {
             gy = gy2[e];
             if (p.Z.p) {
-              const float zz = z2[e], sg = sigmoid_fast(zz);
+              const float zz = z2[e], sg = sigmoid_of<T>(zz);
               if constexpr (S == ALL) gate = gy * sg * (1.0f + zz * (1.0f - sg));
               gy *= zz * sg;
             }

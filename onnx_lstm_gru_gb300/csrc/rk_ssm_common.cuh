@@ -129,7 +129,21 @@ __device__ __forceinline__ float rcp_fast(float x) {
   return y;
 }
 
-__device__ __forceinline__ float sigmoid_fast(float x) { return rcp_fast(1.0f + exp2_fast(-kLog2e * x)); }
+constexpr float kLn2 = 0.6931471805599453f;
+
+// sigmoid(x) for tensors of T.  2^t of the rounded product t = -x log2(e) alone
+// is off by a relative error that grows with -x (7e-7 at -20, 4e-6 at -80), far
+// below what a 16-bit element keeps.  float32 ones get the rest too: e^-x is
+// 2^t e^r with r = -x - t ln(2), which the fused multiply-add leaves exact but
+// for ln(2)'s own rounding, t 2e-9, and e^r = 1 + r, |r| being under 1e-5.
+template <typename T>
+__device__ __forceinline__ float sigmoid_of(float x) {
+  const float t = -kLog2e * x;
+  float e = exp2_fast(t);
+  // at least a half: beyond the exponential's range r is anything, and e is 0 or infinite
+  if constexpr (sizeof(T) == 4) e *= fmaxf(1.0f + fmaf(-t, kLn2, -x), 0.5f);
+  return rcp_fast(1.0f + e);
+}
 
 // log(1 + e^x) = max(x, 0) + log(1 + e) with e = e^-|x| <= 1, and
 // log(1 + e) = 2 artanh(s), s = e / (2 + e) <= 1/3; artanh(s) / s is a
@@ -138,11 +152,13 @@ __device__ __forceinline__ float sigmoid_fast(float x) { return rcp_fast(1.0f + 
 // is lost to 1 + e.
 __device__ __forceinline__ float softplus_from(float x, float& e) {
   const float n = -(fabsf(x) < 100.0f ? fabsf(x) : 100.0f), t = n * kLog2e;
-  // what the product rounded away (its own factor's rounding too), put back
-  // behind the exponential
-  const float lo = fmaf(n, kLog2e, -t) + n * 1.9259629911e-8f;
+  // what the product rounded away, its own factor's rounding too, put back
+  // behind the exponential: a fused multiply-add gives the first exactly
+  // (Dekker's two-product), the second is what kLog2e is short of log2(e)
+  constexpr float kLow = (float)(1.4426950408889634 - (double)kLog2e);
+  const float lo = fmaf(n, kLog2e, -t) + n * kLow;
   const float e0 = exp2_fast(t);
-  e = fmaf(e0, lo * 0.6931471806f, e0);
+  e = fmaf(e0, lo * kLn2, e0);
   const float s = e * rcp_fast(2.0f + e), q = s * s;
   float r = fmaf(q, 0.14078889f, 0.13982579f);
   r = fmaf(r, q, 0.20012298f);

@@ -92,6 +92,53 @@ def test_conv_special_weights(layer, seq, batch, channels, lens, act, dtype):
             past_zero(p, got, ("Y", "dX"), lens)
 
 
+# ---- accuracy of float32 outputs ------------------------------------------------------------------------
+
+def relative(got, want, bound):
+    off = ((got.double().cpu() - want) / want).abs()
+    assert float(off.max()) <= bound, f"off by {float(off.max()):.3g} at {int(off.argmax())}"
+
+
+def test_silu_and_gates_far_below_zero(layer):
+    """x sigmoid(x) and its slope keep their relative accuracy where they are
+    tiny.  The exponential is off by 2^-22 and three roundings of 2^-24, 1 + e by
+    2^-24, the reciprocal by 2^-23, the product by 2^-24: under 3 * 2^-22.  The
+    slope, sigmoid(x) (1 + x (1 - sigmoid(x))), is taken below -3, where its
+    second factor is at least 1.8: three roundings more and at most twice the
+    sigmoid's error, 2^-20."""
+    x = torch.linspace(-85.0, -3.0, 4096, device="cuda")
+    z = x.double().cpu()
+    s = torch.sigmoid(z)
+    silu, slope = z * s, s * (1 + z * (1 - s))
+    p = rk.ConvProblem(1, 1, 4096, 1)
+    one, rows = torch.ones(4096, 1, device="cuda"), x.view(1, 1, -1)
+    relative(layer.conv(p, X=rows, W=one)["Y"].view(-1), silu, 3 * 2.0 ** -22)
+    relative(layer.conv_grad(p, X=rows, W=one, dY=torch.ones_like(rows))["dX"].view(-1), slope, 2.0 ** -20)
+    for steps in (1, 5):  # D u alone behind the gate
+        q = rk.ScanProblem(steps, 1, 4096, 4)
+        Z, B = x.expand(steps, 1, 4096).contiguous(), torch.zeros(steps, 1, 4, device="cuda")
+        o, D = torch.ones_like(Z), torch.ones(4096, device="cuda")
+        args = dict(X=o, Delta=o, A=-torch.ones(4096, 4, device="cuda"), B=B, C=B, D=D, Z=Z)
+        got = {**layer.scan(q, **args), **layer.scan_grad(q, **args, dY=o, want=("dZ", "dX"))}
+        for i in range(steps):
+            relative(got["Y"][i, 0], silu, 3 * 2.0 ** -22)
+            relative(got["dZ"][i, 0], slope, 2.0 ** -20)
+            relative(got["dX"][i, 0], silu, 2.0 ** -20)
+
+
+def test_silu_and_gates_at_the_ends(layer):
+    """What is beyond float32: 0 far below, x far above; an infinity above and
+    a NaN stay what they are."""
+    x = torch.tensor([-1e30, -200.0, -89.0, 0.0, 89.0, 200.0, 1e30, float("inf"), float("nan")], device="cuda")
+    want = torch.tensor([0.0, 0.0, 0.0, 0.0, 89.0, 200.0, 1e30, float("inf"), float("nan")], device="cuda")
+    rows, o, B = x.view(1, 1, -1), torch.ones(1, 1, 9, device="cuda"), torch.zeros(1, 1, 4, device="cuda")
+    for y in (layer.conv(rk.ConvProblem(1, 1, 9, 1), X=rows, W=torch.ones(9, 1, device="cuda"))["Y"],
+              layer.scan(rk.ScanProblem(1, 1, 9, 4), X=o, Delta=o, A=-torch.ones(9, 4, device="cuda"), B=B, C=B,
+                         D=torch.ones(9, device="cuda"), Z=rows)["Y"]):
+        assert torch.equal(y.view(-1).isnan(), want.isnan())
+        assert torch.equal(y.view(-1)[:-1], want[:-1]), y
+
+
 # ---- calls ----------------------------------------------------------------------------------------------
 
 def test_inputs_are_not_made_up(layer):
