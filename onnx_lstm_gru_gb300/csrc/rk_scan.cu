@@ -173,11 +173,15 @@ __global__ void __launch_bounds__(kThreads, kBlocks) scan_kernel(ScanParams p) {
         float dt = Elem<T>::to_f(d[i]) + bias, uu = Elem<T>::to_f(u[i]);
         if (p.softplus) dt = softplus_f(dt);
         if (!on) dt = 0.0f, uu = 0.0f;
+        // float32's longer gate is computed before the states, where it does not
+        // wait (4096 x 1 x 2048 x 16: 94.2 us, behind them 96.3), 16-bit tensors'
+        // behind them (bf16 93.3 us, before them 94.3)
         float gate = 1.0f;
-        if (OUT && z) {
+        auto gated = [&] {
           const float zf = Elem<T>::to_f(zz[i]);
-          gate = zf * sigmoid_of<T>(zf);
-        }
+          return zf * sigmoid_of<T>(zf);
+        };
+        if (OUT && sizeof(T) == 4 && z) gate = gated();
         const float du = dt * uu;
         const F2 dt2 = f2(dt, dt), du2 = f2(du, du);
         F2 y0 = f2(0.0f, 0.0f), y1 = y0;
@@ -197,7 +201,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks) scan_kernel(ScanParams p) {
           float o = s2.x + s2.y;
 #pragma unroll
           for (int m = TPC / 2; m > 0; m >>= 1) o += __shfl_xor_sync(0xffffffffu, o, m);
-          o = fmaf(skip, uu, o) * gate;
+          o = fmaf(skip, uu, o);
+          if (sizeof(T) == 4) o *= gate;
+          else if (z) o *= gated();
           if (on && stores) *y = Elem<T>::from_f(o);
           y += p.Y.ss;
         } else {
