@@ -349,9 +349,9 @@ rk_status rk_describe_plan(rk_handle* h, const rk_problem* p, char* buf, int64_t
  * boundaries are read and written in 16-byte pieces.
  *
  * sequence_lens (int32 [batch], optional, else seq) clamps to [0, seq].
- * Steps past a row's length are not read; Y and the row gradients are
- * exactly 0 there.  A row of length 0 leaves its state as it was: the final
- * state is the initial state (zeros if absent).
+ * Steps past a row's length have no effect, whatever they hold; Y and the row
+ * gradients are exactly 0 there.  A row of length 0 leaves its state as it
+ * was: the final state is the initial state (zeros if absent).
  *
  * final_state may be the same buffer as initial_state (the same address: a
  * state updated in place); no other output may overlap an operand.  Null
@@ -446,7 +446,12 @@ typedef struct rk_conv_grad_operands {
  * [channels] (optional, else 0) are float32, and so are initial_state
  * (optional, else 0) and final_state [batch, channels, state]: a state that
  * is carried over many steps is not rounded between them.  state is 1 to
- * 128; groups divides channels. */
+ * 128; groups divides channels.
+ * A rate that is no number makes none of its states; a step of dt = 0 keeps a
+ * state whatever its rate, an infinite one included.  Long sequences are run
+ * in pieces side by side.  Rates and steps are meant to decay a state (dt A <=
+ * 0): one that grows, by a product of exp(dt A) over a piece that passes
+ * float32's range, and its gradients come out infinite or NaN. */
 typedef struct rk_scan_problem {
   int32_t dtype, layout;
   int32_t softplus;
@@ -459,7 +464,10 @@ typedef struct rk_scan_operands {
   rk_tensor A, D, delta_bias, sequence_lens, initial_state, final_state;
 } rk_scan_operands;
 
-/* Its gradient.  The row gradients dX, dDelta, dB, dC, dZ (dZ only with Z)
+/* Its gradient.  Its scratch is mostly states at every eighth step, batch *
+ * seq * channels * state / 8 floats, and partial sums of dB and dC: about 2^26
+ * floats at most, or what dB and dC have themselves.
+ * The row gradients dX, dDelta, dB, dC, dZ (dZ only with Z)
  * have the problem's dtype; dA, dD, d_delta_bias, d_initial_state and the
  * optional input d_final_state are float32. */
 typedef struct rk_scan_grad_operands {
@@ -477,8 +485,9 @@ int64_t rk_scan_grad_scratch_length(const rk_scan_problem* p);
  * device pointers.  Errors are those of rk_encode: RK_ERR_ARG for a null
  * handle, problem or operand list, RK_ERR_SHAPE for a bad size, pitch,
  * offset or missing operand (the message names the operator and the
- * argument), RK_ERR_UNSUPPORTED past the limits above or 2^31 - 1 rows or
- * elements of a row, RK_ERR_OOM, RK_ERR_CUDA.  rows, seq and batch may be 0:
+ * argument), RK_ERR_UNSUPPORTED past the limits above, 2^24 elements of a row
+ * (cols, channels, groups, groups * state), 2^30 steps or batch rows or
+ * 2^31 - 1 rows in all, RK_ERR_OOM, RK_ERR_CUDA.  rows, seq and batch may be 0:
  * what is left of the outputs is written (weights' gradients over no rows
  * are 0, the final state after no steps is the initial state).  cols,
  * channels and state are at least 1. */

@@ -8,9 +8,11 @@
 // reads the width - 1 inputs before it once more (from L2).
 //   p[s] = b + sum_j w[j] x[s - (width - 1) + j], y = p sigmoid(p) or p
 // 512 steps x 8 x 2048 Half, width 4, half of the steps past their length: 8.3
-// us, the floor of its bytes being 3.7; 4096 x 4 x 2048 without lengths: 31.3 us
-// (4.3 TB/s).  At these sizes a wave of blocks is short: what is left is
-// starting and draining it.
+// us, the floor of its bytes being 3.8: two waves of blocks, mostly starting and
+// draining them.  4096 x 4 x 2048 bf16 without lengths: 31.1 us (4.3 TB/s) over
+// seven waves; a block loads all it needs, computes and ends, so nothing of its
+// own is on the way while it computes, and three of its eleven rows are read
+// again.
 #include <algorithm>
 
 #include "rk.h"
@@ -131,10 +133,11 @@ __global__ void __launch_bounds__(128) conv_kernel(ConvParams p) {
 // the chunk are run for their dp alone.  Steps go in groups of four, the next
 // group's elements on their way.  A block is 32 pieces of channels by
 // kGradRows chunks; its weights' gradients are added up in shared memory and
-// written as one slice.  512 x 8 x 2048 bf16, width 4: 24.4 us with the second
-// launch's 3.8 (50 MB: 2.1 TB/s); bound by its instructions, about 30 per
-// element for the pre-activation, SiLU's slope, dx and dw, and by the registers
-// (two groups' elements, inputs, gradients, taps), which leave few warps.
+// written as one slice.  512 x 8 x 2048 bf16, width 4: 24.3 us with the second
+// launch's 3.8 (50 MB: 2.1 TB/s); bound by its instructions, 39 per element,
+// most of them for the pre-activation, SiLU's slope, dx and dw, and by the
+// registers (two groups' elements, inputs, gradients, taps), which leave few
+// warps.
 constexpr int kGradRows = 4;
 constexpr int kGroup = 4;  // steps loaded ahead
 

@@ -33,13 +33,13 @@
 // scan; e is linear in what arrives at a chunk's end with the same factor
 // exp(A sum dt), so one launch prepares both directions.
 //
-// Bound by instructions: 38 per step, channel and state on the way back, half
+// Bound by instructions: 39 per step, channel and state on the way back, half
 // of them the formulas above (2.5 decays, each an exponential, among them) and
 // half exchanges, shared memory and what belongs to a channel's step.
-// 512 steps x 8 sequences x 2048 channels x 16 states, bf16 with a gate: 357 us
-// in all, of which forward 87 us, chunks' carry 12, back 249 (2.1 instructions
+// 512 steps x 8 sequences x 2048 channels x 16 states, bf16 with a gate: 351 us
+// in all, of which forward 87 us, chunks' carry 12, back 243 (2.2 instructions
 // per clock and SM, 16 warps), rows 10, weights 4; the bytes alone would take
-// 17 us, the exponentials of two passes 29.
+// 18 us, the exponentials of two passes 29.
 #include <algorithm>
 #include <type_traits>
 
@@ -816,7 +816,9 @@ ScanPlan scan_grad_plan(long long seq, long long batch, long long channels, int 
   const long long tiles = (per + ch - 1) / ch;
   const long long blocks = batch * groups * tiles;
   // Chunks where the sequences alone fill up to two thirds of the card's places
-  // (four blocks per SM): 1024 steps x 2048 channels x 16 states bf16, 8
+  // (four blocks per SM, which the registers leave room for; with at most 8
+  // states shared memory leaves it for two in float32 and three in 16 bits, and
+  // the rule was not measured there): 1024 steps x 2048 channels x 16 states bf16, 8
   // sequences 831 us without and 625 with, 12 sequences 1084 and 899, 14
   // sequences 1081 and 1134.  Twice as many blocks as places fill the card more
   // evenly (8 sequences 625 against 677 us) while a chunk keeps 64 steps (a

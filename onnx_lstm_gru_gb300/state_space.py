@@ -288,9 +288,12 @@ class StateSpaceLayer:
     """Owns an rk handle.  Every method enqueues one operator on the current
     torch stream (or ``stream``) and returns the outputs named in ``want``,
     allocated unless they are passed by name (an input cannot be wanted that
-    was not passed).  Scratch comes from torch's
-    allocator, so calls may run on any stream and be captured into a graph.
-    No CPU path exists."""
+    was not passed).  Scratch comes from torch's allocator, so calls may run on
+    any stream and be captured into a graph.  Like the recurrent layer's, the
+    outputs carry no autograd history, also of tensors that require gradients:
+    the gradients are methods of their own, which ``examples/state_space_layer.py``
+    ties into ``torch.autograd.Function``.  A problem that is kept saves a
+    decoding step the look-up of an equal one.  No CPU path exists."""
 
     def __init__(self, flags: int = 0):
         load()
