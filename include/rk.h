@@ -447,9 +447,9 @@ typedef struct rk_conv_grad_operands {
  * (optional, else 0) and final_state [batch, channels, state]: a state that
  * is carried over many steps is not rounded between them.  state is 1 to
  * 128; groups divides channels.
- * A rate that is no number makes none of its states; a step of dt = 0 keeps a
- * state whatever its rate, an infinite one included.  Long sequences are run
- * in pieces side by side.  Rates and steps are meant to decay a state (dt A <=
+ * A step of dt = 0 keeps a state at any rate, an infinite one included; a
+ * rate that is NaN makes its state NaN from the first step on.  Long sequences
+ * are run in pieces side by side.  Rates and steps are meant to decay a state (dt A <=
  * 0): one that grows, by a product of exp(dt A) over a piece that passes
  * float32's range, and its gradients come out infinite or NaN. */
 typedef struct rk_scan_problem {
