@@ -448,10 +448,7 @@ typedef struct rk_conv_grad_operands {
  * is carried over many steps is not rounded between them.  state is 1 to
  * 128; groups divides channels.
  * A step of dt = 0 keeps a state at any rate, an infinite one included; a
- * rate that is NaN makes its state NaN from the first step on.  Long sequences
- * are run in pieces side by side.  Rates and steps are meant to decay a state (dt A <=
- * 0): one that grows, by a product of exp(dt A) over a piece that passes
- * float32's range, and its gradients come out infinite or NaN. */
+ * rate that is NaN makes its state NaN from the first step on. */
 typedef struct rk_scan_problem {
   int32_t dtype, layout;
   int32_t softplus;
@@ -466,7 +463,9 @@ typedef struct rk_scan_operands {
 
 /* Its gradient.  Its scratch is mostly states at every eighth step, batch *
  * seq * channels * state / 8 floats, and partial sums of dB and dC: about 2^26
- * floats at most, or what dB and dC have themselves.
+ * floats at most, or what dB and dC have themselves.  Long sequences are run
+ * in pieces side by side: where states grow, and the product of exp(dt A) over
+ * a piece passes float32's range, the gradients come out infinite or NaN.
  * The row gradients dX, dDelta, dB, dC, dZ (dZ only with Z)
  * have the problem's dtype; dA, dD, d_delta_bias, d_initial_state and the
  * optional input d_final_state are float32. */

@@ -235,36 +235,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) scan_kernel(ScanParams p) {
   }
 }
 
-// The chunks of one sequence in order, for one state of one channel: the state
-// each starts from takes the place of its own final state.  A factor past
-// float32's range (rates above 0 alone) is infinite here; taken in two parts, so
-// that a state of 0 stays 0, it cost 777 x 8 x 1030 x 16 float32 with lengths
-// 59.4 us instead of 54.4.
-__device__ __forceinline__ void carry_chunks(const ScanParams& p, int n, unsigned at, unsigned c, long long ck,
-                                             float A2) {
-  const long long i = n * ck + at;
-  float run = p.h0 ? p.h0[i] : 0.0f;
-  float* carry = p.carry + (long long)n * p.chunks * ck + at;
-  const float* sumdt = p.sumdt + (long long)n * p.chunks * p.C + c;
-  // a batch is read before any of it is overwritten: its loads are in flight together
-  constexpr int kBatch = 24;
-  for (int q0 = 0; q0 < p.chunks; q0 += kBatch) {
-    float s[kBatch], d[kBatch];
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      if (q0 + j < p.chunks) s[j] = carry[(q0 + j) * ck], d[j] = sumdt[(long long)(q0 + j) * p.C];
-    }
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      if (q0 + j < p.chunks) {
-        carry[(q0 + j) * ck] = run;
-        run = fmaf(chunk_decay(A2, d[j]), run, s[j]);
-      }
-    }
-  }
-  if (p.hT) p.hT[i] = run;
-}
-
+// The chunks' states in order: what each starts from takes the place of its own
+// final state.
 __global__ void __launch_bounds__(64) scan_carry_kernel(ScanParams p) {
   const unsigned ck = (unsigned)p.C * (unsigned)p.K;  // at most 2^31
   const unsigned at = blockIdx.x * 64u + threadIdx.x;
@@ -274,7 +246,15 @@ __global__ void __launch_bounds__(64) scan_carry_kernel(ScanParams p) {
   previous_done();
   if (!on) return;
   const unsigned c = at / (unsigned)p.K;
-  for (int n = blockIdx.y; n < p.N; n += gridDim.y) carry_chunks(p, n, at, c, ck, A2);
+  for (int n = blockIdx.y; n < p.N; n += gridDim.y) {
+    const long long i = (long long)n * ck + at;
+    float* carry = p.carry + (long long)n * p.chunks * ck + at;
+    const float* sumdt = p.sumdt + (long long)n * p.chunks * p.C + c;
+    float run = p.h0 ? p.h0[i] : 0.0f;
+    run = may_grow(p, A2) ? join_batches<4, true>(carry, ck, sumdt, p.C, p.chunks, false, A2, run)
+                          : join_batches<24, false>(carry, ck, sumdt, p.C, p.chunks, false, A2, run);
+    if (p.hT) p.hT[i] = run;
+  }
 }
 
 // Single tokens: four states per thread, TPC threads per channel, the state

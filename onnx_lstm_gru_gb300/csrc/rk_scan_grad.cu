@@ -441,23 +441,8 @@ __global__ void __launch_bounds__(64) scan_grad_carry_kernel(ScanParams p) {
     const float* sumdt = p.sumdt + (long long)n * p.chunks * p.C + c;
     const float* from = back ? p.dhT : p.h0;
     float run = from ? from[i] : 0.0f;
-    // a batch is read before any of it is overwritten: its loads are in flight together
-    constexpr int kBatch = 16;
-    for (int q0 = 0; q0 < p.chunks; q0 += kBatch) {
-      float s[kBatch], d[kBatch];
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const int q = back ? p.chunks - 1 - q0 - j : q0 + j;
-        if (q0 + j < p.chunks) s[j] = carry[q * ck], d[j] = sumdt[(long long)q * p.C];
-      }
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        if (q0 + j < p.chunks) {
-          carry[(back ? p.chunks - 1 - q0 - j : q0 + j) * ck] = run;
-          run = fmaf(chunk_decay(A2, d[j]), run, s[j]);
-        }
-      }
-    }
+    run = may_grow(p, A2) ? join_batches<4, true>(carry, ck, sumdt, p.C, p.chunks, back, A2, run)
+                          : join_batches<16, false>(carry, ck, sumdt, p.C, p.chunks, back, A2, run);
     if (back && p.dh0) p.dh0[i] = run;
   }
 }

@@ -238,9 +238,45 @@ __device__ __forceinline__ float rate2(float a) {
   return r;
 }
 
-// What a chunk whose steps sum to d leaves of the state that enters it.  All
-// of it where no step is within the row's length, whatever the rate.
-__device__ __forceinline__ float chunk_decay(float A2, float d) { return d == 0.0f ? 1.0f : exp2_fast(A2 * d); }
+// Where decays may grow a state (a rate above 0, or steps that no softplus keeps
+// from being negative) 2^x can pass float32's range.  2^x v is then taken in two
+// parts, so that it is 0 for v = 0 and finite wherever it can be.
+__device__ __forceinline__ bool may_grow(const ScanParams& p, float A2) { return A2 > 0.0f || !p.softplus; }
+__device__ __forceinline__ float scale2(float x, float v) {
+  const float over = fminf(fmaxf(x - 127.0f, 0.0f), 127.0f);
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(127.0f));
+  return exp2_fast(x) * (exp2_fast(over) * v);
+}
+
+// The chunks of a sequence in order, for one state of one channel: from what
+// enters the first one, run, each chunk's own end (carry) is replaced by what
+// enters it; returns what leaves the last one.  The chunk whose steps sum to d
+// leaves 2^(A2 d) run and its own end; all of run where no step is within the
+// row's length, whatever the rate.  BACK: from the last chunk to the first.
+// A batch is read before any of it is overwritten: its loads are in flight
+// together.  States that may grow go through a loop of their own, with fewer.
+template <int BATCH, bool GROWS>
+__device__ __forceinline__ float join_batches(float* carry, long long ck, const float* sumdt, int C, int chunks,
+                                              bool back, float A2, float run) {
+#pragma unroll 1
+  for (int q0 = 0; q0 < chunks; q0 += BATCH) {
+    float s[BATCH], d[BATCH];
+#pragma unroll
+    for (int j = 0; j < BATCH; ++j) {
+      const int q = back ? chunks - 1 - q0 - j : q0 + j;
+      if (q0 + j < chunks) s[j] = carry[q * ck], d[j] = sumdt[(long long)q * C];
+    }
+#pragma unroll
+    for (int j = 0; j < BATCH; ++j) {
+      if (q0 + j < chunks) {
+        carry[(back ? chunks - 1 - q0 - j : q0 + j) * ck] = run;
+        if constexpr (GROWS) run = s[j] + scale2(d[j] == 0.0f ? 0.0f : A2 * d[j], run);
+        else run = fmaf(d[j] == 0.0f ? 1.0f : exp2_fast(A2 * d[j]), run, s[j]);
+      }
+    }
+  }
+  return run;
+}
 
 // Adds COUNT values over the lanes whose bits from FIRST down to LAST
 // differ.  Each exchange leaves a lane half of its values until one is left;

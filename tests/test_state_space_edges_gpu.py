@@ -94,6 +94,41 @@ def test_conv_special_weights(layer, seq, batch, channels, lens, act, dtype):
             past_zero(p, got, ("Y", "dX"), lens)
 
 
+# ---- states that grow --------------------------------------------------------------------------------------
+
+def growing(S, batch, C, K, tiny, seed=5):
+    """Zeros through steps of e^20 until the last two steps' inputs; or a state
+    of 1e-30 that grows by e^120 within a chunk.  The gradients' way back alike."""
+    i = Inputs(seed, "f32")
+    t = dict(X=torch.zeros(S, batch, C, device="cuda"), Delta=torch.zeros(S, batch, C, device="cuda"),
+             B=i.normal(S, batch, K), C=i.normal(S, batch, K), A=torch.full((C, K), 2.0, device="cuda"))
+    g = dict(dY=torch.zeros(S, batch, C, device="cuda"))
+    if tiny:
+        t["Delta"][64:70] = 10.0
+        t["initial_state"] = i.normal(batch, C, K) * 1e-30
+        g["d_final_state"] = i.normal(batch, C, K) * 1e-30
+    else:
+        t["Delta"] += 10.0
+        t["X"][-2:] = i.normal(2, batch, C)
+        g["dY"][:2] = i.normal(2, batch, C)
+    return t, g
+
+
+@pytest.mark.parametrize("tiny", [False, True])
+@pytest.mark.parametrize("batch,state", [(1, 16), (3, 5)])
+def test_scan_growing_over_chunks(layer, batch, state, tiny):
+    """Chunks that run side by side give what the steps give, although the
+    product of a chunk's factors passes float32's range."""
+    p = rk.ScanProblem(200, batch, 24, state, softplus=False)
+    assert rk.rk_scan_scratch_length(p.to_c()) > 0  # chunks
+    t, _ = growing(200, batch, 24, state, tiny)
+    t["A"][1] = -2.0  # and a channel that forgets beside them
+    want = scan_want(p, t)
+    assert float(want["final_state"].abs().max()) > 1e2
+    for k, v in layer.scan(p, **t).items():
+        check_all(v, want[k], k)
+
+
 # ---- accuracy of float32 outputs ------------------------------------------------------------------------
 
 def relative(got, want, bound):
