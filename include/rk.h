@@ -463,9 +463,7 @@ typedef struct rk_scan_operands {
 
 /* Its gradient.  Its scratch is mostly states at every eighth step, batch *
  * seq * channels * state / 8 floats, and partial sums of dB and dC: about 2^26
- * floats at most, or what dB and dC have themselves.  Long sequences are run
- * in pieces side by side: where states grow, and the product of exp(dt A) over
- * a piece passes float32's range, the gradients come out infinite or NaN.
+ * floats at most, or what dB and dC have themselves.
  * The row gradients dX, dDelta, dB, dC, dZ (dZ only with Z)
  * have the problem's dtype; dA, dD, d_delta_bias, d_initial_state and the
  * optional input d_final_state are float32. */

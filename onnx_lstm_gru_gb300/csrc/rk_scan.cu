@@ -18,8 +18,8 @@
 // exponential (the unit takes 32 lanes per clock and SM) and three (states) or
 // four (outputs) multiply-adds per step, channel and state.  Two states to a
 // packed register halve the issue slots of the multiply-adds.  4096 steps x 1
-// sequence x 2048 channels x 16 states, bf16 with a gate: 94 us, of which
-// states 38, carry 7, outputs 52; the exponentials of both passes would take
+// sequence x 2048 channels x 16 states, bf16 with a gate: 92 us, of which
+// states 38, carry 6, outputs 52; the exponentials of both passes would take
 // 28 us alone, the bytes 10.  One thread per channel of 16 states keeps the
 // sum for y in registers; two channels per thread, one-warp blocks with
 // asynchronous copies, groups of two steps and six blocks per SM all measured

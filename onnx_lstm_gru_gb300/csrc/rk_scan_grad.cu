@@ -36,7 +36,7 @@
 // Bound by instructions: 39 per step, channel and state on the way back, half
 // of them the formulas above (2.5 decays, each an exponential, among them) and
 // half exchanges, shared memory and what belongs to a channel's step.
-// 512 steps x 8 sequences x 2048 channels x 16 states, bf16 with a gate: 351 us
+// 512 steps x 8 sequences x 2048 channels x 16 states, bf16 with a gate: 353 us
 // in all, of which forward 87 us, chunks' carry 12, back 243 (2.2 instructions
 // per clock and SM, 16 warps), rows 10, weights 4; the bytes alone would take
 // 18 us, the exponentials of two passes 29.
@@ -311,6 +311,15 @@ struct States {
       store_states<4, TPC>(rows + (long long)(c + e) * p.K, p.K, part, p.k_vec, x);
     }
   }
+  __device__ __forceinline__ bool finite() const {
+    bool all = true;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 a = f2_get(v[i / 2][i % 2]);
+      all = all && isfinite(a.x) && isfinite(a.y);
+    }
+    return all;
+  }
   __device__ __forceinline__ void to_rates() {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -327,6 +336,16 @@ constexpr int kLeft = COUNT > LANES ? COUNT / LANES : 1;
 __device__ __forceinline__ float halves(F2 a) {
   const float2 v = f2_get(a);
   return v.x + v.y;
+}
+
+// 2^(2 half A2) start + own, the factor in two halves: no infinity meets a start
+// of 0, and a small one grows as far as float32 goes.
+__device__ __forceinline__ F2 join2(F2 half, F2 A2, F2 start, F2 own) {
+  float2 x = f2_get(fma2(half, A2, f2(3e-8f, 3e-8f)));
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(x.x) : "f"(127.0f));
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(x.y) : "f"(127.0f));
+  const F2 root = exp2_fast2(f2(x.x, x.y));
+  return fma2(root, mul2(root, start), own);
 }
 
 // h = a h + (dt u) B of one step.
@@ -347,7 +366,8 @@ __device__ __forceinline__ void update(const Sm& sm, int r, int j, int part, con
 // decayed by the sum) and at the chunk's end.  ADJOINT, for chunks that run
 // side by side: what leaves the chunk's start of the state's gradient when
 // nothing arrives at its end, the sum over its steps of (product of a from
-// the chunk's start) C dy.
+// the chunk's start) C dy.  The product is carried along; where it overflowed,
+// for states that grow, the block sums once more from its exponent.
 template <typename T, int TPC, bool ADJOINT>
 __global__ void __launch_bounds__(kThreads, 4) scan_grad_states_kernel(ScanParams p) {
   using Sm = GradSmem<T, TPC>;
@@ -414,6 +434,34 @@ __global__ void __launch_bounds__(kThreads, 4) scan_grad_states_kernel(ScanParam
     }
   }
   if constexpr (ADJOINT) {
+    // Products past float32's range (states that grow): the sum again, from the
+    // products' exponents
+    if (__syncthreads_or(!pr.finite())) {
+      pr.zero(), e.zero();
+      if (t0 < live) b.template fetch<S>(first);
+      for (int t = first; t < live; t += kT) {
+        copies_done();
+        __syncthreads();
+        b.template put<S>(t);
+        __syncthreads();
+        if (t + kT < live) b.template fetch<S>(t + kT);
+#pragma unroll 1
+        for (int r = 0; r < kT; ++r) {
+          const ulonglong2 C = *reinterpret_cast<const ulonglong2*>(&sm.C[r][part * 4]);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const F2 dt{reinterpret_cast<const ulonglong2*>(&sm.dtu[r][k * Sm::P + j])->x};
+            const F2 dy{*reinterpret_cast<const unsigned long long*>(&sm.dy[r][k * Sm::P + j])};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              pr.v[k][i] = fma2(dt, A2.v[k][i], pr.v[k][i]);
+              const float2 x = f2_get(pr.v[k][i]), v = f2_get(mul2(F2{i ? C.y : C.x}, dy));
+              e.v[k][i] = add2(e.v[k][i], f2(scale2(x.x, v.x), scale2(x.y, v.y)));
+            }
+          }
+        }
+      }
+    }
     const long long row = ((long long)n * p.chunks + chunk) * p.C;
     h.template store<TPC>(p.carry + row * p.K, c, left, p, part);
     e.template store<TPC>(p.gcarry + row * p.K, c, left, p, part);
@@ -486,9 +534,9 @@ __device__ __forceinline__ void grad_tile(const ScanParams& p, GradSmem<T, TPC>&
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const float cum = k < left ? p.cum[at * p.C + c + k] : 0.0f;
+          const F2 half = f2(0.5f * cum, 0.5f * cum);
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            h.v[k][i] = fma2(decay2(f2(cum, cum), A2.v[k][i]), h0.v[k][i], h.v[k][i]);
+          for (int i = 0; i < 2; ++i) h.v[k][i] = join2(half, A2.v[k][i], h0.v[k][i], h.v[k][i]);
         }
       }
     }

@@ -104,12 +104,13 @@ def growing(S, batch, C, K, tiny, seed=5):
              B=i.normal(S, batch, K), C=i.normal(S, batch, K), A=torch.full((C, K), 2.0, device="cuda"))
     g = dict(dY=torch.zeros(S, batch, C, device="cuda"))
     if tiny:
-        t["Delta"][64:70] = 10.0
+        t["Delta"][S // 3 - 3:S // 3 + 3] = 10.0
         t["initial_state"] = i.normal(batch, C, K) * 1e-30
         g["d_final_state"] = i.normal(batch, C, K) * 1e-30
     else:
         t["Delta"] += 10.0
         t["X"][-2:] = i.normal(2, batch, C)
+        t["initial_state"] = torch.zeros(batch, C, K, device="cuda")
         g["dY"][:2] = i.normal(2, batch, C)
     return t, g
 
@@ -126,6 +127,20 @@ def test_scan_growing_over_chunks(layer, batch, state, tiny):
     want = scan_want(p, t)
     assert float(want["final_state"].abs().max()) > 1e2
     for k, v in layer.scan(p, **t).items():
+        check_all(v, want[k], k)
+
+
+@pytest.mark.parametrize("tiny", [False, True])
+@pytest.mark.parametrize("seq,batch,state", [(200, 1, 16), (203, 3, 5), (20, 2, 16), (17, 1, 64)])
+def test_scan_grad_growing(layer, seq, batch, state, tiny):
+    """The way back alike, in chunks and without them, where the state at a
+    step is found from what entered the chunk."""
+    p = rk.ScanProblem(seq, batch, 24, state, softplus=False)
+    t, g = growing(seq, batch, 24, state, tiny)
+    t["A"][1] = -2.0
+    want = scan_want(p, t, g)
+    names = tuple(n for n in SCAN_GRADS if n != "dZ")
+    for k, v in layer.scan_grad(p, **t, **g, want=names).items():
         check_all(v, want[k], k)
 
 
