@@ -37,7 +37,7 @@
 // of them the formulas above (2.5 decays, each an exponential, among them) and
 // half exchanges, shared memory and what belongs to a channel's step.
 // 512 steps x 8 sequences x 2048 channels x 16 states, bf16 with a gate: 353 us
-// in all, of which forward 87 us, chunks' carry 12, back 243 (2.2 instructions
+// in all, of which forward 87 us, chunks' carry 14, back 243 (2.2 instructions
 // per clock and SM, 16 warps), rows 10, weights 4; the bytes alone would take
 // 18 us, the exponentials of two passes 29.
 #include <algorithm>
