@@ -499,6 +499,99 @@ rk_status rk_scan_encode(rk_handle* h, const rk_scan_problem* p, const rk_scan_o
 rk_status rk_scan_grad_encode(rk_handle* h, const rk_scan_problem* p, const rk_scan_grad_operands* ops,
                               const rk_workspace* scratch, void* stream);
 
+/* ---- linear attention layers ---------------------------------------------
+ *
+ * The operators of a recurrent layer whose state is a matrix for each head:
+ * the normalisation and rotation of its queries and keys, attention through
+ * the state, and the gradients of both.  Their frame is that of the state
+ * space layers above: rows, layouts, sequence_lens, states, scratch, errors.
+ * A row holds its heads one after the other, each of consecutive elements. */
+
+/* Queries and keys by head, x the `size` elements of one head of one row:
+ *   n = x inv scale,  inv = 1, 1 / sqrt(sum x^2 / size + epsilon) (norm 1) or
+ *                           1 / sqrt(sum x^2 + epsilon) (norm 2),
+ * and of its first `rotary` elements each pair (a, b) is turned by its angle,
+ *   a' = a cos - b sin,  b' = b cos + a sin,  angle = position * Frequencies[i],
+ * pair i being the elements i and i + rotary / 2, or 2 i and 2 i + 1 with
+ * interleaved 1.  The others stay.  Q and YQ are rows of heads * size, K and
+ * YK of key_heads * size elements, QScale and KScale [size] (optional, 1), all
+ * of the problem's dtype; Frequencies float32 [rotary / 2] (radians per
+ * position, required with rotary > 0); positions int32 [seq, batch] (layout 0)
+ * or [batch, seq], else the step's number.  Angles are taken modulo a turn in
+ * 64 bits: those of far positions are as exact as those of near ones. */
+typedef struct rk_qk_problem {
+  int32_t dtype, layout;
+  int32_t norm;        /* 0: none, 1: root mean square, 2: length */
+  int32_t interleaved; /* 0: pairs half of `rotary` apart, 1: neighbours */
+  int32_t rotary;      /* even, 0 to size */
+  float epsilon;       /* >= 0 */
+  int64_t seq, batch, heads, key_heads, size; /* size: 1 to 256 */
+} rk_qk_problem;
+
+typedef struct rk_qk_operands {
+  rk_rows Q, K, YQ, YK;
+  rk_tensor QScale, KScale, Frequencies, positions, sequence_lens;
+} rk_qk_operands;
+
+/* Its gradient: dQ and dK rows in the problem's dtype, dQScale and dKScale
+ * float32 [size], sums over all rows and heads.  dYQ and dYK are required. */
+typedef struct rk_qk_grad_operands {
+  rk_rows Q, K, dYQ, dYK, dQ, dK;
+  rk_tensor QScale, KScale, Frequencies, positions, sequence_lens, dQScale, dKScale;
+} rk_qk_grad_operands;
+
+/* Attention through a state that decays by head.  Per batch row and head:
+ *   g = Decay[s, head] + decay_bias[head]   (either may be absent: 0),
+ *   H = e^g H + k v^T,   y = scale H^T q,
+ * H being [key_size, value_size].  Q are rows of query_heads * key_size
+ * elements, K of key_heads * key_size, V of value_heads * value_size, Y of
+ * heads * value_size, in the problem's dtype.  query_heads, key_heads and
+ * value_heads each divide heads (0: as many): head h reads head h /
+ * (heads / query_heads) of Q, and so on.  Decay are float32 rows of `heads`
+ * elements, decay_bias float32 [heads]; initial_state (optional, else 0) and
+ * final_state float32 [batch, heads, key_size, value_size].  key_size and
+ * value_size are 1 to 128.
+ * g is the decay's natural logarithm: 0 keeps the state, minus infinity
+ * forgets it, so that a row may hold several documents.  Above 0 the state
+ * grows; products of decays beyond float32's range are infinite.
+ * Infinities and NaN of a step reach that step's and later outputs only. */
+typedef struct rk_attn_problem {
+  int32_t dtype, layout;
+  float scale;
+  int32_t query_heads, key_heads, value_heads;
+  int64_t seq, batch, heads, key_size, value_size;
+} rk_attn_problem;
+
+typedef struct rk_attn_operands {
+  rk_rows Q, K, V, Decay, Y;
+  rk_tensor decay_bias, sequence_lens, initial_state, final_state;
+} rk_attn_operands;
+
+/* Its gradient.  dQ, dK, dV have the problem's dtype (heads that share are
+ * added up before the one rounding), dDecay (float32 rows of `heads`
+ * elements), d_decay_bias, d_initial_state and the optional input
+ * d_final_state are float32.  dDecay is taken from running sums, in float64,
+ * over the sequence of what queries and keys contribute: where it is far
+ * smaller than those contributions it has their float32 accuracy.  Infinities and NaN in an
+ * operand may reach the gradients of any step of their batch row. */
+typedef struct rk_attn_grad_operands {
+  rk_rows Q, K, V, Decay, dY, dQ, dK, dV, dDecay;
+  rk_tensor decay_bias, sequence_lens, initial_state, d_final_state, d_decay_bias, d_initial_state;
+} rk_attn_grad_operands;
+
+int64_t rk_qk_grad_scratch_length(const rk_qk_problem* p);
+int64_t rk_attn_scratch_length(const rk_attn_problem* p);
+int64_t rk_attn_grad_scratch_length(const rk_attn_problem* p);
+
+/* As the state space entries; batch * heads is at most 2^24. */
+rk_status rk_qk_encode(rk_handle* h, const rk_qk_problem* p, const rk_qk_operands* ops, void* stream);
+rk_status rk_qk_grad_encode(rk_handle* h, const rk_qk_problem* p, const rk_qk_grad_operands* ops,
+                            const rk_workspace* scratch, void* stream);
+rk_status rk_attn_encode(rk_handle* h, const rk_attn_problem* p, const rk_attn_operands* ops,
+                         const rk_workspace* scratch, void* stream);
+rk_status rk_attn_grad_encode(rk_handle* h, const rk_attn_problem* p, const rk_attn_grad_operands* ops,
+                              const rk_workspace* scratch, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

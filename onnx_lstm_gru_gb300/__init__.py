@@ -28,10 +28,11 @@ __all__ = [
     "rk_encode_noalloc", "rk_validate_lengths", "RK_OK", "RK_ERR_SHAPE", "RK_ERR_UNSUPPORTED", "RK_ERR_CUDA", "RK_ERR_TIMEOUT", "RK_ERR_OOM", "RK_ERR_ARG",
     "RK_FORCE_SIMT_PROJECTION", "RK_FORCE_GRID_STEP", "RK_FORCE_GENERAL_STEP", "RK_FORCE_SIMT_STEP",
     "RK_SEPARATE_PROJECTION", "RK_PREFER_TENSOR_STEP", "EXPORTED_SYMBOLS",
-    "StateSpaceLayer", "NormProblem", "ConvProblem", "ScanProblem",
+    "StateSpaceLayer", "NormProblem", "ConvProblem", "ScanProblem", "QkProblem", "AttnProblem",
     "rk_norm_encode", "rk_norm_grad_encode", "rk_conv_encode", "rk_conv_grad_encode", "rk_scan_encode",
     "rk_scan_grad_encode", "rk_norm_grad_scratch_length", "rk_conv_grad_scratch_length", "rk_scan_scratch_length",
-    "rk_scan_grad_scratch_length",
+    "rk_scan_grad_scratch_length", "rk_qk_encode", "rk_qk_grad_encode", "rk_attn_encode", "rk_attn_grad_encode",
+    "rk_qk_grad_scratch_length", "rk_attn_scratch_length", "rk_attn_grad_scratch_length",
 ]
 
 RK_OK, RK_ERR_SHAPE, RK_ERR_UNSUPPORTED, RK_ERR_CUDA, RK_ERR_TIMEOUT, RK_ERR_OOM, RK_ERR_ARG = range(7)
@@ -58,7 +59,8 @@ EXPORTED_SYMBOLS = [
     "rk_encode_noalloc", "rk_validate_lengths",
     "rk_norm_encode", "rk_norm_grad_encode", "rk_conv_encode", "rk_conv_grad_encode", "rk_scan_encode",
     "rk_scan_grad_encode", "rk_norm_grad_scratch_length", "rk_conv_grad_scratch_length", "rk_scan_scratch_length",
-    "rk_scan_grad_scratch_length",
+    "rk_scan_grad_scratch_length", "rk_qk_encode", "rk_qk_grad_encode", "rk_attn_encode", "rk_attn_grad_encode",
+    "rk_qk_grad_scratch_length", "rk_attn_scratch_length", "rk_attn_grad_scratch_length",
 ]
 
 
@@ -432,7 +434,9 @@ class RecurrentLayer:
 
 from . import state_space  # noqa: E402  (uses the names above)
 from .state_space import (  # noqa: E402,F401
-    ConvProblem, NormProblem, ScanProblem, StateSpaceLayer, rk_conv_encode, rk_conv_grad_encode,
-    rk_conv_grad_scratch_length, rk_conv_problem, rk_norm_encode, rk_norm_grad_encode, rk_norm_grad_scratch_length,
-    rk_norm_problem, rk_rows, rk_scan_encode, rk_scan_grad_encode, rk_scan_grad_scratch_length, rk_scan_problem,
+    AttnProblem, ConvProblem, NormProblem, QkProblem, ScanProblem, StateSpaceLayer, rk_attn_encode,
+    rk_attn_grad_encode, rk_attn_grad_scratch_length, rk_attn_problem, rk_attn_scratch_length, rk_conv_encode,
+    rk_conv_grad_encode, rk_conv_grad_scratch_length, rk_conv_problem, rk_norm_encode, rk_norm_grad_encode,
+    rk_norm_grad_scratch_length, rk_norm_problem, rk_qk_encode, rk_qk_grad_encode, rk_qk_grad_scratch_length,
+    rk_qk_problem, rk_rows, rk_scan_encode, rk_scan_grad_encode, rk_scan_grad_scratch_length, rk_scan_problem,
     rk_scan_scratch_length, rk_workspace)

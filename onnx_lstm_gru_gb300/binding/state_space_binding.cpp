@@ -47,6 +47,7 @@ struct Plan {
 };
 
 constexpr int kMaxOperands = 21, kWords = 5 * kMaxOperands;
+// The operand that run() takes by itself is a plan's first.
 
 const Entry* find(const Plan* p, PyObject* name) {
   for (const Entry& e : *p->entries)
@@ -113,7 +114,7 @@ bool pack(const Entry& e, PyObject* obj, c10::Device device, int64_t* words) {
   return true;
 }
 
-// run(handle, X, want, tensors): the outputs as a dict, or the entry's error code.
+// run(handle, X, want, tensors): the outputs as a dict, or the entry's error code.  X: the first operand.
 PyObject* plan_run(PyObject* self, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   Plan* p = reinterpret_cast<Plan*>(self);
@@ -126,8 +127,9 @@ PyObject* plan_run(PyObject* self, PyObject* const* args, Py_ssize_t n) {
     if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "the layer is closed");
     return nullptr;
   }
+  const Entry* const first = p->entries->data();
   if (!THPVariable_Check(args[1]) || !THPVariable_Unpack(args[1]).is_cuda()) {
-    PyErr_SetString(PyExc_ValueError, "X: expected a CUDA tensor");
+    PyErr_Format(PyExc_ValueError, "%U: expected a CUDA tensor", first->name);
     return nullptr;
   }
   const c10::Device device = THPVariable_Unpack(args[1]).device();
@@ -135,9 +137,8 @@ PyObject* plan_run(PyObject* self, PyObject* const* args, Py_ssize_t n) {
   if (device.index() != c10::cuda::current_device()) guard.set_device(device);
 
   int64_t words[kWords] = {};
-  static PyObject* const kX = PyUnicode_InternFromString("X");
-  const Entry* e = find(p, kX);
-  if (e == nullptr || !pack(*e, args[1], device, words)) return nullptr;
+  const Entry* e = first;
+  if (!pack(*e, args[1], device, words)) return nullptr;
   uint32_t seen = 1u << (e - p->entries->data());
   PyObject *key, *value;
   for (Py_ssize_t pos = 0; PyDict_Next(args[3], &pos, &key, &value);) {
@@ -159,7 +160,7 @@ PyObject* plan_run(PyObject* self, PyObject* const* args, Py_ssize_t n) {
   for (Py_ssize_t i = 0; i < PySequence_Fast_GET_SIZE(want.get()); ++i) {
     PyObject* name = PySequence_Fast_GET_ITEM(want.get(), i);
     if ((e = find(p, name)) == nullptr) return nullptr;
-    PyObject* given = e->name == kX ? args[1] : PyDict_GetItemWithError(args[3], name);
+    PyObject* given = e == first ? args[1] : PyDict_GetItemWithError(args[3], name);
     if (given != nullptr && given != Py_None) {
       if (PyDict_SetItem(out, name, given) != 0) return nullptr;
       continue;
@@ -222,6 +223,10 @@ PyObject* plan_new(PyTypeObject* type, PyObject* args, PyObject*) {
       if (PyErr_Occurred()) return nullptr;
     }
     entries.push_back(std::move(e));
+  }
+  if (entries.empty()) {
+    PyErr_SetString(PyExc_ValueError, "Plan: no entries");
+    return nullptr;
   }
   Plan* p = reinterpret_cast<Plan*>(type->tp_alloc(type, 0));
   if (p == nullptr) return nullptr;

@@ -1,0 +1,266 @@
+// rk_attn.cu -- attention through a state that decays by head, step by step;
+// the decays' gradient and the sums over heads that share.
+//
+//   H = e^g H + su k v^T,  o = so H^T q          (a pass of rk_attn.h)
+#include <algorithm>
+
+#include "rk.h"
+#include "rk_attn.h"
+#include "rk_ssm_common.cuh"
+
+namespace rk {
+namespace {
+
+constexpr int kStepThreads = 256, kStepRows = 16, kStepCols = 32, kMaxHead = 128;
+constexpr int kGroups = kStepThreads / kStepCols, kStates = kMaxHead / kGroups;
+
+// The recurrence as it stands: a block holds 32 columns of one state, a warp
+// an eighth of their rows, a lane one column of those in registers.  Sixteen
+// steps' rows are fetched together; their outputs are added up over the warps
+// at the end.
+template <typename T>
+__global__ void __launch_bounds__(kStepThreads) attn_step_kernel(AttnParams p, int blocks) {
+  __shared__ float sq[kStepRows][kMaxHead], sk[kStepRows][kMaxHead], sv[kStepRows][kStepCols], sd[kStepRows];
+  __shared__ float part[kStepRows][kGroups][kStepCols];
+  long long id = blockIdx.x;
+  const int vb = (int)(id % blocks);
+  id /= blocks;
+  const int h = (int)(id % p.H);
+  id /= p.H;
+  const int n = (int)(id % p.N);
+  const AttnPass& a = p.pass[id / p.N];
+  const int v0 = vb * kStepCols;
+  if (v0 >= a.V) return;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int per = (a.K + kGroups - 1) / kGroups, k0 = warp * per, mine = max(min(per, a.K - k0), 0);
+  const int v = v0 + lane;
+  const long long state = ((long long)n * p.H + h) * a.K * a.V;
+  auto at = [&](int i) { return state + (a.v_major ? (long long)v * a.K + k0 + i : (long long)(k0 + i) * a.V + v); };
+  float s[kStates];
+#pragma unroll
+  for (int i = 0; i < kStates; ++i) s[i] = a.first && i < mine && v < a.V ? a.first[at(i)] : 0.0f;
+  const int L = row_length(p.lens, n, p.S);
+  const float bias = p.bias ? p.bias[h] : 0.0f;
+  const T* q = static_cast<const T*>(a.q.p) + n * a.q.ns + (long long)(h / a.q_of) * a.K;
+  const T* k = static_cast<const T*>(a.k.p) + n * a.k.ns + (long long)(h / a.k_of) * a.K;
+  const T* x = static_cast<const T*>(a.v.p) + n * a.v.ns + (long long)(h / a.v_of) * a.V;
+  const float* g = static_cast<const float*>(p.decay.p) + n * p.decay.ns + h;
+  T* o = static_cast<T*>(a.o.p) + n * a.o.ns + (long long)(h / a.o_of) * a.V;
+  const T* w = static_cast<const T*>(a.dot_with.p) + n * a.dot_with.ns + (long long)(h / a.o_of) * a.V;
+  auto put = [&](int t, float y) {
+    if (v >= a.V) return;
+    if (a.o32) a.o32[(((long long)n * p.S + t) * p.H + h) * a.V + v] = y;
+    else if (a.o.p) o[t * a.o.ss + v] = Elem<T>::from_f(y);
+  };
+#pragma unroll 1
+  for (int base = 0; base < L; base += kStepRows) {
+    const int rows = min(kStepRows, L - base);
+    auto step = [&](int j) { return a.backward ? L - 1 - base - j : base + j; };
+    for (int i = threadIdx.x; i < rows * kMaxHead; i += kStepThreads) {
+      const int j = i / kMaxHead, c = i % kMaxHead;
+      const long long t = step(j);
+      if (c < a.K) sq[j][c] = Elem<T>::to_f(q[t * a.q.ss + c]), sk[j][c] = Elem<T>::to_f(k[t * a.k.ss + c]);
+    }
+    for (int i = threadIdx.x; i < rows * kStepCols; i += kStepThreads) {
+      const int j = i / kStepCols, c = v0 + i % kStepCols;
+      sv[j][i % kStepCols] = c < a.V ? a.su * Elem<T>::to_f(x[step(j) * a.v.ss + c]) : 0.0f;
+    }
+    if (threadIdx.x < rows) sd[threadIdx.x] = expf((p.decay.p ? g[step(threadIdx.x) * p.decay.ss] : 0.0f) + bias);
+    __syncthreads();
+#pragma unroll 1
+    for (int j = 0; j < rows; ++j) {
+      const float d = sd[j], c = sv[j][lane];
+      float y = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kStates; ++i) {
+        if (i < mine) {
+          s[i] = fmaf(sk[j][k0 + i], c, a.backward ? s[i] : d * s[i]);
+          y = fmaf(sq[j][k0 + i], s[i], y);
+          if (a.backward) s[i] *= d;
+        }
+      }
+      part[j][warp][lane] = y;
+    }
+    __syncthreads();
+    for (int j = warp; j < rows; j += kGroups) {
+      float y = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i) y += part[j][i][lane];
+      y *= a.so;
+      const int t = step(j);
+      put(t, y);
+      if (a.dot) {
+        const float d = warp_sum(v < a.V ? y * Elem<T>::to_f(w[t * a.dot_with.ss + v]) : 0.0f);
+        if (lane == 0) a.dot[(((long long)vb * p.N + n) * p.H + h) * p.S + t] = d;
+      }
+    }
+    // no wait: the next rows are read after the first barrier, `part` is written after the second
+  }
+  for (int t = L + warp; t < p.S; t += kGroups) put(t, 0.0f);
+  float with = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kStates; ++i) {
+    if (i < mine && v < a.V) {
+      if (a.last) a.last[at(i)] = s[i];
+      if (a.with) with = fmaf(a.with[at(i)], s[i], with);
+    }
+  }
+  if (a.cross) {
+    __shared__ float sums[kGroups];
+    with = warp_sum(with);
+    if (lane == 0) sums[warp] = with;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      float y = 0.0f;
+      for (int i = 0; i < kGroups; ++i) y += sums[i];
+      a.cross[((long long)vb * p.N + n) * p.H + h] = y;
+    }
+  }
+}
+
+// A step's decay lies between the steps before it, which wrote the state, and
+// those from it on, which read it; with A_t = q dq and B_t = k dk of a step
+//   dg_t = E_0 + sum over s < t of (B_s - A_s),   E_0 = <H, dH> before the first,
+// and the same sum over all steps ends at E_L = <H, dH> behind the last.  The
+// sums are float64 (they run over the whole sequence); what the float32
+// products leave at the end is known, E_L, and is taken back evenly along the
+// way: with no states to start from or to end at, both ends are exact.
+constexpr int kDecayThreads = 256;
+__device__ __forceinline__ double decay_term(const AttnDecayParams& p, long long head, long long plane, int t) {
+  double x = 0.0;
+  for (int b = 0; b < p.blocks; ++b)
+    x += (double)p.of[(b * plane + head) * p.S + t] - (double)p.to[(b * plane + head) * p.S + t];
+  return x;
+}
+// Every thread gets the block's sum.
+__device__ __forceinline__ double decay_sum(double x, double* sums) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  __syncthreads();
+  if (threadIdx.x % 32 == 0) sums[threadIdx.x / 32] = x;
+  __syncthreads();
+  x = sums[0];
+  for (int i = 1; i < kDecayThreads / 32; ++i) x += sums[i];
+  return x;
+}
+__global__ void __launch_bounds__(kDecayThreads) attn_decay_kernel(AttnDecayParams p) {
+  __shared__ double sums[kDecayThreads / 32], carry;
+  const int h = (int)(blockIdx.x % p.H), n = (int)(blockIdx.x / p.H);
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int L = row_length(p.lens, n, p.S);
+  const long long head = (long long)n * p.H + h, plane = (long long)p.N * p.H;
+  float* out = static_cast<float*>(p.dDecay.p) + n * p.dDecay.ns + h;
+  const float* g = static_cast<const float*>(p.decay.p) + n * p.decay.ns + h;
+  const float bias = p.bias ? p.bias[h] : 0.0f;
+  double first = 0.0, last = 0.0, all = 0.0;
+  for (int b = 0; b < p.blocks; ++b) {
+    if (p.first) first += p.first[b * plane + head];
+    if (p.last) last += p.last[b * plane + head];
+  }
+  for (int t = threadIdx.x; t < L; t += kDecayThreads) all += decay_term(p, head, plane, t);
+  all = decay_sum(all, sums);
+  const double back = L > 0 ? (last - first - all) / L : 0.0;
+  double run = first, total = 0.0;
+  for (int base = 0; base < L; base += kDecayThreads) {
+    const int t = base + threadIdx.x;
+    const double own = t < L ? decay_term(p, head, plane, t) : 0.0;
+    double x = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const double y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) sums[warp] = x;
+    __syncthreads();
+    for (int i = 0; i < warp; ++i) x += sums[i];
+    x += run;
+    if (threadIdx.x == kDecayThreads - 1) carry = x;
+    if (t < L) {
+      // a decay of 0 has no gradient: the factor itself is in it
+      const float d = (p.decay.p ? g[t * p.decay.ss] : 0.0f) + bias;
+      const double y = d < -104.0f ? 0.0 : x - own + back * t;
+      if (p.dDecay.p) out[t * p.dDecay.ss] = (float)y;
+      total += y;
+    }
+    __syncthreads();
+    run = carry;
+  }
+  if (p.dDecay.p)
+    for (int t = L + threadIdx.x; t < p.S; t += kDecayThreads) out[t * p.dDecay.ss] = 0.0f;
+  if (p.partial) {
+    total = decay_sum(total, sums);
+    if (threadIdx.x == 0) p.partial[head] = total;
+  }
+}
+
+__global__ void __launch_bounds__(256) attn_decay_bias_kernel(AttnDecayParams p) {
+  const int h = blockIdx.x * 8 + threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (h >= p.H) return;
+  double x = 0.0;
+  for (int n = lane; n < p.N; n += 32) x += p.partial[(long long)n * p.H + h];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  if (lane == 0) p.dbias[h] = (float)x;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) attn_share_kernel(AttnShareParams p) {
+  const int width = p.H / p.of * p.V;
+  const long long count = (long long)p.N * p.S * width;
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < count; i += (long long)gridDim.x * 256) {
+    const long long r = i / width;
+    const int c = (int)(i - r * width), head = c / p.V, v = c - head * p.V;
+    const int n = (int)(r / p.S), s = (int)(r - (long long)n * p.S);
+    const float* x = p.o32 + (r * p.H + (long long)head * p.of) * p.V + v;
+    float y = 0.0f;
+    for (int j = 0; j < p.of; ++j) y += x[(long long)j * p.V];
+    static_cast<T*>(p.o.p)[s * p.o.ss + n * p.o.ns + c] = Elem<T>::from_f(y);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_attn(const AttnParams& p, cudaStream_t s, int* launches) {
+  int width = 1;
+  for (int i = 0; i < p.passes; ++i) width = std::max(width, p.pass[i].V);
+  const int blocks = (width + kStepCols - 1) / kStepCols;
+  const unsigned grid = (unsigned)((long long)p.passes * p.N * p.H * blocks);
+  switch (p.dtype) {
+    case RK_F32: attn_step_kernel<float><<<grid, kStepThreads, 0, s>>>(p, blocks); break;
+    case RK_F16: attn_step_kernel<__half><<<grid, kStepThreads, 0, s>>>(p, blocks); break;
+    default: attn_step_kernel<__nv_bfloat16><<<grid, kStepThreads, 0, s>>>(p, blocks);
+  }
+  const cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) ++*launches;
+  return e;
+}
+
+int attn_dot_blocks(int size) { return (size + kStepCols - 1) / kStepCols; }
+
+cudaError_t launch_attn_decay(const AttnDecayParams& p, cudaStream_t s, int* launches) {
+  attn_decay_kernel<<<(unsigned)((long long)p.N * p.H), kDecayThreads, 0, s>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  ++*launches;
+  if (p.dbias == nullptr) return e;
+  attn_decay_bias_kernel<<<(p.H + 7) / 8, 256, 0, s>>>(p);
+  e = cudaGetLastError();
+  if (e == cudaSuccess) ++*launches;
+  return e;
+}
+
+cudaError_t launch_attn_share(const AttnShareParams& p, cudaStream_t s, int* launches) {
+  const long long count = (long long)p.N * p.S * (p.H / p.of) * p.V;
+  const unsigned grid = (unsigned)std::min<long long>((count + 255) / 256, kPlanSms * 32);
+  switch (p.dtype) {
+    case RK_F32: attn_share_kernel<float><<<grid, 256, 0, s>>>(p); break;
+    case RK_F16: attn_share_kernel<__half><<<grid, 256, 0, s>>>(p); break;
+    default: attn_share_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(p);
+  }
+  const cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) ++*launches;
+  return e;
+}
+
+}  // namespace rk

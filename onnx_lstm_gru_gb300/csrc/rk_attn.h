@@ -1,0 +1,99 @@
+// rk_attn.h -- what the host side of the linear attention operators passes to
+// their kernels: operands with element offsets applied, strides in elements,
+// and the launch plans.  Not part of the ABI.
+#pragma once
+
+#include "rk_ssm.h"
+
+namespace rk {
+
+// ---- queries and keys --------------------------------------------------------------
+
+struct QkSide {          // the queries, or the keys
+  RowsArg X, Y, dY, dX;  // a row of `heads` heads
+  const void* scale;
+  float* dscale;
+  int heads;
+};
+struct QkParams {
+  int dtype, norm, interleaved, rotary, size;
+  int piece;             // elements of one access: 16 bytes, 8 or 1 element
+  float epsilon;
+  int S, N;
+  int layout;
+  QkSide side[2];
+  const float* freq;
+  const int* positions;  // by row of the layout
+  const int* lens;
+  float* partial;        // [blocks][2][size]
+  int blocks;            // the gradient's
+  int share;             // warps that share a row's heads
+};
+// Elements of one access that every row, scale and pair allows.
+int qk_piece(int eb, int size, int rotary, int interleaved);
+int qk_grad_blocks(long long rows);
+cudaError_t launch_qk(const QkParams& p, cudaStream_t s);
+cudaError_t launch_qk_grad(const QkParams& p, cudaStream_t s, int* launches);
+
+// ---- attention -----------------------------------------------------------------------
+
+// One linear attention of rows q, k, v to o over the steps, forward or
+// backward in time:
+//   forward:   H = e^g H + su k v^T,  o = so H^T q
+//   backward:  H = H + su k v^T,      o = so H^T q,  then H = e^g H
+// The layer is one forward pass; its gradient is three: dQ is the pass of (dY,
+// V, K), forward, and dV and dK are those of (K, Q, dY) and (V, dY, Q),
+// backward.  H is [K, V], or its transpose as the operand has it.
+struct AttnPass {
+  RowsArg q, k, v, o;
+  int q_of, k_of, v_of, o_of;  // heads that share one of the rows' heads
+  int K, V;                    // elements of q and k; of v and o
+  float su, so;
+  int backward;
+  int v_major;                 // a state's element (k, v) lies at [v][k]
+  const float* first;          // [N][H][..], or null
+  float* last;
+  const float* with;           // a state like `last`: its product with what `last` is goes to cross
+  float* cross;                // [N][H]
+  RowsArg dot_with;            // rows like o's: their products with the unrounded o
+  float* dot;                  // [N][H][S], or null
+  float* o32;                  // [N * S][H][V] in o's place: heads that share are added up from there
+};
+struct AttnParams {
+  int dtype;
+  int S, N, H;
+  RowsArg decay;
+  const float* bias;
+  const int* lens;
+  int passes;
+  AttnPass pass[3];
+};
+cudaError_t launch_attn(const AttnParams& p, cudaStream_t s, int* launches);
+// Planes of `dot` and `cross` that a pass over rows of `size` elements writes.
+int attn_dot_blocks(int size);
+
+// dDecay and d_decay_bias from the products of q and dQ (to) and k and dK (of).
+struct AttnDecayParams {
+  int S, N, H;
+  int blocks;          // planes of `to`, `of`, `first` and `last` that are added up
+  RowsArg decay, dDecay;
+  const float* bias;
+  const int* lens;
+  const float* to;
+  const float* of;
+  const float* first;  // [N][H], or null: the state's product with its gradient before the first step
+  const float* last;   // and behind the last
+  double* partial;     // [N][H]
+  float* dbias;        // [H], or null
+};
+cudaError_t launch_attn_decay(const AttnDecayParams& p, cudaStream_t s, int* launches);
+
+// o = sums over the heads that share of o32.
+struct AttnShareParams {
+  int dtype, S, N, H, V, of;
+  const float* o32;
+  RowsArg o;
+};
+cudaError_t launch_attn_share(const AttnShareParams& p, cudaStream_t s, int* launches);
+
+}  // namespace rk

@@ -1,7 +1,9 @@
-"""The operators of a selective state space layer, on the C ABI of ``include/rk.h``.
+"""The operators of selective state space and linear attention layers, on the C ABI of ``include/rk.h``.
 
 ``StateSpaceLayer`` takes torch CUDA tensors: layer normalisation, the short
-causal convolution and the selective scan, each with its gradient.  The
+causal convolution and the selective scan; queries and keys normalised and
+rotated by head, and attention through a state that decays by head; each with
+its gradient.  The
 formulas, shapes and rules are those the header states; here only arguments
 are checked and packed (by the module that ``binding/state_space_binding.cpp``
 builds: a call's host time is what a single token waits for).  Row operands may be slices of wider rows, some steps
@@ -49,6 +51,20 @@ class rk_scan_problem(ctypes.Structure):
                 ("channels", ctypes.c_int64), ("state", ctypes.c_int64)]
 
 
+class rk_qk_problem(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("layout", ctypes.c_int32), ("norm", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("rotary", ctypes.c_int32), ("epsilon", ctypes.c_float),
+                ("seq", ctypes.c_int64), ("batch", ctypes.c_int64), ("heads", ctypes.c_int64),
+                ("key_heads", ctypes.c_int64), ("size", ctypes.c_int64)]
+
+
+class rk_attn_problem(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("layout", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("query_heads", ctypes.c_int32), ("key_heads", ctypes.c_int32), ("value_heads", ctypes.c_int32),
+                ("seq", ctypes.c_int64), ("batch", ctypes.c_int64), ("heads", ctypes.c_int64),
+                ("key_size", ctypes.c_int64), ("value_size", ctypes.c_int64)]
+
+
 # Operand lists in the C structs' order: row tensors, then the others.
 _OPERANDS = {
     "norm": (("X", "Y"), ("Scale", "B", "Mean", "InvStdDev")),
@@ -61,6 +77,13 @@ _OPERANDS = {
     "scan_grad": (("X", "Delta", "B", "C", "Z", "dY", "dX", "dDelta", "dB", "dC", "dZ"),
                   ("A", "D", "delta_bias", "sequence_lens", "initial_state", "d_final_state", "dA", "dD",
                    "d_delta_bias", "d_initial_state")),
+    "qk": (("Q", "K", "YQ", "YK"), ("QScale", "KScale", "Frequencies", "positions", "sequence_lens")),
+    "qk_grad": (("Q", "K", "dYQ", "dYK", "dQ", "dK"),
+                ("QScale", "KScale", "Frequencies", "positions", "sequence_lens", "dQScale", "dKScale")),
+    "attn": (("Q", "K", "V", "Decay", "Y"), ("decay_bias", "sequence_lens", "initial_state", "final_state")),
+    "attn_grad": (("Q", "K", "V", "Decay", "dY", "dQ", "dK", "dV", "dDecay"),
+                  ("decay_bias", "sequence_lens", "initial_state", "d_final_state", "d_decay_bias",
+                   "d_initial_state")),
 }
 
 
@@ -76,6 +99,10 @@ rk_conv_operands = _operand_struct("conv")
 rk_conv_grad_operands = _operand_struct("conv_grad")
 rk_scan_operands = _operand_struct("scan")
 rk_scan_grad_operands = _operand_struct("scan_grad")
+rk_qk_operands = _operand_struct("qk")
+rk_qk_grad_operands = _operand_struct("qk_grad")
+rk_attn_operands = _operand_struct("attn")
+rk_attn_grad_operands = _operand_struct("attn_grad")
 
 _P = ctypes.c_void_p
 SIGNATURES = {
@@ -83,12 +110,19 @@ SIGNATURES = {
     "rk_conv_grad_scratch_length": (ctypes.c_int64, [_P]),
     "rk_scan_scratch_length": (ctypes.c_int64, [_P]),
     "rk_scan_grad_scratch_length": (ctypes.c_int64, [_P]),
+    "rk_qk_grad_scratch_length": (ctypes.c_int64, [_P]),
+    "rk_attn_scratch_length": (ctypes.c_int64, [_P]),
+    "rk_attn_grad_scratch_length": (ctypes.c_int64, [_P]),
     "rk_norm_encode": (ctypes.c_int32, [_P, _P, _P, _P]),
     "rk_norm_grad_encode": (ctypes.c_int32, [_P, _P, _P, _P, _P]),
     "rk_conv_encode": (ctypes.c_int32, [_P, _P, _P, _P]),
     "rk_conv_grad_encode": (ctypes.c_int32, [_P, _P, _P, _P, _P]),
     "rk_scan_encode": (ctypes.c_int32, [_P, _P, _P, _P, _P]),
     "rk_scan_grad_encode": (ctypes.c_int32, [_P, _P, _P, _P, _P]),
+    "rk_qk_encode": (ctypes.c_int32, [_P, _P, _P, _P]),
+    "rk_qk_grad_encode": (ctypes.c_int32, [_P, _P, _P, _P, _P]),
+    "rk_attn_encode": (ctypes.c_int32, [_P, _P, _P, _P, _P]),
+    "rk_attn_grad_encode": (ctypes.c_int32, [_P, _P, _P, _P, _P]),
 }
 
 
@@ -114,6 +148,18 @@ def rk_scan_grad_scratch_length(problem: rk_scan_problem) -> int:
     return load().rk_scan_grad_scratch_length(_ref(problem))
 
 
+def rk_qk_grad_scratch_length(problem: rk_qk_problem) -> int:
+    return load().rk_qk_grad_scratch_length(_ref(problem))
+
+
+def rk_attn_scratch_length(problem: rk_attn_problem) -> int:
+    return load().rk_attn_scratch_length(_ref(problem))
+
+
+def rk_attn_grad_scratch_length(problem: rk_attn_problem) -> int:
+    return load().rk_attn_grad_scratch_length(_ref(problem))
+
+
 def rk_norm_encode(handle, problem, ops, stream) -> int:
     return load().rk_norm_encode(handle, _ref(problem), _ref(ops), stream)
 
@@ -136,6 +182,22 @@ def rk_scan_encode(handle, problem, ops, scratch, stream) -> int:
 
 def rk_scan_grad_encode(handle, problem, ops, scratch, stream) -> int:
     return load().rk_scan_grad_encode(handle, _ref(problem), _ref(ops), _ref(scratch), stream)
+
+
+def rk_qk_encode(handle, problem, ops, stream) -> int:
+    return load().rk_qk_encode(handle, _ref(problem), _ref(ops), stream)
+
+
+def rk_qk_grad_encode(handle, problem, ops, scratch, stream) -> int:
+    return load().rk_qk_grad_encode(handle, _ref(problem), _ref(ops), _ref(scratch), stream)
+
+
+def rk_attn_encode(handle, problem, ops, scratch, stream) -> int:
+    return load().rk_attn_encode(handle, _ref(problem), _ref(ops), _ref(scratch), stream)
+
+
+def rk_attn_grad_encode(handle, problem, ops, scratch, stream) -> int:
+    return load().rk_attn_grad_encode(handle, _ref(problem), _ref(ops), _ref(scratch), stream)
 
 
 # ---- problem descriptions ----------------------------------------------------------------------
@@ -252,14 +314,96 @@ class ScanProblem(_Problem):
         return names
 
 
+@dataclass(frozen=True)
+class QkProblem(_Problem):
+    """Queries and keys normalised and rotated by head (mirrors rk_qk_problem).  ``key_heads``: as many as ``heads``
+    unless given; ``norm`` is "rms", "l2" or "none"; the first ``rotary`` elements of a head are rotated, in pairs of
+    neighbours where ``interleaved``."""
+    seq: int
+    batch: int
+    heads: int
+    size: int
+    key_heads: int | None = None
+    rotary: int = 0
+    interleaved: bool = False
+    norm: str = "rms"
+    epsilon: float = 1e-6
+    dtype: str = "f32"
+    layout: int = 0
+
+    @property
+    def _key_heads(self):
+        return self.heads if self.key_heads is None else self.key_heads
+
+    def to_c(self) -> rk_qk_problem:
+        return rk_qk_problem(DTYPES[self.dtype], self.layout, {"none": 0, "rms": 1, "l2": 2}[self.norm],
+                             int(self.interleaved), self.rotary, self.epsilon, self.seq, self.batch, self.heads,
+                             self._key_heads, self.size)
+
+    def _operands(self):
+        q = _row_shape(self.layout, self.seq, self.batch, self.heads * self.size)
+        k = _row_shape(self.layout, self.seq, self.batch, self._key_heads * self.size)
+        one = (self.size,)
+        names = {n: (q, "t") for n in ("Q", "YQ", "dYQ", "dQ")}
+        names.update({n: (k, "t") for n in ("K", "YK", "dYK", "dK")})
+        names.update({"QScale": (one, "t"), "KScale": (one, "t"), "dQScale": (one, "f"), "dKScale": (one, "f"),
+                      "Frequencies": ((self.rotary // 2,), "f"),
+                      "positions": (q[:2], "i"), "sequence_lens": ((self.batch,), "i")})
+        return names
+
+
+@dataclass(frozen=True)
+class AttnProblem(_Problem):
+    """Attention through a state that decays by head (mirrors rk_attn_problem).  ``query_heads``, ``key_heads``,
+    ``value_heads``: as many as ``heads`` unless given; ``scale``: 1 / sqrt(key_size) unless given."""
+    seq: int
+    batch: int
+    heads: int
+    key_size: int
+    value_size: int
+    query_heads: int | None = None
+    key_heads: int | None = None
+    value_heads: int | None = None
+    scale: float | None = None
+    dtype: str = "f32"
+    layout: int = 0
+
+    def _shared(self):
+        return [self.heads if n is None else n for n in (self.query_heads, self.key_heads, self.value_heads)]
+
+    def to_c(self) -> rk_attn_problem:
+        scale = self.scale if self.scale is not None else self.key_size ** -0.5 if self.key_size > 0 else 1.0
+        # 0 heads given here are none; in the C structure 0 stands for as many as heads
+        shared = [-1 if n == 0 else n for n in self._shared()]
+        return rk_attn_problem(DTYPES[self.dtype], self.layout, scale, *shared, self.seq, self.batch, self.heads,
+                               self.key_size, self.value_size)
+
+    def _operands(self):
+        def row(heads, size):
+            return _row_shape(self.layout, self.seq, self.batch, heads * size)
+        qh, kh, vh = self._shared()
+        state, one = (self.batch, self.heads, self.key_size, self.value_size), (self.heads,)
+        names = {n: (row(qh, self.key_size), "t") for n in ("Q", "dQ")}
+        names.update({n: (row(kh, self.key_size), "t") for n in ("K", "dK")})
+        names.update({n: (row(vh, self.value_size), "t") for n in ("V", "dV")})
+        names.update({n: (row(self.heads, self.value_size), "t") for n in ("Y", "dY")})
+        names.update({n: (row(self.heads, 1), "f") for n in ("Decay", "dDecay")})
+        names.update({n: (state, "f") for n in ("initial_state", "final_state", "d_initial_state", "d_final_state")})
+        names.update({"decay_bias": (one, "f"), "d_decay_bias": (one, "f"), "sequence_lens": ((self.batch,), "i")})
+        return names
+
+
 _REQUIRED = {
     "norm": ("X",), "norm_grad": ("X", "Mean", "InvStdDev", "dY"), "conv": ("X", "W"), "conv_grad": ("X", "W", "dY"),
     "scan": ("X", "Delta", "A", "B", "C"), "scan_grad": ("X", "Delta", "A", "B", "C", "dY"),
+    "qk": ("Q", "K"), "qk_grad": ("Q", "K", "dYQ", "dYK"), "attn": ("Q", "K", "V"), "attn_grad": ("Q", "K", "V", "dY"),
 }
 _OUTPUTS = {
     "norm": ("Y", "Mean", "InvStdDev"), "norm_grad": ("dX", "dScale", "dB"), "conv": ("Y", "final_state"),
     "conv_grad": ("dX", "dW", "dB", "d_initial_state"), "scan": ("Y", "final_state"),
     "scan_grad": ("dX", "dDelta", "dB", "dC", "dZ", "dA", "dD", "d_delta_bias", "d_initial_state"),
+    "qk": ("YQ", "YK"), "qk_grad": ("dQ", "dK", "dQScale", "dKScale"), "attn": ("Y", "final_state"),
+    "attn_grad": ("dQ", "dK", "dV", "dDecay", "d_decay_bias", "d_initial_state"),
 }
 
 
@@ -337,6 +481,22 @@ class StateSpaceLayer:
                   want=("dX", "dDelta", "dA", "dB", "dC", "dD", "d_delta_bias"), stream=None, **tensors) -> dict:
         """dX, dDelta, dA, dB, dC, dD, d_delta_bias, dZ, d_initial_state from scan's operands, dY and d_final_state."""
         return self._run("scan_grad", ScanProblem, problem, X, want, stream, tensors)
+
+    def qk(self, problem: QkProblem, Q, want=("YQ", "YK"), stream=None, **tensors) -> dict:
+        """YQ, YK from Q, K, QScale, KScale, Frequencies, positions, sequence_lens."""
+        return self._run("qk", QkProblem, problem, Q, want, stream, tensors)
+
+    def qk_grad(self, problem: QkProblem, Q, want=("dQ", "dK", "dQScale", "dKScale"), stream=None, **tensors) -> dict:
+        """dQ, dK, dQScale, dKScale from qk's operands, dYQ and dYK."""
+        return self._run("qk_grad", QkProblem, problem, Q, want, stream, tensors)
+
+    def attn(self, problem: AttnProblem, Q, want=("Y", "final_state"), stream=None, **tensors) -> dict:
+        """Y, final_state from Q, K, V, Decay, decay_bias, sequence_lens, initial_state."""
+        return self._run("attn", AttnProblem, problem, Q, want, stream, tensors)
+
+    def attn_grad(self, problem: AttnProblem, Q, want=("dQ", "dK", "dV"), stream=None, **tensors) -> dict:
+        """dQ, dK, dV, dDecay, d_decay_bias, d_initial_state from attn's operands, dY and d_final_state."""
+        return self._run("attn_grad", AttnProblem, problem, Q, want, stream, tensors)
 
     def _run(self, op, kind, problem, X, want, stream, tensors):
         if type(problem) is not kind:
