@@ -20,6 +20,7 @@
 #include <string>
 
 #include "rk.h"
+#include "rk_attn.h"
 #include "rk_handle.h"
 #include "rk_internal.h"
 
@@ -1111,9 +1112,9 @@ rk_status rk_encode_host(rk_handle* h, const rk_problem* p, const rk_operands* h
 
 rk_status rk_status_poll(rk_handle* h, void* stream_ptr) {
   if (h == nullptr) return RK_ERR_ARG;
-  if (!h->dev_ready && h->noalloc_status == nullptr) return RK_OK;
+  if (!h->dev_ready && h->noalloc_status == nullptr && !h->attn_chunks) return RK_OK;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
-  int v = 0, w = 0;
+  int v = 0, w = 0, a = 0;
   cudaError_t e = cudaStreamSynchronize(stream);
   if (e == cudaSuccess && h->dev_ready) e = cudaMemcpy(&v, h->status, sizeof(int), cudaMemcpyDeviceToHost);
   if (e == cudaSuccess && h->dev_ready) e = cudaMemset(h->status, 0, sizeof(int));
@@ -1121,7 +1122,8 @@ rk_status rk_status_poll(rk_handle* h, void* stream_ptr) {
   if (e == cudaSuccess && h->noalloc_status != nullptr)
     e = cudaMemcpy(&w, h->noalloc_status, sizeof(int), cudaMemcpyDeviceToHost);
   if (e == cudaSuccess && h->noalloc_status != nullptr) e = cudaMemset(h->noalloc_status, 0, sizeof(int));
-  v |= w;
+  if (e == cudaSuccess && h->attn_chunks) e = rk::take_attn_status(stream, &a);
+  v |= w | a;
   if (e != cudaSuccess) {
     h->last_error = std::string("recurrent: status poll: ") + cudaGetErrorName(e);
     return RK_ERR_CUDA;

@@ -14,28 +14,24 @@ namespace {
 constexpr int kStepThreads = 256, kStepRows = 16, kStepCols = 32, kMaxHead = 128;
 constexpr int kGroups = kStepThreads / kStepCols, kStates = kMaxHead / kGroups;
 
-// The recurrence as it stands: a block holds 32 columns of one state, a warp
-// an eighth of their rows, a lane one column of those in registers.  Sixteen
-// steps' rows are fetched together; their outputs are added up over the warps
-// at the end.
+// The recurrence as it stands, forward: a block holds 32 columns of one state,
+// a warp an eighth of their rows, a lane one column of those in registers.
+// Sixteen steps' rows are fetched together; their outputs are added up over
+// the warps at the end.
 template <typename T>
 __global__ void __launch_bounds__(kStepThreads) attn_step_kernel(AttnParams p, int blocks) {
   __shared__ float sq[kStepRows][kMaxHead], sk[kStepRows][kMaxHead], sv[kStepRows][kStepCols], sd[kStepRows];
   __shared__ float part[kStepRows][kGroups][kStepCols];
+  const AttnPass& a = p.pass[0];
   long long id = blockIdx.x;
-  const int vb = (int)(id % blocks);
+  const int v0 = (int)(id % blocks) * kStepCols;
   id /= blocks;
-  const int h = (int)(id % p.H);
-  id /= p.H;
-  const int n = (int)(id % p.N);
-  const AttnPass& a = p.pass[id / p.N];
-  const int v0 = vb * kStepCols;
-  if (v0 >= a.V) return;
+  const int h = (int)(id % p.H), n = (int)(id / p.H);
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int per = (a.K + kGroups - 1) / kGroups, k0 = warp * per, mine = max(min(per, a.K - k0), 0);
   const int v = v0 + lane;
   const long long state = ((long long)n * p.H + h) * a.K * a.V;
-  auto at = [&](int i) { return state + (a.v_major ? (long long)v * a.K + k0 + i : (long long)(k0 + i) * a.V + v); };
+  auto at = [&](int i) { return state + (long long)(k0 + i) * a.V + v; };
   float s[kStates];
 #pragma unroll
   for (int i = 0; i < kStates; ++i) s[i] = a.first && i < mine && v < a.V ? a.first[at(i)] : 0.0f;
@@ -45,27 +41,20 @@ __global__ void __launch_bounds__(kStepThreads) attn_step_kernel(AttnParams p, i
   const T* k = static_cast<const T*>(a.k.p) + n * a.k.ns + (long long)(h / a.k_of) * a.K;
   const T* x = static_cast<const T*>(a.v.p) + n * a.v.ns + (long long)(h / a.v_of) * a.V;
   const float* g = static_cast<const float*>(p.decay.p) + n * p.decay.ns + h;
-  T* o = static_cast<T*>(a.o.p) + n * a.o.ns + (long long)(h / a.o_of) * a.V;
-  const T* w = static_cast<const T*>(a.dot_with.p) + n * a.dot_with.ns + (long long)(h / a.o_of) * a.V;
-  auto put = [&](int t, float y) {
-    if (v >= a.V) return;
-    if (a.o32) a.o32[(((long long)n * p.S + t) * p.H + h) * a.V + v] = y;
-    else if (a.o.p) o[t * a.o.ss + v] = Elem<T>::from_f(y);
-  };
+  T* o = static_cast<T*>(a.o.p) + n * a.o.ns + (long long)h * a.V;
 #pragma unroll 1
   for (int base = 0; base < L; base += kStepRows) {
     const int rows = min(kStepRows, L - base);
-    auto step = [&](int j) { return a.backward ? L - 1 - base - j : base + j; };
     for (int i = threadIdx.x; i < rows * kMaxHead; i += kStepThreads) {
       const int j = i / kMaxHead, c = i % kMaxHead;
-      const long long t = step(j);
+      const long long t = base + j;
       if (c < a.K) sq[j][c] = Elem<T>::to_f(q[t * a.q.ss + c]), sk[j][c] = Elem<T>::to_f(k[t * a.k.ss + c]);
     }
     for (int i = threadIdx.x; i < rows * kStepCols; i += kStepThreads) {
       const int j = i / kStepCols, c = v0 + i % kStepCols;
-      sv[j][i % kStepCols] = c < a.V ? a.su * Elem<T>::to_f(x[step(j) * a.v.ss + c]) : 0.0f;
+      sv[j][i % kStepCols] = c < a.V ? a.su * Elem<T>::to_f(x[(base + j) * a.v.ss + c]) : 0.0f;
     }
-    if (threadIdx.x < rows) sd[threadIdx.x] = expf((p.decay.p ? g[step(threadIdx.x) * p.decay.ss] : 0.0f) + bias);
+    if (threadIdx.x < rows) sd[threadIdx.x] = expf((p.decay.p ? g[(base + threadIdx.x) * p.decay.ss] : 0.0f) + bias);
     __syncthreads();
 #pragma unroll 1
     for (int j = 0; j < rows; ++j) {
@@ -74,9 +63,8 @@ __global__ void __launch_bounds__(kStepThreads) attn_step_kernel(AttnParams p, i
 #pragma unroll
       for (int i = 0; i < kStates; ++i) {
         if (i < mine) {
-          s[i] = fmaf(sk[j][k0 + i], c, a.backward ? s[i] : d * s[i]);
+          s[i] = fmaf(sk[j][k0 + i], c, d * s[i]);
           y = fmaf(sq[j][k0 + i], s[i], y);
-          if (a.backward) s[i] *= d;
         }
       }
       part[j][warp][lane] = y;
@@ -86,35 +74,16 @@ __global__ void __launch_bounds__(kStepThreads) attn_step_kernel(AttnParams p, i
       float y = 0.0f;
 #pragma unroll
       for (int i = 0; i < kGroups; ++i) y += part[j][i][lane];
-      y *= a.so;
-      const int t = step(j);
-      put(t, y);
-      if (a.dot) {
-        const float d = warp_sum(v < a.V ? y * Elem<T>::to_f(w[t * a.dot_with.ss + v]) : 0.0f);
-        if (lane == 0) a.dot[(((long long)vb * p.N + n) * p.H + h) * p.S + t] = d;
-      }
+      if (a.o.p && v < a.V) o[(base + j) * a.o.ss + v] = Elem<T>::from_f(a.so * y);
     }
-    // no wait: the next rows are read after the first barrier, `part` is written after the second
+    // no wait: the next rows are read after the first barrier, `part` is written after it
   }
-  for (int t = L + warp; t < p.S; t += kGroups) put(t, 0.0f);
-  float with = 0.0f;
+  if (a.o.p && v < a.V)
+    for (int t = L + warp; t < p.S; t += kGroups) o[t * a.o.ss + v] = Elem<T>::from_f(0.0f);
+  if (a.last) {
 #pragma unroll
-  for (int i = 0; i < kStates; ++i) {
-    if (i < mine && v < a.V) {
-      if (a.last) a.last[at(i)] = s[i];
-      if (a.with) with = fmaf(a.with[at(i)], s[i], with);
-    }
-  }
-  if (a.cross) {
-    __shared__ float sums[kGroups];
-    with = warp_sum(with);
-    if (lane == 0) sums[warp] = with;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      float y = 0.0f;
-      for (int i = 0; i < kGroups; ++i) y += sums[i];
-      a.cross[((long long)vb * p.N + n) * p.H + h] = y;
-    }
+    for (int i = 0; i < kStates; ++i)
+      if (i < mine && v < a.V) a.last[at(i)] = s[i];
   }
 }
 
@@ -126,11 +95,8 @@ __global__ void __launch_bounds__(kStepThreads) attn_step_kernel(AttnParams p, i
 // products leave at the end is known, E_L, and is taken back evenly along the
 // way: with no states to start from or to end at, both ends are exact.
 constexpr int kDecayThreads = 256;
-__device__ __forceinline__ double decay_term(const AttnDecayParams& p, long long head, long long plane, int t) {
-  double x = 0.0;
-  for (int b = 0; b < p.blocks; ++b)
-    x += (double)p.of[(b * plane + head) * p.S + t] - (double)p.to[(b * plane + head) * p.S + t];
-  return x;
+__device__ __forceinline__ double decay_term(const AttnDecayParams& p, long long head, int t) {
+  return (double)p.of[head * p.S + t] - (double)p.to[head * p.S + t];
 }
 // Every thread gets the block's sum.
 __device__ __forceinline__ double decay_sum(double x, double* sums) {
@@ -148,22 +114,19 @@ __global__ void __launch_bounds__(kDecayThreads) attn_decay_kernel(AttnDecayPara
   const int h = (int)(blockIdx.x % p.H), n = (int)(blockIdx.x / p.H);
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int L = row_length(p.lens, n, p.S);
-  const long long head = (long long)n * p.H + h, plane = (long long)p.N * p.H;
+  const long long head = (long long)n * p.H + h;
   float* out = static_cast<float*>(p.dDecay.p) + n * p.dDecay.ns + h;
   const float* g = static_cast<const float*>(p.decay.p) + n * p.decay.ns + h;
   const float bias = p.bias ? p.bias[h] : 0.0f;
-  double first = 0.0, last = 0.0, all = 0.0;
-  for (int b = 0; b < p.blocks; ++b) {
-    if (p.first) first += p.first[b * plane + head];
-    if (p.last) last += p.last[b * plane + head];
-  }
-  for (int t = threadIdx.x; t < L; t += kDecayThreads) all += decay_term(p, head, plane, t);
+  const double first = p.first ? p.first[head] : 0.0, last = p.last ? p.last[head] : 0.0;
+  double all = 0.0;
+  for (int t = threadIdx.x; t < L; t += kDecayThreads) all += decay_term(p, head, t);
   all = decay_sum(all, sums);
   const double back = L > 0 ? (last - first - all) / L : 0.0;
   double run = first, total = 0.0;
   for (int base = 0; base < L; base += kDecayThreads) {
     const int t = base + threadIdx.x;
-    const double own = t < L ? decay_term(p, head, plane, t) : 0.0;
+    const double own = t < L ? decay_term(p, head, t) : 0.0;
     double x = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -221,11 +184,9 @@ __global__ void __launch_bounds__(256) attn_share_kernel(AttnShareParams p) {
 
 }  // namespace
 
-cudaError_t launch_attn(const AttnParams& p, cudaStream_t s, int* launches) {
-  int width = 1;
-  for (int i = 0; i < p.passes; ++i) width = std::max(width, p.pass[i].V);
-  const int blocks = (width + kStepCols - 1) / kStepCols;
-  const unsigned grid = (unsigned)((long long)p.passes * p.N * p.H * blocks);
+cudaError_t launch_attn_steps(const AttnParams& p, cudaStream_t s, int* launches) {
+  const int blocks = (p.pass[0].V + kStepCols - 1) / kStepCols;
+  const unsigned grid = (unsigned)((long long)p.N * p.H * blocks);
   switch (p.dtype) {
     case RK_F32: attn_step_kernel<float><<<grid, kStepThreads, 0, s>>>(p, blocks); break;
     case RK_F16: attn_step_kernel<__half><<<grid, kStepThreads, 0, s>>>(p, blocks); break;
@@ -236,7 +197,53 @@ cudaError_t launch_attn(const AttnParams& p, cudaStream_t s, int* launches) {
   return e;
 }
 
-int attn_dot_blocks(int size) { return (size + kStepCols - 1) / kStepCols; }
+cudaError_t launch_attn_chunks(const AttnParams& p, cudaStream_t s, int* launches) {
+  switch (p.dtype) {
+    case RK_F32: return launch_attn_chunks_f32(p, s, launches);
+    case RK_F16: return launch_attn_chunks_f16(p, s, launches);
+    default: return launch_attn_chunks_bf16(p, s, launches);
+  }
+}
+
+cudaError_t take_attn_status(cudaStream_t s, int* to) {
+  int one = 0;
+  *to = 0;
+  for (auto take : {take_attn_status_f32, take_attn_status_f16, take_attn_status_bf16}) {
+    const cudaError_t e = take(s, &one);
+    if (e != cudaSuccess) return e;
+    *to |= one;
+  }
+  return cudaSuccess;
+}
+
+namespace {
+// States that run side by side: two heads of at most 64 elements share a block.
+long long streams_of(long long batch, long long heads, int key_size, int value_size, int passes) {
+  const int together = key_size <= 64 && value_size <= 64 ? 2 : 1;
+  return passes * batch * ((heads + together - 1) / together);
+}
+}  // namespace
+
+AttnPlan attn_plan(long long seq, long long batch, long long heads, int key_size, int value_size, int passes) {
+  AttnPlan plan{};
+  const long long streams = streams_of(batch, heads, key_size, value_size, passes);
+  const long long chunks = (seq + 63) / 64;
+  // pieces of two chunks at least, and as many as fit the card together
+  long long segments = streams > 0 ? std::min(kPlanSms / streams, chunks / 2) : 1;
+  segments = std::max<long long>(segments, 1);
+  plan.per = (int)((chunks + segments - 1) / segments);
+  plan.segments = plan.per > 0 ? (int)((chunks + plan.per - 1) / plan.per) : 1;
+  // a gradient's passes contract over keys or values
+  plan.deep = std::max(key_size, passes > 1 ? value_size : 0) > 64 ? 128 : 64;
+  return plan;
+}
+
+long long attn_plan_scratch(const AttnPlan& plan, long long batch, long long heads, int key_size, int value_size,
+                            int passes) {
+  if (plan.segments <= 1) return 0;
+  const long long streams = streams_of(batch, heads, key_size, value_size, passes);
+  return streams * plan.segments * (plan.deep * 128LL + 4);
+}
 
 cudaError_t launch_attn_decay(const AttnDecayParams& p, cudaStream_t s, int* launches) {
   attn_decay_kernel<<<(unsigned)((long long)p.N * p.H), kDecayThreads, 0, s>>>(p);

@@ -59,6 +59,15 @@ struct AttnPass {
   float* dot;                  // [N][H][S], or null
   float* o32;                  // [N * S][H][V] in o's place: heads that share are added up from there
 };
+// How a call's sequences are cut: pieces that run side by side where there are
+// too few states to fill the card, and what each adds to the state.
+struct AttnPlan {
+  int segments, per;  // pieces of a sequence, and the chunks of 64 steps in each
+  int deep;           // elements that a kernel's states have along q and k: 64 or 128
+  int vec;            // rows take 16-byte pieces
+  float* states;      // [streams][segments][deep][128]
+  double* left;       // [streams][segments][2]: logarithms (base 2) of what a piece leaves of its first state
+};
 struct AttnParams {
   int dtype;
   int S, N, H;
@@ -67,15 +76,30 @@ struct AttnParams {
   const int* lens;
   int passes;
   AttnPass pass[3];
+  AttnPlan plan;
 };
-cudaError_t launch_attn(const AttnParams& p, cudaStream_t s, int* launches);
-// Planes of `dot` and `cross` that a pass over rows of `size` elements writes.
-int attn_dot_blocks(int size);
+// The longest sequences that run step by step.
+constexpr int kAttnSteps = 16;
+// The plan of `passes` passes, its pointers left out; and the floats of its scratch.
+AttnPlan attn_plan(long long seq, long long batch, long long heads, int key_size, int value_size, int passes);
+long long attn_plan_scratch(const AttnPlan& plan, long long batch, long long heads, int key_size, int value_size,
+                            int passes);
+// Step by step: one forward pass.
+cudaError_t launch_attn_steps(const AttnParams& p, cudaStream_t s, int* launches);
+// In chunks.
+cudaError_t launch_attn_chunks(const AttnParams& p, cudaStream_t s, int* launches);
+cudaError_t launch_attn_chunks_f32(const AttnParams& p, cudaStream_t s, int* launches);
+cudaError_t launch_attn_chunks_f16(const AttnParams& p, cudaStream_t s, int* launches);
+cudaError_t launch_attn_chunks_bf16(const AttnParams& p, cudaStream_t s, int* launches);
+// Whether a wait of theirs has failed on the current device; cleared.
+cudaError_t take_attn_status(cudaStream_t s, int* to);
+cudaError_t take_attn_status_f32(cudaStream_t s, int* to);
+cudaError_t take_attn_status_f16(cudaStream_t s, int* to);
+cudaError_t take_attn_status_bf16(cudaStream_t s, int* to);
 
 // dDecay and d_decay_bias from the products of q and dQ (to) and k and dK (of).
 struct AttnDecayParams {
   int S, N, H;
-  int blocks;          // planes of `to`, `of`, `first` and `last` that are added up
   RowsArg decay, dDecay;
   const float* bias;
   const int* lens;

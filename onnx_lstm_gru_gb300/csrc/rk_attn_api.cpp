@@ -116,20 +116,33 @@ RowsArg decay_rows(Call& c, const char* name, const rk_rows& t, const rk_attn_pr
 // What a gradient needs: its passes' products for the decays, and float32
 // outputs where heads share.
 struct GradPlan {
-  int64_t to, of, cross, partial, q32, k32, v32;
-  int64_t total() const { return to + of + cross + partial + q32 + k32 + v32; }
+  int64_t to, of, cross, partial, q32, k32, v32, chunks;
+  int64_t total() const { return to + of + cross + partial + q32 + k32 + v32 + chunks; }
 };
+rk::AttnPlan plan_of(const rk_attn_problem* p, int passes) {
+  return rk::attn_plan(p->seq, p->batch, p->heads, (int)p->key_size, (int)p->value_size, passes);
+}
+int64_t plan_scratch(const rk_attn_problem* p, int passes) {
+  if (p->seq * p->batch == 0 || (passes == 1 && p->seq <= rk::kAttnSteps)) return 0;
+  return rk::attn_plan_scratch(plan_of(p, passes), p->batch, p->heads, (int)p->key_size, (int)p->value_size, passes);
+}
+// Its regions, from w on.
+void place(rk::AttnPlan& plan, float* w, int64_t floats) {
+  const int64_t state = plan.deep * 128;
+  plan.states = w;
+  plan.left = reinterpret_cast<double*>(w + floats / (state + 4) * state);
+}
 int64_t four(int64_t x) { return (x + 3) / 4 * 4; }
 GradPlan grad_plan(const rk_attn_problem* p) {
   const int64_t heads = p->batch * p->heads, rows = heads * p->seq;
-  const int64_t blocks = rk::attn_dot_blocks((int)p->key_size);
   GradPlan g{};
-  g.to = g.of = four(blocks * rows);
-  g.cross = four(2 * blocks * heads);
+  g.to = g.of = four(rows);
+  g.cross = four(2 * heads);
   g.partial = four(2 * heads);
   if (shared(p->heads, p->query_heads) > 1) g.q32 = four(rows * p->key_size);
   if (shared(p->heads, p->key_heads) > 1) g.k32 = four(rows * p->key_size);
   if (shared(p->heads, p->value_heads) > 1) g.v32 = four(rows * p->value_size);
+  g.chunks = plan_scratch(p, 3);
   return g;
 }
 
@@ -146,7 +159,7 @@ int64_t rk_qk_grad_scratch_length(const rk_qk_problem* p) {
 int64_t rk_attn_scratch_length(const rk_attn_problem* p) {
   Call c = begin(nullptr, "LinearAttention", p, nullptr, false);
   if (c.ok()) check(c, p);
-  return c.ok() ? 0 : -1;
+  return c.ok() ? plan_scratch(p, 1) : -1;
 }
 
 int64_t rk_attn_grad_scratch_length(const rk_attn_problem* p) {
@@ -229,7 +242,16 @@ rk_status rk_attn_encode(rk_handle* h, const rk_attn_problem* p, const rk_attn_o
     return c.st;
   }
   int launches = 0;
-  c.cuda("launch", rk::launch_attn(ap, s, &launches));
+  if (p->seq <= rk::kAttnSteps) {
+    c.cuda("launch", rk::launch_attn_steps(ap, s, &launches));
+  } else {
+    ap.plan = plan_of(p, 1);
+    const int64_t need = plan_scratch(p, 1);
+    place(ap.plan, c.scratch(scratch, need, s), need);
+    ap.plan.vec = a.q.vec && a.k.vec && a.v.vec;
+    if (c.ok()) h->attn_chunks = true;
+    if (c.ok()) c.cuda("launch", rk::launch_attn_chunks(ap, s, &launches));
+  }
   h->launches += launches;
   return c.st;
 }
@@ -271,7 +293,6 @@ rk_status rk_attn_grad_encode(rk_handle* h, const rk_attn_problem* p, const rk_a
   float* w = c.scratch(scratch, g.total(), s);
   if (!c.ok()) return c.st;
   const bool decays = dDecay.p || dbias;
-  const int blocks = rk::attn_dot_blocks(dk);
   float *to = w, *of = to + g.to, *cross = of + g.of, *partial = cross + g.cross;
   float *q32 = partial + g.partial, *k32 = q32 + g.q32, *v32 = k32 + g.k32;
 
@@ -284,7 +305,7 @@ rk_status rk_attn_grad_encode(rk_handle* h, const rk_attn_problem* p, const rk_a
     a.K = dv, a.V = dk, a.su = 1.0f, a.so = p->scale, a.v_major = 1;
     a.first = first;
     if (decays) a.dot = to, a.dot_with = Q;
-    if (decays && dlast) a.with = dlast, a.cross = cross + blocks * heads;
+    if (decays && dlast) a.with = dlast, a.cross = cross + heads;
     if (q_of > 1 && dQ.p) a.o32 = q32;
   }
   // dV: dY, written by the queries and read by the keys, backward
@@ -308,13 +329,19 @@ rk_status rk_attn_grad_encode(rk_handle* h, const rk_attn_problem* p, const rk_a
     if (k_of > 1 && dK.p) a.o32 = k32;
   }
   int launches = 0;
-  if (ap.passes) c.cuda("launch", rk::launch_attn(ap, s, &launches));
+  if (ap.passes) {
+    ap.plan = plan_of(p, 3);
+    place(ap.plan, v32 + g.v32, g.chunks);
+    ap.plan.vec = Q.vec && K.vec && V.vec && dY.vec;
+    h->attn_chunks = true;
+    c.cuda("launch", rk::launch_attn_chunks(ap, s, &launches));
+  }
   if (c.ok() && decays) {
     rk::AttnDecayParams d{};
-    d.S = ap.S, d.N = ap.N, d.H = H, d.blocks = blocks, d.lens = ap.lens;
+    d.S = ap.S, d.N = ap.N, d.H = H, d.lens = ap.lens;
     d.decay = ap.decay, d.bias = ap.bias, d.dDecay = dDecay;
     d.to = to, d.of = of, d.dbias = dbias;
-    d.first = first ? cross : nullptr, d.last = dlast ? cross + blocks * heads : nullptr;
+    d.first = first ? cross : nullptr, d.last = dlast ? cross + heads : nullptr;
     d.partial = dbias ? reinterpret_cast<double*>(partial) : nullptr;
     c.cuda("launch", rk::launch_attn_decay(d, s, &launches));
   }

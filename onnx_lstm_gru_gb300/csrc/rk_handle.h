@@ -32,6 +32,7 @@ struct rk_handle {
   // scratch of the state space operators (scan chunks, gradients' partial sums)
   float* work = nullptr;
   size_t work_cap = 0;
+  bool attn_chunks = false;  // an attention of this handle has waited on the device
   unsigned char* host_arena = nullptr;  // device buffers for rk_encode_host
   size_t host_arena_cap = 0;
   bool profiling = false;
