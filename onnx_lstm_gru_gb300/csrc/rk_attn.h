@@ -74,6 +74,7 @@ struct AttnParams {
   RowsArg decay;
   const float* bias;
   const int* lens;
+  int gradient;  // its passes, rather than the one forward pass
   int passes;
   AttnPass pass[3];
   AttnPlan plan;

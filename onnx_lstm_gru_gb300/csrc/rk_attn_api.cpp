@@ -267,7 +267,7 @@ rk_status rk_attn_grad_encode(rk_handle* h, const rk_attn_problem* p, const rk_a
   const int dk = (int)p->key_size, dv = (int)p->value_size, H = (int)p->heads;
   const int q_of = shared(H, p->query_heads), k_of = shared(H, p->key_heads), v_of = shared(H, p->value_heads);
   rk::AttnParams ap{};
-  ap.dtype = p->dtype, ap.S = (int)p->seq, ap.N = (int)p->batch, ap.H = H;
+  ap.dtype = p->dtype, ap.S = (int)p->seq, ap.N = (int)p->batch, ap.H = H, ap.gradient = 1;
   const RowsArg Q = c.steps("Q", o->Q, p, (int64_t)(H / q_of) * dk, dk, true);
   const RowsArg K = c.steps("K", o->K, p, (int64_t)(H / k_of) * dk, dk, true);
   const RowsArg V = c.steps("V", o->V, p, (int64_t)(H / v_of) * dv, dv, true);

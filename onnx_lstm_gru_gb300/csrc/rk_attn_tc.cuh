@@ -44,9 +44,10 @@ namespace atc {
 
 using namespace ptc;
 
-constexpr int kChunk = 64, kThreads = 256, kTerms = 3;
+constexpr int kChunk = 64, kThreads = 512, kTerms = 3;
 constexpr uint32_t kSub = kChunk * 128;      // bytes of 64 rows of 64 elements
 constexpr uint32_t kTile = 2 * kSub;         // an operand's term: 64 rows of 128 elements, or of two heads of 64
+constexpr int kCols = kChunk / 4;            // of a chunk's columns of S and O, those of a thread
 constexpr long long kWaitNs = 2000000000LL;  // a wait that takes this long has failed
 
 template <typename T>
@@ -54,9 +55,9 @@ constexpr int kSplit = sizeof(T) == 4 ? 3 : 2;
 template <>
 constexpr int kSplit<__nv_bfloat16> = 1;
 
-// Shared memory: operand tiles (bfloat16: two stages), ck K, P (float32: where
-// K was), and small arrays.
-template <typename T, int HPC>
+// Shared memory: operand tiles (bfloat16: two stages), ck K, P in NT terms
+// (float32: where K was), and small arrays.
+template <typename T, int HPC, int NT>
 struct Layout {
   static constexpr int kIn = kSplit<T>;
   static constexpr int kStages = kIn == 1 ? 2 : 1;
@@ -65,24 +66,25 @@ struct Layout {
   static constexpr bool kOver = kIn == 3;
   static constexpr uint32_t kP = kOver ? kK : kScaled + kTerms * kTile;
   static constexpr uint32_t kPTerm = HPC * kSub;
-  static constexpr uint32_t kEnd = kScaled + kTerms * kTile + (kOver ? 0 : kTerms * kPTerm);
-  static_assert(kTerms * kPTerm <= kIn * kTile || !kOver, "P fits over K");
+  static constexpr uint32_t kEnd = kScaled + kTerms * kTile + (kOver ? 0 : NT * kPTerm);
+  static_assert(NT * kPTerm <= kIn * kTile || !kOver, "P fits over K");
   static constexpr size_t kBytes = kEnd + 1024;  // alignment
 };
 
 // Decays of a chunk, by head of the block.
 struct Decays {
-  float hi[kChunk], lo[kChunk];  // signed G: whole part and fraction
-  float cq[kChunk], ck[kChunk];  // 2^.. of the state's part of a step's output, and of its part of the state
-  float d[kChunk];               // a step's own decay
-  double log2;                   // of the chunk's whole decay
-  float total;                   // the decay
+  float hi[kChunk], lo[kChunk];    // signed G: whole part and fraction
+  float nhi[kChunk], nlo[kChunk];  // their negatives
+  float cq[kChunk], ck[kChunk];    // so 2^.. of the state's part of a step's output, su 2^.. of a step's part of the state
+  float d[kChunk];                 // a step's own decay
+  double log2;                     // of the chunk's whole decay
+  float total;                     // the decay
 };
 
 struct Small {
-  Decays decays[2][2];
-  float dots[8][32];
-  float part[2][128];
+  __align__(16) Decays decays[2][2];
+  float dots[16][kCols];
+  float part[4][128];
   uint64_t bars[4];
   uint32_t tmem;
   int wrong[2];
@@ -90,31 +92,60 @@ struct Small {
 };
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) { return Elem<__nv_bfloat16>::pair_from_f(lo, hi); }
-__device__ __forceinline__ float low_of(uint32_t u) { return __uint_as_float(u << 16); }
-__device__ __forceinline__ float high_of(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+__device__ __forceinline__ F2 pair_of(uint32_t u) { return f2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)); }
 
 // Two factors as N terms each; the first terms' product with 0 goes to
 // `finite`, which they leave 0 unless one of them is infinite or NaN.
 template <int N>
-__device__ __forceinline__ void split(float a, float b, uint32_t (&t)[N], float& finite) {
-  t[0] = pack2(a, b);
-  finite = fmaf(low_of(t[0]), 0.0f, fmaf(high_of(t[0]), 0.0f, finite));
+__device__ __forceinline__ void split(F2 x, uint32_t (&t)[N], F2& finite) {
+  float2 v = f2_get(x);
+  t[0] = pack2(v.x, v.y);
+  F2 h = pair_of(t[0]);
+  finite = fma2(h, f2(0.0f, 0.0f), finite);
 #pragma unroll
   for (int i = 1; i < N; ++i) {
-    a -= low_of(t[i - 1]), b -= high_of(t[i - 1]);
-    t[i] = pack2(a, b);
+    x = fma2(h, f2(-1.0f, -1.0f), x);
+    v = f2_get(x);
+    t[i] = pack2(v.x, v.y);
+    if (i + 1 < N) h = pair_of(t[i]);
   }
 }
+__device__ __forceinline__ bool is_finite(F2 finite) {
+  const float2 v = f2_get(finite);
+  return v.x == 0.0f && v.y == 0.0f;
+}
 
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16};" ::"r"(addr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t* r) {
+  static_assert(N == 8 || N == 16, "columns");
+  if constexpr (N == 8) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+  } else {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+  }
 }
 __device__ __forceinline__ void tmem_st_done() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// 16 columns; complete after tmem_ld_done, which the values pass through.
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&x)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(r[i]);
+}
 
 // A in tensor memory.
 __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
@@ -129,7 +160,7 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t bdesc
 // matrix dimension are a row's 128 bytes, the next 64 lie a sub-tile on, eight
 // steps of the inner one are 1024 bytes.
 __device__ __forceinline__ uint64_t desc_mn(uint32_t addr) {
-  return smem_desc_sw128(addr) & ~((uint64_t)0x3FFF << 16) | ((uint64_t)(kSub >> 4) << 16);
+  return (smem_desc_sw128(addr) & ~((uint64_t)0x3FFF << 16)) | ((uint64_t)(kSub >> 4) << 16);
 }
 
 constexpr uint32_t kRowsA = 1u << 15, kRowsB = 1u << 16;  // operand read along its rows
@@ -174,8 +205,9 @@ __device__ __forceinline__ float pow2_of(long long g) {
 }
 
 // One warp: the decays of the chunk that starts at t0, L the row's length.
-__device__ __forceinline__ void chunk_decays(const AttnParams& p, bool backward, int n, int h, int t0, int L,
+__device__ __forceinline__ void chunk_decays(const AttnParams& p, const AttnPass& a, int n, int h, int t0, int L,
                                              Decays& out, int* wrong) {
+  const bool backward = a.backward;
   const int lane = threadIdx.x % 32;
   const float* g = static_cast<const float*>(p.decay.p) + n * p.decay.ns + h;
   const float bias = p.bias ? p.bias[h] : 0.0f;
@@ -201,12 +233,13 @@ __device__ __forceinline__ void chunk_decays(const AttnParams& p, bool backward,
   for (int j = 0; j < 2; ++j) {
     const long long G = j ? sum : sum - fix[1], s = backward ? -G : G;
     const int i = 2 * lane + j;
-    out.hi[i] = (float)(int)(s >> 32);
-    out.lo[i] = (float)((uint32_t)s >> 8) * 5.9604644775390625e-8f;
+    const float hi = (float)(int)(s >> 32), lo = (float)((uint32_t)s >> 8) * 5.9604644775390625e-8f;
+    out.hi[i] = hi, out.lo[i] = lo;
+    out.nhi[i] = -hi, out.nlo[i] = -lo;
     if (G >> 32 > 120 || (total - G) >> 32 > 120) *wrong = 1;
     const float up = pow2_of(G), down = pow2_of(total - G);
-    out.cq[i] = backward ? down : up;
-    out.ck[i] = backward ? up : down;
+    out.cq[i] = a.so * (backward ? down : up);
+    out.ck[i] = a.su * (backward ? up : down);
   }
   if (lane == 0) out.total = pow2_of(total), out.log2 = (double)total * 2.3283064365386962890625e-10;
 }
@@ -217,57 +250,67 @@ __device__ __forceinline__ const T* head_rows(const RowsArg& a, int n, int h, in
   return static_cast<const T*>(a.p) + n * a.ns + (long long)(h / of) * size;
 }
 
-// Fetches 64 rows of an operand into its tile: sub-tile b is the elements
-// from 64 b on, or head b.  Steps from L on, elements from `size` on and heads
-// that there are not are zeros.
-template <typename T, int HPC, int KB>
-__device__ __forceinline__ void load_tile(unsigned char* tile, const RowsArg& a, int n, int h0, int heads, int of, int size,
-                                          int t0, int L, int vec) {
-  constexpr int kIn = kSplit<T>;
-  constexpr int kPieces = HPC == 2 ? 2 : KB;
+// A thread's part of an operand's tiles: one piece of 8 elements of a row of
+// each of the two sub-tiles, which are the elements from 0 and 64 on, or two
+// heads.
+template <typename T, int HPC>
+struct Rows {
+  const T* src;       // the thread's first step's piece of sub-tile 0
+  long long next, ss; // to sub-tile 1; to the next step
+  int size, heads;    // elements of a head; heads that there are from the block's first on
+  __device__ __forceinline__ Rows(const RowsArg& a, int n, int h0, int H, int of, int size_)
+      : ss(a.ss), size(size_), heads(H - h0) {
+    src = head_rows<T>(a, n, h0, of, size) + (threadIdx.x / 8) * a.ss + 8 * (threadIdx.x % 8);
+    next = HPC == 1 ? 64 : (long long)(min(h0 + 1, H - 1) / of - h0 / of) * size;
+  }
+  // Fetches the 64 rows from t0 on into the tile at `tile`.  Steps from L on,
+  // elements from `size` on and heads that there are not are zeros.
+  template <int SUBS>
+  __device__ __forceinline__ void load(unsigned char* tile, int t0, int L, int vec) const {
+    constexpr int kIn = kSplit<T>;
+    const int r = threadIdx.x / 8, c = threadIdx.x % 8;
+    const T* at = src + t0 * ss;
+    unsigned char* to = tile + r * 128 + ((c ^ (r & 7)) << 4);
 #pragma unroll
-  for (int b = 0; b < kPieces; ++b) {
-    const int h = HPC == 2 ? h0 + b : h0, first = HPC == 2 ? 0 : 64 * b;
-    const T* rows = head_rows<T>(a, n, min(h, heads - 1), of, size) + first;
-#pragma unroll
-    for (int r0 = 0; r0 < kChunk; r0 += kThreads / 8) {
-      const int r = r0 + threadIdx.x / 8, c = threadIdx.x % 8, t = t0 + r;
-      const bool on = t < L && h < heads;
-      const T* src = rows + (long long)t * a.ss + 8 * c;
-      unsigned char* dst = tile + b * kSub + r * 128 + ((c ^ (r & 7)) << 4);
+    for (int b = 0; b < SUBS; ++b) {
+      const int first = (HPC == 2 ? 0 : 64 * b) + 8 * c;
+      const bool on = t0 + r < L && (HPC == 1 || b < heads);
+      unsigned char* dst = to + b * kSub;
+      const T* from = at + b * next;
       if constexpr (kIn == 1) {
         if (vec) {
-          const bool fetch = on && first + 8 * c < size;
-          cp16(su32(dst), fetch ? src : static_cast<const T*>(a.p), fetch);
+          const bool fetch = on && first < size;
+          cp16(su32(dst), fetch ? from : src, fetch);
           continue;
         }
       }
       float x[8];
+      fill(x, 0.0f);
       if (vec) {
-        if (on && first + 8 * c < size) {
+        if (on && first < size) {
           if constexpr (sizeof(T) == 4) {
             float y[4];
-            Piece<T, 4>::load(src, y);
+            Piece<T, 4>::load(from, y);
             x[0] = y[0], x[1] = y[1], x[2] = y[2], x[3] = y[3];
-            if (first + 8 * c + 4 < size) Piece<T, 4>::load(src + 4, y);
-            else fill(y, 0.0f);
-            x[4] = y[0], x[5] = y[1], x[6] = y[2], x[7] = y[3];
+            if (first + 4 < size) {
+              Piece<T, 4>::load(from + 4, y);
+              x[4] = y[0], x[5] = y[1], x[6] = y[2], x[7] = y[3];
+            }
           } else {
-            Piece<T, 8>::load(src, x);
+            Piece<T, 8>::load(from, x);
           }
-        } else {
-          fill(x, 0.0f);
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = on && first + 8 * c + i < size ? Elem<T>::to_f(src[i]) : 0.0f;
+        for (int i = 0; i < 8; ++i)
+          if (on && first + i < size) x[i] = Elem<T>::to_f(from[i]);
       }
       uint32_t w[kIn][4];
-      float unused = 0.0f;
+      F2 unused = f2(0.0f, 0.0f);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         uint32_t s[kIn];
-        split<kIn>(x[2 * i], x[2 * i + 1], s, unused);
+        split<kIn>(f2(x[2 * i], x[2 * i + 1]), s, unused);
 #pragma unroll
         for (int j = 0; j < kIn; ++j) w[j][i] = s[j];
       }
@@ -275,68 +318,70 @@ __device__ __forceinline__ void load_tile(unsigned char* tile, const RowsArg& a,
       for (int j = 0; j < kIn; ++j) *reinterpret_cast<uint4*>(dst + j * kTile) = make_uint4(w[j][0], w[j][1], w[j][2], w[j][3]);
     }
   }
-}
+  // Has the rows from t0 on brought into L2.
+  __device__ __forceinline__ void prefetch(int t0, int L) const {
+    if (t0 + (int)(threadIdx.x / 8) >= L) return;
+    const T* at = src + t0 * ss;
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+      if ((HPC == 1 ? 64 * b + 8 * (int)(threadIdx.x % 8) < size : b < heads && 8 * (int)(threadIdx.x % 8) < size))
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(at + b * next));
+  }
+};
 
-// ck K as three terms, and whether all of K and V is finite.
-template <typename T, int HPC, int KB>
-__device__ __forceinline__ void scale_tile(const unsigned char* k, unsigned char* out, const Decays* d, float& finite) {
+// ck K as three terms, of the tile's SUBS sub-tiles, by THREADS threads.
+template <typename T, int HPC, int SUBS, int THREADS>
+__device__ __forceinline__ void scale_tile(const unsigned char* k, unsigned char* out, const Decays* d, int thread, F2& finite) {
   constexpr int kIn = kSplit<T>;
-  constexpr int kPieces = HPC == 2 ? 2 : KB;
 #pragma unroll
-  for (int b = 0; b < kPieces; ++b) {
+  for (int i0 = 0; i0 < SUBS * 512; i0 += THREADS) {
+    const int i = i0 + thread, r = i / 8 % kChunk, b = i / 512;
+    const uint32_t at = b * kSub + i % 512 * 16;  // its swizzled place: any order of a row's pieces does
+    const float f = d[HPC == 2 ? b : 0].ck[r];
+    uint32_t w[kTerms][4];
+    uint32_t t[kIn][4];
 #pragma unroll
-    for (int r0 = 0; r0 < kChunk; r0 += kThreads / 8) {
-      const int r = r0 + threadIdx.x / 8, c = threadIdx.x % 8;
-      const uint32_t at = b * kSub + r * 128 + ((c ^ (r & 7)) << 4);
-      const float f = d[HPC == 2 ? b : 0].ck[r];
-      float x[8];
-      fill(x, 0.0f);
-#pragma unroll
-      for (int j = kIn - 1; j >= 0; --j) {
-        const uint4 u = *reinterpret_cast<const uint4*>(k + j * kTile + at);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[2 * i] += low_of(w[i]), x[2 * i + 1] += high_of(w[i]);
-      }
-      uint32_t w[kTerms][4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t s[kTerms];
-        split<kTerms>(x[2 * i] * f, x[2 * i + 1] * f, s, finite);
-#pragma unroll
-        for (int j = 0; j < kTerms; ++j) w[j][i] = s[j];
-      }
-#pragma unroll
-      for (int j = 0; j < kTerms; ++j)
-        *reinterpret_cast<uint4*>(out + j * kTile + at) = make_uint4(w[j][0], w[j][1], w[j][2], w[j][3]);
+    for (int j = 0; j < kIn; ++j) {
+      const uint4 u = *reinterpret_cast<const uint4*>(k + j * kTile + at);
+      t[j][0] = u.x, t[j][1] = u.y, t[j][2] = u.z, t[j][3] = u.w;
     }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      F2 x = pair_of(t[kIn - 1][e]);
+#pragma unroll
+      for (int j = kIn - 2; j >= 0; --j) x = add2(x, pair_of(t[j][e]));
+      uint32_t s[kTerms];
+      split<kTerms>(mul2(x, f2(f, f)), s, finite);
+#pragma unroll
+      for (int j = 0; j < kTerms; ++j) w[j][e] = s[j];
+    }
+#pragma unroll
+    for (int j = 0; j < kTerms; ++j)
+      *reinterpret_cast<uint4*>(out + j * kTile + at) = make_uint4(w[j][0], w[j][1], w[j][2], w[j][3]);
   }
 }
 
-// Whether a tile's first term is finite: its exponents are not all ones.
-template <int PIECES>
-__device__ __forceinline__ bool tile_finite(const unsigned char* tile) {
-  uint32_t bad = 0;
+// Whether a tile's first term is finite, by THREADS threads: the largest of
+// its magnitudes as whole numbers, 16 bits each.
+template <int THREADS>
+__device__ __forceinline__ bool tile_finite(const unsigned char* tile, int thread) {
+  uint32_t top = 0;
 #pragma unroll
-  for (int b = 0; b < PIECES; ++b) {
-#pragma unroll
-    for (int i = 0; i < (int)kSub / 16 / kThreads; ++i) {
-      const uint4 u = *reinterpret_cast<const uint4*>(tile + b * kSub + (i * kThreads + threadIdx.x) * 16);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) bad |= ((w[j] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
-    }
+  for (int i = 0; i < (int)kTile / 16 / THREADS; ++i) {
+    const uint4 u = *reinterpret_cast<const uint4*>(tile + (i * THREADS + thread) * 16);
+    top = __vmaxu2(top, u.x & 0x7fff7fffu), top = __vmaxu2(top, u.y & 0x7fff7fffu);
+    top = __vmaxu2(top, u.z & 0x7fff7fffu), top = __vmaxu2(top, u.w & 0x7fff7fffu);
   }
-  return bad == 0;
+  return (top & 0xffffu) < 0x7f80u && (top >> 16) < 0x7f80u;
 }
 
-// One thread: all products of NA terms of A and NB of B down to 2^-24,
+// One thread: the products of NA terms of A and NB of B down to 2^-8 NT,
 // smallest first, STEPS products of 16 each.
-template <int NA, int NB, int STEPS, typename F>
+template <int NA, int NB, int NT, int STEPS, typename F>
 __device__ __forceinline__ void products(F mma) {
   uint32_t more = 0;
 #pragma unroll
-  for (int sum = (NA + NB - 2 < kTerms - 1 ? NA + NB - 2 : kTerms - 1); sum >= 0; --sum) {
+  for (int sum = (NA + NB - 2 < NT - 1 ? NA + NB - 2 : NT - 1); sum >= 0; --sum) {
 #pragma unroll
     for (int a = 0; a < NA; ++a) {
       const int b = sum - a;
@@ -350,29 +395,32 @@ __device__ __forceinline__ void products(F mma) {
   }
 }
 
-// OUT: the outputs too; else only what the segment adds to the state.
-template <typename T, int HPC, int KB, bool OUT>
+// OUT: the outputs too, with P and the state in NT terms; else only what the
+// segment adds to the state.
+template <typename T, int HPC, int KB, int NT, bool OUT>
 __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_constant__ AttnParams p) {
-  using Lay = Layout<T, HPC>;
+  using Lay = Layout<T, HPC, NT>;
   constexpr int kIn = kSplit<T>;
-  constexpr int NH = HPC == 2 ? 32 : 32 * KB;       // state elements of a thread
-  constexpr int KW = HPC == 2 ? 32 : 32 * KB;       // tensor memory columns of one of the state's terms
+  constexpr int NH = HPC == 2 ? 16 : 16 * KB;  // state elements of a thread
+  constexpr int KW = HPC == 2 ? 32 : 32 * KB;  // tensor memory columns of one of the state's terms
   constexpr uint32_t kS = 0, kOi = 64 * HPC, kU = 128 * HPC, kH = kU + 128;
-  static_assert(kH + kTerms * KW <= 512, "tensor memory");
+  static_assert(kH + NT * KW <= 512, "tensor memory");
   constexpr int kHeadSteps = HPC == 2 ? 4 : 4 * KB;  // steps of 16 over a head's elements
   extern __shared__ unsigned char raw[];
   unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   __shared__ Small sh;
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, quarter = warp & 3, half = warp >> 2;
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, quarter = warp & 3, part = warp >> 2;
   const int r = quarter * 32 + lane;
-  const Place<HPC> at(p, OUT ? p.plan.segments : p.plan.segments - 1);
+  const int segments = p.plan.segments;
+  const Place<HPC> at(p, OUT ? segments : segments - 1);
   const AttnPass& a = *at.pass;
   const bool back = a.backward;
-  // the segments' order is the pass's; the one that the last state leaves adds to none
-  const int segments = p.plan.segments, order = at.segment, segment = back ? segments - 1 - order : order;
+  // the segments' order is the pass's; the last one's state is the pass's own
+  const int order = at.segment, segment = back ? segments - 1 - order : order;
   const int head = HPC == 2 ? r >> 6 : 0, h = at.h0 + head, v = HPC == 2 ? r & 63 : r;
   const bool mine = v < a.V && h < p.H;
-  const int k0 = half * NH, ucol = HPC == 2 ? head * 64 + half * 32 : half * NH;  // state elements, U's columns
+  const int k0 = part * NH, ucol = HPC == 2 ? head * 64 + part * 16 : part * NH;  // state elements, U's columns
+  const int ocol = (HPC == 2 ? head * 64 : 0) + part * kCols;                     // columns of S and O
   const int S = p.S, L = row_length(p.lens, at.n, S);
   const int chunks = (S + kChunk - 1) / kChunk, live = (L + kChunk - 1) / kChunk;
   const int c_begin = segment * p.plan.per, c_end = min(c_begin + p.plan.per, chunks);
@@ -399,48 +447,52 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
   auto state_at = [&](int i) {
     return state + (a.v_major ? (long long)v * a.K + k0 + i : (long long)(k0 + i) * a.V + v);
   };
-  const long long kept = (long long)KB * 64 * 128;  // a state in scratch: [k][lane]
-  const int heads_k = HPC == 2 ? 64 : 64 * KB;
-  float H[NH];
-  if (OUT && segments > 1) {
-    const float* from = p.plan.states + ((long long)at.stream * segments + order) * kept;
+  constexpr long long kept = (long long)KB * 64 * 128;  // a state in scratch: [k][lane]
+  F2 H[NH / 2];
+  {
+    float first[NH];
+    if (OUT && segments > 1) {
+      const float* from = p.plan.states + ((long long)at.stream * segments + order) * kept;
 #pragma unroll
-    for (int i = 0; i < NH; ++i) H[i] = k0 + i < heads_k ? from[(k0 + i) * 128 + r] : 0.0f;
-  } else {
+      for (int i = 0; i < NH; ++i) first[i] = from[(k0 + i) * 128 + r];
+    } else {
 #pragma unroll
-    for (int i = 0; i < NH; ++i) H[i] = OUT && a.first && mine && k0 + i < a.K ? a.first[state_at(i)] : 0.0f;
+      for (int i = 0; i < NH; ++i) first[i] = OUT && a.first && mine && k0 + i < a.K ? a.first[state_at(i)] : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < NH / 2; ++i) H[i] = f2(first[2 * i], first[2 * i + 1]);
   }
 
-  float bad_state = 0.0f;  // 0 while the state is finite
-  auto publish = [&]() {   // the state's terms to tensor memory
+  const F2 zero = f2(0.0f, 0.0f);
+  F2 state_finite = zero;
+  auto publish = [&]() {  // the state's terms to tensor memory
+    uint32_t w[NT][NH / 2];
 #pragma unroll
-    for (int j = 0; j < NH; j += 32) {
-      uint32_t w[kTerms][16];
+    for (int i = 0; i < NH / 2; ++i) {
+      uint32_t s[NT];
+      split<NT>(H[i], s, state_finite);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        uint32_t s[kTerms];
-        split<kTerms>(H[j + 2 * i], H[j + 2 * i + 1], s, bad_state);
-#pragma unroll
-        for (int x = 0; x < kTerms; ++x) w[x][i] = s[x];
-      }
-#pragma unroll
-      for (int x = 0; x < kTerms; ++x) tmem_st16(lanes + kH + x * KW + (k0 + j) / 2, w[x]);
+      for (int x = 0; x < NT; ++x) w[x][i] = s[x];
     }
+#pragma unroll
+    for (int x = 0; x < NT; ++x) tmem_st<NH / 2>(lanes + kH + x * KW + k0 / 2, w[x]);
     tmem_st_done();
   };
+  const Rows<T, HPC> rq(a.q, at.n, at.h0, p.H, a.q_of, a.K), rk(a.k, at.n, at.h0, p.H, a.k_of, a.K),
+      rv(a.v, at.n, at.h0, p.H, a.v_of, a.V);
+  constexpr int kSubs = HPC == 2 ? 2 : KB;
   auto fetch = [&](int c, int stage) {
     unsigned char* tiles = sm + stage * Lay::kStage;
-    const int t0 = c * kChunk;
-    if (OUT) load_tile<T, HPC, KB>(tiles + Lay::kQ, a.q, at.n, at.h0, p.H, a.q_of, a.K, t0, L, p.plan.vec);
-    load_tile<T, HPC, KB>(tiles + Lay::kK, a.k, at.n, at.h0, p.H, a.k_of, a.K, t0, L, p.plan.vec);
-    load_tile<T, HPC, 2>(tiles + Lay::kV, a.v, at.n, at.h0, p.H, a.v_of, a.V, t0, L, p.plan.vec);
+    if (OUT) rq.template load<kSubs>(tiles + Lay::kQ, c * kChunk, L, p.plan.vec);
+    rk.template load<kSubs>(tiles + Lay::kK, c * kChunk, L, p.plan.vec);
+    rv.template load<2>(tiles + Lay::kV, c * kChunk, L, p.plan.vec);
     cp_commit();
   };
-  auto decays_of = [&](int i) {
-    if (warp < HPC && at.h0 + warp < p.H)
-      chunk_decays(p, back, at.n, at.h0 + warp, chunk_at(i) * kChunk, L, sh.decays[i & 1][warp], &sh.wrong[i & 1]);
-    else if (warp < HPC)
-      chunk_decays(p, back, at.n, at.h0, S, 0, sh.decays[i & 1][warp], &sh.wrong[i & 1]);
+  auto decays_of = [&](int i) {  // by the last warps: warp 0 issues the products
+    const int x = warp - (16 - HPC);
+    if (x >= 0)
+      chunk_decays(p, a, at.n, min(at.h0 + x, p.H - 1), chunk_at(i) * kChunk, at.h0 + x < p.H ? L : 0, sh.decays[i & 1][x],
+                   &sh.wrong[i & 1]);
   };
   auto wait = [&](int bar, uint32_t phase) {
     if (!sh.gave_up && !bar_wait(su32(&sh.bars[bar]), phase, kWaitNs)) {
@@ -453,18 +505,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
     if (OUT && a.dot && tid < 64 * HPC) {
       const int hd = tid / 64, i = tid % 64, t = c * kChunk + i;
       if (t < L && at.h0 + hd < p.H) {
-        const float* x = &sh.dots[(i / 32) * 4][i % 32];
-        const float y = HPC == 2 ? x[(2 * hd) * 32] + x[(2 * hd + 1) * 32] : (x[0] + x[32]) + (x[64] + x[96]);
+        const float* x = &sh.dots[i / kCols * 4][i % kCols];
+        const float y = HPC == 2 ? x[2 * hd * kCols] + x[(2 * hd + 1) * kCols]
+                                 : (x[0] + x[kCols]) + (x[2 * kCols] + x[3 * kCols]);
         a.dot[((long long)at.n * p.H + at.h0 + hd) * S + t] = y;
       }
     }
   };
-  // outputs of lane v at step t
+  // outputs of lane v
   T* out = static_cast<T*>(a.o.p) + at.n * a.o.ns + (long long)(h / a.o_of) * a.V + v;
+  float* out32 = a.o32 + ((long long)at.n * S * p.H + h) * a.V + v;
+  const long long ss32 = (long long)p.H * a.V;
   const T* dot_row = static_cast<const T*>(a.dot_with.p) + at.n * a.dot_with.ns + (long long)(h / a.o_of) * a.V + v;
   auto put = [&](int t, float y) {
     if (!mine || t >= S) return;
-    if (a.o32) a.o32[(((long long)at.n * S + t) * p.H + h) * a.V + v] = y;
+    if (a.o32) out32[t * ss32] = y;
     else if (a.o.p) out[t * a.o.ss] = Elem<T>::from_f(y);
   };
 
@@ -475,6 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
   if (OUT) publish();
   uint32_t phase = 0;
   double left = 0.0;  // logarithm of the segment's decay
+  const float near = a.so * a.su;
 #pragma unroll 1
   for (int i = 0; i < count; ++i) {
     const int c = chunk_at(i), t0 = c * kChunk;
@@ -484,66 +540,78 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
     cp_wait();
     to_async();
     tc_fence_before();
-    const bool failed = __syncthreads_or(sh.gave_up);
+    __syncthreads();
     tc_fence_after();
-    if (failed) break;
     const uint32_t tq = su32(tiles + Lay::kQ), tk = su32(tiles + Lay::kK), tv = su32(tiles + Lay::kV);
-    const uint32_t ts = su32(sm + Lay::kScaled), tp = (Lay::kOver ? tk : su32(sm + Lay::kP));
+    const uint32_t ts = su32(sm + Lay::kScaled), tp = Lay::kOver ? tk : su32(sm + Lay::kP);
     if (OUT && tid == 0) {
       constexpr uint32_t id = idesc_of(64 * HPC);
-      products<kIn, kIn, kHeadSteps>([&](int x, int y, int s, uint32_t more) {
-        const uint32_t o = (s / 4) * kSub + (s % 4) * 32;
-        tc_mma(tmem + kS, smem_desc_sw128(tq + x * kTile + o), smem_desc_sw128(tk + y * kTile + o), id, more);
+      const uint64_t dq = smem_desc_sw128(tq), dk = smem_desc_sw128(tk);
+      products<kIn, kIn, NT, kHeadSteps>([&](int x, int y, int s, uint32_t more) {
+        const uint32_t o = ((s / 4) * kSub + (s % 4) * 32) >> 4;
+        tc_mma(tmem + kS, dq + (x * kTile >> 4) + o, dk + (y * kTile >> 4) + o, id, more);
       });
       tc_commit(su32(&sh.bars[0]));
-      products<kTerms, kIn, kHeadSteps>([&](int x, int y, int s, uint32_t more) {
-        tc_mma_ts(tmem + kOi, tmem + kH + x * KW + s * 8, smem_desc_sw128(tq + y * kTile + (s / 4) * kSub + (s % 4) * 32), id,
-                  more);
+      products<NT, kIn, NT, kHeadSteps>([&](int x, int y, int s, uint32_t more) {
+        tc_mma_ts(tmem + kOi, tmem + kH + x * KW + s * 8, dq + ((y * kTile + (s / 4) * kSub + (s % 4) * 32) >> 4), id, more);
       });
       tc_commit(su32(&sh.bars[1]));
     }
-    if (i > 0) dots_out(chunk_at(i - 1));
     if (Lay::kStages == 2 && i + 1 < count) fetch(chunk_at(i + 1), stage ^ 1);
-    float finite = 0.0f;
-    scale_tile<T, HPC, KB>(tiles + Lay::kK, sm + Lay::kScaled, dec, finite);
-    bool bad = !tile_finite<2>(tiles + Lay::kV);
+    if (Lay::kStages == 1 && i + 1 < count) {
+      const int t1 = chunk_at(i + 1) * kChunk;
+      if (OUT) rq.prefetch(t1, L);
+      rk.prefetch(t1, L);
+      rv.prefetch(t1, L);
+    }
+    if (i > 0) dots_out(chunk_at(i - 1));
+    F2 finite = zero;
+    bool bad = false;
+    // a warp's quarter of the lanes is also its quarter of the SM: with one
+    // head S has rows for two of them, and the other two scale K
+    if constexpr (OUT && HPC == 1 && !Lay::kOver) {
+      const int thread = (part * 2 + (quarter & 1)) * 32 + lane;
+      if (quarter >= 2) scale_tile<T, HPC, kSubs, kThreads / 2>(tiles + Lay::kK, sm + Lay::kScaled, dec, thread, finite);
+      else bad = !tile_finite<kThreads / 2>(tiles + Lay::kV, thread);
+    } else {
+      scale_tile<T, HPC, kSubs, kThreads>(tiles + Lay::kK, sm + Lay::kScaled, dec, tid, finite);
+      bad = !tile_finite<kThreads>(tiles + Lay::kV, tid);
+    }
     if (i + 1 < count) decays_of(i + 1);
-    if (OUT) {
+    if constexpr (OUT) {
       if constexpr (Lay::kOver) __syncthreads();  // K is read before P takes its place
       wait(0, phase);
       if (HPC == 2 || quarter < 2) {
-        // row m of S, 32 of its columns
-        const int m = r & 63;
+        // row m of S, 16 of its columns
+        const int m = r & 63, n0 = part * kCols;
         const Decays& d = dec[head];
-        float s[32];
-        tmem_ld32(lanes + kS + (HPC == 2 ? head * 64 : 0) + half * 32, reinterpret_cast<uint32_t(&)[32]>(s));
-        const float hi = d.hi[m], lo = d.lo[m];
-        uint32_t w[kTerms][16];
+        float s[kCols];
+        tmem_ld16(lanes + kS + ocol, s);
+        const F2 hi = f2(d.hi[m], d.hi[m]), lo = f2(d.lo[m], d.lo[m]);
+        uint32_t w[NT][kCols / 2];
 #pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-          float x[2];
+        for (int j = 0; j < kCols; j += 2) {
+          const float2 nh = *reinterpret_cast<const float2*>(&d.nhi[n0 + j]), nl = *reinterpret_cast<const float2*>(&d.nlo[n0 + j]);
+          const F2 f = exp2_fast2(add2(add2(hi, f2(nh.x, nh.y)), add2(lo, f2(nl.x, nl.y))));
+          float2 x = f2_get(mul2(f2(s[j], s[j + 1]), f));
+          const int n = n0 + j;
+          x.x = (back ? n >= m : n <= m) ? x.x : 0.0f;
+          x.y = (back ? n + 1 >= m : n + 1 <= m) ? x.y : 0.0f;
+          uint32_t t[NT];
+          split<NT>(f2(x.x, x.y), t, finite);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int nn = half * 32 + j + e;
-            finite = fmaf(s[j + e], 0.0f, finite);
-            const float f = exp2_fast((hi - d.hi[nn]) + (lo - d.lo[nn]));
-            x[e] = (back ? nn >= m : nn <= m) ? s[j + e] * f : 0.0f;
-          }
-          uint32_t t[kTerms];
-          split<kTerms>(x[0], x[1], t, finite);
-#pragma unroll
-          for (int e = 0; e < kTerms; ++e) w[e][j / 2] = t[e];
+          for (int e = 0; e < NT; ++e) w[e][j / 2] = t[e];
         }
         unsigned char* row = (Lay::kOver ? tiles + Lay::kK : sm + Lay::kP) + (HPC == 2 ? r : m) * 128;
 #pragma unroll
-        for (int e = 0; e < kTerms; ++e)
+        for (int e = 0; e < NT; ++e)
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            *reinterpret_cast<uint4*>(row + e * Lay::kPTerm + (((half * 4 + x) ^ (m & 7)) << 4)) =
+          for (int x = 0; x < kCols / 8; ++x)
+            *reinterpret_cast<uint4*>(row + e * Lay::kPTerm + (((part * (kCols / 8) + x) ^ (m & 7)) << 4)) =
                 make_uint4(w[e][4 * x], w[e][4 * x + 1], w[e][4 * x + 2], w[e][4 * x + 3]);
       }
     }
-    bad = bad || !(finite == 0.0f) || (mine && !(bad_state == 0.0f)) || sh.wrong[i & 1];
+    bad = bad || !is_finite(finite) || (mine && !is_finite(state_finite)) || sh.wrong[i & 1] || sh.gave_up;
     to_async();
     tc_fence_before();
     const bool by_step = __syncthreads_or(bad);
@@ -552,59 +620,74 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
     left += dec[head].log2;
     if (!by_step) {
       if (tid == 0) {
+        const uint64_t dv = desc_mn(tv), ds = desc_mn(ts), dp = smem_desc_sw128(tp);
         constexpr uint32_t idu = idesc_of(HPC == 2 ? 128 : 64 * KB) | kRowsA | kRowsB;
-        products<kIn, kTerms, 4>([&](int x, int y, int s, uint32_t more) {
-          tc_mma(tmem + kU, desc_mn(tv + x * kTile + s * 2048), desc_mn(ts + y * kTile + s * 2048), idu, more);
+        products<kIn, kTerms, kTerms, 4>([&](int x, int y, int s, uint32_t more) {
+          tc_mma(tmem + kU, dv + ((x * kTile + s * 2048) >> 4), ds + ((y * kTile + s * 2048) >> 4), idu, more);
         });
         tc_commit(su32(&sh.bars[2]));
         if (OUT) {
           constexpr uint32_t ido = idesc_of(64 * HPC) | kRowsA;
-          products<kIn, kTerms, 4>([&](int x, int y, int s, uint32_t more) {
-            tc_mma(tmem + kS, desc_mn(tv + x * kTile + s * 2048), smem_desc_sw128(tp + y * Lay::kPTerm + s * 32), ido, more);
+          products<kIn, NT, NT, 4>([&](int x, int y, int s, uint32_t more) {
+            tc_mma(tmem + kS, dv + ((x * kTile + s * 2048) >> 4), dp + ((y * Lay::kPTerm + s * 32) >> 4), ido, more);
           });
           tc_commit(su32(&sh.bars[3]));
         }
       }
-      float far[32];
-      if (OUT) {
+      float far[kCols];
+      if constexpr (OUT) {
         wait(1, phase);
-        tmem_ld32(lanes + kOi + (HPC == 2 ? head * 64 : 0) + half * 32, reinterpret_cast<uint32_t(&)[32]>(far));
+        tmem_ld16(lanes + kOi + ocol, far);
       }
       wait(2, phase);
       const float e = dec[head].total;
 #pragma unroll
-      for (int j = 0; j < NH; j += 32) {
-        float u[32];
-        tmem_ld32(lanes + kU + ucol + j, reinterpret_cast<uint32_t(&)[32]>(u));
+      for (int j = 0; j < NH; j += 16) {
+        float u[16];
+        tmem_ld16(lanes + kU + ucol + j, u);
 #pragma unroll
-        for (int x = 0; x < 32; ++x) H[j + x] = fmaf(e, H[j + x], a.su * u[x]);
+        for (int x = 0; x < 8; ++x) H[j / 2 + x] = fma2(f2(e, e), H[j / 2 + x], f2(u[2 * x], u[2 * x + 1]));
       }
-      if (OUT) {
+      if constexpr (OUT) {
         publish();
         wait(3, phase);
-        float o[32];
-        tmem_ld32(lanes + kS + (HPC == 2 ? head * 64 : 0) + half * 32, reinterpret_cast<uint32_t(&)[32]>(o));
+        float o[kCols];
+        tmem_ld16(lanes + kS + ocol, o);
+        const float* cq = &dec[head].cq[part * kCols];
 #pragma unroll
-        for (int x = 0; x < 32; ++x) {
-          o[x] = a.so * fmaf(dec[head].cq[half * 32 + x], far[x], a.su * o[x]);
-          put(t0 + half * 32 + x, o[x]);
+        for (int x = 0; x < kCols; x += 2) {
+          const float2 f = *reinterpret_cast<const float2*>(cq + x);
+          const float2 y = f2_get(fma2(f2(f.x, f.y), f2(far[x], far[x + 1]), mul2(f2(near, near), f2(o[x], o[x + 1]))));
+          o[x] = y.x, o[x + 1] = y.y;
+        }
+        const int t1 = t0 + part * kCols, rows = min(kCols, S - t1);
+        if (mine) {
+          if (a.o32) {
+            float* to = out32 + t1 * ss32;
+#pragma unroll
+            for (int x = 0; x < kCols; ++x, to += ss32)
+              if (x < rows) *to = o[x];
+          } else if (a.o.p) {
+            T* to = out + t1 * a.o.ss;
+#pragma unroll
+            for (int x = 0; x < kCols; ++x, to += a.o.ss)
+              if (x < rows) *to = Elem<T>::from_f(o[x]);
+          }
         }
         if (a.dot) {
+          const T* with = dot_row + t1 * a.dot_with.ss;
 #pragma unroll
-          for (int x = 0; x < 32; ++x) {
-            const int t = t0 + half * 32 + x;
-            o[x] = mine && t < L ? o[x] * Elem<T>::to_f(dot_row[t * a.dot_with.ss]) : 0.0f;
-          }
+          for (int x = 0; x < kCols; ++x, with += a.dot_with.ss) o[x] = mine && t1 + x < L ? o[x] * Elem<T>::to_f(*with) : 0.0f;
           int to = 0;
-          lanes_sum<32, 16, 1>(o, lane, to);
+          lanes_sum<kCols, 16, 1>(o, lane, to);
           sh.dots[warp][to] = o[0];
         }
       } else {
 #pragma unroll
-        for (int x = 0; x < NH; ++x) bad_state = fmaf(H[x], 0.0f, bad_state);
+        for (int x = 0; x < NH / 2; ++x) state_finite = fma2(H[x], zero, state_finite);
       }
-      if (Lay::kStages == 1 && i + 1 < count) fetch(chunk_at(i + 1), 0);
     } else {
+      if (__syncthreads_or(sh.gave_up)) break;
       // step by step, from the operands themselves
       if (OUT) wait(1, phase);
       const int rows = min(kChunk, L - t0);
@@ -612,6 +695,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
       const T* q = head_rows<T>(a.q, at.n, hc, a.q_of, a.K);
       const T* k = head_rows<T>(a.k, at.n, hc, a.k_of, a.K);
       const T* x = head_rows<T>(a.v, at.n, hc, a.v_of, a.V);
+      float g[NH];
+#pragma unroll
+      for (int b = 0; b < NH / 2; ++b) {
+        const float2 y = f2_get(H[b]);
+        g[2 * b] = y.x, g[2 * b + 1] = y.y;
+      }
 #pragma unroll 1
       for (int j = 0; j < rows; ++j) {
         const int m = back ? rows - 1 - j : j;
@@ -621,33 +710,35 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
 #pragma unroll
         for (int b = 0; b < NH; ++b) {
           if (mine && k0 + b < a.K) {
-            H[b] = fmaf(Elem<T>::to_f(k[t * a.k.ss + k0 + b]), val, back ? H[b] : d * H[b]);
-            if (OUT) y = fmaf(Elem<T>::to_f(q[t * a.q.ss + k0 + b]), H[b], y);
-            if (back) H[b] *= d;
+            g[b] = fmaf(Elem<T>::to_f(k[t * a.k.ss + k0 + b]), val, back ? g[b] : d * g[b]);
+            if (OUT) y = fmaf(Elem<T>::to_f(q[t * a.q.ss + k0 + b]), g[b], y);
+            if (back) g[b] *= d;
           }
         }
         if (OUT) {
-          sh.part[half][r] = y;
+          sh.part[part][r] = y;
           __syncthreads();
-          if (half == 0) {
-            y = a.so * (sh.part[0][r] + sh.part[1][r]);
+          if (part == 0) {
+            y = a.so * ((sh.part[0][r] + sh.part[1][r]) + (sh.part[2][r] + sh.part[3][r]));
             put((int)t, y);
             if (a.dot) {
               const float w = warp_sum(mine ? y * Elem<T>::to_f(dot_row[t * a.dot_with.ss]) : 0.0f);
-              if (lane == 0) sh.dots[(m / 32) * 4 + quarter][m % 32] = w;
+              if (lane == 0) sh.dots[m / kCols * 4 + quarter][m % kCols] = w;
             }
           }
           __syncthreads();
         }
       }
       if (OUT)
-        for (int m = rows + half; m < kChunk; m += 2) put(t0 + m, 0.0f);
-      bad_state = 0.0f;
+        for (int m = rows + part; m < kChunk; m += 4) put(t0 + m, 0.0f);
+#pragma unroll
+      for (int b = 0; b < NH / 2; ++b) H[b] = f2(g[2 * b], g[2 * b + 1]);
+      state_finite = zero;
       if (OUT) {
         publish();
       } else {
 #pragma unroll
-        for (int b = 0; b < NH; ++b) bad_state = fmaf(H[b], 0.0f, bad_state);
+        for (int b = 0; b < NH / 2; ++b) state_finite = fma2(H[b], zero, state_finite);
       }
       // the barriers that this chunk did not use complete all the same
       if (tid == 0) {
@@ -657,36 +748,35 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
       wait(2, phase);
       if (OUT) wait(3, phase);
       __syncthreads();
-      if (Lay::kStages == 1 && i + 1 < count) fetch(chunk_at(i + 1), 0);
     }
+    if (Lay::kStages == 1 && i + 1 < count) fetch(chunk_at(i + 1), 0);
     phase ^= 1;
   }
   cp_wait();
-  if (count > 0) {
-    __syncthreads();
-    if (!sh.gave_up) dots_out(chunk_at(count - 1));
-  }
+  __syncthreads();
+  if (count > 0 && !sh.gave_up) dots_out(chunk_at(count - 1));
   if (OUT) {
     // the rows behind the last live chunk
-    for (int t = max(c_live, c_begin) * kChunk + half; t < min(c_end * kChunk, S); t += 2) put(t, 0.0f);
+    for (int t = max(c_live, c_begin) * kChunk + part; t < min(c_end * kChunk, S); t += 4) put(t, 0.0f);
     if (order == segments - 1) {
       float with = 0.0f;
 #pragma unroll
       for (int i = 0; i < NH; ++i) {
+        const float2 y = f2_get(H[i / 2]);
         if (mine && k0 + i < a.K) {
-          if (a.last) a.last[state_at(i)] = H[i];
-          if (a.with) with = fmaf(a.with[state_at(i)], H[i], with);
+          if (a.last) a.last[state_at(i)] = i % 2 ? y.y : y.x;
+          if (a.with) with = fmaf(a.with[state_at(i)], i % 2 ? y.y : y.x, with);
         }
       }
       if (a.cross) {
-        __syncthreads();
         with = warp_sum(with);
         if (lane == 0) sh.part[0][warp] = with;
         __syncthreads();
         if (tid < HPC && at.h0 + tid < p.H) {
           const float* x = sh.part[0];
-          const float y = HPC == 2 ? (x[2 * tid] + x[2 * tid + 1]) + (x[2 * tid + 4] + x[2 * tid + 5])
-                                   : ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+          float y = 0.0f;
+          for (int w = 0; w < 16; ++w)
+            if (HPC == 1 || (w & 3) >> 1 == tid) y += x[w];
           a.cross[(long long)at.n * p.H + at.h0 + tid] = y;
         }
       }
@@ -694,14 +784,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
   } else {
     float* to = p.plan.states + ((long long)at.stream * segments + order) * kept;
 #pragma unroll
-    for (int i = 0; i < NH; ++i)
-      if (k0 + i < heads_k) to[(k0 + i) * 128 + r] = mine && k0 + i < a.K ? H[i] : 0.0f;
-    if (half == 0 && lane == 0 && (HPC == 2 ? quarter % 2 == 0 : quarter == 0))
+    for (int i = 0; i < NH; ++i) {
+      const float2 y = f2_get(H[i / 2]);
+      to[(k0 + i) * 128 + r] = mine && k0 + i < a.K ? (i % 2 ? y.y : y.x) : 0.0f;
+    }
+    if (part == 0 && lane == 0 && (HPC == 2 ? quarter % 2 == 0 : quarter == 0))
       p.plan.left[((long long)at.stream * segments + order) * 2 + head] = left;
   }
-  // nothing is in flight any more, unless a wait has failed: then what was issued gets as long again
+  // nothing is in flight any more, unless a wait has failed: then what was issued gets some time
   if (sh.gave_up && tid == 0) {
-    tc_commit(su32(&sh.bars[3]));
     const unsigned long long begin = gtime();
     while ((long long)(gtime() - begin) < kWaitNs / 4) {
     }
@@ -745,32 +836,45 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
   }
 }
 
-template <typename T, int HPC, int KB>
+template <typename T, int HPC, int KB, int NT>
 cudaError_t launch_chunks_of(const AttnParams& p, cudaStream_t s, int* launches) {
-  constexpr size_t smem = Layout<T, HPC>::kBytes;
+  constexpr size_t smem = Layout<T, HPC, NT>::kBytes;
   const long long streams = (long long)p.passes * p.N * ((p.H + HPC - 1) / HPC);
-  cudaError_t e = cudaFuncSetAttribute(attn_chunk_kernel<T, HPC, KB, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  auto whole = attn_chunk_kernel<T, HPC, KB, NT, true>;
+  cudaError_t e = cudaFuncSetAttribute(whole, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   if (p.plan.segments > 1) {
-    e = cudaFuncSetAttribute(attn_chunk_kernel<T, HPC, KB, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    auto sums = attn_chunk_kernel<T, HPC, KB, kTerms, false>;
+    constexpr size_t sums_smem = Layout<T, HPC, kTerms>::kBytes;
+    e = cudaFuncSetAttribute(sums, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sums_smem);
     if (e != cudaSuccess) return e;
-    attn_chunk_kernel<T, HPC, KB, false><<<(unsigned)(streams * (p.plan.segments - 1)), kThreads, smem, s>>>(p);
+    sums<<<(unsigned)(streams * (p.plan.segments - 1)), kThreads, sums_smem, s>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     ++*launches;
     attn_join_kernel<HPC, KB><<<dim3((unsigned)streams, KB * 64 * 128 / 256), 256, 0, s>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     ++*launches;
   }
-  attn_chunk_kernel<T, HPC, KB, true><<<(unsigned)(streams * p.plan.segments), kThreads, smem, s>>>(p);
+  whole<<<(unsigned)(streams * p.plan.segments), kThreads, smem, s>>>(p);
   if ((e = cudaGetLastError()) == cudaSuccess) ++*launches;
   return e;
 }
 
+template <typename T, int NT>
+cudaError_t launch_chunks_in(const AttnParams& p, cudaStream_t s, int* launches) {
+  // every pass has the same two sizes, in one order or the other
+  if (p.pass[0].K <= 64 && p.pass[0].V <= 64) return launch_chunks_of<T, 2, 1, NT>(p, s, launches);
+  return p.plan.deep == 64 ? launch_chunks_of<T, 1, 1, NT>(p, s, launches) : launch_chunks_of<T, 1, 2, NT>(p, s, launches);
+}
+
+// P and the state as three terms where float32 comes of them: for float32
+// rows, and in gradients, whose products for the decays are added up over the
+// sequence.  A 16-bit output keeps less than the 2^-17 of two.
 template <typename T>
 cudaError_t launch_chunks(const AttnParams& p, cudaStream_t s, int* launches) {
-  // every pass has the same two sizes, in one order or the other
-  if (p.pass[0].K <= 64 && p.pass[0].V <= 64) return launch_chunks_of<T, 2, 1>(p, s, launches);
-  return p.plan.deep == 64 ? launch_chunks_of<T, 1, 1>(p, s, launches) : launch_chunks_of<T, 1, 2>(p, s, launches);
+  if constexpr (kSplit<T> < kTerms)
+    if (!p.gradient) return launch_chunks_in<T, 2>(p, s, launches);
+  return launch_chunks_in<T, kTerms>(p, s, launches);
 }
 
 // Reads and clears the status word, in stream order; the caller synchronises.
