@@ -66,7 +66,7 @@ struct AttnPlan {
   int deep;           // elements that a kernel's states have along q and k: 64 or 128
   int vec;            // rows take 16-byte pieces
   float* states;      // [streams][segments][deep][128]
-  double* left;       // [streams][segments][2]: logarithms (base 2) of what a piece leaves of its first state
+  float* left;        // [streams][segments][2][2]: logarithms (base 2) of what a piece leaves of its first state
 };
 struct AttnParams {
   int dtype;

@@ -126,11 +126,11 @@ int64_t plan_scratch(const rk_attn_problem* p, int passes) {
   if (p->seq * p->batch == 0 || (passes == 1 && p->seq <= rk::kAttnSteps)) return 0;
   return rk::attn_plan_scratch(plan_of(p, passes), p->batch, p->heads, (int)p->key_size, (int)p->value_size, passes);
 }
-// Its regions, from w on.
+// Its regions, from w on: states, and four floats for each.
 void place(rk::AttnPlan& plan, float* w, int64_t floats) {
   const int64_t state = plan.deep * 128;
   plan.states = w;
-  plan.left = reinterpret_cast<double*>(w + floats / (state + 4) * state);
+  plan.left = w + floats / (state + 4) * state;
 }
 int64_t four(int64_t x) { return (x + 3) / 4 * 4; }
 GradPlan grad_plan(const rk_attn_problem* p) {

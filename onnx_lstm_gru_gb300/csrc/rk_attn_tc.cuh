@@ -23,9 +23,21 @@
 // computed here (P, ck K, H) three.  Differences of G are exact to 2^-24: sums
 // are 64-bit whole numbers of 2^-32, kept as whole part and fraction.
 //
+// Where a chunk's decays stay within 2^-100, P_mn 2^-G_m is S_mn 2^-G_n: then
+// no power is taken for each pair, and O is added to Oi before 2^G_m scales
+// both.  (Backward the same from the chunk's end.)  Chunks that decay further
+// take the powers pair by pair and keep the two apart.
+//
 // A block runs one state (two, stacked along the lanes, where heads have at
 // most 64 elements: of the products' 128 x 128 blocks the diagonal ones are
-// used) over a piece of the sequence.
+// used) over a piece of the sequence.  Sixteen warps compute; four more issue
+// the products, copy tiles in and out (TMA, for bfloat16 rows of whole 16-byte
+// pieces; else the workers do), and take the decays of later chunks.  They
+// meet at mbarriers, and the products of one chunk run while the next one's
+// operands are made ready:
+//   workers:   P_i | state += U_i | ck K of i + 1 | outputs of i | P_(i+1) ...
+//   products:  O_i after P_i; S_(i+1), U_(i+1) after ck K; Oi_(i+1) after the
+//              outputs of i
 //
 // Infinities and NaN must not reach other steps through the products' zeros:
 // a chunk in which an operand, a product of P or the state is not finite is
@@ -34,6 +46,8 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+
+#include <cudaTypedefs.h>
 
 #include "rk_attn.h"
 #include "rk_proj_tc.cuh"
@@ -44,7 +58,11 @@ namespace atc {
 
 using namespace ptc;
 
-constexpr int kChunk = 64, kThreads = 512, kTerms = 3;
+constexpr int kChunk = 64, kWorkers = 512, kThreads = kWorkers + 128, kTerms = 3;
+// Registers: 640 threads are launched with 96 each, and the workers' warps get
+// some of the others'.
+constexpr int kWorkerRegisters = 104, kOtherRegisters = 64;
+static_assert(kWorkers * kWorkerRegisters + 128 * kOtherRegisters <= kThreads * 96, "no more than the block was launched with");
 constexpr uint32_t kSub = kChunk * 128;      // bytes of 64 rows of 64 elements
 constexpr uint32_t kTile = 2 * kSub;         // an operand's term: 64 rows of 128 elements, or of two heads of 64
 constexpr int kCols = kChunk / 4;            // of a chunk's columns of S and O, those of a thread
@@ -55,39 +73,50 @@ constexpr int kSplit = sizeof(T) == 4 ? 3 : 2;
 template <>
 constexpr int kSplit<__nv_bfloat16> = 1;
 
-// Shared memory: operand tiles (bfloat16: two stages), ck K, P in NT terms
-// (float32: where K was), and small arrays.
-template <typename T, int HPC, int NT>
+// Shared memory: operand tiles (bfloat16: two stages), ck K (two where only
+// sums of states are wanted), P in NT terms (float32: where K was).
+template <typename T, int HPC, int NT, bool OUT>
 struct Layout {
   static constexpr int kIn = kSplit<T>;
   static constexpr int kStages = kIn == 1 ? 2 : 1;
-  static constexpr uint32_t kQ = 0, kK = kIn * kTile, kV = 2 * kIn * kTile, kStage = 3 * kIn * kTile;
+  static constexpr uint32_t kK = 0, kV = kIn * kTile, kQ = 2 * kIn * kTile, kStage = (OUT ? 3 : 2) * kIn * kTile;
   static constexpr uint32_t kScaled = kStages * kStage;
+  static constexpr int kScaledCount = OUT ? 1 : 2;
+  static constexpr uint32_t kAfter = kScaled + kScaledCount * kTerms * kTile;
   static constexpr bool kOver = kIn == 3;
-  static constexpr uint32_t kP = kOver ? kK : kScaled + kTerms * kTile;
+  static constexpr uint32_t kP = kOver ? kK : kAfter;
   static constexpr uint32_t kPTerm = HPC * kSub;
-  static constexpr uint32_t kEnd = kScaled + kTerms * kTile + (kOver ? 0 : NT * kPTerm);
+  static constexpr uint32_t kEnd = kAfter + (kOver || !OUT ? 0 : NT * kPTerm);
   static_assert(NT * kPTerm <= kIn * kTile || !kOver, "P fits over K");
   static constexpr size_t kBytes = kEnd + 1024;  // alignment
 };
 
 // Decays of a chunk, by head of the block.
 struct Decays {
-  float hi[kChunk], lo[kChunk];    // signed G: whole part and fraction
-  float nhi[kChunk], nlo[kChunk];  // their negatives
-  float cq[kChunk], ck[kChunk];    // so 2^.. of the state's part of a step's output, su 2^.. of a step's part of the state
-  float d[kChunk];                 // a step's own decay
-  double log2;                     // of the chunk's whole decay
-  float total;                     // the decay
+  float hi[kChunk], lo[kChunk];  // signed G: whole part and fraction
+  float cq[kChunk], ck[kChunk];  // so 2^.. of the state's part of a step's output, su 2^.. of a step's part of the state
+  float bn[kChunk];              // su over 2^.. of cq: what takes S to P where the chunk's decays are mild
+  float d[kChunk];               // a step's own decay
+  long long log2;                // the whole chunk's G
+  float total;                   // the decay
+  int mild;
+};
+
+// Those that the workers' warps arrive at, then those of one arrival (the
+// decays': one for each head).  A barrier that could be two phases ahead of
+// one who waits for it has a second one for odd chunks.
+enum Bar {
+  kTiles, kDone = kTiles + 2, kPairs = kDone + 2, kSteps,
+  kGotS, kGotU, kGotOi = kGotU + 2, kGotO, kFull, kWith = kFull + 2, kDecay, kBars = kDecay + 3
 };
 
 struct Small {
-  __align__(16) Decays decays[2][2];
-  float dots[16][kCols];
+  __align__(16) Decays decays[3][2];
+  float dots[2][16][kCols];  // of a chunk and the one before
   float part[4][128];
-  uint64_t bars[4];
+  uint64_t bars[kBars];
   uint32_t tmem;
-  int wrong[2];
+  int bad[8];  // chunks to be run step by step
   volatile int gave_up;
 };
 
@@ -175,14 +204,46 @@ __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_grou
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ void to_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// Whether the barrier's phase has ended; the warp is taken off the scheduler
+// for some time while it has not.
+__device__ __forceinline__ bool bar_try_long(uint32_t b, uint32_t par) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(b), "r"(par), "r"(20000u)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ void copy_in(uint32_t dst, const CUtensorMap* map, int x, int h, int t, int n, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(h), "r"(t), "r"(n), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void copy_out(const CUtensorMap* map, int x, int h, int t, int n, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(h), "r"(t), "r"(n), "r"(src)
+               : "memory");
+}
+
 // Set where a wait has failed (one per element type's unit).
 static __device__ int gave_up_status;
+
+// What a launch gets: the call, and where tiles are copied by TMA the rows of
+// each pass as tensors (elements, heads, steps, batch rows) in boxes of 64
+// elements of 64 steps.
+struct ChunkArgs {
+  CUtensorMap q[3], k[3], v[3], o[3], with[3];
+  AttnParams p;
+};
 
 // What a block works on.
 template <int HPC>
 struct Place {
-  int n, h0, segment, order, stream;
-  const AttnPass* pass;
+  int n, h0, segment, stream, pass;
   __device__ __forceinline__ Place(const AttnParams& p, int segments) {
     long long id = blockIdx.x;
     segment = (int)(id % segments);
@@ -192,7 +253,7 @@ struct Place {
     h0 = (int)(id % groups) * HPC;
     id /= groups;
     n = (int)(id % p.N);
-    pass = &p.pass[id / p.N];
+    pass = (int)(id / p.N);
   }
 };
 
@@ -204,23 +265,30 @@ __device__ __forceinline__ float pow2_of(long long g) {
   return whole > 127 ? __int_as_float(0x7f800000) : part * __int_as_float((whole + 127) << 23);
 }
 
-// One warp: the decays of the chunk that starts at t0, L the row's length.
-__device__ __forceinline__ void chunk_decays(const AttnParams& p, const AttnPass& a, int n, int h, int t0, int L,
-                                             Decays& out, int* wrong) {
+// The logarithm x of a decay to base 2 in units of 2^-32: the product's whole
+// part, fraction and what it rounded away each exactly.  What is below -1e5
+// leaves nothing in float32, and a chunk's sum of it stays within 2^25.
+__device__ __forceinline__ long long fixed_log2(float x) {
+  x = fminf(fmaxf(x, -1.0e5f), 80.0f);
+  constexpr float kLow = (float)(1.4426950408889634074 - (double)kLog2e);
+  const float t = x * kLog2e, rest = fmaf(x, kLog2e, -t) + x * kLow, whole = floorf(t);
+  return ((long long)(int)whole << 32) + (long long)(unsigned long long)__float2uint_rz((t - whole) * 4294967296.0f) +
+         (long long)__float2int_rn(rest * 4294967296.0f);
+}
+
+// One warp: the decays of a chunk of which the lane has x0 and x1, the
+// logarithms of two steps; whether it has to be run step by step.
+__device__ __forceinline__ bool chunk_decays(const AttnPass& a, float x0, float x1, Decays& out) {
   const bool backward = a.backward;
   const int lane = threadIdx.x % 32;
-  const float* g = static_cast<const float*>(p.decay.p) + n * p.decay.ns + h;
-  const float bias = p.bias ? p.bias[h] : 0.0f;
+  const float x[2] = {x0, x1};
   long long fix[2];
+  bool bad = false;
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    const int t = t0 + 2 * lane + j;
-    float x = 0.0f;
-    if (t < L) x = (p.decay.p ? g[t * p.decay.ss] : 0.0f) + bias;
-    out.d[2 * lane + j] = expf(x);
-    if (!(x < 80.0f)) *wrong = 1;  // NaN, or growth that no float32 holds for long
-    // what is below leaves nothing in float32; a chunk's sum stays within 2^25
-    fix[j] = __double2ll_rn((double)fminf(fmaxf(x, -1.0e5f), 80.0f) * (1.4426950408889634074 * 4294967296.0));
+    out.d[2 * lane + j] = expf(x[j]);
+    bad = bad || !(x[j] < 80.0f);  // NaN, or growth that no float32 holds for long
+    fix[j] = fixed_log2(x[j]);
   }
   long long sum = fix[0] + fix[1];
 #pragma unroll
@@ -229,19 +297,24 @@ __device__ __forceinline__ void chunk_decays(const AttnParams& p, const AttnPass
     if (lane >= o) sum += y;
   }
   const long long total = __shfl_sync(0xffffffffu, sum, 31);
+  bool mild = true;
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const long long G = j ? sum : sum - fix[1], s = backward ? -G : G;
     const int i = 2 * lane + j;
-    const float hi = (float)(int)(s >> 32), lo = (float)((uint32_t)s >> 8) * 5.9604644775390625e-8f;
-    out.hi[i] = hi, out.lo[i] = lo;
-    out.nhi[i] = -hi, out.nlo[i] = -lo;
-    if (G >> 32 > 120 || (total - G) >> 32 > 120) *wrong = 1;
+    out.hi[i] = (float)(int)(s >> 32);
+    out.lo[i] = (float)((uint32_t)s >> 8) * 5.9604644775390625e-8f;
+    const long long from = backward ? total - G : G;
+    bad = bad || G >> 32 > 120 || (total - G) >> 32 > 120;
+    mild = mild && from >> 32 >= -100 && from >> 32 <= 100;
     const float up = pow2_of(G), down = pow2_of(total - G);
     out.cq[i] = a.so * (backward ? down : up);
     out.ck[i] = a.su * (backward ? up : down);
+    out.bn[i] = a.su * pow2_of(-from);
   }
-  if (lane == 0) out.total = pow2_of(total), out.log2 = (double)total * 2.3283064365386962890625e-10;
+  mild = __all_sync(0xffffffffu, mild);
+  if (lane == 0) out.total = pow2_of(total), out.log2 = total, out.mild = mild;
+  return __any_sync(0xffffffffu, bad);
 }
 
 // Row operands of a block, as pointers to its first head's elements.
@@ -252,42 +325,50 @@ __device__ __forceinline__ const T* head_rows(const RowsArg& a, int n, int h, in
 
 // A thread's part of an operand's tiles: one piece of 8 elements of a row of
 // each of the two sub-tiles, which are the elements from 0 and 64 on, or two
-// heads.
+// heads.  What a thread fetches is also what it scales and checks, so that
+// only the products wait for the other threads.
+__device__ __forceinline__ uint32_t piece_at() {
+  const int r = threadIdx.x / 8, c = threadIdx.x % 8;
+  return r * 128 + ((c ^ (r & 7)) << 4);
+}
 template <typename T, int HPC>
 struct Rows {
-  const T* src;       // the thread's first step's piece of sub-tile 0
-  long long next, ss; // to sub-tile 1; to the next step
-  int size, heads;    // elements of a head; heads that there are from the block's first on
-  __device__ __forceinline__ Rows(const RowsArg& a, int n, int h0, int H, int of, int size_)
-      : ss(a.ss), size(size_), heads(H - h0) {
-    src = head_rows<T>(a, n, h0, of, size) + (threadIdx.x / 8) * a.ss + 8 * (threadIdx.x % 8);
-    next = HPC == 1 ? 64 : (long long)(min(h0 + 1, H - 1) / of - h0 / of) * size;
+  const T* src;        // the thread's piece of sub-tile 0 of the next chunk
+  long long ss, step;  // from row to row; to the chunk after it
+  int next;            // to sub-tile 1
+  int on;              // bit b: sub-tile b has the thread's elements
+  int size;
+  // t0: the first chunk's start; step: to the next one's
+  __device__ __forceinline__ Rows(const RowsArg& a, int n, int h0, int H, int of, int size_, int t0, int step_)
+      : ss(a.ss), step(step_ * a.ss), size(size_) {
+    const int c = 8 * (threadIdx.x % 8);
+    src = head_rows<T>(a, n, h0, of, size) + (t0 + (int)(threadIdx.x / 8)) * a.ss + c;
+    next = HPC == 1 ? 64 : (min(h0 + 1, H - 1) / of - h0 / of) * size;
+    on = (c < size ? 1 : 0) | ((HPC == 1 ? 64 + c < size : c < size && h0 + 1 < H) ? 2 : 0);
   }
-  // Fetches the 64 rows from t0 on into the tile at `tile`.  Steps from L on,
-  // elements from `size` on and heads that there are not are zeros.
+  // Fetches the next chunk's 64 rows into the tile at `tile`; live: the
+  // thread's row is a step.  Other steps, elements from `size` on and heads
+  // that there are not are zeros.
   template <int SUBS>
-  __device__ __forceinline__ void load(unsigned char* tile, int t0, int L, int vec) const {
+  __device__ __forceinline__ void load(unsigned char* tile, bool live, int vec, const T* any) {
     constexpr int kIn = kSplit<T>;
-    const int r = threadIdx.x / 8, c = threadIdx.x % 8;
-    const T* at = src + t0 * ss;
-    unsigned char* to = tile + r * 128 + ((c ^ (r & 7)) << 4);
+    unsigned char* to = tile + piece_at();
 #pragma unroll
     for (int b = 0; b < SUBS; ++b) {
-      const int first = (HPC == 2 ? 0 : 64 * b) + 8 * c;
-      const bool on = t0 + r < L && (HPC == 1 || b < heads);
+      const int first = (HPC == 2 ? 0 : 64 * b) + 8 * (threadIdx.x % 8);
+      const bool fetch = live && (on >> b & 1);
       unsigned char* dst = to + b * kSub;
-      const T* from = at + b * next;
+      const T* from = src + b * next;
       if constexpr (kIn == 1) {
         if (vec) {
-          const bool fetch = on && first < size;
-          cp16(su32(dst), fetch ? from : src, fetch);
+          cp16(su32(dst), fetch ? from : any, fetch);
           continue;
         }
       }
       float x[8];
       fill(x, 0.0f);
       if (vec) {
-        if (on && first < size) {
+        if (fetch) {
           if constexpr (sizeof(T) == 4) {
             float y[4];
             Piece<T, 4>::load(from, y);
@@ -303,7 +384,7 @@ struct Rows {
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (on && first + i < size) x[i] = Elem<T>::to_f(from[i]);
+          if (fetch && first + i < size) x[i] = Elem<T>::to_f(from[i]);
       }
       uint32_t w[kIn][4];
       F2 unused = f2(0.0f, 0.0f);
@@ -317,27 +398,24 @@ struct Rows {
 #pragma unroll
       for (int j = 0; j < kIn; ++j) *reinterpret_cast<uint4*>(dst + j * kTile) = make_uint4(w[j][0], w[j][1], w[j][2], w[j][3]);
     }
+    src += step;
   }
-  // Has the rows from t0 on brought into L2.
-  __device__ __forceinline__ void prefetch(int t0, int L) const {
-    if (t0 + (int)(threadIdx.x / 8) >= L) return;
-    const T* at = src + t0 * ss;
+  // Has the next chunk's rows brought into L2.
+  __device__ __forceinline__ void prefetch(bool live) const {
 #pragma unroll
     for (int b = 0; b < 2; ++b)
-      if ((HPC == 1 ? 64 * b + 8 * (int)(threadIdx.x % 8) < size : b < heads && 8 * (int)(threadIdx.x % 8) < size))
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(at + b * next));
+      if (live && (on >> b & 1)) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + b * next));
   }
 };
 
-// ck K as three terms, of the tile's SUBS sub-tiles, by THREADS threads.
-template <typename T, int HPC, int SUBS, int THREADS>
-__device__ __forceinline__ void scale_tile(const unsigned char* k, unsigned char* out, const Decays* d, int thread, F2& finite) {
+// ck K of the thread's pieces as three terms.
+template <typename T, int HPC, int SUBS>
+__device__ __forceinline__ void scale_tile(const unsigned char* k, unsigned char* out, const Decays* d, F2& finite) {
   constexpr int kIn = kSplit<T>;
 #pragma unroll
-  for (int i0 = 0; i0 < SUBS * 512; i0 += THREADS) {
-    const int i = i0 + thread, r = i / 8 % kChunk, b = i / 512;
-    const uint32_t at = b * kSub + i % 512 * 16;  // its swizzled place: any order of a row's pieces does
-    const float f = d[HPC == 2 ? b : 0].ck[r];
+  for (int b = 0; b < SUBS; ++b) {
+    const uint32_t at = b * kSub + piece_at();
+    const float f = d[HPC == 2 ? b : 0].ck[threadIdx.x / 8];
     uint32_t w[kTerms][4];
     uint32_t t[kIn][4];
 #pragma unroll
@@ -361,14 +439,13 @@ __device__ __forceinline__ void scale_tile(const unsigned char* k, unsigned char
   }
 }
 
-// Whether a tile's first term is finite, by THREADS threads: the largest of
-// its magnitudes as whole numbers, 16 bits each.
-template <int THREADS>
-__device__ __forceinline__ bool tile_finite(const unsigned char* tile, int thread) {
+// Whether the thread's pieces of a tile's first term are finite: the largest
+// of the magnitudes as whole numbers, 16 bits each.
+__device__ __forceinline__ bool tile_finite(const unsigned char* tile) {
   uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < (int)kTile / 16 / THREADS; ++i) {
-    const uint4 u = *reinterpret_cast<const uint4*>(tile + (i * THREADS + thread) * 16);
+  for (int b = 0; b < 2; ++b) {
+    const uint4 u = *reinterpret_cast<const uint4*>(tile + b * kSub + piece_at());
     top = __vmaxu2(top, u.x & 0x7fff7fffu), top = __vmaxu2(top, u.y & 0x7fff7fffu);
     top = __vmaxu2(top, u.z & 0x7fff7fffu), top = __vmaxu2(top, u.w & 0x7fff7fffu);
   }
@@ -395,32 +472,111 @@ __device__ __forceinline__ void products(F mma) {
   }
 }
 
+// Waits for a barrier's phase of parity par.  Once a wait has failed all of
+// them return at once: the loops run out, and what they compute is undefined.
+__device__ __forceinline__ void wait_bar(Small& sh, int bar, uint32_t par) {
+  const uint32_t b = su32(&sh.bars[bar]);
+  if (!bar_try(b, par)) {
+    const unsigned long long begin = gtime();
+    for (unsigned it = 1; !sh.gave_up; ++it) {
+      if (bar_try_long(b, par)) break;
+      if ((it & 15u) == 0 && (long long)(gtime() - begin) > kWaitNs) {
+        sh.gave_up = 1;
+        atomicOr(&gave_up_status, 1);
+      }
+    }
+  }
+  tc_fence_after();
+}
+// The warp's writes and reads so far are done: to shared memory for the
+// products, and of tensor memory.
+__device__ __forceinline__ void arrive_bar(Small& sh, int bar) {
+  to_async();
+  tc_fence_before();
+  __syncwarp();
+  if (threadIdx.x % 32 == 0) bar_arrive(su32(&sh.bars[bar]));
+}
+
+// The chunk that starts at t0 step by step, by all workers; g: the thread's
+// elements of the state.  Returns the phases that the steps' barrier has had.
+// Not inlined: it is there for infinities and NaN.
+template <typename T, int HPC, int NH, bool OUT>
+__device__ __noinline__ int run_steps(const AttnParams& p, int pass, int n, int h0, int t0, int L, const Decays* dec,
+                                      float (*dots)[kCols], Small& sh, int meetings, float* g) {
+  const AttnPass& a = p.pass[pass];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, quarter = warp & 3, part = warp >> 2, r = quarter * 32 + lane;
+  const int head = HPC == 2 ? r >> 6 : 0, h = h0 + head, v = HPC == 2 ? r & 63 : r, k0 = part * NH;
+  const bool mine = v < a.V && h < p.H, back = a.backward;
+  const int rows = min(kChunk, L - t0), hc = min(h, p.H - 1);
+  const T* q = head_rows<T>(a.q, n, hc, a.q_of, a.K);
+  const T* k = head_rows<T>(a.k, n, hc, a.k_of, a.K);
+  const T* x = head_rows<T>(a.v, n, hc, a.v_of, a.V);
+  T* out = static_cast<T*>(a.o.p) + n * a.o.ns + (long long)(hc / a.o_of) * a.V + v;
+  const T* with = static_cast<const T*>(a.dot_with.p) + n * a.dot_with.ns + (long long)(hc / a.o_of) * a.V + v;
+  auto put = [&](long long t, float y) {
+    if (!mine || t >= p.S) return;
+    if (a.o32) a.o32[(((long long)n * p.S + t) * p.H + h) * a.V + v] = y;
+    else if (a.o.p) out[t * a.o.ss] = Elem<T>::from_f(y);
+  };
+#pragma unroll 1
+  for (int j = 0; j < rows; ++j) {
+    const int m = back ? rows - 1 - j : j;
+    const long long t = t0 + m;
+    const float d = dec[head].d[m], val = mine ? a.su * Elem<T>::to_f(x[t * a.v.ss + v]) : 0.0f;
+    float y = 0.0f;
+#pragma unroll 4
+    for (int b = 0; b < NH; ++b) {
+      if (mine && k0 + b < a.K) {
+        g[b] = fmaf(Elem<T>::to_f(k[t * a.k.ss + k0 + b]), val, back ? g[b] : d * g[b]);
+        if (OUT) y = fmaf(Elem<T>::to_f(q[t * a.q.ss + k0 + b]), g[b], y);
+        if (back) g[b] *= d;
+      }
+    }
+    if (OUT) {
+      sh.part[part][r] = y;
+      arrive_bar(sh, kSteps);
+      wait_bar(sh, kSteps, meetings++ & 1);
+      if (part == 0) {
+        y = a.so * ((sh.part[0][r] + sh.part[1][r]) + (sh.part[2][r] + sh.part[3][r]));
+        put(t, y);
+        if (a.dot) {
+          const float z = warp_sum(mine ? y * Elem<T>::to_f(with[t * a.dot_with.ss]) : 0.0f);
+          if (lane == 0) dots[m / kCols * 4 + quarter][m % kCols] = z;
+        }
+      }
+      arrive_bar(sh, kSteps);
+      wait_bar(sh, kSteps, meetings++ & 1);
+    }
+  }
+  if (OUT)
+    for (int m = rows + part; m < kChunk; m += 4) put(t0 + m, 0.0f);
+  return meetings;
+}
+
 // OUT: the outputs too, with P and the state in NT terms; else only what the
-// segment adds to the state.
-template <typename T, int HPC, int KB, int NT, bool OUT>
-__global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_constant__ AttnParams p) {
-  using Lay = Layout<T, HPC, NT>;
+// segment adds to the state.  TMA: tiles are copied by it.
+template <typename T, int HPC, int KB, int NT, bool OUT, bool TMA>
+__global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_constant__ ChunkArgs args) {
+  static_assert(!TMA || kSplit<T> == 1, "what is split into terms goes through registers");
+  const AttnParams& p = args.p;
+  using Lay = Layout<T, HPC, NT, OUT>;
   constexpr int kIn = kSplit<T>;
   constexpr int NH = HPC == 2 ? 16 : 16 * KB;  // state elements of a thread
   constexpr int KW = HPC == 2 ? 32 : 32 * KB;  // tensor memory columns of one of the state's terms
   constexpr uint32_t kS = 0, kOi = 64 * HPC, kU = 128 * HPC, kH = kU + 128;
   static_assert(kH + NT * KW <= 512, "tensor memory");
   constexpr int kHeadSteps = HPC == 2 ? 4 : 4 * KB;  // steps of 16 over a head's elements
+  constexpr int kSubs = HPC == 2 ? 2 : KB;
   extern __shared__ unsigned char raw[];
   unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   __shared__ Small sh;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, quarter = warp & 3, part = warp >> 2;
-  const int r = quarter * 32 + lane;
   const int segments = p.plan.segments;
   const Place<HPC> at(p, OUT ? segments : segments - 1);
-  const AttnPass& a = *at.pass;
+  const AttnPass& a = p.pass[at.pass];  // by index: it stays in constant memory
   const bool back = a.backward;
   // the segments' order is the pass's; the last one's state is the pass's own
   const int order = at.segment, segment = back ? segments - 1 - order : order;
-  const int head = HPC == 2 ? r >> 6 : 0, h = at.h0 + head, v = HPC == 2 ? r & 63 : r;
-  const bool mine = v < a.V && h < p.H;
-  const int k0 = part * NH, ucol = HPC == 2 ? head * 64 + part * 16 : part * NH;  // state elements, U's columns
-  const int ocol = (HPC == 2 ? head * 64 : 0) + part * kCols;                     // columns of S and O
   const int S = p.S, L = row_length(p.lens, at.n, S);
   const int chunks = (S + kChunk - 1) / kChunk, live = (L + kChunk - 1) / kChunk;
   const int c_begin = segment * p.plan.per, c_end = min(c_begin + p.plan.per, chunks);
@@ -428,379 +584,510 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
   auto chunk_at = [&](int i) { return back ? c_live - 1 - i : c_begin + i; };
 
   if (tid == 0) {
-    for (int i = 0; i < 4; ++i) bar_init(su32(&sh.bars[i]), 1);
+    for (int i = 0; i < kBars; ++i) bar_init(su32(&sh.bars[i]), i <= kSteps ? kWorkers / 32 : i >= kDecay ? HPC : 1);
     sh.gave_up = 0;
-    sh.wrong[0] = sh.wrong[1] = 0;
+    for (int i = 0; i < 8; ++i) sh.bad[i] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 0) {
+  if (warp == kWorkers / 32) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&sh.tmem)), "r"(512u) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sh.tmem, lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+  const uint32_t tmem = sh.tmem;
+  // Where U of chunk i is: without outputs there is room for two, and the next is on its way while one is added.
+  auto u_at = [](int i) { return OUT ? kU : 128u * (i & 1); };
+  struct Phase {
+    int bar, n;
+  };
+  auto ready = [](int i) { return Phase{kTiles + (i & 1), i >> 1}; };
+  auto done = [](int i) { return Phase{kDone + (i & 1), i >> 1}; };
+  auto got_u = [](int i) { return Phase{kGotU + (i & 1), i >> 1}; };
+  auto full = [](int i) { return Phase{kFull + (i & 1), i >> 1}; };
+  auto decayed = [](int i) { return Phase{kDecay + i % 3, i / 3}; };
+  auto wait = [&](int bar, int n) { wait_bar(sh, bar, n & 1); };
+  auto wait_for = [&](Phase x) { wait(x.bar, x.n); };
+  auto arrive = [&](int bar) { arrive_bar(sh, bar); };
+  auto stage_of = [&](int i) { return (Lay::kStages == 2 ? i & 1 : 0) * Lay::kStage; };
 
-  // the state, transposed: lane v, elements k0 ..
-  const long long state = ((long long)at.n * p.H + h) * a.K * a.V;
-  auto state_at = [&](int i) {
-    return state + (a.v_major ? (long long)v * a.K + k0 + i : (long long)(k0 + i) * a.V + v);
-  };
-  constexpr long long kept = (long long)KB * 64 * 128;  // a state in scratch: [k][lane]
-  F2 H[NH / 2];
-  {
-    float first[NH];
-    if (OUT && segments > 1) {
-      const float* from = p.plan.states + ((long long)at.stream * segments + order) * kept;
+  if (warp < kWorkers / 32) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWorkerRegisters));
+    // ---------------- the workers
+    const int r = quarter * 32 + lane;
+    const int head = HPC == 2 ? r >> 6 : 0, h = at.h0 + head, v = HPC == 2 ? r & 63 : r;
+    const bool mine = v < a.V && h < p.H;
+    const int k0 = part * NH, ucol = HPC == 2 ? head * 64 + part * 16 : part * NH;  // state elements, U's columns
+    const int ocol = (HPC == 2 ? head * 64 : 0) + part * kCols;                     // columns of S and O
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+    // the state, transposed: lane v, elements k0 ..
+    const long long state = ((long long)at.n * p.H + h) * a.K * a.V;
+    auto state_at = [&](int i) {
+      return state + (a.v_major ? (long long)v * a.K + k0 + i : (long long)(k0 + i) * a.V + v);
+    };
+    constexpr long long kept = (long long)KB * 64 * 128;  // a state in scratch: [k][lane]
+    const int step = back ? -kChunk : kChunk, t_first = chunk_at(0) * kChunk, vec = p.plan.vec;
+    Rows<T, HPC> rq(a.q, at.n, at.h0, p.H, a.q_of, a.K, t_first, step), rk(a.k, at.n, at.h0, p.H, a.k_of, a.K, t_first, step),
+        rv(a.v, at.n, at.h0, p.H, a.v_of, a.V, t_first, step);
+    auto fetch = [&](int i) {
+      unsigned char* tiles = sm + stage_of(i);
+      const bool is = chunk_at(i) * kChunk + tid / 8 < L;
+      rk.template load<kSubs>(tiles + Lay::kK, is, vec, static_cast<const T*>(a.k.p));
+      rv.template load<2>(tiles + Lay::kV, is, vec, static_cast<const T*>(a.v.p));
+      if (OUT) rq.template load<kSubs>(tiles + Lay::kQ, is, vec, static_cast<const T*>(a.q.p));
+      cp_commit();
+    };
+    if (!TMA && count > 0) fetch(0);
+    F2 H[NH / 2];
+    {
+      float first[NH];
+      if (OUT && segments > 1) {
+        const float* from = p.plan.states + ((long long)at.stream * segments + order) * kept;
 #pragma unroll
-      for (int i = 0; i < NH; ++i) first[i] = from[(k0 + i) * 128 + r];
-    } else {
-#pragma unroll
-      for (int i = 0; i < NH; ++i) first[i] = OUT && a.first && mine && k0 + i < a.K ? a.first[state_at(i)] : 0.0f;
-    }
-#pragma unroll
-    for (int i = 0; i < NH / 2; ++i) H[i] = f2(first[2 * i], first[2 * i + 1]);
-  }
-
-  const F2 zero = f2(0.0f, 0.0f);
-  F2 state_finite = zero;
-  auto publish = [&]() {  // the state's terms to tensor memory
-    uint32_t w[NT][NH / 2];
-#pragma unroll
-    for (int i = 0; i < NH / 2; ++i) {
-      uint32_t s[NT];
-      split<NT>(H[i], s, state_finite);
-#pragma unroll
-      for (int x = 0; x < NT; ++x) w[x][i] = s[x];
-    }
-#pragma unroll
-    for (int x = 0; x < NT; ++x) tmem_st<NH / 2>(lanes + kH + x * KW + k0 / 2, w[x]);
-    tmem_st_done();
-  };
-  const Rows<T, HPC> rq(a.q, at.n, at.h0, p.H, a.q_of, a.K), rk(a.k, at.n, at.h0, p.H, a.k_of, a.K),
-      rv(a.v, at.n, at.h0, p.H, a.v_of, a.V);
-  constexpr int kSubs = HPC == 2 ? 2 : KB;
-  auto fetch = [&](int c, int stage) {
-    unsigned char* tiles = sm + stage * Lay::kStage;
-    if (OUT) rq.template load<kSubs>(tiles + Lay::kQ, c * kChunk, L, p.plan.vec);
-    rk.template load<kSubs>(tiles + Lay::kK, c * kChunk, L, p.plan.vec);
-    rv.template load<2>(tiles + Lay::kV, c * kChunk, L, p.plan.vec);
-    cp_commit();
-  };
-  auto decays_of = [&](int i) {  // by the last warps: warp 0 issues the products
-    const int x = warp - (16 - HPC);
-    if (x >= 0)
-      chunk_decays(p, a, at.n, min(at.h0 + x, p.H - 1), chunk_at(i) * kChunk, at.h0 + x < p.H ? L : 0, sh.decays[i & 1][x],
-                   &sh.wrong[i & 1]);
-  };
-  auto wait = [&](int bar, uint32_t phase) {
-    if (!sh.gave_up && !bar_wait(su32(&sh.bars[bar]), phase, kWaitNs)) {
-      sh.gave_up = 1;
-      atomicOr(&gave_up_status, 1);
-    }
-    tc_fence_after();
-  };
-  auto dots_out = [&](int c) {  // the products of a chunk's outputs, added up over the lanes' warps
-    if (OUT && a.dot && tid < 64 * HPC) {
-      const int hd = tid / 64, i = tid % 64, t = c * kChunk + i;
-      if (t < L && at.h0 + hd < p.H) {
-        const float* x = &sh.dots[i / kCols * 4][i % kCols];
-        const float y = HPC == 2 ? x[2 * hd * kCols] + x[(2 * hd + 1) * kCols]
-                                 : (x[0] + x[kCols]) + (x[2 * kCols] + x[3 * kCols]);
-        a.dot[((long long)at.n * p.H + at.h0 + hd) * S + t] = y;
-      }
-    }
-  };
-  // outputs of lane v
-  T* out = static_cast<T*>(a.o.p) + at.n * a.o.ns + (long long)(h / a.o_of) * a.V + v;
-  float* out32 = a.o32 + ((long long)at.n * S * p.H + h) * a.V + v;
-  const long long ss32 = (long long)p.H * a.V;
-  const T* dot_row = static_cast<const T*>(a.dot_with.p) + at.n * a.dot_with.ns + (long long)(h / a.o_of) * a.V + v;
-  auto put = [&](int t, float y) {
-    if (!mine || t >= S) return;
-    if (a.o32) out32[t * ss32] = y;
-    else if (a.o.p) out[t * a.o.ss] = Elem<T>::from_f(y);
-  };
-
-  if (count > 0) {
-    fetch(chunk_at(0), 0);
-    decays_of(0);
-  }
-  if (OUT) publish();
-  uint32_t phase = 0;
-  double left = 0.0;  // logarithm of the segment's decay
-  const float near = a.so * a.su;
-#pragma unroll 1
-  for (int i = 0; i < count; ++i) {
-    const int c = chunk_at(i), t0 = c * kChunk;
-    const int stage = Lay::kStages == 2 ? i & 1 : 0;
-    unsigned char* tiles = sm + stage * Lay::kStage;
-    const Decays* dec = sh.decays[i & 1];
-    cp_wait();
-    to_async();
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tq = su32(tiles + Lay::kQ), tk = su32(tiles + Lay::kK), tv = su32(tiles + Lay::kV);
-    const uint32_t ts = su32(sm + Lay::kScaled), tp = Lay::kOver ? tk : su32(sm + Lay::kP);
-    if (OUT && tid == 0) {
-      constexpr uint32_t id = idesc_of(64 * HPC);
-      const uint64_t dq = smem_desc_sw128(tq), dk = smem_desc_sw128(tk);
-      products<kIn, kIn, NT, kHeadSteps>([&](int x, int y, int s, uint32_t more) {
-        const uint32_t o = ((s / 4) * kSub + (s % 4) * 32) >> 4;
-        tc_mma(tmem + kS, dq + (x * kTile >> 4) + o, dk + (y * kTile >> 4) + o, id, more);
-      });
-      tc_commit(su32(&sh.bars[0]));
-      products<NT, kIn, NT, kHeadSteps>([&](int x, int y, int s, uint32_t more) {
-        tc_mma_ts(tmem + kOi, tmem + kH + x * KW + s * 8, dq + ((y * kTile + (s / 4) * kSub + (s % 4) * 32) >> 4), id, more);
-      });
-      tc_commit(su32(&sh.bars[1]));
-    }
-    if (Lay::kStages == 2 && i + 1 < count) fetch(chunk_at(i + 1), stage ^ 1);
-    if (Lay::kStages == 1 && i + 1 < count) {
-      const int t1 = chunk_at(i + 1) * kChunk;
-      if (OUT) rq.prefetch(t1, L);
-      rk.prefetch(t1, L);
-      rv.prefetch(t1, L);
-    }
-    if (i > 0) dots_out(chunk_at(i - 1));
-    F2 finite = zero;
-    bool bad = false;
-    // a warp's quarter of the lanes is also its quarter of the SM: with one
-    // head S has rows for two of them, and the other two scale K
-    if constexpr (OUT && HPC == 1 && !Lay::kOver) {
-      const int thread = (part * 2 + (quarter & 1)) * 32 + lane;
-      if (quarter >= 2) scale_tile<T, HPC, kSubs, kThreads / 2>(tiles + Lay::kK, sm + Lay::kScaled, dec, thread, finite);
-      else bad = !tile_finite<kThreads / 2>(tiles + Lay::kV, thread);
-    } else {
-      scale_tile<T, HPC, kSubs, kThreads>(tiles + Lay::kK, sm + Lay::kScaled, dec, tid, finite);
-      bad = !tile_finite<kThreads>(tiles + Lay::kV, tid);
-    }
-    if (i + 1 < count) decays_of(i + 1);
-    if constexpr (OUT) {
-      if constexpr (Lay::kOver) __syncthreads();  // K is read before P takes its place
-      wait(0, phase);
-      if (HPC == 2 || quarter < 2) {
-        // row m of S, 16 of its columns
-        const int m = r & 63, n0 = part * kCols;
-        const Decays& d = dec[head];
-        float s[kCols];
-        tmem_ld16(lanes + kS + ocol, s);
-        const F2 hi = f2(d.hi[m], d.hi[m]), lo = f2(d.lo[m], d.lo[m]);
-        uint32_t w[NT][kCols / 2];
-#pragma unroll
-        for (int j = 0; j < kCols; j += 2) {
-          const float2 nh = *reinterpret_cast<const float2*>(&d.nhi[n0 + j]), nl = *reinterpret_cast<const float2*>(&d.nlo[n0 + j]);
-          const F2 f = exp2_fast2(add2(add2(hi, f2(nh.x, nh.y)), add2(lo, f2(nl.x, nl.y))));
-          float2 x = f2_get(mul2(f2(s[j], s[j + 1]), f));
-          const int n = n0 + j;
-          x.x = (back ? n >= m : n <= m) ? x.x : 0.0f;
-          x.y = (back ? n + 1 >= m : n + 1 <= m) ? x.y : 0.0f;
-          uint32_t t[NT];
-          split<NT>(f2(x.x, x.y), t, finite);
-#pragma unroll
-          for (int e = 0; e < NT; ++e) w[e][j / 2] = t[e];
-        }
-        unsigned char* row = (Lay::kOver ? tiles + Lay::kK : sm + Lay::kP) + (HPC == 2 ? r : m) * 128;
-#pragma unroll
-        for (int e = 0; e < NT; ++e)
-#pragma unroll
-          for (int x = 0; x < kCols / 8; ++x)
-            *reinterpret_cast<uint4*>(row + e * Lay::kPTerm + (((part * (kCols / 8) + x) ^ (m & 7)) << 4)) =
-                make_uint4(w[e][4 * x], w[e][4 * x + 1], w[e][4 * x + 2], w[e][4 * x + 3]);
-      }
-    }
-    bad = bad || !is_finite(finite) || (mine && !is_finite(state_finite)) || sh.wrong[i & 1] || sh.gave_up;
-    to_async();
-    tc_fence_before();
-    const bool by_step = __syncthreads_or(bad);
-    tc_fence_after();
-    if (tid == 0) sh.wrong[i & 1] = 0;
-    left += dec[head].log2;
-    if (!by_step) {
-      if (tid == 0) {
-        const uint64_t dv = desc_mn(tv), ds = desc_mn(ts), dp = smem_desc_sw128(tp);
-        constexpr uint32_t idu = idesc_of(HPC == 2 ? 128 : 64 * KB) | kRowsA | kRowsB;
-        products<kIn, kTerms, kTerms, 4>([&](int x, int y, int s, uint32_t more) {
-          tc_mma(tmem + kU, dv + ((x * kTile + s * 2048) >> 4), ds + ((y * kTile + s * 2048) >> 4), idu, more);
-        });
-        tc_commit(su32(&sh.bars[2]));
-        if (OUT) {
-          constexpr uint32_t ido = idesc_of(64 * HPC) | kRowsA;
-          products<kIn, NT, NT, 4>([&](int x, int y, int s, uint32_t more) {
-            tc_mma(tmem + kS, dv + ((x * kTile + s * 2048) >> 4), dp + ((y * Lay::kPTerm + s * 32) >> 4), ido, more);
-          });
-          tc_commit(su32(&sh.bars[3]));
-        }
-      }
-      float far[kCols];
-      if constexpr (OUT) {
-        wait(1, phase);
-        tmem_ld16(lanes + kOi + ocol, far);
-      }
-      wait(2, phase);
-      const float e = dec[head].total;
-#pragma unroll
-      for (int j = 0; j < NH; j += 16) {
-        float u[16];
-        tmem_ld16(lanes + kU + ucol + j, u);
-#pragma unroll
-        for (int x = 0; x < 8; ++x) H[j / 2 + x] = fma2(f2(e, e), H[j / 2 + x], f2(u[2 * x], u[2 * x + 1]));
-      }
-      if constexpr (OUT) {
-        publish();
-        wait(3, phase);
-        float o[kCols];
-        tmem_ld16(lanes + kS + ocol, o);
-        const float* cq = &dec[head].cq[part * kCols];
-#pragma unroll
-        for (int x = 0; x < kCols; x += 2) {
-          const float2 f = *reinterpret_cast<const float2*>(cq + x);
-          const float2 y = f2_get(fma2(f2(f.x, f.y), f2(far[x], far[x + 1]), mul2(f2(near, near), f2(o[x], o[x + 1]))));
-          o[x] = y.x, o[x + 1] = y.y;
-        }
-        const int t1 = t0 + part * kCols, rows = min(kCols, S - t1);
-        if (mine) {
-          if (a.o32) {
-            float* to = out32 + t1 * ss32;
-#pragma unroll
-            for (int x = 0; x < kCols; ++x, to += ss32)
-              if (x < rows) *to = o[x];
-          } else if (a.o.p) {
-            T* to = out + t1 * a.o.ss;
-#pragma unroll
-            for (int x = 0; x < kCols; ++x, to += a.o.ss)
-              if (x < rows) *to = Elem<T>::from_f(o[x]);
-          }
-        }
-        if (a.dot) {
-          const T* with = dot_row + t1 * a.dot_with.ss;
-#pragma unroll
-          for (int x = 0; x < kCols; ++x, with += a.dot_with.ss) o[x] = mine && t1 + x < L ? o[x] * Elem<T>::to_f(*with) : 0.0f;
-          int to = 0;
-          lanes_sum<kCols, 16, 1>(o, lane, to);
-          sh.dots[warp][to] = o[0];
-        }
+        for (int i = 0; i < NH; ++i) first[i] = from[(k0 + i) * 128 + r];
       } else {
 #pragma unroll
-        for (int x = 0; x < NH / 2; ++x) state_finite = fma2(H[x], zero, state_finite);
+        for (int i = 0; i < NH; ++i) first[i] = OUT && a.first && mine && k0 + i < a.K ? a.first[state_at(i)] : 0.0f;
       }
-    } else {
-      if (__syncthreads_or(sh.gave_up)) break;
-      // step by step, from the operands themselves
-      if (OUT) wait(1, phase);
-      const int rows = min(kChunk, L - t0);
-      const int hc = min(h, p.H - 1);
-      const T* q = head_rows<T>(a.q, at.n, hc, a.q_of, a.K);
-      const T* k = head_rows<T>(a.k, at.n, hc, a.k_of, a.K);
-      const T* x = head_rows<T>(a.v, at.n, hc, a.v_of, a.V);
+#pragma unroll
+      for (int i = 0; i < NH / 2; ++i) H[i] = f2(first[2 * i], first[2 * i + 1]);
+    }
+    const F2 zero = f2(0.0f, 0.0f);
+    // The state's terms to tensor memory, for chunk i.
+    auto publish = [&](int i) {
+      F2 finite = zero;
+      uint32_t w[NT][NH / 2];
+#pragma unroll
+      for (int x = 0; x < NH / 2; ++x) {
+        uint32_t s[NT];
+        split<NT>(H[x], s, finite);
+#pragma unroll
+        for (int y = 0; y < NT; ++y) w[y][x] = s[y];
+      }
+#pragma unroll
+      for (int x = 0; x < NT; ++x) tmem_st<NH / 2>(lanes + kH + x * KW + k0 / 2, w[x]);
+      tmem_st_done();
+      if (mine && !is_finite(finite)) sh.bad[i & 7] = 1;
+    };
+    // ck K of chunk i, once its tiles are there.
+    auto prepare = [&](int i) {
+      unsigned char* tiles = sm + stage_of(i);
+      if constexpr (TMA) {
+        wait_for(full(i));
+        if (chunk_at(i) * kChunk + tid / 8 >= L) {  // behind the row's end
+          const uint4 none = make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            unsigned char* to = tiles + b * kSub + piece_at();
+            *reinterpret_cast<uint4*>(to + Lay::kV) = none;
+            if (b < kSubs) *reinterpret_cast<uint4*>(to + Lay::kK) = none;
+            if (OUT && b < kSubs) *reinterpret_cast<uint4*>(to + Lay::kQ) = none;
+          }
+        }
+      } else {
+        cp_wait();
+      }
+      wait_for(decayed(i));
+      F2 finite = zero;
+      scale_tile<T, HPC, kSubs>(tiles + Lay::kK, sm + Lay::kScaled + (OUT ? 0 : i & 1) * kTerms * kTile, sh.decays[i % 3], finite);
+      if (!is_finite(finite) || !tile_finite(tiles + Lay::kV)) sh.bad[i & 7] = 1;
+      arrive(ready(i).bar);
+    };
+    // outputs of lane v
+    T* out = static_cast<T*>(a.o.p) + at.n * a.o.ns + (long long)(h / a.o_of) * a.V + v;
+    float* out32 = a.o32 + ((long long)at.n * S * p.H + h) * a.V + v;
+    const long long ss32 = (long long)p.H * a.V;
+    const T* dot_row = static_cast<const T*>(a.dot_with.p) + at.n * a.dot_with.ns + (long long)(h / a.o_of) * a.V + v;
+    auto put = [&](int t, float y) {
+      if (!mine || t >= S) return;
+      if (a.o32) out32[t * ss32] = y;
+      else if (a.o.p) out[t * a.o.ss] = Elem<T>::from_f(y);
+    };
+    auto dots_out = [&](int i) {  // the products of chunk i's outputs, added up over the lanes' warps
+      if (tid < 64 * HPC) {
+        const int hd = tid / 64, m = tid % 64, t = chunk_at(i) * kChunk + m;
+        if (t < L && at.h0 + hd < p.H) {
+          const float* x = &sh.dots[i & 1][m / kCols * 4][m % kCols];
+          const float y = HPC == 2 ? x[2 * hd * kCols] + x[(2 * hd + 1) * kCols]
+                                   : (x[0] + x[kCols]) + (x[2 * kCols] + x[3 * kCols]);
+          a.dot[((long long)at.n * p.H + at.h0 + hd) * S + t] = y;
+        }
+      }
+    };
+    // P of row m of S, 16 of its columns
+    auto pairs = [&](int i) {
+      const int m = r & 63, n0 = part * kCols;
+      const Decays& d = sh.decays[i % 3][head];
+      const bool mild = sh.decays[i % 3][0].mild && (HPC == 1 || sh.decays[i % 3][1].mild);
+      float s[kCols];
+      tmem_ld16(lanes + kS + ocol, s);
+      F2 x[kCols / 2];
+      if (mild) {
+#pragma unroll
+        for (int j = 0; j < kCols; j += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(&d.bn[n0 + j]);
+          x[j / 2] = mul2(f2(s[j], s[j + 1]), f2(f.x, f.y));
+          x[j / 2 + 1] = mul2(f2(s[j + 2], s[j + 3]), f2(f.z, f.w));
+        }
+      } else {
+        const float hi = d.hi[m], lo = d.lo[m];
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) s[j] *= a.su * exp2_fast((hi - d.hi[n0 + j]) + (lo - d.lo[n0 + j]));
+#pragma unroll
+        for (int j = 0; j < kCols / 2; ++j) x[j] = f2(s[2 * j], s[2 * j + 1]);
+      }
+      F2 finite = zero;
+      uint32_t w[NT][kCols / 2];
+      // m - n0 counted from the row's end backward in time
+      const int last = back ? n0 + kCols - 1 - m : m - n0;
+#pragma unroll
+      for (int j = 0; j < kCols; j += 2) {
+        float2 y = f2_get(x[j / 2]);
+        y.x = (back ? kCols - 1 - j : j) <= last ? y.x : 0.0f;
+        y.y = (back ? kCols - 2 - j : j + 1) <= last ? y.y : 0.0f;
+        uint32_t t[NT];
+        split<NT>(f2(y.x, y.y), t, finite);
+#pragma unroll
+        for (int e = 0; e < NT; ++e) w[e][j / 2] = t[e];
+      }
+      if (!is_finite(finite)) sh.bad[i & 7] = 1;
+      unsigned char* row = (Lay::kOver ? sm + Lay::kK : sm + Lay::kP) + (HPC == 2 ? r : m) * 128;
+#pragma unroll
+      for (int e = 0; e < NT; ++e)
+#pragma unroll
+        for (int y = 0; y < kCols / 8; ++y)
+          *reinterpret_cast<uint4*>(row + e * Lay::kPTerm + (((part * (kCols / 8) + y) ^ (m & 7)) << 4)) =
+              make_uint4(w[e][4 * y], w[e][4 * y + 1], w[e][4 * y + 2], w[e][4 * y + 3]);
+    };
+    int meetings = 0;
+    // Chunk i step by step, from the operands themselves.
+    auto by_step = [&](int i) {
       float g[NH];
 #pragma unroll
       for (int b = 0; b < NH / 2; ++b) {
         const float2 y = f2_get(H[b]);
         g[2 * b] = y.x, g[2 * b + 1] = y.y;
       }
-#pragma unroll 1
-      for (int j = 0; j < rows; ++j) {
-        const int m = back ? rows - 1 - j : j;
-        const long long t = t0 + m;
-        const float d = dec[head].d[m], val = mine ? a.su * Elem<T>::to_f(x[t * a.v.ss + v]) : 0.0f;
-        float y = 0.0f;
-#pragma unroll
-        for (int b = 0; b < NH; ++b) {
-          if (mine && k0 + b < a.K) {
-            g[b] = fmaf(Elem<T>::to_f(k[t * a.k.ss + k0 + b]), val, back ? g[b] : d * g[b]);
-            if (OUT) y = fmaf(Elem<T>::to_f(q[t * a.q.ss + k0 + b]), g[b], y);
-            if (back) g[b] *= d;
-          }
-        }
-        if (OUT) {
-          sh.part[part][r] = y;
-          __syncthreads();
-          if (part == 0) {
-            y = a.so * ((sh.part[0][r] + sh.part[1][r]) + (sh.part[2][r] + sh.part[3][r]));
-            put((int)t, y);
-            if (a.dot) {
-              const float w = warp_sum(mine ? y * Elem<T>::to_f(dot_row[t * a.dot_with.ss]) : 0.0f);
-              if (lane == 0) sh.dots[m / kCols * 4 + quarter][m % kCols] = w;
-            }
-          }
-          __syncthreads();
-        }
-      }
-      if (OUT)
-        for (int m = rows + part; m < kChunk; m += 4) put(t0 + m, 0.0f);
+      meetings = run_steps<T, HPC, NH, OUT>(args.p, at.pass, at.n, at.h0, chunk_at(i) * kChunk, L, sh.decays[i % 3],
+                                            sh.dots[i & 1], sh, meetings, g);
 #pragma unroll
       for (int b = 0; b < NH / 2; ++b) H[b] = f2(g[2 * b], g[2 * b + 1]);
-      state_finite = zero;
-      if (OUT) {
-        publish();
-      } else {
+    };
+    auto add_state = [&](int i) {
+      const float e = sh.decays[i % 3][head].total;
 #pragma unroll
-        for (int b = 0; b < NH / 2; ++b) state_finite = fma2(H[b], zero, state_finite);
+      for (int j = 0; j < NH; j += 16) {
+        float u[16];
+        tmem_ld16(lanes + u_at(i) + ucol + j, u);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) H[j / 2 + x] = fma2(f2(e, e), H[j / 2 + x], f2(u[2 * x], u[2 * x + 1]));
       }
-      // the barriers that this chunk did not use complete all the same
-      if (tid == 0) {
-        tc_commit(su32(&sh.bars[2]));
-        if (OUT) tc_commit(su32(&sh.bars[3]));
+    };
+    auto outputs = [&](int i) {
+      const Decays* dec = sh.decays[i % 3];
+      const bool mild = dec[0].mild && (HPC == 1 || dec[1].mild);
+      float o[kCols];
+      tmem_ld16(lanes + kOi + ocol, o);
+      const float* cq = &dec[head].cq[part * kCols];
+#pragma unroll
+      for (int x = 0; x < kCols; x += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(cq + x);
+        const float2 y = f2_get(mul2(f2(f.x, f.y), f2(o[x], o[x + 1]))), z = f2_get(mul2(f2(f.z, f.w), f2(o[x + 2], o[x + 3])));
+        o[x] = y.x, o[x + 1] = y.y, o[x + 2] = z.x, o[x + 3] = z.y;
       }
-      wait(2, phase);
-      if (OUT) wait(3, phase);
-      __syncthreads();
+      if (!mild) {
+        float near[kCols];
+        tmem_ld16(lanes + kS + ocol, near);
+#pragma unroll
+        for (int x = 0; x < kCols; ++x) o[x] = fmaf(a.so, near[x], o[x]);
+      }
+      const int t1 = chunk_at(i) * kChunk + part * kCols, rows = min(kCols, S - t1);
+      if (mine) {
+        if constexpr (TMA) {
+          if (!a.o32) {
+            // a lane's element of 16 rows of the tile that takes Q's place
+            T* to = reinterpret_cast<T*>(sm + stage_of(i) + Lay::kQ + (r >> 6) * kSub + part * kCols * 128) + (r & 63);
+#pragma unroll
+            for (int x = 0; x < kCols; ++x) to[x * 64] = Elem<T>::from_f(o[x]);
+          }
+        }
+        if (a.o32) {
+          float* to = out32 + t1 * ss32;
+#pragma unroll
+          for (int x = 0; x < kCols; ++x, to += ss32)
+            if (x < rows) *to = o[x];
+        } else if (!TMA && a.o.p) {
+          T* to = out + t1 * a.o.ss;
+#pragma unroll
+          for (int x = 0; x < kCols; ++x, to += a.o.ss)
+            if (x < rows) *to = Elem<T>::from_f(o[x]);
+        }
+      }
+      if (a.dot) {
+        if constexpr (TMA) {
+          wait(kWith, i);
+          const T* from = reinterpret_cast<const T*>(sm + stage_of(i) + Lay::kK + (r >> 6) * kSub + part * kCols * 128) + (r & 63);
+          const int rows_live = mine ? L - t1 : 0;
+#pragma unroll
+          for (int x = 0; x < kCols; ++x) {
+            const float w = Elem<T>::to_f(from[x * 64]);
+            o[x] = x < rows_live ? o[x] * w : 0.0f;
+          }
+        } else {
+          const T* with = dot_row + t1 * a.dot_with.ss;
+#pragma unroll
+          for (int x = 0; x < kCols; ++x, with += a.dot_with.ss) o[x] = mine && t1 + x < L ? o[x] * Elem<T>::to_f(*with) : 0.0f;
+        }
+        int to = 0;
+        lanes_sum<kCols, 16, 1>(o, lane, to);
+        sh.dots[i & 1][warp][to] = o[0];
+      }
+    };
+
+    if (OUT && count > 0) {
+      wait_for(decayed(0));
+      publish(0);
     }
-    if (Lay::kStages == 1 && i + 1 < count) fetch(chunk_at(i + 1), 0);
-    phase ^= 1;
-  }
-  cp_wait();
-  __syncthreads();
-  if (count > 0 && !sh.gave_up) dots_out(chunk_at(count - 1));
-  if (OUT) {
-    // the rows behind the last live chunk
-    for (int t = max(c_live, c_begin) * kChunk + part; t < min(c_end * kChunk, S); t += 4) put(t, 0.0f);
-    if (order == segments - 1) {
-      float with = 0.0f;
+    if (count > 0) prepare(0);
+    if (!TMA && Lay::kStages == 2 && count > 1) fetch(1);
+    long long left = 0;  // logarithm of the segment's decay
+    if constexpr (OUT) {
+#pragma unroll 1
+      for (int i = 0; i < count; ++i) {
+        if (Lay::kStages == 1 && i + 1 < count) {
+          const bool is = chunk_at(i + 1) * kChunk + tid / 8 < L;
+          rk.prefetch(is), rv.prefetch(is), rq.prefetch(is);
+        }
+        wait(kGotS, i);
+        if (HPC == 2 || quarter < 2) pairs(i);
+        arrive(kPairs);
+        wait(kPairs, i);  // all of the chunk's flags are set
+        wait_for(got_u(i));
+        wait(kGotOi, i);
+        if (a.dot && i > 0) dots_out(i - 1);
+        const bool bad = sh.bad[i & 7];
+        if (!bad) add_state(i);
+        else by_step(i);
+        if (i + 1 < count) {
+          wait_for(decayed(i + 1));
+          publish(i + 1);
+          // with two stages the next chunk's operands are made ready while O is on its way
+          if (Lay::kStages == 2) prepare(i + 1);
+        }
+        wait(kGotO, i);
+        if (!bad) outputs(i);
+        if (!TMA && i + Lay::kStages < count) fetch(i + Lay::kStages);
+        arrive(done(i).bar);
+        if (Lay::kStages == 1 && i + 1 < count) prepare(i + 1);
+      }
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < count; ++i) {
+        if (Lay::kStages == 2 && i + 1 < count) prepare(i + 1);
+        wait_for(got_u(i));
+        if (!sh.bad[i & 7]) add_state(i);
+        else by_step(i);
+        // what has left nothing leaves nothing: 64 bits hold a thousandfold of that
+        left = max(left + sh.decays[i % 3][head].log2, -(1LL << 45));
+        if (!TMA && i + Lay::kStages < count) fetch(i + Lay::kStages);
+        arrive(done(i).bar);
+        if (Lay::kStages == 1 && i + 1 < count) prepare(i + 1);
+      }
+    }
+    cp_wait();
+    if (OUT) {
+      if (a.dot && count > 0) {
+        wait_for(done(count - 1));
+        if (!sh.gave_up) dots_out(count - 1);
+      }
+      // the rows behind the last live chunk
+      for (int t = max(c_live, c_begin) * kChunk + part; t < min(c_end * kChunk, S); t += 4) put(t, 0.0f);
+      if (order == segments - 1) {
+        float with = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NH; ++i) {
+          const float2 y = f2_get(H[i / 2]);
+          if (mine && k0 + i < a.K) {
+            if (a.last) a.last[state_at(i)] = i % 2 ? y.y : y.x;
+            if (a.with) with = fmaf(a.with[state_at(i)], i % 2 ? y.y : y.x, with);
+          }
+        }
+        with = warp_sum(with);
+        if (lane == 0) sh.part[0][warp] = with;
+      }
+    } else {
+      float* to = p.plan.states + ((long long)at.stream * segments + order) * kept;
 #pragma unroll
       for (int i = 0; i < NH; ++i) {
         const float2 y = f2_get(H[i / 2]);
-        if (mine && k0 + i < a.K) {
-          if (a.last) a.last[state_at(i)] = i % 2 ? y.y : y.x;
-          if (a.with) with = fmaf(a.with[state_at(i)], i % 2 ? y.y : y.x, with);
-        }
+        to[(k0 + i) * 128 + r] = mine && k0 + i < a.K ? (i % 2 ? y.y : y.x) : 0.0f;
       }
-      if (a.cross) {
-        with = warp_sum(with);
-        if (lane == 0) sh.part[0][warp] = with;
-        __syncthreads();
-        if (tid < HPC && at.h0 + tid < p.H) {
-          const float* x = sh.part[0];
-          float y = 0.0f;
-          for (int w = 0; w < 16; ++w)
-            if (HPC == 1 || (w & 3) >> 1 == tid) y += x[w];
-          a.cross[(long long)at.n * p.H + at.h0 + tid] = y;
-        }
+      if (part == 0 && lane == 0 && (HPC == 2 ? quarter % 2 == 0 : quarter == 0)) {
+        // as whole part and fraction; beyond these nothing, or everything, is left
+        const long long x = min(max(left, -(300LL << 32)), 250LL << 32);
+        float* to2 = p.plan.left + (((long long)at.stream * segments + order) * 2 + head) * 2;
+        to2[0] = (float)(int)(x >> 32), to2[1] = (float)((uint32_t)x >> 8) * 5.9604644775390625e-8f;
       }
     }
   } else {
-    float* to = p.plan.states + ((long long)at.stream * segments + order) * kept;
-#pragma unroll
-    for (int i = 0; i < NH; ++i) {
-      const float2 y = f2_get(H[i / 2]);
-      to[(k0 + i) * 128 + r] = mine && k0 + i < a.K ? (i % 2 ? y.y : y.x) : 0.0f;
-    }
-    if (part == 0 && lane == 0 && (HPC == 2 ? quarter % 2 == 0 : quarter == 0))
-      p.plan.left[((long long)at.stream * segments + order) * 2 + head] = left;
-  }
-  // nothing is in flight any more, unless a wait has failed: then what was issued gets some time
-  if (sh.gave_up && tid == 0) {
-    const unsigned long long begin = gtime();
-    while ((long long)(gtime() - begin) < kWaitNs / 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegisters));
+    if (warp == kWorkers / 32) {
+      // ---------------- products
+      bool apart = false;  // the last chunk's outputs are where S is
+  #pragma unroll 1
+      for (int i = 0; i < count; ++i) {
+        const uint32_t tiles = su32(sm) + stage_of(i);
+        const uint32_t scaled = su32(sm) + Lay::kScaled + (OUT ? 0 : i & 1) * kTerms * kTile;
+        const uint64_t dv = desc_mn(tiles + Lay::kV);
+        wait_for(ready(i));
+        if (OUT && apart) wait_for(done(i - 1));
+        if (lane == 0) {
+          if (OUT) {
+            constexpr uint32_t id = idesc_of(64 * HPC);
+            const uint64_t dq = smem_desc_sw128(tiles + Lay::kQ), dk = smem_desc_sw128(tiles + Lay::kK);
+            products<kIn, kIn, NT, kHeadSteps>([&](int x, int y, int s, uint32_t more) {
+              const uint32_t o = ((s / 4) * kSub + (s % 4) * 32) >> 4;
+              tc_mma(tmem + kS, dq + (x * kTile >> 4) + o, dk + (y * kTile >> 4) + o, id, more);
+            });
+            tc_commit(su32(&sh.bars[kGotS]));
+          }
+          constexpr uint32_t idu = idesc_of(HPC == 2 ? 128 : 64 * KB) | kRowsA | kRowsB;
+          const uint64_t ds = desc_mn(scaled);
+          const uint32_t du = tmem + u_at(i);
+          products<kIn, kTerms, kTerms, 4>([&](int x, int y, int s, uint32_t more) {
+            tc_mma(du, dv + ((x * kTile + s * 2048) >> 4), ds + ((y * kTile + s * 2048) >> 4), idu, more);
+          });
+          tc_commit(su32(&sh.bars[got_u(i).bar]));
+        }
+        __syncwarp();
+        if (!OUT) continue;
+        if (i > 0) wait_for(done(i - 1));
+        if (lane == 0) {
+          const uint64_t dq = smem_desc_sw128(tiles + Lay::kQ);
+          products<NT, kIn, NT, kHeadSteps>([&](int x, int y, int s, uint32_t more) {
+            tc_mma_ts(tmem + kOi, tmem + kH + x * KW + s * 8, dq + ((y * kTile + (s / 4) * kSub + (s % 4) * 32) >> 4),
+                      idesc_of(64 * HPC), more);
+          });
+          tc_commit(su32(&sh.bars[kGotOi]));
+        }
+        __syncwarp();
+        const Decays* dec = sh.decays[i % 3];
+        apart = !(dec[0].mild && (HPC == 1 || dec[1].mild));
+        wait(kPairs, i);
+        if (lane == 0) {
+          if (!sh.bad[i & 7]) {
+            const uint64_t dp = smem_desc_sw128(Lay::kOver ? tiles + Lay::kK : su32(sm) + Lay::kP);
+            const uint32_t to = tmem + (apart ? kS : kOi);
+            products<kIn, NT, NT, 4>([&](int x, int y, int s, uint32_t more) {
+              tc_mma(to, dv + ((x * kTile + s * 2048) >> 4), dp + ((y * Lay::kPTerm + s * 32) >> 4), idesc_of(64 * HPC) | kRowsA,
+                     apart ? more : 1u);
+            });
+          }
+          tc_commit(su32(&sh.bars[kGotO]));
+        }
+        __syncwarp();
+      }
+      if (count > 0) {  // all of them complete before tensor memory is given back
+        wait_for(got_u(count - 1));
+        if (OUT) wait(kGotO, count - 1);
+      }
+    } else if (warp == kWorkers / 32 + 1) {
+      // ---------------- copies
+      if constexpr (TMA) {
+        const int z = at.pass;
+        // sub-tile b of an operand whose heads `of` heads share
+        auto head_of = [&](int b, int of) { return HPC == 2 ? (at.h0 + b) / of : at.h0 / of; };
+        auto load = [&](int i) {
+          const uint32_t tiles = su32(sm) + stage_of(i), bar = su32(&sh.bars[full(i).bar]);
+          const int t = chunk_at(i) * kChunk;
+          bar_expect(bar, (2 + kSubs * (OUT ? 2 : 1)) * kSub);
+          for (int b = 0; b < 2; ++b) {
+            const int x = HPC == 2 ? 0 : 64 * b;
+            if (b < kSubs) copy_in(tiles + Lay::kK + b * kSub, &args.k[z], x, head_of(b, a.k_of), t, at.n, bar);
+            copy_in(tiles + Lay::kV + b * kSub, &args.v[z], x, head_of(b, a.v_of), t, at.n, bar);
+            if (OUT && b < kSubs) copy_in(tiles + Lay::kQ + b * kSub, &args.q[z], x, head_of(b, a.q_of), t, at.n, bar);
+          }
+        };
+        if (lane == 0)
+          for (int i = 0; i < min(count, 2); ++i) load(i);
+        const bool out = OUT && a.o.p && !a.o32;
+  #pragma unroll 1
+        for (int i = 0; i < count; ++i) {
+          const uint32_t tiles = su32(sm) + stage_of(i);
+          const int t = chunk_at(i) * kChunk;
+          if (OUT && a.dot) {  // takes the place of K, which S and ck K have been made from
+            wait(kPairs, i);
+            if (lane == 0) {
+              const uint32_t bar = su32(&sh.bars[kWith]);
+              bar_expect(bar, 2 * kSub);
+              for (int b = 0; b < 2; ++b)
+                copy_in(tiles + Lay::kK + b * kSub, &args.with[z], HPC == 2 ? 0 : 64 * b, head_of(b, a.o_of), t, at.n, bar);
+            }
+            __syncwarp();
+          }
+          wait_for(done(i));
+          if (OUT && a.dot) wait(kWith, i);  // also where nobody has read it
+          if (lane == 0) {
+            if (out && !sh.bad[i & 7] && !sh.gave_up) {  // from the place of Q
+              for (int b = 0; b < 2; ++b)
+                if (HPC == 1 ? 64 * b < a.V : at.h0 + b < p.H)
+                  copy_out(&args.o[z], HPC == 2 ? 0 : 64 * b, head_of(b, a.o_of), t, at.n, tiles + Lay::kQ + b * kSub);
+              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+              asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            }
+            if (i + 2 < count && !sh.gave_up) load(i + 2);
+          }
+          __syncwarp();
+        }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        __syncwarp();
+      }
+    } else {
+      // ---------------- decays: a warp for each head
+      const int x = warp - (kWorkers / 32 + 2), h = min(at.h0 + x, p.H - 1), end = at.h0 + x < p.H ? L : 0;
+      if (x < HPC) {
+        const float* g = static_cast<const float*>(p.decay.p) + at.n * p.decay.ns + h;
+        const float bias = p.bias ? p.bias[h] : 0.0f;
+        auto read = [&](int i, int j) {
+          const int t = chunk_at(i) * kChunk + 2 * lane + j;
+          return t < end ? (p.decay.p ? g[t * p.decay.ss] : 0.0f) + bias : 0.0f;
+        };
+        float x0 = 0.0f, x1 = 0.0f;
+        if (count > 0) x0 = read(0, 0), x1 = read(0, 1);
+  #pragma unroll 1
+        for (int i = 0; i < count; ++i) {
+          if (i >= 3) wait_for(done(i - 3));  // whose place these take
+          const float y0 = x0, y1 = x1;
+          if (i + 1 < count) x0 = read(i + 1, 0), x1 = read(i + 1, 1);
+          const bool bad = chunk_decays(a, y0, y1, sh.decays[i % 3][x]);
+          if (lane == 0) {
+            if (x == 0) sh.bad[(i + 4) & 7] = 0;
+            if (bad) sh.bad[i & 7] = 1;
+          }
+          __syncwarp();
+          if (lane == 0) bar_arrive(su32(&sh.bars[decayed(i).bar]));
+        }
+      }
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 0)
+  if (OUT && a.cross && order == segments - 1 && tid < HPC && at.h0 + tid < p.H) {
+    const float* x = sh.part[0];
+    float y = 0.0f;
+    for (int w = 0; w < 16; ++w)
+      if (HPC == 1 || (w & 3) >> 1 == tid) y += x[w];
+    a.cross[(long long)at.n * p.H + at.h0 + tid] = y;
+  }
+  // nothing is in flight any more, unless a wait has failed: then what was issued gets some time
+  if (sh.gave_up && warp == kWorkers / 32) {
+    const unsigned long long begin = gtime();
+    while ((long long)(gtime() - begin) < kWaitNs / 4) {
+    }
+  }
+  if (warp == kWorkers / 32)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
@@ -822,49 +1109,89 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
   if (mine && a.first)
     run = a.first[((long long)n * p.H + h) * a.K * a.V + (a.v_major ? (long long)v * a.K + k : (long long)k * a.V + v)];
   float* s = p.plan.states + id * p.plan.segments * kept + element;
-  const double* f = p.plan.left + id * p.plan.segments * 2 + (HPC == 2 ? r >> 6 : 0);
+  const float* f = p.plan.left + (id * p.plan.segments * 2 + (HPC == 2 ? r >> 6 : 0)) * 2;
   for (int i = 0; i < p.plan.segments; ++i) {
     const bool more = i + 1 < p.plan.segments;
     const float add = more ? s[(long long)i * kept] : 0.0f;
     s[(long long)i * kept] = run;
     if (!more) break;
     // 2^x run in two parts: where decays grow a state the power alone may pass float32's range
-    const double x = fmin(fmax(f[2 * i], -300.0), 250.0);
-    const int whole = (int)floor(x);
+    const int whole = (int)f[4 * i];
     const int w1 = max(min(whole, 127), -126), w2 = max(min(whole - w1, 127), -126);
-    run = run * exp2f((float)(x - whole)) * __int_as_float((w1 + 127) << 23) * __int_as_float((w2 + 127) << 23) + add;
+    run = run * exp2_fast(f[4 * i + 1]) * __int_as_float((w1 + 127) << 23) * __int_as_float((w2 + 127) << 23) + add;
   }
 }
 
-template <typename T, int HPC, int KB, int NT>
-cudaError_t launch_chunks_of(const AttnParams& p, cudaStream_t s, int* launches) {
-  constexpr size_t smem = Layout<T, HPC, NT>::kBytes;
+// operand: swizzled for the products; else plain, for the workers' lanes.
+// Rows as a tensor of (elements, heads, steps, batch rows); heads: those that rows have.
+inline bool make_map(CUtensorMap* map, const RowsArg& a, int size, int heads, int S, int N, bool operand = true) {
+  static const auto encode = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }();
+  if (encode == nullptr) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)size, (cuuint64_t)heads, (cuuint64_t)S, (cuuint64_t)N};
+  // a distance that nothing is away has to be one all the same
+  const cuuint64_t strides[3] = {(cuuint64_t)size * 2, (cuuint64_t)(S > 1 ? a.ss * 2 : 16), (cuuint64_t)(N > 1 ? a.ns * 2 : 16)};
+  const cuuint32_t box[4] = {64, 1, kChunk, 1}, each[4] = {1, 1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, a.p, dims, strides, box, each, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                operand ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// The maps of all passes, where every operand takes them.
+inline bool make_maps(ChunkArgs& args) {
+  const AttnParams& p = args.p;
+  for (int i = 0; i < p.passes; ++i) {
+    const AttnPass& a = p.pass[i];
+    if (!a.q.vec || !a.k.vec || !a.v.vec || (a.o.p && !a.o32 && !a.o.vec) || (a.dot && !a.dot_with.vec)) return false;
+  }
+  for (int i = 0; i < p.passes; ++i) {
+    const AttnPass& a = p.pass[i];
+    if (!make_map(&args.q[i], a.q, a.K, p.H / a.q_of, p.S, p.N) || !make_map(&args.k[i], a.k, a.K, p.H / a.k_of, p.S, p.N) ||
+        !make_map(&args.v[i], a.v, a.V, p.H / a.v_of, p.S, p.N) ||
+        (a.o.p && !a.o32 && !make_map(&args.o[i], a.o, a.V, p.H / a.o_of, p.S, p.N, false)) ||
+        (a.dot && !make_map(&args.with[i], a.dot_with, a.V, p.H / a.o_of, p.S, p.N, false)))
+      return false;
+  }
+  return true;
+}
+
+template <typename T, int HPC, int KB, int NT, bool TMA>
+cudaError_t launch_chunks_of(const ChunkArgs& args, cudaStream_t s, int* launches) {
+  const AttnParams& p = args.p;
+  constexpr size_t smem = Layout<T, HPC, NT, true>::kBytes;
   const long long streams = (long long)p.passes * p.N * ((p.H + HPC - 1) / HPC);
-  auto whole = attn_chunk_kernel<T, HPC, KB, NT, true>;
+  auto whole = attn_chunk_kernel<T, HPC, KB, NT, true, TMA>;
   cudaError_t e = cudaFuncSetAttribute(whole, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   if (p.plan.segments > 1) {
-    auto sums = attn_chunk_kernel<T, HPC, KB, kTerms, false>;
-    constexpr size_t sums_smem = Layout<T, HPC, kTerms>::kBytes;
+    auto sums = attn_chunk_kernel<T, HPC, KB, kTerms, false, TMA>;
+    constexpr size_t sums_smem = Layout<T, HPC, kTerms, false>::kBytes;
     e = cudaFuncSetAttribute(sums, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sums_smem);
     if (e != cudaSuccess) return e;
-    sums<<<(unsigned)(streams * (p.plan.segments - 1)), kThreads, sums_smem, s>>>(p);
+    sums<<<(unsigned)(streams * (p.plan.segments - 1)), kThreads, sums_smem, s>>>(args);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     ++*launches;
     attn_join_kernel<HPC, KB><<<dim3((unsigned)streams, KB * 64 * 128 / 256), 256, 0, s>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     ++*launches;
   }
-  whole<<<(unsigned)(streams * p.plan.segments), kThreads, smem, s>>>(p);
+  whole<<<(unsigned)(streams * p.plan.segments), kThreads, smem, s>>>(args);
   if ((e = cudaGetLastError()) == cudaSuccess) ++*launches;
   return e;
 }
 
-template <typename T, int NT>
-cudaError_t launch_chunks_in(const AttnParams& p, cudaStream_t s, int* launches) {
+template <typename T, int NT, bool TMA>
+cudaError_t launch_chunks_in(const ChunkArgs& args, cudaStream_t s, int* launches) {
   // every pass has the same two sizes, in one order or the other
-  if (p.pass[0].K <= 64 && p.pass[0].V <= 64) return launch_chunks_of<T, 2, 1, NT>(p, s, launches);
-  return p.plan.deep == 64 ? launch_chunks_of<T, 1, 1, NT>(p, s, launches) : launch_chunks_of<T, 1, 2, NT>(p, s, launches);
+  const AttnParams& p = args.p;
+  if (p.pass[0].K <= 64 && p.pass[0].V <= 64) return launch_chunks_of<T, 2, 1, NT, TMA>(args, s, launches);
+  return p.plan.deep == 64 ? launch_chunks_of<T, 1, 1, NT, TMA>(args, s, launches)
+                           : launch_chunks_of<T, 1, 2, NT, TMA>(args, s, launches);
 }
 
 // P and the state as three terms where float32 comes of them: for float32
@@ -872,9 +1199,15 @@ cudaError_t launch_chunks_in(const AttnParams& p, cudaStream_t s, int* launches)
 // sequence.  A 16-bit output keeps less than the 2^-17 of two.
 template <typename T>
 cudaError_t launch_chunks(const AttnParams& p, cudaStream_t s, int* launches) {
+  ChunkArgs args{};
+  args.p = p;
+  if constexpr (kSplit<T> == 1) {
+    if (make_maps(args))
+      return p.gradient ? launch_chunks_in<T, kTerms, true>(args, s, launches) : launch_chunks_in<T, 2, true>(args, s, launches);
+  }
   if constexpr (kSplit<T> < kTerms)
-    if (!p.gradient) return launch_chunks_in<T, 2>(p, s, launches);
-  return launch_chunks_in<T, kTerms>(p, s, launches);
+    if (!p.gradient) return launch_chunks_in<T, 2, false>(args, s, launches);
+  return launch_chunks_in<T, kTerms, false>(args, s, launches);
 }
 
 // Reads and clears the status word, in stream order; the caller synchronises.
