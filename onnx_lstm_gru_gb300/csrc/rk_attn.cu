@@ -94,10 +94,19 @@ __global__ void __launch_bounds__(kStepThreads) attn_step_kernel(AttnParams p, i
 // sums are float64 (they run over the whole sequence); what the float32
 // products leave at the end is known, E_L, and is taken back evenly along the
 // way: with no states to start from or to end at, both ends are exact.
-constexpr int kDecayThreads = 256;
-__device__ __forceinline__ double decay_term(const AttnDecayParams& p, long long head, int t) {
-  return (double)p.of[head * p.S + t] - (double)p.to[head * p.S + t];
-}
+// A block takes kDecayTile steps of one head, with what comes before and in all
+// added up by itself: pairs of float32 that keep what each addition rounds
+// away (Knuth's two-sum), which the card's few float64 units do not wait for.
+constexpr int kDecayThreads = 256, kDecayEach = 4, kDecayTile = kDecayThreads * kDecayEach;
+struct Exact {
+  float hi = 0.0f, lo = 0.0f;
+  __device__ __forceinline__ void add(float x) {
+    const float s = hi + x, b = s - hi;
+    lo += (hi - (s - b)) + (x - b);
+    hi = s;
+  }
+  __device__ __forceinline__ double value() const { return (double)hi + (double)lo; }
+};
 // Every thread gets the block's sum.
 __device__ __forceinline__ double decay_sum(double x, double* sums) {
 #pragma unroll
@@ -109,59 +118,69 @@ __device__ __forceinline__ double decay_sum(double x, double* sums) {
   for (int i = 1; i < kDecayThreads / 32; ++i) x += sums[i];
   return x;
 }
-__global__ void __launch_bounds__(kDecayThreads) attn_decay_kernel(AttnDecayParams p) {
-  __shared__ double sums[kDecayThreads / 32], carry;
-  const int h = (int)(blockIdx.x % p.H), n = (int)(blockIdx.x / p.H);
+__global__ void __launch_bounds__(kDecayThreads) attn_decay_kernel(AttnDecayParams p, int tiles) {
+  __shared__ double sums[kDecayThreads / 32];
+  const long long head = blockIdx.x / tiles;
+  const int tile = (int)(blockIdx.x - head * tiles), h = (int)(head % p.H), n = (int)(head / p.H);
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int L = row_length(p.lens, n, p.S);
-  const long long head = (long long)n * p.H + h;
+  const int L = row_length(p.lens, n, p.S), begin = min(tile * kDecayTile, L);
   float* out = static_cast<float*>(p.dDecay.p) + n * p.dDecay.ns + h;
   const float* g = static_cast<const float*>(p.decay.p) + n * p.decay.ns + h;
+  const float* to = p.to + head * p.S;
+  const float* of = p.of + head * p.S;
   const float bias = p.bias ? p.bias[h] : 0.0f;
+  Exact before, rest;
+  for (int t = threadIdx.x; t < begin; t += kDecayThreads) before.add(of[t]), before.add(-to[t]);
+  for (int t = begin + threadIdx.x; t < L; t += kDecayThreads) rest.add(of[t]), rest.add(-to[t]);
   const double first = p.first ? p.first[head] : 0.0, last = p.last ? p.last[head] : 0.0;
-  double all = 0.0;
-  for (int t = threadIdx.x; t < L; t += kDecayThreads) all += decay_term(p, head, t);
-  all = decay_sum(all, sums);
+  const double so_far = decay_sum(before.value(), sums), all = so_far + decay_sum(rest.value(), sums);
   const double back = L > 0 ? (last - first - all) / L : 0.0;
-  double run = first, total = 0.0;
-  for (int base = 0; base < L; base += kDecayThreads) {
-    const int t = base + threadIdx.x;
-    const double own = t < L ? decay_term(p, head, t) : 0.0;
-    double x = own;
+  const int t0 = begin + threadIdx.x * kDecayEach;
+  double own[kDecayEach], x = 0.0, total = 0.0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
+  for (int i = 0; i < kDecayEach; ++i) {
+    own[i] = x;
+    if (t0 + i < L) x += (double)of[t0 + i] - (double)to[t0 + i];
+  }
+  double scan = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double y = __shfl_up_sync(0xffffffffu, scan, o);
+    if (lane >= o) scan += y;
+  }
+  __syncthreads();
+  if (lane == 31) sums[warp] = scan;
+  __syncthreads();
+  scan += first + so_far - x;
+  for (int i = 0; i < warp; ++i) scan += sums[i];
+  if (begin == tile * kDecayTile) {
+#pragma unroll
+    for (int i = 0; i < kDecayEach; ++i) {
+      const int t = t0 + i;
+      if (t < L) {
+        // a decay of 0 has no gradient: the factor itself is in it
+        const float d = (p.decay.p ? g[t * p.decay.ss] : 0.0f) + bias;
+        const double y = d < -104.0f ? 0.0 : scan + own[i] + back * t;
+        if (p.dDecay.p) out[t * p.dDecay.ss] = (float)y;
+        total += y;
+      }
     }
-    __syncthreads();
-    if (lane == 31) sums[warp] = x;
-    __syncthreads();
-    for (int i = 0; i < warp; ++i) x += sums[i];
-    x += run;
-    if (threadIdx.x == kDecayThreads - 1) carry = x;
-    if (t < L) {
-      // a decay of 0 has no gradient: the factor itself is in it
-      const float d = (p.decay.p ? g[t * p.decay.ss] : 0.0f) + bias;
-      const double y = d < -104.0f ? 0.0 : x - own + back * t;
-      if (p.dDecay.p) out[t * p.dDecay.ss] = (float)y;
-      total += y;
-    }
-    __syncthreads();
-    run = carry;
   }
   if (p.dDecay.p)
-    for (int t = L + threadIdx.x; t < p.S; t += kDecayThreads) out[t * p.dDecay.ss] = 0.0f;
+    for (int t = tile * kDecayTile + threadIdx.x; t < min((tile + 1) * kDecayTile, p.S); t += kDecayThreads)
+      if (t >= L) out[t * p.dDecay.ss] = 0.0f;
   if (p.partial) {
     total = decay_sum(total, sums);
-    if (threadIdx.x == 0) p.partial[head] = total;
+    if (threadIdx.x == 0) p.partial[blockIdx.x] = total;
   }
 }
 
-__global__ void __launch_bounds__(256) attn_decay_bias_kernel(AttnDecayParams p) {
+__global__ void __launch_bounds__(256) attn_decay_bias_kernel(AttnDecayParams p, int tiles) {
   const int h = blockIdx.x * 8 + threadIdx.x / 32, lane = threadIdx.x % 32;
   if (h >= p.H) return;
   double x = 0.0;
-  for (int n = lane; n < p.N; n += 32) x += p.partial[(long long)n * p.H + h];
+  for (long long i = lane; i < (long long)p.N * tiles; i += 32)
+    x += p.partial[(i / tiles * p.H + h) * tiles + i % tiles];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   if (lane == 0) p.dbias[h] = (float)x;
@@ -245,13 +264,18 @@ long long attn_plan_scratch(const AttnPlan& plan, long long batch, long long hea
   return streams * plan.segments * (plan.deep * 128LL + 4);
 }
 
+int attn_decay_tiles(long long seq) { return (int)((seq + kDecayTile - 1) / kDecayTile); }
+
 cudaError_t launch_attn_decay(const AttnDecayParams& p, cudaStream_t s, int* launches) {
-  attn_decay_kernel<<<(unsigned)((long long)p.N * p.H), kDecayThreads, 0, s>>>(p);
+  const int tiles = attn_decay_tiles(p.S);
+  const long long blocks = (long long)p.N * p.H * tiles;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  attn_decay_kernel<<<(unsigned)blocks, kDecayThreads, 0, s>>>(p, tiles);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   ++*launches;
   if (p.dbias == nullptr) return e;
-  attn_decay_bias_kernel<<<(p.H + 7) / 8, 256, 0, s>>>(p);
+  attn_decay_bias_kernel<<<(p.H + 7) / 8, 256, 0, s>>>(p, tiles);
   e = cudaGetLastError();
   if (e == cudaSuccess) ++*launches;
   return e;

@@ -108,9 +108,10 @@ struct AttnDecayParams {
   const float* of;
   const float* first;  // [N][H], or null: the state's product with its gradient before the first step
   const float* last;   // and behind the last
-  double* partial;     // [N][H]
+  double* partial;     // [N][H][tiles]
   float* dbias;        // [H], or null
 };
+int attn_decay_tiles(long long seq);
 cudaError_t launch_attn_decay(const AttnDecayParams& p, cudaStream_t s, int* launches);
 
 // o = sums over the heads that share of o32.

@@ -138,7 +138,7 @@ GradPlan grad_plan(const rk_attn_problem* p) {
   GradPlan g{};
   g.to = g.of = four(rows);
   g.cross = four(2 * heads);
-  g.partial = four(2 * heads);
+  g.partial = four(2 * heads * rk::attn_decay_tiles(p->seq));
   if (shared(p->heads, p->query_heads) > 1) g.q32 = four(rows * p->key_size);
   if (shared(p->heads, p->key_heads) > 1) g.k32 = four(rows * p->key_size);
   if (shared(p->heads, p->value_heads) > 1) g.v32 = four(rows * p->value_size);

@@ -47,70 +47,119 @@ __device__ __forceinline__ unsigned long long turn_of(float f) {
   const double r = t - floor(t);
   return __double2ull_rz(r * 18446744073709551616.0);
 }
+// Every pair's turn, taken once by a block: float64 is slow here.
+struct Turns {
+  unsigned long long step[128];
+  bool none[128];  // the frequency is infinite or NaN
+  __device__ __forceinline__ void fill(const QkParams& p) {
+    for (int i = threadIdx.x; i < p.rotary / 2; i += kQkThreads) {
+      step[i] = turn_of(p.freq[i]);
+      none[i] = !(fabsf(p.freq[i]) <= 3.402823466e38f);
+    }
+    __syncthreads();
+  }
+};
+
+// Cosine and sine of a turn.  The special function unit's are off by 2^-20 at
+// most within half a turn, which no 16-bit element keeps.
+template <typename T>
 __device__ __forceinline__ void turn(unsigned long long step, int position, float& c, float& s) {
   const long long phase = (long long)(step * (unsigned long long)(long long)position);
-  sincospif((float)phase * 1.0842021724855044e-19f, &s, &c);  // 2^-63: in half turns
+  if constexpr (sizeof(T) == 4) {
+    sincospif((float)phase * 1.0842021724855044e-19f, &s, &c);  // 2^-63: in half turns
+  } else {
+    const float angle = (float)(int)(phase >> 32) * (float)(3.14159265358979323846 / 2147483648.0);
+    s = __sinf(angle), c = __cosf(angle);
+  }
 }
 
-// LPH lanes hold a head's units, U each; pieces of V elements.
+// A lane's units of a head: LPH lanes hold them, U each, in pieces of V
+// elements.  Values are kept as packed pairs along V: a[j] the first elements
+// of two of the rotated pairs, b[j] the second ones.
 template <typename T, int V, int LPH, int U>
 struct Lane {
+  static constexpr int J = (V + 1) / 2;
+  using Raw = Packed<T, V>;
   int a[U], b[U], pair[U];
-  unsigned long long step[U][V];
-  __device__ __forceinline__ void init(const QkParams& p, int sub) {
+  const Turns* table;
+  F2 c[U][J], s[U][J];  // of the position they were last taken for
+  int position;
+  bool known;
+  __device__ __forceinline__ Lane(const QkParams& p, int sub, const Turns* turns) : table(turns), known(false) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const Unit x = unit_of<V>(sub + u * LPH, p.size, p.rotary, p.interleaved);
       a[u] = x.a, b[u] = x.b, pair[u] = x.pair;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int j = pair[u] + i;
-        step[u][i] = a[u] >= 0 && j < p.rotary / 2 ? turn_of(p.freq[j]) : 0;
-      }
     }
   }
+  __device__ __forceinline__ bool turns(const QkParams& p, int u, int i) const { return pair[u] + i < p.rotary / 2; }
+  // Rows at the same position, which whole batches are at, share their angles.
   // An infinite or NaN frequency has no turn: its pairs are NaN.
-  __device__ __forceinline__ void angles(const QkParams& p, int position, float (&c)[U][V], float (&s)[U][V]) const {
+  __device__ __forceinline__ void angles(const QkParams& p, int at) {
+    if (known && at == position) return;
+    known = true, position = at;
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int j = pair[u] + i;
-        c[u][i] = 1.0f, s[u][i] = 0.0f;
-        if (a[u] >= 0 && j < p.rotary / 2) {
-          turn(step[u][i], position, c[u][i], s[u][i]);
-          const float f = p.freq[j];
-          if (!(fabsf(f) <= 3.402823466e38f)) c[u][i] = s[u][i] = __int_as_float(0x7fffffff);
+      for (int j = 0; j < J; ++j) {
+        float cs[2] = {1.0f, 1.0f}, sn[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int i = 2 * j + e;
+          if (i < V && a[u] >= 0 && turns(p, u, i)) {
+            turn<T>(table->step[pair[u] + i], at, cs[e], sn[e]);
+            if (table->none[pair[u] + i]) cs[e] = sn[e] = __int_as_float(0x7fffffff);
+          }
         }
+        c[u][j] = f2(cs[0], cs[1]), s[u][j] = f2(sn[0], sn[1]);
       }
   }
-  __device__ __forceinline__ bool turns(const QkParams& p, int u, int i) const { return pair[u] + i < p.rotary / 2; }
+  // A unit's two pieces of a head's row as read.
+  __device__ __forceinline__ void read(const T* row, int u, bool on, Raw (&x)[2]) const {
+    if (on && a[u] >= 0) x[0].load(row + a[u]);
+    else x[0].raw = {};
+    if (on && b[u] >= 0) x[1].load(row + b[u]);
+    else x[1].raw = {};
+  }
+  __device__ __forceinline__ static void widen(bool interleaved, const Raw (&x)[2], F2 (&va)[J], F2 (&vb)[J]) {
+    float e[2 * V];
+    {
+      float lo[V], hi[V];
+      x[0].widen(lo), x[1].widen(hi);
+#pragma unroll
+      for (int i = 0; i < V; ++i) e[i] = lo[i], e[V + i] = hi[i];
+    }
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int i = 2 * j, k = V > 1 ? i + 1 : i;
+      const float y = V > 1 ? 1.0f : 0.0f;
+      va[j] = f2(interleaved ? e[2 * i] : e[i], V > 1 ? (interleaved ? e[2 * k] : e[k]) : y);
+      vb[j] = f2(interleaved ? e[2 * i + 1] : e[V + i], V > 1 ? (interleaved ? e[2 * k + 1] : e[V + k]) : y);
+    }
+  }
+  __device__ __forceinline__ void write(T* row, int u, bool on, bool interleaved, const F2 (&va)[J], const F2 (&vb)[J]) const {
+    float e[2][V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float2 x = f2_get(va[i / 2]), y = f2_get(vb[i / 2]);
+      const float fa = i % 2 ? x.y : x.x, fb = i % 2 ? y.y : y.x;
+      e[0][i] = fa, e[1][i] = fb;
+    }
+    if (interleaved) {
+      float z[2][V];
+#pragma unroll
+      for (int i = 0; i < 2 * V; ++i) z[i / V][i % V] = e[i % 2][i / 2];
+#pragma unroll
+      for (int i = 0; i < V; ++i) e[0][i] = z[0][i], e[1][i] = z[1][i];
+    }
+    if (on && a[u] >= 0) Piece<T, V>::store(row + a[u], e[0]);
+    if (on && b[u] >= 0) Piece<T, V>::store(row + b[u], e[1]);
+  }
 };
-
-// A unit's elements as pairs x[0] (a) and x[1] (b).
-template <typename T, int V>
-__device__ __forceinline__ void load_unit(const T* row, int a, int b, bool interleaved, float (&x)[2][V]) {
-  float e[2][V];
-  fill(e[0], 0.0f);
-  fill(e[1], 0.0f);
-  if (a >= 0) Piece<T, V>::load(row + a, e[0]);
-  if (b >= 0) Piece<T, V>::load(row + b, e[1]);
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    x[0][i] = interleaved ? e[2 * i / V][2 * i % V] : e[0][i];
-    x[1][i] = interleaved ? e[(2 * i + 1) / V][(2 * i + 1) % V] : e[1][i];
-  }
-}
-template <typename T, int V>
-__device__ __forceinline__ void store_unit(T* row, int a, int b, bool interleaved, const float (&x)[2][V]) {
-  float e[2][V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    e[0][i] = interleaved ? x[i % 2][i / 2] : x[0][i];
-    e[1][i] = interleaved ? x[(V + i) % 2][(V + i) / 2] : x[1][i];
-  }
-  if (a >= 0) Piece<T, V>::store(row + a, e[0]);
-  if (b >= 0) Piece<T, V>::store(row + b, e[1]);
+__device__ __forceinline__ F2 negated(F2 x) { return mul2(x, f2(-1.0f, -1.0f)); }
+__device__ __forceinline__ float sum_of(F2 x) {
+  const float2 v = f2_get(x);
+  return v.x + v.y;
 }
 
 template <int LPH>
@@ -120,13 +169,19 @@ __device__ __forceinline__ float head_sum(float v) {
   return v;
 }
 
-// Row r of the layout as step and batch row, and whether it holds work.
-__device__ __forceinline__ bool row_of(const QkParams& p, long long r, int& s, int& n) {
-  const int inner = p.layout == 0 ? p.N : p.S;
-  const int o = (int)(r / inner), i = (int)(r - (long long)o * inner);
-  s = p.layout == 0 ? o : i;
-  n = p.layout == 0 ? i : o;
+// Row number i in the order that they are taken in, as step and batch row, and
+// whether it holds work.  Without positions the rows of a step, which are at
+// the same one, follow each other in either layout.
+__device__ __forceinline__ bool row_of(const QkParams& p, long long i, int& s, int& n) {
+  const bool by_step = p.layout == 0 || p.positions == nullptr;
+  const int inner = by_step ? p.N : p.S;
+  const int o = (int)(i / inner), k = (int)(i - (long long)o * inner);
+  s = by_step ? o : k;
+  n = by_step ? k : o;
   return s < row_length(p.lens, n, p.S);
+}
+__device__ __forceinline__ int position_of(const QkParams& p, int s, int n) {
+  return p.positions ? p.positions[p.layout == 0 ? (long long)s * p.N + n : (long long)n * p.S + s] : s;
 }
 
 __device__ __forceinline__ float inverse(const QkParams& p, float square) {
@@ -134,56 +189,76 @@ __device__ __forceinline__ float inverse(const QkParams& p, float square) {
   return 1.0f / sqrtf((p.norm == 1 ? square / (float)p.size : square) + p.epsilon);
 }
 
+// A warp takes consecutive rows, and a row's heads in turns of kHeads, queries
+// first; a turn's elements are on their way while the one before is computed.
 template <typename T, int V, int LPH, int U>
-__global__ void __launch_bounds__(kQkThreads) qk_kernel(QkParams p) {
-  constexpr int kHeads = 32 / LPH;  // heads that a warp takes at a time
+__global__ void __launch_bounds__(kQkThreads, U > 1 ? 1 : V == 8 ? 2 : 3) qk_kernel(QkParams p) {
+  constexpr int kHeads = 32 / LPH;
+  using L = Lane<T, V, LPH, U>;
+  constexpr int J = L::J;
   const int lane = threadIdx.x % 32, sub = lane % LPH;
-  Lane<T, V, LPH, U> l;
-  l.init(p, sub);
-  const long long rows = (long long)p.S * p.N * p.share;
+  __shared__ Turns turns;
+  turns.fill(p);
+  L l(p, sub, &turns);
+  const long long items = (long long)p.S * p.N * p.share, warps = (long long)gridDim.x * kQkWarps;
+  const long long per = (items + warps - 1) / warps, first = ((long long)blockIdx.x * kQkWarps + threadIdx.x / 32) * per;
   const bool il = p.interleaved;
-  for (long long w = (long long)blockIdx.x * kQkWarps + threadIdx.x / 32; w < rows; w += (long long)gridDim.x * kQkWarps) {
-    const long long r = w / p.share;
-    const int part = (int)(w - r * p.share);
+  typename L::Raw w[2][U][2];
+#pragma unroll
+  for (int side = 0; side < 2; ++side)
+#pragma unroll
+    for (int u = 0; u < U; ++u) l.read(static_cast<const T*>(p.side[side].scale), u, p.side[side].scale != nullptr, w[side][u]);
+  const long long last = min(first + per, items);
+#pragma unroll 1
+  for (long long item = first; item < last; ++item) {
+    const long long r = p.share == 1 ? item : item / p.share;
+    const int part = (int)(item - r * p.share);
     int s, n;
     const bool live = row_of(p, r, s, n);
-    float c[U][V], sn[U][V];
-    if (live) l.angles(p, p.positions ? p.positions[r] : s, c, sn);
-#pragma unroll 1
+    if (live) l.angles(p, position_of(p, s, n));
+#pragma unroll
     for (int side = 0; side < 2; ++side) {
       const QkSide& q = p.side[side];
       if (q.Y.p == nullptr) continue;
       const T* X = static_cast<const T*>(q.X.p) + s * q.X.ss + n * q.X.ns;
       T* Y = static_cast<T*>(q.Y.p) + s * q.Y.ss + n * q.Y.ns;
-      const T* W = static_cast<const T*>(q.scale);
-#pragma unroll 2
-      for (int h0 = part * kHeads; h0 < q.heads; h0 += kHeads * p.share) {
-        const int h = h0 + lane / LPH;
-        const bool on = h < q.heads;
-        float x[U][2][V];
-        float square = 0.0f;
+      const int skip = kHeads * p.share;
+      int h = part * kHeads + lane / LPH;
+      typename L::Raw x[U][2];
+#pragma unroll
+      for (int u = 0; u < U; ++u) l.read(X + h * p.size, u, live && h < q.heads, x[u]);
+#pragma unroll 1
+      for (int h0 = part * kHeads; h0 < q.heads; h0 += skip, h += skip) {
+        typename L::Raw next[U][2];
+#pragma unroll
+        for (int u = 0; u < U; ++u) l.read(X + (h + skip) * p.size, u, live && h + skip < q.heads, next[u]);
+        F2 a[U][J], b[U][J], square = f2(0.0f, 0.0f);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          load_unit<T, V>(X + (long long)h * p.size, on && live ? l.a[u] : -1, on && live ? l.b[u] : -1, il, x[u]);
+          L::widen(il, x[u], a[u], b[u]);
+          if constexpr (V == 1) a[u][0] = mul2(a[u][0], f2(1.0f, 0.0f)), b[u][0] = mul2(b[u][0], f2(1.0f, 0.0f));
 #pragma unroll
-          for (int i = 0; i < V; ++i) square = fmaf(x[u][0][i], x[u][0][i], fmaf(x[u][1][i], x[u][1][i], square));
+          for (int j = 0; j < J; ++j) square = fma2(a[u][j], a[u][j], fma2(b[u][j], b[u][j], square));
         }
-        const float inv = inverse(p, p.norm ? head_sum<LPH>(square) : 0.0f);
+        const float inv = inverse(p, p.norm ? head_sum<LPH>(sum_of(square)) : 0.0f);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           if (live) {
-            float sc[2][V];
-            if (W) load_unit<T, V>(W, l.a[u], l.b[u], il, sc);
+            F2 wa[J], wb[J];
+            L::widen(il, w[side][u], wa, wb);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-              float a = x[u][0][i] * inv, b = x[u][1][i] * inv;
-              if (W) a *= sc[0][i], b *= sc[1][i];
-              const bool t = l.turns(p, u, i);
-              x[u][0][i] = t ? a * c[u][i] - b * sn[u][i] : a;
-              x[u][1][i] = t ? b * c[u][i] + a * sn[u][i] : b;
+            for (int j = 0; j < J; ++j) {
+              F2 va = mul2(a[u][j], f2(inv, inv)), vb = mul2(b[u][j], f2(inv, inv));
+              if (q.scale) va = mul2(va, wa[j]), vb = mul2(vb, wb[j]);
+              F2 ta = fma2(va, l.c[u][j], negated(mul2(vb, l.s[u][j]))), tb = fma2(vb, l.c[u][j], mul2(va, l.s[u][j]));
+              // pairs that stay are left as they are, infinities too
+              const float2 x0 = f2_get(va), y0 = f2_get(vb), x1 = f2_get(ta), y1 = f2_get(tb);
+              const bool t0 = l.turns(p, u, 2 * j), t1 = l.turns(p, u, 2 * j + 1);
+              a[u][j] = f2(t0 ? x1.x : x0.x, t1 ? x1.y : x0.y), b[u][j] = f2(t0 ? y1.x : y0.x, t1 ? y1.y : y0.y);
             }
           }
-          store_unit<T, V>(Y + (long long)h * p.size, on ? l.a[u] : -1, on ? l.b[u] : -1, il, x[u]);
+          l.write(Y + h * p.size, u, h < q.heads, il, a[u], b[u]);
+          x[u][0] = next[u][0], x[u][1] = next[u][1];
         }
       }
     }
@@ -191,107 +266,128 @@ __global__ void __launch_bounds__(kQkThreads) qk_kernel(QkParams p) {
 }
 
 template <typename T, int V, int LPH, int U>
-__global__ void __launch_bounds__(kQkThreads) qk_grad_kernel(QkParams p) {
+__global__ void __launch_bounds__(kQkThreads, U == 1 ? 2 : 1) qk_grad_kernel(QkParams p) {
   constexpr int kHeads = 32 / LPH;
+  using L = Lane<T, V, LPH, U>;
+  constexpr int J = L::J;
   const int lane = threadIdx.x % 32, sub = lane % LPH;
-  Lane<T, V, LPH, U> l;
-  l.init(p, sub);
-  const long long rows = (long long)p.S * p.N;
+  __shared__ Turns turns;
+  turns.fill(p);
+  L l(p, sub, &turns);
+  const long long rows = (long long)p.S * p.N, warps = (long long)gridDim.x * kQkWarps;
+  const long long per = (rows + warps - 1) / warps, first = ((long long)blockIdx.x * kQkWarps + threadIdx.x / 32) * per;
+  const long long last = min(first + per, rows);
   const bool il = p.interleaved;
-  float dw[2][U][2][V];
-#pragma unroll
-  for (int u = 0; u < U; ++u)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) fill(dw[0][u][j], 0.0f), fill(dw[1][u][j], 0.0f);
   const float m = p.norm == 1 ? 1.0f / (float)p.size : 1.0f;
-  for (long long r = (long long)blockIdx.x * kQkWarps + threadIdx.x / 32; r < rows; r += (long long)gridDim.x * kQkWarps) {
-    int s, n;
-    const bool live = row_of(p, r, s, n);
-    float c[U][V], sn[U][V];
-    if (live) l.angles(p, p.positions ? p.positions[r] : s, c, sn);
-#pragma unroll
-    for (int side = 0; side < 2; ++side) {
-      const QkSide& q = p.side[side];
-      if (q.dX.p == nullptr && q.dscale == nullptr) continue;
-      const T* X = static_cast<const T*>(q.X.p) + s * q.X.ss + n * q.X.ns;
-      const T* dY = static_cast<const T*>(q.dY.p) + s * q.dY.ss + n * q.dY.ns;
-      T* dX = static_cast<T*>(q.dX.p) + s * q.dX.ss + n * q.dX.ns;
-      const T* W = static_cast<const T*>(q.scale);
 #pragma unroll 1
-      for (int h0 = 0; h0 < q.heads; h0 += kHeads) {
-        const int h = h0 + lane / LPH;
-        const bool on = h < q.heads, work = on && live;
-        float x[U][2][V], g[U][2][V];
-        float square = 0.0f, dot = 0.0f;
+  for (int side = 0; side < 2; ++side) {
+    const QkSide& q = p.side[side];
+    typename L::Raw w[U][2];
+    F2 dwa[U][J], dwb[U][J];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      l.read(static_cast<const T*>(q.scale), u, q.scale != nullptr, w[u]);
+#pragma unroll
+      for (int j = 0; j < J; ++j) dwa[u][j] = dwb[u][j] = f2(0.0f, 0.0f);
+    }
+    if (q.dX.p || q.dscale) {
+#pragma unroll 1
+      for (long long r = first; r < last; ++r) {
+        int s, n;
+        const bool live = row_of(p, r, s, n);
+        if (live) l.angles(p, position_of(p, s, n));
+        const T* X = static_cast<const T*>(q.X.p) + s * q.X.ss + n * q.X.ns;
+        const T* dY = static_cast<const T*>(q.dY.p) + s * q.dY.ss + n * q.dY.ns;
+        T* dX = static_cast<T*>(q.dX.p) + s * q.dX.ss + n * q.dX.ns;
+        int h = lane / LPH;
+        typename L::Raw x[U][2], g[U][2];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          load_unit<T, V>(X + (long long)h * p.size, work ? l.a[u] : -1, work ? l.b[u] : -1, il, x[u]);
-          load_unit<T, V>(dY + (long long)h * p.size, work ? l.a[u] : -1, work ? l.b[u] : -1, il, g[u]);
-#pragma unroll
-          for (int i = 0; i < V; ++i) square = fmaf(x[u][0][i], x[u][0][i], fmaf(x[u][1][i], x[u][1][i], square));
+          l.read(X + h * p.size, u, live && h < q.heads, x[u]);
+          l.read(dY + h * p.size, u, live && h < q.heads, g[u]);
         }
-        const float inv = inverse(p, p.norm ? head_sum<LPH>(square) : 0.0f);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if (live) {
-            float sc[2][V];
-            if (W) load_unit<T, V>(W, l.a[u], l.b[u], il, sc);
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-              const float a = g[u][0][i], b = g[u][1][i];
-              const bool t = l.turns(p, u, i);
-              const float ga = t ? a * c[u][i] + b * sn[u][i] : a, gb = t ? b * c[u][i] - a * sn[u][i] : b;
-              if (work) {
-                dw[side][u][0][i] = fmaf(ga, x[u][0][i] * inv, dw[side][u][0][i]);
-                dw[side][u][1][i] = fmaf(gb, x[u][1][i] * inv, dw[side][u][1][i]);
-              }
-              g[u][0][i] = W ? ga * sc[0][i] : ga;
-              g[u][1][i] = W ? gb * sc[1][i] : gb;
-              dot = fmaf(g[u][0][i], x[u][0][i], fmaf(g[u][1][i], x[u][1][i], dot));
-            }
-          }
-        }
-        // inv (dot / m) inv inv x, from the left: inv^3 alone may pass float32's range
-        const float f = p.norm ? inv * (head_sum<LPH>(dot) * m) * inv : 0.0f;
-        if (q.dX.p) {
+#pragma unroll 1
+        for (int h0 = 0; h0 < q.heads; h0 += kHeads, h += kHeads) {
+          typename L::Raw x1[U][2], g1[U][2];
 #pragma unroll
           for (int u = 0; u < U; ++u) {
-            if (live) {
+            l.read(X + (h + kHeads) * p.size, u, live && h + kHeads < q.heads, x1[u]);
+            l.read(dY + (h + kHeads) * p.size, u, live && h + kHeads < q.heads, g1[u]);
+          }
+          F2 a[U][J], b[U][J], ga[U][J], gb[U][J], square = f2(0.0f, 0.0f), dot = f2(0.0f, 0.0f);
 #pragma unroll
-              for (int i = 0; i < V; ++i) {
-                g[u][0][i] = inv * (p.norm ? g[u][0][i] - f * x[u][0][i] : g[u][0][i]);
-                g[u][1][i] = inv * (p.norm ? g[u][1][i] - f * x[u][1][i] : g[u][1][i]);
+          for (int u = 0; u < U; ++u) {
+            L::widen(il, x[u], a[u], b[u]);
+            L::widen(il, g[u], ga[u], gb[u]);
+            if constexpr (V == 1) {
+              a[u][0] = mul2(a[u][0], f2(1.0f, 0.0f)), b[u][0] = mul2(b[u][0], f2(1.0f, 0.0f));
+              ga[u][0] = mul2(ga[u][0], f2(1.0f, 0.0f)), gb[u][0] = mul2(gb[u][0], f2(1.0f, 0.0f));
+            }
+#pragma unroll
+            for (int j = 0; j < J; ++j) square = fma2(a[u][j], a[u][j], fma2(b[u][j], b[u][j], square));
+          }
+          const float inv = inverse(p, p.norm ? head_sum<LPH>(sum_of(square)) : 0.0f);
+          if (live) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              F2 wa[J], wb[J];
+              L::widen(il, w[u], wa, wb);
+#pragma unroll
+              for (int j = 0; j < J; ++j) {
+                const F2 ta = fma2(ga[u][j], l.c[u][j], mul2(gb[u][j], l.s[u][j]));
+                const F2 tb = fma2(gb[u][j], l.c[u][j], negated(mul2(ga[u][j], l.s[u][j])));
+                const float2 x0 = f2_get(ga[u][j]), y0 = f2_get(gb[u][j]), x2 = f2_get(ta), y2 = f2_get(tb);
+                const bool t0 = l.turns(p, u, 2 * j), t1 = l.turns(p, u, 2 * j + 1);
+                F2 va = f2(t0 ? x2.x : x0.x, t1 ? x2.y : x0.y), vb = f2(t0 ? y2.x : y0.x, t1 ? y2.y : y0.y);
+                a[u][j] = mul2(a[u][j], f2(inv, inv)), b[u][j] = mul2(b[u][j], f2(inv, inv));  // x inv from here on
+                if (h < q.heads) dwa[u][j] = fma2(va, a[u][j], dwa[u][j]), dwb[u][j] = fma2(vb, b[u][j], dwb[u][j]);
+                if (q.scale) va = mul2(va, wa[j]), vb = mul2(vb, wb[j]);
+                ga[u][j] = va, gb[u][j] = vb;
+                dot = fma2(va, a[u][j], fma2(vb, b[u][j], dot));
               }
             }
-            store_unit<T, V>(dX + (long long)h * p.size, on ? l.a[u] : -1, on ? l.b[u] : -1, il, g[u]);
+          }
+          // inv (g - (x inv) sum(g x inv) / m): x inv is of the head's own size, and inv^3 alone may pass float32's range
+          const float f = p.norm ? -head_sum<LPH>(sum_of(dot)) * m : 0.0f;
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            if (q.dX.p) {
+              if (live) {
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                  if (p.norm) ga[u][j] = fma2(f2(f, f), a[u][j], ga[u][j]), gb[u][j] = fma2(f2(f, f), b[u][j], gb[u][j]);
+                  ga[u][j] = mul2(ga[u][j], f2(inv, inv)), gb[u][j] = mul2(gb[u][j], f2(inv, inv));
+                }
+              }
+              l.write(dX + h * p.size, u, h < q.heads, il, ga[u], gb[u]);
+            }
+            x[u][0] = x1[u][0], x[u][1] = x1[u][1], g[u][0] = g1[u][0], g[u][1] = g1[u][1];
           }
         }
       }
     }
-  }
-  if (p.partial == nullptr) return;
-  // the block's sums: over the head groups of a warp, then over the warps
-  __shared__ float sums[kQkWarps][256];
-#pragma unroll 1
-  for (int side = 0; side < 2; ++side) {
+    if (p.partial == nullptr) continue;
+    // the block's sums: over the head groups of a warp, then over the warps
+    __shared__ float sums[kQkWarps][256];
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          float v = side ? dw[1][u][j][i] : dw[0][u][j][i];
+          const float2 y = f2_get(j ? dwb[u][i / 2] : dwa[u][i / 2]);
+          float v = i % 2 ? y.y : y.x;
 #pragma unroll
           for (int o = 16; o >= LPH; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-          const int at = il ? (2 * i + j < V ? l.a[u] + 2 * i + j : l.b[u] + 2 * i + j - V) : (j ? l.b[u] : l.a[u]) + i;
-          const bool is = il ? (2 * i + j < V ? l.a[u] : l.b[u]) >= 0 : (j ? l.b[u] : l.a[u]) >= 0;
-          if (lane < LPH && is) sums[threadIdx.x / 32][at] = v;
+          const int e = il ? 2 * i + j : i;  // place in the two pieces, or in its own
+          const int from = il ? (e < V ? l.a[u] : l.b[u]) : (j ? l.b[u] : l.a[u]);
+          if (lane < LPH && from >= 0) sums[threadIdx.x / 32][from + (il && e >= V ? e - V : e)] = v;
         }
     __syncthreads();
     for (int i = threadIdx.x; i < p.size; i += kQkThreads) {
       float v = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kQkWarps; ++w) v += sums[w][i];
+      for (int x = 0; x < kQkWarps; ++x) v += sums[x][i];
       p.partial[((long long)blockIdx.x * 2 + side) * p.size + i] = v;
     }
     __syncthreads();
@@ -323,7 +419,7 @@ cudaError_t launch_form(const QkParams& p, cudaStream_t s) {
   } else {
     const long long warps = (long long)p.S * p.N * p.share;
     const long long blocks = (warps + kQkWarps - 1) / kQkWarps;
-    qk_kernel<T, V, LPH, U><<<(unsigned)std::min<long long>(blocks, kPlanSms * 8), kQkThreads, 0, s>>>(p);
+    qk_kernel<T, V, LPH, U><<<(unsigned)std::min<long long>(blocks, kPlanSms * (V == 8 ? 2 : 3)), kQkThreads, 0, s>>>(p);
   }
   return cudaGetLastError();
 }
@@ -377,7 +473,7 @@ int qk_piece(int eb, int size, int rotary, int interleaved) {
 }
 
 int qk_grad_blocks(long long rows) {
-  return (int)std::max<long long>(1, std::min<long long>((rows + kQkWarps - 1) / kQkWarps, kPlanSms * 3));
+  return (int)std::max<long long>(1, std::min<long long>((rows + kQkWarps - 1) / kQkWarps, kPlanSms * 2));
 }
 
 cudaError_t launch_qk(const QkParams& p, cudaStream_t s) { return launch_any<false>(p, s); }
