@@ -30,14 +30,16 @@
 //
 // A block runs one state (two, stacked along the lanes, where heads have at
 // most 64 elements: of the products' 128 x 128 blocks the diagonal ones are
-// used) over a piece of the sequence.  Sixteen warps compute; four more issue
-// the products, copy tiles in and out (TMA, for bfloat16 rows of whole 16-byte
-// pieces; else the workers do), and take the decays of later chunks.  They
-// meet at mbarriers, and the products of one chunk run while the next one's
-// operands are made ready:
-//   workers:   P_i | state += U_i | ck K of i + 1 | outputs of i | P_(i+1) ...
-//   products:  O_i after P_i; S_(i+1), U_(i+1) after ck K; Oi_(i+1) after the
-//              outputs of i
+// used) over a piece of the sequence, in groups of warps that meet at
+// mbarriers:
+//   eight read S, write P and hand out the outputs;
+//   eight keep the state, add U to it and scale K for the next chunk;
+//   one issues the products, one copies tiles in and out (TMA, for bfloat16
+//   rows of whole 16-byte pieces; else the first sixteen do), and one for each
+//   head takes the decays of later chunks.
+// The products of one chunk run while the next one's operands are made ready:
+// O_i follows P_i; S_(i+1) and U_(i+1) follow ck K; Oi_(i+1) follows the
+// outputs of i.
 //
 // Infinities and NaN must not reach other steps through the products' zeros:
 // a chunk in which an operand, a product of P or the state is not finite is
@@ -58,14 +60,16 @@ namespace atc {
 
 using namespace ptc;
 
-constexpr int kChunk = 64, kWorkers = 512, kThreads = kWorkers + 128, kTerms = 3;
-// Registers: 640 threads are launched with 96 each, and the workers' warps get
-// some of the others'.
-constexpr int kWorkerRegisters = 104, kOtherRegisters = 64;
-static_assert(kWorkers * kWorkerRegisters + 128 * kOtherRegisters <= kThreads * 96, "no more than the block was launched with");
+constexpr int kChunk = 64, kGroup = 256, kThreads = 2 * kGroup + 128, kTerms = 3;
+constexpr int kGroupWarps = kGroup / 32;
+// Registers: 640 threads are launched with 96 each; the warps that keep the
+// state get what the others can spare.
+constexpr int kOutRegisters = 80, kStateRegisters = 128, kOtherRegisters = 64;
+static_assert(kGroup * (kOutRegisters + kStateRegisters) + 128 * kOtherRegisters <= kThreads * 96,
+              "no more than the block was launched with");
 constexpr uint32_t kSub = kChunk * 128;      // bytes of 64 rows of 64 elements
 constexpr uint32_t kTile = 2 * kSub;         // an operand's term: 64 rows of 128 elements, or of two heads of 64
-constexpr int kCols = kChunk / 4;            // of a chunk's columns of S and O, those of a thread
+constexpr int kCols = kChunk / 2;            // of a chunk's columns of S and O, those of a thread
 constexpr long long kWaitNs = 2000000000LL;  // a wait that takes this long has failed
 
 template <typename T>
@@ -86,7 +90,8 @@ struct Layout {
   static constexpr bool kOver = kIn == 3;
   static constexpr uint32_t kP = kOver ? kK : kAfter;
   static constexpr uint32_t kPTerm = HPC * kSub;
-  static constexpr uint32_t kEnd = kAfter + (kOver || !OUT ? 0 : NT * kPTerm);
+  static constexpr uint32_t kOut = kAfter + (kOver || !OUT ? 0 : NT * kPTerm);  // outputs, where they are copied out
+  static constexpr uint32_t kEnd = kOut + (OUT && kIn == 1 ? kTile : 0);
   static_assert(NT * kPTerm <= kIn * kTile || !kOver, "P fits over K");
   static constexpr size_t kBytes = kEnd + 1024;  // alignment
 };
@@ -96,24 +101,22 @@ struct Decays {
   float hi[kChunk], lo[kChunk];  // signed G: whole part and fraction
   float cq[kChunk], ck[kChunk];  // so 2^.. of the state's part of a step's output, su 2^.. of a step's part of the state
   float bn[kChunk];              // su over 2^.. of cq: what takes S to P where the chunk's decays are mild
-  float d[kChunk];               // a step's own decay
   long long log2;                // the whole chunk's G
   float total;                   // the decay
   int mild;
 };
 
-// Those that the workers' warps arrive at, then those of one arrival (the
-// decays': one for each head).  A barrier that could be two phases ahead of
-// one who waits for it has a second one for odd chunks.
+// A barrier that could be two phases ahead of one who waits for it has a
+// second one for odd chunks.
 enum Bar {
-  kTiles, kDone = kTiles + 2, kPairs = kDone + 2, kSteps,
-  kGotS, kGotU, kGotOi = kGotU + 2, kGotO, kFull, kWith = kFull + 2, kDecay, kBars = kDecay + 3
+  kTiles, kDone = kTiles + 2, kPairs = kDone + 2, kSteps = kPairs + 2,  // of warps
+  kGotS, kGotU, kGotOi = kGotU + 2, kGotO, kFull, kWith = kFull + 2, kStored, kDecay, kBars = kDecay + 3
 };
 
 struct Small {
   __align__(16) Decays decays[3][2];
-  float dots[2][16][kCols];  // of a chunk and the one before
-  float part[4][128];
+  float dots[2][kGroupWarps][kCols];  // of a chunk and the one before
+  float part[2][128];
   uint64_t bars[kBars];
   uint32_t tmem;
   int bad[8];  // chunks to be run step by step
@@ -161,19 +164,27 @@ __device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t* r) {
   }
 }
 __device__ __forceinline__ void tmem_st_done() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-// 16 columns; complete after tmem_ld_done, which the values pass through.
-__device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&x)[16]) {
-  uint32_t r[16];
+// 8 or 16 columns; what is read may be used after tmem_ld_done.
+__device__ __forceinline__ void tmem_ld(uint32_t addr, float (&x)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld(uint32_t addr, float (&x)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
       "[%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]), "=f"(x[8]),
+        "=f"(x[9]), "=f"(x[10]), "=f"(x[11]), "=f"(x[12]), "=f"(x[13]), "=f"(x[14]), "=f"(x[15])
       : "r"(addr)
       : "memory");
+}
+template <int N>
+__device__ __forceinline__ void tmem_ld_done(float (&x)[N]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < N; ++i) asm volatile("" : "+f"(x[i]));  // not before
 }
 
 // A in tensor memory.
@@ -197,11 +208,6 @@ __host__ __device__ constexpr uint32_t idesc_of(int n) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (8u << 24);  // bfloat16, M = 128
 }
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ void to_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // Whether the barrier's phase has ended; the warp is taken off the scheduler
@@ -214,6 +220,12 @@ __device__ __forceinline__ bool bar_try_long(uint32_t b, uint32_t par) {
       : "r"(b), "r"(par), "r"(20000u)
       : "memory");
   return ok != 0;
+}
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect() {
+  uint32_t is;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(is));
+  return is != 0;
 }
 __device__ __forceinline__ void copy_in(uint32_t dst, const CUtensorMap* map, int x, int h, int t, int n, uint32_t bar) {
   asm volatile(
@@ -286,7 +298,6 @@ __device__ __forceinline__ bool chunk_decays(const AttnPass& a, float x0, float 
   bool bad = false;
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    out.d[2 * lane + j] = expf(x[j]);
     bad = bad || !(x[j] < 80.0f);  // NaN, or growth that no float32 holds for long
     fix[j] = fixed_log2(x[j]);
   }
@@ -323,17 +334,15 @@ __device__ __forceinline__ const T* head_rows(const RowsArg& a, int n, int h, in
   return static_cast<const T*>(a.p) + n * a.ns + (long long)(h / of) * size;
 }
 
-// A thread's part of an operand's tiles: one piece of 8 elements of a row of
-// each of the two sub-tiles, which are the elements from 0 and 64 on, or two
-// heads.  What a thread fetches is also what it scales and checks, so that
-// only the products wait for the other threads.
-__device__ __forceinline__ uint32_t piece_at() {
-  const int r = threadIdx.x / 8, c = threadIdx.x % 8;
+// A group's threads' parts of a tile: pieces of 8 elements of rows, 512 in each
+// of the two sub-tiles, which are the elements from 0 and 64 on, or two heads.
+__device__ __forceinline__ uint32_t piece_at(int i) {  // i: 0 .. 511
+  const int r = i / 8, c = i % 8;
   return r * 128 + ((c ^ (r & 7)) << 4);
 }
 template <typename T, int HPC>
 struct Rows {
-  const T* src;        // the thread's piece of sub-tile 0 of the next chunk
+  const T* src;        // the thread's first piece of sub-tile 0 of the next chunk; 32 rows on lies its second
   long long ss, step;  // from row to row; to the chunk after it
   int next;            // to sub-tile 1
   int on;              // bit b: sub-tile b has the thread's elements
@@ -341,81 +350,82 @@ struct Rows {
   // t0: the first chunk's start; step: to the next one's
   __device__ __forceinline__ Rows(const RowsArg& a, int n, int h0, int H, int of, int size_, int t0, int step_)
       : ss(a.ss), step(step_ * a.ss), size(size_) {
-    const int c = 8 * (threadIdx.x % 8);
-    src = head_rows<T>(a, n, h0, of, size) + (t0 + (int)(threadIdx.x / 8)) * a.ss + c;
+    const int thread = threadIdx.x % kGroup, c = 8 * (thread % 8);
+    src = head_rows<T>(a, n, h0, of, size) + (t0 + thread / 8) * a.ss + c;
     next = HPC == 1 ? 64 : (min(h0 + 1, H - 1) / of - h0 / of) * size;
     on = (c < size ? 1 : 0) | ((HPC == 1 ? 64 + c < size : c < size && h0 + 1 < H) ? 2 : 0);
   }
-  // Fetches the next chunk's 64 rows into the tile at `tile`; live: the
-  // thread's row is a step.  Other steps, elements from `size` on and heads
-  // that there are not are zeros.
+  // Reads the next chunk's 64 rows, of which `rows` are steps, into the tile.
+  // Other steps, elements from `size` on and heads that there are not are zeros.
   template <int SUBS>
-  __device__ __forceinline__ void load(unsigned char* tile, bool live, int vec, const T* any) {
+  __device__ __forceinline__ void load(unsigned char* tile, int rows, int vec) {
     constexpr int kIn = kSplit<T>;
-    unsigned char* to = tile + piece_at();
+    const int thread = threadIdx.x % kGroup;
 #pragma unroll
     for (int b = 0; b < SUBS; ++b) {
-      const int first = (HPC == 2 ? 0 : 64 * b) + 8 * (threadIdx.x % 8);
-      const bool fetch = live && (on >> b & 1);
-      unsigned char* dst = to + b * kSub;
-      const T* from = src + b * next;
-      if constexpr (kIn == 1) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int first = (HPC == 2 ? 0 : 64 * b) + 8 * (thread % 8);
+        const bool fetch = thread / 8 + 32 * half < rows && (on >> b & 1);
+        unsigned char* dst = tile + b * kSub + piece_at(thread + half * kGroup);
+        const T* from = src + b * next + half * 32 * ss;
+        float x[8];
+        fill(x, 0.0f);
         if (vec) {
-          cp16(su32(dst), fetch ? from : any, fetch);
-          continue;
-        }
-      }
-      float x[8];
-      fill(x, 0.0f);
-      if (vec) {
-        if (fetch) {
-          if constexpr (sizeof(T) == 4) {
-            float y[4];
-            Piece<T, 4>::load(from, y);
-            x[0] = y[0], x[1] = y[1], x[2] = y[2], x[3] = y[3];
-            if (first + 4 < size) {
-              Piece<T, 4>::load(from + 4, y);
-              x[4] = y[0], x[5] = y[1], x[6] = y[2], x[7] = y[3];
+          if (fetch) {
+            if constexpr (sizeof(T) == 4) {
+              float y[4];
+              Piece<T, 4>::load(from, y);
+              x[0] = y[0], x[1] = y[1], x[2] = y[2], x[3] = y[3];
+              if (first + 4 < size) {
+                Piece<T, 4>::load(from + 4, y);
+                x[4] = y[0], x[5] = y[1], x[6] = y[2], x[7] = y[3];
+              }
+            } else {
+              Piece<T, 8>::load(from, x);
             }
-          } else {
-            Piece<T, 8>::load(from, x);
           }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (fetch && first + i < size) x[i] = Elem<T>::to_f(from[i]);
         }
-      } else {
+        uint32_t w[kIn][4];
+        F2 unused = f2(0.0f, 0.0f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (fetch && first + i < size) x[i] = Elem<T>::to_f(from[i]);
+        for (int i = 0; i < 4; ++i) {
+          uint32_t s[kIn];
+          split<kIn>(f2(x[2 * i], x[2 * i + 1]), s, unused);
+#pragma unroll
+          for (int j = 0; j < kIn; ++j) w[j][i] = s[j];
+        }
+#pragma unroll
+        for (int j = 0; j < kIn; ++j) *reinterpret_cast<uint4*>(dst + j * kTile) = make_uint4(w[j][0], w[j][1], w[j][2], w[j][3]);
       }
-      uint32_t w[kIn][4];
-      F2 unused = f2(0.0f, 0.0f);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t s[kIn];
-        split<kIn>(f2(x[2 * i], x[2 * i + 1]), s, unused);
-#pragma unroll
-        for (int j = 0; j < kIn; ++j) w[j][i] = s[j];
-      }
-#pragma unroll
-      for (int j = 0; j < kIn; ++j) *reinterpret_cast<uint4*>(dst + j * kTile) = make_uint4(w[j][0], w[j][1], w[j][2], w[j][3]);
     }
     src += step;
   }
   // Has the next chunk's rows brought into L2.
-  __device__ __forceinline__ void prefetch(bool live) const {
+  __device__ __forceinline__ void prefetch(int rows) const {
 #pragma unroll
     for (int b = 0; b < 2; ++b)
-      if (live && (on >> b & 1)) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + b * next));
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+        if ((int)(threadIdx.x % kGroup) / 8 + 32 * half < rows && (on >> b & 1))
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(src + b * next + half * 32 * ss));
   }
 };
 
-// ck K of the thread's pieces as three terms.
+// ck K as three terms, by a group.
 template <typename T, int HPC, int SUBS>
 __device__ __forceinline__ void scale_tile(const unsigned char* k, unsigned char* out, const Decays* d, F2& finite) {
   constexpr int kIn = kSplit<T>;
-#pragma unroll
-  for (int b = 0; b < SUBS; ++b) {
-    const uint32_t at = b * kSub + piece_at();
-    const float f = d[HPC == 2 ? b : 0].ck[threadIdx.x / 8];
+  const int thread = threadIdx.x % kGroup;
+#pragma unroll 1
+  for (int i = 0; i < 2 * SUBS; ++i) {
+    const int b = i / 2, piece = thread + i % 2 * kGroup;
+    const uint32_t at = b * kSub + piece_at(piece);
+    const float f = d[HPC == 2 ? b : 0].ck[piece / 8];
     uint32_t w[kTerms][4];
     uint32_t t[kIn][4];
 #pragma unroll
@@ -439,13 +449,14 @@ __device__ __forceinline__ void scale_tile(const unsigned char* k, unsigned char
   }
 }
 
-// Whether the thread's pieces of a tile's first term are finite: the largest
-// of the magnitudes as whole numbers, 16 bits each.
-__device__ __forceinline__ bool tile_finite(const unsigned char* tile) {
+// Whether a tile's first term is finite, by THREADS threads: the largest of
+// the magnitudes as whole numbers, 16 bits each.
+template <int THREADS>
+__device__ __forceinline__ bool tile_finite(const unsigned char* tile, int thread) {
   uint32_t top = 0;
-#pragma unroll
-  for (int b = 0; b < 2; ++b) {
-    const uint4 u = *reinterpret_cast<const uint4*>(tile + b * kSub + piece_at());
+#pragma unroll 2
+  for (int i = 0; i < (int)kTile / 16 / THREADS; ++i) {
+    const uint4 u = *reinterpret_cast<const uint4*>(tile + (i * THREADS + thread) * 16);
     top = __vmaxu2(top, u.x & 0x7fff7fffu), top = __vmaxu2(top, u.y & 0x7fff7fffu);
     top = __vmaxu2(top, u.z & 0x7fff7fffu), top = __vmaxu2(top, u.w & 0x7fff7fffu);
   }
@@ -497,20 +508,21 @@ __device__ __forceinline__ void arrive_bar(Small& sh, int bar) {
   if (threadIdx.x % 32 == 0) bar_arrive(su32(&sh.bars[bar]));
 }
 
-// The chunk that starts at t0 step by step, by all workers; g: the thread's
-// elements of the state.  Returns the phases that the steps' barrier has had.
+// The chunk that starts at t0 step by step, by the group that keeps the state;
+// g: the thread's elements of it.  Returns the phases that the steps' barrier has had.
 // Not inlined: it is there for infinities and NaN.
 template <typename T, int HPC, int NH, bool OUT>
-__device__ __noinline__ int run_steps(const AttnParams& p, int pass, int n, int h0, int t0, int L, const Decays* dec,
-                                      float (*dots)[kCols], Small& sh, int meetings, float* g) {
+__device__ __noinline__ int run_steps(const AttnParams& p, int pass, int n, int h0, int t0, int L, float (*dots)[kCols],
+                                      Small& sh, int meetings, float* g) {
   const AttnPass& a = p.pass[pass];
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, quarter = warp & 3, part = warp >> 2, r = quarter * 32 + lane;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, quarter = warp & 3, part = warp >> 2 & 1, r = quarter * 32 + lane;
   const int head = HPC == 2 ? r >> 6 : 0, h = h0 + head, v = HPC == 2 ? r & 63 : r, k0 = part * NH;
   const bool mine = v < a.V && h < p.H, back = a.backward;
   const int rows = min(kChunk, L - t0), hc = min(h, p.H - 1);
   const T* q = head_rows<T>(a.q, n, hc, a.q_of, a.K);
   const T* k = head_rows<T>(a.k, n, hc, a.k_of, a.K);
   const T* x = head_rows<T>(a.v, n, hc, a.v_of, a.V);
+  const float* decay = static_cast<const float*>(p.decay.p) + n * p.decay.ns + hc;
   T* out = static_cast<T*>(a.o.p) + n * a.o.ns + (long long)(hc / a.o_of) * a.V + v;
   const T* with = static_cast<const T*>(a.dot_with.p) + n * a.dot_with.ns + (long long)(hc / a.o_of) * a.V + v;
   auto put = [&](long long t, float y) {
@@ -522,7 +534,7 @@ __device__ __noinline__ int run_steps(const AttnParams& p, int pass, int n, int 
   for (int j = 0; j < rows; ++j) {
     const int m = back ? rows - 1 - j : j;
     const long long t = t0 + m;
-    const float d = dec[head].d[m], val = mine ? a.su * Elem<T>::to_f(x[t * a.v.ss + v]) : 0.0f;
+    const float d = expf((p.decay.p ? decay[t * p.decay.ss] : 0.0f) + (p.bias ? p.bias[hc] : 0.0f)), val = mine ? a.su * Elem<T>::to_f(x[t * a.v.ss + v]) : 0.0f;
     float y = 0.0f;
 #pragma unroll 4
     for (int b = 0; b < NH; ++b) {
@@ -537,7 +549,7 @@ __device__ __noinline__ int run_steps(const AttnParams& p, int pass, int n, int 
       arrive_bar(sh, kSteps);
       wait_bar(sh, kSteps, meetings++ & 1);
       if (part == 0) {
-        y = a.so * ((sh.part[0][r] + sh.part[1][r]) + (sh.part[2][r] + sh.part[3][r]));
+        y = a.so * (sh.part[0][r] + sh.part[1][r]);
         put(t, y);
         if (a.dot) {
           const float z = warp_sum(mine ? y * Elem<T>::to_f(with[t * a.dot_with.ss]) : 0.0f);
@@ -549,7 +561,7 @@ __device__ __noinline__ int run_steps(const AttnParams& p, int pass, int n, int 
     }
   }
   if (OUT)
-    for (int m = rows + part; m < kChunk; m += 4) put(t0 + m, 0.0f);
+    for (int m = rows + part; m < kChunk; m += 2) put(t0 + m, 0.0f);
   return meetings;
 }
 
@@ -561,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
   const AttnParams& p = args.p;
   using Lay = Layout<T, HPC, NT, OUT>;
   constexpr int kIn = kSplit<T>;
-  constexpr int NH = HPC == 2 ? 16 : 16 * KB;  // state elements of a thread
+  constexpr int NH = HPC == 2 ? 32 : 32 * KB;  // state elements of a thread
   constexpr int KW = HPC == 2 ? 32 : 32 * KB;  // tensor memory columns of one of the state's terms
   constexpr uint32_t kS = 0, kOi = 64 * HPC, kU = 128 * HPC, kH = kU + 128;
   static_assert(kH + NT * KW <= 512, "tensor memory");
@@ -570,7 +582,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
   extern __shared__ unsigned char raw[];
   unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   __shared__ Small sh;
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, quarter = warp & 3, part = warp >> 2;
+  // of one value for a warp, which is what addresses and descriptors of copies and products are made of
+  const int tid = threadIdx.x, lane = tid % 32, warp = __shfl_sync(0xffffffffu, tid / 32, 0);
+  const int quarter = warp & 3, part = warp >> 2 & 1;
   const int segments = p.plan.segments;
   const Place<HPC> at(p, OUT ? segments : segments - 1);
   const AttnPass& a = p.pass[at.pass];  // by index: it stays in constant memory
@@ -584,12 +598,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
   auto chunk_at = [&](int i) { return back ? c_live - 1 - i : c_begin + i; };
 
   if (tid == 0) {
-    for (int i = 0; i < kBars; ++i) bar_init(su32(&sh.bars[i]), i <= kSteps ? kWorkers / 32 : i >= kDecay ? HPC : 1);
+    // who arrives: the state's warps, or both groups; without outputs the first scales and the second adds
+    const int both = 2 * kGroupWarps;
+    for (int i = 0; i < kBars; ++i) {
+      int n = i >= kDecay ? HPC : 1;
+      if (i < kDone) n = OUT && !TMA ? both : kGroupWarps;
+      else if (i < kPairs) n = OUT ? both : kGroupWarps;
+      else if (i <= kSteps) n = kGroupWarps;
+      bar_init(su32(&sh.bars[i]), n);
+    }
     sh.gave_up = 0;
     for (int i = 0; i < 8; ++i) sh.bad[i] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == kWorkers / 32) {
+  if (warp == 2 * kGroupWarps) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&sh.tmem)), "r"(512u) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -604,6 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
   };
   auto ready = [](int i) { return Phase{kTiles + (i & 1), i >> 1}; };
   auto done = [](int i) { return Phase{kDone + (i & 1), i >> 1}; };
+  auto paired = [](int i) { return Phase{kPairs + (i & 1), i >> 1}; };
   auto got_u = [](int i) { return Phase{kGotU + (i & 1), i >> 1}; };
   auto full = [](int i) { return Phase{kFull + (i & 1), i >> 1}; };
   auto decayed = [](int i) { return Phase{kDecay + i % 3, i / 3}; };
@@ -611,154 +634,299 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
   auto wait_for = [&](Phase x) { wait(x.bar, x.n); };
   auto arrive = [&](int bar) { arrive_bar(sh, bar); };
   auto stage_of = [&](int i) { return (Lay::kStages == 2 ? i & 1 : 0) * Lay::kStage; };
+  auto scaled_of = [&](int i) { return Lay::kScaled + (OUT ? 0 : i & 1) * kTerms * kTile; };
+  auto mild_of = [&](int i) { return sh.decays[i % 3][0].mild && (HPC == 1 || sh.decays[i % 3][1].mild); };
 
-  if (warp < kWorkers / 32) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWorkerRegisters));
-    // ---------------- the workers
-    const int r = quarter * 32 + lane;
-    const int head = HPC == 2 ? r >> 6 : 0, h = at.h0 + head, v = HPC == 2 ? r & 63 : r;
-    const bool mine = v < a.V && h < p.H;
-    const int k0 = part * NH, ucol = HPC == 2 ? head * 64 + part * 16 : part * NH;  // state elements, U's columns
-    const int ocol = (HPC == 2 ? head * 64 : 0) + part * kCols;                     // columns of S and O
-    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+  // the groups' lanes: a value of a head
+  const int r = quarter * 32 + lane;
+  const int head = HPC == 2 ? r >> 6 : 0, h = at.h0 + head, v = HPC == 2 ? r & 63 : r;
+  const bool mine = v < a.V && h < p.H;
+  const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+  const int step = back ? -kChunk : kChunk, t_first = chunk_at(0) * kChunk, vec = p.plan.vec;
+  const F2 zero = f2(0.0f, 0.0f);
+  // The group that has K scales it, and clears rows behind the row's end.
+  auto prepare = [&](int i) {
+    unsigned char* tiles = sm + stage_of(i);
+    if constexpr (TMA) {
+      wait_for(full(i));
+      const int rows = L - chunk_at(i) * kChunk;
+      if (rows < kChunk) {
+        const uint4 none = make_uint4(0, 0, 0, 0);
+        for (int x = 0; x < 4; ++x) {
+          const int piece = tid % kGroup + x % 2 * kGroup, b = x / 2;
+          if (piece / 8 < rows) continue;
+          unsigned char* to = tiles + b * kSub + piece_at(piece);
+          *reinterpret_cast<uint4*>(to + Lay::kV) = none;
+          if (b < kSubs) *reinterpret_cast<uint4*>(to + Lay::kK) = none;
+          if (OUT && b < kSubs) *reinterpret_cast<uint4*>(to + Lay::kQ) = none;
+        }
+      }
+    }
+    wait_for(decayed(i));
+    F2 finite = zero;
+    scale_tile<T, HPC, kSubs>(tiles + Lay::kK, sm + scaled_of(i), sh.decays[i % 3], finite);
+    if (!is_finite(finite)) sh.bad[i & 7] = 1;
+  };
+
+  if (warp < kGroupWarps) {
+    // ---------------- pairs and outputs
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOutRegisters));
+    Rows<T, HPC> rq(a.q, at.n, at.h0, p.H, a.q_of, a.K, t_first, step), rv(a.v, at.n, at.h0, p.H, a.v_of, a.V, t_first, step);
+    auto fetch = [&](int i) {
+      const int rows = L - chunk_at(i) * kChunk;
+      rv.template load<2>(sm + stage_of(i) + Lay::kV, rows, vec);
+      if (OUT) rq.template load<kSubs>(sm + stage_of(i) + Lay::kQ, rows, vec);
+    };
+    if constexpr (!OUT) {
+      // without outputs: K of the next chunk, while the other group adds
+      Rows<T, HPC> rk(a.k, at.n, at.h0, p.H, a.k_of, a.K, t_first, step);
+#pragma unroll 1
+      for (int i = 0; i < count; ++i) {
+        if (!TMA && i >= Lay::kStages) wait_for(got_u(i - Lay::kStages));  // whose tiles these take
+        else if (i >= 2) wait_for(got_u(i - 2));                          // whose ck K this takes
+        if (!TMA) {
+          rk.template load<kSubs>(sm + stage_of(i) + Lay::kK, L - chunk_at(i) * kChunk, vec);
+          fetch(i);
+          if (i + 1 < count) {
+            const int rows = L - chunk_at(i + 1) * kChunk;
+            rk.prefetch(rows), rv.prefetch(rows);
+          }
+        }
+        prepare(i);
+        if (!tile_finite<kGroup>(sm + stage_of(i) + Lay::kV, tid)) sh.bad[i & 7] = 1;
+        arrive(ready(i).bar);
+      }
+    } else {
+      const int ocol = (HPC == 2 ? head * 64 : 0) + part * kCols;  // columns of S and O
+      // outputs of lane v
+      T* out = static_cast<T*>(a.o.p) + at.n * a.o.ns + (long long)(h / a.o_of) * a.V + v;
+      float* out32 = a.o32 + ((long long)at.n * S * p.H + h) * a.V + v;
+      const long long ss32 = (long long)p.H * a.V;
+      const T* dot_row = static_cast<const T*>(a.dot_with.p) + at.n * a.dot_with.ns + (long long)(h / a.o_of) * a.V + v;
+      // The products of chunk i's outputs, added up over the lanes' warps.
+      auto dots_out = [&](int i) {
+        if (tid < 64 * HPC) {
+          const int hd = tid / 64, m = tid % 64, t = chunk_at(i) * kChunk + m;
+          if (t < L && at.h0 + hd < p.H) {
+            const float* x = &sh.dots[i & 1][m / kCols * 4][m % kCols];
+            const float y = HPC == 2 ? x[2 * hd * kCols] + x[(2 * hd + 1) * kCols]
+                                     : (x[0] + x[kCols]) + (x[2 * kCols] + x[3 * kCols]);
+            a.dot[((long long)at.n * p.H + at.h0 + hd) * S + t] = y;
+          }
+        }
+      };
+      // The loops below go by 8 columns and are not unrolled: what runs between
+      // two of a chunk's barriers has to stay in the instruction cache.
+      // P of row m of S, 32 of its columns
+      auto pairs = [&](int i) {
+        const int m = r & 63;
+        const Decays& d = sh.decays[i % 3][head];
+        const bool mild = mild_of(i);
+        const float hi = d.hi[m], lo = d.lo[m];
+        F2 finite = zero;
+        unsigned char* row = (Lay::kOver ? sm + Lay::kK : sm + Lay::kP) + (HPC == 2 ? r : m) * 128;
+#pragma unroll 1
+        for (int c = 0; c < kCols; c += 8) {
+          const int n0 = part * kCols + c;
+          float s[8];
+          tmem_ld(lanes + kS + ocol + c, s);
+          tmem_ld_done(s);
+          F2 x[4];
+          if (mild) {
+            const float4 f = *reinterpret_cast<const float4*>(&d.bn[n0]), g = *reinterpret_cast<const float4*>(&d.bn[n0 + 4]);
+            x[0] = mul2(f2(s[0], s[1]), f2(f.x, f.y)), x[1] = mul2(f2(s[2], s[3]), f2(f.z, f.w));
+            x[2] = mul2(f2(s[4], s[5]), f2(g.x, g.y)), x[3] = mul2(f2(s[6], s[7]), f2(g.z, g.w));
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[j] *= a.su * exp2_fast((hi - d.hi[n0 + j]) + (lo - d.lo[n0 + j]));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] = f2(s[2 * j], s[2 * j + 1]);
+          }
+          uint32_t w[NT][4];
+          const int last = back ? n0 + 7 - m : m - n0;  // of the columns, counted from the first or backward
+#pragma unroll
+          for (int j = 0; j < 8; j += 2) {
+            float2 y = f2_get(x[j / 2]);
+            y.x = (back ? 7 - j : j) <= last ? y.x : 0.0f;
+            y.y = (back ? 6 - j : j + 1) <= last ? y.y : 0.0f;
+            uint32_t t[NT];
+            split<NT>(f2(y.x, y.y), t, finite);
+#pragma unroll
+            for (int e = 0; e < NT; ++e) w[e][j / 2] = t[e];
+          }
+          unsigned char* to = row + (((n0 / 8) ^ (m & 7)) << 4);
+#pragma unroll
+          for (int e = 0; e < NT; ++e) *reinterpret_cast<uint4*>(to + e * Lay::kPTerm) = make_uint4(w[e][0], w[e][1], w[e][2], w[e][3]);
+        }
+        if (!is_finite(finite)) sh.bad[i & 7] = 1;
+      };
+      auto outputs = [&](int i) {
+        const Decays* dec = sh.decays[i % 3];
+        const bool mild = mild_of(i), dot = a.dot, wide = a.o32, any = a.o.p;
+        const int t0 = chunk_at(i) * kChunk + part * kCols;
+        if (TMA && i > 0) wait(kStored, i - 1);
+        if (TMA && dot) wait(kWith, i);
+#pragma unroll 1
+        for (int c = 0; c < kCols; c += 8) {
+          float o[8], near[8];
+          tmem_ld(lanes + kOi + ocol + c, o);
+          if (!mild) tmem_ld(lanes + kS + ocol + c, near);
+          tmem_ld_done(o);
+          const float* cq = &dec[head].cq[part * kCols + c];
+#pragma unroll
+          for (int x = 0; x < 8; x += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(cq + x);
+            const float2 y = f2_get(mul2(f2(f.x, f.y), f2(o[x], o[x + 1]))), z = f2_get(mul2(f2(f.z, f.w), f2(o[x + 2], o[x + 3])));
+            o[x] = y.x, o[x + 1] = y.y, o[x + 2] = z.x, o[x + 3] = z.y;
+          }
+          if (!mild) {
+            tmem_ld_done(near);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) o[x] = fmaf(a.so, near[x], o[x]);
+          }
+          const int t1 = t0 + c, rows = mine ? S - t1 : 0;
+          // a lane's element of 8 rows of the tile, where tiles are copied; it is unused where o32 is written
+          const int at_tile = (r >> 6) * (int)kSub / (int)sizeof(T) + (part * kCols + c) * 64 + (r & 63);
+          if (TMA && !wide) {
+            T* to = reinterpret_cast<T*>(sm + Lay::kOut) + at_tile;
+#pragma unroll
+            for (int x = 0; x < 8; ++x) to[x * 64] = Elem<T>::from_f(o[x]);
+          } else if (wide) {
+            float* to = out32 + t1 * ss32;
+#pragma unroll
+            for (int x = 0; x < 8; ++x, to += ss32)
+              if (x < rows) *to = o[x];
+          } else if (any) {
+            T* to = out + t1 * a.o.ss;
+#pragma unroll
+            for (int x = 0; x < 8; ++x, to += a.o.ss)
+              if (x < rows) *to = Elem<T>::from_f(o[x]);
+          }
+          if (dot) {
+            const int live_rows = mine ? L - t1 : 0;
+            if constexpr (TMA) {
+              const T* from = reinterpret_cast<const T*>(sm + stage_of(i) + Lay::kK) + at_tile;
+#pragma unroll
+              for (int x = 0; x < 8; ++x) {
+                const float w = Elem<T>::to_f(from[x * 64]);
+                o[x] = x < live_rows ? o[x] * w : 0.0f;
+              }
+            } else {
+              const T* with = dot_row + t1 * a.dot_with.ss;
+#pragma unroll
+              for (int x = 0; x < 8; ++x, with += a.dot_with.ss) o[x] = x < live_rows ? o[x] * Elem<T>::to_f(*with) : 0.0f;
+            }
+            int to = 0;
+            lanes_sum<8, 16, 1>(o, lane, to);
+            sh.dots[i & 1][warp][c + to] = o[0];
+          }
+        }
+      };
+      if (!TMA)
+        for (int i = 0; i < min(count, Lay::kStages); ++i) {
+          fetch(i);
+          arrive(ready(i).bar);
+        }
+#pragma unroll 1
+      for (int i = 0; i < count; ++i) {
+        if (Lay::kStages == 1 && i + 1 < count) {
+          const int rows = L - chunk_at(i + 1) * kChunk;
+          rv.prefetch(rows), rq.prefetch(rows);
+        }
+        wait_for(decayed(i));
+        wait(kGotS, i);
+        if (HPC == 2 || quarter < 2) pairs(i);
+        if (TMA) wait_for(full(i));  // V, of the copies' own making
+        // with one head S has rows for two quarters of the lanes; the others look V over
+        if (HPC == 2 && !tile_finite<kGroup>(sm + stage_of(i) + Lay::kV, tid)) sh.bad[i & 7] = 1;
+        if (HPC == 1 && quarter >= 2 && !tile_finite<kGroup / 2>(sm + stage_of(i) + Lay::kV, (part * 2 + (quarter & 1)) * 32 + lane))
+          sh.bad[i & 7] = 1;
+        arrive(paired(i).bar);
+        if (a.dot && i > 0) {
+          wait_for(done(i - 1));
+          dots_out(i - 1);
+        }
+        wait_for(paired(i));  // all of the chunk's flags are set
+        wait(kGotO, i);
+        if (!sh.bad[i & 7]) outputs(i);
+        else if (TMA && a.dot) wait(kWith, i);  // the copies are not left behind
+        arrive(done(i).bar);
+        if (!TMA && i + Lay::kStages < count) {
+          fetch(i + Lay::kStages);
+          arrive(ready(i + Lay::kStages).bar);
+        }
+      }
+      if (a.dot && count > 0) {
+        wait_for(done(count - 1));
+        if (!sh.gave_up) dots_out(count - 1);
+      }
+      // the rows behind the last live chunk
+      for (int t = max(c_live, c_begin) * kChunk + part; t < min(c_end * kChunk, S); t += 2) {
+        if (!mine) break;
+        if (a.o32) out32[t * ss32] = 0.0f;
+        else if (a.o.p) out[t * a.o.ss] = Elem<T>::from_f(0.0f);
+      }
+    }
+  } else if (warp < 2 * kGroupWarps) {
+    // ---------------- the state
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kStateRegisters));
+    const int k0 = part * NH, ucol = HPC == 2 ? head * 64 + part * 32 : part * NH;  // state elements, U's columns
     // the state, transposed: lane v, elements k0 ..
     const long long state = ((long long)at.n * p.H + h) * a.K * a.V;
     auto state_at = [&](int i) {
       return state + (a.v_major ? (long long)v * a.K + k0 + i : (long long)(k0 + i) * a.V + v);
     };
     constexpr long long kept = (long long)KB * 64 * 128;  // a state in scratch: [k][lane]
-    const int step = back ? -kChunk : kChunk, t_first = chunk_at(0) * kChunk, vec = p.plan.vec;
-    Rows<T, HPC> rq(a.q, at.n, at.h0, p.H, a.q_of, a.K, t_first, step), rk(a.k, at.n, at.h0, p.H, a.k_of, a.K, t_first, step),
-        rv(a.v, at.n, at.h0, p.H, a.v_of, a.V, t_first, step);
-    auto fetch = [&](int i) {
-      unsigned char* tiles = sm + stage_of(i);
-      const bool is = chunk_at(i) * kChunk + tid / 8 < L;
-      rk.template load<kSubs>(tiles + Lay::kK, is, vec, static_cast<const T*>(a.k.p));
-      rv.template load<2>(tiles + Lay::kV, is, vec, static_cast<const T*>(a.v.p));
-      if (OUT) rq.template load<kSubs>(tiles + Lay::kQ, is, vec, static_cast<const T*>(a.q.p));
-      cp_commit();
-    };
-    if (!TMA && count > 0) fetch(0);
+    Rows<T, HPC> rk(a.k, at.n, at.h0, p.H, a.k_of, a.K, t_first, step);
+    auto fetch = [&](int i) { rk.template load<kSubs>(sm + stage_of(i) + Lay::kK, L - chunk_at(i) * kChunk, vec); };
     F2 H[NH / 2];
-    {
-      float first[NH];
-      if (OUT && segments > 1) {
-        const float* from = p.plan.states + ((long long)at.stream * segments + order) * kept;
 #pragma unroll
-        for (int i = 0; i < NH; ++i) first[i] = from[(k0 + i) * 128 + r];
-      } else {
+    for (int i = 0; i < NH / 2; ++i) H[i] = zero;
+    // A state that is read or handed out goes through U's place, by loops that are not unrolled.
+    const uint32_t there = lanes + u_at(0) + ucol;
+    if (OUT && (segments > 1 || a.first)) {
+      const float* from = p.plan.states + ((long long)at.stream * segments + order) * kept;
+#pragma unroll 1
+      for (int j = 0; j < NH; j += 8) {
+        uint32_t w[8];
 #pragma unroll
-        for (int i = 0; i < NH; ++i) first[i] = OUT && a.first && mine && k0 + i < a.K ? a.first[state_at(i)] : 0.0f;
+        for (int x = 0; x < 8; ++x) {
+          const int k = k0 + j + x;
+          w[x] = __float_as_uint(segments > 1 ? from[k * 128 + r] : mine && k < a.K ? a.first[state_at(j + x)] : 0.0f);
+        }
+        tmem_st<8>(there + j, w);
       }
-#pragma unroll
-      for (int i = 0; i < NH / 2; ++i) H[i] = f2(first[2 * i], first[2 * i + 1]);
-    }
-    const F2 zero = f2(0.0f, 0.0f);
-    // The state's terms to tensor memory, for chunk i.
-    auto publish = [&](int i) {
-      F2 finite = zero;
-      uint32_t w[NT][NH / 2];
-#pragma unroll
-      for (int x = 0; x < NH / 2; ++x) {
-        uint32_t s[NT];
-        split<NT>(H[x], s, finite);
-#pragma unroll
-        for (int y = 0; y < NT; ++y) w[y][x] = s[y];
-      }
-#pragma unroll
-      for (int x = 0; x < NT; ++x) tmem_st<NH / 2>(lanes + kH + x * KW + k0 / 2, w[x]);
       tmem_st_done();
-      if (mine && !is_finite(finite)) sh.bad[i & 7] = 1;
-    };
-    // ck K of chunk i, once its tiles are there.
-    auto prepare = [&](int i) {
-      unsigned char* tiles = sm + stage_of(i);
-      if constexpr (TMA) {
-        wait_for(full(i));
-        if (chunk_at(i) * kChunk + tid / 8 >= L) {  // behind the row's end
-          const uint4 none = make_uint4(0, 0, 0, 0);
+    }
+    // H = e H + U, and its terms to tensor memory for chunk i.
+    auto advance = [&](uint32_t u_from, float e, bool add, bool terms, int i) {
+      F2 finite = zero;
 #pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            unsigned char* to = tiles + b * kSub + piece_at();
-            *reinterpret_cast<uint4*>(to + Lay::kV) = none;
-            if (b < kSubs) *reinterpret_cast<uint4*>(to + Lay::kK) = none;
-            if (OUT && b < kSubs) *reinterpret_cast<uint4*>(to + Lay::kQ) = none;
+      for (int j = 0; j < NH; j += 16) {
+        if (add) {
+          float u[16];
+          tmem_ld(u_from + j, u);
+          tmem_ld_done(u);
+#pragma unroll
+          for (int x = 0; x < 8; ++x) H[j / 2 + x] = fma2(f2(e, e), H[j / 2 + x], f2(u[2 * x], u[2 * x + 1]));
+        }
+        if (OUT && terms) {
+          uint32_t w[NT][8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            uint32_t s[NT];
+            split<NT>(H[j / 2 + x], s, finite);
+#pragma unroll
+            for (int y = 0; y < NT; ++y) w[y][x] = s[y];
           }
-        }
-      } else {
-        cp_wait();
-      }
-      wait_for(decayed(i));
-      F2 finite = zero;
-      scale_tile<T, HPC, kSubs>(tiles + Lay::kK, sm + Lay::kScaled + (OUT ? 0 : i & 1) * kTerms * kTile, sh.decays[i % 3], finite);
-      if (!is_finite(finite) || !tile_finite(tiles + Lay::kV)) sh.bad[i & 7] = 1;
-      arrive(ready(i).bar);
-    };
-    // outputs of lane v
-    T* out = static_cast<T*>(a.o.p) + at.n * a.o.ns + (long long)(h / a.o_of) * a.V + v;
-    float* out32 = a.o32 + ((long long)at.n * S * p.H + h) * a.V + v;
-    const long long ss32 = (long long)p.H * a.V;
-    const T* dot_row = static_cast<const T*>(a.dot_with.p) + at.n * a.dot_with.ns + (long long)(h / a.o_of) * a.V + v;
-    auto put = [&](int t, float y) {
-      if (!mine || t >= S) return;
-      if (a.o32) out32[t * ss32] = y;
-      else if (a.o.p) out[t * a.o.ss] = Elem<T>::from_f(y);
-    };
-    auto dots_out = [&](int i) {  // the products of chunk i's outputs, added up over the lanes' warps
-      if (tid < 64 * HPC) {
-        const int hd = tid / 64, m = tid % 64, t = chunk_at(i) * kChunk + m;
-        if (t < L && at.h0 + hd < p.H) {
-          const float* x = &sh.dots[i & 1][m / kCols * 4][m % kCols];
-          const float y = HPC == 2 ? x[2 * hd * kCols] + x[(2 * hd + 1) * kCols]
-                                   : (x[0] + x[kCols]) + (x[2 * kCols] + x[3 * kCols]);
-          a.dot[((long long)at.n * p.H + at.h0 + hd) * S + t] = y;
+#pragma unroll
+          for (int x = 0; x < NT; ++x) tmem_st<8>(lanes + kH + x * KW + (k0 + j) / 2, w[x]);
         }
       }
-    };
-    // P of row m of S, 16 of its columns
-    auto pairs = [&](int i) {
-      const int m = r & 63, n0 = part * kCols;
-      const Decays& d = sh.decays[i % 3][head];
-      const bool mild = sh.decays[i % 3][0].mild && (HPC == 1 || sh.decays[i % 3][1].mild);
-      float s[kCols];
-      tmem_ld16(lanes + kS + ocol, s);
-      F2 x[kCols / 2];
-      if (mild) {
-#pragma unroll
-        for (int j = 0; j < kCols; j += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(&d.bn[n0 + j]);
-          x[j / 2] = mul2(f2(s[j], s[j + 1]), f2(f.x, f.y));
-          x[j / 2 + 1] = mul2(f2(s[j + 2], s[j + 3]), f2(f.z, f.w));
-        }
-      } else {
-        const float hi = d.hi[m], lo = d.lo[m];
-#pragma unroll
-        for (int j = 0; j < kCols; ++j) s[j] *= a.su * exp2_fast((hi - d.hi[n0 + j]) + (lo - d.lo[n0 + j]));
-#pragma unroll
-        for (int j = 0; j < kCols / 2; ++j) x[j] = f2(s[2 * j], s[2 * j + 1]);
+      if (OUT && terms) {
+        tmem_st_done();
+        if (mine && !is_finite(finite)) sh.bad[i & 7] = 1;
       }
-      F2 finite = zero;
-      uint32_t w[NT][kCols / 2];
-      // m - n0 counted from the row's end backward in time
-      const int last = back ? n0 + kCols - 1 - m : m - n0;
-#pragma unroll
-      for (int j = 0; j < kCols; j += 2) {
-        float2 y = f2_get(x[j / 2]);
-        y.x = (back ? kCols - 1 - j : j) <= last ? y.x : 0.0f;
-        y.y = (back ? kCols - 2 - j : j + 1) <= last ? y.y : 0.0f;
-        uint32_t t[NT];
-        split<NT>(f2(y.x, y.y), t, finite);
-#pragma unroll
-        for (int e = 0; e < NT; ++e) w[e][j / 2] = t[e];
-      }
-      if (!is_finite(finite)) sh.bad[i & 7] = 1;
-      unsigned char* row = (Lay::kOver ? sm + Lay::kK : sm + Lay::kP) + (HPC == 2 ? r : m) * 128;
-#pragma unroll
-      for (int e = 0; e < NT; ++e)
-#pragma unroll
-        for (int y = 0; y < kCols / 8; ++y)
-          *reinterpret_cast<uint4*>(row + e * Lay::kPTerm + (((part * (kCols / 8) + y) ^ (m & 7)) << 4)) =
-              make_uint4(w[e][4 * y], w[e][4 * y + 1], w[e][4 * y + 2], w[e][4 * y + 3]);
     };
     int meetings = 0;
     // Chunk i step by step, from the operands themselves.
@@ -769,159 +937,96 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
         const float2 y = f2_get(H[b]);
         g[2 * b] = y.x, g[2 * b + 1] = y.y;
       }
-      meetings = run_steps<T, HPC, NH, OUT>(args.p, at.pass, at.n, at.h0, chunk_at(i) * kChunk, L, sh.decays[i % 3],
-                                            sh.dots[i & 1], sh, meetings, g);
+      meetings = run_steps<T, HPC, NH, OUT>(args.p, at.pass, at.n, at.h0, chunk_at(i) * kChunk, L, sh.dots[i & 1], sh, meetings, g);
 #pragma unroll
       for (int b = 0; b < NH / 2; ++b) H[b] = f2(g[2 * b], g[2 * b + 1]);
     };
-    auto add_state = [&](int i) {
-      const float e = sh.decays[i % 3][head].total;
+    // Leaves the state where U is.
+    auto hand_out = [&]() {
 #pragma unroll
       for (int j = 0; j < NH; j += 16) {
-        float u[16];
-        tmem_ld16(lanes + u_at(i) + ucol + j, u);
+        uint32_t w[16];
 #pragma unroll
-        for (int x = 0; x < 8; ++x) H[j / 2 + x] = fma2(f2(e, e), H[j / 2 + x], f2(u[2 * x], u[2 * x + 1]));
+        for (int x = 0; x < 8; ++x) {
+          const float2 y = f2_get(H[j / 2 + x]);
+          w[2 * x] = __float_as_uint(y.x), w[2 * x + 1] = __float_as_uint(y.y);
+        }
+        tmem_st<16>(there + j, w);
       }
+      tmem_st_done();
     };
-    auto outputs = [&](int i) {
-      const Decays* dec = sh.decays[i % 3];
-      const bool mild = dec[0].mild && (HPC == 1 || dec[1].mild);
-      float o[kCols];
-      tmem_ld16(lanes + kOi + ocol, o);
-      const float* cq = &dec[head].cq[part * kCols];
-#pragma unroll
-      for (int x = 0; x < kCols; x += 4) {
-        const float4 f = *reinterpret_cast<const float4*>(cq + x);
-        const float2 y = f2_get(mul2(f2(f.x, f.y), f2(o[x], o[x + 1]))), z = f2_get(mul2(f2(f.z, f.w), f2(o[x + 2], o[x + 3])));
-        o[x] = y.x, o[x + 1] = y.y, o[x + 2] = z.x, o[x + 3] = z.y;
-      }
-      if (!mild) {
-        float near[kCols];
-        tmem_ld16(lanes + kS + ocol, near);
-#pragma unroll
-        for (int x = 0; x < kCols; ++x) o[x] = fmaf(a.so, near[x], o[x]);
-      }
-      const int t1 = chunk_at(i) * kChunk + part * kCols, rows = min(kCols, S - t1);
-      if (mine) {
-        if constexpr (TMA) {
-          if (!a.o32) {
-            // a lane's element of 16 rows of the tile that takes Q's place
-            T* to = reinterpret_cast<T*>(sm + stage_of(i) + Lay::kQ + (r >> 6) * kSub + part * kCols * 128) + (r & 63);
-#pragma unroll
-            for (int x = 0; x < kCols; ++x) to[x * 64] = Elem<T>::from_f(o[x]);
-          }
-        }
-        if (a.o32) {
-          float* to = out32 + t1 * ss32;
-#pragma unroll
-          for (int x = 0; x < kCols; ++x, to += ss32)
-            if (x < rows) *to = o[x];
-        } else if (!TMA && a.o.p) {
-          T* to = out + t1 * a.o.ss;
-#pragma unroll
-          for (int x = 0; x < kCols; ++x, to += a.o.ss)
-            if (x < rows) *to = Elem<T>::from_f(o[x]);
-        }
-      }
-      if (a.dot) {
-        if constexpr (TMA) {
-          wait(kWith, i);
-          const T* from = reinterpret_cast<const T*>(sm + stage_of(i) + Lay::kK + (r >> 6) * kSub + part * kCols * 128) + (r & 63);
-          const int rows_live = mine ? L - t1 : 0;
-#pragma unroll
-          for (int x = 0; x < kCols; ++x) {
-            const float w = Elem<T>::to_f(from[x * 64]);
-            o[x] = x < rows_live ? o[x] * w : 0.0f;
-          }
-        } else {
-          const T* with = dot_row + t1 * a.dot_with.ss;
-#pragma unroll
-          for (int x = 0; x < kCols; ++x, with += a.dot_with.ss) o[x] = mine && t1 + x < L ? o[x] * Elem<T>::to_f(*with) : 0.0f;
-        }
-        int to = 0;
-        lanes_sum<kCols, 16, 1>(o, lane, to);
-        sh.dots[i & 1][warp][to] = o[0];
-      }
-    };
-
-    if (OUT && count > 0) {
-      wait_for(decayed(0));
-      publish(0);
-    }
-    if (count > 0) prepare(0);
-    if (!TMA && Lay::kStages == 2 && count > 1) fetch(1);
-    long long left = 0;  // logarithm of the segment's decay
     if constexpr (OUT) {
+      if (!TMA && count > 0) fetch(0);
+      // i: the chunk whose U is added; -1: the state before the first
 #pragma unroll 1
-      for (int i = 0; i < count; ++i) {
-        if (Lay::kStages == 1 && i + 1 < count) {
-          const bool is = chunk_at(i + 1) * kChunk + tid / 8 < L;
-          rk.prefetch(is), rv.prefetch(is), rq.prefetch(is);
+      for (int i = -1; i < count; ++i) {
+        if (Lay::kStages == 1 && i + 1 < count && i >= 0) rk.prefetch(L - chunk_at(i + 1) * kChunk);
+        bool bad = false;
+        float e = 0.0f;
+        if (i >= 0) wait_for(got_u(i));
+        // ck K of the next chunk takes the place of this one's, and K where there is room
+        if (i + 1 < count && (Lay::kStages == 2 || i < 0)) prepare(i + 1);
+        if (i >= 0) {
+          wait_for(paired(i));  // all of the chunk's flags are set
+          wait(kGotOi, i);
+          bad = sh.bad[i & 7];
+          e = sh.decays[i % 3][head].total;
+          if (bad) by_step(i);
         }
-        wait(kGotS, i);
-        if (HPC == 2 || quarter < 2) pairs(i);
-        arrive(kPairs);
-        wait(kPairs, i);  // all of the chunk's flags are set
-        wait_for(got_u(i));
-        wait(kGotOi, i);
-        if (a.dot && i > 0) dots_out(i - 1);
-        const bool bad = sh.bad[i & 7];
-        if (!bad) add_state(i);
-        else by_step(i);
+        const bool terms = i + 1 < count;
+        if (terms && i >= 0 && Lay::kStages == 1) wait_for(decayed(i + 1));
+        advance(lanes + u_at(i) + ucol, e, !bad && (i >= 0 || segments > 1 || a.first), terms, i + 1);
+        if (i >= 0) arrive(done(i).bar);
         if (i + 1 < count) {
-          wait_for(decayed(i + 1));
-          publish(i + 1);
-          // with two stages the next chunk's operands are made ready while O is on its way
-          if (Lay::kStages == 2) prepare(i + 1);
+          if (Lay::kStages == 1 && i >= 0) {  // K's place is free once P, which may be there, has been multiplied
+            if (Lay::kOver) wait(kGotO, i);
+            fetch(i + 1);
+            prepare(i + 1);
+          }
+          arrive(ready(i + 1).bar);
+          if (!TMA && Lay::kStages == 2 && i + 2 < count) fetch(i + 2);
         }
-        wait(kGotO, i);
-        if (!bad) outputs(i);
-        if (!TMA && i + Lay::kStages < count) fetch(i + Lay::kStages);
-        arrive(done(i).bar);
-        if (Lay::kStages == 1 && i + 1 < count) prepare(i + 1);
       }
-    } else {
-#pragma unroll 1
-      for (int i = 0; i < count; ++i) {
-        if (Lay::kStages == 2 && i + 1 < count) prepare(i + 1);
-        wait_for(got_u(i));
-        if (!sh.bad[i & 7]) add_state(i);
-        else by_step(i);
-        // what has left nothing leaves nothing: 64 bits hold a thousandfold of that
-        left = max(left + sh.decays[i % 3][head].log2, -(1LL << 45));
-        if (!TMA && i + Lay::kStages < count) fetch(i + Lay::kStages);
-        arrive(done(i).bar);
-        if (Lay::kStages == 1 && i + 1 < count) prepare(i + 1);
-      }
-    }
-    cp_wait();
-    if (OUT) {
-      if (a.dot && count > 0) {
-        wait_for(done(count - 1));
-        if (!sh.gave_up) dots_out(count - 1);
-      }
-      // the rows behind the last live chunk
-      for (int t = max(c_live, c_begin) * kChunk + part; t < min(c_end * kChunk, S); t += 4) put(t, 0.0f);
-      if (order == segments - 1) {
+      if (order == segments - 1 && (a.last || a.with)) {
+        hand_out();
         float with = 0.0f;
+#pragma unroll 1
+        for (int j = 0; j < NH; j += 8) {
+          float y[8];
+          tmem_ld(there + j, y);
+          tmem_ld_done(y);
 #pragma unroll
-        for (int i = 0; i < NH; ++i) {
-          const float2 y = f2_get(H[i / 2]);
-          if (mine && k0 + i < a.K) {
-            if (a.last) a.last[state_at(i)] = i % 2 ? y.y : y.x;
-            if (a.with) with = fmaf(a.with[state_at(i)], i % 2 ? y.y : y.x, with);
+          for (int x = 0; x < 8; ++x) {
+            if (mine && k0 + j + x < a.K) {
+              if (a.last) a.last[state_at(j + x)] = y[x];
+              if (a.with) with = fmaf(a.with[state_at(j + x)], y[x], with);
+            }
           }
         }
         with = warp_sum(with);
-        if (lane == 0) sh.part[0][warp] = with;
+        if (lane == 0) sh.part[0][warp % kGroupWarps] = with;
       }
     } else {
+      long long left = 0;  // logarithm of the segment's decay
+#pragma unroll 1
+      for (int i = 0; i < count; ++i) {
+        wait_for(got_u(i));
+        const bool bad = sh.bad[i & 7];
+        if (bad) by_step(i);
+        advance(lanes + u_at(i) + ucol, sh.decays[i % 3][head].total, !bad, false, 0);
+        // what has left nothing leaves nothing: 64 bits hold a thousandfold of that
+        left = max(left + sh.decays[i % 3][head].log2, -(1LL << 45));
+        arrive(done(i).bar);
+      }
+      hand_out();
       float* to = p.plan.states + ((long long)at.stream * segments + order) * kept;
+#pragma unroll 1
+      for (int j = 0; j < NH; j += 8) {
+        float y[8];
+        tmem_ld(there + j, y);
+        tmem_ld_done(y);
 #pragma unroll
-      for (int i = 0; i < NH; ++i) {
-        const float2 y = f2_get(H[i / 2]);
-        to[(k0 + i) * 128 + r] = mine && k0 + i < a.K ? (i % 2 ? y.y : y.x) : 0.0f;
+        for (int x = 0; x < 8; ++x) to[(k0 + j + x) * 128 + r] = mine && k0 + j + x < a.K ? y[x] : 0.0f;
       }
       if (part == 0 && lane == 0 && (HPC == 2 ? quarter % 2 == 0 : quarter == 0)) {
         // as whole part and fraction; beyond these nothing, or everything, is left
@@ -932,39 +1037,50 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegisters));
-    if (warp == kWorkers / 32) {
+    if (warp == 2 * kGroupWarps) {
       // ---------------- products
-      bool apart = false;  // the last chunk's outputs are where S is
-  #pragma unroll 1
+      const bool leader = elect();
+      auto pairs_of = [&](int i) {  // S
+        const uint32_t tiles = su32(sm) + stage_of(i);
+        const uint64_t dq = smem_desc_sw128(tiles + Lay::kQ), dk = smem_desc_sw128(tiles + Lay::kK);
+        if (leader) {
+          products<kIn, kIn, NT, kHeadSteps>([&](int x, int y, int s, uint32_t more) {
+            const uint32_t o = ((s / 4) * kSub + (s % 4) * 32) >> 4;
+            tc_mma(tmem + kS, dq + (x * kTile >> 4) + o, dk + (y * kTile >> 4) + o, idesc_of(64 * HPC), more);
+          });
+          tc_commit(su32(&sh.bars[kGotS]));
+        }
+        __syncwarp();
+      };
+      // A chunk's tiles are there with the copies, but for the one whose last rows have to be cleared.
+      auto early = [&](int i) { return TMA && L - chunk_at(i) * kChunk >= kChunk; };
+      if (OUT && count > 0 && early(0)) {
+        wait_for(full(0));
+        pairs_of(0);
+      }
+#pragma unroll 1
       for (int i = 0; i < count; ++i) {
         const uint32_t tiles = su32(sm) + stage_of(i);
-        const uint32_t scaled = su32(sm) + Lay::kScaled + (OUT ? 0 : i & 1) * kTerms * kTile;
-        const uint64_t dv = desc_mn(tiles + Lay::kV);
+        const uint64_t dv = desc_mn(tiles + Lay::kV), ds = desc_mn(su32(sm) + scaled_of(i));
         wait_for(ready(i));
-        if (OUT && apart) wait_for(done(i - 1));
-        if (lane == 0) {
-          if (OUT) {
-            constexpr uint32_t id = idesc_of(64 * HPC);
-            const uint64_t dq = smem_desc_sw128(tiles + Lay::kQ), dk = smem_desc_sw128(tiles + Lay::kK);
-            products<kIn, kIn, NT, kHeadSteps>([&](int x, int y, int s, uint32_t more) {
-              const uint32_t o = ((s / 4) * kSub + (s % 4) * 32) >> 4;
-              tc_mma(tmem + kS, dq + (x * kTile >> 4) + o, dk + (y * kTile >> 4) + o, id, more);
-            });
-            tc_commit(su32(&sh.bars[kGotS]));
-          }
-          constexpr uint32_t idu = idesc_of(HPC == 2 ? 128 : 64 * KB) | kRowsA | kRowsB;
-          const uint64_t ds = desc_mn(scaled);
+        if (!OUT && i >= 2) wait_for(done(i - 2));  // whose U is where this one's goes
+        if (OUT && !early(i)) {
+          if (i > 0) wait_for(done(i - 1));  // whose outputs may be where S goes
+          pairs_of(i);
+        }
+        if (leader) {
           const uint32_t du = tmem + u_at(i);
           products<kIn, kTerms, kTerms, 4>([&](int x, int y, int s, uint32_t more) {
-            tc_mma(du, dv + ((x * kTile + s * 2048) >> 4), ds + ((y * kTile + s * 2048) >> 4), idu, more);
+            tc_mma(du, dv + ((x * kTile + s * 2048) >> 4), ds + ((y * kTile + s * 2048) >> 4),
+                   idesc_of(HPC == 2 ? 128 : 64 * KB) | kRowsA | kRowsB, more);
           });
           tc_commit(su32(&sh.bars[got_u(i).bar]));
         }
         __syncwarp();
         if (!OUT) continue;
         if (i > 0) wait_for(done(i - 1));
-        if (lane == 0) {
-          const uint64_t dq = smem_desc_sw128(tiles + Lay::kQ);
+        const uint64_t dq = smem_desc_sw128(tiles + Lay::kQ);
+        if (leader) {
           products<NT, kIn, NT, kHeadSteps>([&](int x, int y, int s, uint32_t more) {
             tc_mma_ts(tmem + kOi, tmem + kH + x * KW + s * 8, dq + ((y * kTile + (s / 4) * kSub + (s % 4) * 32) >> 4),
                       idesc_of(64 * HPC), more);
@@ -972,55 +1088,64 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
           tc_commit(su32(&sh.bars[kGotOi]));
         }
         __syncwarp();
-        const Decays* dec = sh.decays[i % 3];
-        apart = !(dec[0].mild && (HPC == 1 || dec[1].mild));
-        wait(kPairs, i);
-        if (lane == 0) {
-          if (!sh.bad[i & 7]) {
-            const uint64_t dp = smem_desc_sw128(Lay::kOver ? tiles + Lay::kK : su32(sm) + Lay::kP);
-            const uint32_t to = tmem + (apart ? kS : kOi);
+        const bool apart = !mild_of(i);  // its outputs go where S is
+        wait_for(paired(i));
+        const uint64_t dp = smem_desc_sw128(Lay::kOver ? tiles + Lay::kK : su32(sm) + Lay::kP);
+        const uint32_t to = tmem + (apart ? kS : kOi);
+        if (leader) {
+          if (!sh.bad[i & 7])
             products<kIn, NT, NT, 4>([&](int x, int y, int s, uint32_t more) {
               tc_mma(to, dv + ((x * kTile + s * 2048) >> 4), dp + ((y * Lay::kPTerm + s * 32) >> 4), idesc_of(64 * HPC) | kRowsA,
                      apart ? more : 1u);
             });
-          }
           tc_commit(su32(&sh.bars[kGotO]));
         }
         __syncwarp();
+        if (i + 1 < count && early(i + 1)) {
+          if (apart) wait_for(done(i));
+          wait_for(full(i + 1));
+          pairs_of(i + 1);
+        }
       }
       if (count > 0) {  // all of them complete before tensor memory is given back
         wait_for(got_u(count - 1));
         if (OUT) wait(kGotO, count - 1);
       }
-    } else if (warp == kWorkers / 32 + 1) {
+    } else if (warp == 2 * kGroupWarps + 1) {
       // ---------------- copies
       if constexpr (TMA) {
         const int z = at.pass;
+        const bool leader = elect();
         // sub-tile b of an operand whose heads `of` heads share
         auto head_of = [&](int b, int of) { return HPC == 2 ? (at.h0 + b) / of : at.h0 / of; };
         auto load = [&](int i) {
           const uint32_t tiles = su32(sm) + stage_of(i), bar = su32(&sh.bars[full(i).bar]);
           const int t = chunk_at(i) * kChunk;
-          bar_expect(bar, (2 + kSubs * (OUT ? 2 : 1)) * kSub);
-          for (int b = 0; b < 2; ++b) {
-            const int x = HPC == 2 ? 0 : 64 * b;
-            if (b < kSubs) copy_in(tiles + Lay::kK + b * kSub, &args.k[z], x, head_of(b, a.k_of), t, at.n, bar);
-            copy_in(tiles + Lay::kV + b * kSub, &args.v[z], x, head_of(b, a.v_of), t, at.n, bar);
-            if (OUT && b < kSubs) copy_in(tiles + Lay::kQ + b * kSub, &args.q[z], x, head_of(b, a.q_of), t, at.n, bar);
+          if (leader) {
+            bar_expect(bar, (2 + kSubs * (OUT ? 2 : 1)) * kSub);
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              const int x = HPC == 2 ? 0 : 64 * b;
+              if (b < kSubs) copy_in(tiles + Lay::kK + b * kSub, &args.k[z], x, head_of(b, a.k_of), t, at.n, bar);
+              if (OUT && b < kSubs) copy_in(tiles + Lay::kQ + b * kSub, &args.q[z], x, head_of(b, a.q_of), t, at.n, bar);
+              copy_in(tiles + Lay::kV + b * kSub, &args.v[z], x, head_of(b, a.v_of), t, at.n, bar);
+            }
           }
+          __syncwarp();
         };
-        if (lane == 0)
-          for (int i = 0; i < min(count, 2); ++i) load(i);
+        for (int i = 0; i < min(count, 2); ++i) load(i);
         const bool out = OUT && a.o.p && !a.o32;
-  #pragma unroll 1
+#pragma unroll 1
         for (int i = 0; i < count; ++i) {
           const uint32_t tiles = su32(sm) + stage_of(i);
           const int t = chunk_at(i) * kChunk;
           if (OUT && a.dot) {  // takes the place of K, which S and ck K have been made from
-            wait(kPairs, i);
-            if (lane == 0) {
+            wait_for(paired(i));
+            wait_for(ready(i));
+            if (leader) {
               const uint32_t bar = su32(&sh.bars[kWith]);
               bar_expect(bar, 2 * kSub);
+#pragma unroll
               for (int b = 0; b < 2; ++b)
                 copy_in(tiles + Lay::kK + b * kSub, &args.with[z], HPC == 2 ? 0 : 64 * b, head_of(b, a.o_of), t, at.n, bar);
             }
@@ -1028,41 +1153,44 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
           }
           wait_for(done(i));
           if (OUT && a.dot) wait(kWith, i);  // also where nobody has read it
-          if (lane == 0) {
-            if (out && !sh.bad[i & 7] && !sh.gave_up) {  // from the place of Q
+          const bool good = !sh.bad[i & 7] && !sh.gave_up;
+          if (i + 2 < count && !sh.gave_up) load(i + 2);
+          if (OUT && leader) {
+            if (out && good) {
+#pragma unroll
               for (int b = 0; b < 2; ++b)
                 if (HPC == 1 ? 64 * b < a.V : at.h0 + b < p.H)
-                  copy_out(&args.o[z], HPC == 2 ? 0 : 64 * b, head_of(b, a.o_of), t, at.n, tiles + Lay::kQ + b * kSub);
+                  copy_out(&args.o[z], HPC == 2 ? 0 : 64 * b, head_of(b, a.o_of), t, at.n, su32(sm) + Lay::kOut + b * kSub);
               asm volatile("cp.async.bulk.commit_group;" ::: "memory");
               asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
             }
-            if (i + 2 < count && !sh.gave_up) load(i + 2);
+            bar_arrive(su32(&sh.bars[kStored]));
           }
           __syncwarp();
         }
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        if (leader) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         __syncwarp();
       }
     } else {
       // ---------------- decays: a warp for each head
-      const int x = warp - (kWorkers / 32 + 2), h = min(at.h0 + x, p.H - 1), end = at.h0 + x < p.H ? L : 0;
+      const int x = warp - (2 * kGroupWarps + 2), hx = min(at.h0 + x, p.H - 1), end = at.h0 + x < p.H ? L : 0;
       if (x < HPC) {
-        const float* g = static_cast<const float*>(p.decay.p) + at.n * p.decay.ns + h;
-        const float bias = p.bias ? p.bias[h] : 0.0f;
+        const float* g = static_cast<const float*>(p.decay.p) + at.n * p.decay.ns + hx;
+        const float bias = p.bias ? p.bias[hx] : 0.0f;
         auto read = [&](int i, int j) {
           const int t = chunk_at(i) * kChunk + 2 * lane + j;
           return t < end ? (p.decay.p ? g[t * p.decay.ss] : 0.0f) + bias : 0.0f;
         };
         float x0 = 0.0f, x1 = 0.0f;
         if (count > 0) x0 = read(0, 0), x1 = read(0, 1);
-  #pragma unroll 1
+#pragma unroll 1
         for (int i = 0; i < count; ++i) {
           if (i >= 3) wait_for(done(i - 3));  // whose place these take
           const float y0 = x0, y1 = x1;
           if (i + 1 < count) x0 = read(i + 1, 0), x1 = read(i + 1, 1);
           const bool bad = chunk_decays(a, y0, y1, sh.decays[i % 3][x]);
           if (lane == 0) {
-            if (x == 0) sh.bad[(i + 4) & 7] = 0;
+            if (x == 0) sh.bad[(i + 2) & 7] = 0;  // read last for chunk i - 6
             if (bad) sh.bad[i & 7] = 1;
           }
           __syncwarp();
@@ -1077,17 +1205,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
   if (OUT && a.cross && order == segments - 1 && tid < HPC && at.h0 + tid < p.H) {
     const float* x = sh.part[0];
     float y = 0.0f;
-    for (int w = 0; w < 16; ++w)
+    for (int w = 0; w < kGroupWarps; ++w)
       if (HPC == 1 || (w & 3) >> 1 == tid) y += x[w];
     a.cross[(long long)at.n * p.H + at.h0 + tid] = y;
   }
   // nothing is in flight any more, unless a wait has failed: then what was issued gets some time
-  if (sh.gave_up && warp == kWorkers / 32) {
+  if (sh.gave_up && warp == 2 * kGroupWarps) {
     const unsigned long long begin = gtime();
     while ((long long)(gtime() - begin) < kWaitNs / 4) {
     }
   }
-  if (warp == kWorkers / 32)
+  if (warp == 2 * kGroupWarps)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
