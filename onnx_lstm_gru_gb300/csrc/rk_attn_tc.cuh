@@ -32,10 +32,11 @@
 // most 64 elements: of the products' 128 x 128 blocks the diagonal ones are
 // used) over a piece of the sequence, in groups of warps that meet at
 // mbarriers:
-//   eight read S, write P and hand out the outputs;
+//   eight read S and write P;
+//   eight hand out the outputs;
 //   eight keep the state, add U to it and scale K for the next chunk;
 //   one issues the products, one copies tiles in and out (TMA, for bfloat16
-//   rows of whole 16-byte pieces; else the first sixteen do), and one for each
+//   rows of whole 16-byte pieces; else the three groups do), and one for each
 //   head takes the decays of later chunks.
 // The products of one chunk run while the next one's operands are made ready:
 // O_i follows P_i; S_(i+1) and U_(i+1) follow ck K; Oi_(i+1) follows the
@@ -60,12 +61,12 @@ namespace atc {
 
 using namespace ptc;
 
-constexpr int kChunk = 64, kGroup = 256, kThreads = 2 * kGroup + 128, kTerms = 3;
+constexpr int kChunk = 64, kGroup = 256, kThreads = 3 * kGroup + 128, kTerms = 3;
 constexpr int kGroupWarps = kGroup / 32;
-// Registers: 640 threads are launched with 96 each; the warps that keep the
-// state get what the others can spare.
-constexpr int kOutRegisters = 80, kStateRegisters = 128, kOtherRegisters = 64;
-static_assert(kGroup * (kOutRegisters + kStateRegisters) + 128 * kOtherRegisters <= kThreads * 96,
+// Registers: 896 threads are launched with 72 each; the group that keeps the
+// state gets what the others can spare.
+constexpr int kStateRegisters = 112, kOtherRegisters = 56;
+static_assert(kGroup * (2 * kOtherRegisters + kStateRegisters) + 128 * kOtherRegisters <= kThreads * 72,
               "no more than the block was launched with");
 constexpr uint32_t kSub = kChunk * 128;      // bytes of 64 rows of 64 elements
 constexpr uint32_t kTile = 2 * kSub;         // an operand's term: 64 rows of 128 elements, or of two heads of 64
@@ -91,7 +92,10 @@ struct Layout {
   static constexpr uint32_t kP = kOver ? kK : kAfter;
   static constexpr uint32_t kPTerm = HPC * kSub;
   static constexpr uint32_t kOut = kAfter + (kOver || !OUT ? 0 : NT * kPTerm);  // outputs, where they are copied out
-  static constexpr uint32_t kEnd = kOut + (OUT && kIn == 1 ? kTile : 0);
+  static constexpr uint32_t kAfterOut = kOut + (OUT && kIn == 1 ? kTile : 0);
+  // what outputs are multiplied with for the decays: where K was, if there is no room
+  static constexpr bool kWithApart = kIn == 1 && OUT && NT == kTerms && HPC == 1;
+  static constexpr uint32_t kEnd = kAfterOut + (kWithApart ? kTile : 0);
   static_assert(NT * kPTerm <= kIn * kTile || !kOver, "P fits over K");
   static constexpr size_t kBytes = kEnd + 1024;  // alignment
 };
@@ -110,7 +114,7 @@ struct Decays {
 // second one for odd chunks.
 enum Bar {
   kTiles, kDone = kTiles + 2, kPairs = kDone + 2, kSteps = kPairs + 2,  // of warps
-  kGotS, kGotU, kGotOi = kGotU + 2, kGotO, kFull, kWith = kFull + 2, kStored, kDecay, kBars = kDecay + 3
+  kGotS, kGotU, kGotOi = kGotU + 2, kGotO, kFull = kGotO + 2, kWith = kFull + 2, kStored, kDecay, kBars = kDecay + 3
 };
 
 struct Small {
@@ -309,7 +313,7 @@ __device__ __forceinline__ bool chunk_decays(const AttnPass& a, float x0, float 
   }
   const long long total = __shfl_sync(0xffffffffu, sum, 31);
   bool mild = true;
-#pragma unroll
+#pragma unroll 1
   for (int j = 0; j < 2; ++j) {
     const long long G = j ? sum : sum - fix[1], s = backward ? -G : G;
     const int i = 2 * lane + j;
@@ -361,41 +365,44 @@ struct Rows {
   __device__ __forceinline__ void load(unsigned char* tile, int rows, int vec) {
     constexpr int kIn = kSplit<T>;
     const int thread = threadIdx.x % kGroup;
-#pragma unroll
+#pragma unroll 1
     for (int b = 0; b < SUBS; ++b) {
+      const int first = (HPC == 2 ? 0 : 64 * b) + 8 * (thread % 8);
+      float x[2][8];  // both are on their way together
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const int first = (HPC == 2 ? 0 : 64 * b) + 8 * (thread % 8);
         const bool fetch = thread / 8 + 32 * half < rows && (on >> b & 1);
-        unsigned char* dst = tile + b * kSub + piece_at(thread + half * kGroup);
         const T* from = src + b * next + half * 32 * ss;
-        float x[8];
-        fill(x, 0.0f);
+        fill(x[half], 0.0f);
         if (vec) {
           if (fetch) {
             if constexpr (sizeof(T) == 4) {
               float y[4];
               Piece<T, 4>::load(from, y);
-              x[0] = y[0], x[1] = y[1], x[2] = y[2], x[3] = y[3];
+              x[half][0] = y[0], x[half][1] = y[1], x[half][2] = y[2], x[half][3] = y[3];
               if (first + 4 < size) {
                 Piece<T, 4>::load(from + 4, y);
-                x[4] = y[0], x[5] = y[1], x[6] = y[2], x[7] = y[3];
+                x[half][4] = y[0], x[half][5] = y[1], x[half][6] = y[2], x[half][7] = y[3];
               }
             } else {
-              Piece<T, 8>::load(from, x);
+              Piece<T, 8>::load(from, x[half]);
             }
           }
         } else {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            if (fetch && first + i < size) x[i] = Elem<T>::to_f(from[i]);
+            if (fetch && first + i < size) x[half][i] = Elem<T>::to_f(from[i]);
         }
+      }
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        unsigned char* dst = tile + b * kSub + piece_at(thread + half * kGroup);
         uint32_t w[kIn][4];
         F2 unused = f2(0.0f, 0.0f);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           uint32_t s[kIn];
-          split<kIn>(f2(x[2 * i], x[2 * i + 1]), s, unused);
+          split<kIn>(f2(x[half][2 * i], x[half][2 * i + 1]), s, unused);
 #pragma unroll
           for (int j = 0; j < kIn; ++j) w[j][i] = s[j];
         }
@@ -421,7 +428,7 @@ template <typename T, int HPC, int SUBS>
 __device__ __forceinline__ void scale_tile(const unsigned char* k, unsigned char* out, const Decays* d, F2& finite) {
   constexpr int kIn = kSplit<T>;
   const int thread = threadIdx.x % kGroup;
-#pragma unroll 1
+#pragma unroll 2
   for (int i = 0; i < 2 * SUBS; ++i) {
     const int b = i / 2, piece = thread + i % 2 * kGroup;
     const uint32_t at = b * kSub + piece_at(piece);
@@ -598,12 +605,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
   auto chunk_at = [&](int i) { return back ? c_live - 1 - i : c_begin + i; };
 
   if (tid == 0) {
-    // who arrives: the state's warps, or both groups; without outputs the first scales and the second adds
-    const int both = 2 * kGroupWarps;
+    // who arrives; without outputs the first group scales and the third adds
     for (int i = 0; i < kBars; ++i) {
       int n = i >= kDecay ? HPC : 1;
-      if (i < kDone) n = OUT && !TMA ? both : kGroupWarps;
-      else if (i < kPairs) n = OUT ? both : kGroupWarps;
+      if (i < kDone) n = OUT && !TMA ? 3 * kGroupWarps : kGroupWarps;
+      else if (i < kPairs) n = OUT ? 2 * kGroupWarps : kGroupWarps;
       else if (i <= kSteps) n = kGroupWarps;
       bar_init(su32(&sh.bars[i]), n);
     }
@@ -611,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
     for (int i = 0; i < 8; ++i) sh.bad[i] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 2 * kGroupWarps) {
+  if (warp == 3 * kGroupWarps) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&sh.tmem)), "r"(512u) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -628,6 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
   auto done = [](int i) { return Phase{kDone + (i & 1), i >> 1}; };
   auto paired = [](int i) { return Phase{kPairs + (i & 1), i >> 1}; };
   auto got_u = [](int i) { return Phase{kGotU + (i & 1), i >> 1}; };
+  auto got_o = [](int i) { return Phase{kGotO + (i & 1), i >> 1}; };
   auto full = [](int i) { return Phase{kFull + (i & 1), i >> 1}; };
   auto decayed = [](int i) { return Phase{kDecay + i % 3, i / 3}; };
   auto wait = [&](int bar, int n) { wait_bar(sh, bar, n & 1); };
@@ -669,16 +676,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
   };
 
   if (warp < kGroupWarps) {
-    // ---------------- pairs and outputs
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOutRegisters));
-    Rows<T, HPC> rq(a.q, at.n, at.h0, p.H, a.q_of, a.K, t_first, step), rv(a.v, at.n, at.h0, p.H, a.v_of, a.V, t_first, step);
-    auto fetch = [&](int i) {
-      const int rows = L - chunk_at(i) * kChunk;
-      rv.template load<2>(sm + stage_of(i) + Lay::kV, rows, vec);
-      if (OUT) rq.template load<kSubs>(sm + stage_of(i) + Lay::kQ, rows, vec);
-    };
+    // ---------------- pairs
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegisters));
     if constexpr (!OUT) {
-      // without outputs: K of the next chunk, while the other group adds
+      // without outputs: K of the next chunk, while the third group adds
+      Rows<T, HPC> rv(a.v, at.n, at.h0, p.H, a.v_of, a.V, t_first, step);
       Rows<T, HPC> rk(a.k, at.n, at.h0, p.H, a.k_of, a.K, t_first, step);
 #pragma unroll 1
       for (int i = 0; i < count; ++i) {
@@ -686,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
         else if (i >= 2) wait_for(got_u(i - 2));                          // whose ck K this takes
         if (!TMA) {
           rk.template load<kSubs>(sm + stage_of(i) + Lay::kK, L - chunk_at(i) * kChunk, vec);
-          fetch(i);
+          rv.template load<2>(sm + stage_of(i) + Lay::kV, L - chunk_at(i) * kChunk, vec);
           if (i + 1 < count) {
             const int rows = L - chunk_at(i + 1) * kChunk;
             rk.prefetch(rows), rv.prefetch(rows);
@@ -698,23 +700,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
       }
     } else {
       const int ocol = (HPC == 2 ? head * 64 : 0) + part * kCols;  // columns of S and O
-      // outputs of lane v
-      T* out = static_cast<T*>(a.o.p) + at.n * a.o.ns + (long long)(h / a.o_of) * a.V + v;
-      float* out32 = a.o32 + ((long long)at.n * S * p.H + h) * a.V + v;
-      const long long ss32 = (long long)p.H * a.V;
-      const T* dot_row = static_cast<const T*>(a.dot_with.p) + at.n * a.dot_with.ns + (long long)(h / a.o_of) * a.V + v;
-      // The products of chunk i's outputs, added up over the lanes' warps.
-      auto dots_out = [&](int i) {
-        if (tid < 64 * HPC) {
-          const int hd = tid / 64, m = tid % 64, t = chunk_at(i) * kChunk + m;
-          if (t < L && at.h0 + hd < p.H) {
-            const float* x = &sh.dots[i & 1][m / kCols * 4][m % kCols];
-            const float y = HPC == 2 ? x[2 * hd * kCols] + x[(2 * hd + 1) * kCols]
-                                     : (x[0] + x[kCols]) + (x[2 * kCols] + x[3 * kCols]);
-            a.dot[((long long)at.n * p.H + at.h0 + hd) * S + t] = y;
-          }
-        }
-      };
       // The loops below go by 8 columns and are not unrolled: what runs between
       // two of a chunk's barriers has to stay in the instruction cache.
       // P of row m of S, 32 of its columns
@@ -725,12 +710,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
         const float hi = d.hi[m], lo = d.lo[m];
         F2 finite = zero;
         unsigned char* row = (Lay::kOver ? sm + Lay::kK : sm + Lay::kP) + (HPC == 2 ? r : m) * 128;
+        float next[8];
+        tmem_ld(lanes + kS + ocol, next);
 #pragma unroll 1
         for (int c = 0; c < kCols; c += 8) {
           const int n0 = part * kCols + c;
           float s[8];
-          tmem_ld(lanes + kS + ocol + c, s);
-          tmem_ld_done(s);
+          tmem_ld_done(next);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) s[j] = next[j];
+          if (c + 8 < kCols) tmem_ld(lanes + kS + ocol + c + 8, next);
           F2 x[4];
           if (mild) {
             const float4 f = *reinterpret_cast<const float4*>(&d.bn[n0]), g = *reinterpret_cast<const float4*>(&d.bn[n0 + 4]);
@@ -760,18 +749,71 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
         }
         if (!is_finite(finite)) sh.bad[i & 7] = 1;
       };
+      Rows<T, HPC> rq(a.q, at.n, at.h0, p.H, a.q_of, a.K, t_first, step);
+      auto fetch = [&](int i) {
+        rq.template load<kSubs>(sm + stage_of(i) + Lay::kQ, L - chunk_at(i) * kChunk, vec);
+        arrive(ready(i).bar);
+      };
+      if (!TMA)
+        for (int i = 0; i < min(count, Lay::kStages); ++i) fetch(i);
+#pragma unroll 1
+      for (int i = 0; i < count; ++i) {
+        if (!TMA && i + Lay::kStages < count) rq.prefetch(L - chunk_at(i + Lay::kStages) * kChunk);
+        wait_for(decayed(i));
+        wait(kGotS, i);
+        if (i > 0) wait_for(got_o(i - 1));  // which P was multiplied for
+        if (HPC == 2 || quarter < 2) pairs(i);
+        if (TMA) wait_for(full(i));  // V, of the copies' own making
+        // with one head S has rows for two quarters of the lanes; the others look V over
+        if (HPC == 2 && !tile_finite<kGroup>(sm + stage_of(i) + Lay::kV, tid)) sh.bad[i & 7] = 1;
+        if (HPC == 1 && quarter >= 2 && !tile_finite<kGroup / 2>(sm + stage_of(i) + Lay::kV, (part * 2 + (quarter & 1)) * 32 + lane))
+          sh.bad[i & 7] = 1;
+        arrive(paired(i).bar);
+        if (!TMA && i + Lay::kStages < count) {
+          wait(kGotOi, i);
+          fetch(i + Lay::kStages);
+        }
+      }
+    }
+  } else if (warp < 2 * kGroupWarps) {
+    // ---------------- outputs
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegisters));
+    if constexpr (OUT) {
+      const int ocol = (HPC == 2 ? head * 64 : 0) + part * kCols;  // columns of S and O
+      const int thread = tid - kGroup;
+      // outputs of lane v
+      T* out = static_cast<T*>(a.o.p) + at.n * a.o.ns + (long long)(h / a.o_of) * a.V + v;
+      float* out32 = a.o32 + ((long long)at.n * S * p.H + h) * a.V + v;
+      const long long ss32 = (long long)p.H * a.V;
+      const T* dot_row = static_cast<const T*>(a.dot_with.p) + at.n * a.dot_with.ns + (long long)(h / a.o_of) * a.V + v;
+      // The products of chunk i's outputs, added up over the lanes' warps.
+      auto dots_out = [&](int i) {
+        if (thread < 64 * HPC) {
+          const int hd = thread / 64, m = thread % 64, t = chunk_at(i) * kChunk + m;
+          if (t < L && at.h0 + hd < p.H) {
+            const float* x = &sh.dots[i & 1][m / kCols * 4][m % kCols];
+            const float y = HPC == 2 ? x[2 * hd * kCols] + x[(2 * hd + 1) * kCols]
+                                     : (x[0] + x[kCols]) + (x[2 * kCols] + x[3 * kCols]);
+            a.dot[((long long)at.n * p.H + at.h0 + hd) * S + t] = y;
+          }
+        }
+      };
       auto outputs = [&](int i) {
         const Decays* dec = sh.decays[i % 3];
         const bool mild = mild_of(i), dot = a.dot, wide = a.o32, any = a.o.p;
         const int t0 = chunk_at(i) * kChunk + part * kCols;
         if (TMA && i > 0) wait(kStored, i - 1);
         if (TMA && dot) wait(kWith, i);
+        float next[8];
+        tmem_ld(lanes + kOi + ocol, next);
 #pragma unroll 1
         for (int c = 0; c < kCols; c += 8) {
           float o[8], near[8];
-          tmem_ld(lanes + kOi + ocol + c, o);
+          tmem_ld_done(next);
+#pragma unroll
+          for (int x = 0; x < 8; ++x) o[x] = next[x];
+          if (c + 8 < kCols) tmem_ld(lanes + kOi + ocol + c + 8, next);
           if (!mild) tmem_ld(lanes + kS + ocol + c, near);
-          tmem_ld_done(o);
           const float* cq = &dec[head].cq[part * kCols + c];
 #pragma unroll
           for (int x = 0; x < 8; x += 4) {
@@ -781,6 +823,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
           }
           if (!mild) {
             tmem_ld_done(near);
+            asm volatile("" ::: "memory");
 #pragma unroll
             for (int x = 0; x < 8; ++x) o[x] = fmaf(a.so, near[x], o[x]);
           }
@@ -805,7 +848,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
           if (dot) {
             const int live_rows = mine ? L - t1 : 0;
             if constexpr (TMA) {
-              const T* from = reinterpret_cast<const T*>(sm + stage_of(i) + Lay::kK) + at_tile;
+              const T* from = reinterpret_cast<const T*>(sm + (Lay::kWithApart ? Lay::kAfterOut : stage_of(i) + Lay::kK)) + at_tile;
 #pragma unroll
               for (int x = 0; x < 8; ++x) {
                 const float w = Elem<T>::to_f(from[x * 64]);
@@ -818,43 +861,31 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
             }
             int to = 0;
             lanes_sum<8, 16, 1>(o, lane, to);
-            sh.dots[i & 1][warp][c + to] = o[0];
+            sh.dots[i & 1][warp - kGroupWarps][c + to] = o[0];
           }
         }
       };
+      Rows<T, HPC> rv(a.v, at.n, at.h0, p.H, a.v_of, a.V, t_first, step);
+      auto fetch = [&](int i) {
+        rv.template load<2>(sm + stage_of(i) + Lay::kV, L - chunk_at(i) * kChunk, vec);
+        arrive(ready(i).bar);
+      };
       if (!TMA)
-        for (int i = 0; i < min(count, Lay::kStages); ++i) {
-          fetch(i);
-          arrive(ready(i).bar);
-        }
+        for (int i = 0; i < min(count, Lay::kStages); ++i) fetch(i);
 #pragma unroll 1
       for (int i = 0; i < count; ++i) {
-        if (Lay::kStages == 1 && i + 1 < count) {
-          const int rows = L - chunk_at(i + 1) * kChunk;
-          rv.prefetch(rows), rq.prefetch(rows);
-        }
+        if (!TMA && i + Lay::kStages < count) rv.prefetch(L - chunk_at(i + Lay::kStages) * kChunk);
         wait_for(decayed(i));
-        wait(kGotS, i);
-        if (HPC == 2 || quarter < 2) pairs(i);
-        if (TMA) wait_for(full(i));  // V, of the copies' own making
-        // with one head S has rows for two quarters of the lanes; the others look V over
-        if (HPC == 2 && !tile_finite<kGroup>(sm + stage_of(i) + Lay::kV, tid)) sh.bad[i & 7] = 1;
-        if (HPC == 1 && quarter >= 2 && !tile_finite<kGroup / 2>(sm + stage_of(i) + Lay::kV, (part * 2 + (quarter & 1)) * 32 + lane))
-          sh.bad[i & 7] = 1;
-        arrive(paired(i).bar);
+        wait_for(paired(i));  // all of the chunk's flags are set
         if (a.dot && i > 0) {
           wait_for(done(i - 1));
           dots_out(i - 1);
         }
-        wait_for(paired(i));  // all of the chunk's flags are set
-        wait(kGotO, i);
+        wait_for(got_o(i));
+        if (!TMA && i + Lay::kStages < count) fetch(i + Lay::kStages);
         if (!sh.bad[i & 7]) outputs(i);
         else if (TMA && a.dot) wait(kWith, i);  // the copies are not left behind
         arrive(done(i).bar);
-        if (!TMA && i + Lay::kStages < count) {
-          fetch(i + Lay::kStages);
-          arrive(ready(i + Lay::kStages).bar);
-        }
       }
       if (a.dot && count > 0) {
         wait_for(done(count - 1));
@@ -867,7 +898,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
         else if (a.o.p) out[t * a.o.ss] = Elem<T>::from_f(0.0f);
       }
     }
-  } else if (warp < 2 * kGroupWarps) {
+  } else if (warp < 3 * kGroupWarps) {
     // ---------------- the state
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kStateRegisters));
     const int k0 = part * NH, ucol = HPC == 2 ? head * 64 + part * 32 : part * NH;  // state elements, U's columns
@@ -979,7 +1010,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
         if (i >= 0) arrive(done(i).bar);
         if (i + 1 < count) {
           if (Lay::kStages == 1 && i >= 0) {  // K's place is free once P, which may be there, has been multiplied
-            if (Lay::kOver) wait(kGotO, i);
+            if (Lay::kOver) wait_for(got_o(i));
             fetch(i + 1);
             prepare(i + 1);
           }
@@ -1037,7 +1068,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegisters));
-    if (warp == 2 * kGroupWarps) {
+    if (warp == 3 * kGroupWarps) {
       // ---------------- products
       const bool leader = elect();
       auto pairs_of = [&](int i) {  // S
@@ -1098,7 +1129,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
               tc_mma(to, dv + ((x * kTile + s * 2048) >> 4), dp + ((y * Lay::kPTerm + s * 32) >> 4), idesc_of(64 * HPC) | kRowsA,
                      apart ? more : 1u);
             });
-          tc_commit(su32(&sh.bars[kGotO]));
+          tc_commit(su32(&sh.bars[got_o(i).bar]));
         }
         __syncwarp();
         if (i + 1 < count && early(i + 1)) {
@@ -1109,9 +1140,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
       }
       if (count > 0) {  // all of them complete before tensor memory is given back
         wait_for(got_u(count - 1));
-        if (OUT) wait(kGotO, count - 1);
+        if (OUT) wait_for(got_o(count - 1));
       }
-    } else if (warp == 2 * kGroupWarps + 1) {
+    } else if (warp == 3 * kGroupWarps + 1) {
       // ---------------- copies
       if constexpr (TMA) {
         const int z = at.pass;
@@ -1137,24 +1168,33 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
         const bool out = OUT && a.o.p && !a.o32;
 #pragma unroll 1
         for (int i = 0; i < count; ++i) {
-          const uint32_t tiles = su32(sm) + stage_of(i);
           const int t = chunk_at(i) * kChunk;
-          if (OUT && a.dot) {  // takes the place of K, which S and ck K have been made from
-            wait_for(paired(i));
-            wait_for(ready(i));
+          if (OUT && a.dot) {
+            if (Lay::kWithApart) {
+              if (i > 0) wait_for(done(i - 1));
+            } else {  // takes the place of K, which S and ck K have been made from
+              wait_for(paired(i));
+              wait_for(ready(i));
+            }
             if (leader) {
-              const uint32_t bar = su32(&sh.bars[kWith]);
+              const uint32_t bar = su32(&sh.bars[kWith]), to = su32(sm) + (Lay::kWithApart ? Lay::kAfterOut : stage_of(i) + Lay::kK);
               bar_expect(bar, 2 * kSub);
 #pragma unroll
               for (int b = 0; b < 2; ++b)
-                copy_in(tiles + Lay::kK + b * kSub, &args.with[z], HPC == 2 ? 0 : 64 * b, head_of(b, a.o_of), t, at.n, bar);
+                copy_in(to + b * kSub, &args.with[z], HPC == 2 ? 0 : 64 * b, head_of(b, a.o_of), t, at.n, bar);
             }
             __syncwarp();
+          }
+          // the stage is free with the last product of the chunk, or once the outputs have been multiplied
+          const bool early = OUT && (Lay::kWithApart || !a.dot);
+          if (early) {
+            wait_for(got_o(i));
+            if (i + 2 < count && !sh.gave_up) load(i + 2);
           }
           wait_for(done(i));
           if (OUT && a.dot) wait(kWith, i);  // also where nobody has read it
           const bool good = !sh.bad[i & 7] && !sh.gave_up;
-          if (i + 2 < count && !sh.gave_up) load(i + 2);
+          if (!early && i + 2 < count && !sh.gave_up) load(i + 2);
           if (OUT && leader) {
             if (out && good) {
 #pragma unroll
@@ -1173,7 +1213,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
       }
     } else {
       // ---------------- decays: a warp for each head
-      const int x = warp - (2 * kGroupWarps + 2), hx = min(at.h0 + x, p.H - 1), end = at.h0 + x < p.H ? L : 0;
+      const int x = warp - (3 * kGroupWarps + 2), hx = min(at.h0 + x, p.H - 1), end = at.h0 + x < p.H ? L : 0;
       if (x < HPC) {
         const float* g = static_cast<const float*>(p.decay.p) + at.n * p.decay.ns + hx;
         const float bias = p.bias ? p.bias[hx] : 0.0f;
@@ -1210,12 +1250,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
     a.cross[(long long)at.n * p.H + at.h0 + tid] = y;
   }
   // nothing is in flight any more, unless a wait has failed: then what was issued gets some time
-  if (sh.gave_up && warp == 2 * kGroupWarps) {
+  if (sh.gave_up && warp == 3 * kGroupWarps) {
     const unsigned long long begin = gtime();
     while ((long long)(gtime() - begin) < kWaitNs / 4) {
     }
   }
-  if (warp == 2 * kGroupWarps)
+  if (warp == 3 * kGroupWarps)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
