@@ -63,11 +63,6 @@ using namespace ptc;
 
 constexpr int kChunk = 64, kGroup = 256, kThreads = 3 * kGroup + 128, kTerms = 3;
 constexpr int kGroupWarps = kGroup / 32;
-// Registers: 896 threads are launched with 72 each; the group that keeps the
-// state gets what the others can spare.
-constexpr int kStateRegisters = 112, kOtherRegisters = 56;
-static_assert(kGroup * (2 * kOtherRegisters + kStateRegisters) + 128 * kOtherRegisters <= kThreads * 72,
-              "no more than the block was launched with");
 constexpr uint32_t kSub = kChunk * 128;      // bytes of 64 rows of 64 elements
 constexpr uint32_t kTile = 2 * kSub;         // an operand's term: 64 rows of 128 elements, or of two heads of 64
 constexpr int kCols = kChunk / 2;            // of a chunk's columns of S and O, those of a thread
@@ -297,14 +292,10 @@ __device__ __forceinline__ long long fixed_log2(float x) {
 __device__ __forceinline__ bool chunk_decays(const AttnPass& a, float x0, float x1, Decays& out) {
   const bool backward = a.backward;
   const int lane = threadIdx.x % 32;
-  const float x[2] = {x0, x1};
   long long fix[2];
-  bool bad = false;
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    bad = bad || !(x[j] < 80.0f);  // NaN, or growth that no float32 holds for long
-    fix[j] = fixed_log2(x[j]);
-  }
+  // NaN, or growth that no float32 holds for long
+  bool bad = !(x0 < 80.0f) || !(x1 < 80.0f);
+  fix[0] = fixed_log2(x0), fix[1] = fixed_log2(x1);
   long long sum = fix[0] + fix[1];
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -481,7 +472,7 @@ __device__ __forceinline__ void products(F mma) {
     for (int a = 0; a < NA; ++a) {
       const int b = sum - a;
       if (b < 0 || b >= NB) continue;
-#pragma unroll
+#pragma unroll 1
       for (int s = 0; s < STEPS; ++s) {
         mma(a, b, s, more);
         more = 1;
@@ -583,7 +574,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
   constexpr int NH = HPC == 2 ? 32 : 32 * KB;  // state elements of a thread
   constexpr int KW = HPC == 2 ? 32 : 32 * KB;  // tensor memory columns of one of the state's terms
   constexpr uint32_t kS = 0, kOi = 64 * HPC, kU = 128 * HPC, kH = kU + 128;
-  static_assert(kH + NT * KW <= 512, "tensor memory");
+  // the state itself: the sum of its terms where there are three, which hold all of float32's bits; else beside
+  // them, or where S would be
+  constexpr bool kSum = OUT && NT == 3;
+  constexpr uint32_t kF = OUT ? kH + NT * KW : 256;
+  static_assert(kF + (kSum ? 0 : 2 * KW) <= 512, "tensor memory");
   constexpr int kHeadSteps = HPC == 2 ? 4 : 4 * KB;  // steps of 16 over a head's elements
   constexpr int kSubs = HPC == 2 ? 2 : KB;
   extern __shared__ unsigned char raw[];
@@ -677,7 +672,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
 
   if (warp < kGroupWarps) {
     // ---------------- pairs
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegisters));
     if constexpr (!OUT) {
       // without outputs: K of the next chunk, while the third group adds
       Rows<T, HPC> rv(a.v, at.n, at.h0, p.H, a.v_of, a.V, t_first, step);
@@ -777,7 +771,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
     }
   } else if (warp < 2 * kGroupWarps) {
     // ---------------- outputs
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegisters));
     if constexpr (OUT) {
       const int ocol = (HPC == 2 ? head * 64 : 0) + part * kCols;  // columns of S and O
       const int thread = tid - kGroup;
@@ -900,7 +893,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
     }
   } else if (warp < 3 * kGroupWarps) {
     // ---------------- the state
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kStateRegisters));
     const int k0 = part * NH, ucol = HPC == 2 ? head * 64 + part * 32 : part * NH;  // state elements, U's columns
     // the state, transposed: lane v, elements k0 ..
     const long long state = ((long long)at.n * p.H + h) * a.K * a.V;
@@ -910,106 +902,162 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
     constexpr long long kept = (long long)KB * 64 * 128;  // a state in scratch: [k][lane]
     Rows<T, HPC> rk(a.k, at.n, at.h0, p.H, a.k_of, a.K, t_first, step);
     auto fetch = [&](int i) { rk.template load<kSubs>(sm + stage_of(i) + Lay::kK, L - chunk_at(i) * kChunk, vec); };
-    F2 H[NH / 2];
+    // The state lives in tensor memory.  Elements j .. j + 15 of it, from there:
+    auto read_state = [&](int j, F2 (&H)[8]) {
+      if constexpr (kSum) {
+        float t[NT][8];
 #pragma unroll
-    for (int i = 0; i < NH / 2; ++i) H[i] = zero;
-    // A state that is read or handed out goes through U's place, by loops that are not unrolled.
-    const uint32_t there = lanes + u_at(0) + ucol;
-    if (OUT && (segments > 1 || a.first)) {
-      const float* from = p.plan.states + ((long long)at.stream * segments + order) * kept;
-#pragma unroll 1
-      for (int j = 0; j < NH; j += 8) {
-        uint32_t w[8];
+        for (int x = 0; x < NT; ++x) tmem_ld(lanes + kH + x * KW + (k0 + j) / 2, t[x]);
+#pragma unroll
+        for (int x = 0; x < NT; ++x) tmem_ld_done(t[x]);
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
-          const int k = k0 + j + x;
-          w[x] = __float_as_uint(segments > 1 ? from[k * 128 + r] : mine && k < a.K ? a.first[state_at(j + x)] : 0.0f);
+          H[x] = pair_of(__float_as_uint(t[NT - 1][x]));
+#pragma unroll
+          for (int y = NT - 2; y >= 0; --y) H[x] = add2(H[x], pair_of(__float_as_uint(t[y][x])));
         }
-        tmem_st<8>(there + j, w);
+      } else {
+        float t[16];
+        tmem_ld(lanes + kF + k0 + j, t);
+        tmem_ld_done(t);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) H[x] = f2(t[2 * x], t[2 * x + 1]);
       }
+    };
+    // Elements j .. j + 15 to there, for chunk i.
+    auto write_state = [&](int j, const F2 (&H)[8], F2& finite) {
+      if constexpr (OUT) {
+        uint32_t w[NT][8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          uint32_t s[NT];
+          split<NT>(H[x], s, finite);
+#pragma unroll
+          for (int y = 0; y < NT; ++y) w[y][x] = s[y];
+        }
+#pragma unroll
+        for (int x = 0; x < NT; ++x) tmem_st<8>(lanes + kH + x * KW + (k0 + j) / 2, w[x]);
+      }
+      if constexpr (!kSum) {
+        uint32_t w[16];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const float2 y = f2_get(H[x]);
+          w[2 * x] = __float_as_uint(y.x), w[2 * x + 1] = __float_as_uint(y.y);
+        }
+        tmem_st<16>(lanes + kF + k0 + j, w);
+      }
+    };
+    auto wrote = [&](F2 finite, int i) {
       tmem_st_done();
-    }
-    // H = e H + U, and its terms to tensor memory for chunk i.
-    auto advance = [&](uint32_t u_from, float e, bool add, bool terms, int i) {
+      if (OUT && mine && !is_finite(finite)) sh.bad[i & 7] = 1;
+    };
+    // The state before the first chunk.
+    auto begin_state = [&]() {
+      const float* from = p.plan.states + ((long long)at.stream * segments + order) * kept;
       F2 finite = zero;
-#pragma unroll
+#pragma unroll 1
       for (int j = 0; j < NH; j += 16) {
-        if (add) {
-          float u[16];
-          tmem_ld(u_from + j, u);
-          tmem_ld_done(u);
+        F2 H[8];
 #pragma unroll
-          for (int x = 0; x < 8; ++x) H[j / 2 + x] = fma2(f2(e, e), H[j / 2 + x], f2(u[2 * x], u[2 * x + 1]));
-        }
-        if (OUT && terms) {
-          uint32_t w[NT][8];
+        for (int x = 0; x < 8; ++x) {
+          float y[2];
 #pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            uint32_t s[NT];
-            split<NT>(H[j / 2 + x], s, finite);
-#pragma unroll
-            for (int y = 0; y < NT; ++y) w[y][x] = s[y];
+          for (int e = 0; e < 2; ++e) {
+            const int k = k0 + j + 2 * x + e;
+            y[e] = 0.0f;
+            if (OUT && segments > 1) y[e] = from[k * 128 + r];
+            else if (OUT && a.first && mine && k < a.K) y[e] = a.first[state_at(j + 2 * x + e)];
           }
-#pragma unroll
-          for (int x = 0; x < NT; ++x) tmem_st<8>(lanes + kH + x * KW + (k0 + j) / 2, w[x]);
+          H[x] = f2(y[0], y[1]);
         }
+        write_state(j, H, finite);
       }
-      if (OUT && terms) {
-        tmem_st_done();
-        if (mine && !is_finite(finite)) sh.bad[i & 7] = 1;
+      wrote(finite, 0);
+    };
+    // H = e H + U for chunk i, and its terms for the next.
+    auto advance = [&](int i) {
+      const float e = sh.decays[i % 3][head].total;
+      F2 finite = zero;
+#pragma unroll 1
+      for (int j = 0; j < NH; j += 16) {
+        float u[16];
+        tmem_ld(lanes + u_at(i) + ucol + j, u);
+        F2 H[8];
+        read_state(j, H);
+        tmem_ld_done(u);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) H[x] = fma2(f2(e, e), H[x], f2(u[2 * x], u[2 * x + 1]));
+        write_state(j, H, finite);
+      }
+      wrote(finite, i + 1);
+    };
+    // An element of the state on its own, infinities too: where it is not finite its first term alone has it.
+    auto one_state = [&](int j, float (&y)[16]) {
+      F2 H[8];
+      read_state(j, H);
+      float first[8];
+      if constexpr (kSum) {
+        tmem_ld(lanes + kH + (k0 + j) / 2, first);
+        tmem_ld_done(first);
+      }
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        float2 z = f2_get(H[x]);
+        if constexpr (kSum) {
+          const float2 t = f2_get(pair_of(__float_as_uint(first[x])));
+          if (!(t.x - t.x == 0.0f)) z.x = t.x;
+          if (!(t.y - t.y == 0.0f)) z.y = t.y;
+        }
+        y[2 * x] = z.x, y[2 * x + 1] = z.y;
       }
     };
     int meetings = 0;
     // Chunk i step by step, from the operands themselves.
     auto by_step = [&](int i) {
       float g[NH];
+#pragma unroll 1
+      for (int j = 0; j < NH; j += 16) {
+        float y[16];
+        one_state(j, y);
 #pragma unroll
-      for (int b = 0; b < NH / 2; ++b) {
-        const float2 y = f2_get(H[b]);
-        g[2 * b] = y.x, g[2 * b + 1] = y.y;
+        for (int x = 0; x < 16; ++x) g[j + x] = y[x];
       }
       meetings = run_steps<T, HPC, NH, OUT>(args.p, at.pass, at.n, at.h0, chunk_at(i) * kChunk, L, sh.dots[i & 1], sh, meetings, g);
-#pragma unroll
-      for (int b = 0; b < NH / 2; ++b) H[b] = f2(g[2 * b], g[2 * b + 1]);
-    };
-    // Leaves the state where U is.
-    auto hand_out = [&]() {
-#pragma unroll
+      F2 finite = zero;
+#pragma unroll 1
       for (int j = 0; j < NH; j += 16) {
-        uint32_t w[16];
+        F2 H[8];
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          const float2 y = f2_get(H[j / 2 + x]);
-          w[2 * x] = __float_as_uint(y.x), w[2 * x + 1] = __float_as_uint(y.y);
-        }
-        tmem_st<16>(there + j, w);
+        for (int x = 0; x < 8; ++x) H[x] = f2(g[j + 2 * x], g[j + 2 * x + 1]);
+        write_state(j, H, finite);
       }
-      tmem_st_done();
+      wrote(finite, i + 1);
     };
     if constexpr (OUT) {
       if (!TMA && count > 0) fetch(0);
-      // i: the chunk whose U is added; -1: the state before the first
+      if (count > 0) wait_for(decayed(0));
+      begin_state();
+      if (count > 0) {
+        prepare(0);
+        arrive(ready(0).bar);
+        if (!TMA && Lay::kStages == 2 && count > 1) fetch(1);
+      }
 #pragma unroll 1
-      for (int i = -1; i < count; ++i) {
-        if (Lay::kStages == 1 && i + 1 < count && i >= 0) rk.prefetch(L - chunk_at(i + 1) * kChunk);
-        bool bad = false;
-        float e = 0.0f;
-        if (i >= 0) wait_for(got_u(i));
+      for (int i = 0; i < count; ++i) {
+        const bool more = i + 1 < count;
+        if (Lay::kStages == 1 && more) rk.prefetch(L - chunk_at(i + 1) * kChunk);
+        wait_for(got_u(i));
         // ck K of the next chunk takes the place of this one's, and K where there is room
-        if (i + 1 < count && (Lay::kStages == 2 || i < 0)) prepare(i + 1);
-        if (i >= 0) {
-          wait_for(paired(i));  // all of the chunk's flags are set
-          wait(kGotOi, i);
-          bad = sh.bad[i & 7];
-          e = sh.decays[i % 3][head].total;
-          if (bad) by_step(i);
-        }
-        const bool terms = i + 1 < count;
-        if (terms && i >= 0 && Lay::kStages == 1) wait_for(decayed(i + 1));
-        advance(lanes + u_at(i) + ucol, e, !bad && (i >= 0 || segments > 1 || a.first), terms, i + 1);
-        if (i >= 0) arrive(done(i).bar);
-        if (i + 1 < count) {
-          if (Lay::kStages == 1 && i >= 0) {  // K's place is free once P, which may be there, has been multiplied
+        if (more && Lay::kStages == 2) prepare(i + 1);
+        wait_for(paired(i));  // all of the chunk's flags are set
+        wait(kGotOi, i);
+        if (more) wait_for(decayed(i + 1));
+        if (!sh.bad[i & 7]) advance(i);
+        else by_step(i);
+        arrive(done(i).bar);
+        if (more) {
+          if (Lay::kStages == 1) {  // K's place is free once P, which may be there, has been multiplied
             if (Lay::kOver) wait_for(got_o(i));
             fetch(i + 1);
             prepare(i + 1);
@@ -1019,15 +1067,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
         }
       }
       if (order == segments - 1 && (a.last || a.with)) {
-        hand_out();
         float with = 0.0f;
 #pragma unroll 1
-        for (int j = 0; j < NH; j += 8) {
-          float y[8];
-          tmem_ld(there + j, y);
-          tmem_ld_done(y);
+        for (int j = 0; j < NH; j += 16) {
+          float y[16];
+          one_state(j, y);
 #pragma unroll
-          for (int x = 0; x < 8; ++x) {
+          for (int x = 0; x < 16; ++x) {
             if (mine && k0 + j + x < a.K) {
               if (a.last) a.last[state_at(j + x)] = y[x];
               if (a.with) with = fmaf(a.with[state_at(j + x)], y[x], with);
@@ -1039,25 +1085,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
       }
     } else {
       long long left = 0;  // logarithm of the segment's decay
+      begin_state();
 #pragma unroll 1
       for (int i = 0; i < count; ++i) {
         wait_for(got_u(i));
-        const bool bad = sh.bad[i & 7];
-        if (bad) by_step(i);
-        advance(lanes + u_at(i) + ucol, sh.decays[i % 3][head].total, !bad, false, 0);
+        if (!sh.bad[i & 7]) advance(i);
+        else by_step(i);
         // what has left nothing leaves nothing: 64 bits hold a thousandfold of that
         left = max(left + sh.decays[i % 3][head].log2, -(1LL << 45));
         arrive(done(i).bar);
       }
-      hand_out();
       float* to = p.plan.states + ((long long)at.stream * segments + order) * kept;
 #pragma unroll 1
-      for (int j = 0; j < NH; j += 8) {
-        float y[8];
-        tmem_ld(there + j, y);
-        tmem_ld_done(y);
+      for (int j = 0; j < NH; j += 16) {
+        float y[16];
+        one_state(j, y);
 #pragma unroll
-        for (int x = 0; x < 8; ++x) to[(k0 + j + x) * 128 + r] = mine && k0 + j + x < a.K ? y[x] : 0.0f;
+        for (int x = 0; x < 16; ++x) to[(k0 + j + x) * 128 + r] = mine && k0 + j + x < a.K ? y[x] : 0.0f;
       }
       if (part == 0 && lane == 0 && (HPC == 2 ? quarter % 2 == 0 : quarter == 0)) {
         // as whole part and fraction; beyond these nothing, or everything, is left
@@ -1067,7 +1111,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegisters));
     if (warp == 3 * kGroupWarps) {
       // ---------------- products
       const bool leader = elect();
