@@ -483,18 +483,21 @@ __device__ __forceinline__ void products(F mma) {
 
 // Waits for a barrier's phase of parity par.  Once a wait has failed all of
 // them return at once: the loops run out, and what they compute is undefined.
-__device__ __forceinline__ void wait_bar(Small& sh, int bar, uint32_t par) {
-  const uint32_t b = su32(&sh.bars[bar]);
-  if (!bar_try(b, par)) {
-    const unsigned long long begin = gtime();
-    for (unsigned it = 1; !sh.gave_up; ++it) {
-      if (bar_try_long(b, par)) break;
-      if ((it & 15u) == 0 && (long long)(gtime() - begin) > kWaitNs) {
-        sh.gave_up = 1;
-        atomicOr(&gave_up_status, 1);
-      }
+// The loop is not inlined: there are waits everywhere, and the code around
+// them has to stay in the instruction cache.
+static __device__ __noinline__ void wait_long(Small& sh, uint32_t b, uint32_t par) {
+  const unsigned long long begin = gtime();
+  for (unsigned it = 1; !sh.gave_up; ++it) {
+    if (bar_try_long(b, par)) break;
+    if ((it & 15u) == 0 && (long long)(gtime() - begin) > kWaitNs) {
+      sh.gave_up = 1;
+      atomicOr(&gave_up_status, 1);
     }
   }
+}
+__device__ __forceinline__ void wait_bar(Small& sh, int bar, uint32_t par) {
+  const uint32_t b = su32(&sh.bars[bar]);
+  if (!bar_try(b, par)) wait_long(sh, b, par);
   tc_fence_after();
 }
 // The warp's writes and reads so far are done: to shared memory for the
@@ -895,10 +898,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
     // ---------------- the state
     const int k0 = part * NH, ucol = HPC == 2 ? head * 64 + part * 32 : part * NH;  // state elements, U's columns
     // the state, transposed: lane v, elements k0 ..
-    const long long state = ((long long)at.n * p.H + h) * a.K * a.V;
-    auto state_at = [&](int i) {
-      return state + (a.v_major ? (long long)v * a.K + k0 + i : (long long)(k0 + i) * a.V + v);
-    };
+    const long long state = ((long long)at.n * p.H + h) * a.K * a.V + (a.v_major ? (long long)v * a.K + k0 : (long long)k0 * a.V + v);
+    const int apart = a.v_major ? 1 : a.V;            // of two of a thread's elements
+    const int elements = mine ? min(NH, a.K - k0) : 0;  // that there are
     constexpr long long kept = (long long)KB * 64 * 128;  // a state in scratch: [k][lane]
     Rows<T, HPC> rk(a.k, at.n, at.h0, p.H, a.k_of, a.K, t_first, step);
     auto fetch = [&](int i) { rk.template load<kSubs>(sm + stage_of(i) + Lay::kK, L - chunk_at(i) * kChunk, vec); };
@@ -954,23 +956,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
     };
     // The state before the first chunk.
     auto begin_state = [&]() {
-      const float* from = p.plan.states + ((long long)at.stream * segments + order) * kept;
+      const bool pieces = OUT && segments > 1;
+      const float* from = pieces ? p.plan.states + ((long long)at.stream * segments + order) * kept + k0 * 128 + r : a.first + state;
+      const int far = pieces ? 128 : apart, there = pieces ? NH : OUT && a.first ? elements : 0;
       F2 finite = zero;
 #pragma unroll 1
       for (int j = 0; j < NH; j += 16) {
         F2 H[8];
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          float y[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int k = k0 + j + 2 * x + e;
-            y[e] = 0.0f;
-            if (OUT && segments > 1) y[e] = from[k * 128 + r];
-            else if (OUT && a.first && mine && k < a.K) y[e] = a.first[state_at(j + 2 * x + e)];
-          }
-          H[x] = f2(y[0], y[1]);
-        }
+        for (int x = 0; x < 8; ++x)
+          H[x] = f2(j + 2 * x < there ? from[(j + 2 * x) * far] : 0.0f, j + 2 * x + 1 < there ? from[(j + 2 * x + 1) * far] : 0.0f);
         write_state(j, H, finite);
       }
       wrote(finite, 0);
@@ -1053,7 +1048,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
         wait_for(paired(i));  // all of the chunk's flags are set
         wait(kGotOi, i);
         if (more) wait_for(decayed(i + 1));
-        if (!sh.bad[i & 7]) advance(i);
+        if (__builtin_expect(!sh.bad[i & 7], 1)) advance(i);
         else by_step(i);
         arrive(done(i).bar);
         if (more) {
@@ -1072,12 +1067,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
         for (int j = 0; j < NH; j += 16) {
           float y[16];
           one_state(j, y);
+          if (a.last) {
 #pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            if (mine && k0 + j + x < a.K) {
-              if (a.last) a.last[state_at(j + x)] = y[x];
-              if (a.with) with = fmaf(a.with[state_at(j + x)], y[x], with);
-            }
+            for (int x = 0; x < 16; ++x)
+              if (j + x < elements) a.last[state + (j + x) * apart] = y[x];
+          }
+          if (a.with) {
+#pragma unroll
+            for (int x = 0; x < 16; ++x)
+              if (j + x < elements) with = fmaf(a.with[state + (j + x) * apart], y[x], with);
           }
         }
         with = warp_sum(with);
@@ -1089,7 +1087,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
 #pragma unroll 1
       for (int i = 0; i < count; ++i) {
         wait_for(got_u(i));
-        if (!sh.bad[i & 7]) advance(i);
+        if (__builtin_expect(!sh.bad[i & 7], 1)) advance(i);
         else by_step(i);
         // what has left nothing leaves nothing: 64 bits hold a thousandfold of that
         left = max(left + sh.decays[i % 3][head].log2, -(1LL << 45));
@@ -1101,7 +1099,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
         float y[16];
         one_state(j, y);
 #pragma unroll
-        for (int x = 0; x < 16; ++x) to[(k0 + j + x) * 128 + r] = mine && k0 + j + x < a.K ? y[x] : 0.0f;
+        for (int x = 0; x < 16; ++x) to[(k0 + j + x) * 128 + r] = j + x < elements ? y[x] : 0.0f;
       }
       if (part == 0 && lane == 0 && (HPC == 2 ? quarter % 2 == 0 : quarter == 0)) {
         // as whole part and fraction; beyond these nothing, or everything, is left
@@ -1321,15 +1319,25 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
     run = a.first[((long long)n * p.H + h) * a.K * a.V + (a.v_major ? (long long)v * a.K + k : (long long)k * a.V + v)];
   float* s = p.plan.states + id * p.plan.segments * kept + element;
   const float* f = p.plan.left + (id * p.plan.segments * 2 + (HPC == 2 ? r >> 6 : 0)) * 2;
-  for (int i = 0; i < p.plan.segments; ++i) {
-    const bool more = i + 1 < p.plan.segments;
-    const float add = more ? s[(long long)i * kept] : 0.0f;
-    s[(long long)i * kept] = run;
-    if (!more) break;
-    // 2^x run in two parts: where decays grow a state the power alone may pass float32's range
-    const int whole = (int)f[4 * i];
-    const int w1 = max(min(whole, 127), -126), w2 = max(min(whole - w1, 127), -126);
-    run = run * exp2_fast(f[4 * i + 1]) * __int_as_float((w1 + 127) << 23) * __int_as_float((w2 + 127) << 23) + add;
+  constexpr int kBatch = 8;  // read before any of it is written: on their way together
+#pragma unroll 1
+  for (int i0 = 0; i0 < p.plan.segments; i0 += kBatch) {
+    float add[kBatch], part[kBatch], whole[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int i = i0 + j;
+      if (i + 1 < p.plan.segments) add[j] = s[(long long)i * kept], whole[j] = f[4 * i], part[j] = f[4 * i + 1];
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int i = i0 + j;
+      if (i >= p.plan.segments) break;
+      s[(long long)i * kept] = run;
+      if (i + 1 >= p.plan.segments) break;
+      // 2^x run in two parts: where decays grow a state the power alone may pass float32's range
+      const int w = (int)whole[j], w1 = max(min(w, 127), -126), w2 = max(min(w - w1, 127), -126);
+      run = run * exp2_fast(part[j]) * __int_as_float((w1 + 127) << 23) * __int_as_float((w2 + 127) << 23) + add[j];
+    }
   }
 }
 
