@@ -11,30 +11,38 @@
 namespace rk {
 namespace {
 
-constexpr int kStepThreads = 256, kStepRows = 16, kStepCols = 32, kMaxHead = 128;
-constexpr int kGroups = kStepThreads / kStepCols, kStates = kMaxHead / kGroups;
+constexpr int kStepThreads = 256, kMaxHead = 128;
 
-// The recurrence as it stands, forward: a block holds 32 columns of one state,
-// a warp an eighth of their rows, a lane one column of those in registers.
-// Sixteen steps' rows are fetched together; their outputs are added up over
-// the warps at the end.
-template <typename T>
-__global__ void __launch_bounds__(kStepThreads) attn_step_kernel(AttnParams p, int blocks) {
-  __shared__ float sq[kStepRows][kMaxHead], sk[kStepRows][kMaxHead], sv[kStepRows][kStepCols], sd[kStepRows];
-  __shared__ float part[kStepRows][kGroups][kStepCols];
+// The recurrence as it stands, forward: a block holds one state, a thread VEC
+// columns of some of its rows in registers.  LANES threads hold a row, the
+// block's 256 / LANES groups take rows in turn.  Some steps' queries, keys and
+// values are fetched together; the outputs are added up over the groups at the
+// end.  A single token's time is that of its state, read and written
+// once, in pieces of 16 bytes where its rows are whole pieces.
+template <typename T, int VEC, int LANES>
+__global__ void __launch_bounds__(kStepThreads) attn_step_kernel(AttnParams p) {
+  constexpr int kGroups = kStepThreads / LANES, kRows = kMaxHead / kGroups, kWide = VEC * LANES;
+  constexpr int kStepRows = VEC == 1 ? 16 : 4;
+  constexpr int kTogether = 32 / LANES > 0 ? 32 / LANES : 1;  // groups of one warp, added up by exchanges
+  constexpr int kParts = kGroups / kTogether;
+  __shared__ float sq[kStepRows][kMaxHead], sk[kStepRows][kMaxHead], sd[kStepRows];
+  __shared__ __align__(16) float sv[kStepRows][kWide];
+  __shared__ __align__(16) float part[kStepRows][kParts][kWide];
   const AttnPass& a = p.pass[0];
-  long long id = blockIdx.x;
-  const int v0 = (int)(id % blocks) * kStepCols;
-  id /= blocks;
+  const int blocks = (a.V + kWide - 1) / kWide;
+  long long id = blockIdx.x / blocks;
+  const int v0 = (int)(blockIdx.x - id * blocks) * kWide;
   const int h = (int)(id % p.H), n = (int)(id / p.H);
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int per = (a.K + kGroups - 1) / kGroups, k0 = warp * per, mine = max(min(per, a.K - k0), 0);
-  const int v = v0 + lane;
-  const long long state = ((long long)n * p.H + h) * a.K * a.V;
-  auto at = [&](int i) { return state + (long long)(k0 + i) * a.V + v; };
-  float s[kStates];
+  const int group = threadIdx.x / LANES, v = v0 + threadIdx.x % LANES * VEC;
+  const bool mine = v < a.V;  // VEC divides V
+  const long long state = ((long long)n * p.H + h) * a.K * a.V + v;
+  float s[kRows][VEC];
 #pragma unroll
-  for (int i = 0; i < kStates; ++i) s[i] = a.first && i < mine && v < a.V ? a.first[at(i)] : 0.0f;
+  for (int i = 0; i < kRows; ++i) {
+    const int k = group + i * kGroups;
+    fill(s[i], 0.0f);
+    if (a.first && mine && k < a.K) Piece<float, VEC>::load(a.first + state + (long long)k * a.V, s[i]);
+  }
   const int L = row_length(p.lens, n, p.S);
   const float bias = p.bias ? p.bias[h] : 0.0f;
   const T* q = static_cast<const T*>(a.q.p) + n * a.q.ns + (long long)(h / a.q_of) * a.K;
@@ -50,41 +58,74 @@ __global__ void __launch_bounds__(kStepThreads) attn_step_kernel(AttnParams p, i
       const long long t = base + j;
       if (c < a.K) sq[j][c] = Elem<T>::to_f(q[t * a.q.ss + c]), sk[j][c] = Elem<T>::to_f(k[t * a.k.ss + c]);
     }
-    for (int i = threadIdx.x; i < rows * kStepCols; i += kStepThreads) {
-      const int j = i / kStepCols, c = v0 + i % kStepCols;
-      sv[j][i % kStepCols] = c < a.V ? a.su * Elem<T>::to_f(x[(base + j) * a.v.ss + c]) : 0.0f;
+    for (int i = threadIdx.x; i < rows * kWide; i += kStepThreads) {
+      const int j = i / kWide, c = v0 + i % kWide;
+      sv[j][i % kWide] = c < a.V ? a.su * Elem<T>::to_f(x[(base + j) * a.v.ss + c]) : 0.0f;
     }
     if (threadIdx.x < rows) sd[threadIdx.x] = expf((p.decay.p ? g[(base + threadIdx.x) * p.decay.ss] : 0.0f) + bias);
     __syncthreads();
 #pragma unroll 1
     for (int j = 0; j < rows; ++j) {
-      const float d = sd[j], c = sv[j][lane];
-      float y = 0.0f;
+      const float d = sd[j];
+      float c[VEC], y[VEC];
+      Piece<float, VEC>::load(&sv[j][v - v0], c);
+      fill(y, 0.0f);
 #pragma unroll
-      for (int i = 0; i < kStates; ++i) {
-        if (i < mine) {
-          s[i] = fmaf(sk[j][k0 + i], c, d * s[i]);
-          y = fmaf(sq[j][k0 + i], s[i], y);
+      for (int i = 0; i < kRows; ++i) {
+        const int r = group + i * kGroups;
+        if (r < a.K) {
+          const float kk = sk[j][r], qq = sq[j][r];
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            s[i][e] = fmaf(kk, c[e], d * s[i][e]);
+            y[e] = fmaf(qq, s[i][e], y[e]);
+          }
         }
       }
-      part[j][warp][lane] = y;
+#pragma unroll
+      for (int m = LANES; m < 32; m *= 2)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) y[e] += __shfl_xor_sync(0xffffffffu, y[e], m);
+      if (group % kTogether == 0) Piece<float, VEC>::store(&part[j][group / kTogether][v - v0], y);
     }
     __syncthreads();
-    for (int j = warp; j < rows; j += kGroups) {
-      float y = 0.0f;
+    if (a.o.p) {
+      for (int i = threadIdx.x; i < rows * kWide; i += kStepThreads) {
+        const int j = i / kWide, c = i % kWide;
+        float y = 0.0f;
 #pragma unroll
-      for (int i = 0; i < kGroups; ++i) y += part[j][i][lane];
-      if (a.o.p && v < a.V) o[(base + j) * a.o.ss + v] = Elem<T>::from_f(a.so * y);
+        for (int e = 0; e < kParts; ++e) y += part[j][e][c];
+        if (v0 + c < a.V) o[(base + j) * a.o.ss + v0 + c] = Elem<T>::from_f(a.so * y);
+      }
     }
     // no wait: the next rows are read after the first barrier, `part` is written after it
   }
-  if (a.o.p && v < a.V)
-    for (int t = L + warp; t < p.S; t += kGroups) o[t * a.o.ss + v] = Elem<T>::from_f(0.0f);
-  if (a.last) {
+  if (a.o.p)
+    for (int t = L + group; t < p.S; t += kGroups)
+      if (mine)
 #pragma unroll
-    for (int i = 0; i < kStates; ++i)
-      if (i < mine && v < a.V) a.last[at(i)] = s[i];
+        for (int e = 0; e < VEC; ++e) o[t * a.o.ss + v + e] = Elem<T>::from_f(0.0f);
+  if (a.last && mine) {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int r = group + i * kGroups;
+      if (r < a.K) Piece<float, VEC>::store(a.last + state + (long long)r * a.V, s[i]);
+    }
   }
+}
+
+template <typename T>
+cudaError_t launch_steps(const AttnParams& p, cudaStream_t s) {
+  const AttnPass& a = p.pass[0];
+  auto run = [&](auto kernel, int wide) {
+    kernel<<<(unsigned)((long long)p.N * p.H * ((a.V + wide - 1) / wide)), kStepThreads, 0, s>>>(p);
+    return cudaGetLastError();
+  };
+  const bool pieces = a.V % 4 == 0 && reinterpret_cast<uintptr_t>(a.first) % 16 == 0 && reinterpret_cast<uintptr_t>(a.last) % 16 == 0;
+  // 64 tokens of 16 heads, states of 128 x 128: 34.8 us element by element (a
+  // block for 32 columns), @ us in pieces
+  if (!pieces) return run(attn_step_kernel<T, 1, 32>, 32);
+  return a.V <= 64 ? run(attn_step_kernel<T, 4, 16>, 64) : run(attn_step_kernel<T, 4, 32>, 128);
 }
 
 // A step's decay lies between the steps before it, which wrote the state, and
@@ -204,14 +245,9 @@ __global__ void __launch_bounds__(256) attn_share_kernel(AttnShareParams p) {
 }  // namespace
 
 cudaError_t launch_attn_steps(const AttnParams& p, cudaStream_t s, int* launches) {
-  const int blocks = (p.pass[0].V + kStepCols - 1) / kStepCols;
-  const unsigned grid = (unsigned)((long long)p.N * p.H * blocks);
-  switch (p.dtype) {
-    case RK_F32: attn_step_kernel<float><<<grid, kStepThreads, 0, s>>>(p, blocks); break;
-    case RK_F16: attn_step_kernel<__half><<<grid, kStepThreads, 0, s>>>(p, blocks); break;
-    default: attn_step_kernel<__nv_bfloat16><<<grid, kStepThreads, 0, s>>>(p, blocks);
-  }
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = p.dtype == RK_F32   ? launch_steps<float>(p, s)
+                        : p.dtype == RK_F16 ? launch_steps<__half>(p, s)
+                                            : launch_steps<__nv_bfloat16>(p, s);
   if (e == cudaSuccess) ++*launches;
   return e;
 }

@@ -79,8 +79,10 @@ struct AttnParams {
   AttnPass pass[3];
   AttnPlan plan;
 };
-// The longest sequences that run step by step.
-constexpr int kAttnSteps = 16;
+// The longest sequences that run step by step.  bfloat16, 16 heads of 128, 8
+// steps and 12, against one chunk: 1 batch row 12.4 and 14.6 us against 12.6,
+// 64 batch rows 57 and 74 us against 94; float32 against 18.7 and 133 us.
+constexpr int kAttnSteps = 12;
 // The plan of `passes` passes, its pointers left out; and the floats of its scratch.
 AttnPlan attn_plan(long long seq, long long batch, long long heads, int key_size, int value_size, int passes);
 long long attn_plan_scratch(const AttnPlan& plan, long long batch, long long heads, int key_size, int value_size,

@@ -615,6 +615,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
     for (int i = 0; i < 8; ++i) sh.bad[i] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (TMA && warp == 3 * kGroupWarps + 1 && lane < 5) {
+    const CUtensorMap* maps[] = {args.k, args.v, args.q, args.o, args.with};
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(maps[lane] + at.pass)) : "memory");
+  }
   if (warp == 3 * kGroupWarps) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&sh.tmem)), "r"(512u) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -835,7 +839,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
 #pragma unroll
             for (int x = 0; x < 8; ++x, to += ss32)
               if (x < rows) *to = o[x];
-          } else if (any) {
+          } else if (!TMA && any) {
             T* to = out + t1 * a.o.ss;
 #pragma unroll
             for (int x = 0; x < 8; ++x, to += a.o.ss)
@@ -1031,7 +1035,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
     };
     if constexpr (OUT) {
       if (!TMA && count > 0) fetch(0);
-      if (count > 0) wait_for(decayed(0));
       begin_state();
       if (count > 0) {
         prepare(0);
