@@ -66,7 +66,10 @@ constexpr int kGroupWarps = kGroup / 32;
 constexpr uint32_t kSub = kChunk * 128;      // bytes of 64 rows of 64 elements
 constexpr uint32_t kTile = 2 * kSub;         // an operand's term: 64 rows of 128 elements, or of two heads of 64
 constexpr int kCols = kChunk / 2;            // of a chunk's columns of S and O, those of a thread
-constexpr long long kWaitNs = 2000000000LL;  // a wait that takes this long has failed
+// A wait that has failed: so many tries, each of which may take up to kTryNs
+// (together two seconds at most, and some tens of milliseconds at least).
+constexpr int kWaitTries = 1000000;
+constexpr uint32_t kTryNs = 2000;
 
 template <typename T>
 constexpr int kSplit = sizeof(T) == 4 ? 3 : 2;
@@ -216,7 +219,7 @@ __device__ __forceinline__ bool bar_try_long(uint32_t b, uint32_t par) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(b), "r"(par), "r"(20000u)
+      : "r"(b), "r"(par), "r"(kTryNs)
       : "memory");
   return ok != 0;
 }
@@ -483,21 +486,16 @@ __device__ __forceinline__ void products(F mma) {
 
 // Waits for a barrier's phase of parity par.  Once a wait has failed all of
 // them return at once: the loops run out, and what they compute is undefined.
-// The loop is not inlined: there are waits everywhere, and the code around
-// them has to stay in the instruction cache.
-static __device__ __noinline__ void wait_long(Small& sh, uint32_t b, uint32_t par) {
-  const unsigned long long begin = gtime();
-  for (unsigned it = 1; !sh.gave_up; ++it) {
-    if (bar_try_long(b, par)) break;
-    if ((it & 15u) == 0 && (long long)(gtime() - begin) > kWaitNs) {
-      sh.gave_up = 1;
-      atomicOr(&gave_up_status, 1);
-    }
-  }
-}
+// There are waits everywhere, and the code around them has to stay in the
+// instruction cache: a count of tries is less of it than a clock.
 __device__ __forceinline__ void wait_bar(Small& sh, int bar, uint32_t par) {
   const uint32_t b = su32(&sh.bars[bar]);
-  if (!bar_try(b, par)) wait_long(sh, b, par);
+#pragma unroll 1
+  for (int tries = kWaitTries; !bar_try_long(b, par); --tries)
+    if (tries == 0 || sh.gave_up) {
+      sh.gave_up = gave_up_status = 1;
+      break;
+    }
   tc_fence_after();
 }
 // The warp's writes and reads so far are done: to shared memory for the
@@ -1296,7 +1294,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
   // nothing is in flight any more, unless a wait has failed: then what was issued gets some time
   if (sh.gave_up && warp == 3 * kGroupWarps) {
     const unsigned long long begin = gtime();
-    while ((long long)(gtime() - begin) < kWaitNs / 4) {
+    while (gtime() - begin < 500000000ull) {
     }
   }
   if (warp == 3 * kGroupWarps)
