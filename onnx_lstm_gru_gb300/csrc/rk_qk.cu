@@ -189,10 +189,57 @@ __device__ __forceinline__ float inverse(const QkParams& p, float square) {
   return 1.0f / sqrtf((p.norm == 1 ? square / (float)p.size : square) + p.epsilon);
 }
 
-// A warp takes consecutive rows, and a row's heads in turns of kHeads, queries
-// first; a turn's elements are on their way while the one before is computed.
+// A warp's way through its rows, and through a row's heads in turns of kHeads:
+// queries first, where both sides are taken.  Rows are counted in the order of
+// row_of; `share` warps take a row's turns between them.
+struct Way {
+  long long item, last;
+  int s, n, side, part, h0;
+  bool live;
+  __device__ __forceinline__ bool more() const { return item < last; }
+  __device__ __forceinline__ void row(const QkParams& p) {
+    const long long r = p.share == 1 ? item : item / p.share;
+    part = (int)(item - r * p.share);
+    live = row_of(p, r, s, n);
+  }
+  __device__ __forceinline__ Way(const QkParams& p, int first_side, int heads, long long items, long long warps, int warp) {
+    const long long per = (items + warps - 1) / warps;
+    item = per * warp, last = item + per < items ? item + per : items;
+    side = first_side;
+    s = n = part = h0 = 0;
+    live = false;
+    if (more()) {
+      row(p);
+      h0 = part * heads;
+    }
+  }
+  // One turn on: the next heads of the row, the other side, or the next row.
+  template <bool BOTH>
+  __device__ __forceinline__ void step(const QkParams& p, int heads) {
+    h0 += heads * p.share;
+    if (h0 < p.side[side].heads) return;
+    if (BOTH && side == 0 && p.side[1].Y.p) {
+      side = 1, h0 = part * heads;
+      return;
+    }
+    if (BOTH && p.side[0].Y.p) side = 0;
+    ++item;
+    if (!more()) return;
+    // the next row in most cases by counting
+    const bool by_step = p.layout == 0 || p.positions == nullptr;
+    if (p.share == 1 && (by_step ? n + 1 < p.N : s + 1 < p.S)) {
+      by_step ? ++n : ++s;
+      live = s < row_length(p.lens, n, p.S);
+    } else {
+      row(p);
+    }
+    h0 = part * heads;
+  }
+};
+
+// Turns' elements are on their way two turns ahead.
 template <typename T, int V, int LPH, int U>
-__global__ void __launch_bounds__(kQkThreads, U > 1 ? 1 : V == 8 ? 2 : 3) qk_kernel(QkParams p) {
+__global__ void __launch_bounds__(kQkThreads, U > 1 ? 1 : V > 1 ? 2 : 3) qk_kernel(QkParams p) {
   constexpr int kHeads = 32 / LPH;
   using L = Lane<T, V, LPH, U>;
   constexpr int J = L::J;
@@ -200,68 +247,74 @@ __global__ void __launch_bounds__(kQkThreads, U > 1 ? 1 : V == 8 ? 2 : 3) qk_ker
   __shared__ Turns turns;
   turns.fill(p);
   L l(p, sub, &turns);
-  const long long items = (long long)p.S * p.N * p.share, warps = (long long)gridDim.x * kQkWarps;
-  const long long per = (items + warps - 1) / warps, first = ((long long)blockIdx.x * kQkWarps + threadIdx.x / 32) * per;
   const bool il = p.interleaved;
   typename L::Raw w[2][U][2];
 #pragma unroll
   for (int side = 0; side < 2; ++side)
 #pragma unroll
     for (int u = 0; u < U; ++u) l.read(static_cast<const T*>(p.side[side].scale), u, p.side[side].scale != nullptr, w[side][u]);
-  const long long last = min(first + per, items);
-#pragma unroll 1
-  for (long long item = first; item < last; ++item) {
-    const long long r = p.share == 1 ? item : item / p.share;
-    const int part = (int)(item - r * p.share);
-    int s, n;
-    const bool live = row_of(p, r, s, n);
-    if (live) l.angles(p, position_of(p, s, n));
+  const long long items = (long long)p.S * p.N * p.share, warps = (long long)gridDim.x * kQkWarps;
+  Way way(p, p.side[0].Y.p ? 0 : 1, kHeads, items, warps, (int)(blockIdx.x * kQkWarps + threadIdx.x / 32));
+
+  struct Turn {
+    T* Y;
+    int at;  // bits 0, 1, 2: a turn, of a live row, of a head that there is; 3: of the keys
+    int position;
+    typename L::Raw x[U][2];
+  };
+  auto fetch = [&](Turn& t) {
+    t.at = 0;
+    if (!way.more()) return;
+    const QkSide& q = p.side[way.side];
+    const int h = way.h0 + lane / LPH;
+    const T* X = static_cast<const T*>(q.X.p) + way.s * q.X.ss + way.n * q.X.ns + h * p.size;
+    t.Y = static_cast<T*>(q.Y.p) + way.s * q.Y.ss + way.n * q.Y.ns + h * p.size;
+    t.at = 1 | (way.live ? 2 : 0) | (h < q.heads ? 4 : 0) | (way.side ? 8 : 0);
+    t.position = way.live ? position_of(p, way.s, way.n) : 0;
 #pragma unroll
-    for (int side = 0; side < 2; ++side) {
-      const QkSide& q = p.side[side];
-      if (q.Y.p == nullptr) continue;
-      const T* X = static_cast<const T*>(q.X.p) + s * q.X.ss + n * q.X.ns;
-      T* Y = static_cast<T*>(q.Y.p) + s * q.Y.ss + n * q.Y.ns;
-      const int skip = kHeads * p.share;
-      int h = part * kHeads + lane / LPH;
-      typename L::Raw x[U][2];
+    for (int u = 0; u < U; ++u) l.read(X, u, (t.at & 6) == 6, t.x[u]);
+    way.step<true>(p, kHeads);
+  };
+  auto compute = [&](Turn& t) {
+    const bool live = t.at & 2, keys = t.at & 8, scaled = p.side[keys].scale;
+    if (live) l.angles(p, t.position);
+    F2 a[U][J], b[U][J], square = f2(0.0f, 0.0f);
 #pragma unroll
-      for (int u = 0; u < U; ++u) l.read(X + h * p.size, u, live && h < q.heads, x[u]);
-#pragma unroll 1
-      for (int h0 = part * kHeads; h0 < q.heads; h0 += skip, h += skip) {
-        typename L::Raw next[U][2];
+    for (int u = 0; u < U; ++u) {
+      L::widen(il, t.x[u], a[u], b[u]);
+      if constexpr (V == 1) a[u][0] = mul2(a[u][0], f2(1.0f, 0.0f)), b[u][0] = mul2(b[u][0], f2(1.0f, 0.0f));
 #pragma unroll
-        for (int u = 0; u < U; ++u) l.read(X + (h + skip) * p.size, u, live && h + skip < q.heads, next[u]);
-        F2 a[U][J], b[U][J], square = f2(0.0f, 0.0f);
+      for (int j = 0; j < J; ++j) square = fma2(a[u][j], a[u][j], fma2(b[u][j], b[u][j], square));
+    }
+    const float inv = inverse(p, p.norm ? head_sum<LPH>(sum_of(square)) : 0.0f);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          L::widen(il, x[u], a[u], b[u]);
-          if constexpr (V == 1) a[u][0] = mul2(a[u][0], f2(1.0f, 0.0f)), b[u][0] = mul2(b[u][0], f2(1.0f, 0.0f));
+    for (int u = 0; u < U; ++u) {
+      if (live) {
+        F2 wa[J], wb[J];
+        typename L::Raw ws[2] = {keys ? w[1][u][0] : w[0][u][0], keys ? w[1][u][1] : w[0][u][1]};
+        L::widen(il, ws, wa, wb);
 #pragma unroll
-          for (int j = 0; j < J; ++j) square = fma2(a[u][j], a[u][j], fma2(b[u][j], b[u][j], square));
-        }
-        const float inv = inverse(p, p.norm ? head_sum<LPH>(sum_of(square)) : 0.0f);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if (live) {
-            F2 wa[J], wb[J];
-            L::widen(il, w[side][u], wa, wb);
-#pragma unroll
-            for (int j = 0; j < J; ++j) {
-              F2 va = mul2(a[u][j], f2(inv, inv)), vb = mul2(b[u][j], f2(inv, inv));
-              if (q.scale) va = mul2(va, wa[j]), vb = mul2(vb, wb[j]);
-              F2 ta = fma2(va, l.c[u][j], negated(mul2(vb, l.s[u][j]))), tb = fma2(vb, l.c[u][j], mul2(va, l.s[u][j]));
-              // pairs that stay are left as they are, infinities too
-              const float2 x0 = f2_get(va), y0 = f2_get(vb), x1 = f2_get(ta), y1 = f2_get(tb);
-              const bool t0 = l.turns(p, u, 2 * j), t1 = l.turns(p, u, 2 * j + 1);
-              a[u][j] = f2(t0 ? x1.x : x0.x, t1 ? x1.y : x0.y), b[u][j] = f2(t0 ? y1.x : y0.x, t1 ? y1.y : y0.y);
-            }
-          }
-          l.write(Y + h * p.size, u, h < q.heads, il, a[u], b[u]);
-          x[u][0] = next[u][0], x[u][1] = next[u][1];
+        for (int j = 0; j < J; ++j) {
+          F2 va = mul2(a[u][j], f2(inv, inv)), vb = mul2(b[u][j], f2(inv, inv));
+          if (scaled) va = mul2(va, wa[j]), vb = mul2(vb, wb[j]);
+          F2 ta = fma2(va, l.c[u][j], negated(mul2(vb, l.s[u][j]))), tb = fma2(vb, l.c[u][j], mul2(va, l.s[u][j]));
+          // pairs that stay are left as they are, infinities too
+          const float2 x0 = f2_get(va), y0 = f2_get(vb), x1 = f2_get(ta), y1 = f2_get(tb);
+          const bool t0 = l.turns(p, u, 2 * j), t1 = l.turns(p, u, 2 * j + 1);
+          a[u][j] = f2(t0 ? x1.x : x0.x, t1 ? x1.y : x0.y), b[u][j] = f2(t0 ? y1.x : y0.x, t1 ? y1.y : y0.y);
         }
       }
+      l.write(t.Y, u, t.at & 4, il, a[u], b[u]);
     }
+  };
+  Turn t0, t1, t2;
+  fetch(t0);
+  fetch(t1);
+#pragma unroll 1
+  while (t0.at) {
+    fetch(t2);
+    compute(t0);
+    t0 = t1, t1 = t2;
   }
 }
 
@@ -275,8 +328,6 @@ __global__ void __launch_bounds__(kQkThreads, U == 1 ? 2 : 1) qk_grad_kernel(QkP
   turns.fill(p);
   L l(p, sub, &turns);
   const long long rows = (long long)p.S * p.N, warps = (long long)gridDim.x * kQkWarps;
-  const long long per = (rows + warps - 1) / warps, first = ((long long)blockIdx.x * kQkWarps + threadIdx.x / 32) * per;
-  const long long last = min(first + per, rows);
   const bool il = p.interleaved;
   const float m = p.norm == 1 ? 1.0f / (float)p.size : 1.0f;
 #pragma unroll 1
@@ -290,81 +341,88 @@ __global__ void __launch_bounds__(kQkThreads, U == 1 ? 2 : 1) qk_grad_kernel(QkP
 #pragma unroll
       for (int j = 0; j < J; ++j) dwa[u][j] = dwb[u][j] = f2(0.0f, 0.0f);
     }
-    if (q.dX.p || q.dscale) {
-#pragma unroll 1
-      for (long long r = first; r < last; ++r) {
-        int s, n;
-        const bool live = row_of(p, r, s, n);
-        if (live) l.angles(p, position_of(p, s, n));
-        const T* X = static_cast<const T*>(q.X.p) + s * q.X.ss + n * q.X.ns;
-        const T* dY = static_cast<const T*>(q.dY.p) + s * q.dY.ss + n * q.dY.ns;
-        T* dX = static_cast<T*>(q.dX.p) + s * q.dX.ss + n * q.dX.ns;
-        int h = lane / LPH;
-        typename L::Raw x[U][2], g[U][2];
+    struct Turn {
+      T* dX;
+      int at;  // bits 0, 1, 2: a turn, of a live row, of a head that there is
+      int position;
+      typename L::Raw x[U][2], g[U][2];
+    };
+    Way way(p, side, kHeads, q.dX.p || q.dscale ? rows : 0, warps, (int)(blockIdx.x * kQkWarps + threadIdx.x / 32));
+    auto fetch = [&](Turn& t) {
+      t.at = 0;
+      if (!way.more()) return;
+      const int h = way.h0 + lane / LPH;
+      const T* X = static_cast<const T*>(q.X.p) + way.s * q.X.ss + way.n * q.X.ns + h * p.size;
+      const T* dY = static_cast<const T*>(q.dY.p) + way.s * q.dY.ss + way.n * q.dY.ns + h * p.size;
+      t.dX = static_cast<T*>(q.dX.p) + way.s * q.dX.ss + way.n * q.dX.ns + h * p.size;
+      t.at = 1 | (way.live ? 2 : 0) | (h < q.heads ? 4 : 0);
+      t.position = way.live ? position_of(p, way.s, way.n) : 0;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        l.read(X, u, (t.at & 6) == 6, t.x[u]);
+        l.read(dY, u, (t.at & 6) == 6, t.g[u]);
+      }
+      way.step<false>(p, kHeads);
+    };
+    auto compute = [&](Turn& t) {
+      const bool live = t.at & 2, is = t.at & 4;
+      if (live) l.angles(p, t.position);
+      F2 a[U][J], b[U][J], ga[U][J], gb[U][J], square = f2(0.0f, 0.0f), dot = f2(0.0f, 0.0f);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        L::widen(il, t.x[u], a[u], b[u]);
+        L::widen(il, t.g[u], ga[u], gb[u]);
+        if constexpr (V == 1) {
+          a[u][0] = mul2(a[u][0], f2(1.0f, 0.0f)), b[u][0] = mul2(b[u][0], f2(1.0f, 0.0f));
+          ga[u][0] = mul2(ga[u][0], f2(1.0f, 0.0f)), gb[u][0] = mul2(gb[u][0], f2(1.0f, 0.0f));
+        }
+#pragma unroll
+        for (int j = 0; j < J; ++j) square = fma2(a[u][j], a[u][j], fma2(b[u][j], b[u][j], square));
+      }
+      const float inv = inverse(p, p.norm ? head_sum<LPH>(sum_of(square)) : 0.0f);
+      if (live) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          l.read(X + h * p.size, u, live && h < q.heads, x[u]);
-          l.read(dY + h * p.size, u, live && h < q.heads, g[u]);
-        }
-#pragma unroll 1
-        for (int h0 = 0; h0 < q.heads; h0 += kHeads, h += kHeads) {
-          typename L::Raw x1[U][2], g1[U][2];
+          F2 wa[J], wb[J];
+          L::widen(il, w[u], wa, wb);
 #pragma unroll
-          for (int u = 0; u < U; ++u) {
-            l.read(X + (h + kHeads) * p.size, u, live && h + kHeads < q.heads, x1[u]);
-            l.read(dY + (h + kHeads) * p.size, u, live && h + kHeads < q.heads, g1[u]);
-          }
-          F2 a[U][J], b[U][J], ga[U][J], gb[U][J], square = f2(0.0f, 0.0f), dot = f2(0.0f, 0.0f);
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            L::widen(il, x[u], a[u], b[u]);
-            L::widen(il, g[u], ga[u], gb[u]);
-            if constexpr (V == 1) {
-              a[u][0] = mul2(a[u][0], f2(1.0f, 0.0f)), b[u][0] = mul2(b[u][0], f2(1.0f, 0.0f));
-              ga[u][0] = mul2(ga[u][0], f2(1.0f, 0.0f)), gb[u][0] = mul2(gb[u][0], f2(1.0f, 0.0f));
-            }
-#pragma unroll
-            for (int j = 0; j < J; ++j) square = fma2(a[u][j], a[u][j], fma2(b[u][j], b[u][j], square));
-          }
-          const float inv = inverse(p, p.norm ? head_sum<LPH>(sum_of(square)) : 0.0f);
-          if (live) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-              F2 wa[J], wb[J];
-              L::widen(il, w[u], wa, wb);
-#pragma unroll
-              for (int j = 0; j < J; ++j) {
-                const F2 ta = fma2(ga[u][j], l.c[u][j], mul2(gb[u][j], l.s[u][j]));
-                const F2 tb = fma2(gb[u][j], l.c[u][j], negated(mul2(ga[u][j], l.s[u][j])));
-                const float2 x0 = f2_get(ga[u][j]), y0 = f2_get(gb[u][j]), x2 = f2_get(ta), y2 = f2_get(tb);
-                const bool t0 = l.turns(p, u, 2 * j), t1 = l.turns(p, u, 2 * j + 1);
-                F2 va = f2(t0 ? x2.x : x0.x, t1 ? x2.y : x0.y), vb = f2(t0 ? y2.x : y0.x, t1 ? y2.y : y0.y);
-                a[u][j] = mul2(a[u][j], f2(inv, inv)), b[u][j] = mul2(b[u][j], f2(inv, inv));  // x inv from here on
-                if (h < q.heads) dwa[u][j] = fma2(va, a[u][j], dwa[u][j]), dwb[u][j] = fma2(vb, b[u][j], dwb[u][j]);
-                if (q.scale) va = mul2(va, wa[j]), vb = mul2(vb, wb[j]);
-                ga[u][j] = va, gb[u][j] = vb;
-                dot = fma2(va, a[u][j], fma2(vb, b[u][j], dot));
-              }
-            }
-          }
-          // inv (g - (x inv) sum(g x inv) / m): x inv is of the head's own size, and inv^3 alone may pass float32's range
-          const float f = p.norm ? -head_sum<LPH>(sum_of(dot)) * m : 0.0f;
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            if (q.dX.p) {
-              if (live) {
-#pragma unroll
-                for (int j = 0; j < J; ++j) {
-                  if (p.norm) ga[u][j] = fma2(f2(f, f), a[u][j], ga[u][j]), gb[u][j] = fma2(f2(f, f), b[u][j], gb[u][j]);
-                  ga[u][j] = mul2(ga[u][j], f2(inv, inv)), gb[u][j] = mul2(gb[u][j], f2(inv, inv));
-                }
-              }
-              l.write(dX + h * p.size, u, h < q.heads, il, ga[u], gb[u]);
-            }
-            x[u][0] = x1[u][0], x[u][1] = x1[u][1], g[u][0] = g1[u][0], g[u][1] = g1[u][1];
+          for (int j = 0; j < J; ++j) {
+            const F2 ta = fma2(ga[u][j], l.c[u][j], mul2(gb[u][j], l.s[u][j]));
+            const F2 tb = fma2(gb[u][j], l.c[u][j], negated(mul2(ga[u][j], l.s[u][j])));
+            const float2 x0 = f2_get(ga[u][j]), y0 = f2_get(gb[u][j]), x2 = f2_get(ta), y2 = f2_get(tb);
+            const bool t0 = l.turns(p, u, 2 * j), t1 = l.turns(p, u, 2 * j + 1);
+            F2 va = f2(t0 ? x2.x : x0.x, t1 ? x2.y : x0.y), vb = f2(t0 ? y2.x : y0.x, t1 ? y2.y : y0.y);
+            a[u][j] = mul2(a[u][j], f2(inv, inv)), b[u][j] = mul2(b[u][j], f2(inv, inv));  // x inv from here on
+            if (is) dwa[u][j] = fma2(va, a[u][j], dwa[u][j]), dwb[u][j] = fma2(vb, b[u][j], dwb[u][j]);
+            if (q.scale) va = mul2(va, wa[j]), vb = mul2(vb, wb[j]);
+            ga[u][j] = va, gb[u][j] = vb;
+            dot = fma2(va, a[u][j], fma2(vb, b[u][j], dot));
           }
         }
       }
+      // inv (g - (x inv) sum(g x inv) / m): x inv is of the head's own size, and inv^3 alone may pass float32's range
+      const float f = p.norm ? -head_sum<LPH>(sum_of(dot)) * m : 0.0f;
+      if (q.dX.p) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (live) {
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+              if (p.norm) ga[u][j] = fma2(f2(f, f), a[u][j], ga[u][j]), gb[u][j] = fma2(f2(f, f), b[u][j], gb[u][j]);
+              ga[u][j] = mul2(ga[u][j], f2(inv, inv)), gb[u][j] = mul2(gb[u][j], f2(inv, inv));
+            }
+          }
+          l.write(t.dX, u, is, il, ga[u], gb[u]);
+        }
+      }
+    };
+    Turn t0, t1;
+    fetch(t0);
+#pragma unroll 1
+    while (t0.at) {
+      fetch(t1);
+      compute(t0);
+      t0 = t1;
     }
     if (p.partial == nullptr) continue;
     // the block's sums: over the head groups of a warp, then over the warps
@@ -419,7 +477,7 @@ cudaError_t launch_form(const QkParams& p, cudaStream_t s) {
   } else {
     const long long warps = (long long)p.S * p.N * p.share;
     const long long blocks = (warps + kQkWarps - 1) / kQkWarps;
-    qk_kernel<T, V, LPH, U><<<(unsigned)std::min<long long>(blocks, kPlanSms * (V == 8 ? 2 : 3)), kQkThreads, 0, s>>>(p);
+    qk_kernel<T, V, LPH, U><<<(unsigned)std::min<long long>(blocks, kPlanSms * (V > 1 ? 2 : 3)), kQkThreads, 0, s>>>(p);
   }
   return cudaGetLastError();
 }
