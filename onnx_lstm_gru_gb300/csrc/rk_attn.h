@@ -17,7 +17,7 @@ struct QkSide {          // the queries, or the keys
 };
 struct QkParams {
   int dtype, norm, interleaved, rotary, size;
-  int piece;             // elements of one access: 16 bytes, 8 or 1 element
+  int piece;             // elements of one access: 16 bytes' at most
   float epsilon;
   int S, N;
   int layout;
@@ -28,6 +28,7 @@ struct QkParams {
   float* partial;        // [blocks][2][size]
   int blocks;            // the gradient's
   int share;             // warps that share a row's heads
+  int lanes;             // lanes that hold a head
 };
 // Elements of one access that every row, scale and pair allows.
 int qk_piece(int eb, int size, int rotary, int interleaved);

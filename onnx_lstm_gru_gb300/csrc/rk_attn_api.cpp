@@ -94,7 +94,7 @@ rk::QkParams qk_params(Call& c, const rk_qk_problem* p, const O* o) {
 // The largest pieces that the sizes and every operand allow.
 void qk_pieces(rk::QkParams& q, int eb) {
   q.piece = rk::qk_piece(eb, q.size, q.rotary, q.interleaved);
-  for (; q.piece > 1; q.piece = q.piece > 4 ? q.piece / 2 : 1) {
+  for (; q.piece > 1; q.piece /= 2) {
     bool fits = true;
     for (const rk::QkSide& s : q.side) {
       for (const RowsArg* a : {&s.X, &s.Y, &s.dY, &s.dX}) fits = fits && Call::pieces(*a, q.piece, eb, q.size);

@@ -101,6 +101,7 @@ struct Packed {
       __builtin_memcpy(&raw, t, sizeof(raw));
     }
   }
+  __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<Raw*>(p) = raw; }
   __device__ __forceinline__ void store_streaming(T* p) const { __stcs(reinterpret_cast<Raw*>(p), raw); }
 };
 
