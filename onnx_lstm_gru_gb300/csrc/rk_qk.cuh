@@ -49,16 +49,27 @@ __device__ __forceinline__ unsigned long long turn_of(float f) {
   const double r = t - floor(t);
   return __double2ull_rz(r * 18446744073709551616.0);
 }
-// Every pair's turn, taken once by a block: float64 is slow here.
+// Every pair's turn, taken once by a block as float64 is slow here, and the
+// scales.
 struct Turns {
   unsigned long long step[128];
   bool none[128];  // the frequency is infinite or NaN
-  __device__ __forceinline__ void fill(const QkParams& p) {
+  __align__(16) float scale[2][256];  // 1 where there is none
+  // Whether there is a pair without a turn.
+  template <typename T>
+  __device__ __forceinline__ bool fill(const QkParams& p) {
+    bool any = false;
     for (int i = threadIdx.x; i < p.rotary / 2; i += kQkThreads) {
       step[i] = turn_of(p.freq[i]);
       none[i] = !(fabsf(p.freq[i]) <= 3.402823466e38f);
+      any |= none[i];
     }
-    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * p.size; i += kQkThreads) {
+      const int side = i >= p.size, e = side ? i - p.size : i;
+      const T* w = static_cast<const T*>(p.side[side].scale);
+      scale[side][e] = w ? Elem<T>::to_f(w[e]) : 1.0f;
+    }
+    return __syncthreads_or(any);
   }
 };
 
@@ -83,15 +94,17 @@ struct Lane {
   static constexpr int J = (V + 1) / 2;
   using Raw = Packed<T, V>;
   int a[U], b[U], pair[U];
+  int na[U], nb[U];  // bytes of the two pieces that there are
   const Turns* table;
-  F2 c[U][J], s[U][J];  // of the position they were last taken for
+  F2 c[U][J], s[U][J], minus[U][J];  // of the position they were last taken for; -s
   int position;
-  bool known, all;  // all pairs turn
-  __device__ __forceinline__ Lane(const QkParams& p, const Turns* turns) : table(turns), known(false), all(p.rotary == p.size) {
+  bool known, all, none;  // all pairs turn; some have none
+  __device__ __forceinline__ Lane(const QkParams& p, const Turns* turns, bool none) : table(turns), known(false), all(p.rotary == p.size), none(none) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const Unit x = unit_of<V, IL>(threadIdx.x % p.lanes + u * p.lanes, p.size, p.rotary);
-      a[u] = x.a, b[u] = x.b, pair[u] = x.pair;
+      a[u] = x.a > 0 ? x.a : 0, b[u] = x.b > 0 ? x.b : 0, pair[u] = x.pair;
+      na[u] = x.a >= 0 ? (int)sizeof(Raw) : 0, nb[u] = x.b >= 0 ? (int)sizeof(Raw) : 0;
     }
   }
   __device__ __forceinline__ bool turns(const QkParams& p, int u, int i) const { return pair[u] + i < p.rotary / 2; }
@@ -108,42 +121,53 @@ struct Lane {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int i = 2 * j + e;
-          if (i < V && a[u] >= 0 && turns(p, u, i)) {
+          if (i < V && na[u] && turns(p, u, i)) {
             turn<T>(table->step[pair[u] + i], at, cs[e], sn[e]);
-            if (table->none[pair[u] + i]) cs[e] = sn[e] = __int_as_float(0x7fffffff);
+            if (none && table->none[pair[u] + i]) cs[e] = sn[e] = __int_as_float(0x7fffffff);
           }
         }
-        c[u][j] = f2(cs[0], cs[1]), s[u][j] = f2(sn[0], sn[1]);
+        c[u][j] = f2(cs[0], cs[1]), s[u][j] = f2(sn[0], sn[1]), minus[u][j] = f2(-sn[0], -sn[1]);
       }
   }
-  // The same on their way to `x`, which is this thread's own place.
+  // A unit's two pieces of a head's row on their way.
   template <typename S>
-  __device__ __forceinline__ void start(const T* row, const T* any, int u, bool on, const S& x, int i) const {
-    x.start(i, on && a[u] >= 0 ? row + a[u] : any, on && a[u] >= 0);
-    x.start(i + 1, on && b[u] >= 0 ? row + b[u] : any, on && b[u] >= 0);
+  __device__ __forceinline__ void start(const T* row, int u, bool on, const S& to, int i) const {
+    to.start(i, row + a[u], on ? na[u] : 0);
+    to.start(i + 1, row + b[u], on ? nb[u] : 0);
   }
-  // A unit's two pieces of a head's row as read.
-  __device__ __forceinline__ void read(const T* row, int u, bool on, Raw (&x)[2]) const {
-    if (on && a[u] >= 0) x[0].load(row + a[u]);
-    else x[0].raw = {};
-    if (on && b[u] >= 0) x[1].load(row + b[u]);
-    else x[1].raw = {};
-  }
-  __device__ __forceinline__ static void widen(const Raw (&x)[2], F2 (&va)[J], F2 (&vb)[J]) {
-    float e[2 * V];
-    {
-      float lo[V], hi[V];
-      x[0].widen(lo), x[1].widen(hi);
-#pragma unroll
-      for (int i = 0; i < V; ++i) e[i] = lo[i], e[V + i] = hi[i];
-    }
+  __device__ __forceinline__ static void pairs(const float (&e)[2 * V], F2 (&va)[J], F2 (&vb)[J]) {
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       const int i = 2 * j, k = V > 1 ? i + 1 : i;
-      const float y = V > 1 ? 1.0f : 0.0f;
-      va[j] = f2(IL ? e[2 * i] : e[i], V > 1 ? (IL ? e[2 * k] : e[k]) : y);
-      vb[j] = f2(IL ? e[2 * i + 1] : e[V + i], V > 1 ? (IL ? e[2 * k + 1] : e[V + k]) : y);
+      va[j] = f2(IL ? e[2 * i] : e[i], V > 1 ? (IL ? e[2 * k] : e[k]) : 0.0f);
+      vb[j] = f2(IL ? e[2 * i + 1] : e[V + i], V > 1 ? (IL ? e[2 * k + 1] : e[V + k]) : 0.0f);
     }
+  }
+  template <typename S>
+  __device__ __forceinline__ static void take(const S& from, int i, F2 (&va)[J], F2 (&vb)[J]) {
+    float lo[V], hi[V], e[2 * V];
+    Raw x[2];
+    x[0].raw = from.piece(i), x[1].raw = from.piece(i + 1);
+    x[0].widen(lo), x[1].widen(hi);
+#pragma unroll
+    for (int i = 0; i < V; ++i) e[i] = lo[i], e[V + i] = hi[i];
+    pairs(e, va, vb);
+  }
+  __device__ __forceinline__ void scales(int side, int u, F2 (&va)[J], F2 (&vb)[J]) const {
+    float e[2 * V];
+    const float* x = table->scale[side];
+    if constexpr (V % 4 == 0) {
+#pragma unroll
+      for (int i = 0; i < V; i += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(x + a[u] + i), g = *reinterpret_cast<const float4*>(x + b[u] + i);
+        e[i] = f.x, e[i + 1] = f.y, e[i + 2] = f.z, e[i + 3] = f.w;
+        e[V + i] = g.x, e[V + i + 1] = g.y, e[V + i + 2] = g.z, e[V + i + 3] = g.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) e[i] = x[a[u] + i], e[V + i] = x[b[u] + i];
+    }
+    pairs(e, va, vb);
   }
   __device__ __forceinline__ void write(T* row, int u, bool on, const F2 (&va)[J], const F2 (&vb)[J]) const {
     float e[2][V];
@@ -162,8 +186,14 @@ struct Lane {
     }
     Raw x[2];
     x[0].narrow(e[0]), x[1].narrow(e[1]);
-    if (on && a[u] >= 0) x[0].store(row + a[u]);
-    if (on && b[u] >= 0) x[1].store(row + b[u]);
+    if (on && na[u]) x[0].store(row + a[u]);
+    if (on && nb[u]) x[1].store(row + b[u]);
+  }
+  __device__ __forceinline__ void forth(int u, int j, F2 x, F2 y, F2& tx, F2& ty) const {
+    tx = fma2(x, c[u][j], mul2(y, minus[u][j])), ty = fma2(y, c[u][j], mul2(x, s[u][j]));
+  }
+  __device__ __forceinline__ void back(int u, int j, F2 x, F2 y, F2& tx, F2& ty) const {
+    tx = fma2(x, c[u][j], mul2(y, s[u][j])), ty = fma2(y, c[u][j], mul2(mul2(x, s[u][j]), f2(-1.0f, -1.0f)));  // registers are short there
   }
   // Pairs that stay are left as they are, infinities too.
   __device__ __forceinline__ void pick(const QkParams& p, int u, int j, F2 ta, F2 tb, F2& va, F2& vb) const {
@@ -172,7 +202,6 @@ struct Lane {
     va = f2(t0 ? x1.x : x0.x, t1 ? x1.y : x0.y), vb = f2(t0 ? y1.x : y0.x, t1 ? y1.y : y0.y);
   }
 };
-__device__ __forceinline__ F2 negated(F2 x) { return mul2(x, f2(-1.0f, -1.0f)); }
 __device__ __forceinline__ float sum_of(F2 x) {
   const float2 v = f2_get(x);
   return v.x + v.y;
@@ -286,15 +315,15 @@ struct Slot {
     return reinterpret_cast<Raw*>(smem + kSlots * kQkThreads * sizeof(Turn))[(slot * N + i) * kQkThreads + threadIdx.x];
   }
   // A piece, or zeros; copies are of 4 bytes at least.
-  __device__ __forceinline__ void start(int i, const void* from, bool on) const {
+  __device__ __forceinline__ void start(int i, const void* from, int bytes) const {
     constexpr int kSize = sizeof(Raw);
     const uint32_t to = (uint32_t)__cvta_generic_to_shared(&piece(i));
     if constexpr (kSize == 16)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(on ? 16 : 0) : "memory");
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
     else if constexpr (kSize >= 4)
-      asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(from), "n"(kSize), "r"(on ? kSize : 0)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(from), "n"(kSize), "r"(bytes)
                    : "memory");
-    else piece(i) = on ? *static_cast<const Raw*>(from) : Raw{};
+    else piece(i) = bytes ? *static_cast<const Raw*>(from) : Raw{};
   }
   __device__ __forceinline__ static void sent() { asm volatile("cp.async.commit_group;" ::: "memory"); }
   // The oldest of kSlots that were sent is there.
@@ -308,13 +337,8 @@ __global__ void __launch_bounds__(kQkThreads, U > 2 ? 1 : 2) qk_kernel(QkParams 
   const int lane = threadIdx.x % 32, heads = 32 / p.lanes, mine = lane / p.lanes, own = mine * p.size;
   const float mean = p.norm == 1 ? 1.0f / (float)p.size : 1.0f;
   __shared__ Turns turns;
-  turns.fill(p);
-  L l(p, &turns);
-  typename L::Raw w[2][U][2];
-#pragma unroll
-  for (int side = 0; side < 2; ++side)
-#pragma unroll
-    for (int u = 0; u < U; ++u) l.read(static_cast<const T*>(p.side[side].scale), u, p.side[side].scale != nullptr, w[side][u]);
+  const bool none = turns.fill<T>(p);
+  L l(p, &turns, none);
   const long long items = (long long)p.S * p.N * p.share, warps = (long long)gridDim.x * kQkWarps;
   Way<T, false> way(p, p.side[0].Y.p ? 0 : 1, heads, items, warps, (int)(blockIdx.x * kQkWarps + threadIdx.x / 32));
 
@@ -324,12 +348,13 @@ __global__ void __launch_bounds__(kQkThreads, U > 2 ? 1 : 2) qk_kernel(QkParams 
   auto fetch = [&] {
     Turn t = {nullptr, 0, 0};
     if (way.more()) {
-      const int at = way.h0 * p.size + own;
+      const bool is = way.h0 + mine < p.side[way.side].heads;
+      const int at = is ? way.h0 * p.size + own : 0;
       t.out = way.out + at;
-      t.at = 1 | (way.live ? 2 : 0) | (way.h0 + mine < p.side[way.side].heads ? 4 : 0) | (way.side ? 8 : 0);
+      t.at = 1 | (way.live ? 2 : 0) | (is ? 4 : 0) | (way.side ? 8 : 0);
       t.position = way.live ? position_of(p, way.s, way.n) : 0;
 #pragma unroll
-      for (int u = 0; u < U; ++u) l.start(way.X + at, way.X, u, (t.at & 6) == 6, into, 2 * u);
+      for (int u = 0; u < U; ++u) l.start(way.X + at, u, is && way.live, into, 2 * u);
       way.step(p, heads);
     }
     S::sent();
@@ -337,15 +362,12 @@ __global__ void __launch_bounds__(kQkThreads, U > 2 ? 1 : 2) qk_kernel(QkParams 
     into.next();
   };
   auto compute = [&](const Turn& t) {
-    const bool live = t.at & 2, keys = t.at & 8, scaled = p.side[keys].scale;
+    const bool live = t.at & 2;
     if (live) l.angles(p, t.position);
     F2 a[U][J], b[U][J], square = f2(0.0f, 0.0f);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      typename L::Raw x[2];
-      x[0].raw = from.piece(2 * u), x[1].raw = from.piece(2 * u + 1);
-      L::widen(x, a[u], b[u]);
-      if constexpr (V == 1) a[u][0] = mul2(a[u][0], f2(1.0f, 0.0f)), b[u][0] = mul2(b[u][0], f2(1.0f, 0.0f));
+      L::take(from, 2 * u, a[u], b[u]);
 #pragma unroll
       for (int j = 0; j < J; ++j) square = fma2(a[u][j], a[u][j], fma2(b[u][j], b[u][j], square));
     }
@@ -354,16 +376,20 @@ __global__ void __launch_bounds__(kQkThreads, U > 2 ? 1 : 2) qk_kernel(QkParams 
     for (int u = 0; u < U; ++u) {
       if (live) {
         F2 wa[J], wb[J];
-        typename L::Raw ws[2] = {keys ? w[1][u][0] : w[0][u][0], keys ? w[1][u][1] : w[0][u][1]};
-        L::widen(ws, wa, wb);
+        l.scales(t.at >> 3, u, wa, wb);
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-          F2 va = mul2(a[u][j], f2(inv, inv)), vb = mul2(b[u][j], f2(inv, inv));
-          if (scaled) va = mul2(va, wa[j]), vb = mul2(vb, wb[j]);
-          F2 ta = fma2(va, l.c[u][j], negated(mul2(vb, l.s[u][j]))), tb = fma2(vb, l.c[u][j], mul2(va, l.s[u][j]));
-          if (l.all) va = ta, vb = tb;
-          else l.pick(p, u, j, ta, tb, va, vb);
-          a[u][j] = va, b[u][j] = vb;
+        for (int j = 0; j < J; ++j)
+          a[u][j] = mul2(mul2(a[u][j], f2(inv, inv)), wa[j]), b[u][j] = mul2(mul2(b[u][j], f2(inv, inv)), wb[j]);
+        if (l.all) {
+#pragma unroll
+          for (int j = 0; j < J; ++j) l.forth(u, j, a[u][j], b[u][j], a[u][j], b[u][j]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < J; ++j) {
+            F2 ta, tb;
+            l.forth(u, j, a[u][j], b[u][j], ta, tb);
+            l.pick(p, u, j, ta, tb, a[u][j], b[u][j]);
+          }
         }
       }
       l.write(static_cast<T*>(t.out), u, t.at & 4, a[u], b[u]);
@@ -389,8 +415,8 @@ __global__ void __launch_bounds__(kQkThreads, U > 2 ? 1 : 2) qk_grad_kernel(QkPa
   const int lane = threadIdx.x % 32, heads = 32 / p.lanes, mine = lane / p.lanes, own = mine * p.size;
   const float mean = p.norm == 1 ? 1.0f / (float)p.size : 1.0f;
   __shared__ Turns turns;
-  turns.fill(p);
-  L l(p, &turns);
+  const bool none = turns.fill<T>(p);
+  L l(p, &turns, none);
   const long long rows = (long long)p.S * p.N, warps = (long long)gridDim.x * kQkWarps;
   extern __shared__ __align__(16) char smem[];
   using S = Slot<typename L::Raw::Raw, 4 * U>;
@@ -398,11 +424,9 @@ __global__ void __launch_bounds__(kQkThreads, U > 2 ? 1 : 2) qk_grad_kernel(QkPa
   for (int side = 0; side < 2; ++side) {
     const QkSide& q = p.side[side];
     S into(smem), from(smem);
-    typename L::Raw w[U][2];
     F2 dwa[U][J], dwb[U][J];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      l.read(static_cast<const T*>(q.scale), u, q.scale != nullptr, w[u]);
 #pragma unroll
       for (int j = 0; j < J; ++j) dwa[u][j] = dwb[u][j] = f2(0.0f, 0.0f);
     }
@@ -410,14 +434,15 @@ __global__ void __launch_bounds__(kQkThreads, U > 2 ? 1 : 2) qk_grad_kernel(QkPa
     auto fetch = [&] {
       Turn t = {nullptr, 0, 0};
       if (way.more()) {
-        const int at = way.h0 * p.size + own;
+        const bool is = way.h0 + mine < q.heads;
+        const int at = is ? way.h0 * p.size + own : 0;
         t.out = way.out + at;
-        t.at = 1 | (way.live ? 2 : 0) | (way.h0 + mine < q.heads ? 4 : 0);
+        t.at = 1 | (way.live ? 2 : 0) | (is ? 4 : 0);
         t.position = way.live ? position_of(p, way.s, way.n) : 0;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          l.start(way.X + at, way.X, u, (t.at & 6) == 6, into, 4 * u);
-          l.start(way.dY + at, way.dY, u, (t.at & 6) == 6, into, 4 * u + 2);
+          l.start(way.X + at, u, is && way.live, into, 4 * u);
+          l.start(way.dY + at, u, is && way.live, into, 4 * u + 2);
         }
         way.step(p, heads);
       }
@@ -431,15 +456,8 @@ __global__ void __launch_bounds__(kQkThreads, U > 2 ? 1 : 2) qk_grad_kernel(QkPa
       F2 a[U][J], b[U][J], ga[U][J], gb[U][J], square = f2(0.0f, 0.0f), dot = f2(0.0f, 0.0f);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        typename L::Raw x[2], g[2];
-        x[0].raw = from.piece(4 * u), x[1].raw = from.piece(4 * u + 1);
-        g[0].raw = from.piece(4 * u + 2), g[1].raw = from.piece(4 * u + 3);
-        L::widen(x, a[u], b[u]);
-        L::widen(g, ga[u], gb[u]);
-        if constexpr (V == 1) {
-          a[u][0] = mul2(a[u][0], f2(1.0f, 0.0f)), b[u][0] = mul2(b[u][0], f2(1.0f, 0.0f));
-          ga[u][0] = mul2(ga[u][0], f2(1.0f, 0.0f)), gb[u][0] = mul2(gb[u][0], f2(1.0f, 0.0f));
-        }
+        L::take(from, 4 * u, a[u], b[u]);
+        L::take(from, 4 * u + 2, ga[u], gb[u]);
 #pragma unroll
         for (int j = 0; j < J; ++j) square = fma2(a[u][j], a[u][j], fma2(b[u][j], b[u][j], square));
       }
@@ -448,19 +466,25 @@ __global__ void __launch_bounds__(kQkThreads, U > 2 ? 1 : 2) qk_grad_kernel(QkPa
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           F2 wa[J], wb[J];
-          L::widen(w[u], wa, wb);
+          l.scales(side, u, wa, wb);
+          if (l.all) {
+#pragma unroll
+            for (int j = 0; j < J; ++j) l.back(u, j, ga[u][j], gb[u][j], ga[u][j], gb[u][j]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+              F2 ta, tb;
+              l.back(u, j, ga[u][j], gb[u][j], ta, tb);
+              l.pick(p, u, j, ta, tb, ga[u][j], gb[u][j]);
+            }
+          }
 #pragma unroll
           for (int j = 0; j < J; ++j) {
-            const F2 ta = fma2(ga[u][j], l.c[u][j], mul2(gb[u][j], l.s[u][j]));
-            const F2 tb = fma2(gb[u][j], l.c[u][j], negated(mul2(ga[u][j], l.s[u][j])));
-            F2 va = ga[u][j], vb = gb[u][j];
-            if (l.all) va = ta, vb = tb;
-            else l.pick(p, u, j, ta, tb, va, vb);
+            const F2 va = ga[u][j], vb = gb[u][j];
             a[u][j] = mul2(a[u][j], f2(inv, inv)), b[u][j] = mul2(b[u][j], f2(inv, inv));  // x inv from here on
             if (is) dwa[u][j] = fma2(va, a[u][j], dwa[u][j]), dwb[u][j] = fma2(vb, b[u][j], dwb[u][j]);
-            if (q.scale) va = mul2(va, wa[j]), vb = mul2(vb, wb[j]);
-            ga[u][j] = va, gb[u][j] = vb;
-            dot = fma2(va, a[u][j], fma2(vb, b[u][j], dot));
+            ga[u][j] = mul2(va, wa[j]), gb[u][j] = mul2(vb, wb[j]);
+            dot = fma2(ga[u][j], a[u][j], fma2(gb[u][j], b[u][j], dot));
           }
         }
       }
@@ -505,8 +529,9 @@ __global__ void __launch_bounds__(kQkThreads, U > 2 ? 1 : 2) qk_grad_kernel(QkPa
 #pragma unroll
           for (int o = 16; o >= p.lanes; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
           const int e = IL ? 2 * i + j : i;  // place in the two pieces, or in its own
-          const int from = IL ? (e < V ? l.a[u] : l.b[u]) : (j ? l.b[u] : l.a[u]);
-          if (lane < p.lanes && from >= 0) sums[threadIdx.x / 32][from + (IL && e >= V ? e - V : e)] = v;
+          const bool second = IL ? e >= V : j;
+          const int from = second ? l.b[u] : l.a[u];
+          if (lane < p.lanes && (second ? l.nb[u] : l.na[u])) sums[threadIdx.x / 32][from + (IL && e >= V ? e - V : e)] = v;
         }
     __syncthreads();
     for (int i = threadIdx.x; i < p.size; i += kQkThreads) {
