@@ -249,7 +249,8 @@ rk_status rk_encode_host(rk_handle* h, const rk_problem* p, const rk_operands* h
 /* Synchronise `stream`, read and clear the device status word of the handle
  * (and, once rk_encode_noalloc has run on the handle, the status word of its
  * fixed array): RK_OK, or RK_ERR_TIMEOUT if a bounded device wait of a step
- * kernel or of the tensor-core projection gave up during a previous encode;
+ * kernel, of the tensor-core projection or of the linear attention in chunks
+ * gave up during a previous encode;
  * the outputs of that encode are then undefined.  The web page "Recurrent
  * layers" has no counterpart: its design waits on nothing inside a launch
  * (one pass per step, paragraph "Why a pass per step"), while this library's
@@ -518,7 +519,8 @@ rk_status rk_scan_grad_encode(rk_handle* h, const rk_scan_problem* p, const rk_s
  * of the problem's dtype; Frequencies float32 [rotary / 2] (radians per
  * position, required with rotary > 0); positions int32 [seq, batch] (layout 0)
  * or [batch, seq], else the step's number.  Angles are taken modulo a turn in
- * 64 bits: those of far positions are as exact as those of near ones. */
+ * 64 bits: those of far positions are as exact as those of near ones.  YQ and
+ * YK may take the place of Q and K: the same rows at the same pitches. */
 typedef struct rk_qk_problem {
   int32_t dtype, layout;
   int32_t norm;        /* 0: none, 1: root mean square, 2: length */

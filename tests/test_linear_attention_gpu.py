@@ -264,6 +264,68 @@ def test_qk_large_values_do_not_overflow(layer):
         check(batch_first(got["d" + side], 0).float(), dX)
 
 
+#       heads of pieces of two elements and of one, of several units a lane; many turns a warp
+QK_MORE = [
+    (3, 2, 3, 2, 256, 252, False, "rms"), (3, 2, 3, 2, 254, 254, True, "rms"), (2, 2, 2, 2, 130, 64, True, "l2"),
+    (2, 2, 3, 1, 100, 50, False, "l2"), (3, 3, 5, 2, 255, 100, False, "rms"), (30, 64, 40, 8, 16, 16, True, "rms"),
+    (40, 64, 3, 9, 62, 62, False, "rms"), (300, 20, 2, 1, 33, 30, True, "l2"),
+]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", QK_MORE)
+def test_qk_pieces_and_turns(layer, shape, dtype):
+    S, N, H, KH, d = shape[:5]
+    for layout, wide, positions in ((0, False, None), (1, False, near), (1, True, None)):
+        i, p, t, lens = qk_case(shape, dtype, layout, wide, sum(shape[:6]), positions)
+        got = layer.qk(p, **t)
+        for side in "QK":
+            check(batch_first(got["Y" + side], layout).to(got["YQ"].dtype), qk_reference(p, t, lens, side), f"Y{side}")
+        t.update(dYQ=i.rows(S, N, H * d), dYK=i.rows(S, N, KH * d))
+        got = layer.qk_grad(p, **t)
+        for side in "QK":
+            dY = batch_first(t["dY" + side], layout)
+            dX, dScale = qk_reference(p, t, lens, side, dY)
+            check(batch_first(got["d" + side], layout).to(got["dQ"].dtype), dX, f"d{side}",
+                  absolute=cancelled(p, t, lens, side, dY))
+            check(got[f"d{side}Scale"], dScale, f"d{side}Scale")
+        same_bits(got, layer.qk_grad(p, **t))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", [(40, 64, 6, 3, 64, 32, False, "rms"), (9, 3, 6, 3, 90, 34, True, "l2")])
+def test_qk_in_place(layer, shape, dtype):
+    """Results may take the operands' place."""
+    i, p, t, lens = qk_case(shape, dtype, 0, False, 3)
+    want = {k: v.clone() for k, v in layer.qk(p, **t).items()}
+    q, k = t["Q"].clone(), t["K"].clone()
+    got = layer.qk(p, **dict(t, Q=q, K=k), YQ=q, YK=k)
+    assert got["YQ"] is q and got["YK"] is k
+    same_bits(got, want)
+
+
+def test_qk_on_streams_and_in_graphs(layer):
+    i, p, t, lens = qk_case((50, 8, 4, 2, 64, 64, False, "rms"), "bf16", 1, False, 5, near)
+    g = dict(t, dYQ=i.rows(50, 8, 256), dYK=i.rows(50, 8, 128))
+    want, gwant = layer.qk(p, **t), layer.qk_grad(p, **g)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    a, b = layer.qk(p, stream=side, **t), layer.qk_grad(p, stream=side, **g)
+    torch.cuda.current_stream().wait_stream(side)
+    same_bits(a, want)
+    same_bits(b, gwant)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a, b = layer.qk(p, **t), layer.qk_grad(p, **g)
+    for _ in range(2):
+        for x in ("Q", "K", "positions"):
+            t[x].copy_(i.rng.integers(0, 99) if x == "positions" else torch.randn_like(t[x].float()))
+        graph.replay()
+        torch.cuda.synchronize()
+        same_bits(a, layer.qk(p, **t))
+        same_bits(b, layer.qk_grad(p, **g))
+
+
 # ---- attention ---------------------------------------------------------------------------------------
 
 class Case:
@@ -484,6 +546,167 @@ def test_attn_operands_past_the_ends_are_not_used(layer, dtype):
         c.compare(layer.attn_grad(c.p, want=c.grads(), **c.t))
         c.t.pop("dY"), c.t.pop("d_final_state")
         c.compare(layer.attn(c.p, **c.t))
+
+
+def cut(c):
+    """Whether the case's sequences are cut into pieces that run side by side."""
+    return rk.rk_attn_scratch_length(c.p.to_c()) > 0
+
+
+def both_ways(layer, c, name=""):
+    """Gradient and outputs against the definition."""
+    c.compare(layer.attn_grad(c.p, want=c.grads(), **c.t), name)
+    for n in ("dY", "d_final_state"):
+        c.t.pop(n, None)
+    c.compare(layer.attn(c.p, **c.t), name)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("sizes", [(64, 48), (128, 128), (72, 30)])
+def test_attn_documents_and_strong_decays_in_pieces(layer, sizes, dtype):
+    """Forgetting and decays beyond a chunk's product, at and off the pieces'
+    and chunks' ends, in sequences that are cut."""
+    c = Case(700, 1, 2, *sizes, dtype, ragged=False, layout=1, grad=True)
+    assert cut(c)
+    g = c.t["Decay"]
+    for at in (0, 63, 64, 65, 128, 300, 383, 448, 699):
+        g[:, at, 0] = -float("inf")
+    g[:, 200:260, 1] = -300.0
+    g[:, 500:520:2, 1] = -90.0
+    both_ways(layer, c)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("name", ["Q", "K", "V", "Decay", "initial_state"])
+def test_attn_numbers_that_are_none_in_pieces(layer, dtype, name):
+    for at in (70, 640):
+        c = Case(700, 1, 3, 64, 64, dtype, ragged=False, layout=0)
+        assert cut(c)
+        clean = layer.attn(c.p, **c.t)
+        x = c.t[name]
+        if name == "initial_state":
+            x[0, 1, 3, 5] = float("inf")
+        else:
+            x[at, 0, 0] = float("nan")
+        got = layer.attn(c.p, **c.t)
+        c.compare(got)
+        # the head that goes with it may be rounded another way, as what the two share is taken step by step
+        assert torch.equal(got["Y"][:, 0, 128:], clean["Y"][:, 0, 128:])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_attn_products_beyond_float32_in_pieces(layer, dtype):
+    c = Case(700, 1, 1, 32, 32, dtype, ragged=False, state=False, layout=1)
+    assert cut(c)
+    c.t["Q"].mul_(1e20), c.t["K"].mul_(1e20), c.t["V"].mul_(1e-22)
+    got = layer.attn(c.p, **c.t)
+    assert torch.isfinite(got["Y"]).all()
+    c.compare(got)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_attn_growth_in_pieces(layer, dtype):
+    """Decays of either sign: their sums stay within a few units."""
+    c = Case(700, 1, 2, 32, 32, dtype, ragged=False, layout=1, grad=True)
+    assert cut(c)
+    c.t["Decay"].copy_(c.i.normal(1, 700, 2, scale=0.3, mean=-0.05, dtype=torch.float32))
+    both_ways(layer, c)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_attn_ragged_rows_in_pieces(layer, dtype):
+    """Rows that end in the first piece, at a piece's end and past all."""
+    c = Case(900, 5, 1, 48, 64, dtype, lens=[0, 1, 64, 899, 2000], layout=0, grad=True, decay="both")
+    assert cut(c)
+    both_ways(layer, c)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("heads", [(3, 3, 3), (5, 1, 5), (3, 3, 1)])
+def test_attn_heads_that_do_not_pair(layer, heads, dtype):
+    """Heads of at most 64 elements go in pairs; of an odd number one goes alone."""
+    H, q, k = heads
+    for S, wide in ((70, False), (300, True)):
+        both_ways(layer, Case(S, 2, H, 64, 32, dtype, q=q, k=k, v=k, decay="both", layout=1, wide=wide, grad=True))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("S", [11, 12, 13, 14])
+def test_attn_between_steps_and_chunks(layer, S, dtype):
+    both_ways(layer, Case(S, 3, 2, 128, 96, dtype, decay="both", layout=S % 2, grad=True))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("at,extra", [(8, 8), (0, 16), (1, 8), (4, 4)])
+def test_attn_slices_of_wider_rows(layer, at, extra, dtype):
+    """Queries, keys and values as one projection's row holds them, on 16-byte
+    boundaries and off them."""
+    S, N, H, dk, dv = 200, 2, 2, 64, 128
+    c = Case(S, N, H, dk, dv, dtype, layout=0, ragged=False, grad=True)
+    width = 2 * H * dk + H * dv + at + extra
+    row = torch.full((S, N, width), float("nan"), dtype=c.t["Q"].dtype, device="cuda")
+    for n, w in (("Q", H * dk), ("K", H * dk), ("V", H * dv)):
+        row[..., at:at + w] = c.t[n]
+        c.t[n] = row[..., at:at + w]
+        at += w
+    both_ways(layer, c)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_attn_rows_far_apart(layer, dtype):
+    """Offsets beyond 32 bits."""
+    S, N, H, d = 20, 1, 2, 64
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB")
+    c = Case(S, N, H, d, d, dtype, layout=0, ragged=False, grad=True)
+    far = torch.empty(S, 1, 2 ** 27 + 512, dtype=c.t["Q"].dtype, device="cuda")
+    assert far.numel() > 2 ** 31
+    at = 0
+    for n in ("Q", "K", "V", "dY"):
+        far[..., at:at + H * d] = c.t[n]
+        c.t[n] = far[..., at:at + H * d]
+        at += H * d
+    both_ways(layer, c)
+    p = rk.QkProblem(seq=S, batch=N, heads=H, size=d, norm="l2", dtype=dtype)
+    near_, far_ = ({k: f(c.t[k]) for k in ("Q", "K")} for f in (torch.Tensor.contiguous, lambda x: x))
+    same_bits(layer.qk(p, **far_), layer.qk(p, **near_))
+
+
+def test_attn_no_decay_keeps_all(layer):
+    """Without decays the state is the sum over all steps: 700 of 128 elements
+    here, sqrt(89600) * 2^-21 by the reckoning at the top."""
+    c = Case(700, 1, 2, 128, 64, "f32", decay="none", ragged=False)
+    assert cut(c)
+    got, want = layer.attn(c.p, **c.t), c.reference()
+    for k in got:
+        check(batch_first(got[k], 0).float() if k == "Y" else got[k], want[k], k, arithmetic=1.5e-4)
+
+
+def test_attn_state_in_place_in_pieces(layer):
+    c = Case(900, 1, 2, 64, 64, "bf16", ragged=False, decay="both")
+    assert cut(c)
+    want = layer.attn(c.p, **c.t)
+    state = c.t["initial_state"].clone()
+    got = layer.attn(c.p, **dict(c.t, initial_state=state), final_state=state)
+    assert got["final_state"] is state
+    same_bits(got, want)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(513, 40, 4, 64, 64), (513, 20, 4, 128, 128), (700, 1, 4, 128, 64)])
+def test_attn_many_calls_in_a_row(layer, shape, dtype):
+    """The same bits every time, and no wait that gave up."""
+    c = Case(*shape, dtype, decay="both", grad=True)
+    f = {k: v for k, v in c.t.items() if k not in ("dY", "d_final_state")}
+    want, gwant = layer.attn(c.p, **f), layer.attn_grad(c.p, want=c.grads(), **c.t)
+    for _ in range(12):
+        outs = [(layer.attn(c.p, **f), layer.attn_grad(c.p, want=c.grads(), **c.t)) for _ in range(3)]
+        for a, b in outs:
+            for k, v in want.items():
+                assert torch.equal(a[k], v), k
+            for k, v in gwant.items():
+                assert torch.equal(b[k], v), k
+    assert rk.rk_status_poll(layer.handle, torch.cuda.current_stream().cuda_stream) == rk.RK_OK
 
 
 def test_attn_no_steps(layer):

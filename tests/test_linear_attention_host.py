@@ -164,6 +164,17 @@ def test_scratch_lengths():
     token = rk.AttnProblem(seq=1, batch=64, heads=16, key_size=128, value_size=128)
     assert rk.rk_attn_scratch_length(token.to_c()) == 0
     assert rk.rk_attn_scratch_length(rk.AttnProblem(seq=0, batch=4, heads=2, key_size=8, value_size=8).to_c()) == 0
+    # one long sequence is cut into pieces, whose states are kept; many sequences fill the GPU as they are
+    one = rk.AttnProblem(seq=4096, batch=1, heads=16, key_size=128, value_size=128)
+    many = rk.AttnProblem(seq=512, batch=64, heads=16, key_size=64, value_size=64)
+    assert rk.rk_attn_scratch_length(one.to_c()) > 0
+    assert rk.rk_attn_scratch_length(many.to_c()) == 0
+    assert rk.rk_attn_grad_scratch_length(one.to_c()) >= 2 * 16 * 4096
+    # heads that share are added up in float32
+    shared = rk.AttnProblem(seq=100, batch=2, heads=4, key_size=8, value_size=8, key_heads=1)
+    alone = rk.AttnProblem(seq=100, batch=2, heads=4, key_size=8, value_size=8)
+    more = rk.rk_attn_grad_scratch_length(shared.to_c()) - rk.rk_attn_grad_scratch_length(alone.to_c())
+    assert more == 100 * 2 * 4 * 8
 
 
 def test_defaults_of_the_problems():
