@@ -274,20 +274,19 @@ struct Place {
 // 2^(whole + fraction) without rounding the sum.
 __device__ __forceinline__ float pow2_of(long long g) {
   const int whole = (int)(g >> 32);
-  const float part = exp2_fast((float)((uint32_t)g >> 8) * 5.9604644775390625e-8f);
+  const float part = exp2_fast((float)(uint32_t)g * 2.3283064365386963e-10f);
   if (whole < -126) return 0.0f;
   return whole > 127 ? __int_as_float(0x7f800000) : part * __int_as_float((whole + 127) << 23);
 }
 
-// The logarithm x of a decay to base 2 in units of 2^-32: the product's whole
-// part, fraction and what it rounded away each exactly.  What is below -1e5
-// leaves nothing in float32, and a chunk's sum of it stays within 2^25.
+// The logarithm x of a decay to base 2 in units of 2^-32, to the nearest: a
+// memory of thousands of steps adds up as many of the same rounding.  What is
+// below -1e5 leaves nothing in float32, and a chunk's sum of it stays within 2^25.
 __device__ __forceinline__ long long fixed_log2(float x) {
   x = fminf(fmaxf(x, -1.0e5f), 80.0f);
   constexpr float kLow = (float)(1.4426950408889634074 - (double)kLog2e);
-  const float t = x * kLog2e, rest = fmaf(x, kLog2e, -t) + x * kLow, whole = floorf(t);
-  return ((long long)(int)whole << 32) + (long long)(unsigned long long)__float2uint_rz((t - whole) * 4294967296.0f) +
-         (long long)__float2int_rn(rest * 4294967296.0f);
+  const float t = x * kLog2e, rest = fmaf(x, kLog2e, -t) + x * kLow;
+  return __float2ll_rn(t * 4294967296.0f) + (long long)__float2int_rn(rest * 4294967296.0f);
 }
 
 // One warp: the decays of a chunk of which the lane has x0 and x1, the
