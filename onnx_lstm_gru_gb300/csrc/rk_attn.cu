@@ -18,9 +18,12 @@ constexpr int kStepThreads = 256, kMaxHead = 128;
 // block's 256 / LANES groups take rows in turn.  Some steps' queries, keys and
 // values are fetched together; the outputs are added up over the groups at the
 // end.  A single token's time is that of its state, read and written
-// once, in pieces of 16 bytes where its rows are whole pieces.
+// once, in pieces of 16 bytes where its rows are whole pieces, past the caches:
+// 64 tokens of 16 heads, states of 128 x 128, 28.6 us or 4.7 TB/s (31.7 through
+// the caches; 31.3 with three blocks on a multiprocessor instead of two, 33.0
+// with half the columns in a block).
 template <typename T, int VEC, int LANES>
-__global__ void __launch_bounds__(kStepThreads) attn_step_kernel(AttnParams p) {
+__global__ void __launch_bounds__(kStepThreads, 2) attn_step_kernel(AttnParams p) {
   constexpr int kGroups = kStepThreads / LANES, kRows = kMaxHead / kGroups, kWide = VEC * LANES;
   constexpr int kStepRows = VEC == 1 ? 16 : 4;
   constexpr int kTogether = 32 / LANES > 0 ? 32 / LANES : 1;  // groups of one warp, added up by exchanges
@@ -41,7 +44,11 @@ __global__ void __launch_bounds__(kStepThreads) attn_step_kernel(AttnParams p) {
   for (int i = 0; i < kRows; ++i) {
     const int k = group + i * kGroups;
     fill(s[i], 0.0f);
-    if (a.first && mine && k < a.K) Piece<float, VEC>::load(a.first + state + (long long)k * a.V, s[i]);
+    if (a.first && mine && k < a.K) {
+      Packed<float, VEC> x;
+      x.load_streaming(a.first + state + (long long)k * a.V);
+      x.widen(s[i]);
+    }
   }
   const int L = row_length(p.lens, n, p.S);
   const float bias = p.bias ? p.bias[h] : 0.0f;
@@ -109,7 +116,11 @@ __global__ void __launch_bounds__(kStepThreads) attn_step_kernel(AttnParams p) {
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
       const int r = group + i * kGroups;
-      if (r < a.K) Piece<float, VEC>::store(a.last + state + (long long)r * a.V, s[i]);
+      if (r < a.K) {
+        Packed<float, VEC> x;
+        x.narrow(s[i]);
+        x.store_streaming(a.last + state + (long long)r * a.V);
+      }
     }
   }
 }
@@ -122,8 +133,8 @@ cudaError_t launch_steps(const AttnParams& p, cudaStream_t s) {
     return cudaGetLastError();
   };
   const bool pieces = a.V % 4 == 0 && reinterpret_cast<uintptr_t>(a.first) % 16 == 0 && reinterpret_cast<uintptr_t>(a.last) % 16 == 0;
-  // 64 tokens of 16 heads, states of 128 x 128: 34.8 us element by element (a
-  // block for 32 columns), @ us in pieces
+  // the same case element by element, a block for 32 columns: 34.8 us, 31.3 in
+  // pieces (both through the caches)
   if (!pieces) return run(attn_step_kernel<T, 1, 32>, 32);
   return a.V <= 64 ? run(attn_step_kernel<T, 4, 16>, 64) : run(attn_step_kernel<T, 4, 32>, 128);
 }
@@ -283,7 +294,10 @@ AttnPlan attn_plan(long long seq, long long batch, long long heads, int key_size
   AttnPlan plan{};
   const long long streams = streams_of(batch, heads, key_size, value_size, passes);
   const long long chunks = (seq + 63) / 64;
-  // pieces of two chunks at least, and as many as fit the card together
+  // pieces of two chunks at least, and as many as fit the card together: 4096 x
+  // 1 x 16 heads of 128 in nine, 64 us; in four 96, whole 188.  More than fit
+  // together cost their sums of states and bring nothing (8 x 777 x 10 heads,
+  // float32, whole 117 us, in two 147; gradient 8 x 512 x 16 139 and 255 us).
   long long segments = streams > 0 ? std::min(kPlanSms / streams, chunks / 2) : 1;
   segments = std::max<long long>(segments, 1);
   plan.per = (int)((chunks + segments - 1) / segments);

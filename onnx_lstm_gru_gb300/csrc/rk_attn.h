@@ -81,8 +81,8 @@ struct AttnParams {
   AttnPlan plan;
 };
 // The longest sequences that run step by step.  bfloat16, 16 heads of 128, 8
-// steps and 12, against one chunk: 1 batch row 12.4 and 14.6 us against 12.6,
-// 64 batch rows 57 and 74 us against 94; float32 against 18.7 and 133 us.
+// steps and 12, against one chunk: 1 batch row 12.4 and 14.5 us against 12.4,
+// 64 batch rows 51 and 66 us against 80; float32 against 18.7 and 130 us.
 constexpr int kAttnSteps = 12;
 // The plan of `passes` passes, its pointers left out; and the floats of its scratch.
 AttnPlan attn_plan(long long seq, long long batch, long long heads, int key_size, int value_size, int passes);
