@@ -572,10 +572,11 @@ typedef struct rk_attn_operands {
 /* Its gradient.  dQ, dK, dV have the problem's dtype (heads that share are
  * added up before the one rounding), dDecay (float32 rows of `heads`
  * elements), d_decay_bias, d_initial_state and the optional input
- * d_final_state are float32.  dDecay is taken from running sums, in float64,
- * over the sequence of what queries and keys contribute: where it is far
- * smaller than those contributions it has their float32 accuracy.  Infinities and NaN in an
- * operand may reach the gradients of any step of their batch row. */
+ * d_final_state are float32.  dDecay is taken from running sums over
+ * the sequence of what queries and keys contribute, in pairs of float32: where
+ * it is far smaller than those contributions it has their float32 accuracy.
+ * Infinities and NaN in an operand may reach the gradients of any step of
+ * their batch row. */
 typedef struct rk_attn_grad_operands {
   rk_rows Q, K, V, Decay, dY, dQ, dK, dV, dDecay;
   rk_tensor decay_bias, sequence_lens, initial_state, d_final_state, d_decay_bias, d_initial_state;

@@ -143,37 +143,61 @@ cudaError_t launch_steps(const AttnParams& p, cudaStream_t s) {
 // those from it on, which read it; with A_t = q dq and B_t = k dk of a step
 //   dg_t = E_0 + sum over s < t of (B_s - A_s),   E_0 = <H, dH> before the first,
 // and the same sum over all steps ends at E_L = <H, dH> behind the last.  The
-// sums are float64 (they run over the whole sequence); what the float32
-// products leave at the end is known, E_L, and is taken back evenly along the
-// way: with no states to start from or to end at, both ends are exact.
-// A block takes kDecayTile steps of one head, with what comes before and in all
-// added up by itself: pairs of float32 that keep what each addition rounds
-// away (Knuth's two-sum), which the card's few float64 units do not wait for.
-constexpr int kDecayThreads = 256, kDecayEach = 4, kDecayTile = kDecayThreads * kDecayEach;
+// sums run over the whole sequence, in pairs of float32 that keep what each
+// addition rounds away (Knuth's two-sum): the card has few float64 units, and
+// the kernel is a chain of sums, bound by their latency.  What the float32 products leave at the end is
+// known, E_L, and is taken back evenly along the way: with no states to start
+// from or to end at, both ends are exact.  A block takes kDecayTile steps of one
+// head, with what comes before and in all added up by itself.
+constexpr int kDecayThreads = 256, kDecayWarps = kDecayThreads / 32, kDecayEach = 4, kDecayTile = kDecayThreads * kDecayEach;
 struct Exact {
-  float hi = 0.0f, lo = 0.0f;
+  float hi, lo;
   __device__ __forceinline__ void add(float x) {
     const float s = hi + x, b = s - hi;
     lo += (hi - (s - b)) + (x - b);
     hi = s;
   }
-  __device__ __forceinline__ double value() const { return (double)hi + (double)lo; }
+  __device__ __forceinline__ void add(Exact x) {
+    add(x.hi);
+    lo += x.lo;
+    const float s = hi + lo;  // keeps lo far below hi
+    lo -= s - hi;
+    hi = s;
+  }
+  __device__ __forceinline__ float value() const { return hi + lo; }
+  __device__ __forceinline__ Exact operator-() const { return {-hi, -lo}; }
 };
-// Every thread gets the block's sum.
-__device__ __forceinline__ double decay_sum(double x, double* sums) {
+constexpr Exact kNothing = {0.0f, 0.0f};
+// The sum over groups of `lanes` lanes, in each of them the same.
+__device__ __forceinline__ Exact pair_sum(Exact x, int lanes) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  __syncthreads();
-  if (threadIdx.x % 32 == 0) sums[threadIdx.x / 32] = x;
-  __syncthreads();
-  x = sums[0];
-  for (int i = 1; i < kDecayThreads / 32; ++i) x += sums[i];
+  for (int o = 1; o < lanes; o <<= 1) {
+    const Exact y = {__shfl_xor_sync(0xffffffffu, x.hi, o), __shfl_xor_sync(0xffffffffu, x.lo, o)};
+    const bool second = threadIdx.x & o;  // one order for both
+    Exact z = second ? y : x;
+    z.add(second ? x : y);
+    x = z;
+  }
   return x;
 }
-__global__ void __launch_bounds__(kDecayThreads) attn_decay_kernel(AttnDecayParams p, int tiles) {
-  __shared__ double sums[kDecayThreads / 32];
-  const long long head = blockIdx.x / tiles;
-  const int tile = (int)(blockIdx.x - head * tiles), h = (int)(head % p.H), n = (int)(head / p.H);
+// The running sum over groups of `lanes` lanes.
+__device__ __forceinline__ Exact pair_scan(Exact x, int lanes) {
+#pragma unroll
+  for (int o = 1; o < lanes; o <<= 1) {
+    Exact y = {__shfl_up_sync(0xffffffffu, x.hi, o), __shfl_up_sync(0xffffffffu, x.lo, o)};
+    if ((int)(threadIdx.x & (lanes - 1)) >= o) {
+      y.add(x);
+      x = y;
+    }
+  }
+  return x;
+}
+__global__ void __launch_bounds__(kDecayThreads) attn_decay_kernel(AttnDecayParams p) {
+  __shared__ Exact sums[4][kDecayWarps];
+  previous_done();
+  next_may_start();
+  const long long head = blockIdx.x / p.tiles;
+  const int tile = (int)(blockIdx.x - head * p.tiles), h = (int)(head % p.H), n = (int)(head / p.H);
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int L = row_length(p.lens, n, p.S), begin = min(tile * kDecayTile, L);
   float* out = static_cast<float*>(p.dDecay.p) + n * p.dDecay.ns + h;
@@ -181,40 +205,47 @@ __global__ void __launch_bounds__(kDecayThreads) attn_decay_kernel(AttnDecayPara
   const float* to = p.to + head * p.S;
   const float* of = p.of + head * p.S;
   const float bias = p.bias ? p.bias[h] : 0.0f;
-  Exact before, rest;
-  for (int t = threadIdx.x; t < begin; t += kDecayThreads) before.add(of[t]), before.add(-to[t]);
-  for (int t = begin + threadIdx.x; t < L; t += kDecayThreads) rest.add(of[t]), rest.add(-to[t]);
-  const double first = p.first ? p.first[head] : 0.0, last = p.last ? p.last[head] : 0.0;
-  const double so_far = decay_sum(before.value(), sums), all = so_far + decay_sum(rest.value(), sums);
-  const double back = L > 0 ? (last - first - all) / L : 0.0;
+  const float first = p.first ? p.first[head] : 0.0f, last = p.last ? p.last[head] : 0.0f;
+  // the thread's own steps, and what is in the tile before each; all that is before the tile; all from it on
   const int t0 = begin + threadIdx.x * kDecayEach;
-  double own[kDecayEach], x = 0.0, total = 0.0;
+  float d[kDecayEach];
+  Exact own[kDecayEach], x = kNothing, before = kNothing, rest = kNothing;
+#pragma unroll
+  for (int i = 0; i < kDecayEach; ++i) d[i] = t0 + i < L && p.decay.p ? g[(t0 + i) * p.decay.ss] : 0.0f;
 #pragma unroll
   for (int i = 0; i < kDecayEach; ++i) {
     own[i] = x;
-    if (t0 + i < L) x += (double)of[t0 + i] - (double)to[t0 + i];
+    if (t0 + i < L) x.add(of[t0 + i]), x.add(-to[t0 + i]);
   }
-  double scan = x;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const double y = __shfl_up_sync(0xffffffffu, scan, o);
-    if (lane >= o) scan += y;
-  }
+  for (int t = threadIdx.x; t < begin; t += kDecayThreads) before.add(of[t]), before.add(-to[t]);
+  for (int t = begin + threadIdx.x; t < L; t += kDecayThreads) rest.add(of[t]), rest.add(-to[t]);
+  const Exact scan = pair_scan(x, 32);
+  before = pair_sum(before, 32), rest = pair_sum(rest, 32);
+  if (lane == 31) sums[0][warp] = before, sums[1][warp] = rest, sums[2][warp] = scan;
   __syncthreads();
-  if (lane == 31) sums[warp] = scan;
-  __syncthreads();
-  scan += first + so_far - x;
-  for (int i = 0; i < warp; ++i) scan += sums[i];
+  before = pair_sum(sums[0][lane % kDecayWarps], kDecayWarps);
+  rest = pair_sum(sums[1][lane % kDecayWarps], kDecayWarps);
+  const Exact warps = pair_scan(sums[2][lane % kDecayWarps], kDecayWarps);
+  Exact base = {__shfl_sync(0xffffffffu, warps.hi, max(warp - 1, 0)), __shfl_sync(0xffffffffu, warps.lo, max(warp - 1, 0))};
+  if (warp == 0) base = kNothing;
+  Exact lanes = {__shfl_up_sync(0xffffffffu, scan.hi, 1), __shfl_up_sync(0xffffffffu, scan.lo, 1)};
+  if (lane == 0) lanes = kNothing;
+  Exact left = -before;
+  left.add(-rest), left.add(last), left.add(-first);
+  const float back = L > 0 ? left.value() / (float)L : 0.0f;
+  base.add(lanes), base.add(before), base.add(first);
+  Exact total = kNothing;
   if (begin == tile * kDecayTile) {
 #pragma unroll
     for (int i = 0; i < kDecayEach; ++i) {
       const int t = t0 + i;
       if (t < L) {
+        Exact y = base;
+        y.add(own[i]), y.add(back * (float)t);
         // a decay of 0 has no gradient: the factor itself is in it
-        const float d = (p.decay.p ? g[t * p.decay.ss] : 0.0f) + bias;
-        const double y = d < -104.0f ? 0.0 : scan + own[i] + back * t;
-        if (p.dDecay.p) out[t * p.dDecay.ss] = (float)y;
-        total += y;
+        const float z = d[i] + bias < -104.0f ? 0.0f : y.value();
+        if (p.dDecay.p) out[t * p.dDecay.ss] = z;
+        total.add(z);
       }
     }
   }
@@ -222,12 +253,18 @@ __global__ void __launch_bounds__(kDecayThreads) attn_decay_kernel(AttnDecayPara
     for (int t = tile * kDecayTile + threadIdx.x; t < min((tile + 1) * kDecayTile, p.S); t += kDecayThreads)
       if (t >= L) out[t * p.dDecay.ss] = 0.0f;
   if (p.partial) {
-    total = decay_sum(total, sums);
-    if (threadIdx.x == 0) p.partial[blockIdx.x] = total;
+    total = pair_sum(total, 32);
+    if (lane == 0) sums[3][warp] = total;
+    __syncthreads();
+    total = pair_sum(sums[3][lane % kDecayWarps], kDecayWarps);
+    if (threadIdx.x == 0) p.partial[blockIdx.x] = (double)total.hi + (double)total.lo;
   }
 }
 
-__global__ void __launch_bounds__(256) attn_decay_bias_kernel(AttnDecayParams p, int tiles) {
+__global__ void __launch_bounds__(256) attn_decay_bias_kernel(AttnDecayParams p) {
+  previous_done();
+  next_may_start();
+  const int tiles = p.tiles;
   const int h = blockIdx.x * 8 + threadIdx.x / 32, lane = threadIdx.x % 32;
   if (h >= p.H) return;
   double x = 0.0;
@@ -240,6 +277,8 @@ __global__ void __launch_bounds__(256) attn_decay_bias_kernel(AttnDecayParams p,
 
 template <typename T>
 __global__ void __launch_bounds__(256) attn_share_kernel(AttnShareParams p) {
+  previous_done();
+  next_may_start();
   const int width = p.H / p.of * p.V;
   const long long count = (long long)p.N * p.S * width;
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < count; i += (long long)gridDim.x * 256) {
@@ -295,7 +334,7 @@ AttnPlan attn_plan(long long seq, long long batch, long long heads, int key_size
   const long long streams = streams_of(batch, heads, key_size, value_size, passes);
   const long long chunks = (seq + 63) / 64;
   // pieces of two chunks at least, and as many as fit the card together: 4096 x
-  // 1 x 16 heads of 128 in nine, 64 us; in four 96, whole 188.  More than fit
+  // 1 x 16 heads of 128 in eight, 64 us; in four 96, whole 188.  More than fit
   // together cost their sums of states and bring nothing (8 x 777 x 10 heads,
   // float32, whole 117 us, in two 147; gradient 8 x 512 x 16 139 and 255 us).
   long long segments = streams > 0 ? std::min(kPlanSms / streams, chunks / 2) : 1;
@@ -316,17 +355,15 @@ long long attn_plan_scratch(const AttnPlan& plan, long long batch, long long hea
 
 int attn_decay_tiles(long long seq) { return (int)((seq + kDecayTile - 1) / kDecayTile); }
 
-cudaError_t launch_attn_decay(const AttnDecayParams& p, cudaStream_t s, int* launches) {
-  const int tiles = attn_decay_tiles(p.S);
-  const long long blocks = (long long)p.N * p.H * tiles;
+cudaError_t launch_attn_decay(AttnDecayParams p, cudaStream_t s, int* launches) {
+  p.tiles = attn_decay_tiles(p.S);
+  const long long blocks = (long long)p.N * p.H * p.tiles;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  attn_decay_kernel<<<(unsigned)blocks, kDecayThreads, 0, s>>>(p, tiles);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_chained(attn_decay_kernel, (unsigned)blocks, kDecayThreads, 0, s, p);
   if (e != cudaSuccess) return e;
   ++*launches;
   if (p.dbias == nullptr) return e;
-  attn_decay_bias_kernel<<<(p.H + 7) / 8, 256, 0, s>>>(p, tiles);
-  e = cudaGetLastError();
+  e = launch_chained(attn_decay_bias_kernel, (unsigned)((p.H + 7) / 8), 256, 0, s, p);
   if (e == cudaSuccess) ++*launches;
   return e;
 }
@@ -334,12 +371,10 @@ cudaError_t launch_attn_decay(const AttnDecayParams& p, cudaStream_t s, int* lau
 cudaError_t launch_attn_share(const AttnShareParams& p, cudaStream_t s, int* launches) {
   const long long count = (long long)p.N * p.S * (p.H / p.of) * p.V;
   const unsigned grid = (unsigned)std::min<long long>((count + 255) / 256, kPlanSms * 32);
-  switch (p.dtype) {
-    case RK_F32: attn_share_kernel<float><<<grid, 256, 0, s>>>(p); break;
-    case RK_F16: attn_share_kernel<__half><<<grid, 256, 0, s>>>(p); break;
-    default: attn_share_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(p);
-  }
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_chained(p.dtype == RK_F32   ? attn_share_kernel<float>
+                                       : p.dtype == RK_F16 ? attn_share_kernel<__half>
+                                                           : attn_share_kernel<__nv_bfloat16>,
+                                       grid, 256, 0, s, p);
   if (e == cudaSuccess) ++*launches;
   return e;
 }

@@ -113,9 +113,10 @@ struct AttnDecayParams {
   const float* last;   // and behind the last
   double* partial;     // [N][H][tiles]
   float* dbias;        // [H], or null
+  int tiles;           // set by the launch
 };
 int attn_decay_tiles(long long seq);
-cudaError_t launch_attn_decay(const AttnDecayParams& p, cudaStream_t s, int* launches);
+cudaError_t launch_attn_decay(AttnDecayParams p, cudaStream_t s, int* launches);
 
 // o = sums over the heads that share of o32.
 struct AttnShareParams {

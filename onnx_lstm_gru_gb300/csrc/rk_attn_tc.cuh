@@ -624,6 +624,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
+  next_may_start();
+  if (OUT) previous_done();  // the states that segments start from
   // Where U of chunk i is: without outputs there is room for two, and the next is on its way while one is added.
   auto u_at = [](int i) { return OUT ? kU : 128u * (i & 1); };
   struct Phase {
@@ -1305,6 +1307,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
 template <int HPC, int KB>
 __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnParams p) {
   constexpr int kept = KB * 64 * 128;
+  next_may_start();
+  previous_done();
   const int element = blockIdx.y * 256 + threadIdx.x;
   const int k = element / 128, r = element % 128;
   if (HPC == 2 && k >= 64) return;
@@ -1395,12 +1399,17 @@ cudaError_t launch_chunks_of(const ChunkArgs& args, cudaStream_t s, int* launche
     sums<<<(unsigned)(streams * (p.plan.segments - 1)), kThreads, sums_smem, s>>>(args);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     ++*launches;
-    attn_join_kernel<HPC, KB><<<dim3((unsigned)streams, KB * 64 * 128 / 256), 256, 0, s>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = launch_chained(attn_join_kernel<HPC, KB>, dim3((unsigned)streams, KB * 64 * 128 / 256), 256, 0, s, p);
+    if (e != cudaSuccess) return e;
     ++*launches;
   }
-  whole<<<(unsigned)(streams * p.plan.segments), kThreads, smem, s>>>(args);
-  if ((e = cudaGetLastError()) == cudaSuccess) ++*launches;
+  if (p.plan.segments > 1) {
+    e = launch_chained(whole, (unsigned)(streams * p.plan.segments), kThreads, smem, s, args);
+  } else {
+    whole<<<(unsigned)streams, kThreads, smem, s>>>(args);
+    e = cudaGetLastError();
+  }
+  if (e == cudaSuccess) ++*launches;
   return e;
 }
 

@@ -410,6 +410,7 @@ __global__ void __launch_bounds__(kQkThreads, U > 2 ? 1 : 2) qk_kernel(QkParams 
 
 template <typename T, int V, int U, bool IL>
 __global__ void __launch_bounds__(kQkThreads, U > 2 ? 1 : 2) qk_grad_kernel(QkParams p) {
+  next_may_start();
   using L = Lane<T, V, U, IL>;
   constexpr int J = L::J;
   const int lane = threadIdx.x % 32, heads = 32 / p.lanes, mine = lane / p.lanes, own = mine * p.size;

@@ -6,6 +6,7 @@ namespace {
 
 // Sums over the blocks, one warp for each element of the two scales.
 __global__ void __launch_bounds__(256) qk_scale_kernel(QkParams p) {
+  previous_done();
   const int i = blockIdx.x * 8 + threadIdx.x / 32, lane = threadIdx.x % 32;
   if (i >= 2 * p.size) return;
   float* out = i < p.size ? p.side[0].dscale : p.side[1].dscale;
@@ -27,8 +28,7 @@ cudaError_t launch_qk_grad(const QkParams& p, cudaStream_t s, int* launches) {
   if (e != cudaSuccess) return e;
   ++*launches;
   if (p.partial == nullptr) return e;
-  qk_scale_kernel<<<(2 * p.size + 7) / 8, 256, 0, s>>>(p);
-  e = cudaGetLastError();
+  e = launch_chained(qk_scale_kernel, (unsigned)((2 * p.size + 7) / 8), 256, 0, s, p);
   if (e == cudaSuccess) ++*launches;
   return e;
 }
