@@ -176,7 +176,7 @@ rk_status rk_qk_encode(rk_handle* h, const rk_qk_problem* p, const rk_qk_operand
   rk::QkParams q = qk_params(c, p, o);
   q.side[0].Y = c.steps("YQ", o->YQ, p, p->heads * p->size, 1, false);
   q.side[1].Y = c.steps("YK", o->YK, p, p->key_heads * p->size, 1, false);
-  if (!c.ok() || p->seq * p->batch == 0) return c.st;
+  if (!c.ok() || p->seq * p->batch == 0 || (q.side[0].Y.p == nullptr && q.side[1].Y.p == nullptr)) return c.st;
   qk_pieces(q, c.eb);
   c.cuda("launch", rk::launch_qk(q, static_cast<cudaStream_t>(stream)));
   if (c.ok()) h->launches += 1;
@@ -197,7 +197,9 @@ rk_status rk_qk_grad_encode(rk_handle* h, const rk_qk_problem* p, const rk_qk_gr
   q.side[1].dX = c.steps("dK", o->dK, p, p->key_heads * p->size, 1, false);
   q.side[0].dscale = c.tensor<float>("dQScale", o->dQScale, p->size, 4);
   q.side[1].dscale = c.tensor<float>("dKScale", o->dKScale, p->size, 4);
-  if (!c.ok()) return c.st;
+  bool wanted = false;
+  for (const rk::QkSide& side : q.side) wanted = wanted || side.dX.p || side.dscale;
+  if (!c.ok() || !wanted) return c.st;
   if (p->seq * p->batch == 0) {
     for (const rk::QkSide& side : q.side) c.zero(side.dscale, p->size * 4, s);
     return c.st;
@@ -236,7 +238,7 @@ rk_status rk_attn_encode(rk_handle* h, const rk_attn_problem* p, const rk_attn_o
   ap.lens = c.tensor<int>("sequence_lens", o->sequence_lens, p->batch, 4);
   a.first = c.tensor<float>("initial_state", o->initial_state, states, 4);
   a.last = c.tensor<float>("final_state", o->final_state, states, 4);
-  if (!c.ok()) return c.st;
+  if (!c.ok() || (a.o.p == nullptr && a.last == nullptr)) return c.st;
   if (p->seq * p->batch == 0) {
     c.copy(a.last, a.first, states * 4, s);
     return c.st;
@@ -283,7 +285,7 @@ rk_status rk_attn_grad_encode(rk_handle* h, const rk_attn_problem* p, const rk_a
   const float* dlast = c.tensor<float>("d_final_state", o->d_final_state, states, 4);
   float* dbias = c.tensor<float>("d_decay_bias", o->d_decay_bias, H, 4);
   float* dfirst = c.tensor<float>("d_initial_state", o->d_initial_state, states, 4);
-  if (!c.ok()) return c.st;
+  if (!c.ok() || !(dQ.p || dK.p || dV.p || dDecay.p || dbias || dfirst)) return c.st;
   if (p->seq * p->batch == 0) {
     c.zero(dbias, H * 4LL, s);
     c.copy(dfirst, dlast, states * 4, s);

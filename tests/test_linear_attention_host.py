@@ -137,6 +137,19 @@ def test_problem_refusals(handle, op, field, value, code, text):
         assert SCRATCH[op](c) == -1
 
 
+@pytest.mark.parametrize("op", list(PROBLEMS))
+def test_nothing_wanted_launches_nothing(handle, op):
+    ops = operands(op, PROBLEMS[op])
+    rows, tensors = ss._OPERANDS[op]
+    for n in rows + tensors:
+        if n in ss._OUTPUTS[op]:
+            getattr(ops, n).ptr = None
+    before = rk.rk_launch_count(handle)
+    st, msg = encode(handle, op, PROBLEMS[op].to_c(), ops)
+    assert st == rk.RK_OK, msg
+    assert rk.rk_launch_count(handle) == before
+
+
 def test_no_heads_is_no_default(handle):
     """In the problem classes None stands for as many as heads; 0 is an error."""
     for name in ("query_heads", "key_heads", "value_heads"):
