@@ -12,15 +12,17 @@
 //   Oi = H^T Q^T          [v][m]     (the state's transpose in tensor memory)
 //   O  = V^T P^T          [v][m]
 //   U  = V^T (ck K)       [v][k]     then H^T = 2^(G_end) H^T + su U
-// Values run along the 128 lanes of tensor memory, so that the state, which a
-// lane's thread keeps in float32 registers, needs no transposition between U,
-// where it is added to, and Oi, where it is the product's A operand.
+// Values run along the 128 lanes of tensor memory, where the state lives too:
+// it needs no transposition between U, where it is added to, and Oi, where it
+// is the product's A operand.  It is kept in float32, or as three bfloat16 terms
+// that add up to it.
 //
 // The tensor cores multiply bfloat16.  A factor of more bits is a sum of two
 // or three bfloat16 terms (each the rounding of what the ones before left),
 // and a product the sum of the terms' products down to 2^-24 of it, smallest
 // first; bfloat16 operands are one term, Half two, float32 three, and what is
-// computed here (P, ck K, H) three.  Differences of G are exact to 2^-24: sums
+// computed here (P, ck K, H) three, or P and H two where only a 16-bit output
+// comes of them, which keeps less than their 2^-17.  Differences of G are exact to 2^-24: sums
 // are 64-bit whole numbers of 2^-32, kept as whole part and fraction.
 //
 // Where a chunk's decays stay within 2^-100, P_mn 2^-G_m is S_mn 2^-G_n: then
@@ -45,6 +47,13 @@
 // Infinities and NaN must not reach other steps through the products' zeros:
 // a chunk in which an operand, a product of P or the state is not finite is
 // run step by step instead.
+//
+// What bounds it are the warps' own instructions and their waits for each
+// other, not the products or HBM: 512 x 64 x 16 heads of 64, bf16, 112 us (2.6
+// TB/s, 2.2 warp instructions a clock and multiprocessor, the tensor pipe 30 %
+// busy); the gradient of 512 x 8 x 16 heads of 128 135 us (2.2, 21 %); 777 x 8 x 10
+// heads of 72 x 103 in float32, 80 blocks, 110 us (1.7, 25 %).  Step by step the
+// three take 2316, 2319 and 646 us.
 #pragma once
 #include <cuda_runtime.h>
 
@@ -1303,44 +1312,53 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
 }
 
 // The states that a stream's segments start from, from what each adds: in the
-// pass's order, element by element.
+// pass's order, four elements of a thread at a time (5.7 us for 16 states of 128 x
+// 128 in eight segments, 13 us element by element; both are round trips).
+constexpr int kJoin = 4 * 256;  // elements of a block
 template <int HPC, int KB>
 __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnParams p) {
   constexpr int kept = KB * 64 * 128;
   next_may_start();
   previous_done();
-  const int element = blockIdx.y * 256 + threadIdx.x;
-  const int k = element / 128, r = element % 128;
-  if (HPC == 2 && k >= 64) return;
+  const int element = blockIdx.y * kJoin + threadIdx.x * 4;
+  const int k = element / 128, r = element % 128, head = HPC == 2 ? r >> 6 : 0;
   long long id = blockIdx.x;
   const int groups = (p.H + HPC - 1) / HPC;
-  const int h = (int)(id % groups) * HPC + (HPC == 2 ? r >> 6 : 0), v = HPC == 2 ? r & 63 : r;
+  const int h = (int)(id % groups) * HPC + head, v = HPC == 2 ? r & 63 : r;
   const int n = (int)(id / groups % p.N);
   const AttnPass& a = p.pass[id / groups / p.N];
-  const bool mine = h < p.H && v < a.V && k < a.K;
-  float run = 0.0f;
-  if (mine && a.first)
-    run = a.first[((long long)n * p.H + h) * a.K * a.V + (a.v_major ? (long long)v * a.K + k : (long long)k * a.V + v)];
-  float* s = p.plan.states + id * p.plan.segments * kept + element;
-  const float* f = p.plan.left + (id * p.plan.segments * 2 + (HPC == 2 ? r >> 6 : 0)) * 2;
+  float run[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (h < p.H && k < a.K && a.first) {
+    const float* from = a.first + ((long long)n * p.H + h) * a.K * a.V;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (v + e < a.V) run[e] = from[a.v_major ? (long long)(v + e) * a.K + k : (long long)k * a.V + v + e];
+  }
+  float4* s = reinterpret_cast<float4*>(p.plan.states + id * p.plan.segments * kept + element);
+  const float* f = p.plan.left + (id * p.plan.segments * 2 + head) * 2;
   constexpr int kBatch = 8;  // read before any of it is written: on their way together
 #pragma unroll 1
   for (int i0 = 0; i0 < p.plan.segments; i0 += kBatch) {
-    float add[kBatch], part[kBatch], whole[kBatch];
+    float4 add[kBatch];
+    float2 left[kBatch];
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
       const int i = i0 + j;
-      if (i + 1 < p.plan.segments) add[j] = s[(long long)i * kept], whole[j] = f[4 * i], part[j] = f[4 * i + 1];
+      if (i + 1 < p.plan.segments)
+        add[j] = s[(long long)i * (kept / 4)], left[j] = *reinterpret_cast<const float2*>(f + 4 * i);
     }
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
       const int i = i0 + j;
       if (i >= p.plan.segments) break;
-      s[(long long)i * kept] = run;
+      s[(long long)i * (kept / 4)] = make_float4(run[0], run[1], run[2], run[3]);
       if (i + 1 >= p.plan.segments) break;
       // 2^x run in two parts: where decays grow a state the power alone may pass float32's range
-      const int w = (int)whole[j], w1 = max(min(w, 127), -126), w2 = max(min(w - w1, 127), -126);
-      run = run * exp2_fast(part[j]) * __int_as_float((w1 + 127) << 23) * __int_as_float((w2 + 127) << 23) + add[j];
+      const int w = (int)left[j].x, w1 = max(min(w, 127), -126), w2 = max(min(w - w1, 127), -126);
+      const float part = exp2_fast(left[j].y), f1 = __int_as_float((w1 + 127) << 23), f2 = __int_as_float((w2 + 127) << 23);
+      const float x[4] = {add[j].x, add[j].y, add[j].z, add[j].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) run[e] = run[e] * part * f1 * f2 + x[e];
     }
   }
 }
@@ -1399,7 +1417,7 @@ cudaError_t launch_chunks_of(const ChunkArgs& args, cudaStream_t s, int* launche
     sums<<<(unsigned)(streams * (p.plan.segments - 1)), kThreads, sums_smem, s>>>(args);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     ++*launches;
-    e = launch_chained(attn_join_kernel<HPC, KB>, dim3((unsigned)streams, KB * 64 * 128 / 256), 256, 0, s, p);
+    e = launch_chained(attn_join_kernel<HPC, KB>, dim3((unsigned)streams, KB * 64 * 128 / kJoin), 256, 0, s, p);
     if (e != cudaSuccess) return e;
     ++*launches;
   }

@@ -3,10 +3,14 @@
 //   n = x inv w;  a' = a c - b s, b' = b c + a s for each pair (a, b) of n
 //   backward: g = the turn back of dy;  dw = sum of g x inv;
 //   dx = inv (g w) - x inv^3 sum(g w x) / m,  m = size (root mean square) or 1
-// Both are bound by HBM: a row is read once and everything is computed in
-// registers.  A warp takes a row's heads in turns, so that a row's cosines and
-// sines, which all heads share, are computed once; a lane holds both elements
-// of its pairs, and a head's sum is a few exchanges of lanes.
+// A row is read once and everything is computed in registers.  A warp takes a
+// row's heads in turns, so that a row's cosines and sines, which all heads
+// share, are computed once; a lane holds both elements of its pairs, and a
+// head's sum is a few exchanges of lanes.
+// What bounds them is HBM and, next to it, instructions: 32768 rows of 16 + 16
+// heads of 64, bf16, 55.6 us or 4.8 TB/s (71 % of a copy) at 2.5 warp instructions a
+// clock and multiprocessor, 308 for a warp's 512 elements; the gradient of 8 + 8
+// heads of 128 92 us, 4.4 TB/s (64 %), at 2.4, its 16 warps bound by registers.
 #pragma once
 #include <algorithm>
 
