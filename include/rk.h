@@ -250,7 +250,7 @@ rk_status rk_encode_host(rk_handle* h, const rk_problem* p, const rk_operands* h
  * (and, once rk_encode_noalloc has run on the handle, the status word of its
  * fixed array): RK_OK, or RK_ERR_TIMEOUT if a bounded device wait of a step
  * kernel, of the tensor-core projection or of the linear attention in chunks
- * gave up during a previous encode;
+ * (of any handle on the device) gave up during a previous encode;
  * the outputs of that encode are then undefined.  The web page "Recurrent
  * layers" has no counterpart: its design waits on nothing inside a launch
  * (one pass per step, paragraph "Why a pass per step"), while this library's

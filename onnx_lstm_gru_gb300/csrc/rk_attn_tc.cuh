@@ -25,7 +25,7 @@
 // comes of them, which keeps less than their 2^-17.  Differences of G are exact to 2^-24: sums
 // are 64-bit whole numbers of 2^-32, kept as whole part and fraction.
 //
-// Where a chunk's decays stay within 2^-100, P_mn 2^-G_m is S_mn 2^-G_n: then
+// Where a chunk's decays (and the scale) stay within 2^-100, P_mn 2^-G_m is S_mn 2^-G_n: then
 // no power is taken for each pair, and O is added to Oi before 2^G_m scales
 // both.  (Backward the same from the chunk's end.)  Chunks that decay further
 // take the powers pair by pair and keep the two apart.
@@ -314,6 +314,8 @@ __device__ __forceinline__ bool chunk_decays(const AttnPass& a, float x0, float 
     if (lane >= o) sum += y;
   }
   const long long total = __shfl_sync(0xffffffffu, sum, 31);
+  // the scale's power goes with the decays': together they stay in float32's range
+  const int limit = 100 - abs((int)(__float_as_uint(a.so * a.su) >> 23 & 255) - 127);
   bool mild = true;
 #pragma unroll 1
   for (int j = 0; j < 2; ++j) {
@@ -323,7 +325,7 @@ __device__ __forceinline__ bool chunk_decays(const AttnPass& a, float x0, float 
     out.lo[i] = (float)((uint32_t)s >> 8) * 5.9604644775390625e-8f;
     const long long from = backward ? total - G : G;
     bad = bad || G >> 32 > 120 || (total - G) >> 32 > 120;
-    mild = mild && from >> 32 >= -100 && from >> 32 <= 100;
+    mild = mild && from >> 32 >= -limit && from >> 32 <= limit;
     const float up = pow2_of(G), down = pow2_of(total - G);
     out.cq[i] = a.so * (backward ? down : up);
     out.ck[i] = a.su * (backward ? up : down);

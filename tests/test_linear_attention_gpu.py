@@ -682,6 +682,15 @@ def test_attn_no_decay_keeps_all(layer):
         check(batch_first(got[k], 0).float() if k == "Y" else got[k], want[k], k, arithmetic=1.5e-4)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("scale", [1e-30, 1e-12, -3.0, 1e30, 0.0])
+def test_attn_scales_of_any_size(layer, scale, dtype):
+    """Decays of 2^-92 over a chunk and a scale that is far from 1 itself."""
+    c = Case(130, 1, 2, 64, 48, dtype, ragged=False, scale=scale, grad=True, layout=1)
+    c.t["Decay"].fill_(-1.0)
+    both_ways(layer, c)
+
+
 def test_attn_state_in_place_in_pieces(layer):
     c = Case(900, 1, 2, 64, 64, "bf16", ragged=False, decay="both")
     assert cut(c)
