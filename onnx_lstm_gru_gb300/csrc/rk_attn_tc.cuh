@@ -623,6 +623,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
     for (int i = 0; i < 8; ++i) sh.bad[i] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (OUT) {  // the states that are read at either end: on their way from HBM
+    const long long from = ((long long)at.n * p.H + at.h0) * a.K * a.V;
+    const int many = min(HPC, p.H - at.h0) * a.K * a.V;
+    for (int i = tid * 32; i < many; i += kThreads * 32) {
+      if (a.first && segments == 1) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.first + from + i));
+      if (a.with && order == segments - 1) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.with + from + i));
+    }
+  }
   if (TMA && warp == 3 * kGroupWarps + 1 && lane < 5) {
     const CUtensorMap* maps[] = {args.k, args.v, args.q, args.o, args.with};
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(maps[lane] + at.pass)) : "memory");
@@ -968,6 +976,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
       tmem_st_done();
       if (OUT && mine && !is_finite(finite)) sh.bad[i & 7] = 1;
     };
+    // Elements j .. j + 15 of the `there` that there are of a state, `far` apart; side by side in pieces of four.
+    auto read16 = [&](const float* from, int j, int far, int there, float (&y)[16]) {
+      if (far == 1 && a.K % 4 == 0 && reinterpret_cast<uintptr_t>(from) % 16 == 0) {
+#pragma unroll
+        for (int x = 0; x < 16; x += 4) {
+          float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (j + x < there) f = *reinterpret_cast<const float4*>(from + j + x);
+          y[x] = f.x, y[x + 1] = f.y, y[x + 2] = f.z, y[x + 3] = f.w;
+        }
+      } else {
+#pragma unroll
+        for (int x = 0; x < 16; ++x) y[x] = j + x < there ? from[(j + x) * far] : 0.0f;
+      }
+    };
     // The state before the first chunk.
     auto begin_state = [&]() {
       const bool pieces = OUT && segments > 1;
@@ -976,10 +998,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
       F2 finite = zero;
 #pragma unroll 1
       for (int j = 0; j < NH; j += 16) {
+        float y[16];
+        read16(from, j, far, there, y);
         F2 H[8];
 #pragma unroll
-        for (int x = 0; x < 8; ++x)
-          H[x] = f2(j + 2 * x < there ? from[(j + 2 * x) * far] : 0.0f, j + 2 * x + 1 < there ? from[(j + 2 * x + 1) * far] : 0.0f);
+        for (int x = 0; x < 8; ++x) H[x] = f2(y[2 * x], y[2 * x + 1]);
         write_state(j, H, finite);
       }
       wrote(finite, 0);
@@ -1080,15 +1103,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
         for (int j = 0; j < NH; j += 16) {
           float y[16];
           one_state(j, y);
-          if (a.last) {
+          if (a.last) {  // of passes that have the state's rows along their values only
 #pragma unroll
             for (int x = 0; x < 16; ++x)
               if (j + x < elements) a.last[state + (j + x) * apart] = y[x];
           }
           if (a.with) {
+            float z[16];
+            read16(a.with + state, j, apart, elements, z);
 #pragma unroll
             for (int x = 0; x < 16; ++x)
-              if (j + x < elements) with = fmaf(a.with[state + (j + x) * apart], y[x], with);
+              if (j + x < elements) with = fmaf(z[x], y[x], with);
           }
         }
         with = warp_sum(with);
