@@ -281,16 +281,17 @@ template <typename T>
 __global__ void __launch_bounds__(256) attn_share_kernel(AttnShareParams p) {
   previous_done();
   next_may_start();
-  const int width = p.H / p.of * p.V;
+  const auto& out = p.out[blockIdx.y];
+  const int width = p.H / out.of * out.V;
   const long long count = (long long)p.N * p.S * width;
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < count; i += (long long)gridDim.x * 256) {
     const long long r = i / width;
-    const int c = (int)(i - r * width), head = c / p.V, v = c - head * p.V;
+    const int c = (int)(i - r * width), head = c / out.V, v = c - head * out.V;
     const int n = (int)(r / p.S), s = (int)(r - (long long)n * p.S);
-    const float* x = p.o32 + (r * p.H + (long long)head * p.of) * p.V + v;
+    const float* x = out.o32 + (r * p.H + (long long)head * out.of) * out.V + v;
     float y = 0.0f;
-    for (int j = 0; j < p.of; ++j) y += x[(long long)j * p.V];
-    static_cast<T*>(p.o.p)[s * p.o.ss + n * p.o.ns + c] = Elem<T>::from_f(y);
+    for (int j = 0; j < out.of; ++j) y += x[(long long)j * out.V];
+    static_cast<T*>(out.o.p)[s * out.o.ss + n * out.o.ns + c] = Elem<T>::from_f(y);
   }
 }
 
@@ -338,7 +339,7 @@ AttnPlan attn_plan(long long seq, long long batch, long long heads, int key_size
   // pieces of two chunks at least, and as many as fit the card together: 4096 x
   // 1 x 16 heads of 128 in eight, 64 us; in four 96, whole 188.  More than fit
   // together cost their sums of states and bring nothing (8 x 777 x 10 heads,
-  // float32, whole 117 us, in two 147; gradient 8 x 512 x 16 139 and 255 us).
+  // float32, whole 117 us, in two 147; gradient 8 x 512 x 16 137 and 255 us).
   long long segments = streams > 0 ? std::min(kPlanSms / streams, chunks / 2) : 1;
   segments = std::max<long long>(segments, 1);
   plan.per = (int)((chunks + segments - 1) / segments);
@@ -371,8 +372,9 @@ cudaError_t launch_attn_decay(AttnDecayParams p, cudaStream_t s, int* launches) 
 }
 
 cudaError_t launch_attn_share(const AttnShareParams& p, cudaStream_t s, int* launches) {
-  const long long count = (long long)p.N * p.S * (p.H / p.of) * p.V;
-  const unsigned grid = (unsigned)std::min<long long>((count + 255) / 256, kPlanSms * 32);
+  long long most = 0;
+  for (int i = 0; i < p.count; ++i) most = std::max(most, (long long)p.N * p.S * (p.H / p.out[i].of) * p.out[i].V);
+  const dim3 grid((unsigned)std::min<long long>((most + 255) / 256, kPlanSms * 32), p.count);
   const cudaError_t e = launch_chained(p.dtype == RK_F32   ? attn_share_kernel<float>
                                        : p.dtype == RK_F16 ? attn_share_kernel<__half>
                                                            : attn_share_kernel<__nv_bfloat16>,

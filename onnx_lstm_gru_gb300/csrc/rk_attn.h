@@ -82,7 +82,7 @@ struct AttnParams {
 };
 // The longest sequences that run step by step.  bfloat16, 16 heads of 128, 8
 // steps and 12, against one chunk: 1 batch row 12.4 and 14.5 us against 12.4,
-// 64 batch rows 51 and 66 us against 80; float32 against 18.7 and 130 us.
+// 64 batch rows 51 and 66 us against 72; float32 against 18.6 and 119 us.
 constexpr int kAttnSteps = 12;
 // The plan of `passes` passes, its pointers left out; and the floats of its scratch.
 AttnPlan attn_plan(long long seq, long long batch, long long heads, int key_size, int value_size, int passes);
@@ -118,11 +118,14 @@ struct AttnDecayParams {
 int attn_decay_tiles(long long seq);
 cudaError_t launch_attn_decay(AttnDecayParams p, cudaStream_t s, int* launches);
 
-// o = sums over the heads that share of o32.
+// o = sums over the heads that share of o32, for up to three outputs.
 struct AttnShareParams {
-  int dtype, S, N, H, V, of;
-  const float* o32;
-  RowsArg o;
+  int dtype, S, N, H, count;
+  struct {
+    int V, of;
+    const float* o32;
+    RowsArg o;
+  } out[3];
 };
 cudaError_t launch_attn_share(const AttnShareParams& p, cudaStream_t s, int* launches);
 

@@ -347,14 +347,14 @@ rk_status rk_attn_grad_encode(rk_handle* h, const rk_attn_problem* p, const rk_a
     d.partial = dbias ? reinterpret_cast<double*>(partial) : nullptr;
     c.cuda("launch", rk::launch_attn_decay(d, s, &launches));
   }
+  rk::AttnShareParams sp{p->dtype, ap.S, ap.N, H};
   auto share = [&](const RowsArg& out, const float* o32, int V_, int n) {
-    if (!c.ok() || n == 1 || !out.p) return;
-    rk::AttnShareParams sp{p->dtype, ap.S, ap.N, H, V_, n, o32, out};
-    c.cuda("launch", rk::launch_attn_share(sp, s, &launches));
+    if (n > 1 && out.p) sp.out[sp.count++] = {V_, n, o32, out};
   };
   share(dQ, q32, dk, q_of);
   share(dK, k32, dk, k_of);
   share(dV, v32, dv, v_of);
+  if (c.ok() && sp.count) c.cuda("launch", rk::launch_attn_share(sp, s, &launches));
   h->launches += launches;
   return c.st;
 }

@@ -49,10 +49,10 @@
 // run step by step instead.
 //
 // What bounds it are the warps' own instructions and their waits for each
-// other, not the products or HBM: 512 x 64 x 16 heads of 64, bf16, 112 us (2.6
+// other, not the products or HBM: 512 x 64 x 16 heads of 64, bf16, 111 us (2.6
 // TB/s, 2.2 warp instructions a clock and multiprocessor, the tensor pipe 30 %
-// busy); the gradient of 512 x 8 x 16 heads of 128 135 us (2.2, 21 %); 777 x 8 x 10
-// heads of 72 x 103 in float32, 80 blocks, 110 us (1.7, 25 %).  Step by step the
+// busy); the gradient of 512 x 8 x 16 heads of 128 137 us (2.2, 21 %); 777 x 8 x 10
+// heads of 72 x 103 in float32, 80 blocks, 106 us (1.7, 25 %).  Step by step the
 // three take 2316, 2319 and 646 us.
 #pragma once
 #include <cuda_runtime.h>
@@ -623,7 +623,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
     for (int i = 0; i < 8; ++i) sh.bad[i] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (OUT) {  // the states that are read at either end: on their way from HBM
+  // The states that are read at either end are on their way from HBM: a gradient of 6 x 8 x 4 heads of 128 with
+  // states 19 us, 35 without this and with single elements of those that lie along the lanes' way.
+  if (OUT) {
     const long long from = ((long long)at.n * p.H + at.h0) * a.K * a.V;
     const int many = min(HPC, p.H - at.h0) * a.K * a.V;
     for (int i = tid * 32; i < many; i += kThreads * 32) {
