@@ -140,18 +140,19 @@ cudaError_t launch_steps(const AttnParams& p, cudaStream_t s) {
 }
 
 // A step's decay lies between the steps before it, which wrote the state, and
-// those from it on, which read it; with A_t = q dq and B_t = k dk of a step
-//   dg_t = E_0 + sum over s < t of (B_s - A_s),   E_0 = <H, dH> before the first,
-// and the same sum over all steps ends at E_L = <H, dH> behind the last.  The
-// sums run over the whole sequence, in pairs of float32 that keep what each
-// addition rounds away (Knuth's two-sum): the card has few float64 units, and
-// the kernel is a chain of sums, bound by their latency (128 heads of 512 steps
-// 11.8 us with float64, the call around it 3.5 us shorter so).  What the float32
-// products leave at the end is known, E_L, and is taken back evenly along the
-// way: with no states to start from or to end at, both ends are exact.  A block
-// takes kDecayTile steps of one head, with what comes before and in all added up
-// by itself.
-constexpr int kDecayThreads = 256, kDecayWarps = kDecayThreads / 32, kDecayEach = 4, kDecayTile = kDecayThreads * kDecayEach;
+// those from it on, which read it: its gradient is E = <H, dH>, the product of
+// the state before the step with its gradient.  With A_t = q dq and B_t = k dk
+// of a step, E grows by B_t - A_t from one step to the next.  The sums run from
+// one mark to the next, kMarkChunks chunks on, where E is taken from the states
+// themselves, as it is at both ends of the sequence: over 4000 steps and more the
+// float32 products' errors would add up to 4e-5 of a bias' gradient.  What they
+// leave at a mark is taken back evenly on the way to it.  A block takes the steps
+// between two marks; the sums are pairs of float32 that keep what each addition
+// rounds away (Knuth's two-sum), as the card has few float64 units and the kernel
+// is a chain of sums, bound by their latency (128 heads of 512 steps 11.8 us with
+// float64, 7.2 so).
+constexpr int kDecayThreads = 256, kDecayWarps = kDecayThreads / 32, kDecayEach = 2, kDecayTile = kDecayThreads * kDecayEach;
+static_assert(kDecayTile == kMarkChunks * 64, "a block's steps are those between two marks");
 struct Exact {
   float hi, lo;
   __device__ __forceinline__ void add(float x) {
@@ -194,56 +195,86 @@ __device__ __forceinline__ Exact pair_scan(Exact x, int lanes) {
   }
   return x;
 }
+// The products of the states at a mark, heads of a block apart.
+__global__ void __launch_bounds__(kDecayThreads) attn_mark_kernel(AttnDecayParams p) {
+  __shared__ float sums[kDecayWarps];
+  previous_done();
+  next_may_start();
+  const long long all = (long long)gridDim.x * p.deep * 128;
+  const float4* x = reinterpret_cast<const float4*>(p.states + (long long)blockIdx.x * p.deep * 128);
+  const float4* y = reinterpret_cast<const float4*>(p.states + all + (long long)blockIdx.x * p.deep * 128);
+  float e = 0.0f;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < p.deep * 32; i += kDecayThreads) {
+    const float4 f = x[i], g = y[i];
+    e = fmaf(f.x, g.x, fmaf(f.y, g.y, fmaf(f.z, g.z, fmaf(f.w, g.w, e))));
+  }
+  // 32 lanes hold a row of 128: the second head's are the upper ones
+  const int together = p.together;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) e += __shfl_xor_sync(0xffffffffu, e, o);
+  const float other = __shfl_xor_sync(0xffffffffu, e, 16);
+  if (together == 1) e += other;
+  __shared__ float upper[kDecayWarps];
+  if (threadIdx.x % 32 == 0) sums[threadIdx.x / 32] = e, upper[threadIdx.x / 32] = other;
+  __syncthreads();
+  const long long group = blockIdx.x / p.marks;
+  const int m = (int)(blockIdx.x - group * p.marks), groups = (p.H + together - 1) / together;
+  const int n = (int)(group / groups), h = (int)(group - (long long)n * groups) * together + threadIdx.x;
+  if (threadIdx.x < together && h < p.H) {
+    float z = 0.0f;
+    for (int w = 0; w < kDecayWarps; ++w) z += threadIdx.x == 0 ? sums[w] : upper[w];
+    p.between[((long long)n * p.H + h) * p.marks + m] = z;
+  }
+}
+
 __global__ void __launch_bounds__(kDecayThreads) attn_decay_kernel(AttnDecayParams p) {
-  __shared__ Exact sums[4][kDecayWarps];
+  __shared__ Exact sums[2][kDecayWarps];
   previous_done();
   next_may_start();
   const long long head = blockIdx.x / p.tiles;
   const int tile = (int)(blockIdx.x - head * p.tiles), h = (int)(head % p.H), n = (int)(head / p.H);
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int L = row_length(p.lens, n, p.S), begin = min(tile * kDecayTile, L);
+  const int L = row_length(p.lens, n, p.S), begin = tile * kDecayTile, end = min(begin + kDecayTile, L), steps = end - begin;
   float* out = static_cast<float*>(p.dDecay.p) + n * p.dDecay.ns + h;
   const float* g = static_cast<const float*>(p.decay.p) + n * p.decay.ns + h;
   const float* to = p.to + head * p.S;
   const float* of = p.of + head * p.S;
   const float bias = p.bias ? p.bias[h] : 0.0f;
-  const float first = p.first ? p.first[head] : 0.0f, last = p.last ? p.last[head] : 0.0f;
-  // the thread's own steps, and what is in the tile before each; all that is before the tile; all from it on
-  const int t0 = begin + threadIdx.x * kDecayEach;
-  float d[kDecayEach];
-  Exact own[kDecayEach], x = kNothing, before = kNothing, rest = kNothing;
-#pragma unroll
-  for (int i = 0; i < kDecayEach; ++i) d[i] = t0 + i < L && p.decay.p ? g[(t0 + i) * p.decay.ss] : 0.0f;
-#pragma unroll
-  for (int i = 0; i < kDecayEach; ++i) {
-    own[i] = x;
-    if (t0 + i < L) x.add(of[t0 + i]), x.add(-to[t0 + i]);
-  }
-  for (int t = threadIdx.x; t < begin; t += kDecayThreads) before.add(of[t]), before.add(-to[t]);
-  for (int t = begin + threadIdx.x; t < L; t += kDecayThreads) rest.add(of[t]), rest.add(-to[t]);
-  const Exact scan = pair_scan(x, 32);
-  before = pair_sum(before, 32), rest = pair_sum(rest, 32);
-  if (lane == 31) sums[0][warp] = before, sums[1][warp] = rest, sums[2][warp] = scan;
-  __syncthreads();
-  before = pair_sum(sums[0][lane % kDecayWarps], kDecayWarps);
-  rest = pair_sum(sums[1][lane % kDecayWarps], kDecayWarps);
-  const Exact warps = pair_scan(sums[2][lane % kDecayWarps], kDecayWarps);
-  Exact base = {__shfl_sync(0xffffffffu, warps.hi, max(warp - 1, 0)), __shfl_sync(0xffffffffu, warps.lo, max(warp - 1, 0))};
-  if (warp == 0) base = kNothing;
-  Exact lanes = {__shfl_up_sync(0xffffffffu, scan.hi, 1), __shfl_up_sync(0xffffffffu, scan.lo, 1)};
-  if (lane == 0) lanes = kNothing;
-  Exact left = -before;
-  left.add(-rest), left.add(last), left.add(-first);
-  const float back = L > 0 ? left.value() / (float)L : 0.0f;
-  base.add(lanes), base.add(before), base.add(first);
   Exact total = kNothing;
-  if (begin == tile * kDecayTile) {
+  if (steps > 0) {
+    const float* between = p.between + head * p.marks;
+    const float first = tile > 0 ? between[tile - 1] : p.first ? p.first[head] : 0.0f;
+    const float last = end < L ? between[tile] : p.last ? p.last[head] : 0.0f;
+    // the thread's own steps, and what comes before each
+    const int t0 = begin + threadIdx.x * kDecayEach;
+    float d[kDecayEach];
+    Exact own[kDecayEach], x = kNothing;
+#pragma unroll
+    for (int i = 0; i < kDecayEach; ++i) d[i] = t0 + i < end && p.decay.p ? g[(t0 + i) * p.decay.ss] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < kDecayEach; ++i) {
+      own[i] = x;
+      if (t0 + i < end) x.add(of[t0 + i]), x.add(-to[t0 + i]);
+    }
+    const Exact scan = pair_scan(x, 32);
+    if (lane == 31) sums[0][warp] = scan;
+    __syncthreads();
+    const Exact warps = pair_scan(sums[0][lane % kDecayWarps], kDecayWarps);
+    auto of_warp = [&](int w) { return Exact{__shfl_sync(0xffffffffu, warps.hi, w), __shfl_sync(0xffffffffu, warps.lo, w)}; };
+    Exact left = -of_warp(kDecayWarps - 1), base = of_warp(max(warp - 1, 0));
+    if (warp == 0) base = kNothing;
+    Exact lanes = {__shfl_up_sync(0xffffffffu, scan.hi, 1), __shfl_up_sync(0xffffffffu, scan.lo, 1)};
+    if (lane == 0) lanes = kNothing;
+    left.add(last), left.add(-first);
+    const float back = left.value() / (float)steps;
+    base.add(lanes), base.add(first);
 #pragma unroll
     for (int i = 0; i < kDecayEach; ++i) {
       const int t = t0 + i;
-      if (t < L) {
+      if (t < end) {
         Exact y = base;
-        y.add(own[i]), y.add(back * (float)t);
+        y.add(own[i]), y.add(back * (float)(t - begin));
         // a decay of 0 has no gradient: the factor itself is in it
         const float z = d[i] + bias < -104.0f ? 0.0f : y.value();
         if (p.dDecay.p) out[t * p.dDecay.ss] = z;
@@ -252,13 +283,13 @@ __global__ void __launch_bounds__(kDecayThreads) attn_decay_kernel(AttnDecayPara
     }
   }
   if (p.dDecay.p)
-    for (int t = tile * kDecayTile + threadIdx.x; t < min((tile + 1) * kDecayTile, p.S); t += kDecayThreads)
+    for (int t = begin + threadIdx.x; t < min(begin + kDecayTile, p.S); t += kDecayThreads)
       if (t >= L) out[t * p.dDecay.ss] = 0.0f;
   if (p.partial) {
     total = pair_sum(total, 32);
-    if (lane == 0) sums[3][warp] = total;
+    if (lane == 0) sums[1][warp] = total;
     __syncthreads();
-    total = pair_sum(sums[3][lane % kDecayWarps], kDecayWarps);
+    total = pair_sum(sums[1][lane % kDecayWarps], kDecayWarps);
     if (threadIdx.x == 0) p.partial[blockIdx.x] = (double)total.hi + (double)total.lo;
   }
 }
@@ -324,10 +355,12 @@ cudaError_t take_attn_status(cudaStream_t s, int* to) {
   return cudaSuccess;
 }
 
+int attn_together(int key_size, int value_size) { return key_size <= 64 && value_size <= 64 ? 2 : 1; }
+
 namespace {
-// States that run side by side: two heads of at most 64 elements share a block.
+// States that run side by side.
 long long streams_of(long long batch, long long heads, int key_size, int value_size, int passes) {
-  const int together = key_size <= 64 && value_size <= 64 ? 2 : 1;
+  const int together = attn_together(key_size, value_size);
   return passes * batch * ((heads + together - 1) / together);
 }
 }  // namespace
@@ -346,6 +379,7 @@ AttnPlan attn_plan(long long seq, long long batch, long long heads, int key_size
   plan.segments = plan.per > 0 ? (int)((chunks + plan.per - 1) / plan.per) : 1;
   // a gradient's passes contract over keys or values
   plan.deep = std::max(key_size, passes > 1 ? value_size : 0) > 64 ? 128 : 64;
+  plan.marks = chunks > 0 ? (int)((chunks - 1) / kMarkChunks) : 0;
   return plan;
 }
 
@@ -362,7 +396,15 @@ cudaError_t launch_attn_decay(AttnDecayParams p, cudaStream_t s, int* launches) 
   p.tiles = attn_decay_tiles(p.S);
   const long long blocks = (long long)p.N * p.H * p.tiles;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  cudaError_t e = launch_chained(attn_decay_kernel, (unsigned)blocks, kDecayThreads, 0, s, p);
+  cudaError_t e = cudaSuccess;
+  if (p.marks > 0) {
+    const long long at = (long long)p.N * ((p.H + p.together - 1) / p.together) * p.marks;
+    if (at > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    e = launch_chained(attn_mark_kernel, (unsigned)at, kDecayThreads, 0, s, p);
+    if (e != cudaSuccess) return e;
+    ++*launches;
+  }
+  e = launch_chained(attn_decay_kernel, (unsigned)blocks, kDecayThreads, 0, s, p);
   if (e != cudaSuccess) return e;
   ++*launches;
   if (p.dbias == nullptr) return e;

@@ -59,6 +59,7 @@ struct AttnPass {
   RowsArg dot_with;            // rows like o's: their products with the unrounded o
   float* dot;                  // [N][H][S], or null
   float* o32;                  // [N * S][H][V] in o's place: heads that share are added up from there
+  float* marks;                // [streams of the pass][marks][deep][128], or null: the states at every kMarkChunks-th chunk's start
 };
 // How a call's sequences are cut: pieces that run side by side where there are
 // too few states to fill the card, and what each adds to the state.
@@ -66,9 +67,13 @@ struct AttnPlan {
   int segments, per;  // pieces of a sequence, and the chunks of 64 steps in each
   int deep;           // elements that a kernel's states have along q and k: 64 or 128
   int vec;            // rows take 16-byte pieces
+  int marks;          // of a sequence, where a gradient's decays are wanted
   float* states;      // [streams][segments][deep][128]
   float* left;        // [streams][segments][2][2]: logarithms (base 2) of what a piece leaves of its first state
 };
+// Chunks between two of the states at which the decays' gradient is taken
+// from the state and its gradient themselves.
+constexpr int kMarkChunks = 8;
 struct AttnParams {
   int dtype;
   int S, N, H;
@@ -84,6 +89,8 @@ struct AttnParams {
 // steps and 12, against one chunk: 1 batch row 12.4 and 14.5 us against 12.4,
 // 64 batch rows 51 and 66 us against 72; float32 against 18.6 and 119 us.
 constexpr int kAttnSteps = 12;
+// Heads that share a block.
+int attn_together(int key_size, int value_size);
 // The plan of `passes` passes, its pointers left out; and the floats of its scratch.
 AttnPlan attn_plan(long long seq, long long batch, long long heads, int key_size, int value_size, int passes);
 long long attn_plan_scratch(const AttnPlan& plan, long long batch, long long heads, int key_size, int value_size,
@@ -111,6 +118,9 @@ struct AttnDecayParams {
   const float* of;
   const float* first;  // [N][H], or null: the state's product with its gradient before the first step
   const float* last;   // and behind the last
+  const float* states; // at the marks, the two passes' one after the other, and [N][H][marks] their products
+  float* between;
+  int marks, deep, together;  // heads that share a block
   double* partial;     // [N][H][tiles]
   float* dbias;        // [H], or null
   int tiles;           // set by the launch

@@ -116,8 +116,8 @@ RowsArg decay_rows(Call& c, const char* name, const rk_rows& t, const rk_attn_pr
 // What a gradient needs: its passes' products for the decays, and float32
 // outputs where heads share.
 struct GradPlan {
-  int64_t to, of, cross, partial, q32, k32, v32, chunks;
-  int64_t total() const { return to + of + cross + partial + q32 + k32 + v32 + chunks; }
+  int64_t to, of, cross, partial, q32, k32, v32, between, marks, chunks;  // marks: of one pass
+  int64_t total() const { return to + of + cross + partial + q32 + k32 + v32 + between + 2 * marks + chunks; }
 };
 rk::AttnPlan plan_of(const rk_attn_problem* p, int passes) {
   return rk::attn_plan(p->seq, p->batch, p->heads, (int)p->key_size, (int)p->value_size, passes);
@@ -142,6 +142,10 @@ GradPlan grad_plan(const rk_attn_problem* p) {
   if (shared(p->heads, p->query_heads) > 1) g.q32 = four(rows * p->key_size);
   if (shared(p->heads, p->key_heads) > 1) g.k32 = four(rows * p->key_size);
   if (shared(p->heads, p->value_heads) > 1) g.v32 = four(rows * p->value_size);
+  const rk::AttnPlan plan = plan_of(p, 3);
+  const int together = rk::attn_together((int)p->key_size, (int)p->value_size);
+  g.between = four(heads * plan.marks);
+  g.marks = p->batch * ((p->heads + together - 1) / together) * plan.marks * plan.deep * 128;
   g.chunks = plan_scratch(p, 3);
   return g;
 }
@@ -297,6 +301,7 @@ rk_status rk_attn_grad_encode(rk_handle* h, const rk_attn_problem* p, const rk_a
   const bool decays = dDecay.p || dbias;
   float *to = w, *of = to + g.to, *cross = of + g.of, *partial = cross + g.cross;
   float *q32 = partial + g.partial, *k32 = q32 + g.q32, *v32 = k32 + g.k32;
+  float *between = v32 + g.v32, *marks = between + g.between;
 
   // dQ: the rows that wrote the state, read by dY
   auto next = [&]() -> rk::AttnPass& { return ap.pass[ap.passes++]; };
@@ -307,6 +312,7 @@ rk_status rk_attn_grad_encode(rk_handle* h, const rk_attn_problem* p, const rk_a
     a.K = dv, a.V = dk, a.su = 1.0f, a.so = p->scale, a.v_major = 1;
     a.first = first;
     if (decays) a.dot = to, a.dot_with = Q;
+    if (decays && g.marks) a.marks = marks;
     if (decays && dlast) a.with = dlast, a.cross = cross + heads;
     if (q_of > 1 && dQ.p) a.o32 = q32;
   }
@@ -327,13 +333,14 @@ rk_status rk_attn_grad_encode(rk_handle* h, const rk_attn_problem* p, const rk_a
     a.K = dv, a.V = dk, a.su = p->scale, a.so = 1.0f, a.backward = 1, a.v_major = 1;
     a.first = dlast;
     if (decays) a.dot = of, a.dot_with = K;
+    if (decays && g.marks) a.marks = marks + g.marks;
     if (decays && first) a.with = first, a.cross = cross;
     if (k_of > 1 && dK.p) a.o32 = k32;
   }
   int launches = 0;
   if (ap.passes) {
     ap.plan = plan_of(p, 3);
-    place(ap.plan, v32 + g.v32, g.chunks);
+    place(ap.plan, marks + 2 * g.marks, g.chunks);
     ap.plan.vec = Q.vec && K.vec && V.vec && dY.vec;
     h->attn_chunks = true;
     c.cuda("launch", rk::launch_attn_chunks(ap, s, &launches));
@@ -344,6 +351,8 @@ rk_status rk_attn_grad_encode(rk_handle* h, const rk_attn_problem* p, const rk_a
     d.decay = ap.decay, d.bias = ap.bias, d.dDecay = dDecay;
     d.to = to, d.of = of, d.dbias = dbias;
     d.first = first ? cross : nullptr, d.last = dlast ? cross + heads : nullptr;
+    d.states = marks, d.between = between, d.marks = ap.plan.marks, d.deep = ap.plan.deep;
+    d.together = rk::attn_together(dk, dv);
     d.partial = dbias ? reinterpret_cast<double*>(partial) : nullptr;
     c.cuda("launch", rk::launch_attn_decay(d, s, &launches));
   }

@@ -1046,6 +1046,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
         y[2 * x] = z.x, y[2 * x + 1] = z.y;
       }
     };
+    // The state at the start of chunk c, where the decays' gradient wants it.
+    auto mark = [&](int c) {
+      if (NT != kTerms || !a.marks || c == 0 || c % kMarkChunks != 0) return;  // gradients have all terms
+      float* to = a.marks + ((long long)(at.stream - at.pass * p.N * ((p.H + HPC - 1) / HPC)) * p.plan.marks + c / kMarkChunks - 1) * kept;
+#pragma unroll 1
+      for (int j = 0; j < NH; j += 16) {
+        float y[16];
+        one_state(j, y);
+#pragma unroll
+        for (int x = 0; x < 16; ++x) to[(k0 + j + x) * 128 + r] = j + x < elements ? y[x] : 0.0f;
+      }
+    };
     int meetings = 0;
     // Chunk i step by step, from the operands themselves.
     auto by_step = [&](int i) {
@@ -1074,6 +1086,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
       if (count > 0) {
         prepare(0);
         arrive(ready(0).bar);
+        if (!back) mark(c_begin);
         if (!TMA && Lay::kStages == 2 && count > 1) fetch(1);
       }
 #pragma unroll 1
@@ -1098,6 +1111,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
           arrive(ready(i + 1).bar);
           if (!TMA && Lay::kStages == 2 && i + 2 < count) fetch(i + 2);
         }
+        if (back || more) mark(back ? chunk_at(i) : chunk_at(i + 1));
       }
       if (order == segments - 1 && (a.last || a.with)) {
         float with = 0.0f;
