@@ -573,8 +573,8 @@ typedef struct rk_attn_operands {
  * added up before the one rounding), dDecay (float32 rows of `heads`
  * elements), d_decay_bias, d_initial_state and the optional input
  * d_final_state are float32.  dDecay is taken from running sums over
- * the sequence of what queries and keys contribute, in pairs of float32: where
- * it is far smaller than those contributions it has their float32 accuracy.
+ * 512 steps of what queries and keys contribute, in pairs of float32: where it
+ * is far smaller than those contributions it has their float32 accuracy.
  * Infinities and NaN in an operand may reach the gradients of any step of
  * their batch row. */
 typedef struct rk_attn_grad_operands {

