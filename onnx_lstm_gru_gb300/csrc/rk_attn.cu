@@ -150,7 +150,7 @@ cudaError_t launch_steps(const AttnParams& p, cudaStream_t s) {
 // between two marks; the sums are pairs of float32 that keep what each addition
 // rounds away (Knuth's two-sum), as the card has few float64 units and the kernel
 // is a chain of sums, bound by their latency (128 heads of 512 steps 11.8 us with
-// float64, 4.7 so).
+// float64, 6.7 so).
 constexpr int kDecayThreads = 256, kDecayWarps = kDecayThreads / 32, kDecayEach = 2, kDecayTile = kDecayThreads * kDecayEach;
 static_assert(kDecayTile == kMarkChunks * 64, "a block's steps are those between two marks");
 struct Exact {
@@ -204,10 +204,13 @@ __global__ void __launch_bounds__(kDecayThreads) attn_mark_kernel(AttnDecayParam
   const float4* x = reinterpret_cast<const float4*>(p.states + (long long)blockIdx.x * p.deep * 128);
   const float4* y = reinterpret_cast<const float4*>(p.states + all + (long long)blockIdx.x * p.deep * 128);
   float e = 0.0f;
-#pragma unroll 8
-  for (int i = threadIdx.x; i < p.deep * 32; i += kDecayThreads) {
-    const float4 f = x[i], g = y[i];
-    e = fmaf(f.x, g.x, fmaf(f.y, g.y, fmaf(f.z, g.z, fmaf(f.w, g.w, e))));
+#pragma unroll 1
+  for (int i0 = threadIdx.x; i0 < p.deep * 32; i0 += 8 * kDecayThreads) {  // 64 rows at a time
+    float4 f[8], g[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = x[i0 + i * kDecayThreads], g[i] = y[i0 + i * kDecayThreads];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e = fmaf(f[i].x, g[i].x, fmaf(f[i].y, g[i].y, fmaf(f[i].z, g[i].z, fmaf(f[i].w, g[i].w, e))));
   }
   // 32 lanes hold a row of 128: the second head's are the upper ones
   const int together = p.together;
