@@ -1479,8 +1479,10 @@ cudaError_t launch_chunks_in(const ChunkArgs& args, cudaStream_t s, int* launche
   // every pass has the same two sizes, in one order or the other
   const AttnParams& p = args.p;
   if (p.pass[0].K <= 64 && p.pass[0].V <= 64) return launch_chunks_of<T, 2, 1, NT, TMA>(args, s, launches);
-  return p.plan.deep == 64 ? launch_chunks_of<T, 1, 1, NT, TMA>(args, s, launches)
-                           : launch_chunks_of<T, 1, 2, NT, TMA>(args, s, launches);
+  // 16-bit rows have all terms in gradients alone, whose states are as deep as the larger size
+  if constexpr (NT != kTerms || kSplit<T> == kTerms)
+    if (p.plan.deep == 64) return launch_chunks_of<T, 1, 1, NT, TMA>(args, s, launches);
+  return launch_chunks_of<T, 1, 2, NT, TMA>(args, s, launches);
 }
 
 // P and the state as three terms where float32 comes of them: for float32
