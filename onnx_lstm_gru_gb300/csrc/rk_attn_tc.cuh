@@ -51,7 +51,7 @@
 // What bounds it are the warps' own instructions and their waits for each
 // other, not the products or HBM: 512 x 64 x 16 heads of 64, bf16, 111 us (2.6
 // TB/s, 2.2 warp instructions a clock and multiprocessor, the tensor pipe 30 %
-// busy); the gradient of 512 x 8 x 16 heads of 128 137 us (2.2, 21 %); 777 x 8 x 10
+// busy); the gradient of 512 x 8 x 16 heads of 128 136 us (2.2, 21 %); 777 x 8 x 10
 // heads of 72 x 103 in float32, 80 blocks, 106 us (1.7, 25 %).  Step by step the
 // three take 2316, 2319 and 646 us.
 #pragma once
@@ -625,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
   }
   // The states that are read at either end are on their way from HBM: a gradient of 6 x 8 x 4 heads of 128 with
   // states 19 us, 35 without this and with single elements of those that lie along the lanes' way.
-  if (OUT) {
+  if (OUT && (a.first || a.with)) {
     const long long from = ((long long)at.n * p.H + at.h0) * a.K * a.V;
     const int many = min(HPC, p.H - at.h0) * a.K * a.V;
     for (int i = tid * 32; i < many; i += kThreads * 32) {
