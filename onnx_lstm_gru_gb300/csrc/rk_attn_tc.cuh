@@ -124,13 +124,22 @@ enum Bar {
   kGotS, kGotU, kGotOi = kGotU + 2, kGotO, kFull = kGotO + 2, kWith = kFull + 2, kStored, kDecay, kBars = kDecay + 3
 };
 
+// Chunks' flags take turns.  Two heads' decay warps may each set one, and the
+// first head's clears the flag of chunk i + kClear while it is at chunk i.  Nobody
+// sets that flag before: the second head's warp comes to a chunk once the one
+// three before it is done, for which both heads' decays have been taken, and the
+// others wait for the chunk's own decays.  Nobody still reads it for chunk i +
+// kClear - kFlags, eleven back: all but the copying warp have read a chunk's flag
+// when it is done (three back), and that one reads it before it fetches the next
+// chunk's tiles but two.
+constexpr int kFlags = 16, kClear = 5;
 struct Small {
   __align__(16) Decays decays[3][2];
   float dots[2][kGroupWarps][kCols];  // of a chunk and the one before
   float part[2][128];
   uint64_t bars[kBars];
   uint32_t tmem;
-  int bad[8];  // chunks to be run step by step
+  int bad[kFlags];  // chunks to be run step by step
   volatile int gave_up;
 };
 
@@ -620,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
       bar_init(su32(&sh.bars[i]), n);
     }
     sh.gave_up = 0;
-    for (int i = 0; i < 8; ++i) sh.bad[i] = 0;
+    for (int i = 0; i < kFlags; ++i) sh.bad[i] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   // The states that are read at either end are on their way from HBM: a gradient of 6 x 8 x 4 heads of 128 with
@@ -694,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
     wait_for(decayed(i));
     F2 finite = zero;
     scale_tile<T, HPC, kSubs>(tiles + Lay::kK, sm + scaled_of(i), sh.decays[i % 3], finite);
-    if (!is_finite(finite)) sh.bad[i & 7] = 1;
+    if (!is_finite(finite)) sh.bad[i % kFlags] = 1;
   };
 
   if (warp < kGroupWarps) {
@@ -716,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
           }
         }
         prepare(i);
-        if (!tile_finite<kGroup>(sm + stage_of(i) + Lay::kV, tid)) sh.bad[i & 7] = 1;
+        if (!tile_finite<kGroup>(sm + stage_of(i) + Lay::kV, tid)) sh.bad[i % kFlags] = 1;
         arrive(ready(i).bar);
       }
     } else {
@@ -768,7 +777,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
 #pragma unroll
           for (int e = 0; e < NT; ++e) *reinterpret_cast<uint4*>(to + e * Lay::kPTerm) = make_uint4(w[e][0], w[e][1], w[e][2], w[e][3]);
         }
-        if (!is_finite(finite)) sh.bad[i & 7] = 1;
+        if (!is_finite(finite)) sh.bad[i % kFlags] = 1;
       };
       Rows<T, HPC> rq(a.q, at.n, at.h0, p.H, a.q_of, a.K, t_first, step);
       auto fetch = [&](int i) {
@@ -786,9 +795,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
         if (HPC == 2 || quarter < 2) pairs(i);
         if (TMA) wait_for(full(i));  // V, of the copies' own making
         // with one head S has rows for two quarters of the lanes; the others look V over
-        if (HPC == 2 && !tile_finite<kGroup>(sm + stage_of(i) + Lay::kV, tid)) sh.bad[i & 7] = 1;
+        if (HPC == 2 && !tile_finite<kGroup>(sm + stage_of(i) + Lay::kV, tid)) sh.bad[i % kFlags] = 1;
         if (HPC == 1 && quarter >= 2 && !tile_finite<kGroup / 2>(sm + stage_of(i) + Lay::kV, (part * 2 + (quarter & 1)) * 32 + lane))
-          sh.bad[i & 7] = 1;
+          sh.bad[i % kFlags] = 1;
         arrive(paired(i).bar);
         if (!TMA && i + Lay::kStages < count) {
           wait(kGotOi, i);
@@ -903,7 +912,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
         }
         wait_for(got_o(i));
         if (!TMA && i + Lay::kStages < count) fetch(i + Lay::kStages);
-        if (!sh.bad[i & 7]) outputs(i);
+        if (!sh.bad[i % kFlags]) outputs(i);
         else if (TMA && a.dot) wait(kWith, i);  // the copies are not left behind
         arrive(done(i).bar);
       }
@@ -976,7 +985,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
     };
     auto wrote = [&](F2 finite, int i) {
       tmem_st_done();
-      if (OUT && mine && !is_finite(finite)) sh.bad[i & 7] = 1;
+      if (OUT && mine && !is_finite(finite)) sh.bad[i % kFlags] = 1;
     };
     // Elements j .. j + 15 of the `there` that there are of a state, `far` apart; side by side in pieces of four.
     auto read16 = [&](const float* from, int j, int far, int there, float (&y)[16]) {
@@ -1099,7 +1108,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
         wait_for(paired(i));  // all of the chunk's flags are set
         wait(kGotOi, i);
         if (more) wait_for(decayed(i + 1));
-        if (__builtin_expect(!sh.bad[i & 7], 1)) advance(i);
+        if (__builtin_expect(!sh.bad[i % kFlags], 1)) advance(i);
         else by_step(i);
         arrive(done(i).bar);
         if (more) {
@@ -1141,7 +1150,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
 #pragma unroll 1
       for (int i = 0; i < count; ++i) {
         wait_for(got_u(i));
-        if (__builtin_expect(!sh.bad[i & 7], 1)) advance(i);
+        if (__builtin_expect(!sh.bad[i % kFlags], 1)) advance(i);
         else by_step(i);
         // what has left nothing leaves nothing: 64 bits hold a thousandfold of that
         left = max(left + sh.decays[i % 3][head].log2, -(1LL << 45));
@@ -1219,7 +1228,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
         const uint64_t dp = smem_desc_sw128(Lay::kOver ? tiles + Lay::kK : su32(sm) + Lay::kP);
         const uint32_t to = tmem + (apart ? kS : kOi);
         if (leader) {
-          if (!sh.bad[i & 7])
+          if (!sh.bad[i % kFlags])
             products<kIn, NT, NT, 4>([&](int x, int y, int s, uint32_t more) {
               tc_mma(to, dv + ((x * kTile + s * 2048) >> 4), dp + ((y * Lay::kPTerm + s * 32) >> 4), idesc_of(64 * HPC) | kRowsA,
                      apart ? more : 1u);
@@ -1288,7 +1297,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
           }
           wait_for(done(i));
           if (OUT && a.dot) wait(kWith, i);  // also where nobody has read it
-          const bool good = !sh.bad[i & 7] && !sh.gave_up;
+          const bool good = !sh.bad[i % kFlags] && !sh.gave_up;
           if (!early && i + 2 < count && !sh.gave_up) load(i + 2);
           if (OUT && leader) {
             if (out && good) {
@@ -1325,8 +1334,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
           if (i + 1 < count) x0 = read(i + 1, 0), x1 = read(i + 1, 1);
           const bool bad = chunk_decays(a, y0, y1, sh.decays[i % 3][x]);
           if (lane == 0) {
-            if (x == 0) sh.bad[(i + 2) & 7] = 0;  // read last for chunk i - 6
-            if (bad) sh.bad[i & 7] = 1;
+            if (x == 0) sh.bad[(i + kClear) % kFlags] = 0;
+            if (bad) sh.bad[i % kFlags] = 1;
           }
           __syncwarp();
           if (lane == 0) bar_arrive(su32(&sh.bars[decayed(i).bar]));
