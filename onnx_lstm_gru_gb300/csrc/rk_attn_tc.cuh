@@ -831,8 +831,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
         const Decays* dec = sh.decays[i % 3];
         const bool mild = mild_of(i), dot = a.dot, wide = a.o32, any = a.o.p;
         const int t0 = chunk_at(i) * kChunk + part * kCols;
-        if (TMA && i > 0) wait(kStored, i - 1);
-        if (TMA && dot) wait(kWith, i);
         float next[8];
         tmem_ld(lanes + kOi + ocol, next);
 #pragma unroll 1
@@ -912,8 +910,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
         }
         wait_for(got_o(i));
         if (!TMA && i + Lay::kStages < count) fetch(i + Lay::kStages);
+        // the chunk before is on its way out of the tile, this one's factors are there; also where neither is used,
+        // as a barrier's phases have to be waited for one by one
+        if (TMA && i > 0) wait(kStored, i - 1);
+        if (TMA && a.dot) wait(kWith, i);
         if (!sh.bad[i % kFlags]) outputs(i);
-        else if (TMA && a.dot) wait(kWith, i);  // the copies are not left behind
         arrive(done(i).bar);
       }
       if (a.dot && count > 0) {

@@ -3,7 +3,7 @@ step by step beside others.  Inputs, checks and tolerances are those of
 ``test_linear_attention_gpu.py`` where a test does not state its own."""
 import pytest
 
-from test_linear_attention_gpu import DTYPES, Case, cut, layer  # noqa: F401  (layer: the fixture)
+from test_linear_attention_gpu import DTYPES, Case, check, cut, layer, same_bits  # noqa: F401  (layer: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -20,3 +20,22 @@ def test_attn_decays_that_are_none_in_the_second_head(layer, N, S, H, dtype):
         assert cut(c) == (N == 1)
         c.t["Decay"][:, at, 1::2] = float("nan")
         c.compare(layer.attn(c.p, **c.t), f"{at}")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("sizes", [(64, 64), (128, 128), (64, 128)])
+def test_attn_every_second_chunk_step_by_step(layer, sizes, dtype):
+    """Chunks whose products of queries and keys pass float32's range lie
+    between ones where they do not; each is compared by itself, as the others'
+    outputs are far larger, and equal calls give equal bits."""
+    c = Case(450, 4, 2, *sizes, dtype, ragged=False, layout=1, state=False)
+    for a in (64, 192, 320):
+        c.t["Q"][:, a:a + 64] *= 1e20
+        c.t["K"][:, a:a + 64] *= 1e20
+        c.t["V"][:, a:a + 64] *= 1e-22
+    got, want = layer.attn(c.p, **c.t), c.reference()
+    check(got["final_state"], want["final_state"], "final_state")
+    for a in range(0, 450, 64):
+        check(got["Y"][:, a:a + 64], want["Y"][:, a:a + 64], f"Y {a}")
+    for _ in range(10):
+        same_bits(got, layer.attn(c.p, **c.t))
