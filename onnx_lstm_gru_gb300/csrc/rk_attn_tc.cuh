@@ -25,10 +25,10 @@
 // comes of them, which keeps less than their 2^-17.  Differences of G are exact to 2^-24: sums
 // are 64-bit whole numbers of 2^-32, kept as whole part and fraction.
 //
-// Where a chunk's decays (and the scale) stay within 2^-100, P_mn 2^-G_m is S_mn 2^-G_n: then
-// no power is taken for each pair, and O is added to Oi before 2^G_m scales
-// both.  (Backward the same from the chunk's end.)  Chunks that decay further
-// take the powers pair by pair and keep the two apart.
+// Where a chunk's decays (and the scale) stay between 2^-80 and 2^20, P_mn 2^-G_m is
+// S_mn 2^-G_n: then no power is taken for each pair, and O is added to Oi before
+// 2^G_m scales both.  (Backward the same from the chunk's end.)  Chunks that decay
+// or grow further take the powers pair by pair and keep the two apart.
 //
 // A block runs one state (two, stacked along the lanes, where heads have at
 // most 64 elements: of the products' 128 x 128 blocks the diagonal ones are
@@ -44,9 +44,12 @@
 // O_i follows P_i; S_(i+1) and U_(i+1) follow ck K; Oi_(i+1) follows the
 // outputs of i.
 //
-// Infinities and NaN must not reach other steps through the products' zeros:
-// a chunk in which an operand, a product of P or the state is not finite is
-// run step by step instead.
+// Infinities and NaN must not reach other steps through the products' zeros, and
+// sums that are scaled down once they are complete must not pass float32's range
+// before.  So a chunk is run step by step instead where a product of P, a scaled
+// key or an element of the state is 2^100 or more (looked at while they are split
+// into terms; from 2^94 on at the earliest), or an element of the queries or values
+// 2^20 or more: below that O + Oi is at most 64 + 128 products of 2^120, and U 64.
 //
 // What bounds it are the warps' own instructions and their waits for each
 // other, not the products or HBM: 512 x 64 x 16 heads of 64, bf16, 111 us (2.6
@@ -146,14 +149,16 @@ struct Small {
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) { return Elem<__nv_bfloat16>::pair_from_f(lo, hi); }
 __device__ __forceinline__ F2 pair_of(uint32_t u) { return f2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)); }
 
-// Two factors as N terms each; the first terms' product with 0 goes to
-// `finite`, which they leave 0 unless one of them is infinite or NaN.
+// Two factors as N terms each; the first terms are added to `sum` 2^29 times,
+// which stays finite only while all of them are below 2^100 (one of 2^100 alone is
+// 2^129, and what has been added up is not below -2^128).
+constexpr float kFar = 536870912.0f;
 template <int N>
-__device__ __forceinline__ void split(F2 x, uint32_t (&t)[N], F2& finite) {
+__device__ __forceinline__ void split(F2 x, uint32_t (&t)[N], F2& sum) {
   float2 v = f2_get(x);
   t[0] = pack2(v.x, v.y);
   F2 h = pair_of(t[0]);
-  finite = fma2(h, f2(0.0f, 0.0f), finite);
+  sum = fma2(h, f2(kFar, kFar), sum);
 #pragma unroll
   for (int i = 1; i < N; ++i) {
     x = fma2(h, f2(-1.0f, -1.0f), x);
@@ -162,9 +167,9 @@ __device__ __forceinline__ void split(F2 x, uint32_t (&t)[N], F2& finite) {
     if (i + 1 < N) h = pair_of(t[i]);
   }
 }
-__device__ __forceinline__ bool is_finite(F2 finite) {
-  const float2 v = f2_get(finite);
-  return v.x == 0.0f && v.y == 0.0f;
+__device__ __forceinline__ bool in_range(F2 sum) {
+  const float2 v = f2_get(sum);
+  return v.x - v.x == 0.0f && v.y - v.y == 0.0f;
 }
 
 template <int N>
@@ -324,7 +329,7 @@ __device__ __forceinline__ bool chunk_decays(const AttnPass& a, float x0, float 
   }
   const long long total = __shfl_sync(0xffffffffu, sum, 31);
   // the scale's power goes with the decays': together they stay in float32's range
-  const int limit = 100 - abs((int)(__float_as_uint(a.so * a.su) >> 23 & 255) - 127);
+  const int limit = 80 - abs((int)(__float_as_uint(a.so * a.su) >> 23 & 255) - 127);
   bool mild = true;
 #pragma unroll 1
   for (int j = 0; j < 2; ++j) {
@@ -334,7 +339,7 @@ __device__ __forceinline__ bool chunk_decays(const AttnPass& a, float x0, float 
     out.lo[i] = (float)((uint32_t)s >> 8) * 5.9604644775390625e-8f;
     const long long from = backward ? total - G : G;
     bad = bad || G >> 32 > 120 || (total - G) >> 32 > 120;
-    mild = mild && from >> 32 >= -limit && from >> 32 <= limit;
+    mild = mild && from >> 32 >= -limit && from >> 32 < min(limit, 20);
     const float up = pow2_of(G), down = pow2_of(total - G);
     out.cq[i] = a.so * (backward ? down : up);
     out.ck[i] = a.su * (backward ? up : down);
@@ -438,7 +443,7 @@ struct Rows {
 
 // ck K as three terms, by a group.
 template <typename T, int HPC, int SUBS>
-__device__ __forceinline__ void scale_tile(const unsigned char* k, unsigned char* out, const Decays* d, F2& finite) {
+__device__ __forceinline__ void scale_tile(const unsigned char* k, unsigned char* out, const Decays* d, F2& range) {
   constexpr int kIn = kSplit<T>;
   const int thread = threadIdx.x % kGroup;
 #pragma unroll 2
@@ -459,7 +464,7 @@ __device__ __forceinline__ void scale_tile(const unsigned char* k, unsigned char
 #pragma unroll
       for (int j = kIn - 2; j >= 0; --j) x = add2(x, pair_of(t[j][e]));
       uint32_t s[kTerms];
-      split<kTerms>(mul2(x, f2(f, f)), s, finite);
+      split<kTerms>(mul2(x, f2(f, f)), s, range);
 #pragma unroll
       for (int j = 0; j < kTerms; ++j) w[j][e] = s[j];
     }
@@ -469,18 +474,19 @@ __device__ __forceinline__ void scale_tile(const unsigned char* k, unsigned char
   }
 }
 
-// Whether a tile's first term is finite, by THREADS threads: the largest of
+// Whether a tile's first term is below 2^20, by THREADS threads: the largest of
 // the magnitudes as whole numbers, 16 bits each.
-template <int THREADS>
-__device__ __forceinline__ bool tile_finite(const unsigned char* tile, int thread) {
+constexpr uint32_t kMost = (127 + 20) << 7;
+template <int THREADS, int BYTES>
+__device__ __forceinline__ bool tile_in_range(const unsigned char* tile, int thread) {
   uint32_t top = 0;
-#pragma unroll 2
-  for (int i = 0; i < (int)kTile / 16 / THREADS; ++i) {
+#pragma unroll 4
+  for (int i = 0; i < BYTES / 16 / THREADS; ++i) {
     const uint4 u = *reinterpret_cast<const uint4*>(tile + (i * THREADS + thread) * 16);
     top = __vmaxu2(top, u.x & 0x7fff7fffu), top = __vmaxu2(top, u.y & 0x7fff7fffu);
     top = __vmaxu2(top, u.z & 0x7fff7fffu), top = __vmaxu2(top, u.w & 0x7fff7fffu);
   }
-  return (top & 0xffffu) < 0x7f80u && (top >> 16) < 0x7f80u;
+  return (top & 0xffffu) < kMost && (top >> 16) < kMost;
 }
 
 // One thread: the products of NA terms of A and NB of B down to 2^-8 NT,
@@ -673,6 +679,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
   auto arrive = [&](int bar) { arrive_bar(sh, bar); };
   auto stage_of = [&](int i) { return (Lay::kStages == 2 ? i & 1 : 0) * Lay::kStage; };
   auto scaled_of = [&](int i) { return Lay::kScaled + (OUT ? 0 : i & 1) * kTerms * kTile; };
+  // A chunk's tiles are there with the copies, but for the one whose last rows have to be cleared.
+  auto early = [&](int i) { return TMA && L - chunk_at(i) * kChunk >= kChunk; };
   auto mild_of = [&](int i) { return sh.decays[i % 3][0].mild && (HPC == 1 || sh.decays[i % 3][1].mild); };
 
   // the groups' lanes: a value of a head
@@ -701,9 +709,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
       }
     }
     wait_for(decayed(i));
-    F2 finite = zero;
-    scale_tile<T, HPC, kSubs>(tiles + Lay::kK, sm + scaled_of(i), sh.decays[i % 3], finite);
-    if (!is_finite(finite)) sh.bad[i % kFlags] = 1;
+    F2 range = zero;
+    scale_tile<T, HPC, kSubs>(tiles + Lay::kK, sm + scaled_of(i), sh.decays[i % 3], range);
+    if (!in_range(range)) sh.bad[i % kFlags] = 1;
   };
 
   if (warp < kGroupWarps) {
@@ -725,7 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
           }
         }
         prepare(i);
-        if (!tile_finite<kGroup>(sm + stage_of(i) + Lay::kV, tid)) sh.bad[i % kFlags] = 1;
+        if (!tile_in_range<kGroup, kTile>(sm + stage_of(i) + Lay::kV, tid)) sh.bad[i % kFlags] = 1;
         arrive(ready(i).bar);
       }
     } else {
@@ -738,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
         const Decays& d = sh.decays[i % 3][head];
         const bool mild = mild_of(i);
         const float hi = d.hi[m], lo = d.lo[m];
-        F2 finite = zero;
+        F2 range = zero;
         unsigned char* row = (Lay::kOver ? sm + Lay::kK : sm + Lay::kP) + (HPC == 2 ? r : m) * 128;
         float next[8];
         tmem_ld(lanes + kS + ocol, next);
@@ -769,7 +777,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
             y.x = (back ? 7 - j : j) <= last ? y.x : 0.0f;
             y.y = (back ? 6 - j : j + 1) <= last ? y.y : 0.0f;
             uint32_t t[NT];
-            split<NT>(f2(y.x, y.y), t, finite);
+            split<NT>(f2(y.x, y.y), t, range);
 #pragma unroll
             for (int e = 0; e < NT; ++e) w[e][j / 2] = t[e];
           }
@@ -777,7 +785,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
 #pragma unroll
           for (int e = 0; e < NT; ++e) *reinterpret_cast<uint4*>(to + e * Lay::kPTerm) = make_uint4(w[e][0], w[e][1], w[e][2], w[e][3]);
         }
-        if (!is_finite(finite)) sh.bad[i % kFlags] = 1;
+        if (!in_range(range)) sh.bad[i % kFlags] = 1;
       };
       Rows<T, HPC> rq(a.q, at.n, at.h0, p.H, a.q_of, a.K, t_first, step);
       auto fetch = [&](int i) {
@@ -790,14 +798,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
       for (int i = 0; i < count; ++i) {
         if (!TMA && i + Lay::kStages < count) rq.prefetch(L - chunk_at(i + Lay::kStages) * kChunk);
         wait_for(decayed(i));
+        // while S is on its way, and the product that P was written for: Q and V are looked over, with one head by the
+        // two quarters of the lanes that S has no rows for
+        if (HPC == 2 || quarter >= 2) {
+          constexpr int kLook = HPC == 2 ? kGroup : kGroup / 2;
+          const int thread = HPC == 2 ? tid : (part * 2 + (quarter & 1)) * 32 + lane;
+          if (early(i)) wait_for(full(i));
+          else wait_for(ready(i));
+          bool fine = tile_in_range<kLook, kTile>(sm + stage_of(i) + Lay::kV, thread);
+          // Half goes up to 2^16, and what is infinite makes P so
+          if constexpr (!std::is_same_v<T, __half>)
+            fine = tile_in_range<kLook, kSubs * kSub>(sm + stage_of(i) + Lay::kQ, thread) && fine;
+          if (!fine) sh.bad[i % kFlags] = 1;
+        }
         wait(kGotS, i);
         if (i > 0) wait_for(got_o(i - 1));  // which P was multiplied for
         if (HPC == 2 || quarter < 2) pairs(i);
-        if (TMA) wait_for(full(i));  // V, of the copies' own making
-        // with one head S has rows for two quarters of the lanes; the others look V over
-        if (HPC == 2 && !tile_finite<kGroup>(sm + stage_of(i) + Lay::kV, tid)) sh.bad[i % kFlags] = 1;
-        if (HPC == 1 && quarter >= 2 && !tile_finite<kGroup / 2>(sm + stage_of(i) + Lay::kV, (part * 2 + (quarter & 1)) * 32 + lane))
-          sh.bad[i % kFlags] = 1;
         arrive(paired(i).bar);
         if (!TMA && i + Lay::kStages < count) {
           wait(kGotOi, i);
@@ -961,13 +977,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
       }
     };
     // Elements j .. j + 15 to there, for chunk i.
-    auto write_state = [&](int j, const F2 (&H)[8], F2& finite) {
+    auto write_state = [&](int j, const F2 (&H)[8], F2& range) {
       if constexpr (OUT) {
         uint32_t w[NT][8];
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
           uint32_t s[NT];
-          split<NT>(H[x], s, finite);
+          split<NT>(H[x], s, range);
 #pragma unroll
           for (int y = 0; y < NT; ++y) w[y][x] = s[y];
         }
@@ -984,9 +1000,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
         tmem_st<16>(lanes + kF + k0 + j, w);
       }
     };
-    auto wrote = [&](F2 finite, int i) {
+    auto wrote = [&](F2 range, int i) {
       tmem_st_done();
-      if (OUT && mine && !is_finite(finite)) sh.bad[i % kFlags] = 1;
+      if (OUT && mine && !in_range(range)) sh.bad[i % kFlags] = 1;
     };
     // Elements j .. j + 15 of the `there` that there are of a state, `far` apart; side by side in pieces of four.
     auto read16 = [&](const float* from, int j, int far, int there, float (&y)[16]) {
@@ -1007,7 +1023,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
       const bool pieces = OUT && segments > 1;
       const float* from = pieces ? p.plan.states + ((long long)at.stream * segments + order) * kept + k0 * 128 + r : a.first + state;
       const int far = pieces ? 128 : apart, there = pieces ? NH : OUT && a.first ? elements : 0;
-      F2 finite = zero;
+      F2 range = zero;
 #pragma unroll 1
       for (int j = 0; j < NH; j += 16) {
         float y[16];
@@ -1015,14 +1031,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
         F2 H[8];
 #pragma unroll
         for (int x = 0; x < 8; ++x) H[x] = f2(y[2 * x], y[2 * x + 1]);
-        write_state(j, H, finite);
+        write_state(j, H, range);
       }
-      wrote(finite, 0);
+      wrote(range, 0);
     };
     // H = e H + U for chunk i, and its terms for the next.
     auto advance = [&](int i) {
       const float e = sh.decays[i % 3][head].total;
-      F2 finite = zero;
+      F2 range = zero;
 #pragma unroll 1
       for (int j = 0; j < NH; j += 16) {
         float u[16];
@@ -1032,9 +1048,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
         tmem_ld_done(u);
 #pragma unroll
         for (int x = 0; x < 8; ++x) H[x] = fma2(f2(e, e), H[x], f2(u[2 * x], u[2 * x + 1]));
-        write_state(j, H, finite);
+        write_state(j, H, range);
       }
-      wrote(finite, i + 1);
+      wrote(range, i + 1);
     };
     // An element of the state on its own, infinities too: where it is not finite its first term alone has it.
     auto one_state = [&](int j, float (&y)[16]) {
@@ -1080,15 +1096,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
         for (int x = 0; x < 16; ++x) g[j + x] = y[x];
       }
       meetings = run_steps<T, HPC, NH, OUT>(args.p, at.pass, at.n, at.h0, chunk_at(i) * kChunk, L, sh.dots[i & 1], sh, meetings, g);
-      F2 finite = zero;
+      F2 range = zero;
 #pragma unroll 1
       for (int j = 0; j < NH; j += 16) {
         F2 H[8];
 #pragma unroll
         for (int x = 0; x < 8; ++x) H[x] = f2(g[j + 2 * x], g[j + 2 * x + 1]);
-        write_state(j, H, finite);
+        write_state(j, H, range);
       }
-      wrote(finite, i + 1);
+      wrote(range, i + 1);
     };
     if constexpr (OUT) {
       if (!TMA && count > 0) fetch(0);
@@ -1188,8 +1204,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
         }
         __syncwarp();
       };
-      // A chunk's tiles are there with the copies, but for the one whose last rows have to be cleared.
-      auto early = [&](int i) { return TMA && L - chunk_at(i) * kChunk >= kChunk; };
       if (OUT && count > 0 && early(0)) {
         wait_for(full(0));
         pairs_of(0);

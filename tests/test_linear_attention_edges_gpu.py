@@ -1,9 +1,10 @@
 """GPU tests of the linear attention where its chunks can go wrong: chunks run
-step by step beside others.  Inputs, checks and tolerances are those of
+step by step beside others, and values and decays at the ends of float32's
+range.  Inputs, checks and tolerances are those of
 ``test_linear_attention_gpu.py`` where a test does not state its own."""
 import pytest
 
-from test_linear_attention_gpu import DTYPES, Case, check, cut, layer, same_bits  # noqa: F401  (layer: the fixture)
+from test_linear_attention_gpu import DTYPES, Case, both_ways, check, cut, layer, same_bits  # noqa: F401  (layer: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -39,3 +40,52 @@ def test_attn_every_second_chunk_step_by_step(layer, sizes, dtype):
         check(got["Y"][:, a:a + 64], want["Y"][:, a:a + 64], f"Y {a}")
     for _ in range(10):
         same_bits(got, layer.attn(c.p, **c.t))
+
+
+# ---- values beyond a chunk's range ---------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_attn_large_products_beside_decays(layer, d, dtype):
+    """Chunks that decay by 2^-99.7, queries and keys whose products are 2^28:
+    scaled by the decays' inverses they would pass float32's range, while the
+    outputs are some 2^30."""
+    c = Case(130, 2, 2, d, d, dtype, ragged=False, layout=1, scale=1.0, state=False, grad=True)
+    c.t["Decay"].fill_(-1.08)
+    c.t["Q"].fill_(2048.0), c.t["K"].fill_(2048.0)
+    both_ways(layer, c)
+    c = Case(130, 2, 2, d, d, dtype, ragged=False, layout=1, scale=1.0, state=False)
+    c.t["Decay"].fill_(-1.08)
+    c.t["Q"].fill_(2048.0), c.t["K"].fill_(2048.0), c.t["V"].fill_(2.0)
+    c.compare(layer.attn(c.p, **c.t))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("sizes", [(64, 48), (128, 72)])
+@pytest.mark.parametrize("power", [30, 60, 85, 100])
+def test_attn_inputs_of_thousands_beside_decays(layer, power, sizes, dtype):
+    c = Case(200, 1, 2, *sizes, dtype, ragged=False, layout=0, grad=True)
+    c.t["Decay"].fill_(-power / 64 * 0.6931471805599453)
+    for n in ("Q", "K", "V", "dY"):
+        c.t[n].mul_(3000.0)
+    both_ways(layer, c)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("d", [64, 128])
+def test_attn_large_states_beside_decays(layer, d, dtype):
+    """A state whose product with the queries passes float32's range unless it
+    decays first."""
+    c = Case(130, 2, 2, d, d, dtype, ragged=False, layout=1, scale=1e-33)
+    c.t["initial_state"].mul_(1e34), c.t["Q"].mul_(1e4)
+    c.t["Decay"].fill_(-0.1)
+    c.t["Decay"][:, 0] = -5.0
+    c.compare(layer.attn(c.p, **c.t))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("name", ["Q", "K", "V", "dY"])
+def test_attn_one_large_operand(layer, name, dtype):
+    c = Case(200, 1, 3, 64, 64, dtype, ragged=False, layout=1, grad=True)
+    c.t[name].mul_(1e12)
+    both_ways(layer, c)
