@@ -302,11 +302,14 @@ __device__ __forceinline__ float pow2_of(long long g) {
   return whole > 127 ? __int_as_float(0x7f800000) : part * __int_as_float((whole + 127) << 23);
 }
 
+// 2^300 in units of 2^-32 of its logarithm: every float32 but 0 times that is infinite, and through it 0.
+constexpr long long kAll = 300LL << 32;
 // The logarithm x of a decay to base 2 in units of 2^-32, to the nearest: a
 // memory of thousands of steps adds up as many of the same rounding.  What is
-// below -1e5 leaves nothing in float32, and a chunk's sum of it stays within 2^25.
+// below -1e5 leaves nothing in float32, what is above 1e5 more than there is, and a
+// chunk's sum of either stays within 2^24.
 __device__ __forceinline__ long long fixed_log2(float x) {
-  x = fminf(fmaxf(x, -1.0e5f), 80.0f);
+  x = fminf(fmaxf(x, -1.0e5f), 1.0e5f);
   constexpr float kLow = (float)(1.4426950408889634074 - (double)kLog2e);
   const float t = x * kLog2e, rest = fmaf(x, kLog2e, -t) + x * kLow;
   return __float2ll_rn(t * 4294967296.0f) + (long long)__float2int_rn(rest * 4294967296.0f);
@@ -1169,8 +1172,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
         wait_for(got_u(i));
         if (__builtin_expect(!sh.bad[i % kFlags], 1)) advance(i);
         else by_step(i);
-        // what has left nothing leaves nothing: 64 bits hold a thousandfold of that
-        left = max(left + sh.decays[i % 3][head].log2, -(1LL << 45));
+        // what has left nothing leaves nothing, what has passed float32's range stays beyond it
+        if (left > -kAll && left < kAll) left += sh.decays[i % 3][head].log2;
         arrive(done(i).bar);
       }
       float* to = p.plan.states + ((long long)at.stream * segments + order) * kept;
@@ -1182,8 +1185,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
         for (int x = 0; x < 16; ++x) to[(k0 + j + x) * 128 + r] = j + x < elements ? y[x] : 0.0f;
       }
       if (part == 0 && lane == 0 && (HPC == 2 ? quarter % 2 == 0 : quarter == 0)) {
-        // as whole part and fraction; beyond these nothing, or everything, is left
-        const long long x = min(max(left, -(300LL << 32)), 250LL << 32);
+        // as whole part and fraction
+        const long long x = min(max(left, -kAll), kAll);
         float* to2 = p.plan.left + (((long long)at.stream * segments + order) * 2 + head) * 2;
         to2[0] = (float)(int)(x >> 32), to2[1] = (float)((uint32_t)x >> 8) * 5.9604644775390625e-8f;
       }
@@ -1420,12 +1423,11 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
       if (i >= p.plan.segments) break;
       s[(long long)i * (kept / 4)] = make_float4(run[0], run[1], run[2], run[3]);
       if (i + 1 >= p.plan.segments) break;
-      // 2^x run in two parts: where decays grow a state the power alone may pass float32's range
-      const int w = (int)left[j].x, w1 = max(min(w, 127), -126), w2 = max(min(w - w1, 127), -126);
-      const float part = exp2_fast(left[j].y), f1 = __int_as_float((w1 + 127) << 23), f2 = __int_as_float((w2 + 127) << 23);
-      const float x[4] = {add[j].x, add[j].y, add[j].z, add[j].w};
+      // 2^left run, which may be a float32 where the power alone is none
+      const int whole = (int)left[j].x;
+      const float part = exp2_fast(left[j].y), x[4] = {add[j].x, add[j].y, add[j].z, add[j].w};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) run[e] = run[e] * part * f1 * f2 + x[e];
+      for (int e = 0; e < 4; ++e) run[e] = fmaf(ldexpf(run[e], whole), part, x[e]);
     }
   }
 }

@@ -89,3 +89,23 @@ def test_attn_one_large_operand(layer, name, dtype):
     c = Case(200, 1, 3, 64, 64, dtype, ragged=False, layout=1, grad=True)
     c.t[name].mul_(1e12)
     both_ways(layer, c)
+
+
+# ---- growth ---------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N", [1, 160])
+@pytest.mark.parametrize("steps", [{100: 85.0}, {70: 60.0, 140: 60.0, 150: 53.6, 200: -75.0},
+                                   {66: 88.0, 67: 85.6, 200: -75.0}])
+def test_attn_strong_growth(layer, steps, N, dtype):
+    """A tiny state that grows by more than a power of two in float32 holds,
+    within the first piece of a sequence that is cut, and in ones that are not."""
+    c = Case(700, N, 1, 32, 32, dtype, ragged=False, layout=1)
+    assert cut(c) == (N == 1)
+    c.t["Decay"].zero_()
+    for at, g in steps.items():
+        c.t["Decay"][:, at] = g
+    c.t["K"][:, :max(steps) + 1] = 0  # nothing else is written before
+    c.t["Q"].mul_(0.02)
+    c.t["initial_state"].copy_(c.t["initial_state"].sign() * (1e-33 if len(steps) == 1 else 2.0 ** -126))
+    c.compare(layer.attn(c.p, **c.t))
