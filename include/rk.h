@@ -250,8 +250,11 @@ rk_status rk_encode_host(rk_handle* h, const rk_problem* p, const rk_operands* h
  * (and, once rk_encode_noalloc has run on the handle, the status word of its
  * fixed array): RK_OK, or RK_ERR_TIMEOUT if a bounded device wait of a step
  * kernel, of the tensor-core projection or of the linear attention in chunks
- * (of any handle on the device) gave up during a previous encode;
- * the outputs of that encode are then undefined.  The web page "Recurrent
+ * gave up during a previous encode;
+ * the outputs of that encode are then undefined.  The attention's waits have
+ * one status word for each device: a failure there is reported once to every
+ * handle that has run attention in chunks on the device before it was read,
+ * by a poll with that device current.  The web page "Recurrent
  * layers" has no counterpart: its design waits on nothing inside a launch
  * (one pass per step, paragraph "Why a pass per step"), while this library's
  * persistent kernels wait on the device, each wait bounded so that a launch
@@ -266,8 +269,10 @@ rk_status rk_set_wait_limit(rk_handle* h, int64_t limit);
 
 /* (No counterpart on the pages; see rk_status_poll.)
  * Run the step kernels' bounded device waits against a release counter and an
- * mbarrier that nothing completes (one CTA, no other memory touched): each
- * must give up after timeout_ns and set the handle's status word.  Returns
+ * mbarrier that nothing completes, and the linear attention's against another
+ * (one CTA each, no other memory touched): each must give up after timeout_ns
+ * (the attention's after at most so long) and set the handle's or the device's
+ * status word.  Returns
  * RK_OK once the check kernel is enqueued on `stream`; rk_status_poll then
  * returns RK_ERR_TIMEOUT.  Used to test the give-up path without a hang. */
 rk_status rk_selftest_timeout(rk_handle* h, void* stream, int64_t timeout_ns);

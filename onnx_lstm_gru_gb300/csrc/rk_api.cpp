@@ -1112,7 +1112,7 @@ rk_status rk_encode_host(rk_handle* h, const rk_problem* p, const rk_operands* h
 
 rk_status rk_status_poll(rk_handle* h, void* stream_ptr) {
   if (h == nullptr) return RK_ERR_ARG;
-  if (!h->dev_ready && h->noalloc_status == nullptr && !h->attn_chunks) return RK_OK;
+  if (!h->dev_ready && h->noalloc_status == nullptr && !h->attn_used) return RK_OK;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
   int v = 0, w = 0, a = 0;
   cudaError_t e = cudaStreamSynchronize(stream);
@@ -1122,7 +1122,7 @@ rk_status rk_status_poll(rk_handle* h, void* stream_ptr) {
   if (e == cudaSuccess && h->noalloc_status != nullptr)
     e = cudaMemcpy(&w, h->noalloc_status, sizeof(int), cudaMemcpyDeviceToHost);
   if (e == cudaSuccess && h->noalloc_status != nullptr) e = cudaMemset(h->noalloc_status, 0, sizeof(int));
-  if (e == cudaSuccess && h->attn_chunks) e = rk::take_attn_status(stream, &a);
+  if (e == cudaSuccess && h->attn_used) e = rk::poll_attn(h, stream, &a);
   v |= w | a;
   if (e != cudaSuccess) {
     h->last_error = std::string("recurrent: status poll: ") + cudaGetErrorName(e);
@@ -1150,8 +1150,12 @@ rk_status rk_selftest_timeout(rk_handle* h, void* stream_ptr, int64_t timeout_ns
   if ((st = grow(h, &h->state, &h->state_cap, rk::kStateHeader, &dummy, "state scratch")) != RK_OK) return st;
   cudaError_t e = cudaMemsetAsync(h->state, 0, sizeof(unsigned), stream);
   if (e == cudaSuccess) e = rk::launch_selftest_timeout(reinterpret_cast<unsigned*>(h->state), h->status, timeout_ns, stream);
+  int launches = 1;
+  rk::use_attn_waits(h);
+  const int64_t tries = std::min<int64_t>(timeout_ns / rk::kAttnTryNs + 1, 1000000);
+  if (e == cudaSuccess) e = rk::launch_attn_selftest((int)tries, stream, &launches);
   if (e != cudaSuccess) return fail(h, RK_ERR_CUDA, "recurrent: self-test launch: %s", cudaGetErrorName(e));
-  h->launches += 1;
+  h->launches += launches;
   return RK_OK;
 }
 

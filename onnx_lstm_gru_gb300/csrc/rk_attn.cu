@@ -358,6 +358,15 @@ cudaError_t take_attn_status(cudaStream_t s, int* to) {
   return cudaSuccess;
 }
 
+cudaError_t launch_attn_selftest(int tries, cudaStream_t s, int* launches) {
+  for (auto launch : {launch_attn_selftest_f32, launch_attn_selftest_f16, launch_attn_selftest_bf16}) {
+    const cudaError_t e = launch(tries, s);
+    if (e != cudaSuccess) return e;
+    ++*launches;
+  }
+  return cudaSuccess;
+}
+
 int attn_together(int key_size, int value_size) { return key_size <= 64 && value_size <= 64 ? 2 : 1; }
 
 namespace {

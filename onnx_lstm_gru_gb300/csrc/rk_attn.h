@@ -5,6 +5,8 @@
 
 #include "rk_ssm.h"
 
+struct rk_handle;
+
 namespace rk {
 
 // ---- queries and keys --------------------------------------------------------------
@@ -107,6 +109,16 @@ cudaError_t take_attn_status(cudaStream_t s, int* to);
 cudaError_t take_attn_status_f32(cudaStream_t s, int* to);
 cudaError_t take_attn_status_f16(cudaStream_t s, int* to);
 cudaError_t take_attn_status_bf16(cudaStream_t s, int* to);
+// The same on behalf of one handle: the failures on the current device are
+// counted by process, and every handle that has run there learns of each.
+void use_attn_waits(rk_handle* h);
+cudaError_t poll_attn(rk_handle* h, cudaStream_t s, int* failed);
+// A wait that runs out after so many tries, for each element type's unit.
+cudaError_t launch_attn_selftest(int tries, cudaStream_t s, int* launches);
+cudaError_t launch_attn_selftest_f32(int tries, cudaStream_t s);
+cudaError_t launch_attn_selftest_f16(int tries, cudaStream_t s);
+cudaError_t launch_attn_selftest_bf16(int tries, cudaStream_t s);
+constexpr int kAttnTryNs = 2000;  // one try waits for so long at most
 
 // dDecay and d_decay_bias from the products of q and dQ (to) and k and dK (of).
 struct AttnDecayParams {

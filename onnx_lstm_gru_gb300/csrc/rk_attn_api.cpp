@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <mutex>
 #include <utility>
 
 #include "rk_attn.h"
@@ -150,7 +151,44 @@ GradPlan grad_plan(const rk_attn_problem* p) {
   return g;
 }
 
+// Failed waits by device; devices past the last share its place.
+std::mutex failures_lock;
+uint64_t failures[rk_handle::kDevices];
+
+int device_place() {
+  int d = 0;
+  if (cudaGetDevice(&d) != cudaSuccess) cudaGetLastError();
+  return std::min(std::max(d, 0), rk_handle::kDevices - 1);
+}
+
 }  // namespace
+
+namespace rk {
+
+void use_attn_waits(rk_handle* h) {
+  auto& w = h->attn_waits[device_place()];
+  if (w.used) return;
+  std::lock_guard<std::mutex> lock(failures_lock);
+  w.used = h->attn_used = true;
+  w.seen = failures[&w - h->attn_waits];
+}
+
+cudaError_t poll_attn(rk_handle* h, cudaStream_t s, int* failed) {
+  const int d = device_place();
+  auto& w = h->attn_waits[d];
+  *failed = 0;
+  if (!w.used) return cudaSuccess;
+  std::lock_guard<std::mutex> lock(failures_lock);
+  int now = 0;
+  const cudaError_t e = take_attn_status(s, &now);
+  if (e != cudaSuccess) return e;
+  failures[d] += now != 0;
+  *failed = w.seen != failures[d];
+  w.seen = failures[d];
+  return e;
+}
+
+}  // namespace rk
 
 extern "C" {
 
@@ -255,7 +293,7 @@ rk_status rk_attn_encode(rk_handle* h, const rk_attn_problem* p, const rk_attn_o
     const int64_t need = plan_scratch(p, 1);
     place(ap.plan, c.scratch(scratch, need, s), need);
     ap.plan.vec = a.q.vec && a.k.vec && a.v.vec;
-    if (c.ok()) h->attn_chunks = true;
+    if (c.ok()) rk::use_attn_waits(h);
     if (c.ok()) c.cuda("launch", rk::launch_attn_chunks(ap, s, &launches));
   }
   h->launches += launches;
@@ -342,7 +380,7 @@ rk_status rk_attn_grad_encode(rk_handle* h, const rk_attn_problem* p, const rk_a
     ap.plan = plan_of(p, 3);
     place(ap.plan, marks + 2 * g.marks, g.chunks);
     ap.plan.vec = Q.vec && K.vec && V.vec && dY.vec;
-    h->attn_chunks = true;
+    rk::use_attn_waits(h);
     c.cuda("launch", rk::launch_attn_chunks(ap, s, &launches));
   }
   if (c.ok() && decays) {

@@ -81,7 +81,7 @@ constexpr int kCols = kChunk / 2;            // of a chunk's columns of S and O,
 // A wait that has failed: so many tries, each of which may take up to kTryNs
 // (together two seconds at most, and some tens of milliseconds at least).
 constexpr int kWaitTries = 1000000;
-constexpr uint32_t kTryNs = 2000;
+constexpr uint32_t kTryNs = kAttnTryNs;
 
 template <typename T>
 constexpr int kSplit = sizeof(T) == 4 ? 3 : 2;
@@ -266,7 +266,7 @@ __device__ __forceinline__ void copy_out(const CUtensorMap* map, int x, int h, i
                : "memory");
 }
 
-// Set where a wait has failed (one per element type's unit).
+// Set where a wait has failed (one per element type's unit; what reads it is static, too).
 static __device__ int gave_up_status;
 
 // What a launch gets: the call, and where tiles are copied by TMA the rows of
@@ -516,10 +516,10 @@ __device__ __forceinline__ void products(F mma) {
 // them return at once: the loops run out, and what they compute is undefined.
 // There are waits everywhere, and the code around them has to stay in the
 // instruction cache: a count of tries is less of it than a clock.
-__device__ __forceinline__ void wait_bar(Small& sh, int bar, uint32_t par) {
+__device__ __forceinline__ void wait_bar(Small& sh, int bar, uint32_t par, int limit = kWaitTries) {
   const uint32_t b = su32(&sh.bars[bar]);
 #pragma unroll 1
-  for (int tries = kWaitTries; !bar_try_long(b, par); --tries)
+  for (int tries = limit; !bar_try_long(b, par); --tries)
     if (tries == 0 || sh.gave_up) {
       sh.gave_up = gave_up_status = 1;
       break;
@@ -1291,7 +1291,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
 #pragma unroll 1
         for (int i = 0; i < count; ++i) {
           const int t = chunk_at(i) * kChunk;
-          if (OUT && a.dot) {
+          if (OUT && a.dot && !sh.gave_up) {
             if (Lay::kWithApart) {
               if (i > 0) wait_for(done(i - 1));
             } else {  // takes the place of K, which S and ck K have been made from
@@ -1527,8 +1527,25 @@ cudaError_t launch_chunks(const AttnParams& p, cudaStream_t s, int* launches) {
   return launch_chunks_in<T, kTerms, false>(args, s, launches);
 }
 
+// A wait for a phase that nothing ends: it gives up after so many tries and sets
+// the status word.
+static __global__ void selftest_kernel(int tries) {
+  __shared__ Small sh;
+  if (threadIdx.x == 0) {
+    bar_init(su32(&sh.bars[0]), 1);
+    sh.gave_up = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  wait_bar(sh, 0, 0, tries);
+}
+static cudaError_t launch_selftest(int tries, cudaStream_t s) {
+  selftest_kernel<<<1, 32, 0, s>>>(tries);
+  return cudaGetLastError();
+}
+
 // Reads and clears the status word, in stream order; the caller synchronises.
-inline cudaError_t take_status(cudaStream_t s, int* to) {
+static cudaError_t take_status(cudaStream_t s, int* to) {
   cudaError_t e = cudaMemcpyFromSymbolAsync(to, gave_up_status, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   if (e != cudaSuccess || *to == 0) return e;

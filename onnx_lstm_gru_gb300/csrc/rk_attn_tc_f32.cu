@@ -7,5 +7,6 @@ cudaError_t launch_attn_chunks_f32(const AttnParams& p, cudaStream_t s, int* lau
   return atc::launch_chunks<float>(p, s, launches);
 }
 cudaError_t take_attn_status_f32(cudaStream_t s, int* to) { return atc::take_status(s, to); }
+cudaError_t launch_attn_selftest_f32(int tries, cudaStream_t s) { return atc::launch_selftest(tries, s); }
 
 }  // namespace rk

@@ -32,7 +32,13 @@ struct rk_handle {
   // scratch of the state space operators (scan chunks, gradients' partial sums)
   float* work = nullptr;
   size_t work_cap = 0;
-  bool attn_chunks = false;  // an attention of this handle has waited on the device
+  static constexpr int kDevices = 64;
+  // by device: whether an attention of this handle has waited there, and the failed waits that it knows of
+  struct {
+    bool used = false;
+    uint64_t seen = 0;
+  } attn_waits[kDevices];
+  bool attn_used = false;
   unsigned char* host_arena = nullptr;  // device buffers for rk_encode_host
   size_t host_arena_cap = 0;
   bool profiling = false;

@@ -21,7 +21,7 @@ import functools
 import os
 from dataclasses import dataclass
 
-from . import DTYPES, RkError, load, rk_create, rk_destroy, rk_last_error, rk_launch_count, rk_tensor
+from . import DTYPES, RkError, load, rk_create, rk_destroy, rk_last_error, rk_launch_count, rk_status_poll, rk_tensor
 from ._build import BINDING_LIB
 
 
@@ -456,6 +456,16 @@ class StateSpaceLayer:
 
     def launches(self) -> int:
         return rk_launch_count(self.handle)
+
+    def poll(self, stream=None):
+        """Synchronises the stream (None: torch's current one); an RkError if a wait of the linear attention in chunks
+        gave up on its device since the last poll: the outputs from before are then undefined."""
+        import torch
+        s = stream if stream is not None else torch.cuda.current_stream()
+        with torch.cuda.device(s.device):
+            st = rk_status_poll(self.handle, s.cuda_stream)
+        if st != 0:
+            raise RkError(st, rk_last_error(self.handle))
 
     def norm(self, problem: NormProblem, X, want=("Y", "Mean", "InvStdDev"), stream=None, **tensors) -> dict:
         """Y, Mean, InvStdDev from X, Scale, B."""

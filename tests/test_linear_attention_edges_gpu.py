@@ -3,7 +3,9 @@ step by step beside others, and values and decays at the ends of float32's
 range.  Inputs, checks and tolerances are those of
 ``test_linear_attention_gpu.py`` where a test does not state its own."""
 import pytest
+import torch
 
+import onnx_lstm_gru_gb300 as rk
 from test_linear_attention_gpu import DTYPES, Case, both_ways, check, cut, layer, same_bits  # noqa: F401  (layer: the fixture)
 
 pytestmark = pytest.mark.gpu
@@ -109,3 +111,28 @@ def test_attn_strong_growth(layer, steps, N, dtype):
     c.t["Q"].mul_(0.02)
     c.t["initial_state"].copy_(c.t["initial_state"].sign() * (1e-33 if len(steps) == 1 else 2.0 ** -126))
     c.compare(layer.attn(c.p, **c.t))
+
+
+# ---- waits that fail ------------------------------------------------------------------------------------
+
+def test_attn_failed_waits_reach_every_handle(layer):
+    """A wait that gives up (a phase that nothing ends, 0.2 ms) is reported
+    once by each handle that has run attention in chunks, whichever polls first,
+    and by none that has not."""
+    c = Case(70, 2, 2, 64, 64, "f32", ragged=False)
+    stream = torch.cuda.current_stream()
+    other, idle, late = (rk.StateSpaceLayer() for _ in range(3))
+    layer.attn(c.p, **c.t), other.attn(c.p, **c.t)
+    layer.poll(), other.poll(stream), idle.poll()
+    failing = rk.RecurrentLayer()
+    assert rk.rk_selftest_timeout(failing.handle, stream.cuda_stream, 200_000) == rk.RK_OK
+    for who in (other, layer, failing):
+        with pytest.raises(rk.RkError) as e:
+            who.poll()
+        assert e.value.code == rk.RK_ERR_TIMEOUT
+        who.poll()
+    idle.poll()
+    c.compare(late.attn(c.p, **c.t))
+    late.poll()
+    for who in (other, idle, late, failing):
+        who.close()
