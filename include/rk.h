@@ -590,6 +590,11 @@ typedef struct rk_attn_grad_operands {
 int64_t rk_qk_grad_scratch_length(const rk_qk_problem* p);
 int64_t rk_attn_scratch_length(const rk_attn_problem* p);
 int64_t rk_attn_grad_scratch_length(const rk_attn_problem* p);
+/* What a gradient call with these operands takes, of which the length above is
+ * the most: an output is wanted where its ptr is not null.  dDecay and
+ * d_decay_bias take most of it in long sequences, and dQ, dK and dV where heads
+ * share.  -1 for an invalid problem; operands are not checked. */
+int64_t rk_attn_grad_scratch_needed(const rk_attn_problem* p, const rk_attn_grad_operands* ops);
 
 /* As the state space entries; batch * heads is at most 2^24. */
 rk_status rk_qk_encode(rk_handle* h, const rk_qk_problem* p, const rk_qk_operands* ops, void* stream);

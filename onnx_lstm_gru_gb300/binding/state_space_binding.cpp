@@ -19,6 +19,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/csrc/utils/object_ptr.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <string>
 #include <vector>
@@ -37,6 +38,7 @@ struct Entry {
 
 using Call = int32_t (*)(void*, const void*, const void*, void*);
 using ScratchCall = int32_t (*)(void*, const void*, const void*, const void*, void*);
+using NeededCall = int64_t (*)(const void*, const void*);
 
 struct Plan {
   PyObject_HEAD
@@ -44,6 +46,7 @@ struct Plan {
   std::string* problem;
   void* encode;
   int64_t scratch;  // floats; -1: the entry takes no scratch
+  void* needed;     // what a call's operands take of it, or null: all
 };
 
 constexpr int kMaxOperands = 21, kWords = 5 * kMaxOperands;
@@ -183,10 +186,12 @@ PyObject* plan_run(PyObject* self, PyObject* const* args, Py_ssize_t n) {
     // from torch's allocator: the stream's own memory, and a graph's where one is captured
     c10::DataPtr memory;
     int64_t work[3] = {};
-    if (p->scratch > 0) {
-      memory = c10::cuda::CUDACachingAllocator::get()->allocate((size_t)p->scratch * sizeof(float));
+    int64_t scratch = p->scratch;
+    if (p->needed != nullptr) scratch = std::max<int64_t>(reinterpret_cast<NeededCall>(p->needed)(p->problem->data(), words), 0);
+    if (scratch > 0) {
+      memory = c10::cuda::CUDACachingAllocator::get()->allocate((size_t)scratch * sizeof(float));
       work[0] = reinterpret_cast<int64_t>(memory.get());
-      work[2] = p->scratch;
+      work[2] = scratch;
     }
     st = reinterpret_cast<ScratchCall>(p->encode)(handle, p->problem->data(), words, work, stream);
   }
@@ -195,16 +200,17 @@ PyObject* plan_run(PyObject* self, PyObject* const* args, Py_ssize_t n) {
 }
 
 // Plan(encode address, problem bytes, scratch floats or -1,
-//      [(name, word, rows, required, output, type code, shape)]); type codes: 0
-//      float32, 1 Half, 2 bfloat16, 3 int32.
+//      [(name, word, rows, required, output, type code, shape)][, address of
+//      the scratch that operands need, or 0]); type codes: 0 float32, 1 Half,
+//      2 bfloat16, 3 int32.
 PyObject* plan_new(PyTypeObject* type, PyObject* args, PyObject*) {
   HANDLE_TH_ERRORS
-  unsigned long long encode;
+  unsigned long long encode, needed = 0;
   const char* bytes;
   Py_ssize_t length;
   long long scratch;
   PyObject* list;
-  if (!PyArg_ParseTuple(args, "Ky#LO!", &encode, &bytes, &length, &scratch, &PyList_Type, &list)) return nullptr;
+  if (!PyArg_ParseTuple(args, "Ky#LO!|K", &encode, &bytes, &length, &scratch, &PyList_Type, &list, &needed)) return nullptr;
   std::vector<Entry> entries;
   for (Py_ssize_t i = 0; i < PyList_GET_SIZE(list); ++i) {
     PyObject *name, *shape;
@@ -238,6 +244,7 @@ PyObject* plan_new(PyTypeObject* type, PyObject* args, PyObject*) {
   p->problem = new std::string(bytes, (size_t)length);
   p->encode = reinterpret_cast<void*>(encode);
   p->scratch = scratch;
+  p->needed = reinterpret_cast<void*>(needed);
   return reinterpret_cast<PyObject*>(p);
   END_HANDLE_TH_ERRORS
 }

@@ -134,19 +134,28 @@ void place(rk::AttnPlan& plan, float* w, int64_t floats) {
   plan.left = w + floats / (state + 4) * state;
 }
 int64_t four(int64_t x) { return (x + 3) / 4 * 4; }
-GradPlan grad_plan(const rk_attn_problem* p) {
+struct GradWants {
+  bool q, k, v, decay, bias, first;
+  bool any() const { return q || k || v || decay || bias || first; }
+};
+constexpr GradWants kEverything = {true, true, true, true, true, true};
+GradPlan grad_plan(const rk_attn_problem* p, const GradWants& want) {
   const int64_t heads = p->batch * p->heads, rows = heads * p->seq;
   GradPlan g{};
-  g.to = g.of = four(rows);
-  g.cross = four(2 * heads);
-  g.partial = four(2 * heads * rk::attn_decay_tiles(p->seq));
-  if (shared(p->heads, p->query_heads) > 1) g.q32 = four(rows * p->key_size);
-  if (shared(p->heads, p->key_heads) > 1) g.k32 = four(rows * p->key_size);
-  if (shared(p->heads, p->value_heads) > 1) g.v32 = four(rows * p->value_size);
+  if (rows == 0 || !want.any()) return g;
+  // the pieces are those of the whole gradient whatever is wanted: equal bits
   const rk::AttnPlan plan = plan_of(p, 3);
-  const int together = rk::attn_together((int)p->key_size, (int)p->value_size);
-  g.between = four(heads * plan.marks);
-  g.marks = p->batch * ((p->heads + together - 1) / together) * plan.marks * plan.deep * 128;
+  if (want.decay || want.bias) {
+    g.to = g.of = four(rows);
+    g.cross = four(2 * heads);
+    if (want.bias) g.partial = four(2 * heads * rk::attn_decay_tiles(p->seq));
+    const int together = rk::attn_together((int)p->key_size, (int)p->value_size);
+    g.between = four(heads * plan.marks);
+    g.marks = p->batch * ((p->heads + together - 1) / together) * plan.marks * plan.deep * 128;
+  }
+  if (want.q && shared(p->heads, p->query_heads) > 1) g.q32 = four(rows * p->key_size);
+  if (want.k && shared(p->heads, p->key_heads) > 1) g.k32 = four(rows * p->key_size);
+  if (want.v && shared(p->heads, p->value_heads) > 1) g.v32 = four(rows * p->value_size);
   g.chunks = plan_scratch(p, 3);
   return g;
 }
@@ -207,7 +216,16 @@ int64_t rk_attn_scratch_length(const rk_attn_problem* p) {
 int64_t rk_attn_grad_scratch_length(const rk_attn_problem* p) {
   Call c = begin(nullptr, "LinearAttentionGrad", p, nullptr, false);
   if (c.ok()) check(c, p);
-  return c.ok() ? grad_plan(p).total() : -1;
+  return c.ok() ? grad_plan(p, kEverything).total() : -1;
+}
+
+int64_t rk_attn_grad_scratch_needed(const rk_attn_problem* p, const rk_attn_grad_operands* o) {
+  Call c = begin(nullptr, "LinearAttentionGrad", p, o, true);
+  if (c.ok()) check(c, p);
+  if (!c.ok()) return -1;
+  const GradWants want = {o->dQ.ptr != nullptr,     o->dK.ptr != nullptr,           o->dV.ptr != nullptr,
+                          o->dDecay.ptr != nullptr, o->d_decay_bias.ptr != nullptr, o->d_initial_state.ptr != nullptr};
+  return grad_plan(p, want).total();
 }
 
 rk_status rk_qk_encode(rk_handle* h, const rk_qk_problem* p, const rk_qk_operands* o, void* stream) {
@@ -327,13 +345,14 @@ rk_status rk_attn_grad_encode(rk_handle* h, const rk_attn_problem* p, const rk_a
   const float* dlast = c.tensor<float>("d_final_state", o->d_final_state, states, 4);
   float* dbias = c.tensor<float>("d_decay_bias", o->d_decay_bias, H, 4);
   float* dfirst = c.tensor<float>("d_initial_state", o->d_initial_state, states, 4);
-  if (!c.ok() || !(dQ.p || dK.p || dV.p || dDecay.p || dbias || dfirst)) return c.st;
+  const GradWants want = {dQ.p != nullptr, dK.p != nullptr, dV.p != nullptr, dDecay.p != nullptr, dbias != nullptr, dfirst != nullptr};
+  if (!c.ok() || !want.any()) return c.st;
   if (p->seq * p->batch == 0) {
     c.zero(dbias, H * 4LL, s);
     c.copy(dfirst, dlast, states * 4, s);
     return c.st;
   }
-  const GradPlan g = grad_plan(p);
+  const GradPlan g = grad_plan(p, want);
   float* w = c.scratch(scratch, g.total(), s);
   if (!c.ok()) return c.st;
   const bool decays = dDecay.p || dbias;

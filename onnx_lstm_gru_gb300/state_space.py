@@ -113,6 +113,7 @@ SIGNATURES = {
     "rk_qk_grad_scratch_length": (ctypes.c_int64, [_P]),
     "rk_attn_scratch_length": (ctypes.c_int64, [_P]),
     "rk_attn_grad_scratch_length": (ctypes.c_int64, [_P]),
+    "rk_attn_grad_scratch_needed": (ctypes.c_int64, [_P, _P]),
     "rk_norm_encode": (ctypes.c_int32, [_P, _P, _P, _P]),
     "rk_norm_grad_encode": (ctypes.c_int32, [_P, _P, _P, _P, _P]),
     "rk_conv_encode": (ctypes.c_int32, [_P, _P, _P, _P]),
@@ -158,6 +159,10 @@ def rk_attn_scratch_length(problem: rk_attn_problem) -> int:
 
 def rk_attn_grad_scratch_length(problem: rk_attn_problem) -> int:
     return load().rk_attn_grad_scratch_length(_ref(problem))
+
+
+def rk_attn_grad_scratch_needed(problem: rk_attn_problem, ops: rk_attn_grad_operands) -> int:
+    return load().rk_attn_grad_scratch_needed(_ref(problem), _ref(ops))
 
 
 def rk_norm_encode(handle, problem, ops, stream) -> int:
@@ -425,7 +430,10 @@ def _plan(op, problem):
     encode = ctypes.cast(getattr(lib, f"rk_{op}_encode"), ctypes.c_void_p).value
     # a problem that the entry will refuse has no scratch length: its message says why
     scratch = -1 if length is None else max(length(ctypes.byref(c)), 0)
-    return _binding().Plan(encode, bytes(c), scratch, entries)
+    # less where the call wants less
+    needed = getattr(lib, f"rk_{op}_scratch_needed", None)
+    return _binding().Plan(encode, bytes(c), scratch, entries,
+                           ctypes.cast(needed, ctypes.c_void_p).value if needed is not None else 0)
 
 
 class StateSpaceLayer:

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import onnx_lstm_gru_gb300 as rk
+from onnx_lstm_gru_gb300 import state_space as ss
 from test_linear_attention_gpu import DTYPES, Case, both_ways, check, cut, layer, same_bits  # noqa: F401  (layer: the fixture)
 
 pytestmark = pytest.mark.gpu
@@ -136,3 +137,30 @@ def test_attn_failed_waits_reach_every_handle(layer):
     late.poll()
     for who in (other, idle, late, failing):
         who.close()
+
+
+# ---- scratch --------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("q,k,v", [(4, 4, 4), (2, 1, 2)])
+@pytest.mark.parametrize("S,N", [(700, 1), (70, 3)])
+def test_attn_grad_in_the_scratch_it_needs(layer, S, N, q, k, v):
+    """Whatever is wanted, no more than that is taken, and the bits are those
+    of all outputs together."""
+    c = Case(S, N, 4, 48, 64, "bf16", q=q, k=k, v=v, decay="both", layout=1, grad=True)
+    every = layer.attn_grad(c.p, want=c.grads(), **c.t)
+    stream = torch.cuda.current_stream().cuda_stream
+    for want in (("dQ",), ("dK", "dV"), ("d_initial_state",), ("dDecay",), ("d_decay_bias", "dQ"), c.grads()):
+        ops = ss.rk_attn_grad_operands()
+        outs = {n: torch.empty_like(every[n]) for n in want}
+        for n, x in {**c.t, **outs}.items():
+            words = (x.data_ptr(), 0, x.numel())
+            setattr(ops, n, ss.rk_rows(*words, 0, 0) if n in ss._OPERANDS["attn_grad"][0] else rk.rk_tensor(*words))
+        need = rk.rk_attn_grad_scratch_needed(c.p.to_c(), ops)
+        room = torch.full((need + 64,), 7.0, device="cuda")
+        work = ss.rk_workspace(room.data_ptr(), 32, 32 + need)
+        assert rk.rk_attn_grad_encode(layer.handle, c.p.to_c(), ops, work, stream) == rk.RK_OK
+        same_bits(outs, {n: every[n] for n in want})
+        assert bool((room[:32] == 7).all()) and bool((room[32 + need:] == 7).all())
+        if need:
+            work.length -= 1
+            assert rk.rk_attn_grad_encode(layer.handle, c.p.to_c(), ops, work, stream) == rk.RK_ERR_SHAPE

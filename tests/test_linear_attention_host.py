@@ -190,6 +190,34 @@ def test_scratch_lengths():
     assert more == 100 * 2 * 4 * 8
 
 
+def test_scratch_of_what_is_wanted():
+    """Gradients that are not wanted take no scratch; all of them take the length by the problem alone."""
+    p = rk.AttnProblem(seq=4096, batch=64, heads=16, key_size=128, value_size=128)
+    c, rows, outputs = p.to_c(), ss._OPERANDS["attn_grad"][0], ss._OUTPUTS["attn_grad"]
+
+    def needed(p, *names):
+        ops = ss.rk_attn_grad_operands()
+        for n in names:
+            setattr(ops, n, ss.rk_rows(0x1000, 0, 1, 0, 0) if n in rows else rk.rk_tensor(0x1000, 0, 1))
+        return rk.rk_attn_grad_scratch_needed(p.to_c(), ops)
+    every = rk.rk_attn_grad_scratch_length(c)
+    assert every * 4 > 900e6
+    assert needed(p, *outputs) == every and needed(p) == 0
+    assert needed(p, "dQ", "dK", "dV", "d_initial_state") == 0
+    assert every - 2 ** 16 < needed(p, "dDecay") < every
+    shared = rk.AttnProblem(seq=100, batch=2, heads=4, key_size=8, value_size=16, query_heads=2, key_heads=1,
+                            value_heads=2)
+    assert [needed(shared, n) for n in ("dQ", "dK", "dV", "d_initial_state")] == [6400, 6400, 12800, 0]
+    assert needed(shared, *outputs) == rk.rk_attn_grad_scratch_length(shared.to_c())
+    # few sequences are cut into the same pieces, whatever is wanted
+    one = rk.AttnProblem(seq=4096, batch=1, heads=16, key_size=128, value_size=128)
+    assert needed(one, "dQ") == needed(one, "dQ", "dK", "dV") == needed(one, "d_initial_state") > 0
+    assert needed(rk.AttnProblem(seq=0, batch=4, heads=2, key_size=8, value_size=8), *outputs) == 0
+    c.layout = 2
+    assert rk.rk_attn_grad_scratch_needed(c, ss.rk_attn_grad_operands()) == -1
+    assert rk.load().rk_attn_grad_scratch_needed(None, None) == -1
+
+
 def test_defaults_of_the_problems():
     p = rk.AttnProblem(seq=1, batch=1, heads=4, key_size=64, value_size=8)
     c = p.to_c()
