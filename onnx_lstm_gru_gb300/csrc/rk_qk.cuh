@@ -77,17 +77,42 @@ struct Turns {
   }
 };
 
-// Cosine and sine of a turn.  The special function unit's are off by 2^-20 at
-// most within half a turn, which no 16-bit element keeps.
+// Cosines and sines of the turns of two pairs.  float32 elements get CUDA's
+// function, 16-bit ones polynomials of the distance x to the nearest quarter turn,
+// |x| <= 1/2 quarters, in packed arithmetic: sin(pi x / 2) / x and (cos(pi x / 2) -
+// 1) / x^2 as cubics in x^2, interpolated at the Chebyshev nodes of [0, 1/4].  They
+// are off by 1e-7 at most, x's own rounding included.  (The special function unit
+// is off by 4e-7, which elements turned to near zero show in Half and bfloat16.)
 template <typename T>
-__device__ __forceinline__ void turn(unsigned long long step, int position, float& c, float& s) {
-  const long long phase = (long long)(step * (unsigned long long)(long long)position);
+__device__ __forceinline__ void turns_of(const long long (&phase)[2], F2& c, F2& s) {
+  float cs[2], sn[2];
   if constexpr (sizeof(T) == 4) {
-    sincospif((float)phase * 1.0842021724855044e-19f, &s, &c);  // 2^-63: in half turns
+#pragma unroll
+    for (int e = 0; e < 2; ++e) sincospif((float)phase[e] * 1.0842021724855044e-19f, &sn[e], &cs[e]);  // 2^-63: in half turns
   } else {
-    const float angle = (float)(int)(phase >> 32) * (float)(3.14159265358979323846 / 2147483648.0);
-    s = __sinf(angle), c = __cosf(angle);
+    int quarter[2];
+    float x[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const uint32_t top = (uint32_t)((unsigned long long)phase[e] >> 32);  // turns in units of 2^-32
+      quarter[e] = (int)((top + (1u << 29)) >> 30);
+      x[e] = (float)(int)(top - ((uint32_t)quarter[e] << 30)) * 9.31322574615478515625e-10f;  // 2^-30
+    }
+    const F2 v = f2(x[0], x[1]), z = mul2(v, v);
+    F2 p = f2(-0.004602149f, -0.004602149f), q = f2(0.0009067399f, 0.0009067399f);
+    p = fma2(p, z, f2(0.07968022f, 0.07968022f)), q = fma2(q, z, f2(-0.020861529f, -0.020861529f));
+    p = fma2(p, z, f2(-0.6459635f, -0.6459635f)), q = fma2(q, z, f2(0.2536694f, 0.2536694f));
+    p = fma2(p, z, f2(1.5707964f, 1.5707964f)), q = fma2(q, z, f2(-1.2337005f, -1.2337005f));
+    const float2 sine = f2_get(mul2(p, v)), cosine = f2_get(fma2(q, z, f2(1.0f, 1.0f)));
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float a = e ? sine.y : sine.x, b = e ? cosine.y : cosine.x;
+      const uint32_t odd = quarter[e] & 1, half = (uint32_t)quarter[e] >> 1 & 1;
+      sn[e] = __uint_as_float(__float_as_uint(odd ? b : a) ^ half << 31);
+      cs[e] = __uint_as_float(__float_as_uint(odd ? a : b) ^ (odd ^ half) << 31);
+    }
   }
+  c = f2(cs[0], cs[1]), s = f2(sn[0], sn[1]);
 }
 
 // A lane's units of a head: `lanes` lanes hold them, U each, in pieces of V
@@ -121,16 +146,23 @@ struct Lane {
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int j = 0; j < J; ++j) {
-        float cs[2] = {1.0f, 1.0f}, sn[2] = {0.0f, 0.0f};
+        long long phase[2] = {0, 0};  // of a pair that stays
+        bool nan[2] = {false, false};
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int i = 2 * j + e;
           if (i < V && na[u] && turns(p, u, i)) {
-            turn<T>(table->step[pair[u] + i], at, cs[e], sn[e]);
-            if (none && table->none[pair[u] + i]) cs[e] = sn[e] = __int_as_float(0x7fffffff);
+            phase[e] = (long long)(table->step[pair[u] + i] * (unsigned long long)(long long)at);
+            nan[e] = none && table->none[pair[u] + i];
           }
         }
-        c[u][j] = f2(cs[0], cs[1]), s[u][j] = f2(sn[0], sn[1]), minus[u][j] = f2(-sn[0], -sn[1]);
+        turns_of<T>(phase, c[u][j], s[u][j]);
+        if (none) {
+          const float2 x = f2_get(c[u][j]), y = f2_get(s[u][j]);
+          const float bad = __int_as_float(0x7fffffff);
+          c[u][j] = f2(nan[0] ? bad : x.x, nan[1] ? bad : x.y), s[u][j] = f2(nan[0] ? bad : y.x, nan[1] ? bad : y.y);
+        }
+        minus[u][j] = mul2(s[u][j], f2(-1.0f, -1.0f));
       }
   }
   // A unit's two pieces of a head's row on their way.

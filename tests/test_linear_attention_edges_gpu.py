@@ -7,7 +7,7 @@ import torch
 
 import onnx_lstm_gru_gb300 as rk
 from onnx_lstm_gru_gb300 import state_space as ss
-from test_linear_attention_gpu import DTYPES, Case, both_ways, check, cut, layer, same_bits  # noqa: F401  (layer: the fixture)
+from test_linear_attention_gpu import DTYPES, F64, UNIT, Case, both_ways, check, cut, layer, same_bits  # noqa: F401  (layer: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -164,3 +164,28 @@ def test_attn_grad_in_the_scratch_it_needs(layer, S, N, q, k, v):
         if need:
             work.length -= 1
             assert rk.rk_attn_grad_encode(layer.handle, c.p.to_c(), ops, work, stream) == rk.RK_ERR_SHAPE
+
+
+# ---- turns ----------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_qk_turns_near_the_zeros_of_the_sine(layer, interleaved, dtype):
+    """Pairs (0, 1) turned by about a multiple of half a turn: the first element
+    is the sine, far smaller than the second.  An angle of up to half a turn in
+    float32 is off by pi 2^-25, the sine by one unit of 2^-24 at most, and the
+    element then by its own rounding: 2^-22.5 in all beside that, in gradients
+    too, and 2^-25 for Half's numbers below its normal ones."""
+    S, r = 3000, 64
+    p = rk.QkProblem(seq=S, batch=1, heads=1, size=r, rotary=r, interleaved=interleaved, norm="none", dtype=dtype)
+    f = (torch.pi * (1 + 3e-7 * torch.arange(r // 2, dtype=F64) ** 2)).float()
+    x = torch.zeros(S, 1, r)
+    x[..., slice(1, None, 2) if interleaved else slice(r // 2, None)] = 1.0
+    x = x.to(rk.torch_dtype(dtype)).cuda()
+    angle = torch.arange(S, dtype=F64)[:, None] * f.double()
+    first = slice(0, None, 2) if interleaved else slice(0, r // 2)
+    t = dict(K=x, Frequencies=f.cuda())
+    for y, sign in ((layer.qk(p, x, **t)["YQ"], -1), (layer.qk_grad(p, x, dYQ=x, dYK=x, want=("dQ",), **t)["dQ"], 1)):
+        got, want = y[:, 0, first].double().cpu(), sign * torch.sin(angle)
+        bound = UNIT[y.dtype] * want.abs() + 2.0 ** -22.5 + 2.0 ** -25
+        assert bool(((got - want).abs() <= bound).all()), float(((got - want).abs() - bound).max())
