@@ -1,13 +1,15 @@
 """GPU tests of the linear attention where its chunks can go wrong: chunks run
-step by step beside others, and values and decays at the ends of float32's
-range.  Inputs, checks and tolerances are those of
-``test_linear_attention_gpu.py`` where a test does not state its own."""
+step by step beside others, values and decays at the ends of float32's range,
+waits that fail, scratch, and errors in the mean square.  Inputs, checks and
+tolerances are those of ``test_linear_attention_gpu.py`` where a test does not
+state its own."""
 import pytest
 import torch
 
 import onnx_lstm_gru_gb300 as rk
 from onnx_lstm_gru_gb300 import state_space as ss
-from test_linear_attention_gpu import DTYPES, F64, UNIT, Case, both_ways, check, cut, layer, same_bits  # noqa: F401  (layer: the fixture)
+from test_linear_attention_gpu import (  # noqa: F401  (layer: the fixture)
+    DTYPES, F64, UNIT, Case, batch_first, both_ways, check, cut, layer, same_bits)
 
 pytestmark = pytest.mark.gpu
 
@@ -189,3 +191,71 @@ def test_qk_turns_near_the_zeros_of_the_sine(layer, interleaved, dtype):
         got, want = y[:, 0, first].double().cpu(), sign * torch.sin(angle)
         bound = UNIT[y.dtype] * want.abs() + 2.0 ** -22.5 + 2.0 ** -25
         assert bool(((got - want).abs() <= bound).all()), float(((got - want).abs() - bound).max())
+
+
+# ---- errors in the mean square ----------------------------------------------------------------------------
+
+TIGHT_SHAPES = [(300, 2, 4, 64, 64), (300, 2, 2, 128, 128), (700, 1, 2, 64, 48), (1500, 1, 1, 128, 128),
+                (777, 2, 2, 72, 103), (513, 60, 3, 40, 64), (12, 3, 2, 128, 96)]
+
+
+def relative(got, want):
+    return float((got.double().cpu() - want).norm() / want.norm())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", TIGHT_SHAPES)
+def test_attn_mean_square(layer, shape, dtype):
+    """What is float32 is off by 1e-6 of its size in the mean square.  An
+    element goes through at most 250 roundings of 2^-24 of what it is then: 8 x 6
+    of 128 elements' products for S (sums of sixteen, six pairs of terms), 4 x 6
+    for P's and 8 x 6 for the state's, 3 each for the terms of P, of the scaled
+    keys and of the state, 4 for each of two powers of two (off by 2^-22), and
+    26 for a chunk that the state passes, of which the decays here leave
+    at most four in sight.  Inputs have no sign of their own, so that roundings
+    add up by their squares: sqrt(250) 2^-24 = 9.4e-7.  A term of a factor left
+    out alone (two bfloat16 numbers in place of three, off by 2^-17 at most and
+    by 0.4 of that in the mean square) is 3e-6.
+    16-bit outputs are the definition's, rounded, but where that lies next to
+    the middle of two numbers: P and the state as two bfloat16 numbers are off by
+    2^-17, an output by 2^-16 of what its terms are, in the mean twice its size
+    or less, on either side of a middle, and numbers are a unit roundoff or two
+    apart: a share of 2^-14 of an output's size through that spacing.  With one
+    number in place of two a third of bfloat16's outputs would differ.
+    dDecay is a sum of k dk - q dq over the at most 512 steps to a mark, each
+    element's product off by as much, again by their squares; what is left
+    at the mark and taken back is at most as large again.  d_decay_bias adds up
+    dDecay, and what a block of 512 steps is off by with it, at each of them."""
+    c = Case(*shape, dtype, ragged=False, decay="both", layout=1, grad=True)
+    p, got, want = c.p, layer.attn_grad(c.p, want=c.grads(), **c.t), c.reference()
+    for n in ("dY", "d_final_state"):
+        c.t.pop(n)
+    got.update(layer.attn(p, **c.t))
+    want.update(c.reference())
+    far = {}
+    for k, v in got.items():
+        if v.dtype == torch.float32 and k not in ("dDecay", "d_decay_bias"):
+            v = batch_first(v, 1) if k in ("Y", "dQ", "dK", "dV") else v
+            off = relative(v, want[k])
+            if off > 1e-6:
+                far[k] = off
+        elif v.dtype != torch.float32:
+            near = want[k].to(v.dtype)
+            share = float((batch_first(v, 1) != near.double()).float().mean())
+            if share > 2.0 ** -14 / (2 * UNIT[v.dtype]):
+                far[k] = share
+    square = torch.zeros(p.batch, p.seq, p.heads, dtype=F64)
+    for x, dx in (("Q", "dQ"), ("K", "dK")):
+        a = (batch_first(c.t[x], 1) * want[dx]).square()
+        square += a.unflatten(-1, (p.heads, -1)).sum(-1)
+    pad = torch.nn.functional.pad(square, (0, 0, 0, -p.seq % 512)).unflatten(1, (-1, 512)).sum(2, keepdim=True)
+    block = (4 * 1e-12 * pad).sqrt().expand(-1, -1, 512, -1)  # by step, the same for all of a block's
+    steps = block.flatten(1, 2)[:, :p.seq]
+    off = (got["dDecay"].double().cpu() - want["dDecay"]).norm() / steps.norm()
+    if off > 1:
+        far["dDecay"] = float(off)
+    bias = (512 ** 2 * block[:, :, 0].square()).sum((0, 1)).sqrt()
+    off = (got["d_decay_bias"].double().cpu() - want["d_decay_bias"]).norm() / bias.norm()
+    if off > 1:
+        far["d_decay_bias"] = float(off)
+    assert not far, far
