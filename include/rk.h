@@ -561,7 +561,12 @@ typedef struct rk_qk_grad_operands {
  * g is the decay's natural logarithm: 0 keeps the state, minus infinity
  * forgets it, so that a row may hold several documents.  Above 0 the state
  * grows; products of decays beyond float32's range are infinite.
- * Infinities and NaN of a step reach that step's and later outputs only. */
+ * Infinities and NaN of a step reach that step's and later outputs only.
+ * Sequences of more than twelve steps run in chunks of 64.  A chunk of
+ * far larger numbers than usual (queries or values of 2^20 and more, products
+ * or states of 2^100) runs step by step, about twenty times slower, as one with
+ * infinities or NaN does; and chunks compute their outputs whether Y is wanted
+ * or not, so that the final state has the same bits. */
 typedef struct rk_attn_problem {
   int32_t dtype, layout;
   float scale;
@@ -579,7 +584,8 @@ typedef struct rk_attn_operands {
  * elements), d_decay_bias, d_initial_state and the optional input
  * d_final_state are float32.  dDecay is taken from running sums over
  * 512 steps of what queries and keys contribute, in pairs of float32: where it
- * is far smaller than those contributions it has their float32 accuracy.
+ * is far smaller than those contributions it has their float32 accuracy, and
+ * d_decay_bias, which adds dDecay up, that of the sum of its magnitudes.
  * Infinities and NaN in an operand may reach the gradients of any step of
  * their batch row. */
 typedef struct rk_attn_grad_operands {

@@ -144,9 +144,14 @@ cudaError_t launch_steps(const AttnParams& p, cudaStream_t s) {
 // the state before the step with its gradient.  With A_t = q dq and B_t = k dk
 // of a step, E grows by B_t - A_t from one step to the next.  The sums run from
 // one mark to the next, kMarkChunks chunks on, where E is taken from the states
-// themselves, as it is at both ends of the sequence: over 4000 steps and more the
-// float32 products' errors would add up to 4e-5 of a bias' gradient.  What they
-// leave at a mark is taken back evenly on the way to it.  A block takes the steps
+// themselves, as it is at both ends of the sequence: what the float32 products are
+// off by (1e-7 of them) adds up on the way, and a bias' gradient adds that up once
+// more.  What they leave at a mark is taken back evenly on the way to it.  Of 500
+// cases drawn around those measured dDecay is off by 2.7e-7 of its size in the
+// middle and 1.1e-6 at most, a bias' gradient by 1.7e-7 and 2.6e-5, where short
+// memories leave little of its sum (plain form in float32: 1.8e-7 and 4e-7, 1.6e-7
+// and 3.1e-6).  Marks every 128 steps take that to 9e-6 for a fifth of the gradient's
+// time (8 x 512 x 16 heads of 128, 140 and 165 us).  A block takes the steps
 // between two marks; the sums are pairs of float32 that keep what each addition
 // rounds away (Knuth's two-sum), as the card has few float64 units and the kernel
 // is a chain of sums, bound by their latency (128 heads of 512 steps 11.8 us with
@@ -382,9 +387,9 @@ AttnPlan attn_plan(long long seq, long long batch, long long heads, int key_size
   const long long streams = streams_of(batch, heads, key_size, value_size, passes);
   const long long chunks = (seq + 63) / 64;
   // pieces of two chunks at least, and as many as fit the card together: 4096 x
-  // 1 x 16 heads of 128 in eight, 64 us; in four 96, whole 188.  More than fit
-  // together cost their sums of states and bring nothing (8 x 777 x 10 heads,
-  // float32, whole 117 us, in two 147; gradient 8 x 512 x 16 137 and 255 us).
+  // 1 x 16 heads of 128 in eight, 59 us; in sixteen 71, in four 90, whole 189.  More
+  // than fit together cost their sums of states and bring nothing (8 x 777 x 10
+  // heads, float32, whole 128 us, in two 180; gradient 8 x 512 x 16 135 and 209).
   long long segments = streams > 0 ? std::min(kPlanSms / streams, chunks / 2) : 1;
   segments = std::max<long long>(segments, 1);
   plan.per = (int)((chunks + segments - 1) / segments);

@@ -87,9 +87,11 @@ struct AttnParams {
   AttnPass pass[3];
   AttnPlan plan;
 };
-// The longest sequences that run step by step.  bfloat16, 16 heads of 128, 8
-// steps and 12, against one chunk: 1 batch row 12.4 and 14.5 us against 12.4,
-// 64 batch rows 51 and 66 us against 72; float32 against 18.6 and 119 us.
+// The longest sequences that run step by step.  16 heads with their states, 8
+// steps and 12 against one chunk of 13, us: heads of 128, 1 batch row 12.4 and
+// 14.8 against 12.5, 64 batch rows 52 and 68 against 82, float32 against 18.6 and
+// 119; heads of 64, two to a block, 8.3 and 10.3 against 10.5, 25 and 32 against 36,
+// float32 against 14.5 and 51.
 constexpr int kAttnSteps = 12;
 // Heads that share a block.
 int attn_together(int key_size, int value_size);

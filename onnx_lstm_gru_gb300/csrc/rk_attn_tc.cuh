@@ -22,7 +22,7 @@
 // and a product the sum of the terms' products down to 2^-24 of it, smallest
 // first; bfloat16 operands are one term, Half two, float32 three, and what is
 // computed here (P, ck K, H) three, or P and H two where only a 16-bit output
-// comes of them, which keeps less than their 2^-17.  Differences of G are exact to 2^-24: sums
+// comes of them (launch_chunks).  Differences of G are exact to 2^-24: sums
 // are 64-bit whole numbers of 2^-32, kept as whole part and fraction.
 //
 // Where a chunk's decays (and the scale) stay between 2^-80 and 2^20, P_mn 2^-G_m is
@@ -52,11 +52,11 @@
 // 2^20 or more: below that O + Oi is at most 64 + 128 products of 2^120, and U 64.
 //
 // What bounds it are the warps' own instructions and their waits for each
-// other, not the products or HBM: 512 x 64 x 16 heads of 64, bf16, 111 us (2.6
-// TB/s, 2.2 warp instructions a clock and multiprocessor, the tensor pipe 30 %
-// busy); the gradient of 512 x 8 x 16 heads of 128 136 us (2.2, 21 %); 777 x 8 x 10
-// heads of 72 x 103 in float32, 80 blocks, 106 us (1.7, 25 %).  Step by step the
-// three take 2316, 2319 and 646 us.
+// other, not the products or HBM: 512 x 64 x 16 heads of 64, bf16, 114 us (2.5
+// TB/s, 2.2 warp instructions a clock and multiprocessor, the tensor pipe 29 %
+// busy); the gradient of 512 x 8 x 16 heads of 128 137 us (2.2, 21 %); 777 x 8 x 10
+// heads of 72 x 103 in float32, 80 blocks, 110 to 126 us as the lengths are (1.8,
+// 25 %).  Step by step the three take 2316, 2319 and 646 us.
 #pragma once
 #include <cuda_runtime.h>
 
@@ -1513,7 +1513,13 @@ cudaError_t launch_chunks_in(const ChunkArgs& args, cudaStream_t s, int* launche
 
 // P and the state as three terms where float32 comes of them: for float32
 // rows, and in gradients, whose products for the decays are added up over the
-// sequence.  A 16-bit output keeps less than the 2^-17 of two.
+// sequence.  Where 16-bit outputs alone do, two: off by 2^-17 of what they are,
+// while the rows that they come of are rounded to 2^-9 or 2^-12 of theirs.  An
+// output that is far smaller than its terms keeps 2^-17 of those.  Three cost a
+// seventh: 512 x 64 x 16 heads of 64, bf16, 132 us for 114, 4096 x 1 x 16 of 128 68
+// for 59; the outputs are then 3e-5 to 4e-5 of their size from float32
+// arithmetic's, rounded, in the mean square, and 9e-5 to 1e-4 so.  From the
+// definition both are 1.7e-3 (Half 2.1e-4), which is their own rounding.
 template <typename T>
 cudaError_t launch_chunks(const AttnParams& p, cudaStream_t s, int* launches) {
   ChunkArgs args{};

@@ -8,9 +8,9 @@
 // share, are computed once; a lane holds both elements of its pairs, and a
 // head's sum is a few exchanges of lanes.
 // What bounds them is HBM and, next to it, instructions: 32768 rows of 16 + 16
-// heads of 64, bf16, 55.6 us or 4.8 TB/s (71 % of a copy) at 2.5 warp instructions a
-// clock and multiprocessor, 308 for a warp's 512 elements; the gradient of 8 + 8
-// heads of 128 92 us, 4.4 TB/s (64 %), at 2.4, its 16 warps bound by registers.
+// heads of 64, bf16, 53.3 us or 5.0 TB/s (74 % of a copy) at 2.4 warp instructions a
+// clock and multiprocessor, 284 for a warp's 512 elements; the gradient of 8 + 8
+// heads of 128 94 us, 4.3 TB/s (63 %), at 2.4, its 16 warps bound by registers.
 #pragma once
 #include <algorithm>
 
