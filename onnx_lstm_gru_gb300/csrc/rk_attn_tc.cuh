@@ -41,8 +41,8 @@
 //   rows of whole 16-byte pieces; else the three groups do), and one for each
 //   head takes the decays of later chunks.
 // The products of one chunk run while the next one's operands are made ready:
-// O_i follows P_i; S_(i+1) and U_(i+1) follow ck K; Oi_(i+1) follows the
-// outputs of i.
+// O_i follows P_i; S_(i+1) and U_(i+1) follow ck K; Oi_(i+1), or with three terms
+// what is small of it, follows the outputs of i.
 //
 // Infinities and NaN must not reach other steps through the products' zeros, and
 // sums that are scaled down once they are complete must not pass float32's range
@@ -493,12 +493,12 @@ __device__ __forceinline__ bool tile_in_range(const unsigned char* tile, int thr
 }
 
 // One thread: the products of NA terms of A and NB of B down to 2^-8 NT,
-// smallest first, STEPS products of 16 each.
-template <int NA, int NB, int NT, int STEPS, typename F>
-__device__ __forceinline__ void products(F mma) {
-  uint32_t more = 0;
+// smallest first, STEPS products of 16 each.  LAST 1: all but the first terms'
+// own, which FIRST 0 are.
+template <int NA, int NB, int NT, int STEPS, int LAST = 0, int FIRST = NT - 1, typename F>
+__device__ __forceinline__ void products(F mma, uint32_t more = 0) {
 #pragma unroll
-  for (int sum = (NA + NB - 2 < NT - 1 ? NA + NB - 2 : NT - 1); sum >= 0; --sum) {
+  for (int sum = (NA + NB - 2 < FIRST ? NA + NB - 2 : FIRST); sum >= LAST; --sum) {
 #pragma unroll
     for (int a = 0; a < NA; ++a) {
       const int b = sum - a;
@@ -1233,12 +1233,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
         if (!OUT) continue;
         if (i > 0) wait_for(done(i - 1));
         const uint64_t dq = smem_desc_sw128(tiles + Lay::kQ);
+        auto oi = [&](int x, int y, int s, uint32_t more) {
+          tc_mma_ts(tmem + kOi, tmem + kH + x * KW + s * 8, dq + ((y * kTile + (s / 4) * kSub + (s % 4) * 32) >> 4),
+                    idesc_of(64 * HPC), more);
+        };
+        // The tensor cores' sums are cut off, not rounded: each product that is added to a sum takes something of it,
+        // always towards zero.  Where float32 comes of it the small products of both Oi and O come first, then the
+        // large ones: without decays float32 outputs are off by 2e-7 of their size so, by 6e-7 with all of O behind
+        // Oi, for a fiftieth of a gradient's time.
         if (leader) {
-          products<NT, kIn, NT, kHeadSteps>([&](int x, int y, int s, uint32_t more) {
-            tc_mma_ts(tmem + kOi, tmem + kH + x * KW + s * 8, dq + ((y * kTile + (s / 4) * kSub + (s % 4) * 32) >> 4),
-                      idesc_of(64 * HPC), more);
-          });
-          tc_commit(su32(&sh.bars[kGotOi]));
+          if constexpr (kSum) {
+            products<NT, kIn, NT, kHeadSteps, 1>(oi);
+          } else {
+            products<NT, kIn, NT, kHeadSteps>(oi);
+            tc_commit(su32(&sh.bars[kGotOi]));
+          }
         }
         __syncwarp();
         const bool apart = !mild_of(i);  // its outputs go where S is
@@ -1246,11 +1255,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
         const uint64_t dp = smem_desc_sw128(Lay::kOver ? tiles + Lay::kK : su32(sm) + Lay::kP);
         const uint32_t to = tmem + (apart ? kS : kOi);
         if (leader) {
-          if (!sh.bad[i % kFlags])
-            products<kIn, NT, NT, 4>([&](int x, int y, int s, uint32_t more) {
-              tc_mma(to, dv + ((x * kTile + s * 2048) >> 4), dp + ((y * Lay::kPTerm + s * 32) >> 4), idesc_of(64 * HPC) | kRowsA,
-                     apart ? more : 1u);
-            });
+          const bool good = !sh.bad[i % kFlags];
+          auto o = [&](int x, int y, int s, uint32_t more) {
+            tc_mma(to, dv + ((x * kTile + s * 2048) >> 4), dp + ((y * Lay::kPTerm + s * 32) >> 4), idesc_of(64 * HPC) | kRowsA,
+                   apart ? more : 1u);
+          };
+          if constexpr (kSum) {
+            if (good) {
+              products<kIn, NT, NT, 4, 1>(o);
+              products<NT, kIn, NT, kHeadSteps, 0, 0>(oi, 1);
+            }
+            tc_commit(su32(&sh.bars[kGotOi]));
+            if (good) products<kIn, NT, NT, 4, 0, 0>(o, 1);
+          } else if (good) {
+            products<kIn, NT, NT, 4>(o);
+          }
           tc_commit(su32(&sh.bars[got_o(i).bar]));
         }
         __syncwarp();

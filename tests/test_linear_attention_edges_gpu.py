@@ -259,3 +259,23 @@ def test_attn_mean_square(layer, shape, dtype):
     if off > 1:
         far["d_decay_bias"] = float(off)
     assert not far, far
+
+
+@pytest.mark.parametrize("shape", [(195, 2, 4, 64, 64), (784, 2, 2, 125, 128), (784, 20, 4, 128, 96)])
+def test_attn_long_memories_in_the_mean_square(layer, shape):
+    """Without decays an output is mostly what the state adds to it, a sum of
+    eight products of sixteen elements to which four of P and the values are
+    added.  The tensor cores cut sums off, towards zero: by half a unit of 2^-23
+    in the mean, 0.72 of that where bits are spread evenly, of partial sums that
+    grow as the root of their number: (5.6 + 4) 0.72 2^-24 = 4.1e-7, and what is
+    rounded besides 2e-7, together 4.6e-7.  (The small products of the terms,
+    added up before, cost nothing; 20 of them behind the large ones would be
+    twice that.)"""
+    c = Case(*shape, "f32", ragged=False, decay="none", layout=1, grad=True)
+    got, want = layer.attn_grad(c.p, want=c.grads(), **c.t), c.reference()
+    for n in ("dY", "d_final_state"):
+        c.t.pop(n)
+    got.update(layer.attn(c.p, **c.t))
+    want.update(c.reference())
+    far = {k: relative(batch_first(v, 1) if k in ("Y", "dQ", "dK", "dV") else v, want[k]) for k, v in got.items()}
+    assert max(far.values()) <= 5e-7, far
