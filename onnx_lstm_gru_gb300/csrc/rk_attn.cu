@@ -147,8 +147,8 @@ cudaError_t launch_steps(const AttnParams& p, cudaStream_t s) {
 // themselves, as it is at both ends of the sequence: what the float32 products are
 // off by (1e-7 of them) adds up on the way, and a bias' gradient adds that up once
 // more.  What they leave at a mark is taken back evenly on the way to it.  Of 500
-// cases drawn around those measured dDecay is off by 2.7e-7 of its size in the
-// middle and 1.1e-6 at most, a bias' gradient by 1.7e-7 and 2.6e-5, where short
+// cases drawn around those measured dDecay is off by 2.5e-7 of its size in the
+// middle and 1.0e-6 at most, a bias' gradient by 2.2e-7 and 2.4e-5, where short
 // memories leave little of its sum (plain form in float32: 1.8e-7 and 4e-7, 1.6e-7
 // and 3.1e-6).  Marks every 128 steps take that to 9e-6 for a fifth of the gradient's
 // time (8 x 512 x 16 heads of 128, 140 and 165 us).  A block takes the steps

@@ -54,7 +54,7 @@
 // What bounds it are the warps' own instructions and their waits for each
 // other, not the products or HBM: 512 x 64 x 16 heads of 64, bf16, 114 us (2.5
 // TB/s, 2.2 warp instructions a clock and multiprocessor, the tensor pipe 29 %
-// busy); the gradient of 512 x 8 x 16 heads of 128 137 us (2.2, 21 %); 777 x 8 x 10
+// busy); the gradient of 512 x 8 x 16 heads of 128 141 us (2.1, 20 %); 777 x 8 x 10
 // heads of 72 x 103 in float32, 80 blocks, 110 to 126 us as the lengths are (1.8,
 // 25 %).  Step by step the three take 2316, 2319 and 646 us.
 #pragma once
@@ -1536,9 +1536,10 @@ cudaError_t launch_chunks_in(const ChunkArgs& args, cudaStream_t s, int* launche
 // while the rows that they come of are rounded to 2^-9 or 2^-12 of theirs.  An
 // output that is far smaller than its terms keeps 2^-17 of those.  Three cost a
 // seventh: 512 x 64 x 16 heads of 64, bf16, 132 us for 114, 4096 x 1 x 16 of 128 68
-// for 59; the outputs are then 3e-5 to 4e-5 of their size from float32
-// arithmetic's, rounded, in the mean square, and 9e-5 to 1e-4 so.  From the
-// definition both are 1.7e-3 (Half 2.1e-4), which is their own rounding.
+// for 59 (three of the state alone 123 and 65); the outputs are then 3e-5 to 4e-5
+// (7e-5 to 9e-5) of their size from float32 arithmetic's, rounded, in the mean
+// square, and 9e-5 to 1e-4 with two.  From the definition all are 1.7e-3 (Half
+// 2.1e-4), which is their own rounding.
 template <typename T>
 cudaError_t launch_chunks(const AttnParams& p, cudaStream_t s, int* launches) {
   ChunkArgs args{};
