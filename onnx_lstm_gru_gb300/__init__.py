@@ -435,8 +435,8 @@ class RecurrentLayer:
 from . import state_space  # noqa: E402  (uses the names above)
 from .state_space import (  # noqa: E402,F401
     AttnProblem, ConvProblem, NormProblem, QkProblem, ScanProblem, StateSpaceLayer, rk_attn_encode,
-    rk_attn_grad_encode, rk_attn_grad_scratch_length, rk_attn_grad_scratch_needed, rk_attn_problem, rk_attn_scratch_length, rk_conv_encode,
-    rk_conv_grad_encode, rk_conv_grad_scratch_length, rk_conv_problem, rk_norm_encode, rk_norm_grad_encode,
-    rk_norm_grad_scratch_length, rk_norm_problem, rk_qk_encode, rk_qk_grad_encode, rk_qk_grad_scratch_length,
-    rk_qk_problem, rk_rows, rk_scan_encode, rk_scan_grad_encode, rk_scan_grad_scratch_length, rk_scan_problem,
-    rk_scan_scratch_length, rk_workspace)
+    rk_attn_grad_encode, rk_attn_grad_scratch_length, rk_attn_grad_scratch_needed, rk_attn_problem,
+    rk_attn_scratch_length, rk_conv_encode, rk_conv_grad_encode, rk_conv_grad_scratch_length, rk_conv_problem,
+    rk_norm_encode, rk_norm_grad_encode, rk_norm_grad_scratch_length, rk_norm_problem, rk_qk_encode,
+    rk_qk_grad_encode, rk_qk_grad_scratch_length, rk_qk_problem, rk_rows, rk_scan_encode, rk_scan_grad_encode,
+    rk_scan_grad_scratch_length, rk_scan_problem, rk_scan_scratch_length, rk_workspace)

@@ -132,9 +132,9 @@ enum Bar {
 // sets that flag before: the second head's warp comes to a chunk once the one
 // three before it is done, for which both heads' decays have been taken, and the
 // others wait for the chunk's own decays.  Nobody still reads it for chunk i +
-// kClear - kFlags, eleven back: all but the copying warp have read a chunk's flag
-// when it is done (three back), and that one reads it before it fetches the next
-// chunk's tiles but two.
+// kClear - kFlags, eleven back: chunk i - 3 is done, with which all but the copying
+// warp have read its flag, and that one fetched its tiles after it had read the
+// flag of chunk i - 6.
 constexpr int kFlags = 16, kClear = 5;
 struct Small {
   __align__(16) Decays decays[3][2];
