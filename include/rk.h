@@ -583,7 +583,8 @@ typedef struct rk_attn_operands {
  * added up before the one rounding), dDecay (float32 rows of `heads`
  * elements), d_decay_bias, d_initial_state and the optional input
  * d_final_state are float32.  dDecay is taken from running sums over
- * 512 steps of what queries and keys contribute, in pairs of float32: where it
+ * 512 steps (over 64 in smaller calls with decay_bias or d_decay_bias) of
+ * what queries and keys contribute, in pairs of float32: where it
  * is far smaller than those contributions it has their float32 accuracy, and
  * d_decay_bias, which adds dDecay up, that of the sum of its magnitudes.
  * Infinities and NaN in an operand may reach the gradients of any step of

@@ -143,21 +143,21 @@ cudaError_t launch_steps(const AttnParams& p, cudaStream_t s) {
 // those from it on, which read it: its gradient is E = <H, dH>, the product of
 // the state before the step with its gradient.  With A_t = q dq and B_t = k dk
 // of a step, E grows by B_t - A_t from one step to the next.  The sums run from
-// one mark to the next, kMarkChunks chunks on, where E is taken from the states
+// one mark to the next, eight chunks on or one, where E is taken from the states
 // themselves, as it is at both ends of the sequence: what the float32 products are
 // off by (1e-7 of them) adds up on the way, and a bias' gradient adds that up once
 // more.  What they leave at a mark is taken back evenly on the way to it.  Of 500
 // cases drawn around those measured dDecay is off by 2.5e-7 of its size in the
-// middle and 1.0e-6 at most, a bias' gradient by 2.2e-7 and 2.4e-5, where short
-// memories leave little of its sum (plain form in float32: 1.8e-7 and 4e-7, 1.6e-7
-// and 3.1e-6).  Marks every 128 steps take that to 9e-6 for a fifth of the gradient's
-// time (8 x 512 x 16 heads of 128, 140 and 165 us).  A block takes the steps
+// middle and 9e-7 at most, a bias' gradient by 1.4e-7 and 7e-6, where short
+// memories leave little of its sum (with marks every eight chunks alone 2.2e-7 and
+// 2.4e-5; plain form in float32: 1.8e-7 and 4e-7, 1.6e-7 and 3.1e-6).  A block takes the steps
 // between two marks; the sums are pairs of float32 that keep what each addition
 // rounds away (Knuth's two-sum), as the card has few float64 units and the kernel
 // is a chain of sums, bound by their latency (128 heads of 512 steps 11.8 us with
-// float64, 6.7 so).
-constexpr int kDecayThreads = 256, kDecayWarps = kDecayThreads / 32, kDecayEach = 2, kDecayTile = kDecayThreads * kDecayEach;
-static_assert(kDecayTile == kMarkChunks * 64, "a block's steps are those between two marks");
+// float64, 6.7 so).  EVERY: chunks from mark to mark.
+constexpr int kDecayThreads = 256, kDecayWarps = kDecayThreads / 32, kDecayEach = 2;
+__host__ __device__ constexpr int decay_threads(int every) { return every * 64 / kDecayEach; }
+static_assert(decay_threads(kMarkChunks) == kDecayThreads, "a block's steps are those between two marks");
 struct Exact {
   float hi, lo;
   __device__ __forceinline__ void add(float x) {
@@ -236,7 +236,9 @@ __global__ void __launch_bounds__(kDecayThreads) attn_mark_kernel(AttnDecayParam
   }
 }
 
-__global__ void __launch_bounds__(kDecayThreads) attn_decay_kernel(AttnDecayParams p) {
+template <int EVERY>
+__global__ void __launch_bounds__(decay_threads(EVERY)) attn_decay_kernel(AttnDecayParams p) {
+  constexpr int kDecayThreads = decay_threads(EVERY), kDecayWarps = kDecayThreads / 32, kDecayTile = EVERY * 64;
   __shared__ Exact sums[2][kDecayWarps];
   previous_done();
   next_may_start();
@@ -382,7 +384,8 @@ long long streams_of(long long batch, long long heads, int key_size, int value_s
 }
 }  // namespace
 
-AttnPlan attn_plan(long long seq, long long batch, long long heads, int key_size, int value_size, int passes) {
+AttnPlan attn_plan(long long seq, long long batch, long long heads, int key_size, int value_size, int passes,
+                   bool bias) {
   AttnPlan plan{};
   const long long streams = streams_of(batch, heads, key_size, value_size, passes);
   const long long chunks = (seq + 63) / 64;
@@ -396,7 +399,10 @@ AttnPlan attn_plan(long long seq, long long batch, long long heads, int key_size
   plan.segments = plan.per > 0 ? (int)((chunks + plan.per - 1) / plan.per) : 1;
   // a gradient's passes contract over keys or values
   plan.deep = std::max(key_size, passes > 1 ? value_size : 0) > 64 ? 128 : 64;
-  plan.marks = chunks > 0 ? (int)((chunks - 1) / kMarkChunks) : 0;
+  const long long marks = std::max<long long>(chunks - 1, 0);
+  const bool near = bias && 2 * (streams / passes) * marks * plan.deep * 128 * 4 <= kNearMarkBytes;
+  plan.every = near ? kNearMarkChunks : kMarkChunks;
+  plan.marks = (int)(marks / plan.every);
   return plan;
 }
 
@@ -407,10 +413,10 @@ long long attn_plan_scratch(const AttnPlan& plan, long long batch, long long hea
   return streams * plan.segments * (plan.deep * 128LL + 4);
 }
 
-int attn_decay_tiles(long long seq) { return (int)((seq + kDecayTile - 1) / kDecayTile); }
+int attn_decay_tiles(long long seq, int every) { return (int)((seq + every * 64 - 1) / (every * 64)); }
 
 cudaError_t launch_attn_decay(AttnDecayParams p, cudaStream_t s, int* launches) {
-  p.tiles = attn_decay_tiles(p.S);
+  p.tiles = attn_decay_tiles(p.S, p.every);
   const long long blocks = (long long)p.N * p.H * p.tiles;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   cudaError_t e = cudaSuccess;
@@ -421,7 +427,8 @@ cudaError_t launch_attn_decay(AttnDecayParams p, cudaStream_t s, int* launches) 
     if (e != cudaSuccess) return e;
     ++*launches;
   }
-  e = launch_chained(attn_decay_kernel, (unsigned)blocks, kDecayThreads, 0, s, p);
+  e = launch_chained(p.every == kMarkChunks ? attn_decay_kernel<kMarkChunks> : attn_decay_kernel<kNearMarkChunks>,
+                     (unsigned)blocks, decay_threads(p.every), 0, s, p);
   if (e != cudaSuccess) return e;
   ++*launches;
   if (p.dbias == nullptr) return e;

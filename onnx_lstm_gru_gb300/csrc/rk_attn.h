@@ -61,7 +61,7 @@ struct AttnPass {
   RowsArg dot_with;            // rows like o's: their products with the unrounded o
   float* dot;                  // [N][H][S], or null
   float* o32;                  // [N * S][H][V] in o's place: heads that share are added up from there
-  float* marks;                // [streams of the pass][marks][deep][128], or null: the states at every kMarkChunks-th chunk's start
+  float* marks;                // [streams of the pass][marks][deep][128], or null: the states at the marks
 };
 // How a call's sequences are cut: pieces that run side by side where there are
 // too few states to fill the card, and what each adds to the state.
@@ -69,13 +69,19 @@ struct AttnPlan {
   int segments, per;  // pieces of a sequence, and the chunks of 64 steps in each
   int deep;           // elements that a kernel's states have along q and k: 64 or 128
   int vec;            // rows take 16-byte pieces
-  int marks;          // of a sequence, where a gradient's decays are wanted
+  int every, marks;   // chunks from one mark to the next, and the marks of a sequence
   float* states;      // [streams][segments][deep][128]
   float* left;        // [streams][segments][2][2]: logarithms (base 2) of what a piece leaves of its first state
 };
-// Chunks between two of the states at which the decays' gradient is taken
-// from the state and its gradient themselves.
-constexpr int kMarkChunks = 8;
+// Chunks between two of the states at which the decays' gradient is taken from
+// the state and its gradient themselves: every chunk where there is a bias, whose
+// gradient adds up what is lost between two, and these states of both directions
+// are at most so many bytes, a quarter of L2 (512 x 2 x 16 heads of 128, 29 MB: 66 us
+// for 54; 201 x 3 x 12, 14 MB: 56 for 47; 590 x 4 alone: 41 for 40).  More of them cost
+// large calls a third of their time (512 x 8 x 16 heads of 128, every second chunk
+// 165 us for 140), and there many heads and rows make up for it.
+constexpr int kMarkChunks = 8, kNearMarkChunks = 1;
+constexpr long long kNearMarkBytes = 32LL << 20;
 struct AttnParams {
   int dtype;
   int S, N, H;
@@ -96,7 +102,8 @@ constexpr int kAttnSteps = 12;
 // Heads that share a block.
 int attn_together(int key_size, int value_size);
 // The plan of `passes` passes, its pointers left out; and the floats of its scratch.
-AttnPlan attn_plan(long long seq, long long batch, long long heads, int key_size, int value_size, int passes);
+AttnPlan attn_plan(long long seq, long long batch, long long heads, int key_size, int value_size, int passes,
+                   bool bias = false);
 long long attn_plan_scratch(const AttnPlan& plan, long long batch, long long heads, int key_size, int value_size,
                             int passes);
 // Step by step: one forward pass.
@@ -134,12 +141,12 @@ struct AttnDecayParams {
   const float* last;   // and behind the last
   const float* states; // at the marks, the two passes' one after the other, and [N][H][marks] their products
   float* between;
-  int marks, deep, together;  // heads that share a block
+  int every, marks, deep, together;  // heads that share a block
   double* partial;     // [N][H][tiles]
   float* dbias;        // [H], or null
   int tiles;           // set by the launch
 };
-int attn_decay_tiles(long long seq);
+int attn_decay_tiles(long long seq, int every);
 cudaError_t launch_attn_decay(AttnDecayParams p, cudaStream_t s, int* launches);
 
 // o = sums over the heads that share of o32, for up to three outputs.

@@ -120,8 +120,8 @@ struct GradPlan {
   int64_t to, of, cross, partial, q32, k32, v32, between, marks, chunks;  // marks: of one pass
   int64_t total() const { return to + of + cross + partial + q32 + k32 + v32 + between + 2 * marks + chunks; }
 };
-rk::AttnPlan plan_of(const rk_attn_problem* p, int passes) {
-  return rk::attn_plan(p->seq, p->batch, p->heads, (int)p->key_size, (int)p->value_size, passes);
+rk::AttnPlan plan_of(const rk_attn_problem* p, int passes, bool bias = false) {
+  return rk::attn_plan(p->seq, p->batch, p->heads, (int)p->key_size, (int)p->value_size, passes, bias);
 }
 int64_t plan_scratch(const rk_attn_problem* p, int passes) {
   if (p->seq * p->batch == 0 || (passes == 1 && p->seq <= rk::kAttnSteps)) return 0;
@@ -136,19 +136,20 @@ void place(rk::AttnPlan& plan, float* w, int64_t floats) {
 int64_t four(int64_t x) { return (x + 3) / 4 * 4; }
 struct GradWants {
   bool q, k, v, decay, bias, first;
+  bool has_bias;  // among the operands: dDecay is the same then whether the bias' gradient is wanted or not
   bool any() const { return q || k || v || decay || bias || first; }
 };
-constexpr GradWants kEverything = {true, true, true, true, true, true};
+constexpr GradWants kEverything = {true, true, true, true, true, true, true};
 GradPlan grad_plan(const rk_attn_problem* p, const GradWants& want) {
   const int64_t heads = p->batch * p->heads, rows = heads * p->seq;
   GradPlan g{};
   if (rows == 0 || !want.any()) return g;
   // the pieces are those of the whole gradient whatever is wanted: equal bits
-  const rk::AttnPlan plan = plan_of(p, 3);
+  const rk::AttnPlan plan = plan_of(p, 3, want.bias || want.has_bias);
   if (want.decay || want.bias) {
     g.to = g.of = four(rows);
     g.cross = four(2 * heads);
-    if (want.bias) g.partial = four(2 * heads * rk::attn_decay_tiles(p->seq));
+    if (want.bias) g.partial = four(2 * heads * rk::attn_decay_tiles(p->seq, plan.every));
     const int together = rk::attn_together((int)p->key_size, (int)p->value_size);
     g.between = four(heads * plan.marks);
     g.marks = p->batch * ((p->heads + together - 1) / together) * plan.marks * plan.deep * 128;
@@ -223,8 +224,10 @@ int64_t rk_attn_grad_scratch_needed(const rk_attn_problem* p, const rk_attn_grad
   Call c = begin(nullptr, "LinearAttentionGrad", p, o, true);
   if (c.ok()) check(c, p);
   if (!c.ok()) return -1;
-  const GradWants want = {o->dQ.ptr != nullptr,     o->dK.ptr != nullptr,           o->dV.ptr != nullptr,
-                          o->dDecay.ptr != nullptr, o->d_decay_bias.ptr != nullptr, o->d_initial_state.ptr != nullptr};
+  const GradWants want = {o->dQ.ptr != nullptr,           o->dK.ptr != nullptr,
+                          o->dV.ptr != nullptr,           o->dDecay.ptr != nullptr,
+                          o->d_decay_bias.ptr != nullptr, o->d_initial_state.ptr != nullptr,
+                          o->decay_bias.ptr != nullptr};
   return grad_plan(p, want).total();
 }
 
@@ -345,7 +348,8 @@ rk_status rk_attn_grad_encode(rk_handle* h, const rk_attn_problem* p, const rk_a
   const float* dlast = c.tensor<float>("d_final_state", o->d_final_state, states, 4);
   float* dbias = c.tensor<float>("d_decay_bias", o->d_decay_bias, H, 4);
   float* dfirst = c.tensor<float>("d_initial_state", o->d_initial_state, states, 4);
-  const GradWants want = {dQ.p != nullptr, dK.p != nullptr, dV.p != nullptr, dDecay.p != nullptr, dbias != nullptr, dfirst != nullptr};
+  const GradWants want = {dQ.p != nullptr,  dK.p != nullptr,   dV.p != nullptr,   dDecay.p != nullptr,
+                          dbias != nullptr, dfirst != nullptr, ap.bias != nullptr};
   if (!c.ok() || !want.any()) return c.st;
   if (p->seq * p->batch == 0) {
     c.zero(dbias, H * 4LL, s);
@@ -396,7 +400,7 @@ rk_status rk_attn_grad_encode(rk_handle* h, const rk_attn_problem* p, const rk_a
   }
   int launches = 0;
   if (ap.passes) {
-    ap.plan = plan_of(p, 3);
+    ap.plan = plan_of(p, 3, want.bias || want.has_bias);
     place(ap.plan, marks + 2 * g.marks, g.chunks);
     ap.plan.vec = Q.vec && K.vec && V.vec && dY.vec;
     rk::use_attn_waits(h);
@@ -408,7 +412,8 @@ rk_status rk_attn_grad_encode(rk_handle* h, const rk_attn_problem* p, const rk_a
     d.decay = ap.decay, d.bias = ap.bias, d.dDecay = dDecay;
     d.to = to, d.of = of, d.dbias = dbias;
     d.first = first ? cross : nullptr, d.last = dlast ? cross + heads : nullptr;
-    d.states = marks, d.between = between, d.marks = ap.plan.marks, d.deep = ap.plan.deep;
+    d.states = marks, d.between = between, d.deep = ap.plan.deep;
+    d.every = ap.plan.every, d.marks = ap.plan.marks;
     d.together = rk::attn_together(dk, dv);
     d.partial = dbias ? reinterpret_cast<double*>(partial) : nullptr;
     c.cuda("launch", rk::launch_attn_decay(d, s, &launches));

@@ -1077,8 +1077,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
     };
     // The state at the start of chunk c, where the decays' gradient wants it.
     auto mark = [&](int c) {
-      if (NT != kTerms || !a.marks || c == 0 || c % kMarkChunks != 0) return;  // gradients have all terms
-      float* to = a.marks + ((long long)(at.stream - at.pass * p.N * ((p.H + HPC - 1) / HPC)) * p.plan.marks + c / kMarkChunks - 1) * kept;
+      const int every = p.plan.every;
+      if (NT != kTerms || !a.marks || c == 0 || (every > 1 && c % every != 0)) return;  // gradients have all terms
+      float* to = a.marks + ((long long)(at.stream - at.pass * p.N * ((p.H + HPC - 1) / HPC)) * p.plan.marks + c / every - 1) * kept;
 #pragma unroll 1
       for (int j = 0; j < NH; j += 16) {
         float y[16];

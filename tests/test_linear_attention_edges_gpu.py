@@ -193,6 +193,20 @@ def test_qk_turns_near_the_zeros_of_the_sine(layer, interleaved, dtype):
         assert bool(((got - want).abs() <= bound).all()), float(((got - want).abs() - bound).max())
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("S,N,H,dk,dv", [(260, 6, 3, 64, 32), (330, 6, 1, 128, 72), (130, 60, 3, 24, 16),
+                                         (700, 1, 2, 128, 128), (260, 40, 4, 128, 128)])
+def test_attn_rows_that_end_where_sums_start_anew_with_a_bias(layer, S, N, H, dk, dv, dtype):
+    """With a bias the sums start anew at every chunk, unless that takes more
+    than 32 MB (the last shape); rows end before, at and behind chunks' ends, in
+    sequences cut and not, and the bias' gradient is there without a bias too."""
+    lens = ([64, 65, 128, 192, 63, 0] * 10)[:N] if N > 1 else None
+    c = Case(S, N, H, dk, dv, dtype, lens=lens, ragged=False, layout=N % 2, decay="both", grad=True)
+    c.compare(layer.attn_grad(c.p, want=c.grads(), **c.t))
+    c.t["Decay"] = c.t["Decay"] + c.t.pop("decay_bias")
+    c.compare(layer.attn_grad(c.p, want=("dDecay", "d_decay_bias"), **c.t))
+
+
 # ---- errors in the mean square ----------------------------------------------------------------------------
 
 TIGHT_SHAPES = [(300, 2, 4, 64, 64), (300, 2, 2, 128, 128), (700, 1, 2, 64, 48), (1500, 1, 1, 128, 128),

@@ -212,6 +212,13 @@ def test_scratch_of_what_is_wanted():
     # few sequences are cut into the same pieces, whatever is wanted
     one = rk.AttnProblem(seq=4096, batch=1, heads=16, key_size=128, value_size=128)
     assert needed(one, "dQ") == needed(one, "dQ", "dK", "dV") == needed(one, "d_initial_state") > 0
+    # with a bias the decays take the states at every chunk, up to 32 MB: here of 3 x 12 heads, three chunks, both ways
+    few = rk.AttnProblem(seq=201, batch=3, heads=12, key_size=48, value_size=80, dtype="f16")
+    more = needed(few, "dDecay", "decay_bias") - needed(few, "dDecay")
+    assert 36 * 3 * 2 * 128 * 128 <= more < 36 * 3 * 2 * 128 * 128 + 1024
+    assert needed(few, "dDecay", "decay_bias") < needed(few, "d_decay_bias") == needed(few, "d_decay_bias", "decay_bias")
+    many = rk.AttnProblem(seq=512, batch=8, heads=16, key_size=128, value_size=128)
+    assert needed(many, "dDecay", "decay_bias") == needed(many, "dDecay")
     assert needed(rk.AttnProblem(seq=0, batch=4, heads=2, key_size=8, value_size=8), *outputs) == 0
     c.layout = 2
     assert rk.rk_attn_grad_scratch_needed(c, ss.rk_attn_grad_operands()) == -1
